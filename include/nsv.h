@@ -112,8 +112,11 @@ enum {
                                read slot outside the pool; skipped */
     NSV_DEV_BAD_SLOT = 4u,  /* write slot outside [0, (num_blocks+1)*block_size);
                                that row's K/V was not written */
-    NSV_DEV_TIMEOUT = 8u    /* an in-kernel wait gave up after its limit and the
+    NSV_DEV_TIMEOUT = 8u,   /* an in-kernel wait gave up after its limit and the
                                kernel returned early; results are invalid */
+    NSV_DEV_BAD_CHUNK = 16u /* chunk starts that are not an ascending pair within
+                               [0, tokens]; the row was read as having no new
+                               tokens */
 };
 
 /* Sizes of one decode batch.  Limits: 0 <= rows <= 8192; num_heads a
@@ -403,6 +406,84 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
                                    int64_t slot_row_stride, const int32_t *context_lens,
                                    float scale, void *out, void *workspace,
                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache: the read for
+ * everything that is not one step of one token per row.  Whole prompts,
+ * chunks of long prompts, speculative tokens and single tokens mix freely in
+ * one batch: row r brings the query tokens chunk_starts[r] ..
+ * chunk_starts[r + 1] - 1 (none, one or thousands), which are the last
+ * positions of its context_lens[r].
+ *
+ *   q, out        [tokens][num_heads][head_dim]
+ *   chunk_starts  [rows + 1] int32, ascending, within [0, tokens]
+ *
+ * Token i of row r (counted within the row) sits at position
+ * pos = context_lens[r] - (chunk_starts[r + 1] - chunk_starts[r]) + i.  With
+ * `scores` NULL it sees the positions t <= pos (causal) and
+ *   out = softmax_t(scale * q.k_t) v.
+ * A token that sees no position (an empty context, a chunk longer than its
+ * context) outputs 0.  Tokens of no row (before chunk_starts[0], at and after
+ * chunk_starts[rows], as in a batch padded to a captured size) are not
+ * touched in `out`.  Pool contents at and past a row's context length are
+ * never used and may hold anything, NaN included.
+ *
+ * `scores` changes the score before the softmax, in this order:
+ *   softcap > 0         s = softcap * tanh(scale * q.k / softcap)
+ *   slopes (per head)   s = s - slopes[h] * |pos - t|
+ *   see_begin, see_end  the token sees max(0, see_begin) <= t <
+ *                       min(see_end, context length) instead of 0 <= t <= pos
+ *                       (one of them NULL: that bound stays)
+ * The bounds express a sliding window (see_begin = pos + 1 - window), a
+ * document mask over packed documents (see_begin = the document's first
+ * position), a prefix that every token sees in full (see_end = max(pos + 1,
+ * prefix length)), and an encoder-like read (see_end = the context length).
+ *
+ * Uses shape.rows, num_heads, num_kv_heads (at most 64 query heads per KV
+ * head), head_dim, block_size, max_blocks, num_blocks and dtype; query_len
+ * must be 0 or 1.  0 <= tokens < 2^30.  For bf16
+ * (num_blocks+1)*num_kv_heads*2 < 2^31.  The lengths live in device memory and
+ * are only read by kernels, so a captured call replays with new ones.
+ *
+ * workspace: device memory of at least the bytes nsv_chunk_workspace gives,
+ * 256-byte aligned, owned by the caller, uninitialised.  It holds nothing
+ * between calls; two calls that overlap on the GPU need two.
+ * Where a row is cut between CTAs its pieces are merged in the order of their
+ * positions, so the same call on the same inputs gives the same bits.
+ */
+typedef struct nsv_scores {
+    float softcap;            /* 0: no cap; else finite and > 0 */
+    const float *slopes;      /* [num_heads] device memory, or NULL */
+    const int32_t *see_begin; /* [tokens] device memory, or NULL */
+    const int32_t *see_end;   /* [tokens] device memory, or NULL */
+} nsv_scores;
+
+/* Workspace bytes of nsv_paged_chunk and nsv_chunk_step for up to `tokens`
+ * query tokens on a GPU with num_sms SMs (<= 0: the current device's).  Grows
+ * with rows and tokens: what a larger batch needs serves a smaller one.
+ * Returns NSV_ERR_{NULLPTR, DTYPE, SHAPE, UNSUPPORTED, CUDA}. */
+NSV_API int nsv_chunk_workspace(const nsv_shape *shape, int64_t tokens, int num_sms,
+                                int64_t *bytes);
+
+NSV_API int nsv_paged_chunk(const nsv_shape *shape, const nsv_scores *scores, int64_t tokens,
+                            const void *q, const void *k_pool, const void *v_pool,
+                            const int32_t *block_tables, const int32_t *chunk_starts,
+                            const int32_t *context_lens, float scale, void *out,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The serving step of a mixed batch: append every new token's key and value
+ * (k_new, v_new [tokens][num_kv_heads][head_dim], write_slots [tokens] int64;
+ * rules as in nsv_kv_write, a padded token names the sink slot), then
+ * nsv_paged_chunk on the same stream.  context_lens already count the new
+ * tokens.  Both halves' arguments are checked before either is launched.
+ */
+NSV_API int nsv_chunk_step(const nsv_shape *shape, const nsv_scores *scores, int64_t tokens,
+                           const void *q, const void *k_new, const void *v_new,
+                           const int64_t *write_slots, void *k_pool, void *v_pool,
+                           const int32_t *block_tables, const int32_t *chunk_starts,
+                           const int32_t *context_lens, float scale, void *out,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Self-test of the bounded wait (the pages have no counterpart; this checks

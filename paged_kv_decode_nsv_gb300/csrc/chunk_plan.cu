@@ -1,0 +1,166 @@
+// Planning kernel of the chunk attention: from the chunk starts, context
+// lengths and visibility bounds in device memory to the list of tiles, each
+// with the key range that its query tokens see, and the prefix sums of their
+// units.  Lengths never reach the host, so a captured step replays with new
+// ones.  One CTA: the list is short (rows + tokens / tile tokens).
+//
+// Bad values are caught here: a context length outside [0, max_blocks * 16] is
+// taken as 0 (NSV_DEV_BAD_CTX) and a pair of chunk starts that is not an
+// ascending pair within [0, tokens] as no tokens (NSV_DEV_BAD_CHUNK); a list
+// that would outgrow its room (starts that overlap) is cut off and flagged.
+
+#include "chunk.cuh"
+
+namespace nsv {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive sum over the block's threads; *total is the block's.
+__device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
+                                                long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(sm::kFull, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(sm::kFull, w, o);
+      if (lane >= o) w += x;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  if (warp) v += s_warp[warp - 1];
+  *total = s_warp[31];
+  __syncthreads();
+  return v;
+}
+
+struct RowChunk {
+  int start, n, ctx;
+};
+
+__device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool flag) {
+  const int a = __ldg(p.chunk_starts + r), b = __ldg(p.chunk_starts + r + 1);
+  RowChunk c{a, b - a, __ldg(p.context_lens + r)};
+  if (a < 0 || b < a || b > p.tokens) {
+    c.n = 0;
+    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+  }
+  if (c.ctx < 0 || (long long)c.ctx > (long long)p.max_blocks * kBlock) {
+    c.ctx = 0;
+    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CTX);
+  }
+  return c;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+  __shared__ int s_first[kMaxRows + 1];  // tiles before each row
+  __shared__ int s_kb[kPlanThreads], s_ke[kPlanThreads];
+  __shared__ long long s_warp[32];
+  sm::griddep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tt = p.tile_tokens;
+
+  long long carry = 0;
+  for (int base = 0; base < p.rows; base += kPlanThreads) {
+    const int r = base + tid;
+    long long n = 0;
+    if (r < p.rows) n = (row_chunk(p, r, true).n + (long long)tt - 1) / tt;
+    long long total;
+    const long long upto = carry + block_scan(n, s_warp, &total);
+    if (r < p.rows) s_first[r] = (int)min(upto - n, (long long)p.max_tiles);
+    carry += total;
+  }
+  if (carry > p.max_tiles) {
+    if (tid == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+    carry = p.max_tiles;
+  }
+  if (tid == 0) s_first[p.rows] = (int)carry;
+  __syncthreads();
+  const int ntiles = (int)carry;
+
+  auto tile_of = [&](int i, int& row, RowChunk& c, int& tok0) {
+    int lo = 0, hi = p.rows;  // the last row whose first tile is at most i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] <= i) lo = mid; else hi = mid;
+    }
+    row = lo;
+    c = row_chunk(p, row, false);
+    tok0 = (i - s_first[row]) * tt;
+  };
+
+  long long units = 0;
+  for (int base = 0; base < ntiles; base += kPlanThreads) {
+    if (p.see_begin || p.see_end) {
+      // a warp per tile: the range that its tokens see
+      for (int i = warp; i < kPlanThreads && base + i < ntiles; i += kPlanThreads / 32) {
+        int row, tok0;
+        RowChunk c;
+        tile_of(base + i, row, c, tok0);
+        const int n = min(tt, c.n - tok0);
+        int kb = 0x7fffffff, ke = 0;
+        for (int t = lane; t < n; t += 32) {
+          const int2 v = chunk_sees(p, (long long)c.start + tok0 + t, c.ctx - c.n + tok0 + t, c.ctx);
+          if (v.x < v.y) {
+            kb = min(kb, v.x);
+            ke = max(ke, v.y);
+          }
+        }
+        kb = __reduce_min_sync(sm::kFull, kb);
+        ke = __reduce_max_sync(sm::kFull, ke);
+        if (lane == 0) {
+          s_kb[i] = kb < ke ? kb / kBlock * kBlock : 0;
+          s_ke[i] = ke;
+        }
+      }
+      __syncthreads();
+    }
+    const int i = base + tid;
+    long long n = 0;
+    if (i < ntiles) {
+      int row, tok0;
+      RowChunk c;
+      tile_of(i, row, c, tok0);
+      const int nt = min(tt, c.n - tok0), pos0 = c.ctx - c.n + tok0;
+      int kb = 0, ke = 0;
+      if (p.see_begin || p.see_end) {
+        kb = s_kb[tid];
+        ke = s_ke[tid];
+      } else {
+        ke = max(0, min(pos0 + nt, c.ctx));
+      }
+      p.ws_tiles[2 * (size_t)i] = make_int4(row, c.start + tok0, nt, pos0);
+      p.ws_tiles[2 * (size_t)i + 1] = make_int4(kb, ke, c.ctx, 0);
+      n = chunk_units(kb, ke, p.keys);
+    }
+    long long total;
+    const long long upto = block_scan(n, s_warp, &total);
+    if (i < ntiles) p.ws_prefix[i] = units + upto - n;
+    units += total;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.ws_prefix[ntiles] = units;
+    p.ws_head[0] = units;
+    p.ws_head[1] = ntiles;
+  }
+  for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
+  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace nsv

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "chunk.cuh"
 #include "nsv_common.cuh"
 
 namespace nsv {
@@ -45,16 +46,7 @@ std::mutex g_mu;
 
 // cuTensorMapEncodeTiled, reached through the runtime's driver entry point
 // so that the library needs no link against libcuda.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
-
-int cuda_fail() {
-  (void)cudaGetLastError();  // do not leave a stale error for the next caller
-  return NSV_ERR_CUDA;
-}
 
 // cuCtxGetCurrent, reached like cuTensorMapEncodeTiled below (loaded once).
 using CtxGetCurrentFn = CUresult (*)(CUcontext*);
@@ -62,6 +54,11 @@ CtxGetCurrentFn g_ctx_current = nullptr;
 std::once_flag g_ctx_once;
 
 }  // namespace
+
+int cuda_fail() {
+  (void)cudaGetLastError();  // do not leave a stale error for the next caller
+  return NSV_ERR_CUDA;
+}
 
 void* current_cuda_context() {
   std::call_once(g_ctx_once, [] {
@@ -106,6 +103,8 @@ int device_state(DeviceState** out) {
     if (cudaGetSymbolAddress(reinterpret_cast<void**>(&d.walked), g_walked) != cudaSuccess)
       return cuda_fail();
     if (prepare_decode_kernels() != cudaSuccess) return cuda_fail();
+    if (prepare_chunk_bf16() != cudaSuccess || prepare_chunk_f32() != cudaSuccess)
+      return cuda_fail();
     if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return cuda_fail();
     if (!g_encode) {
@@ -130,6 +129,16 @@ int query_len(const nsv_shape* s) { return s->query_len > 0 ? s->query_len : 1; 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
+int device_info(DeviceInfo* out) {
+  DeviceState* d = nullptr;
+  const int rc = device_state(&d);
+  if (rc) return rc;
+  *out = DeviceInfo{d->status, d->num_sms, g_encode};
+  return NSV_OK;
+}
+
 int check_shape(const nsv_shape* s) {
   if (!s) return NSV_ERR_NULLPTR;
   if (s->dtype != NSV_F32 && s->dtype != NSV_BF16) return NSV_ERR_DTYPE;
@@ -147,6 +156,8 @@ int check_shape(const nsv_shape* s) {
   if (s->num_blocks < 1 || s->num_blocks > (int64_t(1) << 31) - 2) return NSV_ERR_SHAPE;
   return NSV_OK;
 }
+
+namespace {
 
 // Rows of the [block][kv_head][token] pool seen as one 2-D tensor of
 // head_dim-wide rows, the tensor consumer's TMA view; its row coordinate is

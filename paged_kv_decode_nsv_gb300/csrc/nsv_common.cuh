@@ -331,6 +331,23 @@ cudaError_t decode_occupancy(int dtype, int head_dim, int qw, int consumer, int 
 // a wait that gives up also sets NSV_DEV_TIMEOUT in *status.
 cudaError_t launch_wait_probe(unsigned long long limit_ns, unsigned long long* result,
                               uint32_t* status, cudaStream_t stream);
+// What other translation units need of the per-device state (set up on first
+// use): the status word, the SM count, cuTensorMapEncodeTiled.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+struct DeviceInfo {
+  uint32_t* status;
+  int num_sms;
+  EncodeTiledFn encode;
+};
+int device_info(DeviceInfo* out);
+// The checks of nsv_shape that every entry point makes.
+int check_shape(const nsv_shape* s);
+// Clears the runtime's last error and returns NSV_ERR_CUDA.
+int cuda_fail();
+
 // The CUDA context current on the calling thread (null when there is none or
 // it cannot be read): per-device state is keyed on it.
 void* current_cuda_context();

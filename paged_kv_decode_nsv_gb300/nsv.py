@@ -13,6 +13,14 @@ CUDA device, C-contiguous, in the layouts nsv.h documents:
   block_tables    [rows, max_blocks] int32
   context_lens    [rows] int32
 
+The chunk attention (paged_chunk, chunk_step) takes ragged batches instead:
+
+  q, out          [tokens, num_heads, head_dim]
+  k_new, v_new    [tokens, num_kv_heads, head_dim], write_slots [tokens] int64
+  chunk_starts    [rows + 1] int32: row r's tokens are chunk_starts[r] ..
+                  chunk_starts[r + 1] - 1
+  slopes          [num_heads] float32; see_begin, see_end [tokens] int32
+
 Importing this module loads the library and raises ImportError if it has not
 been built (``python -m paged_kv_decode_nsv_gb300.build``); there is no
 fallback path.
@@ -34,7 +42,7 @@ ABI_VERSION = 102  # the layout of Shape and Plan below
 F32, BF16 = 0, 1
 (CONSUMER_AUTO, CONSUMER_CUDA, CONSUMER_TENSOR, CONSUMER_TENSOR_VECTOR_ROWS,
  CONSUMER_TENSOR_TMEM) = 0, 1, 2, 3, 4
-DEV_BAD_CTX, DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_CTX, DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_BAD_CHUNK = 1, 2, 4, 8, 16
 ERRORS = {0: "NSV_OK", -1: "NSV_ERR_NULLPTR", -2: "NSV_ERR_DTYPE", -3: "NSV_ERR_SHAPE",
           -4: "NSV_ERR_ALIGN", -5: "NSV_ERR_RANGE", -6: "NSV_ERR_CAPTURE", -7: "NSV_ERR_CUDA",
           -8: "NSV_ERR_WORKSPACE", -10: "NSV_ERR_UNSUPPORTED"}
@@ -58,6 +66,11 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class Scores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("see_begin", ctypes.c_void_p), ("see_end", ctypes.c_void_p)]
 
 
 _vp, _i32, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -90,6 +103,15 @@ _lib.nsv_paged_decode_slots.argtypes = [_SP, _PP, _vp, _vp, _vp, _vp, ctypes.c_i
                                         ctypes.c_int64, _vp, _f, _vp, _vp, _sz, _vp]
 _lib.nsv_paged_decode_noalloc.restype = _i32
 _lib.nsv_paged_decode_noalloc.argtypes = [_SP, _vp, _vp, _vp, _vp, _vp, _f, _vp, _vp]
+_i64 = ctypes.c_int64
+_lib.nsv_chunk_workspace.restype = _i32
+_lib.nsv_chunk_workspace.argtypes = [_SP, _i64, _i32, ctypes.POINTER(_i64)]
+_lib.nsv_paged_chunk.restype = _i32
+_lib.nsv_paged_chunk.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _f, _vp, _vp, _sz, _vp]
+_lib.nsv_chunk_step.restype = _i32
+_lib.nsv_chunk_step.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _f, _vp, _vp, _sz, _vp]
 _lib.nsv_device_status.restype = _i32
 _lib.nsv_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32),
                                    ctypes.POINTER(ctypes.c_uint64), _i32]
@@ -307,6 +329,114 @@ def decode_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, cont
                                 _ptr(context_lens, "context_lens"), float(scale),
                                 _ptr(out, "out"), ws_ptr, ws_bytes, _stream(stream)),
            "nsv_decode_step")
+    return out
+
+
+def _arg(t, what, dtype, shape, device):
+    """The pointer of an argument that must be a contiguous CUDA tensor of this
+    type and shape (-1: any) on `device`; None passes as NULL."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != len(shape) or \
+            any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, list(shape), t.dtype,
+                                                          list(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not on the current device %s" % (what, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def _scratch(nbytes, workspace, stream):
+    """(tensor, pointer, bytes) of a call's workspace: the caller's, or one
+    from torch's allocator that belongs to the call's stream."""
+    import torch
+    if workspace is not None:
+        return workspace, _ptr(workspace, "workspace"), \
+            workspace.numel() * workspace.element_size()
+    if stream is None or stream == torch.cuda.current_stream():
+        t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return t, t.data_ptr(), nbytes
+
+
+def chunk_workspace_bytes(shape, tokens, num_sms=0):
+    """Workspace bytes of paged_chunk and chunk_step for up to `tokens` tokens."""
+    n = _i64(0)
+    _check(_lib.nsv_chunk_workspace(ctypes.byref(shape), int(tokens), int(num_sms),
+                                    ctypes.byref(n)), "nsv_chunk_workspace")
+    return n.value
+
+
+def _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
+                see_begin, see_end):
+    import torch
+    dev = _current_device()
+    if q.dim() != 3 or k_pool.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q must be [tokens, heads, head_dim], the pools [blocks + 1, kv_heads, "
+                         "16, head_dim] and block_tables [rows, max_blocks]")
+    T, H, D = q.shape
+    R, MB = block_tables.shape
+    NB1, Hkv, B, D2 = k_pool.shape
+    if D2 != D:
+        raise ValueError("q head_dim %d != pool head_dim %d" % (D, D2))
+    shape = make_shape(R, H, Hkv, D, MB, NB1 - 1, _dtype_code(k_pool), B)
+    dt, i32 = k_pool.dtype, torch.int32
+    ptrs = (_arg(q, "q", dt, (T, H, D), dev), _arg(k_pool, "k_pool", dt, k_pool.shape, dev),
+            _arg(v_pool, "v_pool", dt, k_pool.shape, dev),
+            _arg(block_tables, "block_tables", i32, (R, MB), dev),
+            _arg(chunk_starts, "chunk_starts", i32, (R + 1,), dev),
+            _arg(context_lens, "context_lens", i32, (R,), dev))
+    out_ptr = _arg(out, "out", dt, (T, H, D), dev)
+    scores = None
+    if softcap or slopes is not None or see_begin is not None or see_end is not None:
+        scores = Scores(float(softcap), _arg(slopes, "slopes", torch.float32, (H,), dev),
+                        _arg(see_begin, "see_begin", i32, (T,), dev),
+                        _arg(see_end, "see_end", i32, (T,), dev))
+    return shape, scores, T, ptrs, out_ptr
+
+
+def paged_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, scale, out,
+                softcap=0.0, slopes=None, see_begin=None, see_end=None, workspace=None,
+                stream=None):
+    """Attention of each row's new tokens over its paged context (nsv_paged_chunk
+    in nsv.h): causal, or with capped and biased scores and visibility bounds.
+    workspace: chunk_workspace_bytes() of uint8, or None to allocate it."""
+    shape, scores, T, ptrs, out_ptr = _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts,
+                                                  context_lens, out, softcap, slopes, see_begin,
+                                                  see_end)
+    need = chunk_workspace_bytes(shape, T) if workspace is None else 0
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
+    _check(_lib.nsv_paged_chunk(ctypes.byref(shape), ctypes.byref(scores) if scores else None, T,
+                                *ptrs, float(scale), out_ptr, ws_ptr, ws_bytes, _stream(stream)),
+           "nsv_paged_chunk")
+    return out
+
+
+def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk_starts,
+               context_lens, scale, out, softcap=0.0, slopes=None, see_begin=None, see_end=None,
+               workspace=None, stream=None):
+    """Append the new tokens' keys and values, then paged_chunk, on one stream."""
+    import torch
+    shape, scores, T, ptrs, out_ptr = _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts,
+                                                  context_lens, out, softcap, slopes, see_begin,
+                                                  see_end)
+    dev, new = q.device, (T, k_pool.shape[1], q.shape[2])
+    new_ptrs = (_arg(k_new, "k_new", q.dtype, new, dev), _arg(v_new, "v_new", q.dtype, new, dev),
+                _arg(write_slots, "write_slots", torch.int64, (T,), dev))
+    need = chunk_workspace_bytes(shape, T) if workspace is None else 0
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
+    _check(_lib.nsv_chunk_step(ctypes.byref(shape), ctypes.byref(scores) if scores else None, T,
+                               ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr, ws_ptr,
+                               ws_bytes, _stream(stream)), "nsv_chunk_step")
     return out
 
 

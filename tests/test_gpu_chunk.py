@@ -1,0 +1,381 @@
+"""Attention of a chunk of new tokens over the paged cache (GPU), against the
+definition in 64 bits row by row.
+
+Tolerances, per (token, head), against the largest |v| that the token sees
+(every output is a convex combination of those values, with weights p / sum p):
+
+  fp32  Products of 128 terms with fp32 accumulation, the exponential, the
+        running rescales and the sum each cost a few 2^-24 relative to the
+        scores' size; scores here are below 16 in log2 units, so a weight is off
+        by at most about 16 * 128 * 2^-24 = 1.2e-4 in the worst case and by
+        sqrt(128) in place of 128, 1.1e-5, as the terms' signs fall: 4e-5.
+  bf16  The probabilities are rounded to bf16 once (2^-9 of each: half of
+        2^-8's spacing) and so is the output (2^-9 of itself): at most
+        2^-9 + 2^-9 = 2^-8 of the largest |v|, and 2^-12 for the scores'
+        fp32 arithmetic and the exponential unit.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+F32_TOL = 4e-5
+BF16_TOL = 2.0 ** -8 + 2.0 ** -12
+NAN = float("nan")
+
+
+def batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=0, pad=0, garbage=NAN):
+    """Inputs on the GPU: scattered blocks, `garbage` in every pool position
+    that holds no token (the sink and free blocks too), `pad` tokens of no row."""
+    import torch
+    rng = np.random.default_rng(seed)
+    nb = [-(-c // 16) for c in ctx]
+    blocks = sum(nb) + 3
+    perm = rng.permutation(blocks).astype(np.int32)
+    width = max(nb + [1]) + 1
+    tables = np.full((len(ctx), width), -1, np.int32)
+    written = np.zeros((blocks + 1, 16), bool)
+    at = 0
+    for r, n in enumerate(nb):
+        tables[r, :n] = perm[at:at + n]
+        at += n
+        for t in range(ctx[r]):
+            written[tables[r, t // 16], t % 16] = True
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    tdt = torch.float32 if dtype == "f32" else torch.bfloat16
+    g = torch.Generator().manual_seed(seed)
+
+    def draw(*shape):
+        return torch.randn(shape, generator=g).to(tdt).cuda()
+
+    T = int(starts[-1]) + pad
+    hold = torch.from_numpy(written).cuda()[:, None, :, None]
+    pools = [torch.where(hold, draw(blocks + 1, kv_heads, 16, head_dim), garbage) for _ in range(2)]
+    return {"q": draw(T, heads, head_dim), "k": pools[0], "v": pools[1],
+            "bt": torch.from_numpy(tables).cuda(), "starts": torch.from_numpy(starts).cuda(),
+            "ctx": torch.tensor(ctx, dtype=torch.int32).cuda(), "scale": head_dim ** -0.5,
+            "lens": (list(ctx), list(new)), "group": heads // kv_heads}
+
+
+def reference(b, softcap=0.0, slopes=None, see_begin=None, see_end=None):
+    """The definition in 64 bits, and the largest |v| that each token sees."""
+    import torch
+    q = b["q"].double()
+    out = torch.zeros_like(q)
+    big = torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    at = 0
+    for r, (c, n) in enumerate(zip(*b["lens"])):
+        ids = b["bt"][r, :-(-c // 16)].long()
+        for i in range(n):
+            pos = c - n + i
+            lo = 0 if see_begin is None else max(0, int(see_begin[at + i]))
+            hi = min(c, pos + 1 if see_end is None else int(see_end[at + i]))
+            if lo >= hi:
+                continue
+            k = b["k"][ids].transpose(1, 2).reshape(-1, b["k"].shape[1], q.shape[2])[lo:hi].double()
+            v = b["v"][ids].transpose(1, 2).reshape(-1, b["k"].shape[1], q.shape[2])[lo:hi].double()
+            k = k.repeat_interleave(b["group"], 1)
+            v = v.repeat_interleave(b["group"], 1)
+            s = torch.einsum("hd,thd->ht", q[at + i], k) * b["scale"]
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+            if slopes is not None:
+                t = torch.arange(lo, hi, device="cuda", dtype=torch.float64)
+                s = s - slopes.double()[:, None] * (pos - t).abs()
+            out[at + i] = torch.einsum("ht,thd->hd", torch.softmax(s, -1), v)
+            big[at + i] = v.abs().amax((0, 2))
+        at += n
+    return out, big
+
+
+def check(b, dtype, garbage_out=7.5, status=0, **scores):
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    nsv.device_status(clear=True)
+    out = torch.full_like(b["q"], garbage_out)
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out,
+                    **scores)
+    st, _ = nsv.device_status(clear=True)
+    assert st == status, "device status %#x" % st
+    ref, big = reference(b, **scores)
+    T = int(sum(b["lens"][1]))
+    assert torch.isfinite(out.float()).all()
+    err = (out[:T].double() - ref[:T]).abs().amax(-1)
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    worst = (err - tol * big[:T]).max().item() if T else 0.0
+    assert worst <= 0.0, "off by %.3g above the tolerance (largest error %.3g)" % (worst, err.max())
+    assert (out[T:] == garbage_out).all(), "tokens of no row were written"
+    return out
+
+
+SHAPES = [(4, 4, 64), (8, 2, 64), (4, 4, 128), (8, 2, 128), (6, 2, 128), (5, 1, 64), (16, 1, 128),
+          (64, 1, 128)]
+MIXES = [
+    ([1], [1]),
+    ([16, 40, 100, 257, 0], [1, 1, 1, 1, 0]),
+    ([17], [17]),
+    ([128, 129, 127], [128, 129, 127]),
+    ([300], [300]),
+    ([700, 5, 1, 333], [65, 5, 0, 1]),
+    ([2000], [3]),
+    ([1025, 640], [64, 200]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,head_dim", SHAPES)
+@pytest.mark.parametrize("mix", range(len(MIXES)))
+def test_causal(dtype, heads, kv_heads, head_dim, mix):
+    ctx, new = MIXES[mix]
+    check(batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=mix, pad=mix % 3), dtype)
+
+
+def _bounds(b, kind, rng):
+    """see_begin / see_end of a document mask, a window or a prefix, and a
+    general pair that leaves some tokens with nothing to see."""
+    import torch
+    begin, end = [], []
+    for c, n in zip(*b["lens"]):
+        pos = np.arange(c - n, c)
+        e = pos + 1
+        if kind == "documents":
+            cuts = np.unique(np.concatenate([[0], rng.integers(0, max(c, 1), 4)]))
+            s = cuts[np.searchsorted(cuts, pos, side="right") - 1]
+        elif kind == "window":
+            s = pos + 1 - 50
+        elif kind == "prefix":
+            s, e = np.zeros(n), np.maximum(e, c // 2)
+        else:
+            s = rng.integers(-5, c + 3, n)
+            e = s + rng.integers(-3, 200, n)
+        begin.append(s)
+        end.append(e)
+    as_gpu = lambda a: torch.from_numpy(  # noqa: E731
+        np.concatenate(a + [np.zeros(len(b["q"]) - sum(b["lens"][1]))]).astype(np.int32)).cuda()
+    got = {"see_begin": as_gpu(begin), "see_end": as_gpu(end)}
+    if kind in ("documents", "window"):
+        del got["see_end"]
+    elif kind == "prefix":
+        del got["see_begin"]
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["documents", "window", "prefix", "any"])
+@pytest.mark.parametrize("heads,kv_heads,head_dim", [(8, 2, 64), (4, 4, 128), (5, 1, 128)])
+@pytest.mark.parametrize("ctx,new", [([400, 33, 260], [300, 33, 1]), ([900], [40])])
+def test_masks(dtype, kind, heads, kv_heads, head_dim, ctx, new):
+    b = batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=5, pad=2)
+    check(b, dtype, **_bounds(b, kind, np.random.default_rng(3)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("softcap,slopes", [(20.0, False), (0.5, False), (5e4, False), (0.0, True),
+                                            (30.0, True)])
+@pytest.mark.parametrize("heads,kv_heads,head_dim", [(8, 2, 64), (12, 4, 128)])
+@pytest.mark.parametrize("ctx,new,kind", [([400, 33, 1], [300, 33, 1], None),
+                                          ([513, 77], [1, 1], None), ([300, 40], [130, 9], "any")])
+def test_scores(dtype, softcap, slopes, heads, kv_heads, head_dim, ctx, new, kind):
+    import torch
+    b = batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=6)
+    kw = _bounds(b, kind, np.random.default_rng(4)) if kind else {}
+    if slopes:
+        kw["slopes"] = torch.exp2(-torch.arange(heads, device="cuda", dtype=torch.float32) / 2)
+    check(b, dtype, softcap=softcap, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scale_of_any_sign(dtype):
+    for scale in (-0.1, 0.0, 0.3):
+        b = batch([200, 130], [129, 1], 4, 2, 64, dtype, seed=7)
+        b["scale"] = scale
+        check(b, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_chunk_longer_than_its_context(dtype):
+    """The first tokens sit before position 0: they see nothing and give 0."""
+    b = batch([40], [40], 4, 2, 64, dtype, seed=8)
+    b["ctx"][0] = 25
+    b["lens"] = ([25], [40])
+    b["k"][:] = b["k"].nan_to_num(0.0)
+    b["v"][:] = b["v"].nan_to_num(0.0)
+    out = check(b, dtype)
+    assert (out[:15] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_scores_need_the_running_maximum(dtype):
+    """Scores that grow along the context raise the maximum run after run."""
+    import torch
+    b = batch([1500], [130], 4, 2, 64, dtype, seed=9)
+    b["q"].fill_(1.0)
+    for t in range(1500):
+        b["k"][b["bt"][0, t // 16].item(), :, t % 16] = t / 256.0 / 8 * 4
+    torch.cuda.synchronize()
+    check(b, dtype)
+
+
+def test_same_call_same_bits():
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([3000, 700, 64], [40, 300, 1], 8, 2, 128, "bf16", seed=10)
+    outs = [torch.empty_like(b["q"]) for _ in range(3)]
+    for o in outs:
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_single_tokens_agree_with_the_decode_read(dtype):
+    """One token per row: the same read as paged_decode, by another kernel."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    ctx = [1, 16, 700, 2049, 300]
+    b = batch(ctx, [1] * 5, 8, 2, 128, dtype, seed=11)
+    out = check(b, dtype)
+    want = nsv.paged_decode(b["q"], b["k"], b["v"], b["bt"], b["ctx"], b["scale"],
+                            torch.empty_like(out))
+    _, big = reference(b)
+    tol = 2 * (F32_TOL if dtype == "f32" else BF16_TOL)   # each within one of the definition
+    assert ((out.double() - want.double()).abs().amax(-1) <= tol * big).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bad_values_are_skipped_and_flagged(dtype):
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([200, 100, 60], [50, 30, 20], 4, 2, 64, dtype, seed=12)
+
+    def call():
+        out = torch.full_like(b["q"], 3.0)
+        nsv.device_status(clear=True)
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out)
+        return out, nsv.device_status(clear=True)[0]
+
+    good, st = call()
+    assert st == 0
+    # a block id outside the pool: its positions are left out, other rows stay
+    keep = b["bt"].clone()
+    b["bt"][1, 2] = 10 ** 6
+    b["bt"][2, 0] = -7
+    out, st = call()
+    assert st == nsv.DEV_BAD_BLOCK
+    assert torch.equal(out[:50], good[:50]) and torch.isfinite(out.float()).all()
+    b["bt"] = keep
+    # a context beyond the table: the row reads as empty
+    b["ctx"][1] = 16 * b["bt"].shape[1] + 1
+    out, st = call()
+    assert st == nsv.DEV_BAD_CTX
+    assert (out[50:80] == 0).all() and torch.equal(out[:50], good[:50])
+    b["ctx"][1] = 100
+    # starts that do not ascend, or leave [0, tokens]: no tokens of that row
+    for starts, untouched in (([0, 50, 40, 100], (50, 50)), ([0, 50, 80, 101], (80, 100)),
+                              ([-5, 50, 80, 100], (0, 50))):
+        b["starts"] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        out, st = call()
+        assert st & nsv.DEV_BAD_CHUNK
+        assert (out[untouched[0]:untouched[1]] == 3.0).all()
+    # rows that all claim every token: more tiles than there is room for
+    R = 64
+    wide = dict(b, bt=b["bt"][:1].repeat(R, 1), ctx=b["ctx"][:1].repeat(R),
+                starts=torch.tensor([0, 100] * (R // 2) + [0], dtype=torch.int32, device="cuda"))
+    out = torch.zeros_like(b["q"])
+    nsv.paged_chunk(wide["q"], b["k"], b["v"], wide["bt"], wide["starts"], wide["ctx"], 0.1, out)
+    assert nsv.device_status(clear=True)[0] & nsv.DEV_BAD_CHUNK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_step_appends_then_reads(dtype):
+    """The step's new tokens are in the pool before the read, bit for bit."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([300, 40, 1], [130, 40, 1], 8, 2, 128, dtype, seed=13, pad=4)
+    T, live = len(b["q"]), sum(b["lens"][1])
+    sink = (b["k"].shape[0] - 1) * 16
+    slots = np.full(T, sink, np.int64)
+    at = 0
+    for r, (c, n) in enumerate(zip(*b["lens"])):
+        for i in range(n):
+            pos = c - n + i
+            slots[at] = int(b["bt"][r, pos // 16]) * 16 + pos % 16
+            at += 1
+    slots = torch.from_numpy(slots).cuda()
+    blk, off = slots[:live] // 16, slots[:live] % 16
+    new = [torch.zeros(T, 2, 128, dtype=b["q"].dtype, device="cuda") for _ in range(2)]
+    want_k, want_v = b["k"].clone(), b["v"].clone()
+    for pool, x in ((b["k"], new[0]), (b["v"], new[1])):
+        x[:live] = pool[blk, :, off]
+        pool[blk, :, off] = NAN     # nothing there before the step
+    out = torch.full_like(b["q"], 7.5)
+    nsv.device_status(clear=True)
+    nsv.chunk_step(b["q"], new[0], new[1], slots, b["k"], b["v"], b["bt"], b["starts"], b["ctx"],
+                   b["scale"], out)
+    assert nsv.device_status(clear=True)[0] == 0
+    assert torch.equal(b["k"][:-1].nan_to_num(9.0), want_k[:-1].nan_to_num(9.0))
+    assert torch.equal(b["v"][:-1].nan_to_num(9.0), want_v[:-1].nan_to_num(9.0))
+    ref, big = reference(b)
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert ((out[:live].double() - ref[:live]).abs().amax(-1) <= tol * big[:live]).all()
+    assert (out[live:] == 7.5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_captured_call_replays_with_new_lengths(dtype):
+    """Captured on one batch, replayed on others of the same sizes: lengths,
+    chunk starts and tables are read by the kernels alone."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    a = batch([500, 90, 33], [70, 20, 6], 8, 2, 128, dtype, seed=14, garbage=0.0)
+    c = batch([64, 411, 148], [1, 90, 3], 8, 2, 128, dtype, seed=15, garbage=0.0, pad=2)
+    assert len(a["q"]) == len(c["q"])
+    # one pool for both: c's blocks behind a's
+    na = a["k"].shape[0]
+    k, v = torch.cat([a["k"], c["k"]]), torch.cat([a["v"], c["v"]])
+    width = max(a["bt"].shape[1], c["bt"].shape[1])
+    tables = [torch.full((3, width), -1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    tables[0][:, :a["bt"].shape[1]] = a["bt"]
+    tables[1][:, :c["bt"].shape[1]] = torch.where(c["bt"] >= 0, c["bt"] + na, -1)
+    q, bt, starts, ctx = (x.clone() for x in (a["q"], tables[0], a["starts"], a["ctx"]))
+    out = torch.zeros_like(q)
+    shape = nsv.make_shape(3, 8, 2, 128, width, k.shape[0] - 1,
+                           nsv.F32 if dtype == "f32" else nsv.BF16)
+    ws = torch.empty(nsv.chunk_workspace_bytes(shape, len(q)), dtype=torch.uint8, device="cuda")
+    run = lambda: nsv.paged_chunk(q, k, v, bt, starts, ctx, a["scale"], out,  # noqa: E731
+                                  workspace=ws)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for b, t in ((c, tables[1]), (a, tables[0]), (c, tables[1])):
+        q.copy_(b["q"]), bt.copy_(t), starts.copy_(b["starts"]), ctx.copy_(b["ctx"])
+        out.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, big = reference(b)
+        live = sum(b["lens"][1])
+        tol = F32_TOL if dtype == "f32" else BF16_TOL
+        assert ((out[:live].double() - ref[:live]).abs().amax(-1) <= tol * big[:live]).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    bs = [batch([2000, 64], [64, 3], 8, 2, 128, "bf16", seed=s) for s in (16, 17)]
+    outs = [torch.empty_like(b["q"]) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, o, st in zip(bs, outs, streams):
+            nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o,
+                            stream=st)
+    torch.cuda.synchronize()
+    for b, o in zip(bs, outs):
+        ref, big = reference(b)
+        assert ((o.double() - ref).abs().amax(-1) <= BF16_TOL * big).all()
