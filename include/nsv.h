@@ -114,9 +114,15 @@ enum {
                                that row's K/V was not written */
     NSV_DEV_TIMEOUT = 8u,   /* an in-kernel wait gave up after its limit and the
                                kernel returned early; results are invalid */
-    NSV_DEV_BAD_CHUNK = 16u /* chunk starts that are not an ascending pair within
+    NSV_DEV_BAD_CHUNK = 16u,/* chunk starts that are not an ascending pair within
                                [0, tokens]; the row was read as having no new
                                tokens */
+    NSV_DEV_BAD_ROW = 32u,  /* a row id outside [0, rows), a fork into a row that
+                               is not empty or was named before, or a row to
+                               extend whose last, partly filled block is not its
+                               own alone; skipped */
+    NSV_DEV_NO_BLOCKS = 64u /* the pool has too few free blocks for a fork or an
+                               extension; that row was left as it was */
 };
 
 /* Sizes of one decode batch.  Limits: 0 <= rows <= 8192; num_heads a
@@ -484,6 +490,91 @@ NSV_API int nsv_chunk_step(const nsv_shape *shape, const nsv_scores *scores, int
                            const int32_t *block_tables, const int32_t *chunk_starts,
                            const int32_t *context_lens, float scale, void *out,
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Page operators: the allocator of the paged cache, on the device.
+ *
+ * Its state is block_refs [num_blocks] int32, the number of block-table entries
+ * (within the rows' context lengths) that name each block; a block with 0 is
+ * free.  An empty cache is all zeros.  The sink block is not counted.  All
+ * operators run on `stream` without a host round trip, may be captured, and
+ * deal out free blocks lowest id first, in the order of their rows or forks: the
+ * same state gives the same result.  Rows may share blocks: only full blocks
+ * are ever shared, so that a row appends to a block of its own.
+ *
+ * They use shape.rows, max_blocks, num_blocks, block_size, and, where blocks
+ * are copied, num_kv_heads, head_dim and dtype (the rest must be valid).
+ * Data pointers must be 16-byte aligned, index arrays to their element.
+ * workspace: at least the bytes nsv_pages_workspace gives, 256-byte aligned,
+ * owned by the caller, uninitialised; operators that overlap on the GPU need
+ * one each, and must not work on the same cache.
+ */
+NSV_API int nsv_pages_workspace(const nsv_shape *shape, int64_t *bytes);
+
+/*
+ * Copy blocks: for i < count, block dst[i] of both pools receives block src[i],
+ * bit for bit.  The destinations must be distinct and none may be a source of
+ * another pair (the contents of such blocks are unspecified).  A pair of two -1
+ * is a filler and does nothing; an id outside [0, num_blocks] is skipped and
+ * sets NSV_DEV_BAD_BLOCK.  src, dst: device memory, int32.
+ */
+NSV_API int nsv_blocks_copy(const nsv_shape *shape, int32_t count, const int32_t *src,
+                            const int32_t *dst, void *k_pool, void *v_pool,
+                            cudaStream_t stream);
+
+/*
+ * Fork rows: for i < count (at most shape.rows), row children[i], which must be
+ * empty, becomes a copy of row parents[i] as it was before the call: it names the
+ * parent's full blocks (their references grow), and a partly filled last block
+ * is copied into a free one.  A parent may be forked many times; a child that is
+ * named twice belongs to its first fork.  A fork is refused when the blocks that
+ * it and all forks before it need exceed the free ones (NSV_DEV_NO_BLOCKS), and
+ * its child stays empty.  A pair of two -1 is a filler.  Table entries past the
+ * child's blocks are left as they were.  parents, children: device memory, int32.
+ */
+NSV_API int nsv_rows_fork(const nsv_shape *shape, int32_t count, const int32_t *parents,
+                          const int32_t *children, int32_t *block_tables,
+                          int32_t *context_lens, int32_t *block_refs, void *k_pool,
+                          void *v_pool, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/*
+ * Extend rows: row r grows by its chunk_starts[r + 1] - chunk_starts[r] new
+ * tokens: its context length counts them, its table gets the free blocks they
+ * need, and write_slots [tokens] (int64) gets every new token's slot, which is
+ * what nsv_chunk_step takes (tokens of no row get the sink slot).  A row is
+ * refused when the blocks that it and all rows before it need exceed the free
+ * ones (NSV_DEV_NO_BLOCKS), or when it would outgrow its table
+ * (NSV_DEV_BAD_CTX); it stays as it was and its tokens get the sink slot.
+ */
+NSV_API int nsv_rows_extend(const nsv_shape *shape, int64_t tokens,
+                            const int32_t *chunk_starts, int32_t *block_tables,
+                            int32_t *context_lens, int32_t *block_refs,
+                            int64_t *write_slots, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
+ * Free rows: for i < count, every block of row rows_list[i] loses a reference
+ * (at 0 it is free), its table entries become -1 and its context length 0.  An
+ * empty row, or one named before, has nothing to free; -1 is a filler.  An entry
+ * that names a block outside the pool, or a free one, sets NSV_DEV_BAD_BLOCK; a
+ * context length outside its range sets NSV_DEV_BAD_CTX and becomes 0.
+ */
+NSV_API int nsv_rows_free(const nsv_shape *shape, int32_t count, const int32_t *rows_list,
+                          int32_t *block_tables, int32_t *context_lens, int32_t *block_refs,
+                          cudaStream_t stream);
+
+/*
+ * Compact the pool: with n blocks in use, those with ids at and past n move, in
+ * order, into the free ones below n, in order, so that the used blocks are [0, n)
+ * and the pool's tail can be given back.  Table entries of all rows (within
+ * their context lengths) and block_refs follow.  Contents of blocks that are
+ * free afterwards are unspecified.
+ */
+NSV_API int nsv_blocks_compact(const nsv_shape *shape, int32_t *block_tables,
+                               const int32_t *context_lens, int32_t *block_refs,
+                               void *k_pool, void *v_pool, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Self-test of the bounded wait (the pages have no counterpart; this checks

@@ -21,6 +21,10 @@ The chunk attention (paged_chunk, chunk_step) takes ragged batches instead:
                   chunk_starts[r + 1] - 1
   slopes          [num_heads] float32; see_begin, see_end [tokens] int32
 
+The page operators (blocks_copy, rows_fork, rows_extend, rows_free,
+blocks_compact) keep block_refs [num_blocks] int32, the references to each
+block (0: free), with the tables and lengths, and change them in place.
+
 Importing this module loads the library and raises ImportError if it has not
 been built (``python -m paged_kv_decode_nsv_gb300.build``); there is no
 fallback path.
@@ -42,7 +46,8 @@ ABI_VERSION = 102  # the layout of Shape and Plan below
 F32, BF16 = 0, 1
 (CONSUMER_AUTO, CONSUMER_CUDA, CONSUMER_TENSOR, CONSUMER_TENSOR_VECTOR_ROWS,
  CONSUMER_TENSOR_TMEM) = 0, 1, 2, 3, 4
-DEV_BAD_CTX, DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_BAD_CHUNK = 1, 2, 4, 8, 16
+DEV_BAD_CTX, DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_CHUNK, DEV_BAD_ROW, DEV_NO_BLOCKS = 16, 32, 64
 ERRORS = {0: "NSV_OK", -1: "NSV_ERR_NULLPTR", -2: "NSV_ERR_DTYPE", -3: "NSV_ERR_SHAPE",
           -4: "NSV_ERR_ALIGN", -5: "NSV_ERR_RANGE", -6: "NSV_ERR_CAPTURE", -7: "NSV_ERR_CUDA",
           -8: "NSV_ERR_WORKSPACE", -10: "NSV_ERR_UNSUPPORTED"}
@@ -112,6 +117,16 @@ _lib.nsv_paged_chunk.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _v
 _lib.nsv_chunk_step.restype = _i32
 _lib.nsv_chunk_step.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp, _vp, _f, _vp, _vp, _sz, _vp]
+_lib.nsv_pages_workspace.restype = _i32
+_lib.nsv_pages_workspace.argtypes = [_SP, ctypes.POINTER(_i64)]
+_i32c = ctypes.c_int32
+for _name, _args in (("blocks_copy", [_i32c, _vp, _vp, _vp, _vp, _vp]),
+                     ("rows_fork", [_i32c, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+                     ("rows_extend", [_i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+                     ("rows_free", [_i32c, _vp, _vp, _vp, _vp, _vp]),
+                     ("blocks_compact", [_vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])):
+    getattr(_lib, "nsv_" + _name).restype = _i32
+    getattr(_lib, "nsv_" + _name).argtypes = [_SP] + _args
 _lib.nsv_device_status.restype = _i32
 _lib.nsv_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32),
                                    ctypes.POINTER(ctypes.c_uint64), _i32]
@@ -438,6 +453,116 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
                                ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr, ws_ptr,
                                ws_bytes, _stream(stream)), "nsv_chunk_step")
     return out
+
+
+def pages_workspace_bytes(rows, num_blocks):
+    """Workspace bytes of rows_fork, rows_extend and blocks_compact."""
+    n = _i64(0)
+    shape = make_shape(rows, 1, 1, 64, 1, num_blocks, F32)
+    _check(_lib.nsv_pages_workspace(ctypes.byref(shape), ctypes.byref(n)), "nsv_pages_workspace")
+    return n.value
+
+
+def _pool_args(k_pool, v_pool, num_blocks, dev):
+    if k_pool.dim() != 4:
+        raise ValueError("the pools must be [blocks + 1, kv_heads, 16, head_dim]")
+    if num_blocks is not None and k_pool.shape[0] != num_blocks + 1:
+        raise ValueError("the pools have %d blocks and the sink, block_refs %d"
+                         % (k_pool.shape[0] - 1, num_blocks))
+    return (_arg(k_pool, "k_pool", k_pool.dtype, k_pool.shape, dev),
+            _arg(v_pool, "v_pool", k_pool.dtype, k_pool.shape, dev))
+
+
+def _cache_args(block_tables, context_lens, block_refs, dev):
+    import torch
+    i32 = torch.int32
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [rows, max_blocks]")
+    return (_arg(block_tables, "block_tables", i32, block_tables.shape, dev),
+            _arg(context_lens, "context_lens", i32, (block_tables.shape[0],), dev),
+            _arg(block_refs, "block_refs", i32, (-1,), dev))
+
+
+def _page_shape(block_tables, num_blocks, k_pool=None):
+    R, MB = block_tables.shape if block_tables is not None else (0, 1)
+    if k_pool is None:
+        return make_shape(R, 1, 1, 64, MB, num_blocks, F32)
+    _, Hkv, B, D = k_pool.shape
+    return make_shape(R, Hkv, Hkv, D, MB, num_blocks, _dtype_code(k_pool), B)
+
+
+def blocks_copy(src_blocks, dst_blocks, k_pool, v_pool, stream=None):
+    """Copy blocks src_blocks[i] of both pools to dst_blocks[i] (int32 tensors)."""
+    import torch
+    dev = _current_device()
+    pools = _pool_args(k_pool, v_pool, None, dev)
+    n = src_blocks.numel()
+    shape = _page_shape(None, k_pool.shape[0] - 1, k_pool)
+    _check(_lib.nsv_blocks_copy(ctypes.byref(shape), n,
+                                _arg(src_blocks, "src_blocks", torch.int32, (n,), dev),
+                                _arg(dst_blocks, "dst_blocks", torch.int32, (n,), dev), *pools,
+                                _stream(stream)), "nsv_blocks_copy")
+
+
+def rows_fork(parents, children, block_tables, context_lens, block_refs, k_pool, v_pool,
+              workspace=None, stream=None):
+    """Make empty rows children[i] copies of rows parents[i] (int32 tensors):
+    full blocks are shared, a partly filled last one is copied."""
+    import torch
+    dev = _current_device()
+    cache = _cache_args(block_tables, context_lens, block_refs, dev)
+    pools = _pool_args(k_pool, v_pool, block_refs.numel(), dev)
+    n = parents.numel()
+    shape = _page_shape(block_tables, block_refs.numel(), k_pool)
+    ids = (_arg(parents, "parents", torch.int32, (n,), dev),
+           _arg(children, "children", torch.int32, (n,), dev))
+    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
+    _check(_lib.nsv_rows_fork(ctypes.byref(shape), n, *ids, *cache, *pools, ws_ptr, ws_bytes,
+                              _stream(stream)), "nsv_rows_fork")
+
+
+def rows_extend(chunk_starts, block_tables, context_lens, block_refs, write_slots, workspace=None,
+                stream=None):
+    """Grow each row by its new tokens: blocks, lengths, and the tokens' write
+    slots (int64 [tokens]), as chunk_step takes them."""
+    import torch
+    dev = _current_device()
+    cache = _cache_args(block_tables, context_lens, block_refs, dev)
+    starts = _arg(chunk_starts, "chunk_starts", torch.int32, (block_tables.shape[0] + 1,), dev)
+    T = write_slots.numel()
+    slots = _arg(write_slots, "write_slots", torch.int64, (T,), dev)
+    shape = _page_shape(block_tables, block_refs.numel())
+    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
+    _check(_lib.nsv_rows_extend(ctypes.byref(shape), T, starts, *cache, slots, ws_ptr, ws_bytes,
+                                _stream(stream)), "nsv_rows_extend")
+    return write_slots
+
+
+def rows_free(rows, block_tables, context_lens, block_refs, stream=None):
+    """Free the rows listed in `rows` (an int32 tensor)."""
+    import torch
+    dev = _current_device()
+    cache = _cache_args(block_tables, context_lens, block_refs, dev)
+    n = rows.numel()
+    shape = _page_shape(block_tables, block_refs.numel())
+    _check(_lib.nsv_rows_free(ctypes.byref(shape), n, _arg(rows, "rows", torch.int32, (n,), dev),
+                              *cache, _stream(stream)), "nsv_rows_free")
+
+
+def blocks_compact(block_tables, context_lens, block_refs, k_pool, v_pool, workspace=None,
+                   stream=None):
+    """Move the blocks in use to the front of the pool; tables and references
+    follow."""
+    dev = _current_device()
+    cache = _cache_args(block_tables, context_lens, block_refs, dev)
+    pools = _pool_args(k_pool, v_pool, block_refs.numel(), dev)
+    shape = _page_shape(block_tables, block_refs.numel(), k_pool)
+    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
+    _check(_lib.nsv_blocks_compact(ctypes.byref(shape), *cache, *pools, ws_ptr, ws_bytes,
+                                   _stream(stream)), "nsv_blocks_compact")
 
 
 def selftest_bounded_wait(limit_ns, stream=None):
