@@ -11,13 +11,14 @@
 // product, as its tensor-core operand: half an ulp each (2^-9 relative),
 // which is what rounding the output costs anyway.
 //
-// One CTA per SM, ten warps:
+// One CTA per SM, twelve warps:
 //   warps 0-3, 4-7  softmax of stream 0 and stream 1: thread r of a stream owns
 //                   MMA row r (TMEM lane r): its scores, its state, its output
 //   warp 8          TMA producer: query rows, then K and V of each run, block by
 //                   block through the block table, into a ring of stages
 //   warp 9          MMA issue: S = Q.K^T (both operands in shared memory) and
 //                   O += P.V (P in tensor memory), accumulators in tensor memory
+//   warps 10, 11    idle: they complete the warpgroup that gives registers away
 // The rows of an MMA are the tile's query tokens times the query heads that
 // share the KV head, so K and V are read once for all of them.  A tile with
 // more than 128 rows gives each stream its half of the rows and both the same
@@ -39,7 +40,12 @@ namespace {
 
 using namespace sm;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers per thread: 168 at launch (12 warps); the two softmax warpgroups
+// (whose threads hold a row's 128 scores) take 208 from the third's share:
+// 2 x 208 + 80 = 496 <= 3 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "more registers than the launch has");
 constexpr int kStreamWarps = 4;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
@@ -374,32 +380,31 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
         // were issued after them.
         if (!fresh && __any_sync(kFull, raise)) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(t_o + x * D + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(t_o + x * D + c * 16, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(t_o + x * D + c * 32, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st16(t_o + x * D + c * 16, o);
           }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int c = h * 64 + 2 * k;
+          for (int k = 0; k < 16; ++k) {
             float a, b;
-            fma2(a, b, __uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1]),
-                 mul, mul, neg, neg);
+            fma2(a, b, __uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]), mul, mul,
+                 neg, neg);
             a = ex2_approx(a);
             b = ex2_approx(b);
             add2(l0, l1, a, b);
             w[k] = pack_bf16(a, b);
           }
-          tmem_st32(t_s + h * 32, w);
+          tmem_st16(t_s + c * 16, w);
         }
         l += l0 + l1;
         tmem_wait_st();
@@ -532,17 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   wk.init(p, blockIdx.x, lane);
   bool ok = true;
   if (warp < 8) {
+    regs_raise<kRegsSoftmax>();
     ok = softmax<D, CAP, BIAS>(p, B, smem0, smem, tmem, s_meta,
                                reinterpret_cast<volatile int*>(smem + L::kOffWords) + 2, wk, warp,
                                lane);
-  } else if (warp == 8) {
+  } else {
+    regs_drop<kRegsOther>();
+  }
+  if (warp == 8) {
     uint32_t i = 0, nq = 0;
     ok = produce<D>(p, B, smem0, s_meta, wk, lane, i, nq);
     // every copy issued lands before the CTA can end, even after a timeout
     for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
     if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
-  } else {
+  } else if (warp == 9) {
     ok = issue_mma<D>(p, B, smem0, tmem, wk, lane == 0);
     umma_commit(B.drained(), lane == 0);  // arrives once every MMA issued is done
     (void)mbar_wait(B.drained(), 0);
