@@ -54,6 +54,13 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
   // Every row's last tile may be partial.
   W.max_tiles = (int)(rows + tokens / tt);
   W.tile_rows = (int)(tokens < tt ? tokens : tt) * group;
+  // bf16: a tile of few rows leaves up to four partial states per row, of at
+  // most 128 rows together
+  if (dtype == NSV_BF16) {
+    const long long four = 4 * tokens * group;
+    const int copies = four < kChunkHalfRows ? (int)four : kChunkHalfRows;
+    if (copies > W.tile_rows) W.tile_rows = copies;
+  }
   auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
   W.off_prefix = 256;
   W.off_tiles = W.off_prefix + up((uint64_t)(W.max_tiles + 1) * 8);
@@ -65,7 +72,8 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
 }
 
 struct ChunkParams {
-  CUtensorMap tmap_q, tmap_k, tmap_v;  // bf16 only
+  // bf16 only; tmap_q: boxes of 128, 64 and 32 MMA rows
+  CUtensorMap tmap_q[3], tmap_k, tmap_v;
   const void* q;
   const void* k_pool;
   const void* v_pool;
@@ -201,27 +209,114 @@ __device__ __forceinline__ int chunk_slot(int c, bool starts_tile) {
 
 // Merge of a cut tile by the warps of the CTA whose piece arrived last (nw
 // warps, this one w): out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over
-// the pieces i.  Each warp takes every nw-th row; its 32 lanes hold the row's
-// head_dim values.  A row that saw nothing in any piece gives 0.
-template <typename T, int D>
-__device__ __forceinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& wk,
-                                            const ChunkSegment& s, int w, int nw, int lane) {
+// the pieces i, in their order.  A piece holds `copies` states per row, row after
+// row within a copy.  A row that saw nothing in any piece gives 0.
+//
+// The states were just written by other SMs, so every load is an L2 round trip
+// (about 0.4 us) and what counts is how many are in flight: a warp takes up to
+// 32 consecutive rows, finds all their maxima and sums at once (a group of
+// lanes per row, the states dealt out to the lanes), then sums NR rows x NS
+// states per round, each row's head_dim values over the 32 lanes.  (One row at a
+// time, as first written, took 40 us for a tile of 256 rows.)
+struct ChunkMerge {
+  const ChunkParams& p;
+  const ChunkSegment& s;
+  int c0, n, rows, shift;
+  // workspace row of state i of tile row r
+  __device__ __forceinline__ size_t at(int i, int r) const {
+    const int c = c0 + (i >> shift);
+    return (size_t)chunk_slot(c, c == c0) * p.tile_rows + (i & ((1 << shift) - 1)) * rows + r;
+  }
+};
+
+// Rows r0 .. r0 + count - 1, whose maxima and inverse sums lane k * group holds
+// for row r0 + k.
+template <typename T, int D, int NR, int NS>
+__device__ __forceinline__ void chunk_merge_rows(const ChunkMerge& m, int r0, int count, int group,
+                                                 float M, float inv, int lane) {
   constexpr int kPer = D / 32;
+  const ChunkParams& p = m.p;
+  for (int k0 = 0; k0 < count; k0 += NR) {
+    float a[NR][kPer], Mk[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      Mk[k] = __shfl_sync(sm::kFull, M, min(k0 + k, count - 1) * group);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) a[k][e] = 0.f;
+    }
+    for (int b = 0; b < m.n; b += NS) {
+      float x[NR][NS][kPer], wt[NR][NS];
+#pragma unroll
+      for (int k = 0; k < NR; ++k)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const size_t at = m.at(min(b + i, m.n - 1), r0 + min(k0 + k, count - 1));
+          wt[k][i] = __ldcg(p.ws_ml + at).x;
+          const float* src = p.ws_acc + at * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            x[k][i][0] = v.x, x[k][i][1] = v.y, x[k][i][2] = v.z, x[k][i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            x[k][i][0] = v.x, x[k][i][1] = v.y;
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < NR; ++k)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          // (a state that saw nothing may hold anything)
+          const float w =
+              (b + i >= m.n || wt[k][i] == -INFINITY) ? 0.f : exp2f(wt[k][i] - Mk[k]);
+          if (w != 0.f)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) a[k][e] = fmaf(w, x[k][i][e], a[k][e]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const float iv = __shfl_sync(sm::kFull, inv, min(k0 + k, count - 1) * group);
+      if (k0 + k >= count) continue;
+      const int r = r0 + k0 + k, tok = r / p.group, g = r - tok * p.group;
+      T* o = static_cast<T*>(p.out) +
+             (((size_t)m.s.t.q0 + tok) * p.heads + m.s.head * p.group + g) * D + lane * kPer;
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+          *reinterpret_cast<float2*>(o + e) = make_float2(a[k][e] * iv, a[k][e + 1] * iv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+          *reinterpret_cast<uint32_t*>(o + e) = sm::pack_bf16(a[k][e] * iv, a[k][e + 1] * iv);
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+__device__ __noinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& wk,
+                                         const ChunkSegment& s, int copies, int w, int nw,
+                                         int lane) {
   const long long u0 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile);
   const long long u1 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile + 1);
   const int c0 = wk.cta_of(u0), c1 = wk.cta_of(u1 - 1);
-  const int rows = s.t.n_tok * p.group;
-  for (int r = w; r < rows; r += nw) {
+  const ChunkMerge m{p, s, c0, (c1 - c0 + 1) * copies, s.t.n_tok * p.group,
+                     copies == 4 ? 2 : copies == 2 ? 1 : 0};
+  const int per = min(32, (m.rows + nw - 1) / nw);  // rows of a warp at a time
+  int group = 32;                                    // lanes per row
+  while (group * per > 32) group >>= 1;
+  for (int r0 = w * per; r0 < m.rows; r0 += nw * per) {
+    const int count = min(per, m.rows - r0);
+    const int r = r0 + min(lane / group, count - 1);
     float M = -INFINITY, L = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 ml = __ldcg(p.ws_ml + (size_t)chunk_slot(c, c == c0) * p.tile_rows + r);
+    for (int i = lane % group; i < m.n; i += group) {
+      const float2 ml = __ldcg(p.ws_ml + m.at(i, r));
       if (ml.x == -INFINITY) continue;
       const float mn = fmaxf(M, ml.x);
       L = L * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
       M = mn;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int o = 1; o < group; o <<= 1) {
       const float Mo = __shfl_xor_sync(sm::kFull, M, o), Lo = __shfl_xor_sync(sm::kFull, L, o);
       const float mn = fmaxf(M, Mo);
       if (mn != -INFINITY) {
@@ -229,45 +324,11 @@ __device__ __forceinline__ void chunk_merge(const ChunkParams& p, const ChunkWal
         M = mn;
       }
     }
-    float a[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
-    for (int cb = c0; cb <= c1; cb += 4) {
-      float x[4][kPer], wt[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = min(cb + i, c1);
-        const size_t at = (size_t)chunk_slot(c, c == c0) * p.tile_rows + r;
-        const float2 ml = __ldcg(p.ws_ml + at);
-        wt[i] = (cb + i > c1 || ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-        const float* src = p.ws_acc + at * D + lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          x[i][0] = v.x, x[i][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (wt[i] != 0.f)
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) a[e] = fmaf(wt[i], x[i][e], a[e]);
-    }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int tok = r / p.group, g = r - tok * p.group;
-    T* o = static_cast<T*>(p.out) +
-           (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D + lane * kPer;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<float2*>(o + e) = make_float2(a[e] * inv, a[e + 1] * inv);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<uint32_t*>(o + e) = sm::pack_bf16(a[e] * inv, a[e + 1] * inv);
-    }
+    if (count >= 4)
+      chunk_merge_rows<T, D, 8, 2>(m, r0, count, group, M, inv, lane);
+    else
+      chunk_merge_rows<T, D, 1, 8>(m, r0, count, group, M, inv, lane);
   }
 }
 

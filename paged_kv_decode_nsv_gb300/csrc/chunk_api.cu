@@ -52,14 +52,17 @@ bool encode_pool(const DeviceInfo& d, const nsv_shape* s, const void* pool, CUte
 }
 
 // The query tokens as [head_dim][heads][tokens]; one box is 64 dims of the
-// query heads of one KV head for one half's tokens.
-bool encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int half_tokens,
-              const void* q, CUtensorMap* map) {
+// query heads of one KV head for as many tokens as fit `rows` MMA rows (no map
+// where not even one does).
+bool encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows, const void* q,
+              CUtensorMap* map) {
+  const int box_tokens = rows / (s->num_heads / s->num_kv_heads);
+  if (box_tokens == 0) return true;
   const cuuint64_t D = (cuuint64_t)s->head_dim, H = (cuuint64_t)s->num_heads;
   const cuuint64_t dims[3] = {D, H, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {D * 2, D * 2 * H};
   const cuuint32_t box[3] = {64u, (cuuint32_t)(s->num_heads / s->num_kv_heads),
-                             (cuuint32_t)half_tokens};
+                             (cuuint32_t)box_tokens};
   const cuuint32_t one[3] = {1u, 1u, 1u};
   return d.encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
                   box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -126,7 +129,9 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
   p.cap = sc ? sc->softcap : 0.f;
   if (s->dtype == NSV_BF16 &&
-      (!encode_q(d, s, tokens, p.tile_tokens / 2, q, &p.tmap_q) ||
+      (!encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||
+       !encode_q(d, s, tokens, kChunkHalfRows / 2, q, &p.tmap_q[1]) ||
+       !encode_q(d, s, tokens, kChunkHalfRows / 4, q, &p.tmap_q[2]) ||
        !encode_pool(d, s, k_pool, &p.tmap_k) || !encode_pool(d, s, v_pool, &p.tmap_v)))
     return cuda_fail();
   if (append && launch_kv_write(*append, stream) != cudaSuccess) return cuda_fail();

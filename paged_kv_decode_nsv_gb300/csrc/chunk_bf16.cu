@@ -25,6 +25,10 @@
 // keys; a smaller tile gives both streams the same rows and every other run of
 // keys, and the two states are joined at the end.  Either way one stream's
 // softmax runs while the tensor core works for the other.
+// A tile of at most 64 or 32 rows is laid out 2 or 4 times over the 128 MMA
+// rows, and each copy takes its part of every run's keys (the probabilities of
+// the rest are zeros), so that all warps share the softmax of a few rows; the
+// copies' states are joined like the pieces of a cut tile.
 //
 // Tensor memory (512 columns): S of stream x at 128 x, its probabilities over
 // the first 64 of them, O of stream x at 256 + D x.
@@ -90,9 +94,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(kFull, mbar_wait(bar, parity));
 }
 
-// Whether a tile's rows need both halves.
-__device__ __forceinline__ bool is_pair(const ChunkParams& p, const ChunkSegment& s) {
-  return s.t.n_tok * 2 > p.tile_tokens;
+// How a tile's rows lie: 0: over both halves; else how many copies of them one
+// half holds.
+__device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegment& s) {
+  const int rows = s.t.n_tok * p.group;
+  return s.t.n_tok * 2 > p.tile_tokens          ? 0
+         : rows <= kChunkHalfRows / 4           ? 4
+         : rows <= kChunkHalfRows / 2           ? 2
+                                                : 1;
 }
 
 // ------------------------------------------------------------------ producer
@@ -106,16 +115,22 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
   uint32_t run = 0;
   ChunkSegment s;
   while (wk.next(p, s)) {
-    // the query rows: one box of (tokens, group heads, 64 dims) per half and
-    // 64-dim slice; tokens past the tensor are filled with zeros
+    // the query rows: one box of (tokens, group heads, 64 dims) per half or
+    // copy and 64-dim slice; tokens past the tensor are filled with zeros
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
-    const int halves = is_pair(p, s) ? 2 : 1;
+    const int copies = copies_of(p, s);
     if (lane == 0) {
-      mbar_arrive_tx(B.qfull(), (uint32_t)(halves * half_tok * p.group * D * 2));
-      for (int x = 0; x < halves; ++x)
+      const int boxes = copies == 0 ? 2 : copies;
+      const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
+      const int box_tok = box_rows / p.group;
+      const CUtensorMap* map = &p.tmap_q[copies == 4 ? 2 : copies == 2 ? 1 : 0];
+      mbar_arrive_tx(B.qfull(), (uint32_t)(boxes * box_tok * p.group * D * 2));
+      for (int x = 0; x < boxes; ++x)
         for (int d = 0; d < D / 64; ++d)
-          tma_load_3d(smem0 + L::kOffQ + x * L::kHalf + d * (kChunkHalfRows * 128), &p.tmap_q,
-                      d * 64, s.head * p.group, s.t.q0 + x * half_tok, B.qfull());
+          tma_load_3d(smem0 + L::kOffQ + (copies == 0 ? x * L::kHalf : x * box_rows * 128) +
+                          d * (kChunkHalfRows * 128),
+                      map, d * 64, s.head * p.group, s.t.q0 + (copies == 0 ? x * half_tok : 0),
+                      B.qfull());
     }
     ++nseg;
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
@@ -189,7 +204,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
   ChunkSegment s;
   while (wk.next(p, s)) {
     const int n = s.j1 - s.j0;
-    const bool pair = is_pair(p, s);
+    const bool pair = copies_of(p, s) == 0;
     if (!warp_wait(B.qfull(), nseg & 1)) return false;
     // before O is written again: the previous segment's has been read
     auto free_o = [&]() { return nseg == 0 || warp_wait(B.ofree(), (nseg - 1) & 1); };
@@ -269,6 +284,119 @@ __device__ __forceinline__ float capped(float s, float cap_z, float cap_out) {
   return (z2 < 0.0625f ? small : big) * cap_out;
 }
 
+// The state of one row of a stream, as its thread holds it.
+struct RowState {
+  bool valid, fresh;  // whether the row exists; whether O holds nothing yet
+  int pos;            // the query token's position
+  int2 see;           // what it sees
+  float slope;        // slope * log2(e)
+  float m, l;         // running maximum (log2 units) and sum
+};
+
+// Folds NCH x 32 keys of one run (columns col0 .. of the scores t_s) into a row:
+// maximum, rescale of O (t_o) where it rises, probabilities over the scores.
+template <int D, bool CAP, bool BIAS, int NCH>
+__device__ __forceinline__ void fold_run(const ChunkParams& p, RowState& f, uint32_t t_s,
+                                         uint32_t t_o, int t0, int col0, int mask) {
+  uint32_t sr[NCH][32];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) tmem_ld32(t_s + col0 + c * 32, sr[c]);
+  tmem_wait_ld();
+  float mul = p.qscale;
+  if constexpr (CAP || BIAS) {
+    mul = 1.f;
+    const float d0 = (float)(f.pos - t0 - col0);
+    const float cap_z = CAP ? p.scale / p.cap : 0.f, cap_out = p.cap * 1.4426950408889634f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        float v = __uint_as_float(sr[c][k]);
+        v = CAP ? capped(v, cap_z, cap_out) : v * p.qscale;
+        if (BIAS) v = fmaf(-f.slope, fabsf(d0 - (float)(c * 32 + k)), v);
+        sr[c][k] = __float_as_uint(v);
+      }
+  }
+  // positions that the row does not see; nothing to mask in most runs
+  const int lo = f.see.x - t0, hi = f.see.y - t0;
+  const bool dense = mask == 0xff && lo <= col0 && hi >= col0 + 32 * NCH && mul > 0.f;
+  if (!__all_sync(kFull, dense)) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int cc = col0 + 32 * c;
+      const int a = min(max(lo - cc, 0), 32), b = min(max(hi - cc, 0), 32);
+      uint32_t bits = (b == 32 ? ~0u : (1u << b) - 1u) & ~(a == 32 ? ~0u : (1u << a) - 1u);
+      const int bm = mask >> (cc / kBlock);
+      bits &= ((bm & 1) ? 0xffffu : 0u) | ((bm & 2) ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float v = __uint_as_float(sr[c][k]) * mul;
+        sr[c][k] = __float_as_uint((bits >> k) & 1u ? v : -INFINITY);
+      }
+    }
+    mul = 1.f;
+  }
+  float mxs[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    mxs[c] = fmaxf(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
+#pragma unroll
+    for (int k = 2; k < 32; k += 2)
+      mxs[c] = fmaxf(mxs[c], fmaxf(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])));
+  }
+  float mx = mxs[0];
+#pragma unroll
+  for (int c = 1; c < NCH; ++c) mx = fmaxf(mx, mxs[c]);
+  mx *= mul;
+  const bool raise = f.valid && mx > f.m + kSlack;  // also the first finite one
+  float alpha = 1.f;
+  if (raise) {
+    alpha = ex2_approx(f.m - mx);
+    f.m = mx;
+    f.l *= alpha;
+  }
+  // The products that O holds are complete: the scores just waited for were
+  // issued after them.
+  if (!f.fresh && __any_sync(kFull, raise)) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t o[16];
+      tmem_ld16(t_o + c * 16, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+      tmem_st16(t_o + c * 16, o);
+    }
+  }
+  const float neg = f.m == -INFINITY ? 0.f : -f.m;
+  float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float a, b;
+      fma2(a, b, __uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]), mul, mul, neg,
+           neg);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      add2(l0, l1, a, b);
+      w[k] = pack_bf16(a, b);
+    }
+    tmem_st16(t_s + col0 / 2 + c * 16, w);
+  }
+  if constexpr (NCH < 4) {  // the keys of the other copies
+    uint32_t zero[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) zero[k] = 0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c * 32 < col0 || c * 32 >= col0 + 32 * NCH) tmem_st16(t_s + c * 16, zero);
+  }
+  f.l += l0 + l1;
+  tmem_wait_st();
+}
+
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
                                         unsigned char* smem, uint32_t tmem,
@@ -282,7 +410,6 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
   const uint32_t t_s = tmem + lane_base + x * kChunkKeys;
   const uint32_t t_o = tmem + lane_base + kColO;
   const int half_tok = p.tile_tokens / 2;
-  const int ti = r / p.group, g = r - ti * p.group;
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
   uint32_t nscore = 0, nseg = 0, njoin = 0, run0 = 0;
   // all eight softmax warps meet
@@ -293,19 +420,29 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
   };
   ChunkSegment s;
   while (wk.next(p, s)) {
-    const bool pair = is_pair(p, s);
+    const int copies = copies_of(p, s);
+    const bool pair = copies == 0;
     const int n = s.j1 - s.j0;
+    // this thread's row within its half or copy, and its part of a run's keys:
+    // nch chunks of 32 columns from col0 on
+    const int shift = copies == 4 ? 2 : copies == 2 ? 1 : 0;
+    const int copy_rows = kChunkHalfRows >> shift;
+    const int copy = r / copy_rows, rc = r - copy * copy_rows;
+    const int nch = 4 >> shift, col0 = copy * 32 * nch;
+    const int ti = rc / p.group, g = rc - ti * p.group;
     const int tok = (pair && x ? half_tok : 0) + ti;  // query token within the tile
-    const bool valid = ti < half_tok && tok < s.t.n_tok;
+    const bool valid = ti < copy_rows / p.group && tok < s.t.n_tok;
     const bool any_valid = __any_sync(kFull, valid);
-    const int pos = s.t.pos0 + tok;
-    int2 see = make_int2(0, 0x7fffffff);  // rows that are not there mask nothing
-    if (valid) see = chunk_sees(p, (long long)s.t.q0 + tok, pos, s.t.ctx);
-    const float slope =
-        BIAS && valid ? __ldg(p.slopes + s.head * p.group + g) * 1.4426950408889634f : 0.f;
-    float m = -INFINITY, l = 0.f;
+    RowState f;
+    f.valid = valid;
+    f.fresh = true;
+    f.pos = s.t.pos0 + tok;
+    f.see = make_int2(0, 0x7fffffff);  // rows that are not there mask nothing
+    if (valid) f.see = chunk_sees(p, (long long)s.t.q0 + tok, f.pos, s.t.ctx);
+    f.slope = BIAS && valid ? __ldg(p.slopes + s.head * p.group + g) * 1.4426950408889634f : 0.f;
+    f.m = -INFINITY;
+    f.l = 0.f;
     const int step = pair ? 1 : 2;
-    bool fresh = true;
     for (int j = s.j0 + (pair ? 0 : x); j < s.j1; j += step) {
       const uint32_t run = run0 + (uint32_t)(j - s.j0);
       const int t0 = s.t.kb + j * kChunkKeys;
@@ -327,89 +464,14 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
         fence_proxy_async_smem();
       }
       if (any_valid) {
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, sr[c]);
-        tmem_wait_ld();
-        float mul = p.qscale;
-        if constexpr (CAP || BIAS) {
-          mul = 1.f;
-          const float d0 = (float)(pos - t0);
-          const float cap_z = CAP ? p.scale / p.cap : 0.f, cap_out = p.cap * 1.4426950408889634f;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            float v = __uint_as_float(sr[c >> 5][c & 31]);
-            v = CAP ? capped(v, cap_z, cap_out) : v * p.qscale;
-            if (BIAS) v = fmaf(-slope, fabsf(d0 - (float)c), v);
-            sr[c >> 5][c & 31] = __float_as_uint(v);
-          }
-        }
-        const int lo = see.x - t0, hi = see.y - t0;
-        const bool dense = mask == 0xff && lo <= 0 && hi >= kChunkKeys && mul > 0.f;
-        if (!__all_sync(kFull, dense)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int a = min(max(lo - 32 * c, 0), 32), b = min(max(hi - 32 * c, 0), 32);
-            uint32_t bits = (b == 32 ? ~0u : (1u << b) - 1u) & ~(a == 32 ? ~0u : (1u << a) - 1u);
-            const int bm = mask >> (2 * c);
-            bits &= ((bm & 1) ? 0xffffu : 0u) | ((bm & 2) ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float v = __uint_as_float(sr[c][k]) * mul;
-              sr[c][k] = __float_as_uint((bits >> k) & 1u ? v : -INFINITY);
-            }
-          }
-          mul = 1.f;
-        }
-        float mx4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx4[c] = __uint_as_float(sr[c][0]);
-#pragma unroll
-          for (int k = 1; k < 32; ++k) mx4[c] = fmaxf(mx4[c], __uint_as_float(sr[c][k]));
-        }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
-        const bool raise = valid && mx > m + kSlack;  // also the first finite one
-        float alpha = 1.f;
-        if (raise) {
-          alpha = ex2_approx(m - mx);
-          m = mx;
-          l *= alpha;
-        }
-        // The products that O holds are complete: the scores just waited for
-        // were issued after them.
-        if (!fresh && __any_sync(kFull, raise)) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(t_o + x * D + c * 16, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st16(t_o + x * D + c * 16, o);
-          }
-        }
-        const float neg = m == -INFINITY ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a, b;
-            fma2(a, b, __uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]), mul, mul,
-                 neg, neg);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            add2(l0, l1, a, b);
-            w[k] = pack_bf16(a, b);
-          }
-          tmem_st16(t_s + c * 16, w);
-        }
-        l += l0 + l1;
-        tmem_wait_st();
+        if (nch == 4)
+          fold_run<D, CAP, BIAS, 4>(p, f, t_s, t_o + x * D, t0, col0, mask);
+        else if (nch == 2)
+          fold_run<D, CAP, BIAS, 2>(p, f, t_s, t_o + x * D, t0, col0, mask);
+        else
+          fold_run<D, CAP, BIAS, 1>(p, f, t_s, t_o + x * D, t0, col0, mask);
       }
-      fresh = false;
+      f.fresh = false;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(B.probs(x));
@@ -419,32 +481,37 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
     // The segment's end: O is complete once its last product is.
     if (!warp_wait(B.out(x), nseg & 1)) return false;
     tc_fence_after();
-    const bool whole = s.first && s.last;
+    const bool alone = s.first && s.last;      // the tile is this CTA's
+    const bool whole = alone && copies <= 1;   // and its rows are complete here
     // columns of O that this thread writes, and the weights of the streams' O
-    int col0 = 0, ncol = D;
-    float w0 = 1.f, w1 = 0.f, L_ = l, M_ = m;
+    int c_lo = 0, c_n = D;
+    float w0 = 1.f, w1 = 0.f, L_ = f.l, M_ = f.m;
     if (!pair) {
-      s_ml[x * kChunkHalfRows + r] = make_float2(m, l);
+      s_ml[x * kChunkHalfRows + r] = make_float2(f.m, f.l);
       if (!join()) return false;
       const float2 other = s_ml[(x ^ 1) * kChunkHalfRows + r];
-      const float m0 = x ? other.x : m, m1 = x ? m : other.x;
-      const float l0 = x ? other.y : l, l1 = x ? l : other.y;
+      const float m0 = x ? other.x : f.m, m1 = x ? f.m : other.x;
+      const float l0 = x ? other.y : f.l, l1 = x ? f.l : other.y;
       M_ = fmaxf(m0, m1);
       w0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M_);
       w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M_);
       L_ = l0 * w0 + l1 * w1;
-      col0 = x * (D / 2);
-      ncol = D / 2;
+      c_lo = x * (D / 2);
+      c_n = D / 2;
     }
+    // (the join above, or this one: no warp still merges the previous tile from
+    // the slot that is written now)
+    if (pair && !whole && !join()) return false;
     const float inv = whole ? (L_ > 0.f ? 1.f / L_ : 0.f) : 1.f;
-    const int rr = tok * p.group + g;  // the row within the tile
+    // the row within the tile, after the copies before this one
+    const int rr = tok * p.group + g + copy * s.t.n_tok * p.group;
     const size_t piece =
         (size_t)chunk_slot(blockIdx.x, s.first) * p.tile_rows + (valid ? rr : 0);
     T* out = static_cast<T*>(p.out) +
              (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-      if (c * 32 < col0 || c * 32 >= col0 + ncol) continue;  // warp-uniform
+      if (c * 32 < c_lo || c * 32 >= c_lo + c_n) continue;  // warp-uniform
       uint32_t o[32];
       tmem_ld32(t_o + (pair ? x * D : 0) + c * 32, o);
       if (!pair && n > 1) {
@@ -486,12 +553,12 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
       if (!join()) return false;
       if (warp == 0 && lane == 0) {
         int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
+        *s_merge = alone || atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
       }
       if (!join()) return false;
       if (*s_merge) {
         __threadfence();
-        chunk_merge<T, D>(p, wk, s, warp, 2 * kStreamWarps, lane);
+        chunk_merge<T, D>(p, wk, s, copies < 1 ? 1 : copies, warp, 2 * kStreamWarps, lane);
       }
     }
   }

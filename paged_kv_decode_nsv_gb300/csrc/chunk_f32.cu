@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       __syncthreads();
       if (*s_merge) {
         __threadfence();
-        chunk_merge<float, D>(p, wk, s, warp, kThreadsF32 / 32, lane);
+        chunk_merge<float, D>(p, wk, s, 1, warp, kThreadsF32 / 32, lane);
       }
     }
   }
