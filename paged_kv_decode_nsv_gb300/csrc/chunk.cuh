@@ -41,7 +41,8 @@ __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
 //           position of the first}, {first key, one past the last key, ctx, 0}
 //   cnt     int32 [max_tiles][kv_heads]  pieces of a cut tile that finished
 //   ml      float2 [grid][2][tile_rows]  running max (log2 units) and sum
-//   acc     float [grid][2][tile_rows][head_dim]
+//   acc     float4 [grid][2][head_dim / 4][tile_rows]  unnormalised outputs; the
+//           rows are innermost, because a warp's lanes hold consecutive rows
 struct ChunkWs {
   uint64_t off_prefix, off_tiles, off_cnt, off_ml, off_acc, total;
   int max_tiles, tile_rows;
@@ -54,13 +55,6 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
   // Every row's last tile may be partial.
   W.max_tiles = (int)(rows + tokens / tt);
   W.tile_rows = (int)(tokens < tt ? tokens : tt) * group;
-  // bf16: a tile of few rows leaves up to four partial states per row, of at
-  // most 128 rows together
-  if (dtype == NSV_BF16) {
-    const long long four = 4 * tokens * group;
-    const int copies = four < kChunkHalfRows ? (int)four : kChunkHalfRows;
-    if (copies > W.tile_rows) W.tile_rows = copies;
-  }
   auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
   W.off_prefix = 256;
   W.off_tiles = W.off_prefix + up((uint64_t)(W.max_tiles + 1) * 8);
@@ -207,128 +201,108 @@ __device__ __forceinline__ int chunk_slot(int c, bool starts_tile) {
   return 2 * c + (starts_tile ? 1 : 0);
 }
 
-// Merge of a cut tile by the warps of the CTA whose piece arrived last (nw
-// warps, this one w): out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over
-// the pieces i, in their order.  A piece holds `copies` states per row, row after
-// row within a copy.  A row that saw nothing in any piece gives 0.
-//
-// The states were just written by other SMs, so every load is an L2 round trip
-// (about 0.4 us) and what counts is how many are in flight: a warp takes up to
-// 32 consecutive rows, finds all their maxima and sums at once (a group of
-// lanes per row, the states dealt out to the lanes), then sums NR rows x NS
-// states per round, each row's head_dim values over the 32 lanes.  (One row at a
-// time, as first written, took 40 us for a tile of 256 rows.)
-struct ChunkMerge {
-  const ChunkParams& p;
-  const ChunkSegment& s;
-  int c0, n, rows, shift;
-  // workspace row of state i of tile row r
-  __device__ __forceinline__ size_t at(int i, int r) const {
-    const int c = c0 + (i >> shift);
-    return (size_t)chunk_slot(c, c == c0) * p.tile_rows + (i & ((1 << shift) - 1)) * rows + r;
-  }
-};
+// A row's four output values at columns 4 v .. of one workspace slot.
+__device__ __forceinline__ float4* chunk_acc(const ChunkParams& p, int slot, int head_dim, int v,
+                                             int row) {
+  return reinterpret_cast<float4*>(p.ws_acc) +
+         ((size_t)slot * (head_dim / 4) + v) * p.tile_rows + row;
+}
 
-// Rows r0 .. r0 + count - 1, whose maxima and inverse sums lane k * group holds
-// for row r0 + k.
-template <typename T, int D, int NR, int NS>
-__device__ __forceinline__ void chunk_merge_rows(const ChunkMerge& m, int r0, int count, int group,
-                                                 float M, float inv, int lane) {
-  constexpr int kPer = D / 32;
-  const ChunkParams& p = m.p;
-  for (int k0 = 0; k0 < count; k0 += NR) {
-    float a[NR][kPer], Mk[NR];
+// Where a tile's row goes in `out`.
+template <typename T>
+__device__ __forceinline__ T* chunk_out(const ChunkParams& p, const ChunkSegment& s, int row,
+                                        int head_dim) {
+  const int tok = row / p.group, g = row - tok * p.group;
+  return static_cast<T*>(p.out) +
+         (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * head_dim;
+}
+
+// Merge of a cut tile by all NT threads of a group of the CTA whose piece
+// arrived last: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the
+// pieces i, in their order.  A row that saw nothing in any piece gives 0.
+//
+// The pieces were just written by other SMs, so a load is an L2 round trip
+// (about 0.5 us) and what counts is how many are in flight: a thread takes one
+// row and, where there are fewer rows than threads, a part of its columns, and
+// sums NV column groups x NS pieces per round.
+template <typename T, int D, int NV, int NS>
+__device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, int n, int row,
+                                                 int v0, int step, float M, float inv, T* out) {
+  for (int v = v0; v < D / 4; v += NV * step) {
+    float4 a[NV];
 #pragma unroll
-    for (int k = 0; k < NR; ++k) {
-      Mk[k] = __shfl_sync(sm::kFull, M, min(k0 + k, count - 1) * group);
+    for (int k = 0; k < NV; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < n; b += NS) {
+      float4 x[NV][NS];
+      float m[NS];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) a[k][e] = 0.f;
-    }
-    for (int b = 0; b < m.n; b += NS) {
-      float x[NR][NS][kPer], wt[NR][NS];
+      for (int i = 0; i < NS; ++i) {
+        const int j = min(b + i, n - 1), slot = chunk_slot(c0 + j, j == 0);
+        m[i] = __ldcg(p.ws_ml + (size_t)slot * p.tile_rows + row).x;
 #pragma unroll
-      for (int k = 0; k < NR; ++k)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const size_t at = m.at(min(b + i, m.n - 1), r0 + min(k0 + k, count - 1));
-          wt[k][i] = __ldcg(p.ws_ml + at).x;
-          const float* src = p.ws_acc + at * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-            x[k][i][0] = v.x, x[k][i][1] = v.y, x[k][i][2] = v.z, x[k][i][3] = v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            x[k][i][0] = v.x, x[k][i][1] = v.y;
-          }
-        }
-#pragma unroll
-      for (int k = 0; k < NR; ++k)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          // (a state that saw nothing may hold anything)
-          const float w =
-              (b + i >= m.n || wt[k][i] == -INFINITY) ? 0.f : exp2f(wt[k][i] - Mk[k]);
-          if (w != 0.f)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) a[k][e] = fmaf(w, x[k][i][e], a[k][e]);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < NR; ++k) {
-      const float iv = __shfl_sync(sm::kFull, inv, min(k0 + k, count - 1) * group);
-      if (k0 + k >= count) continue;
-      const int r = r0 + k0 + k, tok = r / p.group, g = r - tok * p.group;
-      T* o = static_cast<T*>(p.out) +
-             (((size_t)m.s.t.q0 + tok) * p.heads + m.s.head * p.group + g) * D + lane * kPer;
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2)
-          *reinterpret_cast<float2*>(o + e) = make_float2(a[k][e] * iv, a[k][e + 1] * iv);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2)
-          *reinterpret_cast<uint32_t*>(o + e) = sm::pack_bf16(a[k][e] * iv, a[k][e + 1] * iv);
+        for (int k = 0; k < NV; ++k)
+          x[k][i] = __ldcg(chunk_acc(p, slot, D, min(v + k * step, D / 4 - 1), row));
       }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (b + i >= n || m[i] == -INFINITY) continue;  // such a state may hold anything
+        const float w = exp2f(m[i] - M);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          a[k].x = fmaf(w, x[k][i].x, a[k].x);
+          a[k].y = fmaf(w, x[k][i].y, a[k].y);
+          a[k].z = fmaf(w, x[k][i].z, a[k].z);
+          a[k].w = fmaf(w, x[k][i].w, a[k].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (v + k * step >= D / 4) continue;
+      T* o = out + 4 * (v + k * step);
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(o) =
+            make_float4(a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv);
+      else
+        *reinterpret_cast<uint2*>(o) = make_uint2(sm::pack_bf16(a[k].x * inv, a[k].y * inv),
+                                                  sm::pack_bf16(a[k].z * inv, a[k].w * inv));
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 __device__ __noinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& wk,
-                                         const ChunkSegment& s, int copies, int w, int nw,
-                                         int lane) {
+                                         const ChunkSegment& s, int tid) {
   const long long u0 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile);
   const long long u1 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile + 1);
-  const int c0 = wk.cta_of(u0), c1 = wk.cta_of(u1 - 1);
-  const ChunkMerge m{p, s, c0, (c1 - c0 + 1) * copies, s.t.n_tok * p.group,
-                     copies == 4 ? 2 : copies == 2 ? 1 : 0};
-  const int per = min(32, (m.rows + nw - 1) / nw);  // rows of a warp at a time
-  int group = 32;                                    // lanes per row
-  while (group * per > 32) group >>= 1;
-  for (int r0 = w * per; r0 < m.rows; r0 += nw * per) {
-    const int count = min(per, m.rows - r0);
-    const int r = r0 + min(lane / group, count - 1);
+  const int c0 = wk.cta_of(u0), n = wk.cta_of(u1 - 1) - c0 + 1;
+  const int rows = s.t.n_tok * p.group;
+  int tpr = 1;  // threads per row
+  while (tpr < D / 4 && 2 * tpr * rows <= NT) tpr *= 2;
+  const int per = NT / tpr, sub = tid / per;
+  for (int r = tid % per; r < rows; r += per) {
     float M = -INFINITY, L = 0.f;
-    for (int i = lane % group; i < m.n; i += group) {
-      const float2 ml = __ldcg(p.ws_ml + m.at(i, r));
-      if (ml.x == -INFINITY) continue;
-      const float mn = fmaxf(M, ml.x);
-      L = L * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
-      M = mn;
-    }
-    for (int o = 1; o < group; o <<= 1) {
-      const float Mo = __shfl_xor_sync(sm::kFull, M, o), Lo = __shfl_xor_sync(sm::kFull, L, o);
-      const float mn = fmaxf(M, Mo);
-      if (mn != -INFINITY) {
-        L = (M == -INFINITY ? 0.f : L * exp2f(M - mn)) + (Mo == -INFINITY ? 0.f : Lo * exp2f(Mo - mn));
+    for (int b = 0; b < n; b += 4) {
+      float2 ml[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = min(b + i, n - 1);
+        ml[i] = __ldcg(p.ws_ml + (size_t)chunk_slot(c0 + j, j == 0) * p.tile_rows + r);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (b + i >= n || ml[i].x == -INFINITY) continue;
+        const float mn = fmaxf(M, ml[i].x);
+        L = L * exp2f(M - mn) + ml[i].y * exp2f(ml[i].x - mn);
         M = mn;
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    if (count >= 4)
-      chunk_merge_rows<T, D, 8, 2>(m, r0, count, group, M, inv, lane);
+    T* out = chunk_out<T>(p, s, r, D);
+    if (D / 4 / tpr >= 8)
+      chunk_merge_cols<T, D, 8, 2>(p, c0, n, r, sub, tpr, M, inv, out);
     else
-      chunk_merge_rows<T, D, 1, 8>(m, r0, count, group, M, inv, lane);
+      chunk_merge_cols<T, D, 1, 8>(p, c0, n, r, sub, tpr, M, inv, out);
   }
 }
 

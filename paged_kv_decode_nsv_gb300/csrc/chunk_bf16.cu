@@ -28,7 +28,7 @@
 // A tile of at most 64 or 32 rows is laid out 2 or 4 times over the 128 MMA
 // rows, and each copy takes its part of every run's keys (the probabilities of
 // the rest are zeros), so that all warps share the softmax of a few rows; the
-// copies' states are joined like the pieces of a cut tile.
+// copies' states are joined through shared memory.
 //
 // Tensor memory (512 columns): S of stream x at 128 x, its probabilities over
 // the first 64 of them, O of stream x at 256 + D x.
@@ -64,9 +64,15 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr uint32_t kHalf = kChunkHalfRows * D * 2;  // query rows of one half
   static constexpr uint32_t kOffQ = kStages * kStage;
-  static constexpr uint32_t kOffMl = kOffQ + 2 * kHalf;  // float2 [2][128]
+  // Exchange of the copies' outputs, [2 streams][128 rows][32 columns] floats:
+  // over the second half's query rows, which a tile with copies has none of
+  // (head_dim 64 has room beside them).
+  static constexpr uint32_t kStreamX = kChunkHalfRows * 32 * 4;
+  static constexpr uint32_t kOffX = D == 128 ? kOffQ + kHalf : kOffQ + 2 * kHalf;
+  static constexpr uint32_t kOffMl = D == 128 ? kOffQ + 2 * kHalf : kOffX + 2 * kStreamX;
+  // kOffMl: float2 [2][128]
   static constexpr uint32_t kOffBars = kOffMl + 2 * kChunkHalfRows * 8;
-  static constexpr int kBars = 2 * kStages + 11;
+  static constexpr int kBars = 2 * kStages + 13;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8;
   static constexpr uint32_t kOffWords = kOffMeta + kMetaRing * 4;  // TMEM address, abort, merge
   static constexpr uint32_t kTotal = kOffWords + 16;
@@ -87,6 +93,7 @@ struct Bars {
   __device__ uint32_t ofree() const { return b + 8 * (2 * S + 8); }
   __device__ uint32_t join() const { return b + 8 * (2 * S + 9); }
   __device__ uint32_t drained() const { return b + 8 * (2 * S + 10); }
+  __device__ uint32_t meet(int x) const { return b + 8 * (2 * S + 11 + x); }
 };
 
 // A bounded wait with one answer for the whole warp.
@@ -113,12 +120,16 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
   constexpr uint32_t kBlockBytes = kBlock * D * 2;
   const int half_tok = p.tile_tokens / 2;
   uint32_t run = 0;
+  int before = 0;  // the previous segment's copies
   ChunkSegment s;
   while (wk.next(p, s)) {
     // the query rows: one box of (tokens, group heads, 64 dims) per half or
     // copy and 64-dim slice; tokens past the tensor are filled with zeros
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
     const int copies = copies_of(p, s);
+    // (the second half may still serve the previous tile's copies)
+    if (copies == 0 && before > 1 && !warp_wait(B.ofree(), (nseg - 1) & 1)) return false;
+    before = copies;
     if (lane == 0) {
       const int boxes = copies == 0 ? 2 : copies;
       const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
@@ -201,10 +212,11 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
   auto wait_full = [&](uint32_t i) {
     return warp_wait(B.full(i % L::kStages), (i / L::kStages) & 1);
   };
-  ChunkSegment s;
-  while (wk.next(p, s)) {
+  ChunkSegment s, next;
+  for (bool more = wk.next(p, s); more; s = next) {
     const int n = s.j1 - s.j0;
     const bool pair = copies_of(p, s) == 0;
+    more = wk.next(p, next);  // its loads overlap this segment's work
     if (!warp_wait(B.qfull(), nseg & 1)) return false;
     // before O is written again: the previous segment's has been read
     auto free_o = [&]() { return nseg == 0 || warp_wait(B.ofree(), (nseg - 1) & 1); };
@@ -216,7 +228,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
       if (n == 1) umma_commit(B.qfree(), lead);
       for (int j = 0; j < n; ++j) {
         const uint32_t iv = base + 2 * j + 1, ik = iv + 1;
-        const bool more = j + 1 < n;
+        const bool again = j + 1 < n;
         if (j == 0 && !free_o()) return false;
         if (!wait_full(iv)) return false;
 #pragma unroll
@@ -225,7 +237,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
           tc_fence_after();
           values(x, slot_of(iv), j == 0);
           if (x == 1) umma_commit(B.empty(slot_of(iv)), lead);
-          if (more) {
+          if (again) {
             if (x == 0 && !wait_full(ik)) return false;
             scores(x, x, slot_of(ik));
             if (x == 1) {
@@ -411,15 +423,22 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
   const uint32_t t_o = tmem + lane_base + kColO;
   const int half_tok = p.tile_tokens / 2;
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
-  uint32_t nscore = 0, nseg = 0, njoin = 0, run0 = 0;
+  float* s_x = reinterpret_cast<float*>(smem + L::kOffX + x * L::kStreamX);
+  uint32_t nscore = 0, nseg = 0, njoin = 0, nmeet = 0, run0 = 0;
+  // the stream's four warps meet
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.meet(x));
+    return warp_wait(B.meet(x), nmeet++ & 1);
+  };
   // all eight softmax warps meet
   auto join = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(B.join());
     return warp_wait(B.join(), njoin++ & 1);
   };
-  ChunkSegment s;
-  while (wk.next(p, s)) {
+  ChunkSegment s, next;
+  for (bool more = wk.next(p, s); more; s = next) {
     const int copies = copies_of(p, s);
     const bool pair = copies == 0;
     const int n = s.j1 - s.j0;
@@ -478,87 +497,109 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
     }
     run0 += (uint32_t)n;
 
+    more = wk.next(p, next);  // its loads overlap the wait
     // The segment's end: O is complete once its last product is.
     if (!warp_wait(B.out(x), nseg & 1)) return false;
     tc_fence_after();
-    const bool alone = s.first && s.last;      // the tile is this CTA's
-    const bool whole = alone && copies <= 1;   // and its rows are complete here
-    // columns of O that this thread writes, and the weights of the streams' O
-    int c_lo = 0, c_n = D;
-    float w0 = 1.f, w1 = 0.f, L_ = f.l, M_ = f.m;
+    const bool whole = s.first && s.last;
+    const int row = tok * p.group + g;  // within the tile
+    const int slot = chunk_slot(blockIdx.x, s.first);
+    // weights of the two streams' O (lane r of both holds the same row where the
+    // tile is not a pair), and the row's maximum and sum
+    float w0 = 1.f, w1 = 0.f, M = f.m, Lsum = f.l;
     if (!pair) {
       s_ml[x * kChunkHalfRows + r] = make_float2(f.m, f.l);
       if (!join()) return false;
-      const float2 other = s_ml[(x ^ 1) * kChunkHalfRows + r];
-      const float m0 = x ? other.x : f.m, m1 = x ? f.m : other.x;
-      const float l0 = x ? other.y : f.l, l1 = x ? f.l : other.y;
-      M_ = fmaxf(m0, m1);
-      w0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M_);
-      w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M_);
-      L_ = l0 * w0 + l1 * w1;
-      c_lo = x * (D / 2);
-      c_n = D / 2;
+      M = -INFINITY;
+      for (int c = 0; c < copies; ++c)
+        M = fmaxf(M, fmaxf(s_ml[c * copy_rows + rc].x, s_ml[kChunkHalfRows + c * copy_rows + rc].x));
+      Lsum = 0.f;
+      auto weight = [&](float mm) { return mm == -INFINITY ? 0.f : ex2_approx(mm - M); };
+      for (int c = 0; c < copies; ++c) {
+        const float2 a = s_ml[c * copy_rows + rc], b = s_ml[kChunkHalfRows + c * copy_rows + rc];
+        Lsum += a.y * weight(a.x) + b.y * weight(b.x);
+      }
+      w0 = weight(s_ml[r].x);
+      w1 = weight(s_ml[kChunkHalfRows + r].x);
     }
-    // (the join above, or this one: no warp still merges the previous tile from
-    // the slot that is written now)
-    if (pair && !whole && !join()) return false;
-    const float inv = whole ? (L_ > 0.f ? 1.f / L_ : 0.f) : 1.f;
-    // the row within the tile, after the copies before this one
-    const int rr = tok * p.group + g + copy * s.t.n_tok * p.group;
-    const size_t piece =
-        (size_t)chunk_slot(blockIdx.x, s.first) * p.tile_rows + (valid ? rr : 0);
-    T* out = static_cast<T*>(p.out) +
-             (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      if (c * 32 < c_lo || c * 32 >= c_lo + c_n) continue;  // warp-uniform
+    const float inv = whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f;
+    T* out = valid ? chunk_out<T>(p, s, row, D) : nullptr;
+    // 8 consecutive columns of this thread's row
+    auto store8 = [&](int col, const float* v) {
+      if (whole) {
+        *reinterpret_cast<uint4*>(out + col) =
+            make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                       pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+      } else {
+        *chunk_acc(p, slot, D, col / 4, row) = make_float4(v[0], v[1], v[2], v[3]);
+        *chunk_acc(p, slot, D, col / 4 + 1, row) = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    };
+    // A pair's streams write all columns of their own rows; otherwise each
+    // stream takes half of the columns.
+    const int c_lo = pair ? 0 : x * (D / 2), c_hi = pair ? D : c_lo + D / 2;
+    for (int c = c_lo; c < c_hi; c += 32) {
       uint32_t o[32];
-      tmem_ld32(t_o + (pair ? x * D : 0) + c * 32, o);
+      float v[32];
+      tmem_ld32(t_o + (pair ? x * D : 0) + c, o);
       if (!pair && n > 1) {
         uint32_t o1[32];
-        tmem_ld32(t_o + D + c * 32, o1);
+        tmem_ld32(t_o + D + c, o1);
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          o[k] = __float_as_uint(__uint_as_float(o[k]) * w0 + __uint_as_float(o1[k]) * w1);
+          v[k] = __uint_as_float(o[k]) * w0 + __uint_as_float(o1[k]) * w1;
       } else {
         tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * w0;
       }
-      if (!valid) continue;
-      if (whole) {
+      if (copies <= 1) {
+        if (valid) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          uint4 v;
-          v.x = pack_bf16(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
-          v.y = pack_bf16(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
-          v.z = pack_bf16(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv);
-          v.w = pack_bf16(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv);
-          *reinterpret_cast<uint4*>(out + c * 32 + k) = v;
+          for (int k = 0; k < 32; k += 8) store8(c + k, v + k);
         }
-      } else {
-        float* a = p.ws_acc + piece * D + c * 32;
+        continue;
+      }
+      // the copies of a row add up; each sums its share of the columns
+      if (c > c_lo && !meet()) return false;  // the columns before have been read
+      if (valid) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 4)
-          *reinterpret_cast<uint4*>(a + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        for (int k = 0; k < 32; ++k) s_x[(copy * 32 + k) * copy_rows + rc] = v[k];
+      }
+      if (!meet()) return false;
+      if (valid) {
+        const int share = 32 / copies;
+        for (int k0 = copy * share; k0 < (copy + 1) * share; k0 += 8) {
+          float sum[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] = s_x[(k0 + k) * copy_rows + rc];
+          for (int cp = 1; cp < copies; ++cp)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] += s_x[(cp * 32 + k0 + k) * copy_rows + rc];
+          store8(c + k0, sum);
+        }
       }
     }
-    if (!whole && valid && (pair || x == 0)) p.ws_ml[piece] = make_float2(M_, L_);
+    if (!whole && valid && (pair || (x == 0 && copy == 0)))
+      p.ws_ml[(size_t)slot * p.tile_rows + row] = make_float2(M, Lsum);
     tc_fence_before();
+    fence_proxy_async_smem();  // the exchange's bytes may become query rows again
     __syncwarp();
     if (lane == 0) mbar_arrive(B.ofree());
     ++nseg;
     if (!whole) {
       // publish the piece; the CTA whose piece is the last merges them all
-      __threadfence();
       if (!join()) return false;
       if (warp == 0 && lane == 0) {
+        __threadfence();
         int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        *s_merge = alone || atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
+        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
       }
       if (!join()) return false;
       if (*s_merge) {
         __threadfence();
-        chunk_merge<T, D>(p, wk, s, copies < 1 ? 1 : copies, warp, 2 * kStreamWarps, lane);
+        chunk_merge<T, D, 2 * kStreamWarps * 32>(p, wk, s, threadIdx.x);
       }
     }
   }
@@ -586,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
         mbar_init(B.scores(x), 1);
         mbar_init(B.probs(x), kStreamWarps);
         mbar_init(B.out(x), 1);
+        mbar_init(B.meet(x), kStreamWarps);
       }
       mbar_init(B.ofree(), 2 * kStreamWarps);
       mbar_init(B.join(), 2 * kStreamWarps);

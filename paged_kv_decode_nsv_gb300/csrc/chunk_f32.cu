@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
   float* sv = reinterpret_cast<float*>(smem + L::kOffV);
   int* s_ok = reinterpret_cast<int*>(smem + L::kOffOk);
   int* s_merge = reinterpret_cast<int*>(smem + L::kOffMerge);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int ty = tid >> 4, tx = tid & 15;
   const float* q = static_cast<const float*>(p.q);
   const float* kp = static_cast<const float*>(p.k_pool);
@@ -189,33 +189,33 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       }
     }
     const bool whole = s.first && s.last;
+    const int slot = chunk_slot(blockIdx.x, s.first);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i, tok = r / p.group, g = r - tok * p.group;
+      const int r = ty * 4 + i;
       if (r >= rows) continue;
-      const size_t piece = (size_t)chunk_slot(blockIdx.x, s.first) * p.tile_rows + r;
-      float* o = whole ? static_cast<float*>(p.out) +
-                             (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D
-                       : p.ws_acc + piece * D;
+      float* o = chunk_out<float>(p, s, r, D);
       const float inv = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
 #pragma unroll
       for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<float4*>(o + v * 64 + tx * 4) =
+        *(whole ? reinterpret_cast<float4*>(o + v * 64 + tx * 4)
+                : chunk_acc(p, slot, D, v * 16 + tx, r)) =
             make_float4(acc[i][4 * v] * inv, acc[i][4 * v + 1] * inv, acc[i][4 * v + 2] * inv,
                         acc[i][4 * v + 3] * inv);
-      if (!whole && tx == 0) p.ws_ml[piece] = make_float2(m[i], l[i]);
+      if (!whole && tx == 0) p.ws_ml[(size_t)slot * p.tile_rows + r] = make_float2(m[i], l[i]);
     }
     if (!whole) {
-      __threadfence();
+      // publish the piece; the CTA whose piece is the last merges them all
       __syncthreads();
       if (tid == 0) {
+        __threadfence();
         int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
         *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
       }
       __syncthreads();
       if (*s_merge) {
         __threadfence();
-        chunk_merge<float, D>(p, wk, s, 1, warp, kThreadsF32 / 32, lane);
+        chunk_merge<float, D, kThreadsF32>(p, wk, s, tid);
       }
     }
   }
