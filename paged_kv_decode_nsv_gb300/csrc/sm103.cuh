@@ -12,16 +12,11 @@ namespace nsv {
 namespace sm {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s
+// Limit of a wait, in SM cycles: about a second.
+constexpr long long kWaitLimitCycles = 2000000000ll;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ unsigned long long global_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
 }
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -57,13 +52,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for the phase of `bar` with the given parity; false when it has not
-// completed after the limit.  The common case is inline, the loop is not.
-static __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = global_ns();
+// completed after the limit.  (The SM's cycle counter times it: reading the
+// global timer, as a wait with a limit in nanoseconds would, costs a microsecond
+// in every wait that does not succeed at once.)
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
   while (true) {
     for (int i = 0; i < 16; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) return false;
+    if (clock64() - t0 > kWaitLimitCycles) return false;
   }
 }
 
