@@ -122,22 +122,43 @@ struct ChunkSegment {
   bool first, last;  // whether it starts and ends the tile
 };
 
-// Walks the segments of CTA `c`.  All lanes of a warp call together.
+// The CTAs that share the units: as many as have at least one.
+struct ChunkShare {
+  long long per_head, U;  // units of one KV head, of all
+  int grid;
+  __device__ explicit ChunkShare(const ChunkParams& p)
+      : per_head(__ldcg(p.ws_head)), U(per_head * p.kv_heads),
+        grid(U < (long long)gridDim.x ? (int)U : (int)gridDim.x) {}
+  // CTA that runs unit x.
+  __device__ int cta_of(long long x) const {
+    const long long c = ((x + 1) * grid + U - 1) / U - 1;
+    return (int)(c < grid - 1 ? c : grid - 1);
+  }
+};
+
+// The CTAs whose pieces make up a tile: the first one, and how many.
+__device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, int head, int tile) {
+  const ChunkShare sh(p);
+  const long long u0 = head * sh.per_head + __ldcg(p.ws_prefix + tile);
+  const long long u1 = head * sh.per_head + __ldcg(p.ws_prefix + tile + 1);
+  const int c0 = sh.cta_of(u0);
+  return make_int2(c0, sh.cta_of(u1 - 1) - c0 + 1);
+}
+
+// Walks the segments of CTA `c`.  All lanes of a warp call together.  (Kept to
+// a few registers: what the attention kernel spills it reads back from L2,
+// because shared memory leaves the L1 cache next to nothing.)
 struct ChunkWalk {
-  long long u, end, per_head, U;
-  int grid, head, tile, ntiles, skip;
+  int left, head, tile, ntiles, skip;  // units left; where the next segment starts
   __device__ void init(const ChunkParams& p, int c, int lane) {
-    per_head = __ldcg(p.ws_head);
+    const ChunkShare sh(p);
     ntiles = (int)__ldcg(p.ws_head + 1);
-    U = per_head * p.kv_heads;
-    grid = U < (long long)gridDim.x ? (int)U : (int)gridDim.x;
-    u = end = 0;
-    head = tile = skip = 0;
-    if (c >= grid) return;
-    u = (long long)c * U / grid;
-    end = (long long)(c + 1) * U / grid;
-    head = (int)(u / per_head);
-    const long long rem = u - head * per_head;
+    left = head = tile = skip = 0;
+    if (c >= sh.grid) return;
+    const long long u = (long long)c * sh.U / sh.grid;
+    left = (int)((long long)(c + 1) * sh.U / sh.grid - u);
+    head = (int)(u / sh.per_head);
+    const long long rem = u - head * sh.per_head;
     // the last tile whose first unit is at most rem, 32 candidates at a time
     int lo = 0, hi = ntiles;
     while (hi - lo > 1) {
@@ -152,7 +173,7 @@ struct ChunkWalk {
     skip = (int)(rem - __ldcg(p.ws_prefix + tile));
   }
   __device__ bool next(const ChunkParams& p, ChunkSegment& s) {
-    if (u >= end) return false;
+    if (left <= 0) return false;
     const int4 a = __ldcg(p.ws_tiles + 2 * (size_t)tile);
     const int4 b = __ldcg(p.ws_tiles + 2 * (size_t)tile + 1);
     s.t.row = a.x;
@@ -164,25 +185,19 @@ struct ChunkWalk {
     s.t.ctx = b.z;
     s.head = head;
     s.tile = tile;
-    const int n = chunk_units(s.t.kb, s.t.ke, p.keys);
-    const int left = n - skip;
-    const int take = end - u < left ? (int)(end - u) : left;
+    const int of_tile = chunk_units(s.t.kb, s.t.ke, p.keys) - skip;
+    const int take = min(left, of_tile);
     s.j0 = skip;
     s.j1 = skip + take;
     s.first = skip == 0;
-    s.last = take == left;
-    u += take;
+    s.last = take == of_tile;
+    left -= take;
     skip = 0;
     if (s.last && ++tile == ntiles) {
       tile = 0;
       ++head;
     }
     return true;
-  }
-  // CTA that runs unit x (every CTA below `grid` has at least one unit).
-  __device__ int cta_of(long long x) const {
-    const long long c = ((x + 1) * grid + U - 1) / U - 1;
-    return (int)(c < grid - 1 ? c : grid - 1);
   }
 };
 
@@ -210,11 +225,10 @@ __device__ __forceinline__ float4* chunk_acc(const ChunkParams& p, int slot, int
 
 // Where a tile's row goes in `out`.
 template <typename T>
-__device__ __forceinline__ T* chunk_out(const ChunkParams& p, const ChunkSegment& s, int row,
+__device__ __forceinline__ T* chunk_out(const ChunkParams& p, int q0, int head, int row,
                                         int head_dim) {
   const int tok = row / p.group, g = row - tok * p.group;
-  return static_cast<T*>(p.out) +
-         (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * head_dim;
+  return static_cast<T*>(p.out) + (((size_t)q0 + tok) * p.heads + head * p.group + g) * head_dim;
 }
 
 // Merge of a cut tile by all NT threads of a group of the CTA whose piece
@@ -271,12 +285,11 @@ __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, i
 }
 
 template <typename T, int D, int NT>
-__device__ __noinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& wk,
-                                         const ChunkSegment& s, int tid) {
-  const long long u0 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile);
-  const long long u1 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile + 1);
-  const int c0 = wk.cta_of(u0), n = wk.cta_of(u1 - 1) - c0 + 1;
-  const int rows = s.t.n_tok * p.group;
+__device__ __noinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok, int head, int tile,
+                                         int tid) {
+  const int2 pc = chunk_pieces(p, head, tile);
+  const int c0 = pc.x, n = pc.y;
+  const int rows = n_tok * p.group;
   int tpr = 1;  // threads per row
   while (tpr < D / 4 && 2 * tpr * rows <= NT) tpr *= 2;
   const int per = NT / tpr, sub = tid / per;
@@ -298,7 +311,7 @@ __device__ __noinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& 
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    T* out = chunk_out<T>(p, s, r, D);
+    T* out = chunk_out<T>(p, q0, head, r, D);
     if (D / 4 / tpr >= 8)
       chunk_merge_cols<T, D, 8, 2>(p, c0, n, r, sub, tpr, M, inv, out);
     else
@@ -306,13 +319,6 @@ __device__ __noinline__ void chunk_merge(const ChunkParams& p, const ChunkWalk& 
   }
 }
 
-// Pieces of a cut tile.
-__device__ __forceinline__ int chunk_pieces(const ChunkParams& p, const ChunkWalk& wk,
-                                            const ChunkSegment& s) {
-  const long long u0 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile);
-  const long long u1 = s.head * wk.per_head + __ldcg(p.ws_prefix + s.tile + 1);
-  return wk.cta_of(u1 - 1) - wk.cta_of(u0) + 1;
-}
 #endif  // __CUDACC__
 
 }  // namespace nsv

@@ -11,14 +11,15 @@
 // product, as its tensor-core operand: half an ulp each (2^-9 relative),
 // which is what rounding the output costs anyway.
 //
-// One CTA per SM, twelve warps:
-//   warps 0-3, 4-7  softmax of stream 0 and stream 1: thread r of a stream owns
-//                   MMA row r (TMEM lane r): its scores, its state, its output
-//   warp 8          TMA producer: query rows, then K and V of each run, block by
+// One CTA per SM, twenty warps:
+//   warps 0-7, 8-15 softmax of stream 0 and stream 1: MMA row r (TMEM lane r) of a
+//                   stream belongs to two threads, one in each warp of a pair,
+//                   which split its columns (scores and output)
+//   warp 16         TMA producer: query rows, then K and V of each run, block by
 //                   block through the block table, into a ring of stages
-//   warp 9          MMA issue: S = Q.K^T (both operands in shared memory) and
+//   warp 17         MMA issue: S = Q.K^T (both operands in shared memory) and
 //                   O += P.V (P in tensor memory), accumulators in tensor memory
-//   warps 10, 11    idle: they complete the warpgroup that gives registers away
+//   warps 18, 19    idle: they complete the warpgroup that gives registers away
 // The rows of an MMA are the tile's query tokens times the query heads that
 // share the KV head, so K and V are read once for all of them.  A tile with
 // more than 128 rows gives each stream its half of the rows and both the same
@@ -30,8 +31,9 @@
 // the rest are zeros), so that all warps share the softmax of a few rows; the
 // copies' states are joined through shared memory.
 //
-// Tensor memory (512 columns): S of stream x at 128 x, its probabilities over
-// the first 64 of them, O of stream x at 256 + D x.
+// Tensor memory (512 columns): S of stream x at 128 x, a column per key; the
+// bf16 probabilities of each 16 keys over the first 8 columns of their scores; O
+// of stream x at 256 + D x.
 // Work is dealt out in equal numbers of units (chunk.cuh); a tile cut between
 // CTAs leaves partial states in the workspace and the CTA whose piece arrives
 // last merges them.  All waits are bounded; one that gives up sets
@@ -44,13 +46,13 @@ namespace {
 
 using namespace sm;
 
-constexpr int kThreads = 384;
-// Registers per thread: 168 at launch (12 warps); the two softmax warpgroups
-// (whose threads hold a row's 128 scores) take 208 from the third's share:
-// 2 x 208 + 80 = 496 <= 3 x 168.
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "more registers than the launch has");
-constexpr int kStreamWarps = 4;
+constexpr int kSoftWarps = 16;
+constexpr int kThreads = 640;
+// Registers per thread: 96 at launch (20 warps); the four softmax warpgroups
+// (whose threads hold half a row's scores) take 104 from the fifth's share:
+// 4 x 104 + 64 = 5 x 96.
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;
+static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * 96, "more registers than the launch has");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr int kMetaRing = 16;
@@ -64,18 +66,20 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr uint32_t kHalf = kChunkHalfRows * D * 2;  // query rows of one half
   static constexpr uint32_t kOffQ = kStages * kStage;
-  // Exchange of the copies' outputs, [2 streams][128 rows][32 columns] floats:
-  // over the second half's query rows, which a tile with copies has none of
-  // (head_dim 64 has room beside them).
-  static constexpr uint32_t kStreamX = kChunkHalfRows * 32 * 4;
+  // Exchange of the copies' outputs, [2 streams][2 halves][128 rows][16 columns]
+  // floats: over the second half's query rows, which a tile with copies has
+  // none of (head_dim 64 has room beside them).
+  static constexpr uint32_t kQuarterX = kChunkHalfRows * 16 * 4;
   static constexpr uint32_t kOffX = D == 128 ? kOffQ + kHalf : kOffQ + 2 * kHalf;
-  static constexpr uint32_t kOffMl = D == 128 ? kOffQ + 2 * kHalf : kOffX + 2 * kStreamX;
+  static constexpr uint32_t kOffMl = D == 128 ? kOffQ + 2 * kHalf : kOffX + 4 * kQuarterX;
   // kOffMl: float2 [2][128]
-  static constexpr uint32_t kOffBars = kOffMl + 2 * kChunkHalfRows * 8;
-  static constexpr int kBars = 2 * kStages + 13;
+  static constexpr uint32_t kOffTodo = kOffMl + 2 * kChunkHalfRows * 8;  // int4 [2]: tiles to merge
+  static constexpr uint32_t kOffBars = kOffTodo + 32;
+  static constexpr int kBars = 2 * kStages + 15;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8;
-  static constexpr uint32_t kOffWords = kOffMeta + kMetaRing * 4;  // TMEM address, abort, merge
-  static constexpr uint32_t kTotal = kOffWords + 16;
+  static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
+  static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address
+  static constexpr uint32_t kTotal = kOffWord + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
@@ -93,7 +97,7 @@ struct Bars {
   __device__ uint32_t ofree() const { return b + 8 * (2 * S + 8); }
   __device__ uint32_t join() const { return b + 8 * (2 * S + 9); }
   __device__ uint32_t drained() const { return b + 8 * (2 * S + 10); }
-  __device__ uint32_t meet(int x) const { return b + 8 * (2 * S + 11 + x); }
+  __device__ uint32_t meet(int i) const { return b + 8 * (2 * S + 11 + i); }
 };
 
 // A bounded wait with one answer for the whole warp.
@@ -179,9 +183,15 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
 }
 
 // ------------------------------------------------------------------------ MMA
+// One warp issues for both streams, in turn: products of one stream's
+// probabilities and its next scores, then the other's.  (A warp per stream let
+// both streams fall into step, their softmax at the same time and their MMAs at
+// the same time: 2167 against 1753 us for 4096 tokens over 32768.)  The CTA holds
+// all of tensor memory, which starts at column 0, so that all operands but the
+// stage are compile-time constants.
 template <int D>
 __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
-                                          uint32_t tmem, ChunkWalk wk, bool lead) {
+                                          ChunkWalk wk, bool lead) {
   using L = Smem<D>;
   // K and V stages: tokens in groups of 8, a group's 64-dim halves one
   // 1024-byte swizzle atom after the other
@@ -191,91 +201,79 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
   const uint64_t dq = umma_desc128(smem0 + L::kOffQ, 16, 1024);
   const uint64_t dk = umma_desc128(smem0, 16, kGroup);
   const uint64_t dv = umma_desc128(smem0, 1024, kGroup);
-  auto scores = [&](int x, int half, uint32_t slot) {
+  // descriptors are linear in the start address: a base plus an offset
+  auto stage_at = [](uint32_t i) {
+    return __reduce_or_sync(kFull, (i % L::kStages) * (L::kStage >> 4));  // warp-uniform
+  };
+  auto scores = [&](uint32_t x, uint32_t half, uint32_t i) {
     tc_fence_after();
-    const uint64_t a = dq + ((half * L::kHalf) >> 4), b = dk + ((slot * L::kStage) >> 4);
+    const uint64_t a = dq + half * (L::kHalf >> 4), b = dk + stage_at(i);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
-      umma_ss(tmem + x * kChunkKeys, a + (((ks >> 2) * (kChunkHalfRows * 128) + (ks & 3) * 32) >> 4),
+      umma_ss(x * kChunkKeys, a + (((ks >> 2) * (kChunkHalfRows * 128) + (ks & 3) * 32) >> 4),
               b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0, lead);
     umma_commit(B.scores(x), lead);
   };
-  auto values = [&](int x, uint32_t slot, bool fresh) {
-    const uint64_t b = dv + ((slot * L::kStage) >> 4);
+  auto values = [&](uint32_t x, uint32_t i, bool fresh) {
+    const uint64_t b = dv + stage_at(i);
 #pragma unroll
     for (int ks = 0; ks < kChunkKeys / 16; ++ks)
-      umma_ts(tmem + kColO + x * D, tmem + x * kChunkKeys + ks * 8, b + ((ks * 2 * kGroup) >> 4),
-              idesc_o, !fresh || ks > 0, lead);
+      umma_ts(kColO + x * D, x * kChunkKeys + ks * kBlock, b + ((ks * 2 * kGroup) >> 4), idesc_o,
+              !fresh || ks > 0, lead);
   };
   uint32_t base = 0, nseg = 0, np[2] = {0, 0};
-  auto slot_of = [](uint32_t i) { return i % L::kStages; };
   auto wait_full = [&](uint32_t i) {
     return warp_wait(B.full(i % L::kStages), (i / L::kStages) & 1);
   };
+  auto free_stage = [&](uint32_t i) { umma_commit(B.empty(i % L::kStages), lead); };
   ChunkSegment s, next;
   for (bool more = wk.next(p, s); more; s = next) {
     const int n = s.j1 - s.j0;
     const bool pair = copies_of(p, s) == 0;
     more = wk.next(p, next);  // its loads overlap this segment's work
     if (!warp_wait(B.qfull(), nseg & 1)) return false;
-    // before O is written again: the previous segment's has been read
-    auto free_o = [&]() { return nseg == 0 || warp_wait(B.ofree(), (nseg - 1) & 1); };
-    if (pair) {
-      if (!wait_full(base)) return false;
-      scores(0, 0, slot_of(base));
-      scores(1, 1, slot_of(base));
-      umma_commit(B.empty(slot_of(base)), lead);
-      if (n == 1) umma_commit(B.qfree(), lead);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t iv = base + 2 * j + 1, ik = iv + 1;
-        const bool again = j + 1 < n;
-        if (j == 0 && !free_o()) return false;
-        if (!wait_full(iv)) return false;
+    // Turn k: stream x = k & 1 multiplies the probabilities of its run and starts
+    // its next scores.  A pair's streams take every run each (turn 2 j + x), the
+    // others run k.
+    const int turns = pair ? 2 * n : n;
+    const int ahead = pair ? 1 : 2;  // runs between a stream's runs
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!warp_wait(B.probs(x), np[x]++ & 1)) return false;
-          tc_fence_after();
-          values(x, slot_of(iv), j == 0);
-          if (x == 1) umma_commit(B.empty(slot_of(iv)), lead);
-          if (again) {
-            if (x == 0 && !wait_full(ik)) return false;
-            scores(x, x, slot_of(ik));
-            if (x == 1) {
-              umma_commit(B.empty(slot_of(ik)), lead);
-              if (j + 2 == n) umma_commit(B.qfree(), lead);
-            }
-          } else {
-            umma_commit(B.out(x), lead);
-          }
-        }
-      }
-    } else {
-      for (int j = 0; j < 2 && j < n; ++j) {
-        const uint32_t ik = base + 2 * j;
-        if (!wait_full(ik)) return false;
-        scores(j, 0, slot_of(ik));
-        umma_commit(B.empty(slot_of(ik)), lead);
-      }
-      if (n <= 2) umma_commit(B.qfree(), lead);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t iv = base + 2 * j + 1, ik = base + 2 * j + 4;
-        const int x = j & 1;
-        if (j == 0 && !free_o()) return false;
-        if (!wait_full(iv)) return false;
-        if (!warp_wait(B.probs(x), np[x]++ & 1)) return false;
-        tc_fence_after();
-        values(x, slot_of(iv), j < 2);
-        umma_commit(B.empty(slot_of(iv)), lead);
-        if (j + 2 < n) {
-          if (!wait_full(ik)) return false;
-          scores(x, 0, slot_of(ik));
-          umma_commit(B.empty(slot_of(ik)), lead);
-          if (j + 3 == n) umma_commit(B.qfree(), lead);
-        }
-      }
-      umma_commit(B.out(0), lead);
-      umma_commit(B.out(1), lead);
+    for (int x = 0; x < 2; ++x) {
+      if (!pair && x >= n) break;
+      const uint32_t ik = base + (pair ? 0 : 2 * x);
+      if (!wait_full(ik)) return false;
+      scores(x, pair ? x : 0, ik);
+      if (!pair || x == 1) free_stage(ik);
     }
+    if (n <= ahead) umma_commit(B.qfree(), lead);
+    // before O is written again: the previous segment's has been read
+    if (nseg && !warp_wait(B.ofree(), (nseg - 1) & 1)) return false;
+    auto turn = [&](uint32_t x, int j) {
+      const uint32_t iv = base + 2 * j + 1, ik = base + 2 * (j + ahead);
+      if (!wait_full(iv)) return false;
+      if (!warp_wait(B.probs(x), np[x]++ & 1)) return false;
+      tc_fence_after();
+      values(x, iv, j < ahead);
+      const bool last_reader = !pair || x == 1;
+      if (j + ahead < n) {
+        if (!wait_full(ik)) return false;
+        scores(x, pair ? x : 0, ik);
+        if (last_reader) {
+          free_stage(iv);
+          free_stage(ik);
+          if (j + ahead + 1 == n) umma_commit(B.qfree(), lead);
+        }
+      } else {
+        if (last_reader) free_stage(iv);
+      }
+      return true;
+    };
+    for (int k = 0; k < turns; k += 2) {
+      if (!turn(0, pair ? k / 2 : k)) return false;
+      if (k + 1 < turns && !turn(1, pair ? k / 2 : k + 1)) return false;
+    }
+    umma_commit(B.out(0), lead);
+    umma_commit(B.out(1), lead);
     base += 2 * n;
     ++nseg;
   }
@@ -283,155 +281,223 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
 }
 
 // -------------------------------------------------------------------- softmax
-// cap * tanh(s * scale / cap) in log2 units.  z = s * scale / cap; below 1/4 the
-// series z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315) (relative error under 4e-7), above
-// it 1 - 2 / (1 + e^2z), whose cancellation is harmless there.
-__device__ __forceinline__ float capped(float s, float cap_z, float cap_out) {
+// cap * tanh(s * scale / cap) in log2 units for caps so large that the scores
+// stay near the tanh's linear part: z = s * scale / cap; below 1/4 the series
+// z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315) (relative error under 4e-7), above it
+// 1 - 2 / (1 + e^2z).  For smaller caps that second form alone is off by at most
+// cap * 1.7e-7, far below a bf16 probability's rounding.
+constexpr float kLargeCap = 4096.f;
+__device__ __forceinline__ float large_cap(float s, float cap_z, float cap_out) {
   const float z = s * cap_z;
-  const float e = ex2_approx(z * 2.8853900817779268f);  // 2 log2(e)
-  const float big = 1.f - 2.f * rcp_approx(1.f + e);
+  const float big = 1.f - 2.f * rcp_approx(1.f + ex2_approx(z * 2.8853900817779268f));
   const float z2 = z * z;
   const float small =
       z * fmaf(z2, fmaf(z2, fmaf(z2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
   return (z2 < 0.0625f ? small : big) * cap_out;
 }
 
-// The state of one row of a stream, as its thread holds it.
+// The state of one row of a stream, as each of its two threads holds it.
 struct RowState {
   bool valid, fresh;  // whether the row exists; whether O holds nothing yet
   int pos;            // the query token's position
   int2 see;           // what it sees
   float slope;        // slope * log2(e)
-  float m, l;         // running maximum (log2 units) and sum
+  float m, l;         // running maximum (log2 units); this thread's part of the sum
 };
 
-// Folds NCH x 32 keys of one run (columns col0 .. of the scores t_s) into a row:
-// maximum, rescale of O (t_o) where it rises, probabilities over the scores.
-template <int D, bool CAP, bool BIAS, int NCH>
-__device__ __forceinline__ void fold_run(const ChunkParams& p, RowState& f, uint32_t t_s,
-                                         uint32_t t_o, int t0, int col0, int mask) {
-  uint32_t sr[NCH][32];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) tmem_ld32(t_s + col0 + c * 32, sr[c]);
-  tmem_wait_ld();
+// What the two warps of a pair share: whose lanes must raise their maximum
+// (two runs in turn), and whether one of them has given up.
+struct PairWords {
+  uint32_t raise[2][2];
+  uint32_t failed;
+};
+
+// The two warps of a pair meet.  False when the other one has given up a wait
+// (it came here on its way out).
+__device__ __forceinline__ bool pair_sync(int bar, volatile PairWords* w) {
+  asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+  return w->failed == 0;
+}
+
+// Folds the NC keys of one run that are this thread's (columns col0 .. of the
+// scores t_s) into its row: the maximum over both threads' columns, rescale of
+// this thread's half of O (t_o) where it rises, probabilities (bf16) over the
+// scores.
+//
+// Two passes over the scores in tensor memory, 16 columns at a time, instead of
+// one with the row in registers: unrolled over 64 columns the loop's code, run by
+// 16 warps each at its own place, did not fit the instruction cache, and warps
+// waited for instructions more than for anything else.
+template <int D, bool CAP, bool BIAS>
+__device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint32_t t_s,
+                                         uint32_t t_o, int t0, int col0, int NC, int hf, int copy,
+                                         int mask, bool past, int bar, volatile PairWords* w,
+                                         volatile float2* s_ml, uint32_t turn, int lane) {
+  constexpr int kW = 16;
   float mul = p.qscale;
-  if constexpr (CAP || BIAS) {
-    mul = 1.f;
-    const float d0 = (float)(f.pos - t0 - col0);
-    const float cap_z = CAP ? p.scale / p.cap : 0.f, cap_out = p.cap * 1.4426950408889634f;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        float v = __uint_as_float(sr[c][k]);
-        v = CAP ? capped(v, cap_z, cap_out) : v * p.qscale;
-        if (BIAS) v = fmaf(-f.slope, fabsf(d0 - (float)(c * 32 + k)), v);
-        sr[c][k] = __float_as_uint(v);
-      }
-  }
   // positions that the row does not see; nothing to mask in most runs
-  const int lo = f.see.x - t0, hi = f.see.y - t0;
-  const bool dense = mask == 0xff && lo <= col0 && hi >= col0 + 32 * NCH && mul > 0.f;
-  if (!__all_sync(kFull, dense)) {
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int cc = col0 + 32 * c;
-      const int a = min(max(lo - cc, 0), 32), b = min(max(hi - cc, 0), 32);
-      uint32_t bits = (b == 32 ? ~0u : (1u << b) - 1u) & ~(a == 32 ? ~0u : (1u << a) - 1u);
-      const int bm = mask >> (cc / kBlock);
-      bits &= ((bm & 1) ? 0xffffu : 0u) | ((bm & 2) ? 0xffff0000u : 0u);
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float v = __uint_as_float(sr[c][k]) * mul;
-        sr[c][k] = __float_as_uint((bits >> k) & 1u ? v : -INFINITY);
-      }
-    }
-    mul = 1.f;
-  }
-  float mxs[NCH];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    mxs[c] = fmaxf(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
-#pragma unroll
-    for (int k = 2; k < 32; k += 2)
-      mxs[c] = fmaxf(mxs[c], fmaxf(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])));
-  }
-  float mx = mxs[0];
-#pragma unroll
-  for (int c = 1; c < NCH; ++c) mx = fmaxf(mx, mxs[c]);
-  mx *= mul;
-  const bool raise = f.valid && mx > f.m + kSlack;  // also the first finite one
-  float alpha = 1.f;
-  if (raise) {
-    alpha = ex2_approx(f.m - mx);
-    f.m = mx;
-    f.l *= alpha;
-  }
-  // The products that O holds are complete: the scores just waited for were
-  // issued after them.
-  if (!f.fresh && __any_sync(kFull, raise)) {
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      uint32_t o[16];
-      tmem_ld16(t_o + c * 16, o);
+  const int lo = f.see.x - t0 - col0, hi = f.see.y - t0 - col0;
+  const int bm = mask >> (col0 / kBlock);
+  const int all = (1 << (NC / kBlock)) - 1;
+  const bool dense = (bm & all) == all && lo <= 0 && hi >= NC && mul > 0.f;
+  float mx = -INFINITY;
+  if (!CAP && !BIAS && __all_sync(kFull, dense)) {
+    float m1 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < NC; c += kW) {
+      float s[kW];
+      tmem_ld16(t_s + col0 + c, s);
       tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-      tmem_st16(t_o + c * 16, o);
+      for (int k = 0; k < kW; k += 4) {
+        mx = max3(mx, s[k], s[k + 1]);
+        m1 = max3(m1, s[k + 2], s[k + 3]);
+      }
+    }
+    mx = fmaxf(mx, m1) * mul;
+  } else {
+    // scale, cap, bias and mask, and put the result back
+    const float d0 = (float)(f.pos - t0 - col0);
+    const float cap_out = p.cap * 1.4426950408889634f;
+    const float cap_z = CAP ? p.scale / p.cap : 0.f, cap_in = cap_z * 2.8853900817779268f;
+#pragma unroll 1
+    for (int c = 0; c < NC; c += kW) {
+      float s[kW];
+      tmem_ld16(t_s + col0 + c, s);
+      tmem_wait_ld();
+      if (CAP) {
+        if (p.cap > kLargeCap) {
+#pragma unroll
+          for (int k = 0; k < kW; ++k) s[k] = large_cap(s[k], cap_z, cap_out);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kW; ++k)
+            s[k] = fmaf(rcp_approx(1.f + ex2_approx(s[k] * cap_in)), -2.f * cap_out, cap_out);
+        }
+      }
+      const float m0 = CAP ? 1.f : mul;
+      if (BIAS) {
+        const float d = d0 - (float)c;
+        if (past) {  // - slope * (d - k), in two multiply-adds for two columns
+          const float b0 = -f.slope * d;
+#pragma unroll
+          for (int k = 0; k < kW; k += 2) {
+            float x0, x1;
+            fma2(x0, x1, f.slope, f.slope, (float)k, (float)(k + 1), b0, b0);
+            fma2(s[k], s[k + 1], s[k], s[k + 1], m0, m0, x0, x1);
+          }
+        } else {  // positions on both sides of the token
+#pragma unroll
+          for (int k = 0; k < kW; ++k)
+            s[k] = fmaf(-f.slope, fabsf(d - (float)k), s[k] * m0);
+        }
+      } else if (!CAP) {
+#pragma unroll
+        for (int k = 0; k < kW; ++k) s[k] *= m0;
+      }
+      const int a = min(max(lo - c, 0), kW), b = min(max(hi - c, 0), kW);
+      const uint32_t bits = ((bm >> (c / kBlock)) & 1) ? ((1u << b) - 1u) & ~((1u << a) - 1u) : 0u;
+      if (!__all_sync(kFull, bits == 0xffffu)) {
+#pragma unroll
+        for (int k = 0; k < kW; ++k) s[k] = (bits >> k) & 1u ? s[k] : -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < kW; k += 2) mx = max3(mx, s[k], s[k + 1]);
+      tmem_st16(t_s + col0 + c, s);
+    }
+    tmem_wait_st();
+    mul = 1.f;
+  }
+  // Both warps learn which rows exceed the running maximum; in most runs none
+  // does, and the maxima themselves need no exchange.
+  const uint32_t mine = __ballot_sync(kFull, f.valid && mx > f.m + kSlack);
+  if (lane == 0) w->raise[turn & 1][hf] = mine;
+  if (!pair_sync(bar, w)) return false;
+  if (mine | w->raise[turn & 1][hf ^ 1]) {
+    (hf ? s_ml->y : s_ml->x) = mx;
+    if (!pair_sync(bar, w)) return false;
+    mx = fmaxf(mx, hf ? s_ml->x : s_ml->y);
+    const bool raise = f.valid && mx > f.m + kSlack;  // also the first finite one
+    float alpha = 1.f;
+    if (raise) {
+      alpha = ex2_approx(f.m - mx);
+      f.m = mx;
+      f.l *= alpha;
+    }
+    // The products that O holds are complete: the scores just waited for were
+    // issued after them.
+    if (!f.fresh && __any_sync(kFull, raise)) {
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 16) {
+        float o[16];
+        tmem_ld16(t_o + hf * (D / 2) + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] *= alpha;
+        tmem_st16(t_o + hf * (D / 2) + c, o);
+      }
     }
   }
   const float neg = f.m == -INFINITY ? 0.f : -f.m;
   float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < NC; c += kW) {
+    float s[kW];
+    tmem_ld16(t_s + col0 + c, s);
+    tmem_wait_ld();
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    uint32_t w[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < kW; k += 2) {
       float a, b;
-      fma2(a, b, __uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1]), mul, mul, neg,
-           neg);
+      fma2(a, b, s[k], s[k + 1], mul, mul, neg, neg);
       a = ex2_approx(a);
       b = ex2_approx(b);
       add2(l0, l1, a, b);
-      w[k] = pack_bf16(a, b);
+      s[k / 2] = __uint_as_float(pack_bf16(a, b));
     }
-    tmem_st16(t_s + col0 / 2 + c * 16, w);
+    tmem_st8(t_s + col0 + c, s);
   }
-  if constexpr (NCH < 4) {  // the keys of the other copies
-    uint32_t zero[16];
+  if (NC < 64) {  // the keys of the other copies: zeros, every other block each
+    float zero[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) zero[k] = 0u;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * 32 < col0 || c * 32 >= col0 + 32 * NCH) tmem_st16(t_s + c * 16, zero);
+    for (int k = 0; k < 8; ++k) zero[k] = 0.f;
+    const int first = 2 * copy * NC / kBlock, n = 2 * NC / kBlock;  // the copy's blocks
+#pragma unroll 1
+    for (int b = hf; b < kChunkKeys / kBlock; b += 2)
+      if (b < first || b >= first + n) tmem_st8(t_s + b * kBlock, zero);
   }
   f.l += l0 + l1;
   tmem_wait_st();
+  return true;
 }
 
+// How a softmax warp ends.
+enum : int { kDone = 0, kTimedOut = 1, kPartnerFailed = 2 };
+
 template <int D, bool CAP, bool BIAS>
-__device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
-                                        unsigned char* smem, uint32_t tmem,
-                                        const volatile int* s_meta, volatile int* s_merge,
-                                        ChunkWalk wk, int warp, int lane) {
+__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
+                                       unsigned char* smem, const volatile int* s_meta, int4* s_todo,
+                                       volatile PairWords* words, ChunkWalk wk, int warp,
+                                       int lane) {
   using L = Smem<D>;
   using T = __nv_bfloat16;
-  const int x = warp >> 2;                     // stream
+  const int x = warp >> 3;                     // stream
+  const int hf = (warp >> 2) & 1;              // which of the pair: its half of the columns
   const int r = (warp & 3) * 32 + lane;        // MMA row, TMEM lane
+  const int bar = 1 + x * 4 + (warp & 3);      // the pair's barrier
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-  const uint32_t t_s = tmem + lane_base + x * kChunkKeys;
-  const uint32_t t_o = tmem + lane_base + kColO;
+  const uint32_t t_s = lane_base + x * kChunkKeys;
+  const uint32_t t_o = lane_base + kColO;
   const int half_tok = p.tile_tokens / 2;
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
-  float* s_x = reinterpret_cast<float*>(smem + L::kOffX + x * L::kStreamX);
-  uint32_t nscore = 0, nseg = 0, njoin = 0, nmeet = 0, run0 = 0;
-  // the stream's four warps meet
+  float* s_x = reinterpret_cast<float*>(smem + L::kOffX + (x * 2 + hf) * L::kQuarterX);
+  uint32_t nscore = 0, nseg = 0, njoin = 0, nmeet = 0, run0 = 0, turn = 0;
+  // the four warps with this stream and half meet
   auto meet = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(B.meet(x));
-    return warp_wait(B.meet(x), nmeet++ & 1);
+    if (lane == 0) mbar_arrive(B.meet(x * 2 + hf));
+    return warp_wait(B.meet(x * 2 + hf), nmeet++ & 1);
   };
-  // all eight softmax warps meet
+  // all softmax warps meet
   auto join = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(B.join());
@@ -443,11 +509,11 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
     const bool pair = copies == 0;
     const int n = s.j1 - s.j0;
     // this thread's row within its half or copy, and its part of a run's keys:
-    // nch chunks of 32 columns from col0 on
+    // 64, 32 or 16 columns from col0 on
     const int shift = copies == 4 ? 2 : copies == 2 ? 1 : 0;
     const int copy_rows = kChunkHalfRows >> shift;
     const int copy = r / copy_rows, rc = r - copy * copy_rows;
-    const int nch = 4 >> shift, col0 = copy * 32 * nch;
+    const int col0 = (2 * copy + hf) * (64 >> shift);
     const int ti = rc / p.group, g = rc - ti * p.group;
     const int tok = (pair && x ? half_tok : 0) + ti;  // query token within the tile
     const bool valid = ti < copy_rows / p.group && tok < s.t.n_tok;
@@ -461,11 +527,12 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
     f.slope = BIAS && valid ? __ldg(p.slopes + s.head * p.group + g) * 1.4426950408889634f : 0.f;
     f.m = -INFINITY;
     f.l = 0.f;
+    const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
     for (int j = s.j0 + (pair ? 0 : x); j < s.j1; j += step) {
       const uint32_t run = run0 + (uint32_t)(j - s.j0);
       const int t0 = s.t.kb + j * kChunkKeys;
-      if (!warp_wait(B.scores(x), nscore++ & 1)) return false;
+      if (!warp_wait(B.scores(x), nscore++ & 1)) return kTimedOut;
       tc_fence_after();
       const int mask = s_meta[run % kMetaRing];
       // Values of positions that hold nothing (past the context, or in a
@@ -473,22 +540,21 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
       // 0 * NaN is not.
       if (mask != 0xff || s.t.ctx - t0 < kChunkKeys) {
         const uint32_t i = 2 * run + 1, slot = i % L::kStages;
-        if (!warp_wait(B.full(slot), (i / L::kStages) & 1)) return false;
+        if (!warp_wait(B.full(slot), (i / L::kStages) & 1)) return kTimedOut;
         if (!((mask >> (r >> 4)) & 1) || r >= s.t.ctx - t0) {
           unsigned char* v = smem + slot * L::kStage + (r >> 3) * (D / 64) * 1024 + (r & 7) * 128;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
+#pragma unroll 1
+          for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c)
             *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
       if (any_valid) {
-        if (nch == 4)
-          fold_run<D, CAP, BIAS, 4>(p, f, t_s, t_o + x * D, t0, col0, mask);
-        else if (nch == 2)
-          fold_run<D, CAP, BIAS, 2>(p, f, t_s, t_o + x * D, t0, col0, mask);
-        else
-          fold_run<D, CAP, BIAS, 1>(p, f, t_s, t_o + x * D, t0, col0, mask);
+        const bool ok = fold_run<D, CAP, BIAS>(p, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
+                                               copy, mask, past, bar, words,
+                                               s_ml + x * kChunkHalfRows + r, turn, lane);
+        if (!ok) return kPartnerFailed;
+        ++turn;
       }
       f.fresh = false;
       tc_fence_before();
@@ -499,17 +565,25 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
 
     more = wk.next(p, next);  // its loads overlap the wait
     // The segment's end: O is complete once its last product is.
-    if (!warp_wait(B.out(x), nseg & 1)) return false;
+    if (!warp_wait(B.out(x), nseg & 1)) return kTimedOut;
     tc_fence_after();
     const bool whole = s.first && s.last;
     const int row = tok * p.group + g;  // within the tile
     const int slot = chunk_slot(blockIdx.x, s.first);
+    // the row's maximum and sum over both threads
+    float2* own = s_ml + x * kChunkHalfRows + r;
+    if (hf) own->y = f.l;
+    if (!pair_sync(bar, words)) return kPartnerFailed;
+    if (!hf) *own = make_float2(f.m, f.l + own->y);
     // weights of the two streams' O (lane r of both holds the same row where the
-    // tile is not a pair), and the row's maximum and sum
-    float w0 = 1.f, w1 = 0.f, M = f.m, Lsum = f.l;
-    if (!pair) {
-      s_ml[x * kChunkHalfRows + r] = make_float2(f.m, f.l);
-      if (!join()) return false;
+    // tile is not a pair), and the row's maximum and sum over streams and copies
+    float w0 = 1.f, w1 = 0.f, M, Lsum;
+    if (pair) {
+      if (!pair_sync(bar, words)) return kPartnerFailed;
+      M = own->x;
+      Lsum = own->y;
+    } else {
+      if (!join()) return kTimedOut;
       M = -INFINITY;
       for (int c = 0; c < copies; ++c)
         M = fmaxf(M, fmaxf(s_ml[c * copy_rows + rc].x, s_ml[kChunkHalfRows + c * copy_rows + rc].x));
@@ -521,67 +595,73 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
       }
       w0 = weight(s_ml[r].x);
       w1 = weight(s_ml[kChunkHalfRows + r].x);
+      if (!join()) return kTimedOut;  // read, before the next tile's states go there
     }
     const float inv = whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f;
-    T* out = valid ? chunk_out<T>(p, s, row, D) : nullptr;
-    // 8 consecutive columns of this thread's row
-    auto store8 = [&](int col, const float* v) {
-      if (whole) {
-        *reinterpret_cast<uint4*>(out + col) =
-            make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                       pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-      } else {
-        *chunk_acc(p, slot, D, col / 4, row) = make_float4(v[0], v[1], v[2], v[3]);
-        *chunk_acc(p, slot, D, col / 4 + 1, row) = make_float4(v[4], v[5], v[6], v[7]);
-      }
+    w0 *= inv;
+    w1 *= inv;
+    T* out = valid ? chunk_out<T>(p, s.t.q0, s.head, row, D) : nullptr;
+    // 4 consecutive columns of this thread's row
+    auto store4 = [&](int col, float a, float b, float c, float d) {
+      if (whole)
+        *reinterpret_cast<uint2*>(out + col) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+      else
+        *chunk_acc(p, slot, D, col / 4, row) = make_float4(a, b, c, d);
     };
-    // A pair's streams write all columns of their own rows; otherwise each
-    // stream takes half of the columns.
-    const int c_lo = pair ? 0 : x * (D / 2), c_hi = pair ? D : c_lo + D / 2;
-    for (int c = c_lo; c < c_hi; c += 32) {
-      uint32_t o[32];
-      float v[32];
-      tmem_ld32(t_o + (pair ? x * D : 0) + c, o);
+    // A pair's stream writes all columns of its own rows, half by each warp;
+    // otherwise each of a row's four warps takes a quarter of the columns.
+    const int c_lo = pair ? hf * (D / 2) : (x * 2 + hf) * (D / 4);
+    const int c_hi = c_lo + (pair ? D / 2 : D / 4);
+#pragma unroll 1
+    for (int c = c_lo; c < c_hi; c += 16) {
+      float v[16];
+      tmem_ld16(t_o + (pair ? x * D : 0) + c, v);
       if (!pair && n > 1) {
-        uint32_t o1[32];
-        tmem_ld32(t_o + D + c, o1);
+        float v1[16];
+        tmem_ld16(t_o + D + c, v1);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          v[k] = __uint_as_float(o[k]) * w0 + __uint_as_float(o1[k]) * w1;
+        for (int k = 0; k < 16; ++k) v[k] = v[k] * w0 + v1[k] * w1;
       } else {
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * w0;
+        for (int k = 0; k < 16; ++k) v[k] *= w0;
       }
       if (copies <= 1) {
-        if (valid) {
+        if (!valid) continue;
+        if (whole) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) store8(c + k, v + k);
+          for (int k = 0; k < 16; k += 8)
+            *reinterpret_cast<uint4*>(out + c + k) =
+                make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]),
+                           pack_bf16(v[k + 4], v[k + 5]), pack_bf16(v[k + 6], v[k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            *chunk_acc(p, slot, D, (c + k) / 4, row) =
+                make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
         continue;
       }
       // the copies of a row add up; each sums its share of the columns
-      if (c > c_lo && !meet()) return false;  // the columns before have been read
+      if (c > c_lo && !meet()) return kTimedOut;  // the columns before have been read
       if (valid) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s_x[(copy * 32 + k) * copy_rows + rc] = v[k];
+        for (int k = 0; k < 16; ++k) s_x[(copy * 16 + k) * copy_rows + rc] = v[k];
       }
-      if (!meet()) return false;
+      if (!meet()) return kTimedOut;
       if (valid) {
-        const int share = 32 / copies;
-        for (int k0 = copy * share; k0 < (copy + 1) * share; k0 += 8) {
-          float sum[8];
+        const int share = 16 / copies;
+        for (int k0 = copy * share; k0 < (copy + 1) * share; k0 += 4) {
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int cp = 0; cp < copies; ++cp)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sum[k] = s_x[(k0 + k) * copy_rows + rc];
-          for (int cp = 1; cp < copies; ++cp)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += s_x[(cp * 32 + k0 + k) * copy_rows + rc];
-          store8(c + k0, sum);
+            for (int k = 0; k < 4; ++k) sum[k] += s_x[(cp * 16 + k0 + k) * copy_rows + rc];
+          store4(c + k0, sum[0], sum[1], sum[2], sum[3]);
         }
       }
     }
-    if (!whole && valid && (pair || (x == 0 && copy == 0)))
+    if (!whole && valid && hf == 0 && (pair || (x == 0 && copy == 0)))
       p.ws_ml[(size_t)slot * p.tile_rows + row] = make_float2(M, Lsum);
     tc_fence_before();
     fence_proxy_async_smem();  // the exchange's bytes may become query rows again
@@ -589,21 +669,26 @@ __device__ __forceinline__ bool softmax(const ChunkParams& p, const Bars<D>& B, 
     if (lane == 0) mbar_arrive(B.ofree());
     ++nseg;
     if (!whole) {
-      // publish the piece; the CTA whose piece is the last merges them all
-      if (!join()) return false;
+      // publish the piece; the CTA whose piece is the last merges them all, once
+      // it has no other work (a call in this loop would have the compiler keep
+      // the loop's state in memory)
+      if (!join()) return kTimedOut;
       if (warp == 0 && lane == 0) {
         __threadfence();
         int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
-      }
-      if (!join()) return false;
-      if (*s_merge) {
-        __threadfence();
-        chunk_merge<T, D, 2 * kStreamWarps * 32>(p, wk, s, threadIdx.x);
+        if (atomicAdd(cnt, 1) == chunk_pieces(p, s.head, s.tile).y - 1)
+          s_todo[s.first ? 1 : 0] = make_int4(s.t.q0, s.t.n_tok, s.head, s.tile);
       }
     }
   }
-  return true;
+  if (!join()) return kTimedOut;
+  for (int k = 0; k < 2; ++k) {
+    const int4 t = s_todo[k];
+    if (t.y == 0) continue;
+    __threadfence();
+    chunk_merge<T, D, kSoftWarps * 32>(p, t.x, t.y, t.z, t.w, threadIdx.x);
+  }
+  return kDone;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -615,53 +700,68 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Bars<D> B{smem0 + L::kOffBars};
   volatile int* s_meta = reinterpret_cast<volatile int*>(smem + L::kOffMeta);
-  volatile uint32_t* s_words = reinterpret_cast<volatile uint32_t*>(smem + L::kOffWords);
-  if (smem0 & 1023u) {  // the swizzled operands need it; never seen
-    if (threadIdx.x == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
-    return;
-  }
+  volatile PairWords* s_pairs = reinterpret_cast<volatile PairWords*>(smem + L::kOffPairs);
+  volatile uint32_t* s_word = reinterpret_cast<volatile uint32_t*>(smem + L::kOffWord);
+  int4* s_todo = reinterpret_cast<int4*>(smem + L::kOffTodo);
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < 2 * L::kStages + 2; ++i) mbar_init(smem0 + L::kOffBars + 8 * i, 1);
+      mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
-        mbar_init(B.probs(x), kStreamWarps);
+        mbar_init(B.probs(x), kSoftWarps / 2);
         mbar_init(B.out(x), 1);
-        mbar_init(B.meet(x), kStreamWarps);
+        mbar_init(B.meet(2 * x), kSoftWarps / 4);
+        mbar_init(B.meet(2 * x + 1), kSoftWarps / 4);
       }
-      mbar_init(B.ofree(), 2 * kStreamWarps);
-      mbar_init(B.join(), 2 * kStreamWarps);
-      mbar_init(B.drained(), 1);
+      mbar_init(B.ofree(), kSoftWarps);
+      mbar_init(B.join(), kSoftWarps);
       fence_mbar_init();
+      for (int i = 0; i < 8; ++i) s_pairs[i].failed = 0;
+      s_todo[0] = s_todo[1] = make_int4(0, 0, 0, 0);
     }
     __syncwarp();
-    tmem_alloc(smem_u32(smem + L::kOffWords), kTmemCols);
+    tmem_alloc(smem_u32(smem + L::kOffWord), kTmemCols);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_words[0];
+  // What the code takes for granted (never seen otherwise): the swizzled
+  // operands' alignment, and that all of tensor memory starts at column 0.
+  const uint32_t tmem = *s_word;
+  const bool odd = (smem0 & 1023u) != 0 || tmem != 0;
   griddep_wait();  // the tile list, and whatever was written before it
   ChunkWalk wk;
   wk.init(p, blockIdx.x, lane);
-  bool ok = true;
-  if (warp < 8) {
+  bool ok = !odd;
+  if (odd) {
+    // nothing runs; the end below flags it
+  } else if (warp < kSoftWarps) {
     regs_raise<kRegsSoftmax>();
-    ok = softmax<D, CAP, BIAS>(p, B, smem0, smem, tmem, s_meta,
-                               reinterpret_cast<volatile int*>(smem + L::kOffWords) + 2, wk, warp,
-                               lane);
+    volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
+    const int end = softmax<D, CAP, BIAS>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
+    // Every warp but one whose partner failed meets its partner once more: so a
+    // partner that still works learns of a timeout at its next meeting, and none
+    // is left waiting.
+    if (end != kPartnerFailed) {
+      if (end == kTimedOut) words->failed = 1;
+      __syncwarp();
+      (void)pair_sync(1 + (warp >> 3) * 4 + (warp & 3), words);
+    }
+    ok = end == kDone;
   } else {
     regs_drop<kRegsOther>();
   }
-  if (warp == 8) {
+  if (odd) {
+  } else if (warp == kSoftWarps) {
     uint32_t i = 0, nq = 0;
     ok = produce<D>(p, B, smem0, s_meta, wk, lane, i, nq);
     // every copy issued lands before the CTA can end, even after a timeout
     for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
     if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
-  } else if (warp == 9) {
-    ok = issue_mma<D>(p, B, smem0, tmem, wk, lane == 0);
+  } else if (warp == kSoftWarps + 1) {
+    ok = issue_mma<D>(p, B, smem0, wk, lane == 0);
     umma_commit(B.drained(), lane == 0);  // arrives once every MMA issued is done
     (void)mbar_wait(B.drained(), 0);
   }

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= rows) continue;
-      float* o = chunk_out<float>(p, s, r, D);
+      float* o = chunk_out<float>(p, s.t.q0, s.head, r, D);
       const float inv = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
 #pragma unroll
       for (int v = 0; v < kVec; ++v)
@@ -210,12 +210,12 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       if (tid == 0) {
         __threadfence();
         int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, wk, s) - 1;
+        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, s.head, s.tile).y - 1;
       }
       __syncthreads();
       if (*s_merge) {
         __threadfence();
-        chunk_merge<float, D, kThreadsF32>(p, wk, s, tid);
+        chunk_merge<float, D, kThreadsF32>(p, s.t.q0, s.t.n_tok, s.head, s.tile, tid);
       }
     }
   }
