@@ -285,7 +285,7 @@ __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, i
 }
 
 template <typename T, int D, int NT>
-__device__ __noinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok, int head, int tile,
+__device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok, int head, int tile,
                                          int tid) {
   const int2 pc = chunk_pieces(p, head, tile);
   const int c0 = pc.x, n = pc.y;
@@ -312,8 +312,8 @@ __device__ __noinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     T* out = chunk_out<T>(p, q0, head, r, D);
-    if (D / 4 / tpr >= 8)
-      chunk_merge_cols<T, D, 8, 2>(p, c0, n, r, sub, tpr, M, inv, out);
+    if (D / 4 / tpr >= 4)
+      chunk_merge_cols<T, D, 4, 2>(p, c0, n, r, sub, tpr, M, inv, out);
     else
       chunk_merge_cols<T, D, 1, 8>(p, c0, n, r, sub, tpr, M, inv, out);
   }

@@ -11,7 +11,7 @@
 // product, as its tensor-core operand: half an ulp each (2^-9 relative),
 // which is what rounding the output costs anyway.
 //
-// One CTA per SM, twenty warps:
+// One CTA per SM, eighteen warps:
 //   warps 0-7, 8-15 softmax of stream 0 and stream 1: MMA row r (TMEM lane r) of a
 //                   stream belongs to two threads, one in each warp of a pair,
 //                   which split its columns (scores and output)
@@ -19,7 +19,6 @@
 //                   block through the block table, into a ring of stages
 //   warp 17         MMA issue: S = Q.K^T (both operands in shared memory) and
 //                   O += P.V (P in tensor memory), accumulators in tensor memory
-//   warps 18, 19    idle: they complete the warpgroup that gives registers away
 // The rows of an MMA are the tile's query tokens times the query heads that
 // share the KV head, so K and V are read once for all of them.  A tile with
 // more than 128 rows gives each stream its half of the rows and both the same
@@ -47,12 +46,7 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-constexpr int kThreads = 640;
-// Registers per thread: 96 at launch (20 warps); the four softmax warpgroups
-// (whose threads hold half a row's scores) take 104 from the fifth's share:
-// 4 x 104 + 64 = 5 x 96.
-constexpr int kRegsSoftmax = 104, kRegsOther = 64;
-static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * 96, "more registers than the launch has");
+constexpr int kThreads = (kSoftWarps + 2) * 32;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr int kMetaRing = 16;
@@ -737,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   if (odd) {
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
-    regs_raise<kRegsSoftmax>();
     volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
     const int end = softmax<D, CAP, BIAS>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
     // Every warp but one whose partner failed meets its partner once more: so a
@@ -749,10 +742,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       (void)pair_sync(1 + (warp >> 3) * 4 + (warp & 3), words);
     }
     ok = end == kDone;
-  } else {
-    regs_drop<kRegsOther>();
-  }
-  if (odd) {
   } else if (warp == kSoftWarps) {
     uint32_t i = 0, nq = 0;
     ok = produce<D>(p, B, smem0, s_meta, wk, lane, i, nq);
@@ -761,8 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
     if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
   } else if (warp == kSoftWarps + 1) {
-    ok = issue_mma<D>(p, B, smem0, wk, lane == 0);
-    umma_commit(B.drained(), lane == 0);  // arrives once every MMA issued is done
+    const bool lead = elect_one() != 0;
+    ok = issue_mma<D>(p, B, smem0, wk, lead);
+    umma_commit(B.drained(), lead);  // arrives once every MMA issued is done
     (void)mbar_wait(B.drained(), 0);
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);

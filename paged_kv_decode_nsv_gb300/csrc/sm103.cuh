@@ -77,17 +77,6 @@ __device__ __forceinline__ void griddep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Move registers between warpgroups of a CTA (all four warps of a warpgroup
-// run it): the sum over the warpgroups stays within what the launch allotted.
-template <int N>
-__device__ __forceinline__ void regs_raise() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_drop() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy accesses (TMA writes, tcgen05 operand reads) of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -129,6 +118,16 @@ __device__ __forceinline__ uint64_t umma_desc128(uint32_t addr, uint32_t lbo, ui
 __device__ __forceinline__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// 1 in one lane of the warp, 0 in the others.  (With the lane chosen by
+// elect.sync an MMA issues in under 40 cycles, with a comparison of the lane
+// number in its place in 68, more than the 62 that a 128 x 128 x 16 one runs.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(e));
+  return e;
 }
 // D (tensor memory) = A.B (+ D when `accumulate`), run by a whole warp in
 // uniform control flow; only the `lead` lane issues.  A in shared memory (ss)
