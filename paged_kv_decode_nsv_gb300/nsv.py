@@ -31,6 +31,7 @@ fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -349,33 +350,34 @@ def decode_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, cont
 
 def _arg(t, what, dtype, shape, device):
     """The pointer of an argument that must be a contiguous CUDA tensor of this
-    type and shape (-1: any) on `device`; None passes as NULL."""
+    type and shape on device number `device`; None passes as NULL."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != len(shape) or \
-            any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, list(shape), t.dtype,
                                                           list(t.shape)))
-    if t.device != device:
-        raise ValueError("%s is on %s, not on the current device %s" % (what, t.device, device))
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, not on the current CUDA device %d" % (what, t.device, device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
     return t.data_ptr()
 
 
-def _current_device():
+def _raw_stream(stream, device):
+    """The handle of a torch stream (None: the current one on `device`)."""
     import torch
-    return torch.device("cuda", torch.cuda.current_device())
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
-def _scratch(nbytes, workspace, stream):
+def _scratch(nbytes, workspace, stream, device):
     """(tensor, pointer, bytes) of a call's workspace: the caller's, or one
     from torch's allocator that belongs to the call's stream."""
     import torch
     if workspace is not None:
-        return workspace, _ptr(workspace, "workspace"), \
-            workspace.numel() * workspace.element_size()
-    if stream is None or stream == torch.cuda.current_stream():
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the current CUDA device")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if stream is None:
         t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     else:
         with torch.cuda.stream(stream):
@@ -391,32 +393,38 @@ def chunk_workspace_bytes(shape, tokens, num_sms=0):
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _chunk_sizes(device, rows, heads, kv_heads, head_dim, max_blocks, num_blocks, dtype,
+                 block_size, tokens):
+    """A reference to the nsv_shape of these sizes, and its workspace bytes."""
+    shape = make_shape(rows, heads, kv_heads, head_dim, max_blocks, num_blocks, dtype, block_size)
+    return ctypes.byref(shape), chunk_workspace_bytes(shape, tokens)
+
+
 def _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
                 see_begin, see_end):
     import torch
-    dev = _current_device()
-    if q.dim() != 3 or k_pool.dim() != 4 or block_tables.dim() != 2:
+    dev = torch.cuda.current_device()
+    qs, ks, bs, dt, i32 = q.shape, k_pool.shape, block_tables.shape, k_pool.dtype, torch.int32
+    if len(qs) != 3 or len(ks) != 4 or len(bs) != 2:
         raise ValueError("q must be [tokens, heads, head_dim], the pools [blocks + 1, kv_heads, "
                          "16, head_dim] and block_tables [rows, max_blocks]")
-    T, H, D = q.shape
-    R, MB = block_tables.shape
-    NB1, Hkv, B, D2 = k_pool.shape
+    (T, H, D), (NB1, Hkv, B, D2), (R, MB) = qs, ks, bs
     if D2 != D:
         raise ValueError("q head_dim %d != pool head_dim %d" % (D, D2))
-    shape = make_shape(R, H, Hkv, D, MB, NB1 - 1, _dtype_code(k_pool), B)
-    dt, i32 = k_pool.dtype, torch.int32
-    ptrs = (_arg(q, "q", dt, (T, H, D), dev), _arg(k_pool, "k_pool", dt, k_pool.shape, dev),
-            _arg(v_pool, "v_pool", dt, k_pool.shape, dev),
-            _arg(block_tables, "block_tables", i32, (R, MB), dev),
+    ptrs = (_arg(q, "q", dt, qs, dev), _arg(k_pool, "k_pool", dt, ks, dev),
+            _arg(v_pool, "v_pool", dt, ks, dev), _arg(block_tables, "block_tables", i32, bs, dev),
             _arg(chunk_starts, "chunk_starts", i32, (R + 1,), dev),
             _arg(context_lens, "context_lens", i32, (R,), dev))
-    out_ptr = _arg(out, "out", dt, (T, H, D), dev)
+    out_ptr = _arg(out, "out", dt, qs, dev)
+    shape, need = _chunk_sizes(dev, R, H, Hkv, D, MB, NB1 - 1, _dtype_code(k_pool), B, T)
     scores = None
     if softcap or slopes is not None or see_begin is not None or see_end is not None:
-        scores = Scores(float(softcap), _arg(slopes, "slopes", torch.float32, (H,), dev),
-                        _arg(see_begin, "see_begin", i32, (T,), dev),
-                        _arg(see_end, "see_end", i32, (T,), dev))
-    return shape, scores, T, ptrs, out_ptr
+        scores = ctypes.byref(Scores(float(softcap),
+                                     _arg(slopes, "slopes", torch.float32, (H,), dev),
+                                     _arg(see_begin, "see_begin", i32, (T,), dev),
+                                     _arg(see_end, "see_end", i32, (T,), dev)))
+    return shape, scores, T, ptrs, out_ptr, need, dev
 
 
 def paged_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, scale, out,
@@ -425,14 +433,12 @@ def paged_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, sca
     """Attention of each row's new tokens over its paged context (nsv_paged_chunk
     in nsv.h): causal, or with capped and biased scores and visibility bounds.
     workspace: chunk_workspace_bytes() of uint8, or None to allocate it."""
-    shape, scores, T, ptrs, out_ptr = _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts,
-                                                  context_lens, out, softcap, slopes, see_begin,
-                                                  see_end)
-    need = chunk_workspace_bytes(shape, T) if workspace is None else 0
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
-    _check(_lib.nsv_paged_chunk(ctypes.byref(shape), ctypes.byref(scores) if scores else None, T,
-                                *ptrs, float(scale), out_ptr, ws_ptr, ws_bytes, _stream(stream)),
-           "nsv_paged_chunk")
+    shape, scores, T, ptrs, out_ptr, need, dev = _chunk_args(
+        q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
+        see_begin, see_end)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
+    _check(_lib.nsv_paged_chunk(shape, scores, T, *ptrs, float(scale), out_ptr, ws_ptr, ws_bytes,
+                                _raw_stream(stream, dev)), "nsv_paged_chunk")
     return out
 
 
@@ -441,17 +447,15 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
                workspace=None, stream=None):
     """Append the new tokens' keys and values, then paged_chunk, on one stream."""
     import torch
-    shape, scores, T, ptrs, out_ptr = _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts,
-                                                  context_lens, out, softcap, slopes, see_begin,
-                                                  see_end)
-    dev, new = q.device, (T, k_pool.shape[1], q.shape[2])
+    shape, scores, T, ptrs, out_ptr, need, dev = _chunk_args(
+        q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
+        see_begin, see_end)
+    new = (T, k_pool.shape[1], q.shape[2])
     new_ptrs = (_arg(k_new, "k_new", q.dtype, new, dev), _arg(v_new, "v_new", q.dtype, new, dev),
                 _arg(write_slots, "write_slots", torch.int64, (T,), dev))
-    need = chunk_workspace_bytes(shape, T) if workspace is None else 0
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
-    _check(_lib.nsv_chunk_step(ctypes.byref(shape), ctypes.byref(scores) if scores else None, T,
-                               ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr, ws_ptr,
-                               ws_bytes, _stream(stream)), "nsv_chunk_step")
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
+    _check(_lib.nsv_chunk_step(shape, scores, T, ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr,
+                               ws_ptr, ws_bytes, _raw_stream(stream, dev)), "nsv_chunk_step")
     return out
 
 
@@ -463,45 +467,48 @@ def pages_workspace_bytes(rows, num_blocks):
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _page_sizes(rows, max_blocks, num_blocks, kv_heads, head_dim, dtype, block_size):
+    """A reference to the nsv_shape of these sizes, and its workspace bytes."""
+    shape = make_shape(rows, kv_heads, kv_heads, head_dim, max_blocks, num_blocks, dtype,
+                       block_size)
+    return ctypes.byref(shape), pages_workspace_bytes(rows, num_blocks)
+
+
 def _pool_args(k_pool, v_pool, num_blocks, dev):
-    if k_pool.dim() != 4:
+    ks, dt = k_pool.shape, k_pool.dtype
+    if len(ks) != 4:
         raise ValueError("the pools must be [blocks + 1, kv_heads, 16, head_dim]")
-    if num_blocks is not None and k_pool.shape[0] != num_blocks + 1:
+    if num_blocks is not None and ks[0] != num_blocks + 1:
         raise ValueError("the pools have %d blocks and the sink, block_refs %d"
-                         % (k_pool.shape[0] - 1, num_blocks))
-    return (_arg(k_pool, "k_pool", k_pool.dtype, k_pool.shape, dev),
-            _arg(v_pool, "v_pool", k_pool.dtype, k_pool.shape, dev))
+                         % (ks[0] - 1, num_blocks))
+    return _arg(k_pool, "k_pool", dt, ks, dev), _arg(v_pool, "v_pool", dt, ks, dev)
 
 
 def _cache_args(block_tables, context_lens, block_refs, dev):
     import torch
-    i32 = torch.int32
-    if block_tables.dim() != 2:
+    i32, bs, n = torch.int32, block_tables.shape, block_refs.numel()
+    if len(bs) != 2:
         raise ValueError("block_tables must be [rows, max_blocks]")
-    return (_arg(block_tables, "block_tables", i32, block_tables.shape, dev),
-            _arg(context_lens, "context_lens", i32, (block_tables.shape[0],), dev),
-            _arg(block_refs, "block_refs", i32, (-1,), dev))
+    return (_arg(block_tables, "block_tables", i32, bs, dev),
+            _arg(context_lens, "context_lens", i32, bs[:1], dev),
+            _arg(block_refs, "block_refs", i32, (n,), dev)), bs[0], bs[1], n
 
 
-def _page_shape(block_tables, num_blocks, k_pool=None):
-    R, MB = block_tables.shape if block_tables is not None else (0, 1)
-    if k_pool is None:
-        return make_shape(R, 1, 1, 64, MB, num_blocks, F32)
-    _, Hkv, B, D = k_pool.shape
-    return make_shape(R, Hkv, Hkv, D, MB, num_blocks, _dtype_code(k_pool), B)
+def _pool_sizes(rows, max_blocks, k_pool):
+    NB1, Hkv, B, D = k_pool.shape
+    return _page_sizes(rows, max_blocks, NB1 - 1, Hkv, D, _dtype_code(k_pool), B)
 
 
 def blocks_copy(src_blocks, dst_blocks, k_pool, v_pool, stream=None):
     """Copy blocks src_blocks[i] of both pools to dst_blocks[i] (int32 tensors)."""
     import torch
-    dev = _current_device()
+    dev, i32, n = torch.cuda.current_device(), torch.int32, src_blocks.numel()
     pools = _pool_args(k_pool, v_pool, None, dev)
-    n = src_blocks.numel()
-    shape = _page_shape(None, k_pool.shape[0] - 1, k_pool)
-    _check(_lib.nsv_blocks_copy(ctypes.byref(shape), n,
-                                _arg(src_blocks, "src_blocks", torch.int32, (n,), dev),
-                                _arg(dst_blocks, "dst_blocks", torch.int32, (n,), dev), *pools,
-                                _stream(stream)), "nsv_blocks_copy")
+    shape, _ = _pool_sizes(0, 1, k_pool)
+    _check(_lib.nsv_blocks_copy(shape, n, _arg(src_blocks, "src_blocks", i32, (n,), dev),
+                                _arg(dst_blocks, "dst_blocks", i32, (n,), dev), *pools,
+                                _raw_stream(stream, dev)), "nsv_blocks_copy")
 
 
 def rows_fork(parents, children, block_tables, context_lens, block_refs, k_pool, v_pool,
@@ -509,17 +516,14 @@ def rows_fork(parents, children, block_tables, context_lens, block_refs, k_pool,
     """Make empty rows children[i] copies of rows parents[i] (int32 tensors):
     full blocks are shared, a partly filled last one is copied."""
     import torch
-    dev = _current_device()
-    cache = _cache_args(block_tables, context_lens, block_refs, dev)
-    pools = _pool_args(k_pool, v_pool, block_refs.numel(), dev)
-    n = parents.numel()
-    shape = _page_shape(block_tables, block_refs.numel(), k_pool)
-    ids = (_arg(parents, "parents", torch.int32, (n,), dev),
-           _arg(children, "children", torch.int32, (n,), dev))
-    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
-    _check(_lib.nsv_rows_fork(ctypes.byref(shape), n, *ids, *cache, *pools, ws_ptr, ws_bytes,
-                              _stream(stream)), "nsv_rows_fork")
+    dev, i32, n = torch.cuda.current_device(), torch.int32, parents.numel()
+    cache, rows, width, blocks = _cache_args(block_tables, context_lens, block_refs, dev)
+    pools = _pool_args(k_pool, v_pool, blocks, dev)
+    shape, need = _pool_sizes(rows, width, k_pool)
+    ids = _arg(parents, "parents", i32, (n,), dev), _arg(children, "children", i32, (n,), dev)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
+    _check(_lib.nsv_rows_fork(shape, n, *ids, *cache, *pools, ws_ptr, ws_bytes,
+                              _raw_stream(stream, dev)), "nsv_rows_fork")
 
 
 def rows_extend(chunk_starts, block_tables, context_lens, block_refs, write_slots, workspace=None,
@@ -527,42 +531,39 @@ def rows_extend(chunk_starts, block_tables, context_lens, block_refs, write_slot
     """Grow each row by its new tokens: blocks, lengths, and the tokens' write
     slots (int64 [tokens]), as chunk_step takes them."""
     import torch
-    dev = _current_device()
-    cache = _cache_args(block_tables, context_lens, block_refs, dev)
-    starts = _arg(chunk_starts, "chunk_starts", torch.int32, (block_tables.shape[0] + 1,), dev)
-    T = write_slots.numel()
+    dev, T = torch.cuda.current_device(), write_slots.numel()
+    cache, rows, width, blocks = _cache_args(block_tables, context_lens, block_refs, dev)
+    starts = _arg(chunk_starts, "chunk_starts", torch.int32, (rows + 1,), dev)
     slots = _arg(write_slots, "write_slots", torch.int64, (T,), dev)
-    shape = _page_shape(block_tables, block_refs.numel())
-    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
-    _check(_lib.nsv_rows_extend(ctypes.byref(shape), T, starts, *cache, slots, ws_ptr, ws_bytes,
-                                _stream(stream)), "nsv_rows_extend")
+    shape, need = _page_sizes(rows, width, blocks, 1, 64, F32, 16)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
+    _check(_lib.nsv_rows_extend(shape, T, starts, *cache, slots, ws_ptr, ws_bytes,
+                                _raw_stream(stream, dev)), "nsv_rows_extend")
     return write_slots
 
 
 def rows_free(rows, block_tables, context_lens, block_refs, stream=None):
     """Free the rows listed in `rows` (an int32 tensor)."""
     import torch
-    dev = _current_device()
-    cache = _cache_args(block_tables, context_lens, block_refs, dev)
-    n = rows.numel()
-    shape = _page_shape(block_tables, block_refs.numel())
-    _check(_lib.nsv_rows_free(ctypes.byref(shape), n, _arg(rows, "rows", torch.int32, (n,), dev),
-                              *cache, _stream(stream)), "nsv_rows_free")
+    dev, n = torch.cuda.current_device(), rows.numel()
+    cache, R, width, blocks = _cache_args(block_tables, context_lens, block_refs, dev)
+    shape, _ = _page_sizes(R, width, blocks, 1, 64, F32, 16)
+    _check(_lib.nsv_rows_free(shape, n, _arg(rows, "rows", torch.int32, (n,), dev), *cache,
+                              _raw_stream(stream, dev)), "nsv_rows_free")
 
 
 def blocks_compact(block_tables, context_lens, block_refs, k_pool, v_pool, workspace=None,
                    stream=None):
     """Move the blocks in use to the front of the pool; tables and references
     follow."""
-    dev = _current_device()
-    cache = _cache_args(block_tables, context_lens, block_refs, dev)
-    pools = _pool_args(k_pool, v_pool, block_refs.numel(), dev)
-    shape = _page_shape(block_tables, block_refs.numel(), k_pool)
-    need = 0 if workspace is not None else pages_workspace_bytes(shape.rows, shape.num_blocks)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream)
-    _check(_lib.nsv_blocks_compact(ctypes.byref(shape), *cache, *pools, ws_ptr, ws_bytes,
-                                   _stream(stream)), "nsv_blocks_compact")
+    import torch
+    dev = torch.cuda.current_device()
+    cache, rows, width, blocks = _cache_args(block_tables, context_lens, block_refs, dev)
+    pools = _pool_args(k_pool, v_pool, blocks, dev)
+    shape, need = _pool_sizes(rows, width, k_pool)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
+    _check(_lib.nsv_blocks_compact(shape, *cache, *pools, ws_ptr, ws_bytes,
+                                   _raw_stream(stream, dev)), "nsv_blocks_compact")
 
 
 def selftest_bounded_wait(limit_ns, stream=None):
