@@ -39,12 +39,14 @@ __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
 //   prefix  int64 [max_tiles + 1]  units before each tile
 //   tiles   int4 [max_tiles][2]    {row, first query token (global), tokens,
 //           position of the first}, {first key, one past the last key, ctx, 0}
+//   cta     int4 [grid]  where each CTA starts: {units, KV head, tile, units of
+//           the tile before}, and int64 [grid] its first unit
 //   cnt     int32 [max_tiles][kv_heads]  pieces of a cut tile that finished
 //   ml      float2 [grid][2][tile_rows]  running max (log2 units) and sum
 //   acc     float4 [grid][2][head_dim / 4][tile_rows]  unnormalised outputs; the
 //           rows are innermost, because a warp's lanes hold consecutive rows
 struct ChunkWs {
-  uint64_t off_prefix, off_tiles, off_cnt, off_ml, off_acc, total;
+  uint64_t off_prefix, off_tiles, off_cta, off_cnt, off_ml, off_acc, total;
   int max_tiles, tile_rows;
 };
 
@@ -58,7 +60,8 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
   auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
   W.off_prefix = 256;
   W.off_tiles = W.off_prefix + up((uint64_t)(W.max_tiles + 1) * 8);
-  W.off_cnt = W.off_tiles + up((uint64_t)W.max_tiles * 32);
+  W.off_cta = W.off_tiles + up((uint64_t)W.max_tiles * 32);
+  W.off_cnt = W.off_cta + up((uint64_t)grid * 24);
   W.off_ml = W.off_cnt + up((uint64_t)W.max_tiles * kv_heads * 4);
   W.off_acc = W.off_ml + up((uint64_t)grid * 2 * W.tile_rows * 8);
   W.total = W.off_acc + (uint64_t)grid * 2 * W.tile_rows * head_dim * 4;
@@ -81,6 +84,8 @@ struct ChunkParams {
   long long* ws_head;
   long long* ws_prefix;
   int4* ws_tiles;
+  int4* ws_cta;
+  long long* ws_first;
   int32_t* ws_cnt;
   float2* ws_ml;
   float* ws_acc;
@@ -89,6 +94,7 @@ struct ChunkParams {
   long long tokens;
   int rows, heads, kv_heads, group, max_blocks;
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
+  int grid;         // CTAs of the attention kernel
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
@@ -96,8 +102,8 @@ struct ChunkParams {
 
 // Launchers.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
-cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, int grid, cudaStream_t stream);
-cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, int grid, cudaStream_t stream);
+cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t prepare_chunk_bf16();
 cudaError_t prepare_chunk_f32();
 
@@ -105,7 +111,7 @@ cudaError_t prepare_chunk_f32();
 // Units of a tile: runs of `keys` positions; one for a tile that sees nothing
 // (it writes its zeros).
 __device__ __forceinline__ int chunk_units(int kb, int ke, int keys) {
-  return ke > kb ? (ke - kb - 1) / keys + 1 : 1;
+  return ke > kb ? (int)((unsigned)(ke - kb - 1) / (unsigned)keys) + 1 : 1;
 }
 
 // One tile of the list.
@@ -122,57 +128,36 @@ struct ChunkSegment {
   bool first, last;  // whether it starts and ends the tile
 };
 
-// The CTAs that share the units: as many as have at least one.
-struct ChunkShare {
-  long long per_head, U;  // units of one KV head, of all
-  int grid;
-  __device__ explicit ChunkShare(const ChunkParams& p)
-      : per_head(__ldcg(p.ws_head)), U(per_head * p.kv_heads),
-        grid(U < (long long)gridDim.x ? (int)U : (int)gridDim.x) {}
-  // CTA that runs unit x.
-  __device__ int cta_of(long long x) const {
-    const long long c = ((x + 1) * grid + U - 1) / U - 1;
-    return (int)(c < grid - 1 ? c : grid - 1);
+// The CTAs whose pieces make up a tile: the first one, and how many.  All lanes
+// of a warp call together.
+__device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, int head, int tile, int lane) {
+  const long long u0 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile);
+  const long long u1 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile + 1);
+  int before = 0, upto = 0;  // CTAs that start at or before the first, the last unit
+#pragma unroll 1
+  for (int c = 0; c < p.grid; c += 32) {
+    const long long f = c + lane < p.grid ? __ldcg(p.ws_first + c + lane) : u1;
+    before += __popc(__ballot_sync(sm::kFull, f <= u0));
+    upto += __popc(__ballot_sync(sm::kFull, f < u1));
   }
-};
-
-// The CTAs whose pieces make up a tile: the first one, and how many.
-__device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, int head, int tile) {
-  const ChunkShare sh(p);
-  const long long u0 = head * sh.per_head + __ldcg(p.ws_prefix + tile);
-  const long long u1 = head * sh.per_head + __ldcg(p.ws_prefix + tile + 1);
-  const int c0 = sh.cta_of(u0);
-  return make_int2(c0, sh.cta_of(u1 - 1) - c0 + 1);
+  return make_int2(before - 1, upto - before + 1);
 }
 
-// Walks the segments of CTA `c`.  All lanes of a warp call together.  (Kept to
-// a few registers: what the attention kernel spills it reads back from L2,
-// because shared memory leaves the L1 cache next to nothing.)
+// Walks the segments of CTA `c`.  (Kept to a few registers: what the attention
+// kernel spills it reads back from L2, because shared memory leaves the L1 cache
+// next to nothing.)
 struct ChunkWalk {
   int left, head, tile, ntiles, skip;  // units left; where the next segment starts
-  __device__ void init(const ChunkParams& p, int c, int lane) {
-    const ChunkShare sh(p);
+  __device__ void init(const ChunkParams& p, int c) {
+    const int4 at = __ldcg(p.ws_cta + c);
     ntiles = (int)__ldcg(p.ws_head + 1);
-    left = head = tile = skip = 0;
-    if (c >= sh.grid) return;
-    const long long u = (long long)c * sh.U / sh.grid;
-    left = (int)((long long)(c + 1) * sh.U / sh.grid - u);
-    head = (int)(u / sh.per_head);
-    const long long rem = u - head * sh.per_head;
-    // the last tile whose first unit is at most rem, 32 candidates at a time
-    int lo = 0, hi = ntiles;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int i = lo + lane * step;
-      const bool le = i < hi && __ldcg(p.ws_prefix + i) <= rem;
-      const int n = __popc(__ballot_sync(sm::kFull, le));
-      lo += (n - 1) * step;
-      hi = min(hi, lo + step);
-    }
-    tile = lo;
-    skip = (int)(rem - __ldcg(p.ws_prefix + tile));
+    left = at.x;
+    head = at.y;
+    tile = at.z;
+    skip = at.w;
   }
-  __device__ bool next(const ChunkParams& p, ChunkSegment& s) {
+  template <int KEYS>
+  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkSegment& s) {
     if (left <= 0) return false;
     const int4 a = __ldcg(p.ws_tiles + 2 * (size_t)tile);
     const int4 b = __ldcg(p.ws_tiles + 2 * (size_t)tile + 1);
@@ -185,7 +170,7 @@ struct ChunkWalk {
     s.t.ctx = b.z;
     s.head = head;
     s.tile = tile;
-    const int of_tile = chunk_units(s.t.kb, s.t.ke, p.keys) - skip;
+    const int of_tile = chunk_units(s.t.kb, s.t.ke, KEYS) - skip;
     const int take = min(left, of_tile);
     s.j0 = skip;
     s.j1 = skip + take;
@@ -231,38 +216,43 @@ __device__ __forceinline__ T* chunk_out(const ChunkParams& p, int q0, int head, 
   return static_cast<T*>(p.out) + (((size_t)q0 + tok) * p.heads + head * p.group + g) * head_dim;
 }
 
-// Merge of a cut tile by all NT threads of a group of the CTA whose piece
-// arrived last: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the
-// pieces i, in their order.  A row that saw nothing in any piece gives 0.
+// Merge of a cut tile by the NT threads of the CTA whose piece arrived last:
+// out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the n pieces i, of
+// CTAs c0, c0 + 1, ..., in this order.  A row that saw nothing in any piece gives 0.
 //
-// The pieces were just written by other SMs, so a load is an L2 round trip
-// (about 0.5 us) and what counts is how many are in flight: a thread takes one
-// row and, where there are fewer rows than threads, a part of its columns, and
-// sums NV column groups x NS pieces per round.
-template <typename T, int D, int NV, int NS>
+// A warp takes 8 rows and 4 column groups (of 4) at a time, so that both its loads
+// (whole 128-byte lines of consecutive rows) and its stores (32 or 64 bytes of a
+// row) are few lines; where there are few rows the warps share their columns.
+// The pieces were just written by other SMs, a load is an L2 round trip (about
+// 0.5 us), and NG x NS of them are in flight.
+template <typename T, int D, int NG, int NS>
 __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, int n, int row,
-                                                 int v0, int step, float M, float inv, T* out) {
-  for (int v = v0; v < D / 4; v += NV * step) {
-    float4 a[NV];
+                                                 bool valid, int g0, int step, int quad, float M,
+                                                 float inv, T* out) {
+#pragma unroll 1
+  for (int g = g0; g < D / 16; g += NG * step) {
+    float4 a[NG];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < NG; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int b = 0; b < n; b += NS) {
-      float4 x[NV][NS];
+      float4 x[NG][NS];
       float m[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int j = min(b + i, n - 1), slot = chunk_slot(c0 + j, j == 0);
         m[i] = __ldcg(p.ws_ml + (size_t)slot * p.tile_rows + row).x;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-          x[k][i] = __ldcg(chunk_acc(p, slot, D, min(v + k * step, D / 4 - 1), row));
+        for (int k = 0; k < NG; ++k)
+          x[k][i] =
+              __ldcg(chunk_acc(p, slot, D, 4 * min(g + k * step, D / 16 - 1) + quad, row));
       }
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         if (b + i >= n || m[i] == -INFINITY) continue;  // such a state may hold anything
         const float w = exp2f(m[i] - M);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
+        for (int k = 0; k < NG; ++k) {
           a[k].x = fmaf(w, x[k][i].x, a[k].x);
           a[k].y = fmaf(w, x[k][i].y, a[k].y);
           a[k].z = fmaf(w, x[k][i].z, a[k].z);
@@ -271,9 +261,9 @@ __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, i
       }
     }
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (v + k * step >= D / 4) continue;
-      T* o = out + 4 * (v + k * step);
+    for (int k = 0; k < NG; ++k) {
+      if (!valid || g + k * step >= D / 16) continue;
+      T* o = out + 16 * (g + k * step) + 4 * quad;
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4*>(o) =
             make_float4(a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv);
@@ -285,22 +275,24 @@ __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, i
 }
 
 template <typename T, int D, int NT>
-__device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok, int head, int tile,
-                                         int tid) {
-  const int2 pc = chunk_pieces(p, head, tile);
-  const int c0 = pc.x, n = pc.y;
-  const int rows = n_tok * p.group;
-  int tpr = 1;  // threads per row
-  while (tpr < D / 4 && 2 * tpr * rows <= NT) tpr *= 2;
-  const int per = NT / tpr, sub = tid / per;
-  for (int r = tid % per; r < rows; r += per) {
+__device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_tok, int head,
+                                            int c0, int n, int tid) {
+  const int rows = n_tok * p.group, blocks = (rows + 7) / 8;
+  const int lane = tid & 31, quad = lane >> 3;
+  int share = 1;  // warps that share 8 rows
+  while (2 * share <= D / 16 && 2 * share * blocks <= NT / 32) share *= 2;
+#pragma unroll 1
+  for (int rb = (tid >> 5) / share; rb < blocks; rb += NT / 32 / share) {
+    const int row = min(8 * rb + (lane & 7), rows - 1);
+    const bool valid = 8 * rb + (lane & 7) < rows;
     float M = -INFINITY, L = 0.f;
+#pragma unroll 1
     for (int b = 0; b < n; b += 4) {
       float2 ml[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = min(b + i, n - 1);
-        ml[i] = __ldcg(p.ws_ml + (size_t)chunk_slot(c0 + j, j == 0) * p.tile_rows + r);
+        ml[i] = __ldcg(p.ws_ml + (size_t)chunk_slot(c0 + j, j == 0) * p.tile_rows + row);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -311,14 +303,11 @@ __device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    T* out = chunk_out<T>(p, q0, head, r, D);
-    if (D / 4 / tpr >= 4)
-      chunk_merge_cols<T, D, 4, 2>(p, c0, n, r, sub, tpr, M, inv, out);
-    else
-      chunk_merge_cols<T, D, 1, 8>(p, c0, n, r, sub, tpr, M, inv, out);
+    T* out = chunk_out<T>(p, q0, head, row, D);
+    const int g0 = (tid >> 5) % share;
+    chunk_merge_cols<T, D, 2, 4>(p, c0, n, row, valid, g0, share, quad, M, inv, out);
   }
 }
-
 #endif  // __CUDACC__
 
 }  // namespace nsv

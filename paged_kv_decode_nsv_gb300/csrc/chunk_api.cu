@@ -110,6 +110,7 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.ws_head = reinterpret_cast<long long*>(b);
   p.ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
   p.ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
+  p.ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
   p.ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
   p.ws_ml = reinterpret_cast<float2*>(b + W.off_ml);
   p.ws_acc = reinterpret_cast<float*>(b + W.off_acc);
@@ -128,6 +129,8 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.scale = scale;
   p.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
   p.cap = sc ? sc->softcap : 0.f;
+  p.grid = chunk_grid(s, d.num_sms);
+  p.ws_first = reinterpret_cast<long long*>(p.ws_cta + p.grid);
   if (s->dtype == NSV_BF16 &&
       (!encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||
        !encode_q(d, s, tokens, kChunkHalfRows / 2, q, &p.tmap_q[1]) ||
@@ -136,9 +139,8 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
     return cuda_fail();
   if (append && launch_kv_write(*append, stream) != cudaSuccess) return cuda_fail();
   if (launch_chunk_plan(p, stream) != cudaSuccess) return cuda_fail();
-  const int grid = chunk_grid(s, d.num_sms);
-  const cudaError_t e = s->dtype == NSV_F32 ? launch_chunk_f32(p, s->head_dim, grid, stream)
-                                            : launch_chunk_bf16(p, s->head_dim, grid, stream);
+  const cudaError_t e = s->dtype == NSV_F32 ? launch_chunk_f32(p, s->head_dim, stream)
+                                            : launch_chunk_bf16(p, s->head_dim, stream);
   return e == cudaSuccess ? NSV_OK : cuda_fail();
 }
 

@@ -11,7 +11,7 @@
 // product, as its tensor-core operand: half an ulp each (2^-9 relative),
 // which is what rounding the output costs anyway.
 //
-// One CTA per SM, eighteen warps:
+// One CTA per SM, nineteen warps:
 //   warps 0-7, 8-15 softmax of stream 0 and stream 1: MMA row r (TMEM lane r) of a
 //                   stream belongs to two threads, one in each warp of a pair,
 //                   which split its columns (scores and output)
@@ -19,6 +19,7 @@
 //                   block through the block table, into a ring of stages
 //   warp 17         MMA issue: S = Q.K^T (both operands in shared memory) and
 //                   O += P.V (P in tensor memory), accumulators in tensor memory
+//   warp 18         publishes the pieces of cut tiles
 // The rows of an MMA are the tile's query tokens times the query heads that
 // share the KV head, so K and V are read once for all of them.  A tile with
 // more than 128 rows gives each stream its half of the rows and both the same
@@ -46,7 +47,7 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kThreads = (kSoftWarps + 3) * 32;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr int kMetaRing = 16;
@@ -67,9 +68,9 @@ struct Smem {
   static constexpr uint32_t kOffX = D == 128 ? kOffQ + kHalf : kOffQ + 2 * kHalf;
   static constexpr uint32_t kOffMl = D == 128 ? kOffQ + 2 * kHalf : kOffX + 4 * kQuarterX;
   // kOffMl: float2 [2][128]
-  static constexpr uint32_t kOffTodo = kOffMl + 2 * kChunkHalfRows * 8;  // int4 [2]: tiles to merge
-  static constexpr uint32_t kOffBars = kOffTodo + 32;
-  static constexpr int kBars = 2 * kStages + 15;
+  static constexpr uint32_t kOffTodo = kOffMl + 2 * kChunkHalfRows * 8;  // int4 [2][2]: tiles to merge
+  static constexpr uint32_t kOffBars = kOffTodo + 64;
+  static constexpr int kBars = 2 * kStages + 17;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8;
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
   static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address
@@ -92,6 +93,8 @@ struct Bars {
   __device__ uint32_t join() const { return b + 8 * (2 * S + 9); }
   __device__ uint32_t drained() const { return b + 8 * (2 * S + 10); }
   __device__ uint32_t meet(int i) const { return b + 8 * (2 * S + 11 + i); }
+  __device__ uint32_t piece() const { return b + 8 * (2 * S + 15); }
+  __device__ uint32_t published() const { return b + 8 * (2 * S + 16); }
 };
 
 // A bounded wait with one answer for the whole warp.
@@ -120,7 +123,8 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
   uint32_t run = 0;
   int before = 0;  // the previous segment's copies
   ChunkSegment s;
-  while (wk.next(p, s)) {
+#pragma unroll 1
+  while (wk.next<kChunkKeys>(p, s)) {
     // the query rows: one box of (tokens, group heads, 64 dims) per half or
     // copy and 64-dim slice; tokens past the tensor are filled with zeros
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
@@ -134,6 +138,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
       const int box_tok = box_rows / p.group;
       const CUtensorMap* map = &p.tmap_q[copies == 4 ? 2 : copies == 2 ? 1 : 0];
       mbar_arrive_tx(B.qfull(), (uint32_t)(boxes * box_tok * p.group * D * 2));
+#pragma unroll 1
       for (int x = 0; x < boxes; ++x)
         for (int d = 0; d < D / 64; ++d)
           tma_load_3d(smem0 + L::kOffQ + (copies == 0 ? x * L::kHalf : x * box_rows * 128) +
@@ -148,6 +153,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
       return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
     };
     int id = block_id(s.j0);
+#pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
       const bool wanted = lane < kChunkKeys / kBlock &&
                           (long long)s.t.kb + j * kChunkKeys + lane * kBlock < s.t.ke;
@@ -221,10 +227,11 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
   };
   auto free_stage = [&](uint32_t i) { umma_commit(B.empty(i % L::kStages), lead); };
   ChunkSegment s, next;
-  for (bool more = wk.next(p, s); more; s = next) {
+#pragma unroll 1
+  for (bool more = wk.next<kChunkKeys>(p, s); more; s = next) {
     const int n = s.j1 - s.j0;
     const bool pair = copies_of(p, s) == 0;
-    more = wk.next(p, next);  // its loads overlap this segment's work
+    more = wk.next<kChunkKeys>(p, next);  // its loads overlap this segment's work
     if (!warp_wait(B.qfull(), nseg & 1)) return false;
     // Turn k: stream x = k & 1 multiplies the probabilities of its run and starts
     // its next scores.  A pair's streams take every run each (turn 2 j + x), the
@@ -262,6 +269,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
       }
       return true;
     };
+#pragma unroll 1
     for (int k = 0; k < turns; k += 2) {
       if (!turn(0, pair ? k / 2 : k)) return false;
       if (k + 1 < turns && !turn(1, pair ? k / 2 : k + 1)) return false;
@@ -464,6 +472,33 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint
   return true;
 }
 
+// ------------------------------------------------------------------ publishing
+// Once all softmax warps have written a cut tile's piece, counts it; the CTA
+// that counts a tile's last piece will merge it (at most two: the tile that its
+// range starts inside of and the one it ends inside of).
+template <int D>
+__device__ __forceinline__ bool publish(const ChunkParams& p, const Bars<D>& B, int4* s_todo,
+                                        ChunkWalk wk, int lane) {
+  uint32_t n = 0;
+  ChunkSegment s;
+#pragma unroll 1
+  while (wk.next<kChunkKeys>(p, s)) {
+    if (s.first && s.last) continue;
+    const int2 pc = chunk_pieces(p, s.head, s.tile, lane);
+    if (!warp_wait(B.piece(), n++ & 1)) return false;
+    if (lane == 0) {
+      __threadfence();  // (cumulative: what the warps wrote before they arrived)
+      if (atomicAdd(p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head, 1) == pc.y - 1) {
+        s_todo[s.first ? 2 : 0] = make_int4(s.t.q0, s.t.n_tok, s.head, 0);
+        s_todo[s.first ? 3 : 1] = make_int4(pc.x, pc.y, 0, 0);
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(B.published());
+  return true;
+}
+
 // How a softmax warp ends.
 enum : int { kDone = 0, kTimedOut = 1, kPartnerFailed = 2 };
 
@@ -498,7 +533,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     return warp_wait(B.join(), njoin++ & 1);
   };
   ChunkSegment s, next;
-  for (bool more = wk.next(p, s); more; s = next) {
+#pragma unroll 1
+  for (bool more = wk.next<kChunkKeys>(p, s); more; s = next) {
     const int copies = copies_of(p, s);
     const bool pair = copies == 0;
     const int n = s.j1 - s.j0;
@@ -506,11 +542,11 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     // 64, 32 or 16 columns from col0 on
     const int shift = copies == 4 ? 2 : copies == 2 ? 1 : 0;
     const int copy_rows = kChunkHalfRows >> shift;
-    const int copy = r / copy_rows, rc = r - copy * copy_rows;
+    const int copy = r >> (7 - shift), rc = r & (copy_rows - 1);
     const int col0 = (2 * copy + hf) * (64 >> shift);
-    const int ti = rc / p.group, g = rc - ti * p.group;
+    const int ti = (int)((unsigned)rc / (unsigned)p.group), g = rc - ti * p.group;
     const int tok = (pair && x ? half_tok : 0) + ti;  // query token within the tile
-    const bool valid = ti < copy_rows / p.group && tok < s.t.n_tok;
+    const bool valid = (ti + 1) * p.group <= copy_rows && tok < s.t.n_tok;
     const bool any_valid = __any_sync(kFull, valid);
     RowState f;
     f.valid = valid;
@@ -523,6 +559,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     f.l = 0.f;
     const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
+#pragma unroll 1
     for (int j = s.j0 + (pair ? 0 : x); j < s.j1; j += step) {
       const uint32_t run = run0 + (uint32_t)(j - s.j0);
       const int t0 = s.t.kb + j * kChunkKeys;
@@ -557,7 +594,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     }
     run0 += (uint32_t)n;
 
-    more = wk.next(p, next);  // its loads overlap the wait
+    more = wk.next<kChunkKeys>(p, next);  // its loads overlap the wait
     // The segment's end: O is complete once its last product is.
     if (!warp_wait(B.out(x), nseg & 1)) return kTimedOut;
     tc_fence_after();
@@ -579,10 +616,12 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     } else {
       if (!join()) return kTimedOut;
       M = -INFINITY;
+#pragma unroll 1
       for (int c = 0; c < copies; ++c)
         M = fmaxf(M, fmaxf(s_ml[c * copy_rows + rc].x, s_ml[kChunkHalfRows + c * copy_rows + rc].x));
       Lsum = 0.f;
       auto weight = [&](float mm) { return mm == -INFINITY ? 0.f : ex2_approx(mm - M); };
+#pragma unroll 1
       for (int c = 0; c < copies; ++c) {
         const float2 a = s_ml[c * copy_rows + rc], b = s_ml[kChunkHalfRows + c * copy_rows + rc];
         Lsum += a.y * weight(a.x) + b.y * weight(b.x);
@@ -594,14 +633,9 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     const float inv = whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f;
     w0 *= inv;
     w1 *= inv;
-    T* out = valid ? chunk_out<T>(p, s.t.q0, s.head, row, D) : nullptr;
-    // 4 consecutive columns of this thread's row
-    auto store4 = [&](int col, float a, float b, float c, float d) {
-      if (whole)
-        *reinterpret_cast<uint2*>(out + col) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
-      else
-        *chunk_acc(p, slot, D, col / 4, row) = make_float4(a, b, c, d);
-    };
+    // where the tile's rows go: row `off` of this KV head's
+    T* out = static_cast<T*>(p.out) + ((size_t)s.t.q0 * p.heads + s.head * p.group) * D;
+    const int off = valid ? tok * p.heads + g : -1;
     // A pair's stream writes all columns of its own rows, half by each warp;
     // otherwise each of a row's four warps takes a quarter of the columns.
     const int c_lo = pair ? hf * (D / 2) : (x * 2 + hf) * (D / 4);
@@ -621,38 +655,57 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] *= w0;
       }
-      if (copies <= 1) {
+      if (copies > 1) {
+        // the copies of a row add up; each sums its share of the columns
+        if (c > c_lo && !meet()) return kTimedOut;  // the columns before have been read
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) s_x[(copy * 16 + k) * copy_rows + rc] = v[k];
+        }
+        if (!meet()) return kTimedOut;
         if (!valid) continue;
-        if (whole) {
-#pragma unroll
-          for (int k = 0; k < 16; k += 8)
-            *reinterpret_cast<uint4*>(out + c + k) =
-                make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]),
-                           pack_bf16(v[k + 4], v[k + 5]), pack_bf16(v[k + 6], v[k + 7]));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; k += 4)
-            *chunk_acc(p, slot, D, (c + k) / 4, row) =
-                make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+#pragma unroll 1
+        for (int k0 = copy * (16 >> shift); k0 < (copy + 1) * (16 >> shift); k0 += 4) {
+          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float* e = s_x + k0 * copy_rows + rc;
+#pragma unroll 1
+          for (int cp = 0; cp < copies; ++cp, e += 16 * copy_rows) {
+            t.x += e[0];
+            t.y += e[copy_rows];
+            t.z += e[2 * copy_rows];
+            t.w += e[3 * copy_rows];
+          }
+          if (whole)
+            *reinterpret_cast<uint2*>(out + (size_t)off * D + c + k0) =
+                make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+          else
+            *chunk_acc(p, slot, D, (c + k0) / 4, row) = t;
         }
-        continue;
-      }
-      // the copies of a row add up; each sums its share of the columns
-      if (c > c_lo && !meet()) return kTimedOut;  // the columns before have been read
-      if (valid) {
+      } else if (whole) {
+        // Two lanes trade halves, so that each writes 16 of the 32 bytes that the
+        // two have of a row: a store then touches 16 lines and fills its sectors,
+        // where each lane writing its own row would touch 32.
+        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) s_x[(copy * 16 + k) * copy_rows + rc] = v[k];
-      }
-      if (!meet()) return kTimedOut;
-      if (valid) {
-        const int share = 16 / copies;
-        for (int k0 = copy * share; k0 < (copy + 1) * share; k0 += 4) {
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int cp = 0; cp < copies; ++cp)
+        for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+        const bool odd_lane = lane & 1;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum[k] += s_x[(cp * 16 + k0 + k) * copy_rows + rc];
-          store4(c + k0, sum[0], sum[1], sum[2], sum[3]);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t got = __shfl_xor_sync(kFull, odd_lane ? w[k] : w[4 + k], 1);
+          if (odd_lane) w[k] = got; else w[4 + k] = got;
         }
+        // now w[0..3]: the even lane's row, w[4..7]: the odd lane's
+        const int peer = __shfl_xor_sync(kFull, off, 1);
+        const int even = odd_lane ? peer : off, odd = odd_lane ? off : peer;
+        T* o = out + c + (odd_lane ? 8 : 0);
+        if (even >= 0)
+          *reinterpret_cast<uint4*>(o + (size_t)even * D) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (odd >= 0)
+          *reinterpret_cast<uint4*>(o + (size_t)odd * D) = make_uint4(w[4], w[5], w[6], w[7]);
+      } else if (valid) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+          *chunk_acc(p, slot, D, (c + k) / 4, row) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
       }
     }
     if (!whole && valid && hf == 0 && (pair || (x == 0 && copy == 0)))
@@ -663,24 +716,18 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     if (lane == 0) mbar_arrive(B.ofree());
     ++nseg;
     if (!whole) {
-      // publish the piece; the CTA whose piece is the last merges them all, once
-      // it has no other work (a call in this loop would have the compiler keep
-      // the loop's state in memory)
-      if (!join()) return kTimedOut;
-      if (warp == 0 && lane == 0) {
-        __threadfence();
-        int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        if (atomicAdd(cnt, 1) == chunk_pieces(p, s.head, s.tile).y - 1)
-          s_todo[s.first ? 1 : 0] = make_int4(s.t.q0, s.t.n_tok, s.head, s.tile);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.piece());
     }
   }
-  if (!join()) return kTimedOut;
+  // The tiles whose last piece was one of this CTA's are merged now: a merge
+  // within the loop would cost it registers.
+  if (!warp_wait(B.published(), 0)) return kTimedOut;
+  __threadfence();
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    const int4 t = s_todo[k];
-    if (t.y == 0) continue;
-    __threadfence();
-    chunk_merge<T, D, kSoftWarps * 32>(p, t.x, t.y, t.z, t.w, threadIdx.x);
+    const int4 t = s_todo[2 * k], c = s_todo[2 * k + 1];
+    if (t.y) chunk_merge<T, D, kSoftWarps * 32>(p, t.x, t.y, t.z, c.x, c.y, threadIdx.x);
   }
   return kDone;
 }
@@ -710,9 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       }
       mbar_init(B.ofree(), kSoftWarps);
       mbar_init(B.join(), kSoftWarps);
+      mbar_init(B.piece(), kSoftWarps);
+      mbar_init(B.published(), 1);
       fence_mbar_init();
       for (int i = 0; i < 8; ++i) s_pairs[i].failed = 0;
-      s_todo[0] = s_todo[1] = make_int4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) s_todo[i] = make_int4(0, 0, 0, 0);
     }
     __syncwarp();
     tmem_alloc(smem_u32(smem + L::kOffWord), kTmemCols);
@@ -726,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   const bool odd = (smem0 & 1023u) != 0 || tmem != 0;
   griddep_wait();  // the tile list, and whatever was written before it
   ChunkWalk wk;
-  wk.init(p, blockIdx.x, lane);
+  wk.init(p, blockIdx.x);
   bool ok = !odd;
   if (odd) {
     // nothing runs; the end below flags it
@@ -754,6 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     ok = issue_mma<D>(p, B, smem0, wk, lead);
     umma_commit(B.drained(), lead);  // arrives once every MMA issued is done
     (void)mbar_wait(B.drained(), 0);
+  } else {
+    ok = publish<D>(p, B, s_todo, wk, lane);
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();
@@ -763,9 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
 }
 
 template <int D, bool CAP, bool BIAS>
-cudaError_t launch_one(const ChunkParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Smem<D>::kTotal;
   cfg.stream = stream;
@@ -778,12 +829,12 @@ cudaError_t launch_one(const ChunkParams& p, int grid, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_dim(const ChunkParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
   const bool cap = p.cap > 0.f, bias = p.slopes != nullptr;
-  return cap ? (bias ? launch_one<D, true, true>(p, grid, stream)
-                     : launch_one<D, true, false>(p, grid, stream))
-             : (bias ? launch_one<D, false, true>(p, grid, stream)
-                     : launch_one<D, false, false>(p, grid, stream));
+  return cap ? (bias ? launch_one<D, true, true>(p, stream)
+                     : launch_one<D, true, false>(p, stream))
+             : (bias ? launch_one<D, false, true>(p, stream)
+                     : launch_one<D, false, false>(p, stream));
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -808,8 +859,8 @@ cudaError_t prepare_chunk_bf16() {
   return e != cudaSuccess ? e : set_attrs<128>();
 }
 
-cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, int grid, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, grid, stream) : launch_dim<128>(p, grid, stream);
+cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64>(p, stream) : launch_dim<128>(p, stream);
 }
 
 }  // namespace nsv

@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
   constexpr float kLog2e = 1.4426950408889634f;
   griddep_wait();
   ChunkWalk wk;
-  wk.init(p, blockIdx.x, lane);
+  wk.init(p, blockIdx.x);
   ChunkSegment s;
-  while (wk.next(p, s)) {
+  while (wk.next<kC>(p, s)) {
     const int rows = s.t.n_tok * p.group;
     __syncthreads();  // the previous segment's readers are done
     for (int c = tid; c < kR * (D / 4); c += kThreadsF32) {
@@ -207,24 +207,30 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
     if (!whole) {
       // publish the piece; the CTA whose piece is the last merges them all
       __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-        *s_merge = atomicAdd(cnt, 1) == chunk_pieces(p, s.head, s.tile).y - 1;
+      if (tid < 32) {
+        const int2 pc = chunk_pieces(p, s.head, s.tile, lane);
+        if (lane == 0) {
+          __threadfence();
+          int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
+          s_merge[0] = atomicAdd(cnt, 1) == pc.y - 1;
+          s_merge[1] = pc.x;
+          s_merge[2] = pc.y;
+        }
       }
       __syncthreads();
-      if (*s_merge) {
+      if (s_merge[0]) {
         __threadfence();
-        chunk_merge<float, D, kThreadsF32>(p, s.t.q0, s.t.n_tok, s.head, s.tile, tid);
+        chunk_merge<float, D, kThreadsF32>(p, s.t.q0, s.t.n_tok, s.head, s_merge[1], s_merge[2],
+                                           tid);
       }
     }
   }
 }
 
 template <int D>
-cudaError_t launch_dim(const ChunkParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreadsF32);
   cfg.dynamicSmemBytes = SmemF32<D>::kTotal;
   cfg.stream = stream;
@@ -249,8 +255,8 @@ cudaError_t prepare_chunk_f32() {
                                     SmemF32<128>::kTotal);
 }
 
-cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, int grid, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, grid, stream) : launch_dim<128>(p, grid, stream);
+cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64>(p, stream) : launch_dim<128>(p, stream);
 }
 
 }  // namespace nsv

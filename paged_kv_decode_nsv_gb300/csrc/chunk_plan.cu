@@ -63,8 +63,10 @@ __device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool 
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
   __shared__ int s_first[kMaxRows + 1];  // tiles before each row
-  __shared__ int s_kb[kPlanThreads], s_ke[kPlanThreads];
+  __shared__ long long s_prefix[kPlanThreads];
   __shared__ long long s_warp[32];
+  // a tile's key range, before its prefix takes its place
+  int2* s_keys = reinterpret_cast<int2*>(s_prefix);
   sm::griddep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tt = p.tile_tokens;
@@ -118,8 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         kb = __reduce_min_sync(sm::kFull, kb);
         ke = __reduce_max_sync(sm::kFull, ke);
         if (lane == 0) {
-          s_kb[i] = kb < ke ? kb / kBlock * kBlock : 0;
-          s_ke[i] = ke;
+          s_keys[i] = make_int2(kb < ke ? kb / kBlock * kBlock : 0, ke);
         }
       }
       __syncthreads();
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       const int nt = min(tt, c.n - tok0), pos0 = c.ctx - c.n + tok0;
       int kb = 0, ke = 0;
       if (p.see_begin || p.see_end) {
-        kb = s_kb[tid];
-        ke = s_ke[tid];
+        kb = s_keys[tid].x;
+        ke = s_keys[tid].y;
       } else {
         ke = max(0, min(pos0 + nt, c.ctx));
       }
@@ -144,7 +145,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     }
     long long total;
     const long long upto = block_scan(n, s_warp, &total);
-    if (i < ntiles) p.ws_prefix[i] = units + upto - n;
+    if (i < ntiles) {
+      p.ws_prefix[i] = units + upto - n;
+      s_prefix[tid] = units + upto - n;  // used where one pass covers all tiles
+    }
     units += total;
     __syncthreads();
   }
@@ -154,6 +158,33 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     p.ws_head[1] = ntiles;
   }
   for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
+  // Where each CTA's share [c * U / n, (c + 1) * U / n) of the units starts, for
+  // the n CTAs that get at least one; the others get none.
+  __syncthreads();
+  const long long U = units * p.kv_heads;
+  const int n = (int)min(U, (long long)p.grid);
+  for (int c = tid; c < p.grid; c += kPlanThreads) {
+    int4 at = make_int4(0, 0, 0, 0);
+    long long u = U;
+    if (c < n) {
+      u = (long long)c * U / n;
+      at.x = (int)((long long)(c + 1) * U / n - u);
+      at.y = (int)(u / units);
+      const long long rem = u - at.y * units;
+      int lo = 0, hi = ntiles;  // the last tile whose first unit is at most rem
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((ntiles <= kPlanThreads ? s_prefix[mid] : __ldcg(p.ws_prefix + mid)) <= rem)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      at.z = lo;
+      at.w = (int)(rem - (ntiles <= kPlanThreads ? s_prefix[lo] : __ldcg(p.ws_prefix + lo)));
+    }
+    p.ws_cta[c] = at;
+    p.ws_first[c] = u;
+  }
 }
 
 }  // namespace

@@ -57,11 +57,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // in every wait that does not succeed at once.)
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
-  while (true) {
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
     if (clock64() - t0 > kWaitLimitCycles) return false;
-  }
+  return true;
 }
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
