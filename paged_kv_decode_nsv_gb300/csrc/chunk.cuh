@@ -223,34 +223,45 @@ __device__ __forceinline__ T* chunk_out(const ChunkParams& p, int q0, int head, 
 // A warp takes 8 rows and 4 column groups (of 4) at a time, so that both its loads
 // (whole 128-byte lines of consecutive rows) and its stores (32 or 64 bytes of a
 // row) are few lines; where there are few rows the warps share their columns.
-// The pieces were just written by other SMs, a load is an L2 round trip (about
-// 0.5 us), and NG x NS of them are in flight.
+// The pieces were just written by other SMs, a load is an L2 round trip (0.5 to
+// 1 us), and a round has the states of NS pieces and NG x NS of their columns in
+// flight: 8 or 9 loads of 16 bytes a thread.
 template <typename T, int D, int NG, int NS>
 __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, int n, int row,
-                                                 bool valid, int g0, int step, int quad, float M,
-                                                 float inv, T* out) {
+                                                 bool valid, int g0, int step, int quad, T* out) {
 #pragma unroll 1
   for (int g = g0; g < D / 16; g += NG * step) {
+    float M = -INFINITY, L = 0.f;
     float4 a[NG];
 #pragma unroll
     for (int k = 0; k < NG; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int b = 0; b < n; b += NS) {
       float4 x[NG][NS];
-      float m[NS];
+      float2 ml[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int j = min(b + i, n - 1), slot = chunk_slot(c0 + j, j == 0);
-        m[i] = __ldcg(p.ws_ml + (size_t)slot * p.tile_rows + row).x;
+        ml[i] = __ldcg(p.ws_ml + (size_t)slot * p.tile_rows + row);
 #pragma unroll
         for (int k = 0; k < NG; ++k)
           x[k][i] =
               __ldcg(chunk_acc(p, slot, D, 4 * min(g + k * step, D / 16 - 1) + quad, row));
       }
+      float mn = M;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) mn = fmaxf(mn, ml[i].x);
+      if (mn == -INFINITY) continue;  // nothing seen so far
+      const float keep = exp2f(M - mn);
+      M = mn;
+      L *= keep;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) a[k].x *= keep, a[k].y *= keep, a[k].z *= keep, a[k].w *= keep;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        if (b + i >= n || m[i] == -INFINITY) continue;  // such a state may hold anything
-        const float w = exp2f(m[i] - M);
+        if (b + i >= n || ml[i].x == -INFINITY) continue;  // such a state may hold anything
+        const float w = exp2f(ml[i].x - M);
+        L = fmaf(w, ml[i].y, L);
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           a[k].x = fmaf(w, x[k][i].x, a[k].x);
@@ -260,6 +271,7 @@ __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, i
         }
       }
     }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       if (!valid || g + k * step >= D / 16) continue;
@@ -285,27 +297,12 @@ __device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_
   for (int rb = (tid >> 5) / share; rb < blocks; rb += NT / 32 / share) {
     const int row = min(8 * rb + (lane & 7), rows - 1);
     const bool valid = 8 * rb + (lane & 7) < rows;
-    float M = -INFINITY, L = 0.f;
-#pragma unroll 1
-    for (int b = 0; b < n; b += 4) {
-      float2 ml[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = min(b + i, n - 1);
-        ml[i] = __ldcg(p.ws_ml + (size_t)chunk_slot(c0 + j, j == 0) * p.tile_rows + row);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (b + i >= n || ml[i].x == -INFINITY) continue;
-        const float mn = fmaxf(M, ml[i].x);
-        L = L * exp2f(M - mn) + ml[i].y * exp2f(ml[i].x - mn);
-        M = mn;
-      }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
     T* out = chunk_out<T>(p, q0, head, row, D);
     const int g0 = (tid >> 5) % share;
-    chunk_merge_cols<T, D, 2, 4>(p, c0, n, row, valid, g0, share, quad, M, inv, out);
+    if (D / 16 / share >= 4)
+      chunk_merge_cols<T, D, 4, 2>(p, c0, n, row, valid, g0, share, quad, out);
+    else
+      chunk_merge_cols<T, D, 1, 8>(p, c0, n, row, valid, g0, share, quad, out);
   }
 }
 #endif  // __CUDACC__

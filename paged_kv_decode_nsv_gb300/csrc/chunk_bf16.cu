@@ -70,7 +70,7 @@ struct Smem {
   // kOffMl: float2 [2][128]
   static constexpr uint32_t kOffTodo = kOffMl + 2 * kChunkHalfRows * 8;  // int4 [2][2]: tiles to merge
   static constexpr uint32_t kOffBars = kOffTodo + 64;
-  static constexpr int kBars = 2 * kStages + 17;
+  static constexpr int kBars = 2 * kStages + 18;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8;
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
   static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address
@@ -94,6 +94,7 @@ struct Bars {
   __device__ uint32_t drained() const { return b + 8 * (2 * S + 10); }
   __device__ uint32_t meet(int i) const { return b + 8 * (2 * S + 11 + i); }
   __device__ uint32_t piece() const { return b + 8 * (2 * S + 15); }
+  __device__ uint32_t mlfree() const { return b + 8 * (2 * S + 17); }
   __device__ uint32_t published() const { return b + 8 * (2 * S + 16); }
 };
 
@@ -559,6 +560,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     f.l = 0.f;
     const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
+    // the states' exchange is free: every warp has read the previous tile's
+    if (nseg && !warp_wait(B.mlfree(), (nseg - 1) & 1)) return kTimedOut;
 #pragma unroll 1
     for (int j = s.j0 + (pair ? 0 : x); j < s.j1; j += step) {
       const uint32_t run = run0 + (uint32_t)(j - s.j0);
@@ -628,8 +631,9 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
       }
       w0 = weight(s_ml[r].x);
       w1 = weight(s_ml[kChunkHalfRows + r].x);
-      if (!join()) return kTimedOut;  // read, before the next tile's states go there
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.mlfree());  // read: the next tile's states may go there
     const float inv = whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f;
     w0 *= inv;
     w1 *= inv;
@@ -640,72 +644,84 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     // otherwise each of a row's four warps takes a quarter of the columns.
     const int c_lo = pair ? hf * (D / 2) : (x * 2 + hf) * (D / 4);
     const int c_hi = c_lo + (pair ? D / 2 : D / 4);
+    // Copies are added up through shared memory: all columns at once where the
+    // rows fill at most half of a copy's, else 16 at a time.
+    const bool few = 2 * s.t.n_tok * p.group <= copy_rows;
+    const int round = copies > 1 ? (few ? D / 4 : 16) : c_hi - c_lo;
+    const int x_rows = few ? copy_rows / 2 : copy_rows;  // its row stride
 #pragma unroll 1
-    for (int c = c_lo; c < c_hi; c += 16) {
-      float v[16];
-      tmem_ld16(t_o + (pair ? x * D : 0) + c, v);
-      if (!pair && n > 1) {
-        float v1[16];
-        tmem_ld16(t_o + D + c, v1);
-        tmem_wait_ld();
+    for (int cr = c_lo; cr < c_hi; cr += round) {
+      if (cr > c_lo && !meet()) return kTimedOut;  // the columns before have been read
+#pragma unroll 1
+      for (int c = cr; c < cr + round; c += 16) {
+        float v[16];
+        tmem_ld16(t_o + (pair ? x * D : 0) + c, v);
+        if (!pair && n > 1) {
+          float v1[16];
+          tmem_ld16(t_o + D + c, v1);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = v[k] * w0 + v1[k] * w1;
-      } else {
-        tmem_wait_ld();
+          for (int k = 0; k < 16; ++k) v[k] = v[k] * w0 + v1[k] * w1;
+        } else {
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] *= w0;
+          for (int k = 0; k < 16; ++k) v[k] *= w0;
+        }
+        if (copies > 1) {
+          float* e = s_x + (copy * round + c - cr) * x_rows + rc;
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) e[k * x_rows] = v[k];
+          }
+        } else if (whole) {
+          // Two lanes trade halves, so that each writes 16 of the 32 bytes that the
+          // two have of a row: a store then touches 16 lines and fills its sectors,
+          // where each lane writing its own row would touch 32.
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+          const bool odd_lane = lane & 1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t got = __shfl_xor_sync(kFull, odd_lane ? w[k] : w[4 + k], 1);
+            if (odd_lane) w[k] = got; else w[4 + k] = got;
+          }
+          // now w[0..3]: the even lane's row, w[4..7]: the odd lane's
+          const int peer = __shfl_xor_sync(kFull, off, 1);
+          const int even = odd_lane ? peer : off, odd = odd_lane ? off : peer;
+          T* o = out + c + (odd_lane ? 8 : 0);
+          if (even >= 0)
+            *reinterpret_cast<uint4*>(o + (size_t)even * D) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (odd >= 0)
+            *reinterpret_cast<uint4*>(o + (size_t)odd * D) = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (valid) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            *chunk_acc(p, slot, D, (c + k) / 4, row) =
+                make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
       }
       if (copies > 1) {
-        // the copies of a row add up; each sums its share of the columns
-        if (c > c_lo && !meet()) return kTimedOut;  // the columns before have been read
-        if (valid) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) s_x[(copy * 16 + k) * copy_rows + rc] = v[k];
-        }
         if (!meet()) return kTimedOut;
-        if (!valid) continue;
+        // each copy sums its share of the columns
+        const int share = round >> shift;
 #pragma unroll 1
-        for (int k0 = copy * (16 >> shift); k0 < (copy + 1) * (16 >> shift); k0 += 4) {
+        for (int k0 = copy * share; valid && k0 < (copy + 1) * share; k0 += 4) {
           float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float* e = s_x + k0 * copy_rows + rc;
+          const float* e = s_x + k0 * x_rows + rc;
 #pragma unroll 1
-          for (int cp = 0; cp < copies; ++cp, e += 16 * copy_rows) {
+          for (int cp = 0; cp < copies; ++cp, e += round * x_rows) {
             t.x += e[0];
-            t.y += e[copy_rows];
-            t.z += e[2 * copy_rows];
-            t.w += e[3 * copy_rows];
+            t.y += e[x_rows];
+            t.z += e[2 * x_rows];
+            t.w += e[3 * x_rows];
           }
           if (whole)
-            *reinterpret_cast<uint2*>(out + (size_t)off * D + c + k0) =
+            *reinterpret_cast<uint2*>(out + (size_t)off * D + cr + k0) =
                 make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
           else
-            *chunk_acc(p, slot, D, (c + k0) / 4, row) = t;
+            *chunk_acc(p, slot, D, (cr + k0) / 4, row) = t;
         }
-      } else if (whole) {
-        // Two lanes trade halves, so that each writes 16 of the 32 bytes that the
-        // two have of a row: a store then touches 16 lines and fills its sectors,
-        // where each lane writing its own row would touch 32.
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-        const bool odd_lane = lane & 1;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t got = __shfl_xor_sync(kFull, odd_lane ? w[k] : w[4 + k], 1);
-          if (odd_lane) w[k] = got; else w[4 + k] = got;
-        }
-        // now w[0..3]: the even lane's row, w[4..7]: the odd lane's
-        const int peer = __shfl_xor_sync(kFull, off, 1);
-        const int even = odd_lane ? peer : off, odd = odd_lane ? off : peer;
-        T* o = out + c + (odd_lane ? 8 : 0);
-        if (even >= 0)
-          *reinterpret_cast<uint4*>(o + (size_t)even * D) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (odd >= 0)
-          *reinterpret_cast<uint4*>(o + (size_t)odd * D) = make_uint4(w[4], w[5], w[6], w[7]);
-      } else if (valid) {
-#pragma unroll
-        for (int k = 0; k < 16; k += 4)
-          *chunk_acc(p, slot, D, (c + k) / 4, row) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
       }
     }
     if (!whole && valid && hf == 0 && (pair || (x == 0 && copy == 0)))
@@ -759,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       mbar_init(B.join(), kSoftWarps);
       mbar_init(B.piece(), kSoftWarps);
       mbar_init(B.published(), 1);
+      mbar_init(B.mlfree(), kSoftWarps);
       fence_mbar_init();
       for (int i = 0; i < 8; ++i) s_pairs[i].failed = 0;
       for (int i = 0; i < 4; ++i) s_todo[i] = make_int4(0, 0, 0, 0);
