@@ -1,12 +1,24 @@
-// Attention of a chunk of new tokens over a paged cache, fp32, on the CUDA
-// cores (the tensor cores take no fp32 operand; see chunk_bf16.cu for the
-// formulas).  A CTA of 256 threads folds runs of 64 positions into up to 64
-// rows (query tokens x query heads of one KV head).  The scores of a run are a
-// 64 x 64 product of which a thread computes 4 x 4 from shared memory; the
-// probabilities go back through shared memory (over the keys, which are done)
-// for the second product, of which a thread holds 4 rows x head_dim / 16 dims in
-// registers.  Everything is fp32, the exponentials by exp2f.  Two CTAs per SM,
-// so that one computes while the other loads.
+// Attention of a chunk of new tokens over a paged cache, fp32 (see
+// chunk_bf16.cu for the formulas).  A CTA of 256 threads folds runs of 64
+// positions into up to 64 rows (query tokens x query heads of one KV head).
+//
+// Both products run on the tensor cores at fp32's precision, each factor as a
+// sum of two tf32 numbers (x = hi + lo, hi = x rounded to tf32's 11 bits, lo the
+// rest): a b = a_hi b_hi + a_hi b_lo + a_lo b_hi, where what is left out, a_lo
+// b_lo, is 2^-22 of the product, and lo's own truncation to tf32 as much.  With
+// fp32 multiply-adds on the CUDA cores instead the kernel was bound by
+// shared-memory loads (8 of 16 bytes for every 64 multiply-adds of a 4 x 4 tile a
+// thread): 207 us for 638 tokens over up to 2048 positions at 12 heads.
+//
+// Warp (wm, wn) of 4 x 2: 16 rows; half of the keys in the scores, half of the
+// dims in the output.  m16n8k8 fragments, lane = 4 g + t: A rows g and g + 8 at k
+// = t and t + 4, B column g, C rows g and g + 8 at columns 2 t and 2 t + 1.  The
+// probabilities go through shared memory.  The next run's keys are copied
+// (cp.async) from the end of this run's scores on, its values from the end of
+// its products on, and two CTAs share an SM.  Rows of 16-byte chunks are stored
+// swizzled, so that the fragments' loads hit all banks: chunk v of row r at
+// v ^ (r % 8), of the values' rows (which B reads down the columns) at
+// v ^ 2 (r % 4).
 
 #include "chunk.cuh"
 
@@ -20,30 +32,79 @@ constexpr int kR = kChunkRowsF32, kC = kChunkKeysF32;
 
 template <int D>
 struct SmemF32 {
-  static constexpr int kLd = D + 4;  // rows padded so that 16 lanes hit 16 bank groups
-  static constexpr int kLdP = kC + 4;
-  static constexpr uint32_t kOffK = kR * kLd * 4;
-  static constexpr uint32_t kOffV = kOffK + kC * kLd * 4;
-  static constexpr uint32_t kOffOk = kOffV + kC * D * 4;
-  static constexpr uint32_t kOffMerge = kOffOk + kC * 4;
+  static constexpr uint32_t kOffK = kR * D * 4;
+  static constexpr uint32_t kOffV = kOffK + kC * D * 4;
+  static constexpr uint32_t kOffP = kOffV + kC * D * 4;
+  static constexpr uint32_t kOffX = kOffP + kR * kC * 4;   // float [2][64]: maxima, sums
+  static constexpr uint32_t kOffOk = kOffX + 2 * kR * 4;   // blocks of two runs in turn
+  static constexpr uint32_t kOffMerge = kOffOk + 16;
   static constexpr uint32_t kTotal = kOffMerge + 16;
-  static_assert(kR * kLdP <= kC * kLd, "probabilities fit over the keys");
+  static_assert(2 * (kTotal + 1024) <= 228 * 1024, "two CTAs per SM");
 };
+
+// 16 bytes global -> shared, asynchronously; zeros where there is nothing.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Float index of 16-byte chunk v of row r, W floats to a row; of the values'.
+template <int W>
+__device__ __forceinline__ int at_chunk(int r, int v) {
+  return r * W + ((v ^ (r & 7)) << 2);
+}
+template <int W>
+__device__ __forceinline__ int at_value(int r, int v) {
+  return r * W + ((v ^ ((r & 3) << 1)) << 2);
+}
+
+// x = hi + lo.
+struct Split {
+  uint32_t hi, lo;
+  __device__ __forceinline__ explicit Split(float x) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest, ties away from zero
+    lo = __float_as_uint(x - __uint_as_float(hi));
+  }
+};
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += A B, the small products first.
+__device__ __forceinline__ void mma_f32(float (&d)[4], const Split (&a)[4], const Split& b0,
+                                        const Split& b1) {
+  mma_tf32(d, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
+  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
     const __grid_constant__ ChunkParams p) {
   using L = SmemF32<D>;
-  constexpr int kVec = D / 64;  // float4 of a row's dims that a thread owns
+  constexpr int kNt = D / 16;  // 8-column tiles of a warp's half of the dims
   extern __shared__ __align__(16) unsigned char smem[];
   float* sq = reinterpret_cast<float*>(smem);
   float* sk = reinterpret_cast<float*>(smem + L::kOffK);
-  float* sp = sk;
   float* sv = reinterpret_cast<float*>(smem + L::kOffV);
+  float* sp = reinterpret_cast<float*>(smem + L::kOffP);
+  float* s_x = reinterpret_cast<float*>(smem + L::kOffX);
   int* s_ok = reinterpret_cast<int*>(smem + L::kOffOk);
   int* s_merge = reinterpret_cast<int*>(smem + L::kOffMerge);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, t4 = lane & 3;
+  const int r0 = wm * 16 + g;  // this thread's rows: r0 and r0 + 8
   const float* q = static_cast<const float*>(p.q);
   const float* kp = static_cast<const float*>(p.k_pool);
   const float* vp = static_cast<const float*>(p.v_pool);
@@ -52,157 +113,184 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
   ChunkWalk wk;
   wk.init(p, blockIdx.x);
   ChunkSegment s;
+#pragma unroll 1
   while (wk.next<kC>(p, s)) {
     const int rows = s.t.n_tok * p.group;
     __syncthreads();  // the previous segment's readers are done
     for (int c = tid; c < kR * (D / 4); c += kThreadsF32) {
       const int r = c / (D / 4), v = c - r * (D / 4);
-      const int tok = r / p.group, g = r - tok * p.group;
+      const int tok = (int)((unsigned)r / (unsigned)p.group), h = r - tok * p.group;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
         x = __ldg(reinterpret_cast<const float4*>(
-                      q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D) + v);
-      *reinterpret_cast<float4*>(sq + r * L::kLd + v * 4) = x;
+                      q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + h) * D) + v);
+      *reinterpret_cast<float4*>(sq + at_chunk<D>(r, v)) = x;
     }
-    int2 see[4];
-    int pos[4];
-    float slope[4], m[4], l[4], acc[4][4 * kVec];
+    int2 see[2];
+    int pos[2];
+    float slope[2], m[2], l[2], acc[kNt][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i, tok = r / p.group, g = r - tok * p.group;
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i, tok = (int)((unsigned)r / (unsigned)p.group);
       pos[i] = s.t.pos0 + tok;
       see[i] = r < rows ? chunk_sees(p, (long long)s.t.q0 + tok, pos[i], s.t.ctx) : make_int2(0, 0);
-      slope[i] = r < rows && p.slopes ? __ldg(p.slopes + s.head * p.group + g) : 0.f;
+      slope[i] =
+          r < rows && p.slopes ? __ldg(p.slopes + s.head * p.group + r - tok * p.group) : 0.f;
       m[i] = -INFINITY;
       l[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4 * kVec; ++e) acc[i][e] = 0.f;
     }
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
-    for (int j = s.j0; j < s.j1; ++j) {
+    // Copies one run's keys (or values); positions at and past `ke` (at most the
+    // context) and in bad blocks become zeros.
+    auto copy_run = [&](const float* pool, float* dst, int j, bool keys) {
       const int t0 = s.t.kb + j * kC;
-      __syncthreads();  // the run before has been read
+#pragma unroll 4
       for (int c = tid; c < kC * (D / 4); c += kThreadsF32) {
         const int t = c / (D / 4), v = c - t * (D / 4);
-        float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-        bool ok = (long long)t0 + t < s.t.ke;  // ke is at most the context
-        if (ok) {
-          const int b = __ldg(table + (t0 + t) / kBlock);
-          ok = b >= 0 && b < p.pool_blocks;
-          if (ok) {
-            const size_t at =
-                (((size_t)b * p.kv_heads + s.head) * kBlock + (t0 + t) % kBlock) * D + v * 4;
-            kx = __ldg(reinterpret_cast<const float4*>(kp + at));
-            vx = __ldg(reinterpret_cast<const float4*>(vp + at));
-          } else if (v == 0) {
-            atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-          }
-        }
-        if (v == 0) s_ok[t] = ok;
-        *reinterpret_cast<float4*>(sk + t * L::kLd + v * 4) = kx;
-        *reinterpret_cast<float4*>(sv + t * D + v * 4) = vx;
+        bool ok = (long long)t0 + t < s.t.ke;
+        const int b = ok ? __ldg(table + (t0 + t) / kBlock) : 0;
+        const bool bad = b < 0 || b >= p.pool_blocks;
+        if (keys && bad && v == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+        ok = ok && !bad;
+        const size_t at =
+            ok ? (((size_t)b * p.kv_heads + s.head) * kBlock + (t0 + t) % kBlock) * D + v * 4 : 0;
+        copy16(dst + (keys ? at_chunk<D>(t, v) : at_value<D>(t, v)), pool + at, ok);
       }
+      copies_commit();
+    };
+    // which of a run's blocks hold something
+    auto run_blocks = [&](int j) {
+      if (tid < 32) {
+        const int t = s.t.kb + j * kC + tid * kBlock;
+        const int b = tid < kC / kBlock && t < s.t.ke ? __ldg(table + t / kBlock) : -1;
+        const unsigned ok = __ballot_sync(kFull, b >= 0 && b < p.pool_blocks);
+        if (tid == 0) s_ok[j & 1] = (int)ok;
+      }
+    };
+    copy_run(kp, sk, s.j0, true);
+    copy_run(vp, sv, s.j0, false);
+    run_blocks(s.j0);
+#pragma unroll 1
+    for (int j = s.j0; j < s.j1; ++j) {
+      const int t0 = s.t.kb + j * kC;
+      copies_wait<1>();  // the keys
       __syncthreads();
-      float sc[4][4];
+      float sc[4][4];  // keys wn * 32 + n * 8 + 2 t4 + {0, 1}, rows r0 and r0 + 8
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[i][c] = 0.f;
+      for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
+      for (int ks = 0; ks < D / 8; ++ks) {
+        const Split a[4] = {Split(sq[at_chunk<D>(r0, 2 * ks) + t4]),
+                            Split(sq[at_chunk<D>(r0 + 8, 2 * ks) + t4]),
+                            Split(sq[at_chunk<D>(r0, 2 * ks + 1) + t4]),
+                            Split(sq[at_chunk<D>(r0 + 8, 2 * ks + 1) + t4])};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * L::kLd + d);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          b[c] = *reinterpret_cast<const float4*>(sk + (tx + 16 * c) * L::kLd + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            sc[i][c] = fmaf(a[i].x, b[c].x, sc[i][c]);
-            sc[i][c] = fmaf(a[i].y, b[c].y, sc[i][c]);
-            sc[i][c] = fmaf(a[i].z, b[c].z, sc[i][c]);
-            sc[i][c] = fmaf(a[i].w, b[c].w, sc[i][c]);
-          }
+        for (int n = 0; n < 4; ++n) {
+          const int key = wn * 32 + n * 8 + g;
+          mma_f32(sc[n], a, Split(sk[at_chunk<D>(key, 2 * ks) + t4]),
+                  Split(sk[at_chunk<D>(key, 2 * ks + 1) + t4]));
+        }
       }
+      const int blocks = s_ok[j & 1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int t = tx + 16 * c;
-          float x = sc[i][c] * p.scale;
-          if (p.cap > 0.f) x = p.cap * tanhf(x / p.cap);
-          x = fmaf(-slope[i], fabsf((float)(pos[i] - t0 - t)), x) * kLog2e;
-          const bool seen = t0 + t >= see[i].x && t0 + t < see[i].y && s_ok[t];
-          sc[i][c] = seen ? x : -INFINITY;
-          mx = fmaxf(mx, sc[i][c]);
-        }
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-        if (mx > m[i]) {  // the same for the row's 16 lanes
+          for (int e = 0; e < 2; ++e) {
+            const int t = wn * 32 + n * 8 + 2 * t4 + e;
+            float x = sc[n][2 * i + e] * p.scale;
+            if (p.cap > 0.f) x = p.cap * tanhf(x / p.cap);
+            x = fmaf(-slope[i], fabsf((float)(pos[i] - t0 - t)), x) * kLog2e;
+            const bool seen =
+                t0 + t >= see[i].x && t0 + t < see[i].y && ((blocks >> (t / kBlock)) & 1);
+            sc[n][2 * i + e] = seen ? x : -INFINITY;
+            mx = fmaxf(mx, sc[n][2 * i + e]);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        if (t4 == 0) s_x[wn * kR + r0 + 8 * i] = mx;
+      }
+      __syncthreads();  // the keys are free, the maxima of both halves there
+      if (j + 1 < s.j1) {
+        copy_run(kp, sk, j + 1, true);
+        run_blocks(j + 1);
+      } else {
+        copies_commit();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mx = fmaxf(s_x[r0 + 8 * i], s_x[kR + r0 + 8 * i]);
+        if (mx > m[i]) {
           const float alpha = exp2f(m[i] - mx);
           m[i] = mx;
           l[i] *= alpha;
 #pragma unroll
-          for (int e = 0; e < 4 * kVec; ++e) acc[i][e] *= alpha;
+          for (int n = 0; n < kNt; ++n) {
+            acc[n][2 * i] *= alpha;
+            acc[n][2 * i + 1] *= alpha;
+          }
         }
         const float sub = m[i] == -INFINITY ? 0.f : m[i];
-        float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          sc[i][c] = exp2f(sc[i][c] - sub);
-          sum += sc[i][c];
+        for (int n = 0; n < 4; ++n) {
+          const float p0 = exp2f(sc[n][2 * i] - sub), p1 = exp2f(sc[n][2 * i + 1] - sub);
+          l[i] += p0 + p1;  // this thread's keys
+          const int t = wn * 32 + n * 8 + 2 * t4;
+          *reinterpret_cast<float2*>(sp + at_chunk<kC>(r0 + 8 * i, t >> 2) + (t & 3)) =
+              make_float2(p0, p1);
         }
-#pragma unroll
-        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        l[i] += sum;
       }
-      __syncthreads();  // every thread is done with the keys
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sp[(ty * 4 + i) * L::kLdP + tx + 16 * c] = sc[i][c];
-      __syncwarp();  // a row's probabilities are written and read by one warp
+      copies_wait<1>();  // the values (the next run's keys may still be on their way)
+      __syncthreads();
 #pragma unroll 2
-      for (int t = 0; t < kC; t += 4) {
-        float4 pr[4];
+      for (int ks = 0; ks < kC / 8; ++ks) {
+        const Split a[4] = {Split(sp[at_chunk<kC>(r0, 2 * ks) + t4]),
+                            Split(sp[at_chunk<kC>(r0 + 8, 2 * ks) + t4]),
+                            Split(sp[at_chunk<kC>(r0, 2 * ks + 1) + t4]),
+                            Split(sp[at_chunk<kC>(r0 + 8, 2 * ks + 1) + t4])};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pr[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * L::kLdP + t);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const float4 x = *reinterpret_cast<const float4*>(sv + (t + u) * D + v * 64 + tx * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = u == 0 ? pr[i].x : u == 1 ? pr[i].y : u == 2 ? pr[i].z : pr[i].w;
-              acc[i][4 * v] = fmaf(w, x.x, acc[i][4 * v]);
-              acc[i][4 * v + 1] = fmaf(w, x.y, acc[i][4 * v + 1]);
-              acc[i][4 * v + 2] = fmaf(w, x.z, acc[i][4 * v + 2]);
-              acc[i][4 * v + 3] = fmaf(w, x.w, acc[i][4 * v + 3]);
-            }
-          }
+        for (int n = 0; n < kNt; ++n) {
+          const int d = wn * (D / 2) + n * 8 + g;
+          mma_f32(acc[n], a, Split(sv[at_value<D>(ks * 8 + t4, d >> 2) + (d & 3)]),
+                  Split(sv[at_value<D>(ks * 8 + 4 + t4, d >> 2) + (d & 3)]));
+        }
       }
+      __syncthreads();  // the values and probabilities are free
+      if (j + 1 < s.j1)
+        copy_run(vp, sv, j + 1, false);
+      else
+        copies_commit();
     }
+    // the rows' sums over the quad's and both halves' keys
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(kFull, l[i], 1);
+      l[i] += __shfl_xor_sync(kFull, l[i], 2);
+      if (t4 == 0) s_x[wn * kR + r0 + 8 * i] = l[i];
+    }
+    __syncthreads();
     const bool whole = s.first && s.last;
     const int slot = chunk_slot(blockIdx.x, s.first);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i;
       if (r >= rows) continue;
+      const float sum = s_x[r] + s_x[kR + r];
       float* o = chunk_out<float>(p, s.t.q0, s.head, r, D);
-      const float inv = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
+      const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
 #pragma unroll
-      for (int v = 0; v < kVec; ++v)
-        *(whole ? reinterpret_cast<float4*>(o + v * 64 + tx * 4)
-                : chunk_acc(p, slot, D, v * 16 + tx, r)) =
-            make_float4(acc[i][4 * v] * inv, acc[i][4 * v + 1] * inv, acc[i][4 * v + 2] * inv,
-                        acc[i][4 * v + 3] * inv);
-      if (!whole && tx == 0) p.ws_ml[(size_t)slot * p.tile_rows + r] = make_float2(m[i], l[i]);
+      for (int n = 0; n < kNt; ++n) {
+        const int d = wn * (D / 2) + n * 8 + 2 * t4;
+        *reinterpret_cast<float2*>(
+            whole ? o + d : reinterpret_cast<float*>(chunk_acc(p, slot, D, d >> 2, r)) + (d & 3)) =
+            make_float2(acc[n][2 * i] * inv, acc[n][2 * i + 1] * inv);
+      }
+      if (!whole && wn == 0 && t4 == 0)
+        p.ws_ml[(size_t)slot * p.tile_rows + r] = make_float2(m[i], sum);
     }
     if (!whole) {
       // publish the piece; the CTA whose piece is the last merges them all

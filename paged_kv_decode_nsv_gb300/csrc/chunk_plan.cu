@@ -15,6 +15,7 @@ namespace nsv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kWholeUnits = 8;
 
 // Inclusive sum over the block's threads; *total is the block's.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   };
 
   long long units = 0;
+  int longest = 0;  // units of the longest tile
   for (int base = 0; base < ntiles; base += kPlanThreads) {
     if (p.see_begin || p.see_end) {
       // a warp per tile: the range that its tokens see
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       s_prefix[tid] = units + upto - n;  // used where one pass covers all tiles
     }
     units += total;
+    longest = max(longest, (int)n);
     __syncthreads();
   }
   if (tid == 0) {
@@ -158,15 +161,25 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     p.ws_head[1] = ntiles;
   }
   for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
-  // Where each CTA's share [c * U / n, (c + 1) * U / n) of the units starts, for
+  // Where each CTA's share of the units starts: [c * U / n, (c + 1) * U / n) for
   // the n CTAs that get at least one; the others get none.
-  __syncthreads();
+  // Where there is a CTA for every tile and head, and the tiles are short, each
+  // CTA gets one whole: up to kWholeUnits units take less time one after the other
+  // (0.5 us each) than the pieces of a cut tile take to be published and merged
+  // (5 us).
+  const bool whole = !__syncthreads_or(longest > kWholeUnits) &&
+                     (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
-  const int n = (int)min(U, (long long)p.grid);
+  const int n = whole ? ntiles * p.kv_heads : (int)min(U, (long long)p.grid);
   for (int c = tid; c < p.grid; c += kPlanThreads) {
     int4 at = make_int4(0, 0, 0, 0);
     long long u = U;
-    if (c < n) {
+    if (c < n && whole) {
+      at.y = c / ntiles;
+      at.z = c - at.y * ntiles;
+      u = at.y * units + s_prefix[at.z];
+      at.x = (int)((at.z + 1 < ntiles ? s_prefix[at.z + 1] : units) - s_prefix[at.z]);
+    } else if (c < n) {
       u = (long long)c * U / n;
       at.x = (int)((long long)(c + 1) * U / n - u);
       at.y = (int)(u / units);
