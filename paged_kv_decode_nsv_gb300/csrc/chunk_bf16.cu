@@ -791,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   const uint32_t tmem = *s_word;
   const bool odd = (smem0 & 1023u) != 0 || tmem != 0;
   griddep_wait();  // the tile list, and whatever was written before it
+  griddep_launch();
   ChunkWalk wk;
   wk.init(p, blockIdx.x);
   bool ok = !odd;

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
   const float* vp = static_cast<const float*>(p.v_pool);
   constexpr float kLog2e = 1.4426950408889634f;
   griddep_wait();
+  griddep_launch();
   ChunkWalk wk;
   wk.init(p, blockIdx.x);
   ChunkSegment s;

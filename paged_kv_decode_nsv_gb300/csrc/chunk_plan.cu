@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __shared__ long long s_warp[32];
   // a tile's key range, before its prefix takes its place
   int2* s_keys = reinterpret_cast<int2*>(s_prefix);
+  sm::griddep_wait();  // lengths and bounds may be the previous kernel's
   sm::griddep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tt = p.tile_tokens;
@@ -203,8 +204,18 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 }  // namespace
 
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // (programmatic: its launch overlaps the previous kernel's end, and it waits for
+  // that kernel before it reads anything)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p);
 }
 
 }  // namespace nsv

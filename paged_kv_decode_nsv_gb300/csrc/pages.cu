@@ -211,44 +211,56 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   const int rank = cluster_before(mine, at, s_warp, p.ws + kSlots0, &nfree);
   list_free(p.refs, lo, hi, at.lane, rank, __ldcg(p.ws + kTotalNeed), list);
   cluster_sync();
-  // a warp per fork: the child's table, references and length
-  for (int i = at.gw; i < p.count; i += kAllWarps) {
+  // A warp per 128 table entries of a fork: the child's table and references (four
+  // loads in flight before the first store); the first also the copied block and
+  // the length.
+  const int parts = (p.max_blocks + 127) / 128;
+  const long long work = (long long)p.count * parts;
+  for (long long k = at.gw; k < work; k += kAllWarps) {
+    const int i = (int)(k / parts), part = (int)(k - (long long)i * parts);
     const int2 it = __ldcg(items + i);
     const bool need = it.y >= 0;
     const int upto = need ? it.y : -it.y - 1;
-    bool ok = it.x >= 0;
-    if (ok && upto > nfree) {
-      ok = false;
-      if (at.lane == 0) flag(p, NSV_DEV_NO_BLOCKS);
+    const bool ok = it.x >= 0 && upto <= nfree;
+    if (part == 0 && at.lane == 0) {
+      if (it.x >= 0 && !ok) flag(p, NSV_DEV_NO_BLOCKS);
+      if (!ok) pairs[i] = make_int2(-1, -1);
     }
-    int2 pair = make_int2(-1, -1);
-    if (ok) {
-      const int par = __ldg(p.parents + i), c = __ldg(p.children + i);
-      const int32_t* from = p.block_tables + (size_t)par * p.max_blocks;
-      int32_t* to = p.block_tables + (size_t)c * p.max_blocks;
-      const int full = it.x / kBlock;
-      for (int b = at.lane; b < full; b += 32) {
-        const int id = from[b];
-        to[b] = id;
-        if (id >= 0 && id < p.num_blocks)
-          atomicAdd(p.refs + id, 1);
+    if (!ok) continue;
+    const int par = __ldg(p.parents + i), c = __ldg(p.children + i);
+    const int32_t* from = p.block_tables + (size_t)par * p.max_blocks;
+    int32_t* to = p.block_tables + (size_t)c * p.max_blocks;
+    const int full = it.x / kBlock;
+    int id[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = part * 128 + u * 32 + at.lane;
+      id[u] = e < full ? __ldcg(from + e) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = part * 128 + u * 32 + at.lane;
+      if (e >= full) continue;
+      to[e] = id[u];
+      if (id[u] >= 0 && id[u] < p.num_blocks)
+        atomicAdd(p.refs + id[u], 1);
+      else
+        flag(p, NSV_DEV_BAD_BLOCK);
+    }
+    if (part == 0 && at.lane == 0) {
+      int2 pair = make_int2(-1, -1);
+      if (need) {
+        const int fresh = __ldcg(list + upto - 1), src = __ldcg(from + full);
+        to[full] = fresh;
+        p.refs[fresh] = 1;
+        if (src >= 0 && src <= p.num_blocks)
+          pair = make_int2(src, fresh);
         else
           flag(p, NSV_DEV_BAD_BLOCK);
       }
-      if (at.lane == 0) {
-        if (need) {
-          const int id = __ldcg(list + upto - 1), src = from[full];
-          to[full] = id;
-          p.refs[id] = 1;
-          if (src >= 0 && src <= p.num_blocks)
-            pair = make_int2(src, id);
-          else
-            flag(p, NSV_DEV_BAD_BLOCK);
-        }
-        p.context_lens[c] = it.x;
-      }
+      pairs[i] = pair;
+      p.context_lens[c] = it.x;
     }
-    if (at.lane == 0) pairs[i] = pair;
   }
 }
 
@@ -340,7 +352,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
 }
 
 // ----------------------------------------------------------------------- free
-__global__ void __launch_bounds__(128) free_kernel(const PageParams p) {
+constexpr int kFreeThreads = 256;
+__global__ void __launch_bounds__(kFreeThreads) free_kernel(const PageParams p) {
   __shared__ int s_ctx;
   const int row = __ldg(p.parents + blockIdx.x);
   if (row == -1) return;  // a filler of a captured list
@@ -357,8 +370,9 @@ __global__ void __launch_bounds__(128) free_kernel(const PageParams p) {
     return;
   }
   int32_t* table = p.block_tables + (size_t)row * p.max_blocks;
+#pragma unroll 4
   for (int b = threadIdx.x; b < blocks_of(c); b += blockDim.x) {
-    const int id = table[b];
+    const int id = __ldcg(table + b);
     table[b] = -1;
     if (id < 0 || id >= p.num_blocks) {
       flag(p, NSV_DEV_BAD_BLOCK);
@@ -548,7 +562,7 @@ cudaError_t launch_rows_extend(const PageParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_rows_free(const PageParams& p, cudaStream_t stream) {
-  free_kernel<<<p.count, 128, 0, stream>>>(p);
+  free_kernel<<<p.count, kFreeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
