@@ -8,7 +8,11 @@
 // memory; the units of all tiles, KV head after KV head, are laid end to end
 // and CTA c of a persistent grid takes [c*U/grid, (c+1)*U/grid).  So every
 // CTA gets the same number of units whatever the mix of chunk and context
-// lengths, and one long row with few query tokens is split over many CTAs.
+// lengths, and one long row with few query tokens is split over many CTAs.  What
+// a tile costs besides its runs of keys (its query rows, its output) counts as
+// tile_cost units before the first run: without them CTAs that got many short
+// tiles ended last (a 2048-token prompt: 73 us; with 2 units a tile 56, with 4
+// 57).  fp32, whose units take longer, was no faster for it (170 us, with 2 172).
 #pragma once
 
 #include <cuda.h>
@@ -27,6 +31,8 @@ constexpr int kChunkHalfRows = 128;
 constexpr int kChunkKeys = 128;
 constexpr int kChunkRowsF32 = 64;
 constexpr int kChunkKeysF32 = 64;
+
+constexpr int kChunkTileCost = 2;  // bf16, see above
 
 // Query tokens one tile holds.
 __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
@@ -95,6 +101,7 @@ struct ChunkParams {
   int rows, heads, kv_heads, group, max_blocks;
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
   int grid;         // CTAs of the attention kernel
+  int tile_cost;    // units of a tile's own cost
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
@@ -131,7 +138,7 @@ struct ChunkSegment {
 // The CTAs whose pieces make up a tile: the first one, and how many.  All lanes
 // of a warp call together.
 __device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, int head, int tile, int lane) {
-  const long long u0 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile);
+  const long long u0 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile) + p.tile_cost;
   const long long u1 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile + 1);
   int before = 0, upto = 0;  // CTAs that start at or before the first, the last unit
 #pragma unroll 1
@@ -158,31 +165,34 @@ struct ChunkWalk {
   }
   template <int KEYS>
   __device__ __forceinline__ bool next(const ChunkParams& p, ChunkSegment& s) {
-    if (left <= 0) return false;
-    const int4 a = __ldcg(p.ws_tiles + 2 * (size_t)tile);
-    const int4 b = __ldcg(p.ws_tiles + 2 * (size_t)tile + 1);
-    s.t.row = a.x;
-    s.t.q0 = a.y;
-    s.t.n_tok = a.z;
-    s.t.pos0 = a.w;
-    s.t.kb = b.x;
-    s.t.ke = b.y;
-    s.t.ctx = b.z;
-    s.head = head;
-    s.tile = tile;
-    const int of_tile = chunk_units(s.t.kb, s.t.ke, KEYS) - skip;
-    const int take = min(left, of_tile);
-    s.j0 = skip;
-    s.j1 = skip + take;
-    s.first = skip == 0;
-    s.last = take == of_tile;
-    left -= take;
-    skip = 0;
-    if (s.last && ++tile == ntiles) {
-      tile = 0;
-      ++head;
+    while (left > 0) {
+      const int4 a = __ldcg(p.ws_tiles + 2 * (size_t)tile);
+      const int4 b = __ldcg(p.ws_tiles + 2 * (size_t)tile + 1);
+      const int of_tile = p.tile_cost + chunk_units(b.x, b.y, KEYS) - skip;
+      const int take = min(left, of_tile);
+      s.j0 = max(0, skip - p.tile_cost);
+      s.j1 = max(0, skip + take - p.tile_cost);
+      s.first = s.j0 == 0;
+      s.last = take == of_tile;
+      s.head = head;
+      s.tile = tile;
+      left -= take;
+      skip = 0;
+      if (s.last && ++tile == ntiles) {
+        tile = 0;
+        ++head;
+      }
+      if (s.j0 == s.j1) continue;  // the share ends within the tile's own cost
+      s.t.row = a.x;
+      s.t.q0 = a.y;
+      s.t.n_tok = a.z;
+      s.t.pos0 = a.w;
+      s.t.kb = b.x;
+      s.t.ke = b.y;
+      s.t.ctx = b.z;
+      return true;
     }
-    return true;
+    return false;
   }
 };
 

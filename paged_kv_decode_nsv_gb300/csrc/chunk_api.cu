@@ -130,6 +130,7 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
   p.cap = sc ? sc->softcap : 0.f;
   p.grid = chunk_grid(s, d.num_sms);
+  p.tile_cost = s->dtype == NSV_F32 ? 0 : kChunkTileCost;
   p.ws_first = reinterpret_cast<long long*>(p.ws_cta + p.grid);
   if (s->dtype == NSV_BF16 &&
       (!encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||

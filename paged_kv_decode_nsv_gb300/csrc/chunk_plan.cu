@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       }
       p.ws_tiles[2 * (size_t)i] = make_int4(row, c.start + tok0, nt, pos0);
       p.ws_tiles[2 * (size_t)i + 1] = make_int4(kb, ke, c.ctx, 0);
-      n = chunk_units(kb, ke, p.keys);
+      n = p.tile_cost + chunk_units(kb, ke, p.keys);
     }
     long long total;
     const long long upto = block_scan(n, s_warp, &total);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // CTA gets one whole: up to kWholeUnits units take less time one after the other
   // (0.5 us each) than the pieces of a cut tile take to be published and merged
   // (5 us).
-  const bool whole = !__syncthreads_or(longest > kWholeUnits) &&
+  const bool whole = !__syncthreads_or(longest > p.tile_cost + kWholeUnits) &&
                      (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
   const int n = whole ? ntiles * p.kv_heads : (int)min(U, (long long)p.grid);
