@@ -432,7 +432,10 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
  * context) outputs 0.  Tokens of no row (before chunk_starts[0], at and after
  * chunk_starts[rows], as in a batch padded to a captured size) are not
  * touched in `out`.  Pool contents at and past a row's context length are
- * never used and may hold anything, NaN included.
+ * never used and may hold anything, NaN included; so may keys at positions that a
+ * token does not see.  Values below the context length must be finite where any
+ * token of the row's chunk sees the positions around them: the second product
+ * multiplies what a token does not see by 0.
  *
  * `scores` changes the score before the softmax, in this order:
  *   softcap > 0         s = softcap * tanh(scale * q.k / softcap)
@@ -458,7 +461,7 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
  * positions, so the same call on the same inputs gives the same bits.
  */
 typedef struct nsv_scores {
-    float softcap;            /* 0: no cap; else finite and > 0 */
+    float softcap;            /* 0: no cap; else within [1e-6, 1e6] */
     const float *slopes;      /* [num_heads] device memory, or NULL */
     const int32_t *see_begin; /* [tokens] device memory, or NULL */
     const int32_t *see_end;   /* [tokens] device memory, or NULL */
@@ -627,7 +630,7 @@ NSV_API const char *nsv_strerror(int code);
 /* ABI version of this header (major * 100 + minor). */
 NSV_API int nsv_abi_version(void);
 
-#define NSV_ABI_VERSION 102
+#define NSV_ABI_VERSION 102 /* the layouts of nsv_shape and nsv_plan */
 
 #ifdef __cplusplus
 }

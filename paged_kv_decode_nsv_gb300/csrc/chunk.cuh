@@ -8,11 +8,14 @@
 // memory; the units of all tiles, KV head after KV head, are laid end to end
 // and CTA c of a persistent grid takes [c*U/grid, (c+1)*U/grid).  So every
 // CTA gets the same number of units whatever the mix of chunk and context
-// lengths, and one long row with few query tokens is split over many CTAs.  What
-// a tile costs besides its runs of keys (its query rows, its output) counts as
-// tile_cost units before the first run: without them CTAs that got many short
-// tiles ended last (a 2048-token prompt: 73 us; with 2 units a tile 56, with 4
-// 57).  fp32, whose units take longer, was no faster for it (170 us, with 2 172).
+// lengths, and one long row with few query tokens is split over many CTAs.
+//
+// What the shares count is time: a bf16 run takes 4 units where the tile fills
+// both halves and 3 where it fills one (measured 1.9 and 1.45 us), and what a
+// tile costs besides its runs (its query rows, its output) as much as two runs,
+// before the first.  Counting runs alone, CTAs that got many short tiles ended
+// last: a 2048-token prompt took 73 us, with the tiles' own cost 56 (4 runs in
+// place of 2: 57).  fp32, whose runs take longer, was no faster for it.
 #pragma once
 
 #include <cuda.h>
@@ -32,7 +35,8 @@ constexpr int kChunkKeys = 128;
 constexpr int kChunkRowsF32 = 64;
 constexpr int kChunkKeysF32 = 64;
 
-constexpr int kChunkTileCost = 2;  // bf16, see above
+// Costs (see above): of a bf16 tile in runs, of its runs in units.
+constexpr int kChunkTileCost = 2, kChunkPairUnits = 4, kChunkHalfUnits = 3;
 
 // Query tokens one tile holds.
 __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
@@ -44,7 +48,8 @@ __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
 //   head    int64 units of one KV head, int64 tiles
 //   prefix  int64 [max_tiles + 1]  units before each tile
 //   tiles   int4 [max_tiles][2]    {row, first query token (global), tokens,
-//           position of the first}, {first key, one past the last key, ctx, 0}
+//           position of the first}, {first key, one past the last key, ctx,
+//           units of a run}
 //   cta     int4 [grid]  where each CTA starts: {units, KV head, tile, units of
 //           the tile before}, and int64 [grid] its first unit
 //   cnt     int32 [max_tiles][kv_heads]  pieces of a cut tile that finished
@@ -101,7 +106,7 @@ struct ChunkParams {
   int rows, heads, kv_heads, group, max_blocks;
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
   int grid;         // CTAs of the attention kernel
-  int tile_cost;    // units of a tile's own cost
+  int tile_cost;    // a tile's own cost, in runs
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
@@ -115,9 +120,9 @@ cudaError_t prepare_chunk_bf16();
 cudaError_t prepare_chunk_f32();
 
 #ifdef __CUDACC__
-// Units of a tile: runs of `keys` positions; one for a tile that sees nothing
-// (it writes its zeros).
-__device__ __forceinline__ int chunk_units(int kb, int ke, int keys) {
+// Runs of `keys` positions of a tile; one for a tile that sees nothing (it
+// writes its zeros).
+__device__ __forceinline__ int chunk_runs(int kb, int ke, int keys) {
   return ke > kb ? (int)((unsigned)(ke - kb - 1) / (unsigned)keys) + 1 : 1;
 }
 
@@ -125,7 +130,14 @@ __device__ __forceinline__ int chunk_units(int kb, int ke, int keys) {
 struct ChunkTile {
   int row, q0, n_tok, pos0;  // q0: global index of its first query token
   int kb, ke, ctx;           // key positions [kb, ke); the row's context length
+  int cost;                  // units of one of its runs: 1, 3 or 4
 };
+
+// x / cost, rounded up, for x >= 0; 0 below.
+__device__ __forceinline__ int chunk_ceil(int x, int cost) {
+  const unsigned y = (unsigned)max(0, x + cost - 1);
+  return (int)(cost == 3 ? y / 3u : y >> (cost >> 1));
+}
 
 // A CTA's run of units of one tile and KV head.
 struct ChunkSegment {
@@ -135,17 +147,20 @@ struct ChunkSegment {
   bool first, last;  // whether it starts and ends the tile
 };
 
-// The CTAs whose pieces make up a tile: the first one, and how many.  All lanes
-// of a warp call together.
-__device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, int head, int tile, int lane) {
-  const long long u0 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile) + p.tile_cost;
-  const long long u1 = head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + tile + 1);
-  int before = 0, upto = 0;  // CTAs that start at or before the first, the last unit
+// The CTAs whose pieces make up a segment's tile: the first one, and how many.
+// A run belongs to the CTA whose share holds its first unit.  All lanes of a
+// warp call together.
+template <int KEYS>
+__device__ __forceinline__ int2 chunk_pieces(const ChunkParams& p, const ChunkSegment& s, int lane) {
+  const long long u0 =
+      s.head * __ldcg(p.ws_head) + __ldcg(p.ws_prefix + s.tile) + p.tile_cost * s.t.cost;
+  const long long u1 = u0 + (long long)(chunk_runs(s.t.kb, s.t.ke, KEYS) - 1) * s.t.cost;
+  int before = 0, upto = 0;  // CTAs that start at or before the first run, the last one
 #pragma unroll 1
   for (int c = 0; c < p.grid; c += 32) {
-    const long long f = c + lane < p.grid ? __ldcg(p.ws_first + c + lane) : u1;
+    const long long f = c + lane < p.grid ? __ldcg(p.ws_first + c + lane) : u1 + 1;
     before += __popc(__ballot_sync(sm::kFull, f <= u0));
-    upto += __popc(__ballot_sync(sm::kFull, f < u1));
+    upto += __popc(__ballot_sync(sm::kFull, f <= u1));
   }
   return make_int2(before - 1, upto - before + 1);
 }
@@ -168,21 +183,23 @@ struct ChunkWalk {
     while (left > 0) {
       const int4 a = __ldcg(p.ws_tiles + 2 * (size_t)tile);
       const int4 b = __ldcg(p.ws_tiles + 2 * (size_t)tile + 1);
-      const int of_tile = p.tile_cost + chunk_units(b.x, b.y, KEYS) - skip;
+      const int own = p.tile_cost * b.w;
+      const int runs = chunk_runs(b.x, b.y, KEYS);
+      const int of_tile = own + runs * b.w - skip;
       const int take = min(left, of_tile);
-      s.j0 = max(0, skip - p.tile_cost);
-      s.j1 = max(0, skip + take - p.tile_cost);
+      s.j0 = chunk_ceil(skip - own, b.w);
+      s.j1 = chunk_ceil(skip + take - own, b.w);
       s.first = s.j0 == 0;
-      s.last = take == of_tile;
+      s.last = s.j1 == runs;
       s.head = head;
       s.tile = tile;
       left -= take;
       skip = 0;
-      if (s.last && ++tile == ntiles) {
+      if (take == of_tile && ++tile == ntiles) {
         tile = 0;
         ++head;
       }
-      if (s.j0 == s.j1) continue;  // the share ends within the tile's own cost
+      if (s.j0 == s.j1) continue;  // no run starts in the share
       s.t.row = a.x;
       s.t.q0 = a.y;
       s.t.n_tok = a.z;
@@ -190,6 +207,7 @@ struct ChunkWalk {
       s.t.kb = b.x;
       s.t.ke = b.y;
       s.t.ctx = b.z;
+      s.t.cost = b.w;
       return true;
     }
     return false;

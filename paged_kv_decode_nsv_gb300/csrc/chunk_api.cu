@@ -3,7 +3,6 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -85,7 +84,7 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
       !aligned(block_tables, 4) || !aligned(chunk_starts, 4) || !aligned(context_lens, 4))
     return NSV_ERR_ALIGN;
   if (sc) {
-    if (!(sc->softcap >= 0.f) || isinf(sc->softcap)) return NSV_ERR_RANGE;
+    if (sc->softcap != 0.f && !(sc->softcap >= 1e-6f && sc->softcap <= 1e6f)) return NSV_ERR_RANGE;
     if (!aligned(sc->slopes, 4) || !aligned(sc->see_begin, 4) || !aligned(sc->see_end, 4))
       return NSV_ERR_ALIGN;
   }

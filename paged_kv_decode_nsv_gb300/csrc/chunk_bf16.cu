@@ -485,8 +485,13 @@ __device__ __forceinline__ bool publish(const ChunkParams& p, const Bars<D>& B, 
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
     if (s.first && s.last) continue;
-    const int2 pc = chunk_pieces(p, s.head, s.tile, lane);
-    if (!warp_wait(B.piece(), n++ & 1)) return false;
+    const int2 pc = chunk_pieces<kChunkKeys>(p, s, lane);
+    // (this wait lasts as long as the segment: a limit for each of its runs)
+    bool done = false;
+#pragma unroll 1
+    for (int j = s.j0; j <= s.j1 && !done; ++j) done = warp_wait(B.piece(), n & 1);
+    if (!done) return false;
+    ++n;
     if (lane == 0) {
       __threadfence();  // (cumulative: what the warps wrote before they arrived)
       if (atomicAdd(p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head, 1) == pc.y - 1) {

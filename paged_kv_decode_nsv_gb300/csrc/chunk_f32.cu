@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       // publish the piece; the CTA whose piece is the last merges them all
       __syncthreads();
       if (tid < 32) {
-        const int2 pc = chunk_pieces(p, s.head, s.tile, lane);
+        const int2 pc = chunk_pieces<kC>(p, s, lane);
         if (lane == 0) {
           __threadfence();
           int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;

@@ -15,7 +15,10 @@ namespace nsv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kWholeUnits = 8;
+// Where there is a CTA for every tile and head, and no tile has more runs than
+// this, each CTA gets one whole: its runs take less time one after the other (0.5
+// us each) than the pieces of a cut tile take to be published and merged (5 us).
+constexpr int kWholeRuns = 8;
 
 // Inclusive sum over the block's threads; *total is the block's.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   };
 
   long long units = 0;
-  int longest = 0;  // units of the longest tile
+  int longest = 0;  // runs of the longest tile
   for (int base = 0; base < ntiles; base += kPlanThreads) {
     if (p.see_begin || p.see_end) {
       // a warp per tile: the range that its tokens see
@@ -143,8 +146,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         ke = max(0, min(pos0 + nt, c.ctx));
       }
       p.ws_tiles[2 * (size_t)i] = make_int4(row, c.start + tok0, nt, pos0);
-      p.ws_tiles[2 * (size_t)i + 1] = make_int4(kb, ke, c.ctx, 0);
-      n = p.tile_cost + chunk_units(kb, ke, p.keys);
+      // (a tile with more than half of the tokens fills both halves)
+      const int cost = !p.tile_cost     ? 1
+                       : 2 * nt > tt ? kChunkPairUnits
+                                     : kChunkHalfUnits;
+      p.ws_tiles[2 * (size_t)i + 1] = make_int4(kb, ke, c.ctx, cost);
+      const int runs = chunk_runs(kb, ke, p.keys);
+      n = (long long)(p.tile_cost + runs) * cost;
+      longest = max(longest, runs);
     }
     long long total;
     const long long upto = block_scan(n, s_warp, &total);
@@ -153,7 +162,6 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       s_prefix[tid] = units + upto - n;  // used where one pass covers all tiles
     }
     units += total;
-    longest = max(longest, (int)n);
     __syncthreads();
   }
   if (tid == 0) {
@@ -162,40 +170,45 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     p.ws_head[1] = ntiles;
   }
   for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
-  // Where each CTA's share of the units starts: [c * U / n, (c + 1) * U / n) for
-  // the n CTAs that get at least one; the others get none.
-  // Where there is a CTA for every tile and head, and the tiles are short, each
-  // CTA gets one whole: up to kWholeUnits units take less time one after the other
-  // (0.5 us each) than the pieces of a cut tile take to be published and merged
-  // (5 us).
-  const bool whole = !__syncthreads_or(longest > p.tile_cost + kWholeUnits) &&
+  // Where each CTA's share of the units starts: c * U / n for the first n CTAs, of
+  // at least a run's units each, so that a run starts in every share that lies
+  // within a tile; the others get none.  (Moving a boundary that leaves a run or less
+  // on one side of a tile to the tile's edge saved pieces to merge, but the uneven
+  // shares cost more: a 2048-token prompt 58 us instead of 56.)
+  __syncthreads();
+  const bool whole = !__syncthreads_or(longest > kWholeRuns) &&
                      (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
-  const int n = whole ? ntiles * p.kv_heads : (int)min(U, (long long)p.grid);
-  for (int c = tid; c < p.grid; c += kPlanThreads) {
-    int4 at = make_int4(0, 0, 0, 0);
-    long long u = U;
-    if (c < n && whole) {
-      at.y = c / ntiles;
-      at.z = c - at.y * ntiles;
-      u = at.y * units + s_prefix[at.z];
-      at.x = (int)((at.z + 1 < ntiles ? s_prefix[at.z + 1] : units) - s_prefix[at.z]);
-    } else if (c < n) {
-      u = (long long)c * U / n;
-      at.x = (int)((long long)(c + 1) * U / n - u);
-      at.y = (int)(u / units);
-      const long long rem = u - at.y * units;
-      int lo = 0, hi = ntiles;  // the last tile whose first unit is at most rem
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((ntiles <= kPlanThreads ? s_prefix[mid] : __ldcg(p.ws_prefix + mid)) <= rem)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      at.z = lo;
-      at.w = (int)(rem - (ntiles <= kPlanThreads ? s_prefix[lo] : __ldcg(p.ws_prefix + lo)));
+  const int run = p.tile_cost ? kChunkPairUnits : 1;
+  const int n = whole ? ntiles * p.kv_heads : (int)max(1ll, min(U / run, (long long)p.grid));
+  auto prefix = [&](int i) {
+    return i == ntiles ? units : ntiles <= kPlanThreads ? s_prefix[i] : __ldcg(p.ws_prefix + i);
+  };
+  auto start = [&](int c, int& head, int& tile, int& skip) -> long long {
+    head = tile = skip = 0;
+    if (c >= n || U == 0) return U;
+    if (whole) {
+      head = c / ntiles;
+      tile = c - head * ntiles;
+      return head * units + prefix(tile);
     }
+    const long long u = (long long)c * U / n;
+    head = (int)(u / units);
+    const long long rem = u - head * units;
+    int lo = 0, hi = ntiles;  // the last tile whose first unit is at most rem
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix(mid) <= rem) lo = mid; else hi = mid;
+    }
+    tile = lo;
+    skip = (int)(rem - prefix(lo));
+    return u;
+  };
+  for (int c = tid; c < p.grid; c += kPlanThreads) {
+    int4 at;
+    int h, t, k;
+    const long long u = start(c, at.y, at.z, at.w);
+    at.x = (int)(start(c + 1, h, t, k) - u);
     p.ws_cta[c] = at;
     p.ws_first[c] = u;
   }

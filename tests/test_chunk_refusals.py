@@ -84,7 +84,7 @@ def test_null_and_misaligned_pointers(nsv, step):
 
 def test_bad_scores(nsv):
     s = _shape(nsv)
-    for cap in (-1.0, math.nan, math.inf):
+    for cap in (-1.0, math.nan, math.inf, 1e-7, 2e6):
         assert _call(nsv, s, scores=nsv.Scores(cap, None, None, None)) == -5
     for field in ("slopes", "see_begin", "see_end"):
         sc = nsv.Scores(0.0, None, None, None)
