@@ -189,10 +189,12 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
 // both streams fall into step, their softmax at the same time and their MMAs at
 // the same time: 2167 against 1753 us for 4096 tokens over 32768.)  The CTA holds
 // all of tensor memory, which starts at column 0, so that all operands but the
-// stage are compile-time constants.
+// stage are compile-time constants.  One thread, elected, runs all of this: the
+// votes that keep a whole warp together made a turn 1740 cycles long where its
+// MMAs take 1000.
 template <int D>
 __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
-                                          ChunkWalk wk, bool lead) {
+                                          ChunkWalk wk) {
   using L = Smem<D>;
   // K and V stages: tokens in groups of 8, a group's 64-dim halves one
   // 1024-byte swizzle atom after the other
@@ -203,37 +205,35 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
   const uint64_t dk = umma_desc128(smem0, 16, kGroup);
   const uint64_t dv = umma_desc128(smem0, 1024, kGroup);
   // descriptors are linear in the start address: a base plus an offset
-  auto stage_at = [](uint32_t i) {
-    return __reduce_or_sync(kFull, (i % L::kStages) * (L::kStage >> 4));  // warp-uniform
-  };
+  auto stage_at = [](uint32_t i) { return (i % L::kStages) * (L::kStage >> 4); };
   auto scores = [&](uint32_t x, uint32_t half, uint32_t i) {
     tc_fence_after();
     const uint64_t a = dq + half * (L::kHalf >> 4), b = dk + stage_at(i);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
       umma_ss(x * kChunkKeys, a + (((ks >> 2) * (kChunkHalfRows * 128) + (ks & 3) * 32) >> 4),
-              b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0, lead);
-    umma_commit(B.scores(x), lead);
+              b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0, true);
+    umma_commit(B.scores(x), true);
   };
   auto values = [&](uint32_t x, uint32_t i, bool fresh) {
     const uint64_t b = dv + stage_at(i);
 #pragma unroll
     for (int ks = 0; ks < kChunkKeys / 16; ++ks)
       umma_ts(kColO + x * D, x * kChunkKeys + ks * kBlock, b + ((ks * 2 * kGroup) >> 4), idesc_o,
-              !fresh || ks > 0, lead);
+              !fresh || ks > 0, true);
   };
   uint32_t base = 0, nseg = 0, np[2] = {0, 0};
   auto wait_full = [&](uint32_t i) {
-    return warp_wait(B.full(i % L::kStages), (i / L::kStages) & 1);
+    return mbar_wait(B.full(i % L::kStages), (i / L::kStages) & 1);
   };
-  auto free_stage = [&](uint32_t i) { umma_commit(B.empty(i % L::kStages), lead); };
+  auto free_stage = [&](uint32_t i) { umma_commit(B.empty(i % L::kStages), true); };
   ChunkSegment s, next;
 #pragma unroll 1
   for (bool more = wk.next<kChunkKeys>(p, s); more; s = next) {
     const int n = s.j1 - s.j0;
     const bool pair = copies_of(p, s) == 0;
     more = wk.next<kChunkKeys>(p, next);  // its loads overlap this segment's work
-    if (!warp_wait(B.qfull(), nseg & 1)) return false;
+    if (!mbar_wait(B.qfull(), nseg & 1)) return false;
     // Turn k: stream x = k & 1 multiplies the probabilities of its run and starts
     // its next scores.  A pair's streams take every run each (turn 2 j + x), the
     // others run k.
@@ -247,13 +247,13 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
       scores(x, pair ? x : 0, ik);
       if (!pair || x == 1) free_stage(ik);
     }
-    if (n <= ahead) umma_commit(B.qfree(), lead);
+    if (n <= ahead) umma_commit(B.qfree(), true);
     // before O is written again: the previous segment's has been read
-    if (nseg && !warp_wait(B.ofree(), (nseg - 1) & 1)) return false;
+    if (nseg && !mbar_wait(B.ofree(), (nseg - 1) & 1)) return false;
     auto turn = [&](uint32_t x, int j) {
       const uint32_t iv = base + 2 * j + 1, ik = base + 2 * (j + ahead);
       if (!wait_full(iv)) return false;
-      if (!warp_wait(B.probs(x), np[x]++ & 1)) return false;
+      if (!mbar_wait(B.probs(x), np[x]++ & 1)) return false;
       tc_fence_after();
       values(x, iv, j < ahead);
       const bool last_reader = !pair || x == 1;
@@ -263,7 +263,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
         if (last_reader) {
           free_stage(iv);
           free_stage(ik);
-          if (j + ahead + 1 == n) umma_commit(B.qfree(), lead);
+          if (j + ahead + 1 == n) umma_commit(B.qfree(), true);
         }
       } else {
         if (last_reader) free_stage(iv);
@@ -275,8 +275,8 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
       if (!turn(0, pair ? k / 2 : k)) return false;
       if (k + 1 < turns && !turn(1, pair ? k / 2 : k + 1)) return false;
     }
-    umma_commit(B.out(0), lead);
-    umma_commit(B.out(1), lead);
+    umma_commit(B.out(0), true);
+    umma_commit(B.out(1), true);
     base += 2 * n;
     ++nseg;
   }
@@ -822,10 +822,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
     if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
   } else if (warp == kSoftWarps + 1) {
-    const bool lead = elect_one() != 0;
-    ok = issue_mma<D>(p, B, smem0, wk, lead);
-    umma_commit(B.drained(), lead);  // arrives once every MMA issued is done
-    (void)mbar_wait(B.drained(), 0);
+    if (elect_one()) {
+      ok = issue_mma<D>(p, B, smem0, wk);
+      if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
+      umma_commit(B.drained(), true);  // arrives once every MMA issued is done
+      (void)mbar_wait(B.drained(), 0);
+    }
+    __syncwarp();
   } else {
     ok = publish<D>(p, B, s_todo, wk, lane);
   }
