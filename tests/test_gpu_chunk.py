@@ -379,3 +379,134 @@ def test_two_streams_with_a_workspace_each():
     for b, o in zip(bs, outs):
         ref, big = reference(b)
         assert ((o.double() - ref).abs().amax(-1) <= BF16_TOL * big).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,head_dim", [(8, 2, 128), (3, 3, 64)])
+def test_long_rows_are_cut_into_many_pieces(dtype, heads, kv_heads, head_dim):
+    check(batch([20011, 9000], [2, 70], heads, kv_heads, head_dim, dtype, seed=18), dtype)
+
+
+def _sample(b, rows):
+    """The batch cut down to some of its rows, and their tokens' indexes."""
+    import torch
+    ctx, new = b["lens"]
+    starts = np.concatenate([[0], np.cumsum(new)])
+    at = np.concatenate([np.arange(starts[r], starts[r + 1]) for r in rows])
+    idx = torch.from_numpy(at).cuda()
+    cut = dict(b, q=b["q"][idx], bt=b["bt"][torch.tensor(rows).cuda()],
+               lens=([ctx[r] for r in rows], [new[r] for r in rows]))
+    return cut, idx
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", [None, "window"])
+def test_thousands_of_rows(dtype, kind):
+    """More rows and tiles than one pass of the planning kernel covers, up to the
+    largest batch; a few rows are checked."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    rng = np.random.default_rng(19)
+    ctx = [int(x) for x in rng.integers(0, 60, 8192)]
+    new = [min(c, int(x)) for c, x in zip(ctx, rng.integers(0, 4, 8192))]
+    b = batch(ctx, new, 4, 2, 64, dtype, seed=19, pad=3)
+    kw = _bounds(b, kind, rng) if kind else {}
+    nsv.device_status(clear=True)
+    out = torch.full_like(b["q"], 7.5)
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out, **kw)
+    assert nsv.device_status(clear=True)[0] == 0
+    assert (out[-3:] == 7.5).all() and torch.isfinite(out.float()).all()
+    cut, idx = _sample(b, [0, 1, 1023, 1024, 1025, 4000, 8190, 8191] + list(range(5000, 5040)))
+    ref, big = reference(cut, **{k: v[idx] for k, v in kw.items()})
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert ((out[idx].double() - ref).abs().amax(-1) <= tol * big).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pool_offsets_beyond_32_bits(dtype):
+    """Blocks whose element offsets (and byte offsets) pass 2^31 and 2^32."""
+    import torch
+    b = batch([300, 40], [130, 1], 16, 8, 128, dtype, seed=20)
+    blocks = 140000 if dtype == "bf16" else 280000 // 2 + 1000
+    base = blocks - b["k"].shape[0]         # the batch's blocks at the pool's end
+    for name in ("k", "v"):
+        pool = torch.empty((blocks + 1,) + tuple(b[name].shape[1:]), dtype=b[name].dtype,
+                           device="cuda")
+        assert pool.numel() > 2 ** 31
+        pool[:64] = 3.0                     # what a wrapped offset would read
+        pool[base:base + b[name].shape[0]] = b[name]
+        b[name] = pool
+    b["bt"] = torch.where(b["bt"] >= 0, b["bt"] + base, -1).int()
+    check(b, dtype)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured with one workspace and replayed in turn on one stream."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    bs = [batch([2100, 64], [64, 3], 8, 2, 128, "bf16", seed=s) for s in (21, 22)]
+    outs = [torch.zeros_like(b["q"]) for b in bs]
+    shape = nsv.make_shape(2, 8, 2, 128, bs[0]["bt"].shape[1], bs[0]["k"].shape[0] - 1, nsv.BF16)
+    ws = torch.empty(nsv.chunk_workspace_bytes(shape, 67), dtype=torch.uint8, device="cuda")
+
+    def run(b, o):
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o,
+                        workspace=ws)
+
+    run(bs[0], outs[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for b, o in zip(bs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(b, o)
+    for o in outs:
+        o.zero_()
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for b, o in zip(bs, outs):
+        ref, big = reference(b)
+        assert ((o.double() - ref).abs().amax(-1) <= BF16_TOL * big).all()
+
+
+def test_calls_back_to_back_with_one_workspace():
+    """Each call's planning overlaps the call before it; the workspace does not."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    cases = [batch(c, n, 8, 2, 128, "bf16", seed=30 + i) for i, (c, n) in enumerate(
+        [([3000, 64], [40, 3]), ([17], [17]), ([900, 800, 700], [1, 1, 1]), ([2500], [260])])]
+    shape = nsv.make_shape(3, 8, 2, 128, 400, 1000, nsv.BF16)
+    ws = torch.empty(nsv.chunk_workspace_bytes(shape, 300), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(b["q"]) for b in cases]
+    for _ in range(10):
+        for b, o in zip(cases, outs):
+            nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o,
+                            workspace=ws)
+    torch.cuda.synchronize()
+    for b, o in zip(cases, outs):
+        ref, big = reference(b)
+        assert ((o.double() - ref).abs().amax(-1) <= BF16_TOL * big).all()
+
+
+def test_binding_refuses_what_does_not_fit():
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([40], [8], 4, 2, 64, "bf16", seed=23)
+    args = dict(q=b["q"], k_pool=b["k"], v_pool=b["v"], block_tables=b["bt"],
+                chunk_starts=b["starts"], context_lens=b["ctx"], scale=0.1,
+                out=torch.empty_like(b["q"]))
+    for name, bad in (("q", b["q"].float()), ("q", b["q"].transpose(0, 1)), ("v_pool", b["v"][1:]),
+                      ("block_tables", b["bt"].long()), ("chunk_starts", b["starts"][:1]),
+                      ("context_lens", b["ctx"].cpu()), ("out", args["out"][:4]),
+                      ("out", args["out"].expand(8, 4, 64)[:, :, ::2])):
+        with pytest.raises(ValueError):
+            nsv.paged_chunk(**dict(args, **{name: bad}))
+    for name, bad in (("slopes", torch.zeros(3, device="cuda")), ("see_end", b["ctx"])):
+        with pytest.raises(ValueError):
+            nsv.paged_chunk(**args, **{name: bad})
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(nsv.NsvError) as e:
+        nsv.paged_chunk(**args, workspace=small)
+    assert e.value.code == -8

@@ -439,3 +439,26 @@ def test_a_cache_from_prompts_to_compaction(dtype):
     nsv.rows_free(ids(0, 1, 2, 3, 4, 5), bt, ctx, refs)
     assert (refs == 0).all() and (ctx == 0).all()
     assert status() == 0
+
+
+def test_block_offsets_beyond_32_bits():
+    """Copies and moves of blocks whose offsets pass 2^31 elements."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    blocks, shape = 140000, (8, 16, 128)
+    pools = [torch.empty((blocks + 1,) + shape, dtype=torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    assert pools[0].numel() > 2 ** 31
+    for i, p in enumerate(pools):
+        p[0], p[-2], p[-3] = 1.0 + i, 3.0 + i, 5.0 + i
+    nsv.blocks_copy(ids(blocks - 1, 0), ids(7, blocks - 9), *pools)
+    for i, p in enumerate(pools):
+        assert (p[7] == 3.0 + i).all() and (p[blocks - 9] == 1.0 + i).all()
+    bt, ctx = ids(blocks - 2, blocks - 1).view(1, 2), ids(20)
+    refs = torch.zeros(blocks, dtype=torch.int32, device="cuda")
+    refs[bt[0].long()] = 1
+    nsv.blocks_compact(bt, ctx, refs, *pools)
+    assert bt.tolist() == [[0, 1]] and int(refs.sum()) == 2 and refs[:2].tolist() == [1, 1]
+    for i, p in enumerate(pools):
+        assert (p[0] == 5.0 + i).all() and (p[1] == 3.0 + i).all()
+    assert status() == 0
