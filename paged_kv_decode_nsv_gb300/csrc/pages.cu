@@ -153,7 +153,7 @@ __device__ __forceinline__ bool good_ctx(const PageParams& p, int c) {
 }
 
 // Workspace words: slots of the cluster sums, totals, then per-item arrays.
-enum : int { kSlots0 = 0, kSlots1 = 8, kTotalNeed = 16, kMoves = 17, kLive = 18 };
+enum : int { kSlots0 = 0, kSlots1 = 8, kTotalNeed = 16, kMoves = 17, kLive = 18, kParts = 19 };
 
 // ----------------------------------------------------------------------- fork
 // items: {child's length or -1 (refused), see below}
@@ -265,14 +265,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
 }
 
 // --------------------------------------------------------------------- extend
-// items: {blocks needed up to and with this row or -1 (refused), tokens}
+// items: {blocks needed up to and with this row or -1 (refused), tokens}; grown:
+// {parts before this row, its length before}
+//
+// PARTS: a warp takes 128 tokens of a row, else a whole row.  A warp alone took
+// 199 us for a row of 32768 new tokens, in parts they take 13; finding the parts
+// costs 2 us (128 rows of one new token each: 10.9 and 13.0 us).  So rows stay
+// whole where no row can have many more new tokens than one (kManyTokens).
+constexpr int kPartTokens = 128, kManyTokens = 512;
+template <bool PARTS>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
     extend_kernel(const PageParams p) {
   __shared__ int s_warp[kScanWarps];
   __shared__ long long s_scan[kScanWarps];
+  __shared__ int s_parts[PARTS ? kMaxRows : 1];
   const Place at;
   int2* items = reinterpret_cast<int2*>(p.ws + kPageWords);
-  int32_t* list = reinterpret_cast<int32_t*>(items + 2 * (size_t)p.rows);
+  int2* grown = items + p.rows;
+  int32_t* list = reinterpret_cast<int32_t*>(grown + p.rows);
   // tokens of no row, and of rows that cannot grow, write the sink
   for (long long i = (long long)at.cta * kScanThreads + at.tid; i < p.tokens;
        i += kCluster * kScanThreads)
@@ -281,15 +291,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   warp_run(p.num_blocks, at.gw, &lo, &hi);
   const int mine = count_run(p.refs, lo, hi, at.lane, true);
   if (at.cta == 0) {
-    long long taken = 0;
+    long long taken = 0, parts = 0;
     for (int base = 0; base < p.rows; base += kScanThreads) {
       const int r = base + at.tid;
-      int n = 0, need = 0;
+      int n = 0, need = 0, old = 0;
       bool ok = false;
       if (r < p.rows) {
         const int a = __ldg(p.chunk_starts + r), b = __ldg(p.chunk_starts + r + 1);
         const int c = __ldcg(p.context_lens + r);
         n = b - a;
+        old = c;
         if (a < 0 || b < a || b > p.tokens) {
           flag(p, NSV_DEV_BAD_CHUNK);
           n = 0;
@@ -314,40 +325,62 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
       const long long upto = taken + cta_scan(need, at, s_scan, &total);
       if (r < p.rows) __stcg(items + r, make_int2(ok ? clip(upto) : -1, n));
       taken += total;
+      if (PARTS) {
+        const int own = ok ? (n - 1) / kPartTokens + 1 : 0;
+        const long long before = parts + cta_scan(own, at, s_scan, &total) - own;
+        if (r < p.rows) __stcg(grown + r, make_int2(clip(before), old));
+        parts += total;
+      }
     }
-    if (at.tid == 0) __stcg(p.ws + kTotalNeed, clip(taken));
+    if (at.tid == 0) {
+      __stcg(p.ws + kTotalNeed, clip(taken));
+      __stcg(p.ws + kParts, clip(parts));
+    }
     __syncthreads();
   }
   int nfree;
   const int rank = cluster_before(mine, at, s_warp, p.ws + kSlots0, &nfree);
   list_free(p.refs, lo, hi, at.lane, rank, __ldcg(p.ws + kTotalNeed), list);
+  if (PARTS)
+    for (int r = at.tid; r < p.rows; r += kScanThreads) s_parts[r] = __ldcg(grown + r).x;
   cluster_sync();
-  // a warp per row: its new blocks, its tokens' slots, its length
-  for (int r = at.gw; r < p.rows; r += kAllWarps) {
+  // new blocks and the tokens' slots; the row's first warp also its length
+  const int work = PARTS ? __ldcg(p.ws + kParts) : p.rows;
+  for (int k = at.gw; k < work; k += kAllWarps) {
+    int r = k, i0 = 0;
+    if (PARTS) {  // the last row with at most k parts before it
+      int end = p.rows;
+      r = 0;
+      while (end - r > 1) {
+        const int mid = (r + end) >> 1;
+        if (s_parts[mid] <= k) r = mid; else end = mid;
+      }
+      i0 = (k - s_parts[r]) * kPartTokens;
+    }
     const int2 it = __ldcg(items + r);
     if (it.x < 0) continue;
     if (it.x > nfree) {
-      if (at.lane == 0) flag(p, NSV_DEV_NO_BLOCKS);
+      if (i0 == 0 && at.lane == 0) flag(p, NSV_DEV_NO_BLOCKS);
       continue;
     }
-    const int old = __ldcg(p.context_lens + r), n = it.y;
+    const int old = PARTS ? __ldcg(grown + r).y : __ldcg(p.context_lens + r), n = it.y;
     const int had = blocks_of(old), will = blocks_of(old + n);
     int32_t* table = p.block_tables + (size_t)r * p.max_blocks;
     const int32_t* fresh = list + (it.x - (will - had)) - had;  // indexed by table column
-    for (int b = had + at.lane; b < will; b += 32) {
-      const int id = __ldcg(fresh + b);
-      table[b] = id;
-      p.refs[id] = 1;
-    }
     const int start = __ldg(p.chunk_starts + r);
-    const int part = old % kBlock ? table[old / kBlock] : 0;
-    for (int i = at.lane; i < n; i += 32) {
-      const int pos = old + i, b = pos / kBlock;
-      const int id = b < had ? part : __ldcg(fresh + b);
-      p.write_slots[start + i] = (long long)id * kBlock + pos % kBlock;
+    const int i1 = PARTS ? min(n, i0 + kPartTokens) : n;
+#pragma unroll 4
+    for (int i = i0 + at.lane; i < i1; i += 32) {
+      const int pos = old + i, b = pos / kBlock, off = pos % kBlock;
+      const int id = __ldcg(b < had ? table + b : fresh + b);
+      if (b >= had && off == 0) {
+        table[b] = id;
+        p.refs[id] = 1;
+      }
+      p.write_slots[start + i] = (long long)id * kBlock + off;
     }
     __syncwarp();
-    if (at.lane == 0) p.context_lens[r] = old + n;
+    if (i0 == 0 && at.lane == 0) p.context_lens[r] = old + n;
   }
 }
 
@@ -557,7 +590,10 @@ cudaError_t launch_rows_fork(const PageParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_rows_extend(const PageParams& p, cudaStream_t stream) {
-  extend_kernel<<<kCluster, kScanThreads, 0, stream>>>(p);
+  if (p.tokens > (long long)p.rows + kManyTokens)
+    extend_kernel<true><<<kCluster, kScanThreads, 0, stream>>>(p);
+  else
+    extend_kernel<false><<<kCluster, kScanThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -12,9 +12,9 @@ namespace nsv {
 constexpr int kPageWords = 64;
 
 // Workspace bytes that serve every page operator on this shape.  fork: two
-// int2 per row and the free blocks (at most one per row); extend: one int2 per
-// row (its room is two) and the free blocks; compact: the map of the blocks,
-// the holes and the moving blocks (at most half of the blocks each).
+// int2 per row and the free blocks (at most one per row); extend: two int2 per
+// row and the free blocks; compact: the map of the blocks, the holes and the
+// moving blocks (at most half of the blocks each).
 inline uint64_t page_ws_bytes(int rows, long long num_blocks) {
   const uint64_t lists = (uint64_t)rows * 16 + (uint64_t)(num_blocks > rows ? num_blocks : rows) * 4;
   const uint64_t compact = (uint64_t)num_blocks * 4 + 2 * ((uint64_t)num_blocks / 2 + 1) * 4;

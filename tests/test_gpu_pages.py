@@ -462,3 +462,20 @@ def test_block_offsets_beyond_32_bits():
     for i, p in enumerate(pools):
         assert (p[0] == 5.0 + i).all() and (p[1] == 3.0 + i).all()
     assert status() == 0
+
+
+@pytest.mark.parametrize("grow", [[20000], [0, 700, 0, 0, 1300, 128, 129, 0, 1, 4097, 0, 257],
+                                  [1] * 11 + [600], [1] * 11 + [0]])
+def test_extend_by_long_prompts(grow):
+    """Rows whose new tokens are dealt out in parts, beside rows of a few."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    c = Cache(CTX[:len(grow)], 2000, extra=1300, seed=10)
+    got = c.gpu()
+    starts = np.concatenate([[0], np.cumsum(grow)])
+    want = c.extend(starts, int(starts[-1]) + 2)
+    slots = torch.full((len(want),), -9, dtype=torch.int64, device="cuda")
+    nsv.rows_extend(ids(*starts), *got[:3], slots)
+    c.same(got)
+    assert np.array_equal(slots.cpu().numpy(), want)
+    assert status() == 0
