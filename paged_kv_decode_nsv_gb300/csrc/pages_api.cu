@@ -9,10 +9,15 @@
 namespace nsv {
 namespace {
 
+constexpr int64_t kMaxBlockVecs = 1 << 24;  // 256 MiB, 32768 KV heads of 128 bf16 dims
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The parameters that follow from the shape and the device.
 int page_params(const nsv_shape* s, PageParams* p) {
+  const int64_t vecs =
+      (int64_t)s->num_kv_heads * kBlock * s->head_dim * (s->dtype == NSV_F32 ? 4 : 2) / 16;
+  if (vecs > kMaxBlockVecs) return NSV_ERR_SHAPE;
   DeviceInfo d;
   const int rc = device_info(&d);
   if (rc) return rc;
@@ -21,7 +26,7 @@ int page_params(const nsv_shape* s, PageParams* p) {
   p->num_blocks = s->num_blocks;
   p->rows = s->rows;
   p->max_blocks = s->max_blocks;
-  p->block_vecs = s->num_kv_heads * kBlock * s->head_dim * (s->dtype == NSV_F32 ? 4 : 2) / 16;
+  p->block_vecs = (int)vecs;
   p->units_per_block = page_units(p->block_vecs);
   return NSV_OK;
 }

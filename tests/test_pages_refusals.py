@@ -86,3 +86,9 @@ def test_workspace(nsv, op):
     # fork: two int2 per row and the free blocks; compact: map, holes, movers
     assert need == 256 + max(4 * 16 + 200 * 4, 200 * 4 + 2 * 101 * 4)
     assert nsv.pages_workspace_bytes(8192, 10) == 256 + 8192 * 20
+
+
+def test_blocks_too_large_to_count(nsv):
+    s = _shape(nsv, num_heads=1 << 20, num_kv_heads=1 << 20)
+    for op in ("copy", "fork", "compact"):
+        assert _calls(nsv, s)[op]() == -3
