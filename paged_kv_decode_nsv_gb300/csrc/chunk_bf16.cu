@@ -481,16 +481,20 @@ template <int D>
 __device__ __forceinline__ bool publish(const ChunkParams& p, const Bars<D>& B, int4* s_todo,
                                         ChunkWalk wk, int lane) {
   uint32_t n = 0;
+  long long runs = 0;  // since the wait before
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
+    runs += s.j1 - s.j0;
     if (s.first && s.last) continue;
     const int2 pc = chunk_pieces<kChunkKeys>(p, s, lane);
-    // (this wait lasts as long as the segment: a limit for each of its runs)
+    // (this wait lasts as long as all segments since the one before: a limit for
+    // each of their runs)
     bool done = false;
 #pragma unroll 1
-    for (int j = s.j0; j <= s.j1 && !done; ++j) done = warp_wait(B.piece(), n & 1);
+    for (; runs >= 0 && !done; --runs) done = warp_wait(B.piece(), n & 1);
     if (!done) return false;
+    runs = 0;
     ++n;
     if (lane == 0) {
       __threadfence();  // (cumulative: what the warps wrote before they arrived)
