@@ -116,7 +116,9 @@ enum {
                                kernel returned early; results are invalid */
     NSV_DEV_BAD_CHUNK = 16u,/* chunk starts that are not an ascending pair within
                                [0, tokens]; the row was read as having no new
-                               tokens */
+                               tokens.  Also a chunk attention of more than
+                               2^31 runs of positions per SM (a quarter of an
+                               hour's work), which is not run */
     NSV_DEV_BAD_ROW = 32u,  /* a row id outside [0, rows), a fork into a row that
                                is not empty or was named before, or a row to
                                extend whose last, partly filled block is not its
@@ -432,10 +434,12 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
  * context) outputs 0.  Tokens of no row (before chunk_starts[0], at and after
  * chunk_starts[rows], as in a batch padded to a captured size) are not
  * touched in `out`.  Pool contents at and past a row's context length are
- * never used and may hold anything, NaN included; so may keys at positions that a
- * token does not see.  Values below the context length must be finite where any
- * token of the row's chunk sees the positions around them: the second product
- * multiplies what a token does not see by 0.
+ * never used and may hold anything, NaN included.  So may a key at a position
+ * that a token does not see, as far as this token is concerned.  Values below the
+ * context length must be finite, seen or not: a token weighs what it does not see
+ * with 0, and 0 times NaN is NaN.  Blocks that no token of a chunk sees, such as
+ * those that a sliding window has left, need not be there: their table entries
+ * are not used.
  *
  * `scores` changes the score before the softmax, in this order:
  *   softcap > 0         s = softcap * tanh(scale * q.k / softcap)
@@ -450,8 +454,8 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
  *
  * Uses shape.rows, num_heads, num_kv_heads (at most 64 query heads per KV
  * head), head_dim, block_size, max_blocks, num_blocks and dtype; query_len
- * must be 0 or 1.  0 <= tokens < 2^30.  For bf16
- * (num_blocks+1)*num_kv_heads*2 < 2^31.  The lengths live in device memory and
+ * must be 0 or 1.  0 <= tokens < 2^30; without rows or tokens a call does
+ * nothing.  For bf16 (num_blocks+1)*num_kv_heads*2 < 2^31.  The lengths live in device memory and
  * are only read by kernels, so a captured call replays with new ones.
  *
  * workspace: device memory of at least the bytes nsv_chunk_workspace gives,
@@ -506,7 +510,8 @@ NSV_API int nsv_chunk_step(const nsv_shape *shape, const nsv_scores *scores, int
  * are ever shared, so that a row appends to a block of its own.
  *
  * They use shape.rows, max_blocks, num_blocks, block_size, and, where blocks
- * are copied, num_kv_heads, head_dim and dtype (the rest must be valid).
+ * are copied, num_kv_heads (a block of one pool is at most 256 MiB), head_dim and
+ * dtype (the rest must be valid).  Without rows or items a call does nothing.
  * Data pointers must be 16-byte aligned, index arrays to their element.
  * workspace: at least the bytes nsv_pages_workspace gives, 256-byte aligned,
  * owned by the caller, uninitialised; operators that overlap on the GPU need
@@ -548,7 +553,8 @@ NSV_API int nsv_rows_fork(const nsv_shape *shape, int32_t count, const int32_t *
  * what nsv_chunk_step takes (tokens of no row get the sink slot).  A row is
  * refused when the blocks that it and all rows before it need exceed the free
  * ones (NSV_DEV_NO_BLOCKS), or when it would outgrow its table
- * (NSV_DEV_BAD_CTX); it stays as it was and its tokens get the sink slot.
+ * (NSV_DEV_BAD_CTX), or when its last, partly filled block is not its own alone
+ * (NSV_DEV_BAD_ROW); it stays as it was and its tokens get the sink slot.
  */
 NSV_API int nsv_rows_extend(const nsv_shape *shape, int64_t tokens,
                             const int32_t *chunk_starts, int32_t *block_tables,

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
     // which of a run's blocks hold something
     auto run_blocks = [&](int j) {
       if (tid < 32) {
-        const int t = s.t.kb + j * kC + tid * kBlock;
+        const long long t = (long long)s.t.kb + j * kC + tid * kBlock;
         const int b = tid < kC / kBlock && t < s.t.ke ? __ldg(table + t / kBlock) : -1;
         const unsigned ok = __ballot_sync(kFull, b >= 0 && b < p.pool_blocks);
         if (tid == 0) s_ok[j & 1] = (int)ok;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
             if (p.cap > 0.f) x = p.cap * tanhf(x / p.cap);
             x = fmaf(-slope[i], fabsf((float)(pos[i] - t0 - t)), x) * kLog2e;
             const bool seen =
-                t0 + t >= see[i].x && t0 + t < see[i].y && ((blocks >> (t / kBlock)) & 1);
+                t >= see[i].x - t0 && t < see[i].y - t0 && ((blocks >> (t / kBlock)) & 1);
             sc[n][2 * i + e] = seen ? x : -INFINITY;
             mx = fmaxf(mx, sc[n][2 * i + e]);
           }

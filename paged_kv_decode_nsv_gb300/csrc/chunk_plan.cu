@@ -164,6 +164,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     units += total;
     __syncthreads();
   }
+  // (a CTA's share is counted in 32 bits: more would take it a quarter of an hour)
+  if (units > 0x7fffffffll / p.kv_heads * p.grid) {
+    if (tid == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+    units = 0;
+  }
   if (tid == 0) {
     p.ws_prefix[ntiles] = units;
     p.ws_head[0] = units;

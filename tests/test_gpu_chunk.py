@@ -510,3 +510,64 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(nsv.NsvError) as e:
         nsv.paged_chunk(**args, workspace=small)
     assert e.value.code == -8
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_keys_that_a_token_does_not_see_hold_anything(dtype, value):
+    """A key at position 150 of a row, inside the same run of positions as those
+    that earlier tokens and other documents see."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([200, 30], [100, 30], 8, 2, 128, dtype, seed=24)
+    blk = int(b["bt"][0, 150 // 16])
+    begin = torch.zeros(130, dtype=torch.int32, device="cuda")
+    begin[60:100] = 151          # the row's last 40 tokens: another document
+    kw = dict(see_begin=begin)
+    b["k"][blk, :, 150 % 16] = 0.5
+    ref, big = reference(b, **kw)
+    b["k"][blk, :, 150 % 16] = value
+    out = torch.empty_like(b["q"])
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out, **kw)
+    rest = [i for i in range(130) if not 50 <= i < 60]      # those ten see it
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert ((out[rest].double() - ref[rest]).abs().amax(-1) <= tol * big[rest]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_blocks_that_a_window_has_left_need_not_be_there(dtype):
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([1000, 500], [40, 1], 8, 2, 64, dtype, seed=25)
+    begin = torch.tensor([960 + i + 1 - 130 for i in range(40)] + [400], dtype=torch.int32,
+                         device="cuda")
+    end = torch.full((41,), 490, dtype=torch.int32, device="cuda")
+    end[:40] = 990
+    kw = dict(see_begin=begin, see_end=end)
+    ref, big = reference(b, **kw)
+    b["bt"][0, :831 // 16] = -1
+    b["bt"][1, :25] = 1 << 29
+    b["bt"][1, 31:] = 1 << 29
+    nsv.device_status(clear=True)
+    out = torch.empty_like(b["q"])
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out, **kw)
+    assert nsv.device_status(clear=True)[0] == 0
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert ((out.double() - ref).abs().amax(-1) <= tol * big).all()
+
+
+def test_more_work_than_a_share_counts_is_not_run():
+    """65536 tokens that each see 2^31 - 16 positions, a run of 64 at a time."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    tokens, width = 1 << 16, (1 << 27) - 1
+    q = torch.zeros((tokens, 64, 64), device="cuda")
+    out = torch.full_like(q, 7.5)
+    pools = [torch.zeros((2, 1, 16, 64), device="cuda") for _ in range(2)]
+    bt = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([width * 16], dtype=torch.int32, device="cuda")
+    nsv.device_status(clear=True)
+    nsv.paged_chunk(q, *pools, bt, starts, ctx, 0.1, out)
+    assert nsv.device_status(clear=True)[0] == nsv.DEV_BAD_CHUNK
+    assert (out == 7.5).all()
