@@ -58,11 +58,15 @@ __device__ __forceinline__ void copies_wait() {
 // Float index of 16-byte chunk v of row r, W floats to a row; of the values'.
 template <int W>
 __device__ __forceinline__ int at_chunk(int r, int v) {
-  return r * W + ((v ^ (r & 7)) << 2);
+  return r * W + ((v ^ ((r & 1) << 2 | (r & 2))) << 2);
 }
 template <int W>
 __device__ __forceinline__ int at_value(int r, int v) {
-  return r * W + ((v ^ ((r & 3) << 1)) << 2);
+  const int x = r >> 2 & 3;
+  return r * W + ((v ^ (W == 128 ? (x & 1) | (x & 2) << 1 : x << 1)) << 2);
+}
+__device__ __forceinline__ float4 load4(const float* s) {
+  return *reinterpret_cast<const float4*>(s);
 }
 
 // x = hi + lo.
@@ -75,18 +79,24 @@ struct Split {
 };
 __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d += A B, the small products first.
-__device__ __forceinline__ void mma_f32(float (&d)[4], const Split (&a)[4], const Split& b0,
-                                        const Split& b1) {
-  mma_tf32(d, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
-  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
-  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+// d[n] += A B for four column tiles, the small products first; a product waits for
+// the one before it of its tile, so the tiles take turns.
+__device__ __forceinline__ void mma_f32(float (*d)[4], const Split (&a)[4], const Split (&b0)[4],
+                                        const Split (&b1)[4]) {
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    mma_tf32(d[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0[n].hi, b1[n].hi);
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    mma_tf32(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0[n].lo, b1[n].lo);
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    mma_tf32(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0[n].hi, b1[n].hi);
 }
 
 template <int D>
@@ -181,17 +191,25 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       float sc[4][4];  // keys wn * 32 + n * 8 + 2 t4 + {0, 1}, rows r0 and r0 + 8
 #pragma unroll
       for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-#pragma unroll 4
-      for (int ks = 0; ks < D / 8; ++ks) {
-        const Split a[4] = {Split(sq[at_chunk<D>(r0, 2 * ks) + t4]),
-                            Split(sq[at_chunk<D>(r0 + 8, 2 * ks) + t4]),
-                            Split(sq[at_chunk<D>(r0, 2 * ks + 1) + t4]),
-                            Split(sq[at_chunk<D>(r0 + 8, 2 * ks + 1) + t4])};
+#pragma unroll 2
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const float4 x0 = load4(sq + at_chunk<D>(r0, 4 * ks + t4));
+        const float4 x1 = load4(sq + at_chunk<D>(r0 + 8, 4 * ks + t4));
+        float4 y[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int key = wn * 32 + n * 8 + g;
-          mma_f32(sc[n], a, Split(sk[at_chunk<D>(key, 2 * ks) + t4]),
-                  Split(sk[at_chunk<D>(key, 2 * ks + 1) + t4]));
+        for (int n = 0; n < 4; ++n)
+          y[n] = load4(sk + at_chunk<D>(wn * 32 + n * 8 + g, 4 * ks + t4));
+        {
+          const Split a[4] = {Split(x0.x), Split(x1.x), Split(x0.y), Split(x1.y)};
+          const Split b0[4] = {Split(y[0].x), Split(y[1].x), Split(y[2].x), Split(y[3].x)};
+          const Split b1[4] = {Split(y[0].y), Split(y[1].y), Split(y[2].y), Split(y[3].y)};
+          mma_f32(sc, a, b0, b1);
+        }
+        {
+          const Split a[4] = {Split(x0.z), Split(x1.z), Split(x0.w), Split(x1.w)};
+          const Split b0[4] = {Split(y[0].z), Split(y[1].z), Split(y[2].z), Split(y[3].z)};
+          const Split b1[4] = {Split(y[0].w), Split(y[1].w), Split(y[2].w), Split(y[3].w)};
+          mma_f32(sc, a, b0, b1);
         }
       }
       const int blocks = s_ok[j & 1];
@@ -247,17 +265,24 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       }
       copies_wait<1>();  // the values (the next run's keys may still be on their way)
       __syncthreads();
-#pragma unroll 2
-      for (int ks = 0; ks < kC / 8; ++ks) {
-        const Split a[4] = {Split(sp[at_chunk<kC>(r0, 2 * ks) + t4]),
-                            Split(sp[at_chunk<kC>(r0 + 8, 2 * ks) + t4]),
-                            Split(sp[at_chunk<kC>(r0, 2 * ks + 1) + t4]),
-                            Split(sp[at_chunk<kC>(r0 + 8, 2 * ks + 1) + t4])};
+#pragma unroll 1
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const float4 x0 = load4(sp + at_chunk<kC>(r0, 4 * ks + t4));
+        const float4 x1 = load4(sp + at_chunk<kC>(r0 + 8, 4 * ks + t4));
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-          const int d = wn * (D / 2) + n * 8 + g;
-          mma_f32(acc[n], a, Split(sv[at_value<D>(ks * 8 + t4, d >> 2) + (d & 3)]),
-                  Split(sv[at_value<D>(ks * 8 + 4 + t4, d >> 2) + (d & 3)]));
+        for (int half = 0; half < 2; ++half) {
+          const Split a[4] = {Split(half ? x0.z : x0.x), Split(half ? x1.z : x1.x),
+                              Split(half ? x0.w : x0.y), Split(half ? x1.w : x1.y)};
+          const int key = 16 * ks + 4 * t4 + 2 * half;
+#pragma unroll
+          for (int c = 0; c < kNt / 4; ++c) {
+            const int v = wn * (D / 8) + g * (kNt / 4) + c;
+            const float4 y0 = load4(sv + at_value<D>(key, v));
+            const float4 y1 = load4(sv + at_value<D>(key + 1, v));
+            const Split b0[4] = {Split(y0.x), Split(y0.y), Split(y0.z), Split(y0.w)};
+            const Split b1[4] = {Split(y1.x), Split(y1.y), Split(y1.z), Split(y1.w)};
+            mma_f32(acc + 4 * c, a, b0, b1);
+          }
         }
       }
       __syncthreads();  // the values and probabilities are free
@@ -284,12 +309,14 @@ __global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
       float* o = chunk_out<float>(p, s.t.q0, s.head, r, D);
       const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
 #pragma unroll
-      for (int n = 0; n < kNt; ++n) {
-        const int d = wn * (D / 2) + n * 8 + 2 * t4;
-        *reinterpret_cast<float2*>(
-            whole ? o + d : reinterpret_cast<float*>(chunk_acc(p, slot, D, d >> 2, r)) + (d & 3)) =
-            make_float2(acc[n][2 * i] * inv, acc[n][2 * i + 1] * inv);
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < kNt; n += 4) {
+          const int d = wn * (D / 2) + (2 * t4 + e) * kNt + n, k = 2 * i + e;
+          *(whole ? reinterpret_cast<float4*>(o + d) : chunk_acc(p, slot, D, d >> 2, r)) =
+              make_float4(acc[n][k] * inv, acc[n + 1][k] * inv, acc[n + 2][k] * inv,
+                          acc[n + 3][k] * inv);
+        }
       if (!whole && wn == 0 && t4 == 0)
         p.ws_ml[(size_t)slot * p.tile_rows + r] = make_float2(m[i], sum);
     }
