@@ -29,19 +29,19 @@
 namespace nsv {
 
 // bf16: a CTA works on two halves of 128 MMA rows (query tokens x query heads
-// of one KV head); keys in runs of 128.  fp32: one set of 64 rows, runs of 64.
+// of one KV head); keys in runs of 128.  fp32: one set of 128 rows, runs of 64.
 constexpr int kChunkHalfRows = 128;
 constexpr int kChunkKeys = 128;
-constexpr int kChunkRowsF32 = 64;
+constexpr int kChunkRowsF32 = 128;
 constexpr int kChunkKeysF32 = 64;
 
 // Costs (see above): of a bf16 tile in runs, of its runs in units.
 constexpr int kChunkTileCost = 2, kChunkPairUnits = 4, kChunkHalfUnits = 3;
+constexpr int kChunkTileCostF32 = 1;
 
 // Query tokens one tile holds.
 __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
-  return dtype == NSV_F32 ? (kChunkRowsF32 / group > 0 ? kChunkRowsF32 / group : 1)
-                          : 2 * (kChunkHalfRows / group);
+  return dtype == NSV_F32 ? kChunkRowsF32 / group : 2 * (kChunkHalfRows / group);
 }
 
 // Workspace of one chunk attention (offsets are multiples of 256):
@@ -107,6 +107,7 @@ struct ChunkParams {
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
   int grid;         // CTAs of the attention kernel
   int tile_cost;    // a tile's own cost, in runs
+  int pair_units, half_units;  // units of a run of a tile that fills both halves, or one
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
@@ -331,6 +332,71 @@ __device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_
       chunk_merge_cols<T, D, 4, 2>(p, c0, n, row, valid, g0, share, quad, out);
     else
       chunk_merge_cols<T, D, 1, 8>(p, c0, n, row, valid, g0, share, quad, out);
+  }
+}
+// What the two warps of a pair share: whose lanes must raise their maximum
+// (two runs in turn), and whether one of them has given up.
+struct PairWords {
+  uint32_t raise[2][2];
+  uint32_t failed;
+};
+
+// The two warps of a pair meet.  False when the other one has given up a wait
+// (it came here on its way out).
+__device__ __forceinline__ bool pair_sync(int bar, volatile PairWords* w) {
+  asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+  return w->failed == 0;
+}
+
+// How a softmax warp ends.
+enum : int { kDone = 0, kTimedOut = 1, kPartnerFailed = 2 };
+
+
+// Once all softmax warps have written a cut tile's piece, counts it; the CTA
+// that counts a tile's last piece will merge it (at most two: the tile that its
+// range starts inside of and the one it ends inside of).
+template <int KEYS>
+__device__ __forceinline__ bool chunk_publish(const ChunkParams& p, uint32_t piece,
+                                              uint32_t published, int4* s_todo, ChunkWalk wk,
+                                              int lane) {
+  uint32_t n = 0;
+  long long runs = 0;  // since the wait before
+  ChunkSegment s;
+#pragma unroll 1
+  while (wk.next<KEYS>(p, s)) {
+    runs += s.j1 - s.j0;
+    if (s.first && s.last) continue;
+    const int2 pc = chunk_pieces<KEYS>(p, s, lane);
+    // (this wait lasts as long as all segments since the one before: a limit for
+    // each of their runs)
+    bool done = false;
+#pragma unroll 1
+    for (; runs >= 0 && !done; --runs) done = sm::warp_wait(piece, n & 1);
+    if (!done) return false;
+    runs = 0;
+    ++n;
+    if (lane == 0) {
+      __threadfence();  // (cumulative: what the warps wrote before they arrived)
+      if (atomicAdd(p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head, 1) == pc.y - 1) {
+        s_todo[s.first ? 2 : 0] = make_int4(s.t.q0, s.t.n_tok, s.head, 0);
+        s_todo[s.first ? 3 : 1] = make_int4(pc.x, pc.y, 0, 0);
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) sm::mbar_arrive(published);
+  return true;
+}
+
+// The tiles whose last piece was one of this CTA's, merged by its first NT threads
+// once all its work is published: a merge within the loops would cost them registers.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void chunk_merge_todo(const ChunkParams& p, const int4* s_todo) {
+  __threadfence();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int4 t = s_todo[2 * k], c = s_todo[2 * k + 1];
+    if (t.y) chunk_merge<T, D, NT>(p, t.x, t.y, t.z, c.x, c.y, threadIdx.x);
   }
 }
 #endif  // __CUDACC__

@@ -26,12 +26,9 @@ int check_chunk(const nsv_shape* s, int64_t tokens) {
   return NSV_OK;
 }
 
-// bf16: one CTA per SM (it takes all the tensor memory); fp32: two.
-int chunk_grid(const nsv_shape* s, int num_sms) { return num_sms * (s->dtype == NSV_F32 ? 2 : 1); }
-
 ChunkWs workspace_of(const nsv_shape* s, int64_t tokens, int num_sms) {
   return make_chunk_ws(s->rows, tokens, s->num_kv_heads, s->num_heads / s->num_kv_heads,
-                       s->head_dim, s->dtype, chunk_grid(s, num_sms));
+                       s->head_dim, s->dtype, num_sms);
 }
 
 // The pools for the bf16 kernel: the rows of [block][kv_head][token] seen as
@@ -128,8 +125,10 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.scale = scale;
   p.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
   p.cap = sc ? sc->softcap : 0.f;
-  p.grid = chunk_grid(s, d.num_sms);
-  p.tile_cost = s->dtype == NSV_F32 ? 0 : kChunkTileCost;
+  p.grid = d.num_sms;  // one CTA per SM: it takes all the tensor memory
+  p.tile_cost = s->dtype == NSV_F32 ? kChunkTileCostF32 : kChunkTileCost;
+  p.pair_units = s->dtype == NSV_F32 ? 1 : kChunkPairUnits;
+  p.half_units = s->dtype == NSV_F32 ? 1 : kChunkHalfUnits;
   p.ws_first = reinterpret_cast<long long*>(p.ws_cta + p.grid);
   if (s->dtype == NSV_BF16 &&
       (!encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||

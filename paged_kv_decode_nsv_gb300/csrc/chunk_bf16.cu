@@ -98,11 +98,6 @@ struct Bars {
   __device__ uint32_t published() const { return b + 8 * (2 * S + 16); }
 };
 
-// A bounded wait with one answer for the whole warp.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(kFull, mbar_wait(bar, parity));
-}
-
 // How a tile's rows lie: 0: over both halves; else how many copies of them one
 // half holds.
 __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegment& s) {
@@ -308,20 +303,6 @@ struct RowState {
   float m, l;         // running maximum (log2 units); this thread's part of the sum
 };
 
-// What the two warps of a pair share: whose lanes must raise their maximum
-// (two runs in turn), and whether one of them has given up.
-struct PairWords {
-  uint32_t raise[2][2];
-  uint32_t failed;
-};
-
-// The two warps of a pair meet.  False when the other one has given up a wait
-// (it came here on its way out).
-__device__ __forceinline__ bool pair_sync(int bar, volatile PairWords* w) {
-  asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-  return w->failed == 0;
-}
-
 // Folds the NC keys of one run that are this thread's (columns col0 .. of the
 // scores t_s) into its row: the maximum over both threads' columns, rescale of
 // this thread's half of O (t_o) where it rises, probabilities (bf16) over the
@@ -472,45 +453,6 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint
   tmem_wait_st();
   return true;
 }
-
-// ------------------------------------------------------------------ publishing
-// Once all softmax warps have written a cut tile's piece, counts it; the CTA
-// that counts a tile's last piece will merge it (at most two: the tile that its
-// range starts inside of and the one it ends inside of).
-template <int D>
-__device__ __forceinline__ bool publish(const ChunkParams& p, const Bars<D>& B, int4* s_todo,
-                                        ChunkWalk wk, int lane) {
-  uint32_t n = 0;
-  long long runs = 0;  // since the wait before
-  ChunkSegment s;
-#pragma unroll 1
-  while (wk.next<kChunkKeys>(p, s)) {
-    runs += s.j1 - s.j0;
-    if (s.first && s.last) continue;
-    const int2 pc = chunk_pieces<kChunkKeys>(p, s, lane);
-    // (this wait lasts as long as all segments since the one before: a limit for
-    // each of their runs)
-    bool done = false;
-#pragma unroll 1
-    for (; runs >= 0 && !done; --runs) done = warp_wait(B.piece(), n & 1);
-    if (!done) return false;
-    runs = 0;
-    ++n;
-    if (lane == 0) {
-      __threadfence();  // (cumulative: what the warps wrote before they arrived)
-      if (atomicAdd(p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head, 1) == pc.y - 1) {
-        s_todo[s.first ? 2 : 0] = make_int4(s.t.q0, s.t.n_tok, s.head, 0);
-        s_todo[s.first ? 3 : 1] = make_int4(pc.x, pc.y, 0, 0);
-      }
-    }
-  }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(B.published());
-  return true;
-}
-
-// How a softmax warp ends.
-enum : int { kDone = 0, kTimedOut = 1, kPartnerFailed = 2 };
 
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
@@ -745,15 +687,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
       if (lane == 0) mbar_arrive(B.piece());
     }
   }
-  // The tiles whose last piece was one of this CTA's are merged now: a merge
-  // within the loop would cost it registers.
   if (!warp_wait(B.published(), 0)) return kTimedOut;
-  __threadfence();
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    const int4 t = s_todo[2 * k], c = s_todo[2 * k + 1];
-    if (t.y) chunk_merge<T, D, kSoftWarps * 32>(p, t.x, t.y, t.z, c.x, c.y, threadIdx.x);
-  }
+  chunk_merge_todo<T, D, kSoftWarps * 32>(p, s_todo);
   return kDone;
 }
 
@@ -834,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     }
     __syncwarp();
   } else {
-    ok = publish<D>(p, B, s_todo, wk, lane);
+    ok = chunk_publish<kChunkKeys>(p, B.piece(), B.published(), s_todo, wk, lane);
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();

@@ -1,24 +1,34 @@
-// Attention of a chunk of new tokens over a paged cache, fp32 (see
-// chunk_bf16.cu for the formulas).  A CTA of 256 threads folds runs of 64
-// positions into up to 64 rows (query tokens x query heads of one KV head).
+// Attention of a chunk of new tokens over a paged cache, fp32, on the
+// 5th-generation tensor cores (see chunk_bf16.cu for the formulas).
 //
-// Both products run on the tensor cores at fp32's precision, each factor as a
-// sum of two tf32 numbers (x = hi + lo, hi = x rounded to tf32's 11 bits, lo the
-// rest): a b = a_hi b_hi + a_hi b_lo + a_lo b_hi, where what is left out, a_lo
-// b_lo, is 2^-22 of the product, and lo's own truncation to tf32 as much.  With
-// fp32 multiply-adds on the CUDA cores instead the kernel was bound by
-// shared-memory loads (8 of 16 bytes for every 64 multiply-adds of a 4 x 4 tile a
-// thread): 207 us for 638 tokens over up to 2048 positions at 12 heads.
+// Both products run at fp32's precision with each factor as a sum of two tf32
+// numbers (x = hi + lo, each rounded to tf32's 11 bits): a b = a_hi b_hi + a_hi
+// b_lo + a_lo b_hi, where what is left out, a_lo b_lo, is 2^-22 of the product,
+// and lo's own rounding as much.
 //
-// Warp (wm, wn) of 4 x 2: 16 rows; half of the keys in the scores, half of the
-// dims in the output.  m16n8k8 fragments, lane = 4 g + t: A rows g and g + 8 at k
-// = t and t + 4, B column g, C rows g and g + 8 at columns 2 t and 2 t + 1.  The
-// probabilities go through shared memory.  The next run's keys are copied
-// (cp.async) from the end of this run's scores on, its values from the end of
-// its products on, and two CTAs share an SM.  Rows of 16-byte chunks are stored
-// swizzled, so that the fragments' loads hit all banks: chunk v of row r at
-// v ^ (r % 8), of the values' rows (which B reads down the columns) at
-// v ^ 2 (r % 4).
+// One CTA per SM, eighteen warps:
+//   warps 0-7   softmax: MMA row r (TMEM lane r) belongs to two threads, in warps
+//               w and w + 4, which split its 64 scores and its output's columns
+//   warps 8-15  loaders: query rows, keys and values from global memory into
+//               registers, a run ahead; split, and stored as MMA operands
+//   warp 16     MMA issue, one elected thread
+//   warp 17     publishes the pieces of cut tiles
+// The rows of an MMA are the tile's query tokens times the query heads that share
+// the KV head.  All operands are K-major with a 128-byte swizzle, panels of 32
+// elements (128 bytes) of K: query rows and keys by dims, values by keys, so the
+// loaders transpose the values: a thread loads 4 dims of 4 keys and stores 4 keys
+// of 4 dims.  Column n of O is dim 4 (n % (D/4)) + n / (D/4): with it, the stores
+// of neighbouring lanes go to neighbouring rows, and hit all banks.
+//
+// Tensor memory (512 columns): scores of run j at 128 (j % 2), 64 columns, then the
+// upper parts of its probabilities in their place; their lower parts in the next 64;
+// O at 256; the lower parts of the query rows at 384.  (The upper parts are in
+// shared memory: 192 KiB hold them and one run's keys and values.)  Scores of run j
+// + 1 are issued before the products of run j's probabilities, so that each softmax
+// runs while the tensor core works.
+//
+// With mma.sync (64 rows, two CTAs per SM) every warp split the keys and values
+// again, and the kernel was bound by that and by the products' latency.
 
 #include "chunk.cuh"
 
@@ -27,352 +37,561 @@ namespace {
 
 using namespace sm;
 
-constexpr int kThreadsF32 = 256;
+constexpr int kSoftWarps = 8, kLoadWarps = 8;
+constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 2) * 32;
 constexpr int kR = kChunkRowsF32, kC = kChunkKeysF32;
+constexpr uint32_t kColO = 256, kColQ = 384;
+constexpr int kTmemCols = 512;
+constexpr int kMetaRing = 8;
+// The running maximum is raised only when a run exceeds it by more than this (log2
+// units): probabilities stay <= 2^8, and most runs skip the rescale.
+constexpr float kSlack = 8.f;
 
 template <int D>
-struct SmemF32 {
-  static constexpr uint32_t kOffK = kR * D * 4;
-  static constexpr uint32_t kOffV = kOffK + kC * D * 4;
-  static constexpr uint32_t kOffP = kOffV + kC * D * 4;
-  static constexpr uint32_t kOffX = kOffP + kR * kC * 4;   // float [2][64]: maxima, sums
-  static constexpr uint32_t kOffOk = kOffX + 2 * kR * 4;   // blocks of two runs in turn
-  static constexpr uint32_t kOffMerge = kOffOk + 16;
-  static constexpr uint32_t kTotal = kOffMerge + 16;
-  static_assert(2 * (kTotal + 1024) <= 228 * 1024, "two CTAs per SM");
+struct Smem {
+  static constexpr uint32_t kQ = kR * D * 4;  // upper parts of the query rows
+  static constexpr uint32_t kKV = kC * D * 4;  // upper or lower parts of a run's keys or values
+  static constexpr uint32_t kOffK = kQ;
+  static constexpr uint32_t kOffV = kOffK + 2 * kKV;
+  static constexpr uint32_t kOffMax = kOffV + 2 * kKV;    // float2 [128]
+  static constexpr uint32_t kOffSum = kOffMax + kR * 8;   // float [2][128]
+  static constexpr uint32_t kOffTodo = kOffSum + kR * 8;  // int4 [2][2]: tiles to merge
+  static constexpr uint32_t kOffBars = kOffTodo + 64;
+  static constexpr int kBars = 15;
+  static constexpr uint32_t kOffMeta = kOffBars + kBars * 8 + 8;
+  static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [4]
+  static constexpr uint32_t kOffWord = kOffPairs + 4 * 20;         // the TMEM address
+  // (at least half of an SM's, so that no two CTAs share its tensor memory)
+  static constexpr uint32_t kUsed = kOffWord + 16;
+  static constexpr uint32_t kTotal = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
-// 16 bytes global -> shared, asynchronously; zeros where there is nothing.
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// Float index of 16-byte chunk v of row r, W floats to a row; of the values'.
-template <int W>
-__device__ __forceinline__ int at_chunk(int r, int v) {
-  return r * W + ((v ^ ((r & 1) << 2 | (r & 2))) << 2);
-}
-template <int W>
-__device__ __forceinline__ int at_value(int r, int v) {
-  const int x = r >> 2 & 3;
-  return r * W + ((v ^ (W == 128 ? (x & 1) | (x & 2) << 1 : x << 1)) << 2);
-}
-__device__ __forceinline__ float4 load4(const float* s) {
-  return *reinterpret_cast<const float4*>(s);
-}
-
-// x = hi + lo.
-struct Split {
-  uint32_t hi, lo;
-  __device__ __forceinline__ explicit Split(float x) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest, ties away from zero
-    lo = __float_as_uint(x - __uint_as_float(hi));
-  }
+struct Bars {
+  uint32_t b;
+  __device__ uint32_t kfull() const { return b; }
+  __device__ uint32_t kempty() const { return b + 8; }
+  __device__ uint32_t vfull() const { return b + 16; }
+  __device__ uint32_t vempty() const { return b + 24; }  // also: O holds the run's products
+  __device__ uint32_t qfull() const { return b + 32; }
+  __device__ uint32_t qfree() const { return b + 40; }
+  __device__ uint32_t scores(uint32_t x) const { return b + 48 + 8 * x; }
+  __device__ uint32_t probs(uint32_t x) const { return b + 64 + 8 * x; }
+  __device__ uint32_t out() const { return b + 80; }
+  __device__ uint32_t ofree() const { return b + 88; }
+  __device__ uint32_t piece() const { return b + 96; }
+  __device__ uint32_t published() const { return b + 104; }
+  __device__ uint32_t drained() const { return b + 112; }
 };
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+
+// x = hi + lo, both rounded to tf32 (to nearest, ties away from zero).
+__device__ __forceinline__ float to_tf32(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
 }
-// d[n] += A B for four column tiles, the small products first; a product waits for
-// the one before it of its tile, so the tiles take turns.
-__device__ __forceinline__ void mma_f32(float (*d)[4], const Split (&a)[4], const Split (&b0)[4],
-                                        const Split (&b1)[4]) {
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-    mma_tf32(d[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0[n].hi, b1[n].hi);
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-    mma_tf32(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0[n].lo, b1[n].lo);
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-    mma_tf32(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0[n].hi, b1[n].hi);
+__device__ __forceinline__ float4 hi4(float4 x) {
+  return make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w));
+}
+__device__ __forceinline__ float4 lo4(float4 x, float4 h) {
+  return make_float4(to_tf32(x.x - h.x), to_tf32(x.y - h.y), to_tf32(x.z - h.z),
+                     to_tf32(x.w - h.w));
 }
 
+// Byte offset of 16-byte chunk v of row r of an operand with `rows` rows.
+__device__ __forceinline__ uint32_t operand_at(int rows, int r, int v) {
+  return (uint32_t)((v >> 3) * rows * 128 + r * 128 + (((v ^ r) & 7) << 4));
+}
+
+// -------------------------------------------------------------------- loaders
 template <int D>
-__global__ void __launch_bounds__(kThreadsF32, 2) chunk_f32_kernel(
-    const __grid_constant__ ChunkParams p) {
-  using L = SmemF32<D>;
-  constexpr int kNt = D / 16;  // 8-column tiles of a warp's half of the dims
-  extern __shared__ __align__(16) unsigned char smem[];
-  float* sq = reinterpret_cast<float*>(smem);
-  float* sk = reinterpret_cast<float*>(smem + L::kOffK);
-  float* sv = reinterpret_cast<float*>(smem + L::kOffV);
-  float* sp = reinterpret_cast<float*>(smem + L::kOffP);
-  float* s_x = reinterpret_cast<float*>(smem + L::kOffX);
-  int* s_ok = reinterpret_cast<int*>(smem + L::kOffOk);
-  int* s_merge = reinterpret_cast<int*>(smem + L::kOffMerge);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, t4 = lane & 3;
-  const int r0 = wm * 16 + g;  // this thread's rows: r0 and r0 + 8
-  const float* q = static_cast<const float*>(p.q);
+__device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsigned char* smem,
+                                     volatile int* s_meta, ChunkWalk wk, int warp, int lane) {
+  using L = Smem<D>;
+  constexpr int kV = D / 4;                            // 16-byte chunks of a key
+  constexpr int kN = kC * kV / (kLoadWarps * 32);      // a thread's chunks of a run: 8 or 4
+  const int tid = warp * 32 + lane;                    // among the loaders
+  const int v = tid & (kV - 1), t1 = tid / kV;         // its chunk, and its first key or key quad
+  constexpr int kStep = kLoadWarps * 32 / kV;          // keys (or quads) between its tasks: 8 or 16
   const float* kp = static_cast<const float*>(p.k_pool);
   const float* vp = static_cast<const float*>(p.v_pool);
-  constexpr float kLog2e = 1.4426950408889634f;
-  griddep_wait();
-  griddep_launch();
-  ChunkWalk wk;
-  wk.init(p, blockIdx.x);
+  uint32_t run = 0, nseg = 0;
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kC>(p, s)) {
-    const int rows = s.t.n_tok * p.group;
-    __syncthreads();  // the previous segment's readers are done
-    for (int c = tid; c < kR * (D / 4); c += kThreadsF32) {
-      const int r = c / (D / 4), v = c - r * (D / 4);
-      const int tok = (int)((unsigned)r / (unsigned)p.group), h = r - tok * p.group;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows)
-        x = __ldg(reinterpret_cast<const float4*>(
-                      q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + h) * D) + v);
-      *reinterpret_cast<float4*>(sq + at_chunk<D>(r, v)) = x;
-    }
-    int2 see[2];
-    int pos[2];
-    float slope[2], m[2], l[2], acc[kNt][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i, tok = (int)((unsigned)r / (unsigned)p.group);
-      pos[i] = s.t.pos0 + tok;
-      see[i] = r < rows ? chunk_sees(p, (long long)s.t.q0 + tok, pos[i], s.t.ctx) : make_int2(0, 0);
-      slope[i] =
-          r < rows && p.slopes ? __ldg(p.slopes + s.head * p.group + r - tok * p.group) : 0.f;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
-#pragma unroll
-    for (int n = 0; n < kNt; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
-    // Copies one run's keys (or values); positions at and past `ke` (at most the
-    // context) and in bad blocks become zeros.
-    auto copy_run = [&](const float* pool, float* dst, int j, bool keys) {
-      const int t0 = s.t.kb + j * kC;
-#pragma unroll 4
-      for (int c = tid; c < kC * (D / 4); c += kThreadsF32) {
-        const int t = c / (D / 4), v = c - t * (D / 4);
-        bool ok = (long long)t0 + t < s.t.ke;
-        const int b = ok ? __ldg(table + (t0 + t) / kBlock) : 0;
-        const bool bad = b < 0 || b >= p.pool_blocks;
-        if (keys && bad && v == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-        ok = ok && !bad;
-        const size_t at =
-            ok ? (((size_t)b * p.kv_heads + s.head) * kBlock + (t0 + t) % kBlock) * D + v * 4 : 0;
-        copy16(dst + (keys ? at_chunk<D>(t, v) : at_value<D>(t, v)), pool + at, ok);
-      }
-      copies_commit();
+    // lane l's block of run j (l < 4): -1 past the tile's keys, -2 if it is bad
+    auto block_ids = [&](int j) {
+      const long long t = (long long)s.t.kb + (long long)j * kC + lane * kBlock;
+      if (j >= s.j1 || lane >= kC / kBlock || t >= s.t.ke) return -1;
+      const int id = __ldg(table + t / kBlock);
+      return id >= 0 && id < p.pool_blocks ? id : -2;
     };
-    // which of a run's blocks hold something
-    auto run_blocks = [&](int j) {
-      if (tid < 32) {
-        const long long t = (long long)s.t.kb + j * kC + tid * kBlock;
-        const int b = tid < kC / kBlock && t < s.t.ke ? __ldg(table + t / kBlock) : -1;
-        const unsigned ok = __ballot_sync(kFull, b >= 0 && b < p.pool_blocks);
-        if (tid == 0) s_ok[j & 1] = (int)ok;
-      }
+    // 16 bytes of key t (within the run whose blocks are `ids`) or zeros
+    auto fetch = [&](const float* pool, int ids, int t0, int t, int c) {
+      const int id = __shfl_sync(kFull, ids, t / kBlock);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (id >= 0 && (long long)t0 + t < s.t.ke)
+        x = __ldg(reinterpret_cast<const float4*>(
+                      pool + (((size_t)id * p.kv_heads + s.head) * kBlock + t % kBlock) * D) +
+                  c);
+      return x;
     };
-    copy_run(kp, sk, s.j0, true);
-    copy_run(vp, sv, s.j0, false);
-    run_blocks(s.j0);
-#pragma unroll 1
-    for (int j = s.j0; j < s.j1; ++j) {
+    float4 kx[kN], vx[kN];
+    auto fetch_keys = [&](int ids, int j) {
       const int t0 = s.t.kb + j * kC;
-      copies_wait<1>();  // the keys
-      __syncthreads();
-      float sc[4][4];  // keys wn * 32 + n * 8 + 2 t4 + {0, 1}, rows r0 and r0 + 8
 #pragma unroll
-      for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      for (int i = 0; i < kN; ++i) kx[i] = fetch(kp, ids, t0, t1 + i * kStep, v);
+    };
+    auto fetch_values = [&](int ids, int j) {
+      const int t0 = s.t.kb + j * kC;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        vx[i] = fetch(vp, ids, t0, 4 * (t1 + (i >> 2) * kStep) + (i & 3), v);
+    };
+    int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
+    fetch_keys(ids, s.j0);
+    fetch_values(ids, s.j0);
+
+    // The query rows: this thread's row, half of its dims.
+    if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
+    tc_fence_after();
+    {
+      const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+      const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
+      const bool valid = tok < s.t.n_tok;
+      const float4* q = static_cast<const float4*>(p.q) +
+                        (((size_t)s.t.q0 + (valid ? tok : 0)) * p.heads + s.head * p.group + g) * kV;
+      const uint32_t t_q = ((uint32_t)((warp & 3) * 32) << 16) + kColQ;
+      if (__any_sync(kFull, valid)) {
 #pragma unroll 2
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const float4 x0 = load4(sq + at_chunk<D>(r0, 4 * ks + t4));
-        const float4 x1 = load4(sq + at_chunk<D>(r0 + 8, 4 * ks + t4));
-        float4 y[4];
+        for (int c = half * (kV / 2); c < (half + 1) * (kV / 2); c += 2) {
+          float lo[8];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          y[n] = load4(sk + at_chunk<D>(wn * 32 + n * 8 + g, 4 * ks + t4));
-        {
-          const Split a[4] = {Split(x0.x), Split(x1.x), Split(x0.y), Split(x1.y)};
-          const Split b0[4] = {Split(y[0].x), Split(y[1].x), Split(y[2].x), Split(y[3].x)};
-          const Split b1[4] = {Split(y[0].y), Split(y[1].y), Split(y[2].y), Split(y[3].y)};
-          mma_f32(sc, a, b0, b1);
-        }
-        {
-          const Split a[4] = {Split(x0.z), Split(x1.z), Split(x0.w), Split(x1.w)};
-          const Split b0[4] = {Split(y[0].z), Split(y[1].z), Split(y[2].z), Split(y[3].z)};
-          const Split b1[4] = {Split(y[0].w), Split(y[1].w), Split(y[2].w), Split(y[3].w)};
-          mma_f32(sc, a, b0, b1);
-        }
-      }
-      const int blocks = s_ok[j & 1];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = wn * 32 + n * 8 + 2 * t4 + e;
-            float x = sc[n][2 * i + e] * p.scale;
-            if (p.cap > 0.f) x = p.cap * tanhf(x / p.cap);
-            x = fmaf(-slope[i], fabsf((float)(pos[i] - t0 - t)), x) * kLog2e;
-            const bool seen =
-                t >= see[i].x - t0 && t < see[i].y - t0 && ((blocks >> (t / kBlock)) & 1);
-            sc[n][2 * i + e] = seen ? x : -INFINITY;
-            mx = fmaxf(mx, sc[n][2 * i + e]);
+          for (int k = 0; k < 2; ++k) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid) x = __ldg(q + c + k);
+            const float4 h = hi4(x), l = lo4(x, h);
+            *reinterpret_cast<float4*>(smem + operand_at(kR, r, c + k)) = h;
+            lo[4 * k] = l.x, lo[4 * k + 1] = l.y, lo[4 * k + 2] = l.z, lo[4 * k + 3] = l.w;
           }
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-        if (t4 == 0) s_x[wn * kR + r0 + 8 * i] = mx;
-      }
-      __syncthreads();  // the keys are free, the maxima of both halves there
-      if (j + 1 < s.j1) {
-        copy_run(kp, sk, j + 1, true);
-        run_blocks(j + 1);
-      } else {
-        copies_commit();
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mx = fmaxf(s_x[r0 + 8 * i], s_x[kR + r0 + 8 * i]);
-        if (mx > m[i]) {
-          const float alpha = exp2f(m[i] - mx);
-          m[i] = mx;
-          l[i] *= alpha;
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            acc[n][2 * i] *= alpha;
-            acc[n][2 * i + 1] *= alpha;
-          }
+          tmem_st8(t_q + 4 * c, lo);
         }
-        const float sub = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float p0 = exp2f(sc[n][2 * i] - sub), p1 = exp2f(sc[n][2 * i + 1] - sub);
-          l[i] += p0 + p1;  // this thread's keys
-          const int t = wn * 32 + n * 8 + 2 * t4;
-          *reinterpret_cast<float2*>(sp + at_chunk<kC>(r0 + 8 * i, t >> 2) + (t & 3)) =
-              make_float2(p0, p1);
-        }
+        tmem_wait_st();
       }
-      copies_wait<1>();  // the values (the next run's keys may still be on their way)
-      __syncthreads();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.qfull());
+    }
+    ++nseg;
 #pragma unroll 1
-      for (int ks = 0; ks < kC / 16; ++ks) {
-        const float4 x0 = load4(sp + at_chunk<kC>(r0, 4 * ks + t4));
-        const float4 x1 = load4(sp + at_chunk<kC>(r0 + 8, 4 * ks + t4));
+    for (int j = s.j0; j < s.j1; ++j, ++run) {
+      if (!warp_wait(B.kempty(), (run & 1) ^ 1)) return false;
+      if (warp == 0) {
+        const unsigned ok = __ballot_sync(kFull, ids >= 0);
+        if (ids == -2) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+        if (lane == 0) s_meta[run % kMetaRing] = (int)ok;
+      }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const Split a[4] = {Split(half ? x0.z : x0.x), Split(half ? x1.z : x1.x),
-                              Split(half ? x0.w : x0.y), Split(half ? x1.w : x1.y)};
-          const int key = 16 * ks + 4 * t4 + 2 * half;
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t at = L::kOffK + operand_at(kC, t1 + i * kStep, v);
+        const float4 h = hi4(kx[i]);
+        *reinterpret_cast<float4*>(smem + at) = h;
+        *reinterpret_cast<float4*>(smem + at + L::kKV) = lo4(kx[i], h);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.kfull());
+      if (j + 1 < s.j1) fetch_keys(ids_next, j + 1);
+
+      if (!warp_wait(B.vempty(), (run & 1) ^ 1)) return false;
 #pragma unroll
-          for (int c = 0; c < kNt / 4; ++c) {
-            const int v = wn * (D / 8) + g * (kNt / 4) + c;
-            const float4 y0 = load4(sv + at_value<D>(key, v));
-            const float4 y1 = load4(sv + at_value<D>(key + 1, v));
-            const Split b0[4] = {Split(y0.x), Split(y0.y), Split(y0.z), Split(y0.w)};
-            const Split b1[4] = {Split(y1.x), Split(y1.y), Split(y1.z), Split(y1.w)};
-            mma_f32(acc + 4 * c, a, b0, b1);
-          }
+      for (int i = 0; i < kN; i += 4) {
+        // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
+        const int quad = t1 + (i >> 2) * kStep;
+        const float4 a = vx[i], b = vx[i + 1], c = vx[i + 2], d = vx[i + 3];
+        const float4 x[4] = {make_float4(a.x, b.x, c.x, d.x), make_float4(a.y, b.y, c.y, d.y),
+                             make_float4(a.z, b.z, c.z, d.z), make_float4(a.w, b.w, c.w, d.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t at = L::kOffV + operand_at(D, e * kV + v, quad);
+          const float4 h = hi4(x[e]);
+          *reinterpret_cast<float4*>(smem + at) = h;
+          *reinterpret_cast<float4*>(smem + at + L::kKV) = lo4(x[e], h);
         }
       }
-      __syncthreads();  // the values and probabilities are free
-      if (j + 1 < s.j1)
-        copy_run(vp, sv, j + 1, false);
-      else
-        copies_commit();
-    }
-    // the rows' sums over the quad's and both halves' keys
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(kFull, l[i], 1);
-      l[i] += __shfl_xor_sync(kFull, l[i], 2);
-      if (t4 == 0) s_x[wn * kR + r0 + 8 * i] = l[i];
-    }
-    __syncthreads();
-    const bool whole = s.first && s.last;
-    const int slot = chunk_slot(blockIdx.x, s.first);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i;
-      if (r >= rows) continue;
-      const float sum = s_x[r] + s_x[kR + r];
-      float* o = chunk_out<float>(p, s.t.q0, s.head, r, D);
-      const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int n = 0; n < kNt; n += 4) {
-          const int d = wn * (D / 2) + (2 * t4 + e) * kNt + n, k = 2 * i + e;
-          *(whole ? reinterpret_cast<float4*>(o + d) : chunk_acc(p, slot, D, d >> 2, r)) =
-              make_float4(acc[n][k] * inv, acc[n + 1][k] * inv, acc[n + 2][k] * inv,
-                          acc[n + 3][k] * inv);
-        }
-      if (!whole && wn == 0 && t4 == 0)
-        p.ws_ml[(size_t)slot * p.tile_rows + r] = make_float2(m[i], sum);
-    }
-    if (!whole) {
-      // publish the piece; the CTA whose piece is the last merges them all
-      __syncthreads();
-      if (tid < 32) {
-        const int2 pc = chunk_pieces<kC>(p, s, lane);
-        if (lane == 0) {
-          __threadfence();
-          int* cnt = p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head;
-          s_merge[0] = atomicAdd(cnt, 1) == pc.y - 1;
-          s_merge[1] = pc.x;
-          s_merge[2] = pc.y;
-        }
-      }
-      __syncthreads();
-      if (s_merge[0]) {
-        __threadfence();
-        chunk_merge<float, D, kThreadsF32>(p, s.t.q0, s.t.n_tok, s.head, s_merge[1], s_merge[2],
-                                           tid);
-      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.vfull());
+      if (j + 1 < s.j1) fetch_values(ids_next, j + 1);
+      ids = ids_next;
+      ids_next = block_ids(j + 2);
     }
   }
+  return true;
 }
 
+// ------------------------------------------------------------------------ MMA
 template <int D>
-cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
+__device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, uint32_t smem0,
+                                          ChunkWalk wk) {
+  using L = Smem<D>;
+  constexpr uint32_t idesc_s = umma_idesc_tf32(kR, kC), idesc_o = umma_idesc_tf32(kR, D);
+  // (descriptors are linear in the start address: lower parts follow the upper ones)
+  const uint64_t dq = umma_desc128(smem0, 16, 1024);
+  const uint64_t dk = umma_desc128(smem0 + L::kOffK, 16, 1024);
+  const uint64_t dv = umma_desc128(smem0 + L::kOffV, 16, 1024);
+  constexpr uint64_t kLow = L::kKV >> 4;
+  // offset of K step ks (8 elements) of an operand with `rows` rows
+  auto step = [](int rows, int ks) {
+    return (uint64_t)(((ks >> 2) * rows * 128 + (ks & 3) * 32) >> 4);
+  };
+  uint32_t run = 0, nseg = 0;
+  auto scores = [&](uint32_t i) {
+    if (!mbar_wait(B.kfull(), i & 1)) return false;
+    tc_fence_after();
+    const uint32_t d = (i & 1) * 128;
+#pragma unroll
+    for (int ks = 0; ks < D / 8; ++ks)
+      umma_ts_tf32(d, kColQ + ks * 8, dk + step(kC, ks), idesc_s, ks > 0);
+#pragma unroll
+    for (int ks = 0; ks < D / 8; ++ks)
+      umma_ss_tf32(d, dq + step(kR, ks), dk + kLow + step(kC, ks), idesc_s, true);
+#pragma unroll
+    for (int ks = 0; ks < D / 8; ++ks)
+      umma_ss_tf32(d, dq + step(kR, ks), dk + step(kC, ks), idesc_s, true);
+    umma_commit(B.kempty(), true);
+    umma_commit(B.scores(i & 1), true);
+    return true;
+  };
+  auto values = [&](uint32_t i, bool fresh) {
+    if (!mbar_wait(B.vfull(), i & 1)) return false;
+    if (!mbar_wait(B.probs(i & 1), (i >> 1) & 1)) return false;
+    tc_fence_after();
+    const uint32_t a = (i & 1) * 128;
+#pragma unroll
+    for (int ks = 0; ks < kC / 8; ++ks)
+      umma_ts_tf32(kColO, a + kC + ks * 8, dv + step(D, ks), idesc_o, !fresh || ks > 0);
+#pragma unroll
+    for (int ks = 0; ks < kC / 8; ++ks)
+      umma_ts_tf32(kColO, a + ks * 8, dv + kLow + step(D, ks), idesc_o, true);
+#pragma unroll
+    for (int ks = 0; ks < kC / 8; ++ks)
+      umma_ts_tf32(kColO, a + ks * 8, dv + step(D, ks), idesc_o, true);
+    umma_commit(B.vempty(), true);
+    return true;
+  };
+  ChunkSegment s, next;
+#pragma unroll 1
+  for (bool more = wk.next<kC>(p, s); more; s = next) {
+    const int n = s.j1 - s.j0;
+    more = wk.next<kC>(p, next);  // its loads overlap this segment's work
+    if (!mbar_wait(B.qfull(), nseg & 1)) return false;
+#pragma unroll 1
+    for (int j = -1; j < n; ++j) {
+      if (j + 1 < n) {
+        if (!scores(run + j + 1)) return false;
+        if (j + 2 == n) umma_commit(B.qfree(), true);
+      }
+      // before O is written again: the previous segment's has been read
+      if (j == 0 && nseg && !mbar_wait(B.ofree(), (nseg - 1) & 1)) return false;
+      if (j >= 0 && !values(run + j, j == 0)) return false;
+    }
+    umma_commit(B.out(), true);
+    run += n;
+    ++nseg;
+  }
+  return true;
+}
+
+// -------------------------------------------------------------------- softmax
+template <int D, bool CAP>
+__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsigned char* smem,
+                                       const volatile int* s_meta, int4* s_todo,
+                                       volatile PairWords* words, ChunkWalk wk, int warp,
+                                       int lane) {
+  using L = Smem<D>;
+  constexpr int kH = kC / 2;  // this thread's scores of a run
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int hf = warp >> 2;                  // which of the pair
+  const int r = (warp & 3) * 32 + lane;      // MMA row, TMEM lane
+  const int bar = 1 + (warp & 3);            // the pair's barrier
+  const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t t_o = t_lane + kColO;
+  const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
+  volatile float2* s_max = reinterpret_cast<volatile float2*>(smem + L::kOffMax) + r;
+  volatile float* s_sum = reinterpret_cast<volatile float*>(smem + L::kOffSum) + r;
+  uint32_t run = 0, nseg = 0, turn = 0;
+  ChunkSegment s;
+#pragma unroll 1
+  while (wk.next<kC>(p, s)) {
+    const bool valid = tok < s.t.n_tok;
+    const bool any_valid = __any_sync(kFull, valid);
+    const int pos = s.t.pos0 + tok;
+    const int2 see = valid ? chunk_sees(p, (long long)s.t.q0 + tok, pos, s.t.ctx)
+                           : make_int2(0, 0x7fffffff);  // rows that are not there mask nothing
+    const float slope = valid && p.slopes ? __ldg(p.slopes + s.head * p.group + g) : 0.f;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j = s.j0; j < s.j1; ++j, ++run) {
+      const uint32_t t_s = t_lane + (run & 1) * 128 + hf * kH;
+      const int t0 = s.t.kb + j * kC;
+      if (!warp_wait(B.scores(run & 1), (run >> 1) & 1)) return kTimedOut;
+      tc_fence_after();
+      if (any_valid) {
+        float mul = p.scale;
+        if (CAP) {
+#pragma unroll 1
+          for (int c = 0; c < kH; c += 8) {
+            float x[8];
+            tmem_ld8(t_s + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = p.cap * tanhf(x[k] * p.scale / p.cap);
+            tmem_st8(t_s + c, x);
+          }
+          tmem_wait_st();
+          mul = 1.f;
+        }
+        float x[kH];
+        tmem_ld32(t_s, x);
+        tmem_wait_ld();
+        const int d = pos - t0 - hf * kH;
+#pragma unroll
+        for (int k = 0; k < kH; ++k) {
+          x[k] *= mul;
+          if (p.slopes) x[k] = fmaf(-slope, fabsf((float)(d - k)), x[k]);
+          x[k] *= kLog2e;
+        }
+        // what the row does not see; nothing in most runs
+        const int lo = min(max(see.x - t0 - hf * kH, 0), kH);
+        const int hi = min(max(see.y - t0 - hf * kH, 0), kH);
+        const int blocks = s_meta[run % kMetaRing] >> (hf * kH / kBlock);
+        uint32_t bits = (hi == 32 ? kFull : (1u << hi) - 1u) & (lo == 32 ? 0u : kFull << lo);
+        bits &= (blocks & 1 ? 0xffffu : 0u) | (blocks & 2 ? 0xffff0000u : 0u);
+        if (!__all_sync(kFull, bits == kFull)) {
+#pragma unroll
+          for (int k = 0; k < kH; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
+        }
+        float mx = x[0], m1 = x[1];
+#pragma unroll
+        for (int k = 2; k < kH; k += 2) {
+          mx = fmaxf(mx, x[k]);
+          m1 = fmaxf(m1, x[k + 1]);
+        }
+        mx = fmaxf(mx, m1);
+        // Both warps learn which rows exceed the running maximum; in most runs none
+        // does, and the maxima themselves need no exchange.
+        const uint32_t mine = __ballot_sync(kFull, valid && mx > m + kSlack);
+        if (lane == 0) words->raise[turn & 1][hf] = mine;
+        if (!pair_sync(bar, words)) return kPartnerFailed;
+        if (mine | words->raise[turn & 1][hf ^ 1]) {
+          (hf ? s_max->y : s_max->x) = mx;
+          if (!pair_sync(bar, words)) return kPartnerFailed;
+          mx = fmaxf(mx, hf ? s_max->x : s_max->y);
+          const bool raise = valid && mx > m + kSlack;  // also the first finite one
+          float alpha = 1.f;
+          if (raise) {
+            alpha = ex2_approx(m - mx);
+            m = mx;
+            l *= alpha;
+          }
+          if (j > s.j0 && __any_sync(kFull, raise)) {
+            // the products of the run before, which O is to hold, are complete
+            if (!warp_wait(B.vempty(), (run - 1) & 1)) return kTimedOut;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 8) {
+              float o[8];
+              tmem_ld8(t_o + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] *= alpha;
+              tmem_st8(t_o + c, o);
+            }
+          }
+        }
+        ++turn;
+        const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < kH; c += 16) {
+          float low[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float e = ex2_approx(x[c + k] - sub);
+            l += e;
+            x[c + k] = to_tf32(e);
+            low[k] = to_tf32(e - x[c + k]);
+          }
+          tmem_st16(t_s + c, x + c);
+          tmem_st16(t_s + kC + c, low);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.probs(run & 1));
+    }
+    // The segment's end: O is complete once its last product is.
+    if (!warp_wait(B.out(), nseg & 1)) return kTimedOut;
+    tc_fence_after();
+    const bool whole = s.first && s.last;
+    if (any_valid) {
+      s_sum[hf * kR] = l;
+      if (!pair_sync(bar, words)) return kPartnerFailed;
+      l += s_sum[(hf ^ 1) * kR];
+      const int slot = chunk_slot(blockIdx.x, s.first);
+      const int row = tok * p.group + g;  // within the tile
+      const float w = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      float* out = chunk_out<float>(p, s.t.q0, s.head, row, D);
+#pragma unroll 1
+      for (int v = hf * (D / 8); v < (hf + 1) * (D / 8); v += 8) {
+        float o[4][8];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmem_ld8(t_o + e * (D / 4) + v, o[e]);
+        tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *(whole ? reinterpret_cast<float4*>(out) + v + k : chunk_acc(p, slot, D, v + k, row)) =
+                make_float4(o[0][k] * w, o[1][k] * w, o[2][k] * w, o[3][k] * w);
+        }
+      }
+      if (!whole && valid && hf == 0)
+        p.ws_ml[(size_t)slot * p.tile_rows + row] = make_float2(m, l);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(B.ofree());
+      if (!whole) mbar_arrive(B.piece());
+    }
+    ++nseg;
+  }
+  if (!warp_wait(B.published(), 0)) return kTimedOut;
+  chunk_merge_todo<float, D, kSoftWarps * 32>(p, s_todo);
+  return kDone;
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
+    const __grid_constant__ ChunkParams p) {
+  using L = Smem<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t smem0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Bars B{smem0 + L::kOffBars};
+  volatile int* s_meta = reinterpret_cast<volatile int*>(smem + L::kOffMeta);
+  volatile PairWords* s_pairs = reinterpret_cast<volatile PairWords*>(smem + L::kOffPairs);
+  volatile uint32_t* s_word = reinterpret_cast<volatile uint32_t*>(smem + L::kOffWord);
+  int4* s_todo = reinterpret_cast<int4*>(smem + L::kOffTodo);
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(B.kfull(), kLoadWarps);
+      mbar_init(B.kempty(), 1);
+      mbar_init(B.vfull(), kLoadWarps);
+      mbar_init(B.vempty(), 1);
+      mbar_init(B.qfull(), kLoadWarps);
+      mbar_init(B.qfree(), 1);
+      for (uint32_t x = 0; x < 2; ++x) {
+        mbar_init(B.scores(x), 1);
+        mbar_init(B.probs(x), kSoftWarps);
+      }
+      mbar_init(B.out(), 1);
+      mbar_init(B.ofree(), kSoftWarps);
+      mbar_init(B.piece(), kSoftWarps);
+      mbar_init(B.published(), 1);
+      mbar_init(B.drained(), 1);
+      fence_mbar_init();
+      for (int i = 0; i < 4; ++i) s_pairs[i].failed = 0;
+      for (int i = 0; i < 4; ++i) s_todo[i] = make_int4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(smem + L::kOffWord), kTmemCols);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // What the code takes for granted (never seen otherwise): the swizzled operands'
+  // alignment, and that all of tensor memory starts at column 0.
+  const uint32_t tmem = *s_word;
+  const bool odd = (smem0 & 1023u) != 0 || tmem != 0;
+  griddep_wait();  // the tile list, and whatever was written before it
+  griddep_launch();
+  ChunkWalk wk;
+  wk.init(p, blockIdx.x);
+  bool ok = !odd;
+  if (odd) {
+    // nothing runs; the end below flags it
+  } else if (warp < kSoftWarps) {
+    volatile PairWords* words = s_pairs + (warp & 3);
+    const int end = softmax<D, CAP>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
+    // Every warp but one whose partner failed meets its partner once more: so a
+    // partner that still works learns of a timeout at its next meeting, and none
+    // is left waiting.
+    if (end != kPartnerFailed) {
+      if (end == kTimedOut) words->failed = 1;
+      __syncwarp();
+      (void)pair_sync(1 + (warp & 3), words);
+    }
+    ok = end == kDone;
+  } else if (warp < kSoftWarps + kLoadWarps) {
+    ok = load<D>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
+  } else if (warp == kSoftWarps + kLoadWarps) {
+    if (elect_one()) {
+      ok = issue_mma<D>(p, B, smem0, wk);
+      if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
+      umma_commit(B.drained(), true);  // arrives once every MMA issued is done
+      (void)mbar_wait(B.drained(), 0);
+    }
+    __syncwarp();
+  } else {
+    ok = chunk_publish<kC>(p, B.piece(), B.published(), s_todo, wk, lane);
+  }
+  if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, bool CAP>
+cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreadsF32);
-  cfg.dynamicSmemBytes = SmemF32<D>::kTotal;
+  cfg.dynamicSmemBytes = Smem<D>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_f32_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_f32_kernel<D, CAP>, p);
+}
+
+template <int D>
+cudaError_t set_attrs() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(chunk_f32_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<D>::kTotal);
+  return e != cudaSuccess
+             ? e
+             : cudaFuncSetAttribute(chunk_f32_kernel<D, true>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
 }
 
 }  // namespace
 
 cudaError_t prepare_chunk_f32() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(chunk_f32_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           SmemF32<64>::kTotal);
-  return e != cudaSuccess
-             ? e
-             : cudaFuncSetAttribute(chunk_f32_kernel<128>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    SmemF32<128>::kTotal);
+  const cudaError_t e = set_attrs<64>();
+  return e != cudaSuccess ? e : set_attrs<128>();
 }
 
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, stream) : launch_dim<128>(p, stream);
+  const bool cap = p.cap > 0.f;
+  if (head_dim == 64) return cap ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
+  return cap ? launch_one<128, true>(p, stream) : launch_one<128, false>(p, stream);
 }
 
 }  // namespace nsv

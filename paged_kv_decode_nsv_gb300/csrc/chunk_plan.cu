@@ -147,9 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       }
       p.ws_tiles[2 * (size_t)i] = make_int4(row, c.start + tok0, nt, pos0);
       // (a tile with more than half of the tokens fills both halves)
-      const int cost = !p.tile_cost     ? 1
-                       : 2 * nt > tt ? kChunkPairUnits
-                                     : kChunkHalfUnits;
+      const int cost = 2 * nt > tt ? p.pair_units : p.half_units;
       p.ws_tiles[2 * (size_t)i + 1] = make_int4(kb, ke, c.ctx, cost);
       const int runs = chunk_runs(kb, ke, p.keys);
       n = (long long)(p.tile_cost + runs) * cost;
@@ -184,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const bool whole = !__syncthreads_or(longest > kWholeRuns) &&
                      (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
-  const int run = p.tile_cost ? kChunkPairUnits : 1;
+  const int run = p.pair_units;
   const int n = whole ? ntiles * p.kv_heads : (int)max(1ll, min(U / run, (long long)p.grid));
   auto prefix = [&](int i) {
     return i == ntiles ? units : ntiles <= kPlanThreads ? s_prefix[i] : __ldcg(p.ws_prefix + i);

@@ -67,6 +67,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity);
 }
 
+// A bounded wait with one answer for the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(kFull, mbar_wait(bar, parity));
+}
+
 // Programmatic dependent launch: wait until the grid this launch depends on
 // has completed and its writes are visible; let the next grid be scheduled.
 __device__ __forceinline__ void griddep_wait() {
@@ -118,6 +123,12 @@ __device__ __forceinline__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// The same of a kind::tf32 MMA: tf32 A and B (of each 32-bit element the upper 19
+// bits), both K-major.
+__device__ __forceinline__ constexpr uint32_t umma_idesc_tf32(int m, int n) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
 // 1 in one lane of the warp, 0 in the others.  (With the lane chosen by
 // elect.sync an MMA issues in under 40 cycles, with a comparison of the lane
 // number in its place in 68, more than the 62 that a 128 x 128 x 16 one runs.)
@@ -145,6 +156,24 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lead ? 1u : 0u)
+      : "memory");
+}
+// kind::tf32, K of 8: one row's 8 elements are 32 bytes of shared memory or 8 columns of
+// tensor memory.
+__device__ __forceinline__ void umma_ss_tf32(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_tf32(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 // One arrival on `bar` once every MMA the `lead` lane issued so far is done.
@@ -182,6 +211,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
         "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
         "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+                 "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
   asm volatile(
