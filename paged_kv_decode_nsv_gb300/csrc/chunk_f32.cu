@@ -102,17 +102,22 @@ __device__ __forceinline__ uint32_t operand_at(int rows, int r, int v) {
 }
 
 // -------------------------------------------------------------------- loaders
-template <int D>
+// Four warps load the keys (KEYS) and four the values, each for itself, so that the
+// keys of a run are stored during products and its values during scores.
+template <int D, bool KEYS>
 __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsigned char* smem,
                                      volatile int* s_meta, ChunkWalk wk, int warp, int lane) {
   using L = Smem<D>;
-  constexpr int kV = D / 4;                            // 16-byte chunks of a key
-  constexpr int kN = kC * kV / (kLoadWarps * 32);      // a thread's chunks of a run: 8 or 4
-  const int tid = warp * 32 + lane;                    // among the loaders
-  const int v = tid & (kV - 1), t1 = tid / kV;         // its chunk, and its first key or key quad
-  constexpr int kStep = kLoadWarps * 32 / kV;          // keys (or quads) between its tasks: 8 or 16
-  const float* kp = static_cast<const float*>(p.k_pool);
-  const float* vp = static_cast<const float*>(p.v_pool);
+  constexpr int kV = D / 4;                   // 16-byte chunks of a key
+  constexpr int kT = kLoadWarps * 32 / 2;     // threads that share a run
+  constexpr int kN = kC * kV / kT;            // a thread's chunks of a run: 16 or 8
+  constexpr int kStep = kT / kV;              // keys (or quads of them) between a thread's: 4 or 8
+  constexpr int kSame = KEYS ? kBlock / kStep : 4;  // consecutive ones within a block
+  const int tid = (warp & 3) * 32 + lane;
+  const int v = tid & (kV - 1), t1 = tid / kV;  // its chunk, and its first key or quad
+  const float* pool = static_cast<const float*>(KEYS ? p.k_pool : p.v_pool);
+  const uint32_t full = KEYS ? B.kfull() : B.vfull(), empty = KEYS ? B.kempty() : B.vempty();
+  unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV);
   uint32_t run = 0, nseg = 0;
   ChunkSegment s;
 #pragma unroll 1
@@ -125,31 +130,25 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       const int id = __ldg(table + t / kBlock);
       return id >= 0 && id < p.pool_blocks ? id : -2;
     };
-    // 16 bytes of key t (within the run whose blocks are `ids`) or zeros
-    auto fetch = [&](const float* pool, int ids, int t0, int t, int c) {
-      const int id = __shfl_sync(kFull, ids, t / kBlock);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (id >= 0 && (long long)t0 + t < s.t.ke)
-        x = __ldg(reinterpret_cast<const float4*>(
-                      pool + (((size_t)id * p.kv_heads + s.head) * kBlock + t % kBlock) * D) +
-                  c);
-      return x;
-    };
-    float4 kx[kN], vx[kN];
-    auto fetch_keys = [&](int ids, int j) {
-      const int t0 = s.t.kb + j * kC;
+    float4 x[kN];
+    auto fetch = [&](int ids, int j) {
+      const int left = s.t.ke - (s.t.kb + j * kC);  // positions from the run's start on
 #pragma unroll
-      for (int i = 0; i < kN; ++i) kx[i] = fetch(kp, ids, t0, t1 + i * kStep, v);
-    };
-    auto fetch_values = [&](int ids, int j) {
-      const int t0 = s.t.kb + j * kC;
+      for (int i = 0; i < kN; i += kSame) {
+        const int t = KEYS ? t1 + i * kStep : 4 * (t1 + (i >> 2) * kStep);
+        const int id = __shfl_sync(kFull, ids, t / kBlock);
+        const float4* at = reinterpret_cast<const float4*>(
+            pool + (((size_t)max(id, 0) * p.kv_heads + s.head) * kBlock + t % kBlock) * D) + v;
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        vx[i] = fetch(vp, ids, t0, 4 * (t1 + (i >> 2) * kStep) + (i & 3), v);
+        for (int u = 0; u < kSame; ++u) {
+          const int dt = KEYS ? u * kStep : u;
+          x[i + u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (id >= 0 && t + dt < left) x[i + u] = __ldg(at + dt * kV);
+        }
+      }
     };
     int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
-    fetch_keys(ids, s.j0);
-    fetch_values(ids, s.j0);
+    fetch(ids, s.j0);
 
     // The query rows: this thread's row, half of its dims.
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
@@ -167,9 +166,9 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
           float lo[8];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid) x = __ldg(q + c + k);
-            const float4 h = hi4(x), l = lo4(x, h);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid) y = __ldg(q + c + k);
+            const float4 h = hi4(y), l = lo4(y, h);
             *reinterpret_cast<float4*>(smem + operand_at(kR, r, c + k)) = h;
             lo[4 * k] = l.x, lo[4 * k + 1] = l.y, lo[4 * k + 2] = l.z, lo[4 * k + 3] = l.w;
           }
@@ -185,45 +184,41 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
-      if (!warp_wait(B.kempty(), (run & 1) ^ 1)) return false;
-      if (warp == 0) {
+      if (!warp_wait(empty, (run & 1) ^ 1)) return false;
+      if (KEYS && warp == 0) {
         const unsigned ok = __ballot_sync(kFull, ids >= 0);
         if (ids == -2) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
         if (lane == 0) s_meta[run % kMetaRing] = (int)ok;
       }
+      if (KEYS) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t at = L::kOffK + operand_at(kC, t1 + i * kStep, v);
-        const float4 h = hi4(kx[i]);
-        *reinterpret_cast<float4*>(smem + at) = h;
-        *reinterpret_cast<float4*>(smem + at + L::kKV) = lo4(kx[i], h);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(B.kfull());
-      if (j + 1 < s.j1) fetch_keys(ids_next, j + 1);
-
-      if (!warp_wait(B.vempty(), (run & 1) ^ 1)) return false;
+        for (int i = 0; i < kN; ++i) {
+          unsigned char* at = dst + operand_at(kC, t1 + i * kStep, v);
+          const float4 h = hi4(x[i]);
+          *reinterpret_cast<float4*>(at) = h;
+          *reinterpret_cast<float4*>(at + L::kKV) = lo4(x[i], h);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < kN; i += 4) {
-        // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
-        const int quad = t1 + (i >> 2) * kStep;
-        const float4 a = vx[i], b = vx[i + 1], c = vx[i + 2], d = vx[i + 3];
-        const float4 x[4] = {make_float4(a.x, b.x, c.x, d.x), make_float4(a.y, b.y, c.y, d.y),
-                             make_float4(a.z, b.z, c.z, d.z), make_float4(a.w, b.w, c.w, d.w)};
+        for (int i = 0; i < kN; i += 4) {
+          // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
+          const float4 a = x[i], b = x[i + 1], c = x[i + 2], d = x[i + 3];
+          const float4 y[4] = {make_float4(a.x, b.x, c.x, d.x), make_float4(a.y, b.y, c.y, d.y),
+                               make_float4(a.z, b.z, c.z, d.z), make_float4(a.w, b.w, c.w, d.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t at = L::kOffV + operand_at(D, e * kV + v, quad);
-          const float4 h = hi4(x[e]);
-          *reinterpret_cast<float4*>(smem + at) = h;
-          *reinterpret_cast<float4*>(smem + at + L::kKV) = lo4(x[e], h);
+          for (int e = 0; e < 4; ++e) {
+            unsigned char* at = dst + operand_at(D, e * kV + v, t1 + (i >> 2) * kStep);
+            const float4 h = hi4(y[e]);
+            *reinterpret_cast<float4*>(at) = h;
+            *reinterpret_cast<float4*>(at + L::kKV) = lo4(y[e], h);
+          }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(B.vfull());
-      if (j + 1 < s.j1) fetch_values(ids_next, j + 1);
+      if (lane == 0) mbar_arrive(full);
       ids = ids_next;
+      if (j + 1 < s.j1) fetch(ids, j + 1);
       ids_next = block_ids(j + 2);
     }
   }
@@ -487,9 +482,9 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   int4* s_todo = reinterpret_cast<int4*>(smem + L::kOffTodo);
   if (warp == 0) {
     if (lane == 0) {
-      mbar_init(B.kfull(), kLoadWarps);
+      mbar_init(B.kfull(), kLoadWarps / 2);
       mbar_init(B.kempty(), 1);
-      mbar_init(B.vfull(), kLoadWarps);
+      mbar_init(B.vfull(), kLoadWarps / 2);
       mbar_init(B.vempty(), 1);
       mbar_init(B.qfull(), kLoadWarps);
       mbar_init(B.qfree(), 1);
@@ -536,7 +531,9 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
     }
     ok = end == kDone;
   } else if (warp < kSoftWarps + kLoadWarps) {
-    ok = load<D>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
+    ok = warp < kSoftWarps + kLoadWarps / 2
+             ? load<D, true>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane)
+             : load<D, false>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
   } else if (warp == kSoftWarps + kLoadWarps) {
     if (elect_one()) {
       ok = issue_mma<D>(p, B, smem0, wk);
