@@ -38,7 +38,12 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 2) * 32;
+constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 4) * 32;  // two warps are idle
+// Registers of a thread: at launch (what 640 threads get), and as the roles share them.
+constexpr int kRegs = 96, kSoftRegs = 96, kLoadRegs = 104, kOtherRegs = 80;
+static_assert(kSoftWarps * kSoftRegs + kLoadWarps * kLoadRegs + 4 * kOtherRegs <=
+                  (kSoftWarps + kLoadWarps + 4) * kRegs,
+              "more registers than the launch has would be waited for without end");
 constexpr int kR = kChunkRowsF32, kC = kChunkKeysF32;
 constexpr uint32_t kColO = 256, kColQ = 384;
 constexpr int kTmemCols = 512;
@@ -123,32 +128,34 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 #pragma unroll 1
   while (wk.next<kC>(p, s)) {
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
-    // lane l's block of run j (l < 4): -1 past the tile's keys, -2 if it is bad
+    // Lane l's block of run j (l < 4), -1 past the tile's keys.  Whether it is a good
+    // one is looked at where it is used: here the warp would wait for it.
+    auto wanted = [&](int j) {
+      return j < s.j1 && lane < kC / kBlock &&
+             (long long)s.t.kb + (long long)j * kC + lane * kBlock < s.t.ke;
+    };
     auto block_ids = [&](int j) {
-      const long long t = (long long)s.t.kb + (long long)j * kC + lane * kBlock;
-      if (j >= s.j1 || lane >= kC / kBlock || t >= s.t.ke) return -1;
-      const int id = __ldg(table + t / kBlock);
-      return id >= 0 && id < p.pool_blocks ? id : -2;
+      return wanted(j) ? __ldg(table + (s.t.kb + j * kC) / kBlock + lane) : -1;
     };
     float4 x[kN];
-    auto fetch = [&](int ids, int j) {
+    // this thread's chunks i .. i + kSame - 1 of run j
+    auto fetch = [&](int i, int ids, int j) {
       const int left = s.t.ke - (s.t.kb + j * kC);  // positions from the run's start on
+      const int t = KEYS ? t1 + i * kStep : 4 * (t1 + (i >> 2) * kStep);
+      const int id = __shfl_sync(kFull, ids, t / kBlock);
+      const bool ok = id >= 0 && id < p.pool_blocks;
+      const float4* at = reinterpret_cast<const float4*>(
+          pool + (((size_t)(ok ? id : 0) * p.kv_heads + s.head) * kBlock + t % kBlock) * D) + v;
 #pragma unroll
-      for (int i = 0; i < kN; i += kSame) {
-        const int t = KEYS ? t1 + i * kStep : 4 * (t1 + (i >> 2) * kStep);
-        const int id = __shfl_sync(kFull, ids, t / kBlock);
-        const float4* at = reinterpret_cast<const float4*>(
-            pool + (((size_t)max(id, 0) * p.kv_heads + s.head) * kBlock + t % kBlock) * D) + v;
-#pragma unroll
-        for (int u = 0; u < kSame; ++u) {
-          const int dt = KEYS ? u * kStep : u;
-          x[i + u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (id >= 0 && t + dt < left) x[i + u] = __ldg(at + dt * kV);
-        }
+      for (int u = 0; u < kSame; ++u) {
+        const int dt = KEYS ? u * kStep : u;
+        x[i + u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ok && t + dt < left) x[i + u] = __ldg(at + dt * kV);
       }
     };
     int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
-    fetch(ids, s.j0);
+#pragma unroll
+    for (int i = 0; i < kN; i += kSame) fetch(i, ids, s.j0);
 
     // The query rows: this thread's row, half of its dims.
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
@@ -184,23 +191,27 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
+      const int ids_after = block_ids(j + 2);
       if (!warp_wait(empty, (run & 1) ^ 1)) return false;
       if (KEYS && warp == 0) {
-        const unsigned ok = __ballot_sync(kFull, ids >= 0);
-        if (ids == -2) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+        const bool good = ids >= 0 && ids < p.pool_blocks;
+        const unsigned ok = __ballot_sync(kFull, good);
+        if (!good && wanted(j)) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
         if (lane == 0) s_meta[run % kMetaRing] = (int)ok;
       }
-      if (KEYS) {
+      // (each part's next load starts as soon as its registers are free)
+      const bool more = j + 1 < s.j1;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          unsigned char* at = dst + operand_at(kC, t1 + i * kStep, v);
-          const float4 h = hi4(x[i]);
-          *reinterpret_cast<float4*>(at) = h;
-          *reinterpret_cast<float4*>(at + L::kKV) = lo4(x[i], h);
-        }
-      } else {
+      for (int i = 0; i < kN; i += kSame) {
+        if (KEYS) {
 #pragma unroll
-        for (int i = 0; i < kN; i += 4) {
+          for (int u = 0; u < kSame; ++u) {
+            unsigned char* at = dst + operand_at(kC, t1 + (i + u) * kStep, v);
+            const float4 h = hi4(x[i + u]);
+            *reinterpret_cast<float4*>(at) = h;
+            *reinterpret_cast<float4*>(at + L::kKV) = lo4(x[i + u], h);
+          }
+        } else {
           // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
           const float4 a = x[i], b = x[i + 1], c = x[i + 2], d = x[i + 3];
           const float4 y[4] = {make_float4(a.x, b.x, c.x, d.x), make_float4(a.y, b.y, c.y, d.y),
@@ -213,13 +224,13 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
             *reinterpret_cast<float4*>(at + L::kKV) = lo4(y[e], h);
           }
         }
+        if (more) fetch(i, ids_next, j + 1);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
       ids = ids_next;
-      if (j + 1 < s.j1) fetch(ids, j + 1);
-      ids_next = block_ids(j + 2);
+      ids_next = ids_after;
     }
   }
   return true;
@@ -519,6 +530,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   if (odd) {
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
+    reg_dec<kSoftRegs>();
     volatile PairWords* words = s_pairs + (warp & 3);
     const int end = softmax<D, CAP>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
     // Every warp but one whose partner failed meets its partner once more: so a
@@ -531,19 +543,23 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
     }
     ok = end == kDone;
   } else if (warp < kSoftWarps + kLoadWarps) {
+    reg_inc<kLoadRegs>();
     ok = warp < kSoftWarps + kLoadWarps / 2
              ? load<D, true>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane)
              : load<D, false>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
-  } else if (warp == kSoftWarps + kLoadWarps) {
-    if (elect_one()) {
-      ok = issue_mma<D>(p, B, smem0, wk);
-      if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
-      umma_commit(B.drained(), true);  // arrives once every MMA issued is done
-      (void)mbar_wait(B.drained(), 0);
-    }
-    __syncwarp();
   } else {
-    ok = chunk_publish<kC>(p, B.piece(), B.published(), s_todo, wk, lane);
+    reg_dec<kOtherRegs>();
+    if (warp == kSoftWarps + kLoadWarps) {
+      if (elect_one()) {
+        ok = issue_mma<D>(p, B, smem0, wk);
+        if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
+        umma_commit(B.drained(), true);  // arrives once every MMA issued is done
+        (void)mbar_wait(B.drained(), 0);
+      }
+      __syncwarp();
+    } else if (warp == kSoftWarps + kLoadWarps + 1) {
+      ok = chunk_publish<kC>(p, B.piece(), B.published(), s_todo, wk, lane);
+    }
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();

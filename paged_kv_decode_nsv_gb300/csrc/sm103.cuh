@@ -81,6 +81,17 @@ __device__ __forceinline__ void griddep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A warpgroup gives registers back, or takes them from those given back (all its warps
+// together; a thread's count, a multiple of 8).
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy accesses (TMA writes, tcgen05 operand reads) of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_smem() {
