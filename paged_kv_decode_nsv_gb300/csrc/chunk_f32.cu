@@ -97,8 +97,7 @@ __device__ __forceinline__ float4 hi4(float4 x) {
   return make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w));
 }
 __device__ __forceinline__ float4 lo4(float4 x, float4 h) {
-  return make_float4(to_tf32(x.x - h.x), to_tf32(x.y - h.y), to_tf32(x.z - h.z),
-                     to_tf32(x.w - h.w));
+  return make_float4(x.x - h.x, x.y - h.y, x.z - h.z, x.w - h.w);
 }
 
 // Byte offset of 16-byte chunk v of row r of an operand with `rows` rows.
@@ -426,7 +425,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
             const float e = ex2_approx(x[c + k] - sub);
             l += e;
             x[c + k] = to_tf32(e);
-            low[k] = to_tf32(e - x[c + k]);
+            low[k] = e - x[c + k];
           }
           tmem_st16(t_s + c, x + c);
           tmem_st16(t_s + kC + c, low);
