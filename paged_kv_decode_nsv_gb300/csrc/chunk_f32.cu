@@ -153,40 +153,46 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       }
     };
     int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
-#pragma unroll
-    for (int i = 0; i < kN; i += kSame) fetch(i, ids, s.j0);
 
-    // The query rows: this thread's row, half of its dims.
+
+    // The query rows: this thread's row, half of its dims, on their way all at once;
+    // then the first run takes their registers.
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+    const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
+    const bool valid = tok < s.t.n_tok;
+    const float4* q = static_cast<const float4*>(p.q) +
+                      (((size_t)s.t.q0 + (valid ? tok : 0)) * p.heads + s.head * p.group + g) * kV +
+                      half * kN;
+    static_assert(kN == kV / 2, "a thread's part of a query row");
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (valid) x[i] = __ldg(q + i);
+    }
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
     tc_fence_after();
-    {
-      const int r = (warp & 3) * 32 + lane, half = warp >> 2;
-      const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
-      const bool valid = tok < s.t.n_tok;
-      const float4* q = static_cast<const float4*>(p.q) +
-                        (((size_t)s.t.q0 + (valid ? tok : 0)) * p.heads + s.head * p.group + g) * kV;
-      const uint32_t t_q = ((uint32_t)((warp & 3) * 32) << 16) + kColQ;
-      if (__any_sync(kFull, valid)) {
-#pragma unroll 2
-        for (int c = half * (kV / 2); c < (half + 1) * (kV / 2); c += 2) {
-          float lo[8];
+    const uint32_t t_q = ((uint32_t)((warp & 3) * 32) << 16) + kColQ + half * (D / 2);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid) y = __ldg(q + c + k);
-            const float4 h = hi4(y), l = lo4(y, h);
-            *reinterpret_cast<float4*>(smem + operand_at(kR, r, c + k)) = h;
-            lo[4 * k] = l.x, lo[4 * k + 1] = l.y, lo[4 * k + 2] = l.z, lo[4 * k + 3] = l.w;
-          }
-          tmem_st8(t_q + 4 * c, lo);
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      fence_proxy_async_smem();
+    for (int i = 0; i < kN; i += kSame) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(B.qfull());
+#pragma unroll
+      for (int u = 0; u < kSame; u += 2) {
+        float lo[8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 h = hi4(x[i + u + k]), l = lo4(x[i + u + k], h);
+          *reinterpret_cast<float4*>(smem + operand_at(kR, r, half * kN + i + u + k)) = h;
+          lo[4 * k] = l.x, lo[4 * k + 1] = l.y, lo[4 * k + 2] = l.z, lo[4 * k + 3] = l.w;
+        }
+        tmem_st8(t_q + 4 * (i + u), lo);
+      }
+      fetch(i, ids, s.j0);
     }
+    tmem_wait_st();
+    tc_fence_before();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.qfull());
     ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
@@ -232,7 +238,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       ids_next = ids_after;
     }
   }
-  return true;
+  return warp_wait(B.published(), 0);
 }
 
 // ------------------------------------------------------------------------ MMA
@@ -473,9 +479,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
     }
     ++nseg;
   }
-  if (!warp_wait(B.published(), 0)) return kTimedOut;
-  chunk_merge_todo<float, D, kSoftWarps * 32>(p, s_todo);
-  return kDone;
+  return warp_wait(B.published(), 0) ? kDone : kTimedOut;
 }
 
 template <int D, bool CAP>
@@ -560,6 +564,8 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
       ok = chunk_publish<kC>(p, B.piece(), B.published(), s_todo, wk, lane);
     }
   }
+  if (ok && warp < kSoftWarps + kLoadWarps)
+    chunk_merge_todo<float, D, (kSoftWarps + kLoadWarps) * 32>(p, s_todo);
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
