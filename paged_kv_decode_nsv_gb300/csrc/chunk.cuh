@@ -328,7 +328,9 @@ __device__ __forceinline__ void chunk_merge(const ChunkParams& p, int q0, int n_
     const bool valid = 8 * rb + (lane & 7) < rows;
     T* out = chunk_out<T>(p, q0, head, row, D);
     const int g0 = (tid >> 5) % share;
-    if (D / 16 / share >= 4)
+    if (D / 16 / share >= 8)
+      chunk_merge_cols<T, D, 8, 1>(p, c0, n, row, valid, g0, share, quad, out);
+    else if (D / 16 / share >= 4)
       chunk_merge_cols<T, D, 4, 2>(p, c0, n, row, valid, g0, share, quad, out);
     else
       chunk_merge_cols<T, D, 1, 8>(p, c0, n, row, valid, g0, share, quad, out);
