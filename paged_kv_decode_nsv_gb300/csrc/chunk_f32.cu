@@ -56,13 +56,15 @@ template <int D>
 struct Smem {
   static constexpr uint32_t kQ = kR * D * 4;  // upper parts of the query rows
   static constexpr uint32_t kKV = kC * D * 4;  // upper or lower parts of a run's keys or values
+  // runs that the keys' and the values' buffers hold
+  static constexpr uint32_t kStages = D == 64 ? 2 : 1;
   static constexpr uint32_t kOffK = kQ;
-  static constexpr uint32_t kOffV = kOffK + 2 * kKV;
-  static constexpr uint32_t kOffMax = kOffV + 2 * kKV;    // float2 [128]
+  static constexpr uint32_t kOffV = kOffK + kStages * 2 * kKV;
+  static constexpr uint32_t kOffMax = kOffV + kStages * 2 * kKV;  // float2 [128]
   static constexpr uint32_t kOffSum = kOffMax + kR * 8;   // float [2][128]
   static constexpr uint32_t kOffTodo = kOffSum + kR * 8;  // int4 [2][2]: tiles to merge
   static constexpr uint32_t kOffBars = kOffTodo + 64;
-  static constexpr int kBars = 15;
+  static constexpr int kBars = 19;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8 + 8;
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [4]
   static constexpr uint32_t kOffWord = kOffPairs + 4 * 20;         // the TMEM address
@@ -74,19 +76,20 @@ struct Smem {
 
 struct Bars {
   uint32_t b;
-  __device__ uint32_t kfull() const { return b; }
-  __device__ uint32_t kempty() const { return b + 8; }
-  __device__ uint32_t vfull() const { return b + 16; }
-  __device__ uint32_t vempty() const { return b + 24; }  // also: O holds the run's products
-  __device__ uint32_t qfull() const { return b + 32; }
-  __device__ uint32_t qfree() const { return b + 40; }
-  __device__ uint32_t scores(uint32_t x) const { return b + 48 + 8 * x; }
-  __device__ uint32_t probs(uint32_t x) const { return b + 64 + 8 * x; }
-  __device__ uint32_t out() const { return b + 80; }
-  __device__ uint32_t ofree() const { return b + 88; }
-  __device__ uint32_t piece() const { return b + 96; }
-  __device__ uint32_t published() const { return b + 104; }
-  __device__ uint32_t drained() const { return b + 112; }
+  __device__ uint32_t at(uint32_t i) const { return b + 8 * i; }
+  __device__ uint32_t kfull(uint32_t i) const { return at(i); }  // i: the run's stage
+  __device__ uint32_t kempty(uint32_t i) const { return at(2 + i); }
+  __device__ uint32_t vfull(uint32_t i) const { return at(4 + i); }
+  __device__ uint32_t vempty(uint32_t i) const { return at(6 + i); }  // also: O has its products
+  __device__ uint32_t scores(uint32_t x) const { return at(8 + x); }
+  __device__ uint32_t probs(uint32_t x) const { return at(10 + x); }
+  __device__ uint32_t qfull() const { return at(12); }
+  __device__ uint32_t qfree() const { return at(13); }
+  __device__ uint32_t out() const { return at(14); }
+  __device__ uint32_t ofree() const { return at(15); }
+  __device__ uint32_t piece() const { return at(16); }
+  __device__ uint32_t published() const { return at(17); }
+  __device__ uint32_t drained() const { return at(18); }
 };
 
 // x = hi + lo, both rounded to tf32 (to nearest, ties away from zero).
@@ -120,8 +123,6 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
   const int tid = (warp & 3) * 32 + lane;
   const int v = tid & (kV - 1), t1 = tid / kV;  // its chunk, and its first key or quad
   const float* pool = static_cast<const float*>(KEYS ? p.k_pool : p.v_pool);
-  const uint32_t full = KEYS ? B.kfull() : B.vfull(), empty = KEYS ? B.kempty() : B.vempty();
-  unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV);
   uint32_t run = 0, nseg = 0;
   ChunkSegment s;
 #pragma unroll 1
@@ -197,7 +198,9 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
       const int ids_after = block_ids(j + 2);
-      if (!warp_wait(empty, (run & 1) ^ 1)) return false;
+      const uint32_t st = run % L::kStages;
+      unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV) + st * 2 * L::kKV;
+      if (!warp_wait(KEYS ? B.kempty(st) : B.vempty(st), ((run / L::kStages) & 1) ^ 1)) return false;
       if (KEYS && warp == 0) {
         const bool good = ids >= 0 && ids < p.pool_blocks;
         const unsigned ok = __ballot_sync(kFull, good);
@@ -233,7 +236,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full);
+      if (lane == 0) mbar_arrive(KEYS ? B.kfull(st) : B.vfull(st));
       ids = ids_next;
       ids_next = ids_after;
     }
@@ -249,8 +252,8 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
   constexpr uint32_t idesc_s = umma_idesc_tf32(kR, kC), idesc_o = umma_idesc_tf32(kR, D);
   // (descriptors are linear in the start address: lower parts follow the upper ones)
   const uint64_t dq = umma_desc128(smem0, 16, 1024);
-  const uint64_t dk = umma_desc128(smem0 + L::kOffK, 16, 1024);
-  const uint64_t dv = umma_desc128(smem0 + L::kOffV, 16, 1024);
+  const uint64_t dk0 = umma_desc128(smem0 + L::kOffK, 16, 1024);
+  const uint64_t dv0 = umma_desc128(smem0 + L::kOffV, 16, 1024);
   constexpr uint64_t kLow = L::kKV >> 4;
   // offset of K step ks (8 elements) of an operand with `rows` rows
   auto step = [](int rows, int ks) {
@@ -258,9 +261,11 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
   };
   uint32_t run = 0, nseg = 0;
   auto scores = [&](uint32_t i) {
-    if (!mbar_wait(B.kfull(), i & 1)) return false;
+    const uint32_t st = i % L::kStages;
+    if (!mbar_wait(B.kfull(st), (i / L::kStages) & 1)) return false;
     tc_fence_after();
     const uint32_t d = (i & 1) * 128;
+    const uint64_t dk = dk0 + st * 2 * kLow;
 #pragma unroll
     for (int ks = 0; ks < D / 8; ++ks)
       umma_ts_tf32(d, kColQ + ks * 8, dk + step(kC, ks), idesc_s, ks > 0);
@@ -270,12 +275,14 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
 #pragma unroll
     for (int ks = 0; ks < D / 8; ++ks)
       umma_ss_tf32(d, dq + step(kR, ks), dk + step(kC, ks), idesc_s, true);
-    umma_commit(B.kempty(), true);
+    umma_commit(B.kempty(st), true);
     umma_commit(B.scores(i & 1), true);
     return true;
   };
   auto values = [&](uint32_t i, bool fresh) {
-    if (!mbar_wait(B.vfull(), i & 1)) return false;
+    const uint32_t st = i % L::kStages;
+    const uint64_t dv = dv0 + st * 2 * kLow;
+    if (!mbar_wait(B.vfull(st), (i / L::kStages) & 1)) return false;
     if (!mbar_wait(B.probs(i & 1), (i >> 1) & 1)) return false;
     tc_fence_after();
     const uint32_t a = (i & 1) * 128;
@@ -288,7 +295,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
 #pragma unroll
     for (int ks = 0; ks < kC / 8; ++ks)
       umma_ts_tf32(kColO, a + ks * 8, dv + step(D, ks), idesc_o, true);
-    umma_commit(B.vempty(), true);
+    umma_commit(B.vempty(st), true);
     return true;
   };
   ChunkSegment s, next;
@@ -408,7 +415,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
           }
           if (j > s.j0 && __any_sync(kFull, raise)) {
             // the products of the run before, which O is to hold, are complete
-            if (!warp_wait(B.vempty(), (run - 1) & 1)) return kTimedOut;
+            const uint32_t i = run - 1;
+            if (!warp_wait(B.vempty(i % L::kStages), (i / L::kStages) & 1)) return kTimedOut;
             tc_fence_after();
 #pragma unroll 1
             for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 8) {
@@ -496,13 +504,13 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   int4* s_todo = reinterpret_cast<int4*>(smem + L::kOffTodo);
   if (warp == 0) {
     if (lane == 0) {
-      mbar_init(B.kfull(), kLoadWarps / 2);
-      mbar_init(B.kempty(), 1);
-      mbar_init(B.vfull(), kLoadWarps / 2);
-      mbar_init(B.vempty(), 1);
       mbar_init(B.qfull(), kLoadWarps);
       mbar_init(B.qfree(), 1);
       for (uint32_t x = 0; x < 2; ++x) {
+        mbar_init(B.kfull(x), kLoadWarps / 2);
+        mbar_init(B.kempty(x), 1);
+        mbar_init(B.vfull(x), kLoadWarps / 2);
+        mbar_init(B.vempty(x), 1);
         mbar_init(B.scores(x), 1);
         mbar_init(B.probs(x), kSoftWarps);
       }
