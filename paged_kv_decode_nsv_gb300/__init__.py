@@ -1,4 +1,5 @@
-"""GB300-native batched paged-attention decode read and KV append.
+"""GB300-native batched paged-attention reads and KV append: the decode read, the
+attention of ragged chunks of new tokens, and the page operators of their cache.
 
 The compute path is the C-ABI library ``libnsv.so`` (hand-written CUDA for
 sm_103a, sources in ``csrc/``, declarations in ``include/nsv.h``).  The thin

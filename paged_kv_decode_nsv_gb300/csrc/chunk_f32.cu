@@ -2,15 +2,18 @@
 // 5th-generation tensor cores (see chunk_bf16.cu for the formulas).
 //
 // Both products run at fp32's precision with each factor as a sum of two tf32
-// numbers (x = hi + lo, each rounded to tf32's 11 bits): a b = a_hi b_hi + a_hi
-// b_lo + a_lo b_hi, where what is left out, a_lo b_lo, is 2^-22 of the product,
-// and lo's own rounding as much.
+// numbers: x = hi + lo, hi rounded to tf32's 11 bits, and of lo = x - hi, which is
+// exact, the MMA takes the upper 11.  a b = a_hi b_hi + a_hi b_lo + a_lo b_hi: what
+// is left out, a_lo b_lo, is at most 2^-22 of the product, and what the MMA drops of
+// a lo 2^-21 of x.  Against 64 bits the outputs are off by 3.7e-7 (a plain fp32
+// computation: 2.2e-7).
 //
-// One CTA per SM, eighteen warps:
+// One CTA per SM, twenty warps (the last two idle):
 //   warps 0-7   softmax: MMA row r (TMEM lane r) belongs to two threads, in warps
 //               w and w + 4, which split its 64 scores and its output's columns
-//   warps 8-15  loaders: query rows, keys and values from global memory into
-//               registers, a run ahead; split, and stored as MMA operands
+//   warps 8-15  loaders, four for the keys, four for the values, all for the query
+//               rows: from global memory into registers, a run ahead; split, and
+//               stored as MMA operands
 //   warp 16     MMA issue, one elected thread
 //   warp 17     publishes the pieces of cut tiles
 // The rows of an MMA are the tile's query tokens times the query heads that share
@@ -22,13 +25,19 @@
 //
 // Tensor memory (512 columns): scores of run j at 128 (j % 2), 64 columns, then the
 // upper parts of its probabilities in their place; their lower parts in the next 64;
-// O at 256; the lower parts of the query rows at 384.  (The upper parts are in
-// shared memory: 192 KiB hold them and one run's keys and values.)  Scores of run j
-// + 1 are issued before the products of run j's probabilities, so that each softmax
-// runs while the tensor core works.
+// O at 256; the lower parts of the query rows at 384.  (Their upper parts are in
+// shared memory: 192 KiB hold them and one run's keys and values, at head_dim 64 two
+// runs'.)  Scores of run j + 1 are issued before the products of run j's
+// probabilities, so that each softmax runs while the tensor core works.
 //
-// With mma.sync (64 rows, two CTAs per SM) every warp split the keys and values
-// again, and the kernel was bound by that and by the products' latency.
+// A run of 64 positions takes 2.5 us at head_dim 128 and 1.5 to 1.6 at 64 whatever the
+// rows; its MMAs alone would take 1.7 and 0.9, its bytes 1.5 and 0.7.  Nothing is far
+// ahead: a third of the MMAs left out, the global loads, the split or the softmax, it
+// takes 2.1 to 2.3 (head_dim 128), because a buffer of keys holds one run, which is
+// stored after the scores before it are done and before the next can start.  638 tokens
+// over up to 2048 positions, 12 heads: 56 us.  The same split on mma.sync (64 rows, two
+// CTAs per SM), where every warp splits the keys and values again, took 162, and
+// multiply-adds on the CUDA cores 207.
 
 #include "chunk.cuh"
 
@@ -40,6 +49,7 @@ using namespace sm;
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 4) * 32;  // two warps are idle
 // Registers of a thread: at launch (what 640 threads get), and as the roles share them.
+// With 96 for all, the loaders spilled in their loop: 4.3 us a run instead of 2.7.
 constexpr int kRegs = 96, kSoftRegs = 96, kLoadRegs = 104, kOtherRegs = 80;
 static_assert(kSoftWarps * kSoftRegs + kLoadWarps * kLoadRegs + 4 * kOtherRegs <=
                   (kSoftWarps + kLoadWarps + 4) * kRegs,
@@ -92,7 +102,8 @@ struct Bars {
   __device__ uint32_t drained() const { return at(18); }
 };
 
-// x = hi + lo, both rounded to tf32 (to nearest, ties away from zero).
+// x = hi + lo: hi rounded to tf32 (to nearest, ties away from zero), lo exact.  (Rounded
+// too, lo leaves the outputs as far off and costs 4 us of 60.)
 __device__ __forceinline__ float to_tf32(float x) {
   return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
 }
@@ -110,7 +121,8 @@ __device__ __forceinline__ uint32_t operand_at(int rows, int r, int v) {
 
 // -------------------------------------------------------------------- loaders
 // Four warps load the keys (KEYS) and four the values, each for itself, so that the
-// keys of a run are stored during products and its values during scores.
+// keys of a run are stored during products and its values during scores.  (Eight warps
+// for both in turn: 5.7 us a run instead of 3.7.)
 template <int D, bool KEYS>
 __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsigned char* smem,
                                      volatile int* s_meta, ChunkWalk wk, int warp, int lane) {
@@ -200,7 +212,8 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       const int ids_after = block_ids(j + 2);
       const uint32_t st = run % L::kStages;
       unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV) + st * 2 * L::kKV;
-      if (!warp_wait(KEYS ? B.kempty(st) : B.vempty(st), ((run / L::kStages) & 1) ^ 1)) return false;
+      const uint32_t empty = KEYS ? B.kempty(st) : B.vempty(st);
+      if (!warp_wait(empty, ((run / L::kStages) & 1) ^ 1)) return false;
       if (KEYS && warp == 0) {
         const bool good = ids >= 0 && ids < p.pool_blocks;
         const unsigned ok = __ballot_sync(kFull, good);
@@ -616,7 +629,8 @@ cudaError_t prepare_chunk_f32() {
 
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
   const bool cap = p.cap > 0.f;
-  if (head_dim == 64) return cap ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
+  if (head_dim == 64)
+    return cap ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
   return cap ? launch_one<128, true>(p, stream) : launch_one<128, false>(p, stream);
 }
 

@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         const int n = min(tt, c.n - tok0);
         int kb = 0x7fffffff, ke = 0;
         for (int t = lane; t < n; t += 32) {
-          const int2 v = chunk_sees(p, (long long)c.start + tok0 + t, c.ctx - c.n + tok0 + t, c.ctx);
+          const int2 v =
+              chunk_sees(p, (long long)c.start + tok0 + t, c.ctx - c.n + tok0 + t, c.ctx);
           if (v.x < v.y) {
             kb = min(kb, v.x);
             ke = max(ke, v.y);

@@ -16,7 +16,8 @@ constexpr int kPageWords = 64;
 // row and the free blocks; compact: the map of the blocks, the holes and the
 // moving blocks (at most half of the blocks each).
 inline uint64_t page_ws_bytes(int rows, long long num_blocks) {
-  const uint64_t lists = (uint64_t)rows * 16 + (uint64_t)(num_blocks > rows ? num_blocks : rows) * 4;
+  const uint64_t most = num_blocks > rows ? num_blocks : rows;
+  const uint64_t lists = (uint64_t)rows * 16 + most * 4;
   const uint64_t compact = (uint64_t)num_blocks * 4 + 2 * ((uint64_t)num_blocks / 2 + 1) * 4;
   return kPageWords * 4 + (lists > compact ? lists : compact);
 }

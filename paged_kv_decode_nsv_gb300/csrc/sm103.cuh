@@ -35,7 +35,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // One arrival that also adds `bytes` to what the phase waits for.
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(
+          bar),
       "r"(bytes)
       : "memory");
 }

@@ -357,7 +357,8 @@ def _arg(t, what, dtype, shape, device):
         raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, list(shape), t.dtype,
                                                           list(t.shape)))
     if t.get_device() != device:
-        raise ValueError("%s is on %s, not on the current CUDA device %d" % (what, t.device, device))
+        raise ValueError("%s is on %s, not on the current CUDA device %d"
+                         % (what, t.device, device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
     return t.data_ptr()
@@ -454,8 +455,9 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
     new_ptrs = (_arg(k_new, "k_new", q.dtype, new, dev), _arg(v_new, "v_new", q.dtype, new, dev),
                 _arg(write_slots, "write_slots", torch.int64, (T,), dev))
     ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_chunk_step(shape, scores, T, ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr,
-                               ws_ptr, ws_bytes, _raw_stream(stream, dev)), "nsv_chunk_step")
+    _check(_lib.nsv_chunk_step(shape, scores, T, ptrs[0], *new_ptrs, *ptrs[1:], float(scale),
+                               out_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev)),
+           "nsv_chunk_step")
     return out
 
 
