@@ -360,12 +360,12 @@ enum : int { kDone = 0, kTimedOut = 1, kPartnerFailed = 2 };
 
 // Once all softmax warps have written a cut tile's piece, counts it; the CTA
 // that counts a tile's last piece will merge it (at most two: the tile that its
-// range starts inside of and the one it ends inside of).
+// range starts inside of and the one it ends inside of, which have a barrier each:
+// piece0 and, if the tile starts here, piece1).
 template <int KEYS>
-__device__ __forceinline__ bool chunk_publish(const ChunkParams& p, uint32_t piece,
-                                              uint32_t published, int4* s_todo, ChunkWalk wk,
-                                              int lane) {
-  uint32_t n = 0;
+__device__ __forceinline__ bool chunk_publish(const ChunkParams& p, uint32_t piece0,
+                                              uint32_t piece1, uint32_t published, int4* s_todo,
+                                              ChunkWalk wk, int lane) {
   long long runs = 0;  // since the wait before
   ChunkSegment s;
 #pragma unroll 1
@@ -377,10 +377,9 @@ __device__ __forceinline__ bool chunk_publish(const ChunkParams& p, uint32_t pie
     // each of their runs)
     bool done = false;
 #pragma unroll 1
-    for (; runs >= 0 && !done; --runs) done = sm::warp_wait(piece, n & 1);
+    for (; runs >= 0 && !done; --runs) done = sm::warp_wait(s.first ? piece1 : piece0, 0);
     if (!done) return false;
     runs = 0;
-    ++n;
     if (lane == 0) {
       __threadfence();  // (cumulative: what the warps wrote before they arrived)
       if (atomicAdd(p.ws_cnt + (size_t)s.tile * p.kv_heads + s.head, 1) == pc.y - 1) {

@@ -80,10 +80,11 @@ struct Smem {
   // int4 [2][2]: tiles to merge
   static constexpr uint32_t kOffTodo = kOffMl + 2 * kChunkHalfRows * 8;
   static constexpr uint32_t kOffBars = kOffTodo + 64;
-  static constexpr int kBars = 2 * kStages + 18;
+  static constexpr int kBars = 2 * kStages + 19;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8;
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
-  static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address
+  static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address, then kOffDone
+  static constexpr uint32_t kOffDone = kOffWord + 4;        // softmax warps done, over all tiles
   static constexpr uint32_t kTotal = kOffWord + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
@@ -103,10 +104,21 @@ struct Bars {
   __device__ uint32_t join() const { return b + 8 * (2 * S + 9); }
   __device__ uint32_t drained() const { return b + 8 * (2 * S + 10); }
   __device__ uint32_t meet(int i) const { return b + 8 * (2 * S + 11 + i); }
-  __device__ uint32_t piece() const { return b + 8 * (2 * S + 15); }
+  __device__ uint32_t piece(int first) const { return b + 8 * (2 * S + (first ? 18 : 15)); }
   __device__ uint32_t mlfree() const { return b + 8 * (2 * S + 17); }
   __device__ uint32_t published() const { return b + 8 * (2 * S + 16); }
 };
+
+// A bounded wait for a count that only grows.
+__device__ __forceinline__ bool count_wait(const volatile uint32_t* count, uint32_t least) {
+  const long long t0 = clock64();
+  bool ok;
+#pragma unroll 1
+  while (!(ok = *count >= least) && clock64() - t0 <= kWaitLimitCycles) {
+  }
+  __threadfence_block();
+  return __all_sync(kFull, ok);
+}
 
 // How a tile's rows lie: 0: over both halves; else how many copies of them one
 // half holds.
@@ -121,13 +133,13 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 // ------------------------------------------------------------------ producer
 template <int D>
 __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
-                                        volatile int* s_meta, ChunkWalk wk, int lane,
-                                        uint32_t& i, uint32_t& nseg) {
+                                        volatile int* s_meta, const volatile uint32_t* s_done,
+                                        ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
   using L = Smem<D>;
   constexpr uint32_t kBlockBytes = kBlock * D * 2;
   const int half_tok = p.tile_tokens / 2;
   uint32_t run = 0;
-  int before = 0;  // the previous segment's copies
+  uint32_t shared = 0;  // segments up to and with the last one whose copies were exchanged
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
@@ -135,9 +147,11 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
     // copy and 64-dim slice; tokens past the tensor are filled with zeros
     if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
     const int copies = copies_of(p, s);
-    // (the second half may still serve the previous tile's copies)
-    if (copies == 0 && before > 1 && !warp_wait(B.ofree(), (nseg - 1) & 1)) return false;
-    before = copies;
+    // The second half may still serve an earlier tile's copies.  (A count, not a
+    // barrier's parity: their epilogue can be two tiles behind.)
+    if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
+    if (copies == 0) shared = 0;
+    if (copies > 1) shared = nseg + 1;
     if (lane == 0) {
       const int boxes = copies == 0 ? 2 : copies;
       const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
@@ -467,8 +481,9 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
                                        unsigned char* smem, const volatile int* s_meta,
-                                       int4* s_todo, volatile PairWords* words, ChunkWalk wk,
-                                       int warp, int lane) {
+                                       int4* s_todo, uint32_t* s_done,
+                                       volatile PairWords* words, ChunkWalk wk, int warp,
+                                       int lane) {
   using L = Smem<D>;
   using T = __nv_bfloat16;
   const int x = warp >> 3;                     // stream
@@ -691,12 +706,13 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     tc_fence_before();
     fence_proxy_async_smem();  // the exchange's bytes may become query rows again
     __syncwarp();
-    if (lane == 0) mbar_arrive(B.ofree());
-    ++nseg;
-    if (!whole) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(B.piece());
+    if (lane == 0) {
+      mbar_arrive(B.ofree());
+      __threadfence_block();
+      atomicAdd(s_done, 1u);
+      if (!whole) mbar_arrive(B.piece(s.first));
     }
+    ++nseg;
   }
   if (!warp_wait(B.published(), 0)) return kTimedOut;
   chunk_merge_todo<T, D, kSoftWarps * 32>(p, s_todo);
@@ -715,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   volatile PairWords* s_pairs = reinterpret_cast<volatile PairWords*>(smem + L::kOffPairs);
   volatile uint32_t* s_word = reinterpret_cast<volatile uint32_t*>(smem + L::kOffWord);
   int4* s_todo = reinterpret_cast<int4*>(smem + L::kOffTodo);
+  uint32_t* s_done = reinterpret_cast<uint32_t*>(smem + L::kOffDone);
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < 2 * L::kStages + 2; ++i) mbar_init(smem0 + L::kOffBars + 8 * i, 1);
@@ -728,12 +745,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       }
       mbar_init(B.ofree(), kSoftWarps);
       mbar_init(B.join(), kSoftWarps);
-      mbar_init(B.piece(), kSoftWarps);
+      mbar_init(B.piece(0), kSoftWarps);
+      mbar_init(B.piece(1), kSoftWarps);
       mbar_init(B.published(), 1);
       mbar_init(B.mlfree(), kSoftWarps);
       fence_mbar_init();
       for (int i = 0; i < 8; ++i) s_pairs[i].failed = 0;
       for (int i = 0; i < 4; ++i) s_todo[i] = make_int4(0, 0, 0, 0);
+      *s_done = 0;
     }
     __syncwarp();
     tmem_alloc(smem_u32(smem + L::kOffWord), kTmemCols);
@@ -754,7 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
     volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
-    const int end = softmax<D, CAP, BIAS>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
+    const int end = softmax<D, CAP, BIAS>(p, B, smem, s_meta, s_todo, s_done, words, wk, warp,
+                                          lane);
     // Every warp but one whose partner failed meets its partner once more: so a
     // partner that still works learns of a timeout at its next meeting, and none
     // is left waiting.
@@ -766,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     ok = end == kDone;
   } else if (warp == kSoftWarps) {
     uint32_t i = 0, nq = 0;
-    ok = produce<D>(p, B, smem0, s_meta, wk, lane, i, nq);
+    ok = produce<D>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
     // every copy issued lands before the CTA can end, even after a timeout
     for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
@@ -780,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     }
     __syncwarp();
   } else {
-    ok = chunk_publish<kChunkKeys>(p, B.piece(), B.published(), s_todo, wk, lane);
+    ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();

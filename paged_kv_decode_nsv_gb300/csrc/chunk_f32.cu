@@ -74,7 +74,7 @@ struct Smem {
   static constexpr uint32_t kOffSum = kOffMax + kR * 8;   // float [2][128]
   static constexpr uint32_t kOffTodo = kOffSum + kR * 8;  // int4 [2][2]: tiles to merge
   static constexpr uint32_t kOffBars = kOffTodo + 64;
-  static constexpr int kBars = 19;
+  static constexpr int kBars = 20;
   static constexpr uint32_t kOffMeta = kOffBars + kBars * 8 + 8;
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [4]
   static constexpr uint32_t kOffWord = kOffPairs + 4 * 20;         // the TMEM address
@@ -97,7 +97,7 @@ struct Bars {
   __device__ uint32_t qfree() const { return at(13); }
   __device__ uint32_t out() const { return at(14); }
   __device__ uint32_t ofree() const { return at(15); }
-  __device__ uint32_t piece() const { return at(16); }
+  __device__ uint32_t piece(int first) const { return at(first ? 19 : 16); }
   __device__ uint32_t published() const { return at(17); }
   __device__ uint32_t drained() const { return at(18); }
 };
@@ -496,7 +496,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(B.ofree());
-      if (!whole) mbar_arrive(B.piece());
+      if (!whole) mbar_arrive(B.piece(s.first));
     }
     ++nseg;
   }
@@ -529,7 +529,8 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
       }
       mbar_init(B.out(), 1);
       mbar_init(B.ofree(), kSoftWarps);
-      mbar_init(B.piece(), kSoftWarps);
+      mbar_init(B.piece(0), kSoftWarps);
+      mbar_init(B.piece(1), kSoftWarps);
       mbar_init(B.published(), 1);
       mbar_init(B.drained(), 1);
       fence_mbar_init();
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
       }
       __syncwarp();
     } else if (warp == kSoftWarps + kLoadWarps + 1) {
-      ok = chunk_publish<kC>(p, B.piece(), B.published(), s_todo, wk, lane);
+      ok = chunk_publish<kC>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
     }
   }
   if (ok && warp < kSoftWarps + kLoadWarps)

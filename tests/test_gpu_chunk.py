@@ -574,3 +574,32 @@ def test_more_work_than_a_share_counts_is_not_run():
     nsv.paged_chunk(q, *pools, bt, starts, ctx, 0.1, out)
     assert nsv.device_status(clear=True)[0] == nsv.DEV_BAD_CHUNK
     assert (out == 7.5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_few_rows_then_many_on_one_cta(dtype, head_dim):
+    """A tile of one token right before tiles of sixteen: its rows' exchange may
+    still be under way when theirs are loaded."""
+    check(batch([1294, 91, 361, 895], [1019, 81, 197, 766], 64, 4, head_dim, dtype, seed=26), dtype)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_batches(seed):
+    """Mixes of chunks of all lengths, so that tiles of all kinds follow each other."""
+    rng = np.random.default_rng(100 + seed)
+    rows = int(rng.integers(1, 40))
+    new = [int(x) for x in np.exp(rng.uniform(0, math.log(rng.choice([2, 40, 400])), rows))]
+    while sum(new) > 1500:
+        new.pop()
+    ctx = [n + int(rng.choice([0, 3, 150, 900]) * rng.random()) for n in new]
+    kv_heads = int(rng.choice([1, 2, 4, 8]))
+    group = int(rng.choice([1, 2, 4, 5, 16, 33, 64]))
+    dtype = "f32" if seed % 4 == 3 else "bf16"
+    b = batch(ctx, new, group * kv_heads, kv_heads, int(rng.choice([64, 128, 128])), dtype,
+              seed=seed, pad=int(rng.integers(0, 3)))
+    kind = rng.choice(["causal", "documents", "window", "prefix"])
+    kw = {} if kind == "causal" else _bounds(b, kind, rng)
+    if rng.random() < 0.3:
+        kw["softcap"] = 20.0
+    check(b, dtype, **kw)
