@@ -50,10 +50,14 @@ constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 4) * 32;  // two warps are idle
 // Registers of a thread: at launch (what 640 threads get), and as the roles share them.
 // With 96 for all, the loaders spilled in their loop: 4.3 us a run instead of 2.7.
-constexpr int kRegs = 96, kSoftRegs = 96, kLoadRegs = 104, kOtherRegs = 80;
-static_assert(kSoftWarps * kSoftRegs + kLoadWarps * kLoadRegs + 4 * kOtherRegs <=
-                  (kSoftWarps + kLoadWarps + 4) * kRegs,
-              "more registers than the launch has would be waited for without end");
+constexpr int kRegs = 96, kOtherRegs = 80;
+template <int D>
+struct Regs {
+  static constexpr int kSoft = D == 128 ? 120 : 104, kLoad = D == 128 ? 80 : 96;
+  static_assert(kSoftWarps * kSoft + kLoadWarps * kLoad + 4 * kOtherRegs <=
+                    (kSoftWarps + kLoadWarps + 4) * kRegs,
+                "more registers than the launch has would be waited for without end");
+};
 constexpr int kR = kChunkRowsF32, kC = kChunkKeysF32;
 constexpr uint32_t kColO = 256, kColQ = 384;
 constexpr int kTmemCols = 512;
@@ -70,7 +74,11 @@ struct Smem {
   static constexpr uint32_t kStages = D == 64 ? 2 : 1;
   static constexpr uint32_t kOffK = kQ;
   static constexpr uint32_t kOffV = kOffK + kStages * 2 * kKV;
-  static constexpr uint32_t kOffMax = kOffV + kStages * 2 * kKV;  // float2 [128]
+  // Of a loader's 16 or 8 chunks of a run, on their way those it has no registers for
+  // wait here: [loaders][chunks][128 threads] of 16 bytes.
+  static constexpr int kHeld = D == 64 ? 0 : 8;
+  static constexpr uint32_t kOffHeld = kOffV + kStages * 2 * kKV;
+  static constexpr uint32_t kOffMax = kOffHeld + kHeld * kLoadWarps * 32 * 16;  // float2 [128]
   static constexpr uint32_t kOffSum = kOffMax + kR * 8;   // float [2][128]
   static constexpr uint32_t kOffTodo = kOffSum + kR * 8;  // int4 [2][2]: tiles to merge
   static constexpr uint32_t kOffBars = kOffTodo + 64;
@@ -90,13 +98,12 @@ struct Bars {
   __device__ uint32_t kfull(uint32_t i) const { return at(i); }  // i: the run's stage
   __device__ uint32_t kempty(uint32_t i) const { return at(2 + i); }
   __device__ uint32_t vfull(uint32_t i) const { return at(4 + i); }
-  __device__ uint32_t vempty(uint32_t i) const { return at(6 + i); }  // also: O has its products
+  __device__ uint32_t vempty(uint32_t i) const { return at(6 + i); }  // also: O holds its products
   __device__ uint32_t scores(uint32_t x) const { return at(8 + x); }
   __device__ uint32_t probs(uint32_t x) const { return at(10 + x); }
   __device__ uint32_t qfull() const { return at(12); }
   __device__ uint32_t qfree() const { return at(13); }
-  __device__ uint32_t out() const { return at(14); }
-  __device__ uint32_t ofree() const { return at(15); }
+  __device__ uint32_t oread() const { return at(14); }
   __device__ uint32_t piece(int first) const { return at(first ? 19 : 16); }
   __device__ uint32_t published() const { return at(17); }
   __device__ uint32_t drained() const { return at(18); }
@@ -112,6 +119,20 @@ __device__ __forceinline__ float4 hi4(float4 x) {
 }
 __device__ __forceinline__ float4 lo4(float4 x, float4 h) {
   return make_float4(x.x - h.x, x.y - h.y, x.z - h.z, x.w - h.w);
+}
+
+// 16 bytes global -> shared, asynchronously; zeros where there is nothing.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N < 0 ? 0 : N) : "memory");
 }
 
 // Byte offset of 16-byte chunk v of row r of an operand with `rows` rows.
@@ -132,6 +153,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
   constexpr int kN = kC * kV / kT;            // a thread's chunks of a run: 16 or 8
   constexpr int kStep = kT / kV;              // keys (or quads of them) between a thread's: 4 or 8
   constexpr int kSame = KEYS ? kBlock / kStep : 4;  // consecutive ones within a block
+  constexpr int kHeld = L::kHeld;
   const int tid = (warp & 3) * 32 + lane;
   const int v = tid & (kV - 1), t1 = tid / kV;  // its chunk, and its first key or quad
   const float* pool = static_cast<const float*>(KEYS ? p.k_pool : p.v_pool);
@@ -149,8 +171,10 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     auto block_ids = [&](int j) {
       return wanted(j) ? __ldg(table + (s.t.kb + j * kC) / kBlock + lane) : -1;
     };
-    float4 x[kN];
-    // this thread's chunks i .. i + kSame - 1 of run j
+    float4 x[kN - kHeld];  // chunks kHeld and on
+    unsigned char* held = smem + L::kOffHeld + ((KEYS ? 0 : kHeld) * kT + tid) * 16;
+    // This thread's chunks i .. i + kSame - 1 of run j, on their way.  (One group of
+    // copies for each part that is held, whether it has any or not.)
     auto fetch = [&](int i, int ids, int j) {
       const int left = s.t.ke - (s.t.kb + j * kC);  // positions from the run's start on
       const int t = KEYS ? t1 + i * kStep : 4 * (t1 + (i >> 2) * kStep);
@@ -161,15 +185,28 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 #pragma unroll
       for (int u = 0; u < kSame; ++u) {
         const int dt = KEYS ? u * kStep : u;
-        x[i + u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && t + dt < left) x[i + u] = __ldg(at + dt * kV);
+        const bool there = ok && t + dt < left;
+        if (i < kHeld) {
+          copy16(held + (i + u) * kT * 16, at + dt * kV, there);
+        } else {
+          x[i + u - kHeld] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (there) x[i + u - kHeld] = __ldg(at + dt * kV);
+        }
       }
+    };
+    auto chunk = [&](int i) {
+      return i < kHeld ? *reinterpret_cast<const float4*>(held + i * kT * 16) : x[i - kHeld];
     };
     int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
 
+#pragma unroll
+    for (int i = 0; i < kHeld; i += kSame) {
+      fetch(i, ids, s.j0);
+      copies_commit();
+    }
 
-    // The query rows: this thread's row, half of its dims, on their way all at once;
-    // then the first run takes their registers.
+    // The query rows: this thread's row, half of its dims, as many at a time as there
+    // are registers; then the first run takes them.
     const int r = (warp & 3) * 32 + lane, half = warp >> 2;
     const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
     const bool valid = tok < s.t.n_tok;
@@ -177,30 +214,33 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
                       (((size_t)s.t.q0 + (valid ? tok : 0)) * p.heads + s.head * p.group + g) * kV +
                       half * kN;
     static_assert(kN == kV / 2, "a thread's part of a query row");
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (valid) x[i] = __ldg(q + i);
-    }
-    if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
-    tc_fence_after();
     const uint32_t t_q = ((uint32_t)((warp & 3) * 32) << 16) + kColQ + half * (D / 2);
 #pragma unroll
-    for (int i = 0; i < kN; i += kSame) {
+    for (int b = 0; b < kN; b += kN - kHeld) {
+#pragma unroll
+      for (int i = 0; i < kN - kHeld; ++i) {
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid) x[i] = __ldg(q + b + i);
+      }
+      if (b == 0) {
+        if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
+        tc_fence_after();
+      }
       __syncwarp();
 #pragma unroll
-      for (int u = 0; u < kSame; u += 2) {
+      for (int i = 0; i < kN - kHeld; i += 2) {
         float lo[8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float4 h = hi4(x[i + u + k]), l = lo4(x[i + u + k], h);
-          *reinterpret_cast<float4*>(smem + operand_at(kR, r, half * kN + i + u + k)) = h;
+          const float4 h = hi4(x[i + k]), l = lo4(x[i + k], h);
+          *reinterpret_cast<float4*>(smem + operand_at(kR, r, half * kN + b + i + k)) = h;
           lo[4 * k] = l.x, lo[4 * k + 1] = l.y, lo[4 * k + 2] = l.z, lo[4 * k + 3] = l.w;
         }
-        tmem_st8(t_q + 4 * (i + u), lo);
+        tmem_st8(t_q + 4 * (b + i), lo);
       }
-      fetch(i, ids, s.j0);
     }
+#pragma unroll
+    for (int i = kHeld; i < kN; i += kSame) fetch(i, ids, s.j0);
     tmem_wait_st();
     tc_fence_before();
     fence_proxy_async_smem();
@@ -224,17 +264,18 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       const bool more = j + 1 < s.j1;
 #pragma unroll
       for (int i = 0; i < kN; i += kSame) {
+        if (i < kHeld) copies_wait<kHeld / kSame - 1>();  // all groups but the later parts'
         if (KEYS) {
 #pragma unroll
           for (int u = 0; u < kSame; ++u) {
             unsigned char* at = dst + operand_at(kC, t1 + (i + u) * kStep, v);
-            const float4 h = hi4(x[i + u]);
+            const float4 y = chunk(i + u), h = hi4(y);
             *reinterpret_cast<float4*>(at) = h;
-            *reinterpret_cast<float4*>(at + L::kKV) = lo4(x[i + u], h);
+            *reinterpret_cast<float4*>(at + L::kKV) = lo4(y, h);
           }
         } else {
           // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
-          const float4 a = x[i], b = x[i + 1], c = x[i + 2], d = x[i + 3];
+          const float4 a = chunk(i), b = chunk(i + 1), c = chunk(i + 2), d = chunk(i + 3);
           const float4 y[4] = {make_float4(a.x, b.x, c.x, d.x), make_float4(a.y, b.y, c.y, d.y),
                                make_float4(a.z, b.z, c.z, d.z), make_float4(a.w, b.w, c.w, d.w)};
 #pragma unroll
@@ -246,6 +287,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
           }
         }
         if (more) fetch(i, ids_next, j + 1);
+        if (i < kHeld) copies_commit();
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -292,16 +334,17 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
     umma_commit(B.scores(i & 1), true);
     return true;
   };
-  auto values = [&](uint32_t i, bool fresh) {
+  auto values = [&](uint32_t i) {
     const uint32_t st = i % L::kStages;
     const uint64_t dv = dv0 + st * 2 * kLow;
     if (!mbar_wait(B.vfull(st), (i / L::kStages) & 1)) return false;
     if (!mbar_wait(B.probs(i & 1), (i >> 1) & 1)) return false;
+    if (i && !mbar_wait(B.oread(), (i - 1) & 1)) return false;
     tc_fence_after();
     const uint32_t a = (i & 1) * 128;
 #pragma unroll
     for (int ks = 0; ks < kC / 8; ++ks)
-      umma_ts_tf32(kColO, a + kC + ks * 8, dv + step(D, ks), idesc_o, !fresh || ks > 0);
+      umma_ts_tf32(kColO, a + kC + ks * 8, dv + step(D, ks), idesc_o, ks > 0);
 #pragma unroll
     for (int ks = 0; ks < kC / 8; ++ks)
       umma_ts_tf32(kColO, a + ks * 8, dv + kLow + step(D, ks), idesc_o, true);
@@ -323,11 +366,8 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
         if (!scores(run + j + 1)) return false;
         if (j + 2 == n) umma_commit(B.qfree(), true);
       }
-      // before O is written again: the previous segment's has been read
-      if (j == 0 && nseg && !mbar_wait(B.ofree(), (nseg - 1) & 1)) return false;
-      if (j >= 0 && !values(run + j, j == 0)) return false;
+      if (j >= 0 && !values(run + j)) return false;
     }
-    umma_commit(B.out(), true);
     run += n;
     ++nseg;
   }
@@ -351,7 +391,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
   const int tok = (int)((unsigned)r / (unsigned)p.group), g = r - tok * p.group;
   volatile float2* s_max = reinterpret_cast<volatile float2*>(smem + L::kOffMax) + r;
   volatile float* s_sum = reinterpret_cast<volatile float*>(smem + L::kOffSum) + r;
-  uint32_t run = 0, nseg = 0, turn = 0;
+  uint32_t run = 0, turn = 0;
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kC>(p, s)) {
@@ -362,12 +402,39 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
                            : make_int2(0, 0x7fffffff);  // rows that are not there mask nothing
     const float slope = valid && p.slopes ? __ldg(p.slopes + s.head * p.group + g) : 0.f;
     float m = -INFINITY, l = 0.f;
+    float acc[4][D / 8];  // dims 4 v + e of this thread's half of the v
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) acc[e][k] = 0.f;
+    // Adds the products of run i, which O holds, once they are complete.
+    auto add_products = [&](uint32_t i) {
+      if (!warp_wait(B.vempty(i % L::kStages), (i / L::kStages) & 1)) return false;
+      if (any_valid) {
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float o[D / 8];
+#pragma unroll
+          for (int k = 0; k < D / 8; k += 8)
+            tmem_ld8(t_o + e * (D / 4) + hf * (D / 8) + k, o + k);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) acc[e][k] += o[k];
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.oread());
+      return true;
+    };
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
       const uint32_t t_s = t_lane + (run & 1) * 128 + hf * kH;
       const int t0 = s.t.kb + j * kC;
       if (!warp_wait(B.scores(run & 1), (run >> 1) & 1)) return kTimedOut;
       tc_fence_after();
+      float alpha = 1.f;
       if (any_valid) {
         float mul = p.scale;
         if (CAP) {
@@ -420,52 +487,42 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
           if (!pair_sync(bar, words)) return kPartnerFailed;
           mx = fmaxf(mx, hf ? s_max->x : s_max->y);
           const bool raise = valid && mx > m + kSlack;  // also the first finite one
-          float alpha = 1.f;
           if (raise) {
             alpha = ex2_approx(m - mx);
             m = mx;
             l *= alpha;
           }
-          if (j > s.j0 && __any_sync(kFull, raise)) {
-            // the products of the run before, which O is to hold, are complete
-            const uint32_t i = run - 1;
-            if (!warp_wait(B.vempty(i % L::kStages), (i / L::kStages) & 1)) return kTimedOut;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 8) {
-              float o[8];
-              tmem_ld8(t_o + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= alpha;
-              tmem_st8(t_o + c, o);
-            }
-          }
         }
         ++turn;
         const float sub = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int c = 0; c < kH; c += 16) {
-          float low[16];
+        for (int c = 0; c < kH; c += 8) {
+          float low[8];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < 8; ++k) {
             const float e = ex2_approx(x[c + k] - sub);
             l += e;
             x[c + k] = to_tf32(e);
             low[k] = e - x[c + k];
           }
-          tmem_st16(t_s + c, x + c);
-          tmem_st16(t_s + kC + c, low);
+          tmem_st8(t_s + c, x + c);
+          tmem_st8(t_s + kC + c, low);
         }
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(B.probs(run & 1));
+      // While the tensor core goes on: the run before, still at the old maximum.
+      if (j > s.j0 && !add_products(run - 1)) return kTimedOut;
+      if (__any_sync(kFull, alpha != 1.f)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) acc[e][k] *= alpha;
+      }
     }
-    // The segment's end: O is complete once its last product is.
-    if (!warp_wait(B.out(), nseg & 1)) return kTimedOut;
-    tc_fence_after();
+    if (!add_products(run - 1)) return kTimedOut;
     const bool whole = s.first && s.last;
     if (any_valid) {
       s_sum[hf * kR] = l;
@@ -475,30 +532,19 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       const int row = tok * p.group + g;  // within the tile
       const float w = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       float* out = chunk_out<float>(p, s.t.q0, s.head, row, D);
-#pragma unroll 1
-      for (int v = hf * (D / 8); v < (hf + 1) * (D / 8); v += 8) {
-        float o[4][8];
-        __syncwarp();
+      if (valid) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_ld8(t_o + e * (D / 4) + v, o[e]);
-        tmem_wait_ld();
-        if (valid) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *(whole ? reinterpret_cast<float4*>(out) + v + k : chunk_acc(p, slot, D, v + k, row)) =
-                make_float4(o[0][k] * w, o[1][k] * w, o[2][k] * w, o[3][k] * w);
+        for (int k = 0; k < D / 8; ++k) {
+          const int v = hf * (D / 8) + k;
+          *(whole ? reinterpret_cast<float4*>(out) + v : chunk_acc(p, slot, D, v, row)) =
+              make_float4(acc[0][k] * w, acc[1][k] * w, acc[2][k] * w, acc[3][k] * w);
         }
       }
       if (!whole && valid && hf == 0)
         p.ws_ml[(size_t)slot * p.tile_rows + row] = make_float2(m, l);
     }
-    tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(B.ofree());
-      if (!whole) mbar_arrive(B.piece(s.first));
-    }
-    ++nseg;
+    if (lane == 0 && !whole) mbar_arrive(B.piece(s.first));
   }
   return warp_wait(B.published(), 0) ? kDone : kTimedOut;
 }
@@ -527,8 +573,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
         mbar_init(B.scores(x), 1);
         mbar_init(B.probs(x), kSoftWarps);
       }
-      mbar_init(B.out(), 1);
-      mbar_init(B.ofree(), kSoftWarps);
+      mbar_init(B.oread(), kSoftWarps);
       mbar_init(B.piece(0), kSoftWarps);
       mbar_init(B.piece(1), kSoftWarps);
       mbar_init(B.published(), 1);
@@ -555,7 +600,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   if (odd) {
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
-    reg_dec<kSoftRegs>();
+    reg_inc<Regs<D>::kSoft>();
     volatile PairWords* words = s_pairs + (warp & 3);
     const int end = softmax<D, CAP>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
     // Every warp but one whose partner failed meets its partner once more: so a
@@ -568,7 +613,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
     }
     ok = end == kDone;
   } else if (warp < kSoftWarps + kLoadWarps) {
-    reg_inc<kLoadRegs>();
+    reg_dec<Regs<D>::kLoad>();
     ok = warp < kSoftWarps + kLoadWarps / 2
              ? load<D, true>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane)
              : load<D, false>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);

@@ -603,3 +603,19 @@ def test_random_batches(seed):
     if rng.random() < 0.3:
         kw["softcap"] = 20.0
     check(b, dtype, **kw)
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_long_sums_keep_their_precision(head_dim):
+    """fp32 with equal weights: the mean of 8192 values near 3.  A run of 64 goes
+    through 24 accumulating MMAs, which drop up to 2^-23 of the partial sum each, 2.9e-6
+    in all; the sum over runs is rounded to nearest, and 2^-20 is left for it."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([8192, 8000], [1, 2], 4, 4, head_dim, "f32", seed=27)
+    b["q"].zero_()
+    b["v"] += 3.0
+    out = torch.empty_like(b["q"])
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out)
+    ref, _ = reference(b)
+    assert ((out.double() - ref) / ref).abs().max() <= 24 * 2.0 ** -23 + 2.0 ** -20
