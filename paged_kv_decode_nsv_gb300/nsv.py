@@ -370,20 +370,23 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
-def _scratch(nbytes, workspace, stream, device):
-    """(tensor, pointer, bytes) of a call's workspace: the caller's, or one
-    from torch's allocator that belongs to the call's stream."""
+def _call(what, args, need, workspace, stream, device):
+    """Calls `what` of the library with a workspace: the caller's, or memory that
+    torch's caching allocator lends for the call on its stream.  (A raw allocation:
+    a tensor around it costs a call 5 us more.)"""
     import torch
-    if workspace is not None:
+    fn, raw = getattr(_lib, what), _raw_stream(stream, device)
+    if workspace is None:
+        ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, raw)
+        try:
+            rc = fn(*args, ptr, need, raw)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ptr)
+    else:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on the current CUDA device")
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if stream is None:
-        t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    else:
-        with torch.cuda.stream(stream):
-            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    return t, t.data_ptr(), nbytes
+        rc = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    _check(rc, what)
 
 
 def chunk_workspace_bytes(shape, tokens, num_sms=0):
@@ -437,9 +440,8 @@ def paged_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, sca
     shape, scores, T, ptrs, out_ptr, need, dev = _chunk_args(
         q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
         see_begin, see_end)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_paged_chunk(shape, scores, T, *ptrs, float(scale), out_ptr, ws_ptr, ws_bytes,
-                                _raw_stream(stream, dev)), "nsv_paged_chunk")
+    _call("nsv_paged_chunk", (shape, scores, T, *ptrs, float(scale), out_ptr),
+          need, workspace, stream, dev)
     return out
 
 
@@ -454,10 +456,8 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
     new = (T, k_pool.shape[1], q.shape[2])
     new_ptrs = (_arg(k_new, "k_new", q.dtype, new, dev), _arg(v_new, "v_new", q.dtype, new, dev),
                 _arg(write_slots, "write_slots", torch.int64, (T,), dev))
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_chunk_step(shape, scores, T, ptrs[0], *new_ptrs, *ptrs[1:], float(scale),
-                               out_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev)),
-           "nsv_chunk_step")
+    args = (shape, scores, T, ptrs[0], *new_ptrs, *ptrs[1:], float(scale), out_ptr)
+    _call("nsv_chunk_step", args, need, workspace, stream, dev)
     return out
 
 
@@ -523,9 +523,7 @@ def rows_fork(parents, children, block_tables, context_lens, block_refs, k_pool,
     pools = _pool_args(k_pool, v_pool, blocks, dev)
     shape, need = _pool_sizes(rows, width, k_pool)
     ids = _arg(parents, "parents", i32, (n,), dev), _arg(children, "children", i32, (n,), dev)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_rows_fork(shape, n, *ids, *cache, *pools, ws_ptr, ws_bytes,
-                              _raw_stream(stream, dev)), "nsv_rows_fork")
+    _call("nsv_rows_fork", (shape, n, *ids, *cache, *pools), need, workspace, stream, dev)
 
 
 def rows_extend(chunk_starts, block_tables, context_lens, block_refs, write_slots, workspace=None,
@@ -538,9 +536,7 @@ def rows_extend(chunk_starts, block_tables, context_lens, block_refs, write_slot
     starts = _arg(chunk_starts, "chunk_starts", torch.int32, (rows + 1,), dev)
     slots = _arg(write_slots, "write_slots", torch.int64, (T,), dev)
     shape, need = _page_sizes(rows, width, blocks, 1, 64, F32, 16)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_rows_extend(shape, T, starts, *cache, slots, ws_ptr, ws_bytes,
-                                _raw_stream(stream, dev)), "nsv_rows_extend")
+    _call("nsv_rows_extend", (shape, T, starts, *cache, slots), need, workspace, stream, dev)
     return write_slots
 
 
@@ -563,9 +559,7 @@ def blocks_compact(block_tables, context_lens, block_refs, k_pool, v_pool, works
     cache, rows, width, blocks = _cache_args(block_tables, context_lens, block_refs, dev)
     pools = _pool_args(k_pool, v_pool, blocks, dev)
     shape, need = _pool_sizes(rows, width, k_pool)
-    ws, ws_ptr, ws_bytes = _scratch(need, workspace, stream, dev)
-    _check(_lib.nsv_blocks_compact(shape, *cache, *pools, ws_ptr, ws_bytes,
-                                   _raw_stream(stream, dev)), "nsv_blocks_compact")
+    _call("nsv_blocks_compact", (shape, *cache, *pools), need, workspace, stream, dev)
 
 
 def selftest_bounded_wait(limit_ns, stream=None):

@@ -619,3 +619,43 @@ def test_long_sums_keep_their_precision(head_dim):
     nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out)
     ref, _ = reference(b)
     assert ((out.double() - ref) / ref).abs().max() <= 24 * 2.0 ** -23 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lent_workspaces(dtype):
+    """Without a workspace of the caller's: on another stream, and captured, where
+    eager calls and allocations between the replays must not meet the graph's."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    bs = [batch([2100, 64], [64, 3], 8, 2, 128, dtype, seed=s) for s in (28, 29)]
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    outs = [torch.zeros_like(b["q"]) for b in bs]
+
+    def run(b, o, **kw):
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o, **kw)
+
+    def right(b, o):
+        ref, big = reference(b)
+        return bool(((o.double() - ref).abs().amax(-1) <= tol * big).all())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for b, o in zip(bs, outs):
+        run(b, o, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(right(b, o) for b, o in zip(bs, outs))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(bs[0], outs[0])
+        run(bs[1], outs[1])
+    junk = []
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        junk.append(torch.full((1 << 20,), float("nan"), device="cuda"))
+        extra = torch.zeros_like(outs[0])
+        run(bs[0], extra)
+        torch.cuda.synchronize()
+        assert right(bs[0], extra) and all(right(b, o) for b, o in zip(bs, outs))
