@@ -5,15 +5,20 @@
 // numbers: x = hi + lo, hi rounded to tf32's 11 bits, and of lo = x - hi, which is
 // exact, the MMA takes the upper 11.  a b = a_hi b_hi + a_hi b_lo + a_lo b_hi: what
 // is left out, a_lo b_lo, is at most 2^-22 of the product, and what the MMA drops of
-// a lo 2^-21 of x.  Against 64 bits the outputs are off by 3.7e-7 (a plain fp32
-// computation: 2.2e-7).
+// a lo 2^-21 of x.
+//
+// The tensor core's accumulator does not round: it drops what the sum does not hold.
+// Left to it for a whole row, sums over 8192 positions came out 6e-6 to 2e-5 too small.
+// So each run's products start from zero, and the softmax threads add them up in
+// registers, rounded to nearest.  Against 64 bits the outputs are off by 2e-7 to 4e-7 (a
+// plain fp32 computation: 1.4e-7 to 6e-7), over 8192 positions by at most 2e-6 (5e-7).
 //
 // One CTA per SM, twenty warps (the last two idle):
 //   warps 0-7   softmax: MMA row r (TMEM lane r) belongs to two threads, in warps
 //               w and w + 4, which split its 64 scores and its output's columns
 //   warps 8-15  loaders, four for the keys, four for the values, all for the query
-//               rows: from global memory into registers, a run ahead; split, and
-//               stored as MMA operands
+//               rows: from global memory into registers (half of a run at head_dim 128
+//               into shared memory), a run ahead; split, and stored as MMA operands
 //   warp 16     MMA issue, one elected thread
 //   warp 17     publishes the pieces of cut tiles
 // The rows of an MMA are the tile's query tokens times the query heads that share
@@ -30,14 +35,14 @@
 // runs'.)  Scores of run j + 1 are issued before the products of run j's
 // probabilities, so that each softmax runs while the tensor core works.
 //
-// A run of 64 positions takes 2.5 us at head_dim 128 and 1.5 to 1.6 at 64 whatever the
+// A run of 64 positions takes 2.8 us at head_dim 128 and 1.5 to 1.6 at 64 whatever the
 // rows; its MMAs alone would take 1.7 and 0.9, its bytes 1.5 and 0.7.  Nothing is far
-// ahead: a third of the MMAs left out, the global loads, the split or the softmax, it
-// takes 2.1 to 2.3 (head_dim 128), because a buffer of keys holds one run, which is
-// stored after the scores before it are done and before the next can start.  638 tokens
-// over up to 2048 positions, 12 heads: 56 us.  The same split on mma.sync (64 rows, two
-// CTAs per SM), where every warp splits the keys and values again, took 162, and
-// multiply-adds on the CUDA cores 207.
+// ahead: without the global loads or the softmax it takes 2.6 (head_dim 128), because a
+// buffer of keys holds one run, which is stored after the scores before it are done and
+// before the next can start.  638 tokens over up to 2048 positions, 12 heads: 65 us (56
+// when the accumulator kept the sums).  The same split on mma.sync (64 rows, two CTAs per
+// SM), where every warp splits the keys and values again, took 162, and multiply-adds on
+// the CUDA cores 207.
 
 #include "chunk.cuh"
 
@@ -48,8 +53,9 @@ using namespace sm;
 
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kThreadsF32 = (kSoftWarps + kLoadWarps + 4) * 32;  // two warps are idle
-// Registers of a thread: at launch (what 640 threads get), and as the roles share them.
-// With 96 for all, the loaders spilled in their loop: 4.3 us a run instead of 2.7.
+// Registers of a thread: at launch (what 640 threads get), and as the roles share them
+// (with 96 for all, what spilled in the loops cost half as much again).  At head_dim 128
+// 112 and 88 or 104 and 96 are as fast as 120 and 80.
 constexpr int kRegs = 96, kOtherRegs = 80;
 template <int D>
 struct Regs {
