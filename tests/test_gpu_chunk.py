@@ -1,21 +1,19 @@
 """Attention of a chunk of new tokens over the paged cache (GPU), against the
 definition in 64 bits row by row.
 
-Tolerances, per (token, head), against the largest |v| that the token sees
-(every output is a convex combination of those values, with weights p / sum p):
+Tolerances, per (token, head), against `big`, the largest over the dims of
+|out| + sum p |v| (p: the softmax's weights; at most twice the largest |v|):
 
   fp32  Products of 128 terms with fp32 accumulation, the exponential, the
         running rescales and the sum each cost a few 2^-24 relative to the
         scores' size; scores here are below 16 in log2 units, so a weight is off
         by at most about 16 * 128 * 2^-24 = 1.2e-4 in the worst case and by
-        sqrt(128) in place of 128, 1.1e-5, as the terms' signs fall: 4e-5.
-  bf16  The output is rounded by half a step, at most 2^-8 of itself.  So is
-        each probability, which could add as much again, 2^-7 in all; but
-        these fall either way, and where few positions are seen, so that they
-        do not average out, the output is most of the largest |v| only if one
-        weight is near 1, whose own rounding cancels in p / sum p to the
-        others' share.  The tests allow the output's half step and 2^-12 for
-        everything else.
+        sqrt(128) in place of 128, 1.1e-5, as the terms' signs fall: 4e-5 of
+        sum p |v|.
+  bf16  The probabilities are rounded to bf16 by half a step, at most 2^-8 of
+        each, and their sum is taken before: together at most 2^-8 sum p |v|.
+        So is the output, at most 2^-8 of itself.  2^-12 is left for the scores'
+        fp32 arithmetic, the exponential unit and the products of these errors.
 """
 
 import math
@@ -64,7 +62,7 @@ def batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=0, pad=0, garbage=NAN
 
 
 def reference(b, softcap=0.0, slopes=None, see_begin=None, see_end=None):
-    """The definition in 64 bits, and the largest |v| that each token sees."""
+    """The definition in 64 bits, and what its tolerance goes by (see above)."""
     import torch
     q = b["q"].double()
     out = torch.zeros_like(q)
@@ -88,8 +86,9 @@ def reference(b, softcap=0.0, slopes=None, see_begin=None, see_end=None):
             if slopes is not None:
                 t = torch.arange(lo, hi, device="cuda", dtype=torch.float64)
                 s = s - slopes.double()[:, None] * (pos - t).abs()
-            out[at + i] = torch.einsum("ht,thd->hd", torch.softmax(s, -1), v)
-            big[at + i] = v.abs().amax((0, 2))
+            p = torch.softmax(s, -1)
+            out[at + i] = torch.einsum("ht,thd->hd", p, v)
+            big[at + i] = (out[at + i].abs() + torch.einsum("ht,thd->hd", p, v.abs())).amax(-1)
         at += n
     return out, big
 
