@@ -479,3 +479,43 @@ def test_extend_by_long_prompts(grow):
     c.same(got)
     assert np.array_equal(slots.cpu().numpy(), want)
     assert status() == 0
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_lives(seed):
+    """Random sequences of all operators on one cache, its pool nearly full."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    rng = np.random.default_rng(200 + seed)
+    rows = int(rng.choice([5, 40, 300]))
+    ctx = [int(x) if rng.random() < 0.6 else 0 for x in np.exp(rng.uniform(0, 6, rows))]
+    need = sum(-(-c // 16) for c in ctx)
+    c = Cache(ctx, need + int(rng.integers(1, rows + 4)), extra=int(rng.integers(0, 20)),
+              seed=seed, dtype=DTYPES[seed % 2])
+    got = c.gpu()
+    for _ in range(14):
+        kind = rng.choice(["extend", "extend", "fork", "free", "compact"])
+        if kind == "extend":
+            grow = np.where(rng.random(rows) < 0.5, 0, np.exp(rng.uniform(0, 5, rows)).astype(int))
+            starts = np.concatenate([[0], np.cumsum(grow)])
+            want = c.extend(starts, int(starts[-1]))
+            slots = torch.zeros(len(want), dtype=torch.int64, device="cuda")
+            nsv.rows_extend(ids(*starts), *got[:3], slots)
+            assert np.array_equal(slots.cpu().numpy(), want)
+        elif kind == "fork":
+            n = int(rng.integers(1, rows + 1))
+            parents, children = rng.integers(-1, rows, n), rng.integers(-1, rows, n)
+            c.fork(parents, children)
+            nsv.rows_fork(ids(*parents), ids(*children), *got)
+        elif kind == "free":
+            out = rng.integers(0, rows, int(rng.integers(1, rows // 3 + 2)))
+            c.free(out)
+            nsv.rows_free(ids(*out), *got[:3])
+        else:
+            c.compact()
+            nsv.blocks_compact(*got)
+            # what is free now may hold anything: the model takes it over
+            for mine, dev in ((c.k, got[3]), (c.v, got[4])):
+                mine[:-1][c.refs == 0] = dev.contiguous().view(len(dev), -1).view(
+                    torch.int32).cpu().numpy()[:-1][c.refs == 0]
+        c.same(got)
