@@ -217,12 +217,14 @@ struct ChunkWalk {
   }
 };
 
-// First position this row's query sees and one past the last, clipped to the
-// context; g: global index of the query token, pos its position.
+// First position this row's query sees and one past the last, at most the context,
+// and neither below 0 (the kernels subtract positions from them in 32 bits, which
+// bounds near INT_MIN would wrap); g: global index of the query token, pos its
+// position.
 __device__ __forceinline__ int2 chunk_sees(const ChunkParams& p, long long g, int pos, int ctx) {
   const int b = p.see_begin ? max(0, __ldg(p.see_begin + g)) : 0;
   const int e = min(p.see_end ? __ldg(p.see_end + g) : pos + 1, ctx);
-  return make_int2(b, e);
+  return make_int2(b, max(e, 0));
 }
 
 // Workspace slot of a cut tile's piece on CTA c: a CTA cuts at most the tile

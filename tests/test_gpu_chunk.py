@@ -658,3 +658,28 @@ def test_lent_workspaces(dtype):
         run(bs[0], extra)
         torch.cuda.synchronize()
         assert right(bs[0], extra) and all(right(b, o) for b, o in zip(bs, outs))
+
+
+INT_MIN, INT_MAX = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", ["both", "see_begin", "see_end"])
+@pytest.mark.parametrize("heads,kv_heads,head_dim", [(4, 2, 64), (6, 2, 128)])
+@pytest.mark.parametrize("ctx,new", [([700, 300, 40], [200, 1, 40]), ([1500], [3])])
+def test_extreme_bounds(dtype, which, heads, kv_heads, head_dim, ctx, new):
+    """Bounds at both ends of int32 ("sees nothing", "no bound"), in tiles whose other
+    tokens see several runs."""
+    import torch
+    b = batch(ctx, new, heads, kv_heads, head_dim, dtype, seed=31)
+    T = sum(new)
+    end = np.concatenate([np.arange(c - n, c) + 1 for c, n in zip(ctx, new)])
+    begin = np.maximum(end - 400, 0)
+    at = np.arange(T)
+    for step, lows, highs in ((3, end, begin), (7, begin, end)):
+        lows[at % step == 1] = INT_MIN + (at[at % step == 1] * 37) % 600
+        highs[at % (2 * step) == 2] = INT_MAX - at[at % (2 * step) == 2] % 5
+    kw = {"see_begin": begin, "see_end": end}
+    kw = {k: torch.from_numpy(v.astype(np.int32)).cuda() for k, v in kw.items()
+          if which in ("both", k)}
+    check(b, dtype, **kw)
