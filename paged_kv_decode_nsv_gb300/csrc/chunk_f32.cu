@@ -10,8 +10,11 @@
 // The tensor core's accumulator does not round: it drops what the sum does not hold.
 // Left to it for a whole row, sums over 8192 positions came out 6e-6 to 2e-5 too small.
 // So each run's products start from zero, and the softmax threads add them up in
-// registers, rounded to nearest.  Against 64 bits the outputs are off by 2e-7 to 4e-7 (a
-// plain fp32 computation: 1.4e-7 to 6e-7), over 8192 positions by at most 2e-6 (5e-7).
+// registers, rounded to nearest; the sum of the probabilities is compensated (it has more
+// terms, and equal ones round the same way each time).  Against 64 bits
+// the outputs are off by 2e-7 to 4e-7 (a plain fp32 computation: 1.4e-7 to 6e-7); means of
+// values near 3 with nearly equal weights, in rows that one CTA holds whole, by at most
+// 9e-7 over 8192 positions and 2.6e-6 over 131072.
 //
 // One CTA per SM, twenty warps (the last two idle):
 //   warps 0-7   softmax: MMA row r (TMEM lane r) belongs to two threads, in warps
@@ -407,7 +410,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
     const int2 see = valid ? chunk_sees(p, (long long)s.t.q0 + tok, pos, s.t.ctx)
                            : make_int2(0, 0x7fffffff);  // rows that are not there mask nothing
     const float slope = valid && p.slopes ? __ldg(p.slopes + s.head * p.group + g) : 0.f;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, lc = 0.f;  // lc: by how much l is too large
     float acc[4][D / 8];  // dims 4 v + e of this thread's half of the v
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -497,23 +500,30 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
             alpha = ex2_approx(m - mx);
             m = mx;
             l *= alpha;
+            lc *= alpha;
           }
         }
         ++turn;
         const float sub = m == -INFINITY ? 0.f : m;
+        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int c = 0; c < kH; c += 8) {
           float low[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float e = ex2_approx(x[c + k] - sub);
-            l += e;
+            (k & 1 ? l1 : l0) += e;
             x[c + k] = to_tf32(e);
             low[k] = e - x[c + k];
           }
           tmem_st8(t_s + c, x + c);
           tmem_st8(t_s + kC + c, low);
         }
+        // (Kahan's summation.  One by one, without it, a sum over 32768 positions was up
+        // to 1.7e-4 off; it costs single tokens at head_dim 128 1 %, chunks nothing.)
+        const float add = l0 + l1 - lc, sum = l + add;
+        lc = (sum - l) - add;
+        l = sum;
         tmem_wait_st();
       }
       tc_fence_before();

@@ -683,3 +683,33 @@ def test_extreme_bounds(dtype, which, heads, kv_heads, head_dim, ctx, new):
     kw = {k: torch.from_numpy(v.astype(np.int32)).cuda() for k, v in kw.items()
           if which in ("both", k)}
     check(b, dtype, **kw)
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("ctx", [8192, 32768])
+def test_sums_of_weights_keep_their_precision(head_dim, ctx):
+    """fp32, rows that one CTA holds whole, one key above equal others: the row's sum
+    adds the same weight over and over, and only the top key has a value, 1, so that
+    the output is 1 / sum.  Relative errors: a weight is 2^x with x (at most 6 in size)
+    rounded once and log2(e) as it is in fp32, 6 ln 2 (2^-24 + 1.4e-8) = 3.1e-7, and the
+    exponential unit 2^-22; up to 16 additions in a row within a run, 2^-20; the runs'
+    compensated sum, both threads', the quotient and the product, 6 x 2^-24.  Together
+    1.9e-6, below 2^-19."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    heads, rows = 8, torch.cuda.get_device_properties(0).multi_processor_count
+    steps = np.array([0.05, 0.3, 0.7, 1.15, 1.9, 2.6, 3.4, 5.3])
+    c = np.round(steps * math.log(2) * 4096) / 4096     # short enough for exact products
+    pools = [torch.zeros((ctx // 16 + 1, 1, 16, head_dim), device="cuda") for _ in range(2)]
+    pools[0][:, :, :, 0] = -1.0
+    pools[0][0, 0, 0, 0] = 0.0
+    pools[1][0, 0, 0] = 1.0
+    bt = torch.arange(ctx // 16, dtype=torch.int32, device="cuda").repeat(rows, 1)
+    q = torch.zeros((rows, heads, head_dim), device="cuda")
+    q[:, :, 0] = torch.from_numpy(c).float().cuda()
+    starts = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((rows,), ctx, dtype=torch.int32, device="cuda")
+    out = nsv.paged_chunk(q, *pools, bt, starts, lens, 1.0, torch.empty_like(q))
+    want = torch.from_numpy(1 / (1 + (ctx - 1) * np.exp(-c))).cuda()
+    err = (out.double() / want[None, :, None] - 1).abs().amax((0, 2))
+    assert (err <= 2.0 ** -19).all(), err
