@@ -306,9 +306,13 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B
 // cap * tanh(s * scale / cap) in log2 units for caps so large that the scores
 // stay near the tanh's linear part: z = s * scale / cap; below 1/4 the series
 // z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315) (relative error under 4e-7), above it
-// 1 - 2 / (1 + e^2z).  For smaller caps that second form alone is off by at most
-// cap * 1.7e-7, far below a bf16 probability's rounding.
-constexpr float kLargeCap = 4096.f;
+// 1 - 2 r, r = 1 / (1 + e^2z).  For smaller caps that second form alone will do: e^2z
+// is off by 2^-22 of itself, the sum by 2^-24 and the reciprocal by 2^-23, so a score by
+// at most cap * 3.7e-7 besides its own fp32 rounding.  At a cap of 256 that is 2^-13.4 of
+// a weight, twice that where the other score of a ratio is off the other way: below
+// 2^-12, and a probability's rounding to bf16 is up to 2^-8.  (256 single tokens over 512
+// to 8192 positions: the second form alone 559 us, the choice of both 563.)
+constexpr float kLargeCap = 256.f;
 __device__ __forceinline__ float large_cap(float s, float cap_z, float cap_out) {
   const float z = s * cap_z;
   const float big = 1.f - 2.f * rcp_approx(1.f + ex2_approx(z * 2.8853900817779268f));

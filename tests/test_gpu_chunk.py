@@ -713,3 +713,38 @@ def test_sums_of_weights_keep_their_precision(head_dim, ctx):
     want = torch.from_numpy(1 / (1 + (ctx - 1) * np.exp(-c))).cuda()
     err = (out.double() / want[None, :, None] - 1).abs().amax((0, 2))
     assert (err <= 2.0 ** -19).all(), err
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("softcap", [30.0, 200.0, 256.0, 257.0, 1000.0, 4096.0, 4097.0])
+def test_caps_on_both_sides_of_the_short_tanh(head_dim, softcap):
+    """bf16, 31 positions, of which the one with the highest score has the only values:
+    the output is v / sum, v all significands of bf16.  Its own rounding is all that may
+    be seen of bf16: everything else stays within 2^-12 of it."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    tokens, heads, ctx = 16, 8, 31
+    pools = [torch.zeros((3, 1, 16, head_dim), dtype=torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    pools[0][:2, :, :, 0] = 0.5
+    pools[0][0, 0, 7, 0] = 1.0
+    outs, wants = [], []
+    a = torch.from_numpy(np.linspace(0.25, 8.0, tokens * heads)).to(torch.bfloat16).cuda()
+    q = torch.zeros((tokens, heads, head_dim), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = a.view(tokens, heads)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for first in range(0, 128, head_dim):
+        v = 1 + torch.arange(first, first + head_dim, device="cuda").double() / 128
+        pools[1][0, 0, 7] = v.to(torch.bfloat16)
+        out = torch.empty_like(q)
+        nsv.paged_chunk(q, *pools, torch.tensor([[0, 1]], **i32), torch.tensor([0, tokens], **i32),
+                        torch.tensor([ctx], **i32), 1.0, out, softcap=softcap,
+                        see_end=torch.full((tokens,), ctx, **i32))
+        s = q[:, :, 0].double()
+        top, rest = (softcap * torch.tanh(x / softcap) for x in (s, s * 0.5))
+        outs.append(out)
+        wants.append(v / (1 + (ctx - 1) * torch.exp(rest - top))[..., None])
+    out, want = torch.cat(outs, -1), torch.cat(wants, -1)
+    low, high = ((want * (1 + x)).to(torch.bfloat16) for x in (-2.0 ** -12, 2.0 ** -12))
+    bad = (out < low) | (out > high)
+    assert not bad.any(), "%d of %d outside" % (int(bad.sum()), bad.numel())
