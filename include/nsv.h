@@ -578,7 +578,9 @@ NSV_API int nsv_rows_free(const nsv_shape *shape, int32_t count, const int32_t *
  * order, into the free ones below n, in order, so that the used blocks are [0, n)
  * and the pool's tail can be given back.  Table entries of all rows (within
  * their context lengths) and block_refs follow.  Contents of blocks that are
- * free afterwards are unspecified.
+ * free afterwards are unspecified.  An entry that names a block outside the pool, or
+ * a free one at or past n, stays and sets NSV_DEV_BAD_BLOCK; a row whose context
+ * length is outside its range stays and sets NSV_DEV_BAD_CTX.
  */
 NSV_API int nsv_blocks_compact(const nsv_shape *shape, int32_t *block_tables,
                                const int32_t *context_lens, int32_t *block_refs,

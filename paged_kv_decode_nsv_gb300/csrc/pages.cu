@@ -515,7 +515,6 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const PagePa
   const int32_t* movers = holes + p.num_blocks / 2 + 1;
   sm::griddep_wait();
   const int moves = __ldcg(p.ws + kMoves), live = __ldcg(p.ws + kLive);
-  if (moves == 0) return;
   // table entries, a warp per row
   for (long long r = w0; r < p.rows; r += warps) {
     const int c = __ldg(p.context_lens + r);
@@ -526,8 +525,8 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const PagePa
     int32_t* table = p.block_tables + (size_t)r * p.max_blocks;
     for (int b = lane; b < blocks_of(c); b += 32) {
       const int id = table[b];
-      if (id < live) continue;
-      const int k = id < p.num_blocks ? __ldcg(map + id) : -1;
+      if (id >= 0 && id < live) continue;
+      const int k = id >= 0 && id < p.num_blocks ? __ldcg(map + id) : -1;
       if (k >= 0)
         table[b] = __ldcg(holes + k);
       else

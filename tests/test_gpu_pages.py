@@ -519,3 +519,20 @@ def test_random_lives(seed):
                 mine[:-1][c.refs == 0] = dev.contiguous().view(len(dev), -1).view(
                     torch.int32).cpu().numpy()[:-1][c.refs == 0]
         c.same(got)
+
+
+@pytest.mark.parametrize("freed", [[0, 2, 9], []])      # blocks move; none does
+@pytest.mark.parametrize("bad", [-1, -7, -2 ** 31, 60, 61, 2 ** 31 - 1])
+def test_compact_flags_entries_outside_the_pool(freed, bad):
+    from paged_kv_decode_nsv_gb300 import nsv
+    c = Cache(CTX, 60, seed=12)
+    if not freed:       # the used blocks are the pool's first ones already
+        c.compact()
+    c.free(freed)
+    got = c.gpu()
+    c.compact()
+    got[0][6, 3] = bad
+    c.bt[6, 3] = bad
+    nsv.blocks_compact(*got)
+    c.same(got, free_too=False)
+    assert status() == nsv.DEV_BAD_BLOCK
