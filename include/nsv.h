@@ -117,8 +117,10 @@ enum {
     NSV_DEV_BAD_CHUNK = 16u,/* chunk starts that are not an ascending pair within
                                [0, tokens]; the row was read as having no new
                                tokens.  Also a chunk attention of more than
-                               2^31 runs of positions per SM (a quarter of an
-                               hour's work), which is not run */
+                               2^31 units of work per SM, which is not run and
+                               leaves `out` as it was: for bf16 about 2^29 runs
+                               of 128 positions (17 minutes), for fp32 2^31
+                               runs of 64 (an hour or more) */
     NSV_DEV_BAD_ROW = 32u,  /* a row id outside [0, rows), a fork into a row that
                                is not empty or was named before, or a row to
                                extend whose last, partly filled block is not its
