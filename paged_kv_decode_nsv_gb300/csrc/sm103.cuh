@@ -257,13 +257,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
         "f"(r[14]), "f"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(r) : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(r)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
