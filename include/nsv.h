@@ -439,9 +439,17 @@ NSV_API int nsv_paged_decode_slots(const nsv_shape *shape, const nsv_plan *plan,
  * never used and may hold anything, NaN included.  So may a key at a position
  * that a token does not see, as far as this token is concerned.  Values below the
  * context length must be finite, seen or not: a token weighs what it does not see
- * with 0, and 0 times NaN is NaN.  Blocks that no token of a chunk sees, such as
- * those that a sliding window has left, need not be there: their table entries
- * are not used.
+ * with 0, and 0 times NaN is NaN.  Blocks before the first position that any of a
+ * row's new tokens sees, such as those that a sliding window has left, and past the
+ * last one need not be there: their table entries are not used.  Those in between
+ * must be, seen or not.
+ *
+ * fp32 results are those of fp32 products, sums and scores.  bf16 inputs are
+ * multiplied exactly and summed in fp32; their softmax weights, up to 2^8 before the
+ * division, are rounded to bf16 for the product with the values, as in the tensor-core
+ * forms of the decode read, while their sum is not: up to 2^-8 of sum p |v| besides the
+ * output's own rounding.  Values are weighed before the division: a row's sum of them
+ * times 2^8 must stay within fp32's range.
  *
  * `scores` changes the score before the softmax, in this order:
  *   softcap > 0         s = softcap * tanh(scale * q.k / softcap)
@@ -637,10 +645,13 @@ NSV_API int nsv_status_async(uint32_t *dst, int clear, cudaStream_t stream);
 /* Static description of a return code. */
 NSV_API const char *nsv_strerror(int code);
 
-/* ABI version of this header (major * 100 + minor). */
+/* ABI version of the library, NSV_ABI_VERSION of the header it was built with
+ * (major * 100 + minor).  It changes when a struct's layout or an existing entry
+ * point does; entry points, structs and status bits that are only added leave it as
+ * it is, so a program that wants them of an older library looks the symbol up. */
 NSV_API int nsv_abi_version(void);
 
-#define NSV_ABI_VERSION 102 /* the layouts of nsv_shape and nsv_plan */
+#define NSV_ABI_VERSION 102
 
 #ifdef __cplusplus
 }

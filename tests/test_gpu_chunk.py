@@ -748,3 +748,28 @@ def test_caps_on_both_sides_of_the_short_tanh(head_dim, softcap):
     low, high = ((want * (1 + x)).to(torch.bfloat16) for x in (-2.0 ** -12, 2.0 ** -12))
     bad = (out < low) | (out > high)
     assert not bad.any(), "%d of %d outside" % (int(bad.sum()), bad.numel())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bounds_that_leave_a_gap(dtype):
+    """Tokens that see positions far apart, some of them from the middle of a block: what
+    lies before the first of them and past the last need not be there, nor be finite."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([1000, 900], [9, 30], 8, 2, 128, dtype, seed=32)
+    i = torch.arange(39, device="cuda", dtype=torch.int32)
+    kw = dict(see_begin=torch.where(i % 2 == 0, 165 + i, 700), see_end=torch.where(
+        i % 2 == 0, 181 + i, 733 + i))
+    ref, big = reference(b, **kw)
+    for r, c in enumerate((1000, 900)):
+        for blk in list(range(10)) + list(range(772 // 16 + 1, c // 16)):
+            for pool in (b["k"], b["v"]):
+                pool[int(b["bt"][r, blk])] = NAN
+            if blk % 2:
+                b["bt"][r, blk] = -5 - blk
+    nsv.device_status(clear=True)
+    out = torch.empty_like(b["q"])
+    nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], out, **kw)
+    assert nsv.device_status(clear=True)[0] == 0
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert ((out.double() - ref).abs().amax(-1) <= tol * big).all()
