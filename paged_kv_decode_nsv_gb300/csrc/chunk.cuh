@@ -14,9 +14,19 @@
 // both halves and 3 where it fills one (measured 1.9 and 1.45 us), and what a
 // tile costs besides its runs (its query rows, its output) as much as two runs,
 // before the first.  Counting runs alone, CTAs that got many short tiles ended
-// last: a 2048-token prompt took 73 us, with the tiles' own cost 56 (4 runs in
-// place of 2: 57).  An fp32 tile costs one run besides its own (638 tokens over up to
-// 2048 positions: none 58.3, one 56.2, two 56.7 us).
+// last.  No cost suits all mixes: prompts would have more, batches of single tokens
+// less.  Times in us at costs of 0, 1, 2 and 4 runs (fp32: 0, 1, 2 and 3):
+//   bf16  2048-token prompt, 32 heads over 8             73    -   56   57
+//         5000-token prompt, 12 heads over 4, D 128     117  107   96   94
+//         100 single tokens over 100 to 3000 positions  117  109  111  117
+//         64 x 5 tokens over 300 to 4000 positions      104  102  105  107
+//   fp32  2048-token prompt, 16 heads over 4, D 128     168  135  127  127
+//         5000-token prompt, 12 heads over 4, D 128     516  470  428  421
+//         638 tokens over up to 2048 positions           76   74   74   74
+//         the same causal and capped, D 64               86   82   90   90
+//         100 single tokens over 100 to 3000 positions  332  320  324  326
+//         26 x 3 tokens over 22 to 7988 positions         -  356  373    -
+// fp32 stays at one, because what prompts would gain by two other mixes would lose.
 #pragma once
 
 #include <cuda.h>
@@ -258,9 +268,11 @@ __device__ __forceinline__ T* chunk_out(const ChunkParams& p, int q0, int head, 
 // row) are few lines; where there are few rows the warps share their columns.
 // The pieces were just written by other SMs, a load is an L2 round trip (0.5 to
 // 1 us), and a round has the states of NS pieces and NG x NS of their columns in
-// flight: 8 loads of 16 bytes a thread, for as many columns of a piece as the warp has
-// (a 509-token chunk among 32 decodes: 121 us, four columns of two pieces 125, two of four
-// 129).
+// flight: 8 loads of 16 bytes a thread, for as many columns of a piece as the warp has.
+// With four columns of two pieces, or two of four, instead: a 509-token chunk among 32
+// decodes 125 and 129 us (121), a 5000-token prompt 97 and 102 (95), 1000 tokens over
+// 16000 positions 82 and 88 (80), fp32 336 and 326 (324), 100 single tokens in fp32 339 and
+// 319 (321); short prompts the same.
 template <typename T, int D, int NG, int NS>
 __device__ __forceinline__ void chunk_merge_cols(const ChunkParams& p, int c0, int n, int row,
                                                  bool valid, int g0, int step, int quad, T* out) {

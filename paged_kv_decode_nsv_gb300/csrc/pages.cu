@@ -274,9 +274,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
 // {parts before this row, its length before}
 //
 // PARTS: a warp takes 128 tokens of a row, else a whole row.  A warp alone took
-// 199 us for a row of 32768 new tokens, in parts they take 13; finding the parts
-// costs 2 us (128 rows of one new token each: 10.9 and 13.0 us).  So rows stay
-// whole where no row can have many more new tokens than one (kManyTokens).
+// 181 us for a row of 32768 new tokens, in parts they take 13; finding the parts
+// costs time with the number of rows (1024 rows of one new token each: 15 and 17 us,
+// 8192: 50 and 70).  The host knows how many tokens there are, not whose: rows stay whole
+// up to one each and kManyTokens more.  Where a few of very many rows bring all of those,
+// that is the wrong side (8192 rows, one with 8704 new tokens, the others none: 68 us, in
+// parts 23; 1024 rows, one with 1500: 19 and 13); with up to 256 rows the two are within
+// 2 us.
 constexpr int kPartTokens = 128, kManyTokens = 512;
 template <bool PARTS>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
