@@ -773,3 +773,91 @@ def test_bounds_that_leave_a_gap(dtype):
     assert nsv.device_status(clear=True)[0] == 0
     tol = F32_TOL if dtype == "f32" else BF16_TOL
     assert ((out.double() - ref).abs().amax(-1) <= tol * big).all()
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("kv_heads,group", [(1, 8), (2, 1)])
+def test_long_rows_of_one_cta_keep_their_precision(head_dim, kv_heads, group):
+    """fp32, equal weights and values near 3 over 65536 positions, rows that one CTA holds
+    whole: 1024 runs, whose sums are rounded to nearest, 2^-24 of the growing sum each,
+    2^-15 in all; within a run 24 accumulating MMAs may drop 2^-23 of it each; the sum of
+    the weights, the quotient and the product are off by a few 2^-24.  (Left to the tensor
+    core's accumulator, sums over 8192 positions lost 6e-6 to 2e-5.)"""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    ctx, rows = 65536, torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device="cuda").manual_seed(33)
+    pools = [torch.randn((ctx // 16 + 1, kv_heads, 16, head_dim), device="cuda", generator=g)
+             for _ in range(2)]
+    pools[1] += 3.0
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bt = torch.arange(ctx // 16, **i32).repeat(rows, 1)
+    q = torch.zeros((rows, kv_heads * group, head_dim), device="cuda")
+    starts, lens = torch.arange(rows + 1, **i32), torch.full((rows,), ctx, **i32)
+    out = nsv.paged_chunk(q, *pools, bt, starts, lens, 1.0, torch.empty_like(q))
+    v = pools[1][:-1].double()
+    ref = v.mean((0, 2)).repeat_interleave(group, 0)
+    big = v.abs().mean((0, 2)).repeat_interleave(group, 0)
+    assert ((out.double() - ref).abs() <= big * (2.0 ** -15 + 24 * 2.0 ** -23 + 2.0 ** -21)).all()
+
+
+def test_same_call_same_bits_fp32():
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = batch([3000, 700, 64], [40, 300, 1], 8, 2, 128, "f32", seed=10)
+    outs = [torch.empty_like(b["q"]) for _ in range(3)]
+    for o in outs:
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+def test_two_streams_and_two_graphs_fp32():
+    """Calls on two streams with a workspace each, then two graphs that share one."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    bs = [batch([2000, 64], [64, 3], 8, 2, 128, "f32", seed=s) for s in (34, 35)]
+    outs = [torch.empty_like(b["q"]) for b in bs]
+    shape = nsv.make_shape(2, 8, 2, 128, bs[0]["bt"].shape[1], bs[0]["k"].shape[0] - 1, nsv.F32)
+    ws = torch.empty(nsv.chunk_workspace_bytes(shape, 67), dtype=torch.uint8, device="cuda")
+
+    def run(b, o, **kw):
+        nsv.paged_chunk(b["q"], b["k"], b["v"], b["bt"], b["starts"], b["ctx"], b["scale"], o, **kw)
+
+    def right():
+        torch.cuda.synchronize()
+        for b, o in zip(bs, outs):
+            ref, big = reference(b)
+            assert ((o.double() - ref).abs().amax(-1) <= F32_TOL * big).all()
+
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, o, st in zip(bs, outs, streams):
+            run(b, o, stream=st)
+    right()
+    graphs = []
+    for b, o in zip(bs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(b, o, workspace=ws)
+        o.zero_()
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    right()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_exchanges_of_few_rows_before_full_tiles(seed):
+    """Tiles of one or a few tokens, whose rows lie two or four times over the MMA's, right
+    before tiles that fill both halves, over and over on each CTA."""
+    rng = np.random.default_rng(400 + seed)
+    group = [4, 16, 32, 5][seed % 4]
+    tile = 2 * (128 // group)
+    new, ctx = [], []
+    for _ in range(14):
+        for n in (int(rng.integers(1, max(2, tile // 4))), int(rng.integers(1, 3)),
+                  tile * int(rng.integers(1, 4)) + int(rng.integers(0, 2))):
+            new.append(n)
+            ctx.append(n + int(rng.integers(0, 300)))
+    check(batch(ctx, new, 4 * group, 4, [64, 128][seed // 4 % 2], "bf16", seed=seed, pad=1), "bf16")
