@@ -12,7 +12,7 @@
 // So each run's products start from zero, and the softmax threads add them up in
 // registers, rounded to nearest; the sum of the probabilities is compensated (it has more
 // terms, and equal ones round the same way each time).  Against 64 bits
-// the outputs are off by 2e-7 to 4e-7 (a plain fp32 computation: 1.4e-7 to 6e-7); means of
+// the outputs are off by 2e-7 to 6e-7 (a plain fp32 computation: 1.3e-7 to 9e-7); means of
 // values near 3 with nearly equal weights, in rows that one CTA holds whole, by at most
 // 9e-7 over 8192 positions and 2.6e-6 over 131072.
 //
