@@ -116,7 +116,9 @@ enum {
                                kernel returned early; results are invalid */
     NSV_DEV_BAD_CHUNK = 16u,/* chunk starts that are not an ascending pair within
                                [0, tokens]; the row was read as having no new
-                               tokens.  Also a chunk attention of more than
+                               tokens; where starts go back, rows whose tokens
+                               overlap may be left out as well.  Also a chunk
+                               attention of more than
                                2^31 units of work per SM, which is not run and
                                leaves `out` as it was: for bf16 about 2^29 runs
                                of 128 positions (17 minutes), for fp32 2^31

@@ -300,6 +300,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   warp_run(p.num_blocks, at.gw, &lo, &hi);
   const int mine = count_run(p.refs, lo, hi, at.lane, true);
   if (at.cta == 0) {
+    // Rows whose tokens overlap (starts that go back between them, flagged there) could
+    // have more parts than 32 bits count: those past what rows of their own tokens can
+    // have are refused.
+    const long long most = p.tokens / kPartTokens + p.rows;
     long long taken = 0, parts = 0;
     for (int base = 0; base < p.rows; base += kScanThreads) {
       const int r = base + at.tid;
@@ -331,19 +335,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
         }
       }
       long long total;
-      const long long upto = taken + cta_scan(need, at, s_scan, &total);
-      if (r < p.rows) __stcg(items + r, make_int2(ok ? clip(upto) : -1, n));
-      taken += total;
       if (PARTS) {
         const int own = ok ? (n - 1) / kPartTokens + 1 : 0;
         const long long before = parts + cta_scan(own, at, s_scan, &total) - own;
         if (r < p.rows) __stcg(grown + r, make_int2(clip(before), old));
         parts += total;
+        if (ok && before + own > most) {
+          flag(p, NSV_DEV_BAD_CHUNK);
+          ok = false;
+          need = 0;
+        }
       }
+      const long long upto = taken + cta_scan(need, at, s_scan, &total);
+      if (r < p.rows) __stcg(items + r, make_int2(ok ? clip(upto) : -1, n));
+      taken += total;
     }
     if (at.tid == 0) {
       __stcg(p.ws + kTotalNeed, clip(taken));
-      __stcg(p.ws + kParts, clip(parts));
+      __stcg(p.ws + kParts, (int)min(parts, most));
     }
     __syncthreads();
   }

@@ -536,3 +536,19 @@ def test_compact_flags_entries_outside_the_pool(freed, bad):
     nsv.blocks_compact(*got)
     c.same(got, free_too=False)
     assert status() == nsv.DEV_BAD_BLOCK
+
+
+def test_extend_refuses_rows_that_overlap_without_end():
+    """Starts that go back and forth: every other row claims all tokens.  The first is
+    extended; the others' parts would add up beyond what any batch of these tokens has."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    R, T = 64, 20000
+    c = Cache([5] * R, 100000, extra=1300, seed=13)
+    got = c.gpu()
+    want = c.extend([0] + [T] * R, T)
+    slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+    nsv.rows_extend(ids(*([0, T] * (R // 2) + [0])), *got[:3], slots)
+    c.same(got)
+    assert np.array_equal(slots.cpu().numpy(), want)
+    assert status() == nsv.DEV_BAD_CHUNK
