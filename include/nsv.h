@@ -85,14 +85,15 @@ extern "C" {
 #define NSV_API
 #endif
 
-/* Element types of q, out, pools and new K/V (one type for all of them). */
-enum { NSV_F32 = 0, NSV_BF16 = 1 };
+/* Element types of q, out, pools and new K/V (one type for all of them).  NSV_KV4
+ * is the type of a 4-bit pool (nsv_kv4_write), for the page operators alone. */
+enum { NSV_F32 = 0, NSV_BF16 = 1, NSV_KV4 = 4 };
 
 /* Return codes. */
 enum {
     NSV_OK = 0,
     NSV_ERR_NULLPTR = -1,     /* a required pointer is NULL */
-    NSV_ERR_DTYPE = -2,       /* dtype is not NSV_F32 or NSV_BF16 */
+    NSV_ERR_DTYPE = -2,       /* dtype is not one that the call takes */
     NSV_ERR_SHAPE = -3,       /* a size is out of its documented range */
     NSV_ERR_ALIGN = -4,       /* a data pointer is not 16-byte aligned */
     NSV_ERR_RANGE = -5,       /* a plan field is inconsistent with the shape */
@@ -127,8 +128,10 @@ enum {
                                is not empty or was named before, or a row to
                                extend whose last, partly filled block is not its
                                own alone; skipped */
-    NSV_DEV_NO_BLOCKS = 64u /* the pool has too few free blocks for a fork or an
+    NSV_DEV_NO_BLOCKS = 64u,/* the pool has too few free blocks for a fork or an
                                extension; that row was left as it was */
+    NSV_DEV_BAD_POS = 128u  /* a token's position that the rotation's table does not
+                               have; the token was not rotated or written */
 };
 
 /* Sizes of one decode batch.  Limits: 0 <= rows <= 8192; num_heads a
@@ -511,6 +514,114 @@ NSV_API int nsv_chunk_step(const nsv_shape *shape, const nsv_scores *scores, int
                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Appends that rotate on the way, and a cache held in 4 bits.
+ *
+ * Rotation: the first rotary_dim dimensions of every query and key head are taken in
+ * pairs (a, b), dimensions (i, i + rotary_dim / 2) or, interleaved, (2i, 2i + 1),
+ * i < rotary_dim / 2.  With the cosine c and sine s that the table has for the
+ * token's position and pair i, a pair becomes (a c - b s, b c + a s), in fp32 with
+ * every product and sum rounded (no fused multiply-add), so that the same inputs give
+ * the same bits everywhere.  The other dimensions stay as they are.
+ *
+ *   table      [num_positions][rotary_dim] fp32: rotary_dim / 2 cosines, then as many
+ *              sines (whatever scaling the angles have is in the table)
+ *   positions  [tokens] int32; a token whose position is outside [0, num_positions)
+ *              is skipped (no query, key or value of it is written) and sets
+ *              NSV_DEV_BAD_POS
+ *
+ * rotary_dim is a multiple of 16, at most head_dim.
+ */
+typedef struct nsv_rope {
+    const float *table;
+    const int32_t *positions;
+    int64_t num_positions;
+    int32_t rotary_dim;
+    int32_t interleaved;      /* 0 or 1 */
+} nsv_rope;
+
+/*
+ * Rotate a step's queries and keys, and append its keys and values: nsv_kv_write for
+ * keys that are not rotated yet.
+ *
+ *   q             [tokens][num_heads][head_dim], rotated into q_out (contiguous; it may
+ *                 be q itself where that is contiguous, and must not overlap it
+ *                 otherwise), or both NULL
+ *   k_new, v_new  [tokens][num_kv_heads][head_dim]
+ *   *_stride      elements from one token to the next, 0: contiguous.  (Slices of one
+ *                 projection's output have its width.)  A multiple of 16 bytes, below
+ *                 2^31, and no less than a token has
+ *   write_slots   [tokens] int64, rules as in nsv_kv_write (a padded token names the
+ *                 sink slot)
+ *
+ * Results are rounded once to the element type.  Uses num_heads (at most 2^20),
+ * num_kv_heads, head_dim, block_size, num_blocks and dtype of the shape (the rest must
+ * be valid).  0 <= tokens < 2^30.  Asynchronous, without workspace; may be captured.
+ */
+NSV_API int nsv_rope_write(const nsv_shape *shape, const nsv_rope *rope, int64_t tokens,
+                           const void *q, const void *k_new, const void *v_new,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const int64_t *write_slots, void *k_pool, void *v_pool,
+                           void *q_out, cudaStream_t stream);
+
+/*
+ * The same into 4-bit pools.  A pool is [num_blocks + 1][num_kv_heads] tiles of
+ * 9 * head_dim bytes: 16 tokens of head_dim / 2 bytes, each two e2m1 numbers (the even
+ * dimension in the low half), then 16 tokens of head_dim / 16 e4m3 scales, one for 16
+ * dimensions: 4.5 bits an element.  An element is
+ *   number * scale * k_scales[kv_head]   (v_scales for values; NULL: 1)
+ * A token's 16 dimensions x, as y = x / k_scales[kv_head], get the scale
+ * s = e4m3(max |y| / 6) and the numbers e2m1(y / s), zeros where s is 0; keys are
+ * taken from the fp32 rotation.  Quotients are rounded to fp32, conversions to nearest
+ * even, saturating (|y| beyond 2688 becomes that).  x must be finite, and k_scales and
+ * v_scales positive and finite: choose them so that y lies around 1, because a scale
+ * below 2^-6 has fewer digits and one below 2^-10 is 0.
+ *
+ * shape.dtype is the type of q, k_new, v_new and q_out.  rope NULL: nothing is rotated,
+ * and q and q_out must be NULL.  Everything else as in nsv_rope_write.
+ */
+NSV_API int nsv_kv4_write(const nsv_shape *shape, const nsv_rope *rope, const float *k_scales,
+                          const float *v_scales, int64_t tokens, const void *q,
+                          const void *k_new, const void *v_new, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, const int64_t *write_slots,
+                          void *k_pool, void *v_pool, void *q_out, cudaStream_t stream);
+
+/*
+ * Values of slots of 4-bit pools: k_out, v_out [tokens][num_kv_heads][head_dim] of
+ * shape.dtype, rounded to it from fp32.  A slot outside the pool leaves its token's
+ * output as it was and sets NSV_DEV_BAD_SLOT.  Slots may be named more than once.
+ * tokens * num_kv_heads < 2^34.
+ */
+NSV_API int nsv_kv4_read(const nsv_shape *shape, const float *k_scales, const float *v_scales,
+                         int64_t tokens, const int64_t *slots, const void *k_pool,
+                         const void *v_pool, void *k_out, void *v_out, cudaStream_t stream);
+
+/*
+ * nsv_paged_chunk over 4-bit pools: the same batch, scores, bounds and rules, with
+ * keys and values that are the pools' elements.  q and out are of shape.dtype.
+ *
+ * shape.query_len 0: rows bring any number of tokens.  Otherwise no row brings more
+ * than query_len (1 for a decode step), and the call takes the form that suits it; a
+ * row that brings more sets NSV_DEV_BAD_CHUNK and is read as having none.
+ *
+ * The pools' numbers times their scales are multiplied exactly.  bf16: weights are
+ * rounded to fp16 or bf16 for the product with the values, their sum is not: up to 2^-8
+ * of sum p |v| besides the output's own rounding.  fp32: queries and weights are off by
+ * 2^-22 of themselves, products are added in fp32.
+ *
+ * workspace: as in nsv_paged_chunk, of the bytes that nsv_kv4_workspace gives (for any
+ * query_len).
+ */
+NSV_API int nsv_kv4_workspace(const nsv_shape *shape, int64_t tokens, int num_sms,
+                              int64_t *bytes);
+
+NSV_API int nsv_kv4_chunk(const nsv_shape *shape, const nsv_scores *scores,
+                          const float *k_scales, const float *v_scales, int64_t tokens,
+                          const void *q, const void *k_pool, const void *v_pool,
+                          const int32_t *block_tables, const int32_t *chunk_starts,
+                          const int32_t *context_lens, float scale, void *out,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Page operators: the allocator of the paged cache, on the device.
  *
  * Its state is block_refs [num_blocks] int32, the number of block-table entries
@@ -523,7 +634,7 @@ NSV_API int nsv_chunk_step(const nsv_shape *shape, const nsv_scores *scores, int
  *
  * They use shape.rows, max_blocks, num_blocks, block_size, and, where blocks
  * are copied, num_kv_heads (a block of one pool is at most 256 MiB), head_dim and
- * dtype (the rest must be valid).  Without rows or items a call does nothing.
+ * dtype, NSV_KV4 for 4-bit pools (the rest must be valid).  Without rows or items a call does nothing.
  * Data pointers must be 16-byte aligned, index arrays to their element.
  * workspace: at least the bytes nsv_pages_workspace gives, 256-byte aligned,
  * owned by the caller, uninitialised; operators that overlap on the GPU need

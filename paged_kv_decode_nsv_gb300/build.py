@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libnsv.so")
 SOURCES = ["nsv_api.cu", "decode.cu", "kv_write.cu", "noalloc.cu", "chunk_api.cu",
-           "chunk_plan.cu", "chunk_bf16.cu", "chunk_f32.cu", "pages.cu", "pages_api.cu"]
+           "chunk_plan.cu", "chunk_bf16.cu", "chunk_f32.cu", "pages.cu", "pages_api.cu",
+           "rope_write.cu", "kv4_vec.cu", "kv4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

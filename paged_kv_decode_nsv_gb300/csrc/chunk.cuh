@@ -49,6 +49,20 @@ constexpr int kChunkKeysF32 = 64;
 // Costs (see above): of a bf16 tile in runs, of its runs in units.
 constexpr int kChunkTileCost = 2, kChunkPairUnits = 4, kChunkHalfUnits = 3;
 constexpr int kChunkTileCostF32 = 1;
+// Where there is a CTA for every tile and head, and no tile has more runs than
+// this, each CTA gets one whole, which saves publishing and merging the pieces of cut
+// tiles.  How many runs are worth that depends on how many CTAs would be left idle.
+// Single tokens of 4 heads per KV head, D 128, in us with the tiles cut and whole:
+//                        2 runs       4 runs       8 runs       16 runs
+//   bf16  128 tiles    26.6  20.5   28.7  24.6   36.9  32.8   53.2  49.2
+//         32 tiles     21.5  18.4   22.5  20.5   24.6  26.7   28.7  36.9
+//         1 tile       18.4  16.4   20.5  18.8   20.5  24.6   20.5  34.8
+//   fp32  128 tiles    36.9  26.6   41.0  32.8   53.2  45.1   75.8  69.6
+//         32 tiles     26.6  24.6   30.7  30.7   30.7  43.0   36.9  65.5
+//         1 tile       26.6  24.6   26.6  30.7   26.6  41.0   26.7  61.5
+// Eight takes what many tiles gain (up to 8 us) and costs few long ones about as much in
+// bf16 (4 us) and more in fp32 (14 us at 8 runs).
+constexpr int kChunkWholeRuns = 8;
 
 // Query tokens one tile holds.
 __host__ __device__ constexpr int chunk_tile_tokens(int dtype, int group) {
@@ -117,6 +131,9 @@ struct ChunkParams {
   int rows, heads, kv_heads, group, max_blocks;
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
   int grid;         // CTAs of the attention kernel
+  int n_min, n_max; // rows that bring fewer or more tokens have no tiles
+  bool flag_above;  // more than n_max is an error (NSV_DEV_BAD_CHUNK)
+  int whole_runs;   // where there is a CTA for each tile, the most runs of a whole one
   int tile_cost;    // a tile's own cost, in runs
   int pair_units, half_units;  // units of a run of a tile that fills both halves, or one
   float qscale;     // scale * log2(e)

@@ -15,21 +15,6 @@ namespace nsv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-// Where there is a CTA for every tile and head, and no tile has more runs than
-// this, each CTA gets one whole, which saves publishing and merging the pieces of cut
-// tiles.  How many runs are worth that depends on how many CTAs would be left idle.
-// Single tokens of 4 heads per KV head, D 128, in us with the tiles cut and whole:
-//                        2 runs       4 runs       8 runs       16 runs
-//   bf16  128 tiles    26.6  20.5   28.7  24.6   36.9  32.8   53.2  49.2
-//         32 tiles     21.5  18.4   22.5  20.5   24.6  26.7   28.7  36.9
-//         1 tile       18.4  16.4   20.5  18.8   20.5  24.6   20.5  34.8
-//   fp32  128 tiles    36.9  26.6   41.0  32.8   53.2  45.1   75.8  69.6
-//         32 tiles     26.6  24.6   30.7  30.7   30.7  43.0   36.9  65.5
-//         1 tile       26.6  24.6   26.6  30.7   26.6  41.0   26.7  61.5
-// Eight takes what many tiles gain (up to 8 us) and costs few long ones about as much in
-// bf16 (4 us) and more in fp32 (14 us at 8 runs).
-constexpr int kWholeRuns = 8;
-
 // Inclusive sum over the block's threads; *total is the block's.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
                                                 long long* total) {
@@ -67,6 +52,10 @@ __device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool 
   if (a < 0 || b < a || b > p.tokens) {
     c.n = 0;
     if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+  }
+  if (c.n < p.n_min || c.n > p.n_max) {
+    if (flag && p.flag_above && c.n > p.n_max) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+    c.n = 0;
   }
   if (c.ctx < 0 || (long long)c.ctx > (long long)p.max_blocks * kBlock) {
     c.ctx = 0;
@@ -191,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // on one side of a tile to the tile's edge saved pieces to merge, but the uneven
   // shares cost more: a 2048-token prompt 58 us instead of 56.)
   __syncthreads();
-  const bool whole = !__syncthreads_or(longest > kWholeRuns) &&
+  const bool whole = !__syncthreads_or(longest > p.whole_runs) &&
                      (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
   const int run = p.pair_units;

@@ -1,0 +1,331 @@
+// Host side of the rotating appends and of the 4-bit cache: argument checks,
+// workspace layout, launches.
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "kv4.cuh"
+
+namespace nsv {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Null and alignment checks of one call's arguments.
+struct Args {
+  bool null = false, misaligned = false;
+  void need(const void* p, uintptr_t a) {
+    null |= !p;
+    misaligned |= !aligned(p, a);
+  }
+  void may(const void* p, uintptr_t a) { misaligned |= !aligned(p, a); }
+  int code() const { return null ? NSV_ERR_NULLPTR : misaligned ? NSV_ERR_ALIGN : NSV_OK; }
+};
+
+int check_tokens(const nsv_shape* s, int64_t tokens) {
+  const int rc = check_shape(s);
+  if (rc) return rc;
+  return tokens < 0 || tokens >= kMaxTokens ? NSV_ERR_SHAPE : NSV_OK;
+}
+
+// A token's stride in elements: 0 stands for `heads` contiguous heads.  False for one
+// that lets tokens overlap or takes their vectors off 16 bytes.
+bool stride_of(const nsv_shape* s, int64_t given, int heads, long long* stride) {
+  const int64_t least = (int64_t)heads * s->head_dim;
+  *stride = given ? given : least;
+  return *stride >= least && *stride % (s->dtype == NSV_F32 ? 4 : 8) == 0 &&
+         *stride < (int64_t(1) << 31);
+}
+
+// Checks of an append's arguments; on NSV_OK `p` holds its parameters.  `nothing`:
+// there is nothing to do.
+int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, const void* q,
+                  const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
+                  int64_t v_stride, const int64_t* write_slots, void* k_pool, void* v_pool,
+                  void* q_out, bool rope_needed, RopeParams* p, bool* nothing) {
+  int rc = check_tokens(s, tokens);
+  if (rc) return rc;
+  memset(p, 0, sizeof *p);
+  *nothing = tokens == 0;
+  if (*nothing) return NSV_OK;
+  Args a;
+  a.need(k_new, 16), a.need(v_new, 16), a.need(write_slots, 8);
+  a.need(k_pool, 16), a.need(v_pool, 16);
+  if (rope) {
+    a.need(rope->positions, 4), a.need(rope->table, 16);
+  } else if (rope_needed) {
+    return NSV_ERR_NULLPTR;
+  }
+  if (q || q_out) a.need(q, 16), a.need(q_out, 16);
+  if ((rc = a.code()) != NSV_OK) return rc;
+  if (q && !rope) return NSV_ERR_RANGE;  // queries are only ever rotated
+  if (rope && (rope->rotary_dim < 16 || rope->rotary_dim > s->head_dim ||
+               rope->rotary_dim % 16 != 0 || rope->num_positions < 1 ||
+               (rope->interleaved != 0 && rope->interleaved != 1)))
+    return NSV_ERR_RANGE;
+  if (!stride_of(s, q_stride, s->num_heads, &p->q_stride) ||
+      !stride_of(s, k_stride, s->num_kv_heads, &p->k_stride) ||
+      !stride_of(s, v_stride, s->num_kv_heads, &p->v_stride))
+    return NSV_ERR_SHAPE;
+  // a token's units and their products stay within 32 bits
+  if (s->num_heads > (1 << 20)) return NSV_ERR_SHAPE;
+  DeviceInfo d;
+  if ((rc = device_info(&d)) != NSV_OK) return rc;
+  p->q = q;
+  p->k = k_new;
+  p->v = v_new;
+  if (rope) {
+    p->positions = rope->positions;
+    p->rotary = rope->table;
+    p->num_positions = rope->num_positions;
+    p->rotary_dim = rope->rotary_dim;
+    p->interleaved = rope->interleaved;
+  }
+  p->write_slots = write_slots;
+  p->q_out = q_out;
+  p->k_pool = k_pool;
+  p->v_pool = v_pool;
+  p->status = d.status;
+  p->tokens = tokens;
+  p->pool_slots = (s->num_blocks + 1) * (long long)s->block_size;
+  p->heads = s->num_heads;
+  p->kv_heads = s->num_kv_heads;
+  return NSV_OK;
+}
+
+// ------------------------------------------------------------------ attention
+
+// How the vector form takes a shape: column tiles of 8 query vectors, the tokens of a
+// tile, the parts that a KV head's query heads are taken in, and its workers.
+struct VecForm {
+  int col_tiles, tile_tokens, subs, heads_per_worker, workers_per_cta, workers;
+};
+
+VecForm vec_form(const nsv_shape* s, int col_tiles, int num_sms) {
+  VecForm f;
+  const int group = s->num_heads / s->num_kv_heads;
+  f.col_tiles = col_tiles;
+  const int vecs = 8 * col_tiles;
+  f.subs = (group + vecs - 1) / vecs;
+  f.tile_tokens = std::max(1, vecs / group);
+  if (s->query_len > 0) f.tile_tokens = std::min(f.tile_tokens, (int)s->query_len);
+  const int warps = kv4_vec_warps(s->dtype, col_tiles);
+  f.heads_per_worker = 1;
+  for (int h = 2; h <= warps; ++h)
+    if (s->num_kv_heads % h == 0) f.heads_per_worker = h;
+  f.workers_per_cta = warps / f.heads_per_worker;
+  f.workers = num_sms * kv4_vec_ctas_per_sm(s->dtype, col_tiles) * f.workers_per_cta;
+  return f;
+}
+
+// fp32 takes one column tile (its operands are two parts each).  bf16 takes two where
+// rows bring more than 8 query vectors.
+int col_tiles_for(const nsv_shape* s, int64_t tokens) {
+  if (s->dtype == NSV_F32) return 1;
+  const int64_t group = s->num_heads / s->num_kv_heads;
+  const int64_t new_tokens =
+      s->query_len > 0 ? s->query_len : tokens <= s->rows ? 1 : kVecKeys;
+  return group * new_tokens <= 8 ? 1 : 2;
+}
+
+struct VecWs {
+  uint64_t off_prefix, off_tiles, off_cta, off_cnt, off_todo, off_ml, off_acc, total;
+  int max_tiles;
+};
+
+VecWs vec_ws(const nsv_shape* s, const VecForm& f, int64_t tokens) {
+  auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
+  VecWs W;
+  W.max_tiles = (int)(s->rows + tokens / f.tile_tokens);
+  const uint64_t groups = (uint64_t)s->num_kv_heads / f.heads_per_worker * f.subs;
+  const uint64_t states = (uint64_t)f.workers * 2 * f.heads_per_worker * 8 * f.col_tiles;
+  W.off_prefix = 256;
+  W.off_tiles = W.off_prefix + up((uint64_t)(W.max_tiles + 1) * 8);
+  W.off_cta = W.off_tiles + up((uint64_t)W.max_tiles * 32);
+  W.off_cnt = W.off_cta + up((uint64_t)f.workers * 24);
+  W.off_todo = W.off_cnt + up((uint64_t)W.max_tiles * groups * 4);
+  W.off_ml = W.off_todo + up((uint64_t)f.workers * 16);
+  W.off_acc = W.off_ml + up(states * 8);
+  W.total = W.off_acc + states * s->head_dim * 4;
+  return W;
+}
+
+// A larger batch's workspace serves a smaller one, whichever form that takes.
+uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
+  nsv_shape any = *s;
+  any.query_len = 0;
+  uint64_t most = 0;
+  for (int ct = 1; ct <= (s->dtype == NSV_F32 ? 1 : 2); ++ct) {
+    nsv_shape one = any;
+    one.query_len = 1;  // tiles of a single token: the longest list
+    most = std::max({most, vec_ws(&any, vec_form(&any, ct, num_sms), tokens).total,
+                     vec_ws(&one, vec_form(&one, ct, num_sms), tokens).total});
+  }
+  return most;
+}
+
+}  // namespace
+}  // namespace nsv
+
+using namespace nsv;
+
+extern "C" {
+
+NSV_API int nsv_rope_write(const nsv_shape* shape, const nsv_rope* rope, int64_t tokens,
+                           const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int64_t* write_slots,
+                           void* k_pool, void* v_pool, void* q_out, cudaStream_t stream) {
+  RopeParams p;
+  bool nothing;
+  const int rc = append_params(shape, rope, tokens, q, k_new, v_new, q_stride, k_stride, v_stride,
+                               write_slots, k_pool, v_pool, q_out, true, &p, &nothing);
+  if (rc || nothing) return rc;
+  return launch_rope_write(p, shape->dtype, shape->head_dim, stream) == cudaSuccess ? NSV_OK
+                                                                                     : cuda_fail();
+}
+
+NSV_API int nsv_kv4_write(const nsv_shape* shape, const nsv_rope* rope, const float* k_scales,
+                          const float* v_scales, int64_t tokens, const void* q, const void* k_new,
+                          const void* v_new, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          const int64_t* write_slots, void* k_pool, void* v_pool, void* q_out,
+                          cudaStream_t stream) {
+  RopeParams p;
+  bool nothing;
+  const int rc = append_params(shape, rope, tokens, q, k_new, v_new, q_stride, k_stride, v_stride,
+                               write_slots, k_pool, v_pool, q_out, false, &p, &nothing);
+  if (rc || nothing) return rc;
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return NSV_ERR_ALIGN;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  return launch_kv4_write(p, shape->dtype, shape->head_dim, stream) == cudaSuccess ? NSV_OK
+                                                                                    : cuda_fail();
+}
+
+NSV_API int nsv_kv4_read(const nsv_shape* shape, const float* k_scales, const float* v_scales,
+                         int64_t tokens, const int64_t* slots, const void* k_pool,
+                         const void* v_pool, void* k_out, void* v_out, cudaStream_t stream) {
+  int rc = check_tokens(shape, tokens);
+  if (rc) return rc;
+  if (tokens == 0) return NSV_OK;
+  Args a;
+  a.need(slots, 8), a.need(k_pool, 16), a.need(v_pool, 16), a.need(k_out, 16), a.need(v_out, 16);
+  a.may(k_scales, 4), a.may(v_scales, 4);
+  if ((rc = a.code()) != NSV_OK) return rc;
+  // (one thread for eight dimensions; a grid holds 2^31 - 1 CTAs)
+  if ((tokens * (int64_t)shape->num_kv_heads) >= (int64_t(1) << 34)) return NSV_ERR_SHAPE;
+  DeviceInfo d;
+  if ((rc = device_info(&d)) != NSV_OK) return rc;
+  Kv4ReadParams p;
+  p.slots = slots;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.status = d.status;
+  p.tokens = tokens;
+  p.pool_slots = (shape->num_blocks + 1) * (long long)shape->block_size;
+  p.kv_heads = shape->num_kv_heads;
+  return launch_kv4_read(p, shape->dtype, shape->head_dim, stream) == cudaSuccess ? NSV_OK
+                                                                                   : cuda_fail();
+}
+
+NSV_API int nsv_kv4_workspace(const nsv_shape* shape, int64_t tokens, int num_sms,
+                              int64_t* bytes) {
+  if (!bytes) return NSV_ERR_NULLPTR;
+  int rc = check_tokens(shape, tokens);
+  if (rc) return rc;
+  if (num_sms <= 0) {
+    DeviceInfo d;
+    if ((rc = device_info(&d)) != NSV_OK) return rc;
+    num_sms = d.num_sms;
+  }
+  *bytes = (int64_t)chunk4_ws_bytes(shape, tokens, num_sms);
+  return NSV_OK;
+}
+
+NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float* k_scales,
+                          const float* v_scales, int64_t tokens, const void* q, const void* k_pool,
+                          const void* v_pool, const int32_t* block_tables,
+                          const int32_t* chunk_starts, const int32_t* context_lens, float scale,
+                          void* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_tokens(s, tokens);
+  if (rc) return rc;
+  if (s->rows == 0 || tokens == 0) return NSV_OK;
+  Args a;
+  a.need(q, 16), a.need(k_pool, 16), a.need(v_pool, 16), a.need(block_tables, 4);
+  a.need(chunk_starts, 4), a.need(context_lens, 4), a.need(out, 16);
+  a.may(k_scales, 4), a.may(v_scales, 4);
+  if (sc) a.may(sc->slopes, 4), a.may(sc->see_begin, 4), a.may(sc->see_end, 4);
+  if ((rc = a.code()) != NSV_OK) return rc;
+  if (sc && sc->softcap != 0.f && !(sc->softcap >= 1e-6f && sc->softcap <= 1e6f))
+    return NSV_ERR_RANGE;
+  DeviceInfo d;
+  if ((rc = device_info(&d)) != NSV_OK) return rc;
+  if (!ws || ws_bytes < chunk4_ws_bytes(s, tokens, d.num_sms) || !aligned(ws, 256))
+    return NSV_ERR_WORKSPACE;
+  const VecForm f = vec_form(s, col_tiles_for(s, tokens), d.num_sms);
+  const VecWs W = vec_ws(s, f, tokens);
+  char* b = static_cast<char*>(ws);
+  Kv4VecParams p;
+  memset(&p, 0, sizeof p);
+  ChunkParams& c = p.c;
+  c.q = q;
+  c.block_tables = block_tables;
+  c.chunk_starts = chunk_starts;
+  c.context_lens = context_lens;
+  c.slopes = sc ? sc->slopes : nullptr;
+  c.see_begin = sc ? sc->see_begin : nullptr;
+  c.see_end = sc ? sc->see_end : nullptr;
+  c.out = out;
+  c.ws_head = reinterpret_cast<long long*>(b);
+  c.ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
+  c.ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
+  c.ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
+  c.ws_first = reinterpret_cast<long long*>(c.ws_cta + f.workers);
+  c.ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
+  c.status = d.status;
+  c.pool_blocks = s->num_blocks + 1;
+  c.tokens = tokens;
+  c.rows = s->rows;
+  c.heads = s->num_heads;
+  c.kv_heads = s->num_kv_heads / f.heads_per_worker * f.subs;
+  c.group = s->num_heads / s->num_kv_heads;
+  c.max_blocks = s->max_blocks;
+  c.max_tiles = W.max_tiles;
+  c.tile_tokens = f.tile_tokens;
+  c.keys = kVecKeys;
+  c.grid = f.workers;
+  c.n_min = 0;
+  c.n_max = s->query_len > 0 ? s->query_len : 0x7fffffff;
+  c.flag_above = s->query_len > 0;
+  c.whole_runs = kVecWholeRuns;
+  c.tile_cost = kVecTileCost;
+  c.pair_units = c.half_units = 1;
+  c.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
+  c.scale = scale;
+  c.cap = sc ? sc->softcap : 0.f;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.todo = reinterpret_cast<int4*>(b + W.off_todo);
+  p.ml = reinterpret_cast<float2*>(b + W.off_ml);
+  p.acc = reinterpret_cast<float*>(b + W.off_acc);
+  p.kv_heads = s->num_kv_heads;
+  p.heads_per_worker = f.heads_per_worker;
+  p.workers_per_cta = f.workers_per_cta;
+  p.subs = f.subs;
+  if (launch_chunk_plan(c, stream) != cudaSuccess) return cuda_fail();
+  return launch_kv4_vec(p, s->dtype, s->head_dim, f.col_tiles, stream) == cudaSuccess
+             ? NSV_OK
+             : cuda_fail();
+}
+
+}  // extern "C"

@@ -1,0 +1,825 @@
+// Attention over a paged 4-bit cache, for tiles of few query vectors (single
+// tokens, a few guessed ones): the form that HBM bounds.
+//
+// For query vector i (a query token and head) of a tile and the positions t it sees:
+//   x_t = scale * log2(e) * q_i . k_t   (capped and biased as in chunk_bf16.cu)
+//   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m)
+// folded 32 positions at a time with a running maximum m and sum (fp32, of the
+// unrounded weights).
+//
+// A warp works alone: it takes its own share of the units (chunk.cuh; 32 positions,
+// two blocks), copies their tiles into its own ring in shared memory by bulk copies,
+// and needs no other warp until the end.  heads_per_worker warps, one per KV head,
+// share the same rows and positions, so that the tiles of a block, which lie one
+// after the other, are read at about the same time.
+//
+// Both products run on mma.sync m16n8k16 in fp16 with the cache's side as the 16
+// rows and up to 8 query vectors as the columns: the cache's numbers times their
+// scales are exact in fp16, and widening them takes most of the instructions, so that
+// each is widened once for all vectors.  (tcgen05 would want the widened operands in
+// shared memory, written and read again; the vectors are far too few to fill its rows.)
+//   scores: rows are tokens, a lane's k indices are dimensions that lie together in
+//           its 16 bytes; the query vectors are laid out the same way.
+//   output: rows are dimensions, k indices are tokens; the weights change from
+//           accumulators to operands by movmatrix.
+// MMA row r of the scores and k index r of the output stand for token
+// r ^ ((r >> 1) & 1) of a block, which halves the bank conflicts of the values' loads.
+//
+// Rounding: query vectors are scaled by a power of two to [2^14, 2^15) and are exact in
+// fp16 but for elements below 2^-28 of their vector's largest; fp32 ones are the sum of
+// two fp16 numbers (2^-23).  Weights are scaled by 2^kUp to at most 2^15, then
+// rounded to fp16 (2^-11, where the output's rounding to bf16 is 2^-8), for fp32 to the
+// sum of two fp16 numbers (2^-23).
+//
+// A tile cut between workers leaves partial states; kv4_merge_kernel joins them in the
+// order of their positions.  Waits are bounded; one that gives up sets
+// NSV_DEV_TIMEOUT and its warp ends once its own copies have landed.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "kv4.cuh"
+
+namespace nsv {
+namespace {
+
+using namespace sm;
+
+constexpr int kWarps = 8;     // of a CTA, at most
+constexpr int kStages = 3;    // of a warp's ring
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+struct Round;
+// The running maximum is raised when a score exceeds it by more than kSlack (log2
+// units); weights are held times 2^kUp.
+template <>
+struct Round<__nv_bfloat16> {
+  static constexpr int kParts = 1;
+  static constexpr float kSlack = 8.f, kUp = 7.f;
+};
+template <>
+struct Round<float> {
+  static constexpr int kParts = 2;
+  static constexpr float kSlack = 1.f, kUp = 14.f;
+};
+
+template <int D>
+struct Ring {
+  static constexpr uint32_t kTile = kv4_tile_bytes(D);
+  static constexpr uint32_t kStage = 4 * kTile;  // keys of two blocks, values of two blocks
+  static constexpr uint32_t kWarp = kStages * kStage;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t both(uint32_t h, bool upper) {
+  return __byte_perm(h, 0, upper ? 0x3232 : 0x1010);
+}
+
+// A share's walk, its next units and where their tiles are: the cursor that copies
+// run ahead with.
+struct Feed {
+  ChunkWalk wk;
+  ChunkSegment s;
+  const int32_t* table;
+  int j, ids, ids_from;  // next unit; lane's block id of the 32 blocks from ids_from on
+  bool more;
+  __device__ __forceinline__ void open(const Kv4VecParams& p) {
+    more = wk.next<kVecKeys>(p.c, s);
+    if (!more) return;
+    j = s.j0;
+    table = p.c.block_tables + (size_t)s.t.row * p.c.max_blocks;
+    ids_from = -0x40000000;
+  }
+};
+
+template <typename T, int D, int NT, bool CAP, bool BIAS>
+struct Worker {
+  static constexpr int kParts = Round<T>::kParts;
+  static constexpr int kSteps = D / 16;  // k steps of the scores, row tiles of the output
+  static constexpr int kVecs = 8 * NT;
+  using R = Ring<D>;
+
+  const Kv4VecParams& p;
+  int lane, g, t;       // g: MMA row or column, t: its pair
+  uint32_t ring, bars;  // shared-memory addresses
+  int head;             // within a group of heads
+  uint32_t issued, used;
+  uint32_t valid;       // two bits a stage: blocks that hold something
+  Feed feed;
+
+  __device__ __forceinline__ Worker(const Kv4VecParams& p_) : p(p_) {}
+
+  // Copies of the next unit into the ring, if there is one.
+  __device__ __forceinline__ void issue() {
+    if (!feed.more) return;
+    const ChunkSegment& s = feed.s;
+    const int b0 = s.t.kb / kBlock + 2 * feed.j;
+    if (b0 - feed.ids_from >= 32) {
+      const int b = b0 + lane;
+      feed.ids = (long long)b * kBlock < s.t.ke ? __ldg(feed.table + b) : -1;
+      feed.ids_from = b0;
+    }
+    const int which = lane & 1;
+    const int b = b0 + which;
+    const int id = __shfl_sync(kFull, feed.ids, b - feed.ids_from);
+    const bool wanted = (long long)b * kBlock < s.t.ke;
+    const bool ok = wanted && id >= 0 && id < p.c.pool_blocks;
+    if (wanted && !ok && lane < 2) atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+    const uint32_t mask = __ballot_sync(kFull, ok) & 3u;
+    const uint32_t slot = issued % kStages, bar = bars + 8 * slot;
+    if (lane == 0) mbar_arrive_tx(bar, __popc(mask) * 2 * R::kTile);
+    __syncwarp();
+    if (lane < 4 && ok) {
+      const int kv_head = (s.head / p.subs) * p.heads_per_worker + head;
+      const uint8_t* pool = lane < 2 ? p.k_pool : p.v_pool;
+      bulk_load(ring + slot * R::kStage + lane * R::kTile,
+                pool + ((size_t)id * p.kv_heads + kv_head) * R::kTile, R::kTile, bar);
+    }
+    valid = (valid & ~(3u << (2 * slot))) | (mask << (2 * slot));
+    ++issued;
+    if (++feed.j == s.j1) feed.open(p);
+  }
+
+  // Scores of a block: c[nt], rows are tokens, columns query vectors.
+  __device__ __forceinline__ void scores(uint32_t tile, const uint32_t (&q)[kParts][NT][kSteps][2],
+                                         float (&c)[NT][4]) const {
+    const int r0 = g ^ ((g >> 1) & 1), r1 = r0 + 8;
+    const uint32_t sc = tile + kv4_number_bytes(D);
+    uint32_t w[2][D / 32];  // a lane's numbers of its two tokens
+    uint32_t s[2][D / 64];  // their scales, doubled
+    if constexpr (D == 128) {
+      const uint4 a = lds128(tile + r0 * 64 + t * 16), b = lds128(tile + r1 * 64 + t * 16);
+      w[0][0] = a.x, w[0][1] = a.y, w[0][2] = a.z, w[0][3] = a.w;
+      w[1][0] = b.x, w[1][1] = b.y, w[1][2] = b.z, w[1][3] = b.w;
+      const uint32_t e = e4m3x2_to_half(lds16(sc + r0 * 8 + 2 * t));
+      const uint32_t f = e4m3x2_to_half(lds16(sc + r1 * 8 + 2 * t));
+      s[0][0] = both(e, false), s[0][1] = both(e, true);
+      s[1][0] = both(f, false), s[1][1] = both(f, true);
+    } else {
+      const uint2 a = lds64(tile + r0 * 32 + t * 8), b = lds64(tile + r1 * 32 + t * 8);
+      w[0][0] = a.x, w[0][1] = a.y;
+      w[1][0] = b.x, w[1][1] = b.y;
+      s[0][0] = both(e4m3x2_to_half(lds8(sc + r0 * 4 + t)), false);
+      s[1][0] = both(e4m3x2_to_half(lds8(sc + r1 * 4 + t)), false);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {  // 8 dimensions of a lane: two k steps
+      uint32_t a[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        e2m1x8_to_half(w[r][i], a[r]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[r][j] = hmul2(a[r][j], s[r][i / 2]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(c[nt], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
+                q[part][nt][2 * i + j][0], q[part][nt][2 * i + j][1]);
+    }
+  }
+
+  // o += V^T P of two blocks: rows are dimensions (lane g holds D / 8 that lie
+  // together), columns query vectors; dead: a bit for each of a lane's tokens (four a
+  // block) that holds nothing.
+  __device__ __forceinline__ void values(uint32_t tile,
+                                         const uint32_t (&pb)[2][kParts][NT][2], uint32_t dead,
+                                         float (&o)[kSteps][NT][4]) const {
+    constexpr int kWords = D / 64;  // words of a lane's dimensions of one token
+    uint32_t x[2][kWords][4], s[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t base = tile + b * R::kTile, sc = base + kv4_number_bytes(D);
+      uint32_t w[4][kWords], e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int tok = ((2 * t + (j & 1)) ^ (t & 1)) + (j & 2) * 4;
+        if constexpr (D == 128) {
+          const uint2 v = lds64(base + tok * 64 + g * 8);
+          w[j][0] = v.x, w[j][1] = v.y;
+          e[j] = lds8(sc + tok * 8 + g);
+        } else {
+          w[j][0] = lds32(base + tok * 32 + g * 4);
+          e[j] = lds8(sc + tok * 4 + g / 2);
+        }
+      }
+      if (dead) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((dead >> (4 * b + j)) & 1) e[j] = 0;
+      }
+      s[b][0] = e4m3x2_to_half(e[0] | (e[1] << 8));
+      s[b][1] = e4m3x2_to_half(e[2] | (e[3] << 8));
+      // a byte of x: one dimension of two tokens, the k pair of an MMA operand
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = w[2 * h][i], c = w[2 * h + 1][i];
+          x[b][i][2 * h] = (a & 0x0f0f0f0fu) | ((c << 4) & 0xf0f0f0f0u);      // even dimensions
+          x[b][i][2 * h + 1] = ((a >> 4) & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u);  // odd ones
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (kParts == 1) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t a[4][4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            e2m1x8_to_half(x[b][i][h], a[h]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[h][k] = hmul2(a[h][k], s[b][h / 2]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(o[4 * i + k][nt], a[0][k], a[1][k], a[2][k], a[3][k], pb[b][0][nt][0],
+                  pb[b][0][nt][1]);
+        }
+      } else {
+        // The tensor core's accumulator drops what it does not hold, always towards
+        // zero: each unit's sum starts at zero and is added up rounded.
+        float sum[4][NT][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[k][nt][j] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t a[4][4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            e2m1x8_to_half(x[b][i][h], a[h]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[h][k] = hmul2(a[h][k], s[b][h / 2]);
+          }
+#pragma unroll
+          for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(sum[k][nt], a[0][k], a[1][k], a[2][k], a[3][k], pb[b][part][nt][0],
+                    pb[b][part][nt][1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[4 * i + k][nt][j] += sum[k][nt][j];
+      }
+    }
+  }
+
+  // The whole share; false when a wait gave up.
+  __device__ __forceinline__ bool run(int worker) {
+    feed.wk.init(p.c, worker);
+    ChunkWalk wk = feed.wk;
+    feed.open(p);
+    issued = used = valid = 0;
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    ChunkSegment s;
+#pragma unroll 1
+    while (wk.next<kVecKeys>(p.c, s)) {
+      const int sub = s.head % p.subs;
+      const int kv_head = (s.head / p.subs) * p.heads_per_worker + head;
+      const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
+      const int vecs = s.t.n_tok * per;
+      const int h0 = kv_head * p.c.group + sub * kVecs;  // first query head
+      auto row_of = [&](int v) {  // of query vector v, in q and out
+        const int tok = v / per;
+        return ((size_t)s.t.q0 + tok) * p.c.heads + h0 + (v - tok * per);
+      };
+      // the query vectors as operands, and what brings their scores to log2 units
+      uint32_t q[kParts][NT][kSteps][2];
+      float up[NT];  // lane's vector g of each column tile
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int v = 8 * nt + g;
+        float x[D / 4];  // dimensions D / 4 * t ..
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+        if (v < vecs) {
+          const T* src = static_cast<const T*>(p.c.q) + row_of(v) * D + t * (D / 4);
+          if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 4) {
+              const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
+              x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 8) {
+              const uint4 f = __ldg(reinterpret_cast<const uint4*>(src + i));
+              const uint32_t r[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x[i + 2 * k] = __uint_as_float(r[k] << 16);
+                x[i + 2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+              }
+            }
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // top * 2^e in [2^14, 2^15), as far as 2^e is in range
+        const int e = min(126, 14 + 127 - (int)(__float_as_uint(top) >> 23));
+        const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+        up[nt] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 2) {
+          const float a = x[i] * mul, b = x[i + 1] * mul;
+          const uint32_t h = pack_half(a, b);
+          q[0][nt][i / 4][(i / 2) & 1] = h;
+          if constexpr (kParts == 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            q[kParts - 1][nt][i / 4][(i / 2) & 1] = pack_half(a - f.x, b - f.y);
+          }
+        }
+      }
+      // of the two columns of each column tile that this lane's scores are in
+      const float k_unit = p.k_scales ? __ldg(p.k_scales + kv_head) : 1.f;
+      float mul[NT][2], slope[NT][2], m[NT][2], l[NT][2], comp[NT][2];
+      int lo[NT][2], hi[NT][2], pos[NT][2];
+      int lo_all = 0, hi_all = 0x7fffffff;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int v = 8 * nt + 2 * t + c;
+          const float u = __shfl_sync(kFull, up[nt], 4 * (2 * t + c));
+          mul[nt][c] = (CAP ? p.c.scale : p.c.qscale) * k_unit * u;
+          slope[nt][c] = 0.f;
+          m[nt][c] = -INFINITY;
+          l[nt][c] = comp[nt][c] = 0.f;
+          const int tok = v / per;
+          pos[nt][c] = s.t.pos0 + tok;
+          lo[nt][c] = 0;
+          hi[nt][c] = 0x7fffffff;
+          if (v < vecs) {
+            const int2 see = chunk_sees(p.c, (long long)s.t.q0 + tok, pos[nt][c], s.t.ctx);
+            lo[nt][c] = see.x;
+            hi[nt][c] = see.y;
+            if (BIAS) slope[nt][c] = __ldg(p.c.slopes + h0 + (v - tok * per)) * kLog2e;
+          }
+          lo_all = max(lo_all, lo[nt][c]);
+          hi_all = min(hi_all, hi[nt][c]);
+        }
+      lo_all = __reduce_max_sync(kFull, lo_all);
+      hi_all = __reduce_min_sync(kFull, hi_all);
+      float o[kSteps][NT][4];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
+
+#pragma unroll 1
+      for (int j = s.j0; j < s.j1; ++j) {
+        issue();  // into the stage that the unit before last was in
+        const uint32_t slot = used % kStages;
+        if (!warp_wait(bars + 8 * slot, (used / kStages) & 1)) return false;
+        const uint32_t stage = ring + slot * R::kStage;
+        const int t0 = s.t.kb + j * kVecKeys;
+        const uint32_t have = (valid >> (2 * slot)) & 3u;
+        float x[2][NT][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) scores(stage + b * R::kTile, q, x[b]);
+        const bool dense = have == 3u && t0 >= lo_all && hi_all - t0 >= kVecKeys;
+        const int row = g ^ ((g >> 1) & 1);  // this lane's first token within a block
+        uint32_t dead = 0;
+        // to log2 units; what is not seen to -inf
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = i & 1;
+              float y = x[b][nt][i] * mul[nt][c];
+              if (CAP) y = p.c.cap * kLog2e * tanhf(y / p.c.cap);
+              if (BIAS) {
+                const int rel = b * kBlock + row + (i & 2) * 4;
+                y -= slope[nt][c] * fabsf((float)(pos[nt][c] - t0 - rel));
+              }
+              x[b][nt][i] = y;
+            }
+        if (!dense) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = i & 1;
+                const int rel = b * kBlock + row + (i & 2) * 4;
+                if (!((have >> b) & 1) || rel < lo[nt][c] - t0 || rel >= hi[nt][c] - t0)
+                  x[b][nt][i] = -INFINITY;
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rel = b * kBlock + ((2 * t + (k & 1)) ^ (t & 1)) + (k & 2) * 4;
+              if (!((have >> b) & 1) || rel >= s.t.ctx - t0) dead |= 1u << (4 * b + k);
+            }
+          }
+        }
+        // the running maxima
+        float mx[NT][2];
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mx[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+            raise |= mx[nt][c] > m[nt][c] + Round<T>::kSlack;
+          }
+        if (__any_sync(kFull, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float y = mx[nt][c];
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) y = fmaxf(y, __shfl_xor_sync(kFull, y, d));
+              const bool up_here = y > m[nt][c];
+              const float alpha = up_here ? ex2_approx(m[nt][c] - y) : 1.f;
+              if (up_here) m[nt][c] = y;
+              l[nt][c] *= alpha;
+              comp[nt][c] *= alpha;
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) {
+                o[i][nt][c] *= alpha;
+                o[i][nt][c + 2] *= alpha;
+              }
+            }
+        }
+        // weights, and as operands
+        uint32_t pb[2][kParts][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float neg[2], sum[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            neg[c] = m[nt][c] == -INFINITY ? 0.f : Round<T>::kUp - m[nt][c];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ex2_approx(x[b][nt][i] + neg[i & 1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) sum[c] = b ? sum[c] + (w[c] + w[c + 2]) : w[c] + w[c + 2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t up2 = pack_half(w[2 * h], w[2 * h + 1]);
+              pb[b][0][nt][h] = transpose8x8(up2);
+              if constexpr (kParts == 2) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&up2));
+                pb[b][kParts - 1][nt][h] =
+                    transpose8x8(pack_half(w[2 * h] - f.x, w[2 * h + 1] - f.y));
+              }
+            }
+          }
+          // (compensated: nearly equal weights round the same way each time)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float y = sum[c] - comp[nt][c];
+            const float z = l[nt][c] + y;
+            comp[nt][c] = (z - l[nt][c]) - y;
+            l[nt][c] = z;
+          }
+        }
+        values(stage + 2 * R::kTile, pb, dead, o);
+        ++used;
+        __syncwarp();  // all lanes have read the stage
+      }
+
+      // The sums over the lanes that share a column; then the result or the piece.
+      const bool whole = s.first && s.last;
+      const float v_unit = p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f;
+      const int slot = 2 * worker + (s.first ? 1 : 0);
+      const size_t state = ((size_t)slot * p.heads_per_worker + head) * kVecs;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float sum = l[nt][c];
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(kFull, sum, d);
+          const int v = 8 * nt + 2 * t + c;
+          if (v >= vecs) continue;
+          if (whole) {
+            const float inv = sum > 0.f ? v_unit / sum : 0.f;
+            T* out = static_cast<T*>(p.c.out) + row_of(v) * D + g * (D / 8);
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+              for (int i = 0; i < kSteps; i += 2)
+                *reinterpret_cast<float4*>(out + 2 * i) =
+                    make_float4(o[i][nt][c] * inv, o[i][nt][c + 2] * inv, o[i + 1][nt][c] * inv,
+                                o[i + 1][nt][c + 2] * inv);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kSteps; i += 4)
+                *reinterpret_cast<uint4*>(out + 2 * i) =
+                    make_uint4(pack_bf16(o[i][nt][c] * inv, o[i][nt][c + 2] * inv),
+                               pack_bf16(o[i + 1][nt][c] * inv, o[i + 1][nt][c + 2] * inv),
+                               pack_bf16(o[i + 2][nt][c] * inv, o[i + 2][nt][c + 2] * inv),
+                               pack_bf16(o[i + 3][nt][c] * inv, o[i + 3][nt][c + 2] * inv));
+            }
+          } else {
+            if (g == 0) p.ml[state + v] = make_float2(m[nt][c], sum);
+            float* acc = p.acc + (state + v) * D + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < kSteps; i += 2)
+              *reinterpret_cast<float4*>(acc + 2 * i) = make_float4(
+                  o[i][nt][c], o[i][nt][c + 2], o[i + 1][nt][c], o[i + 1][nt][c + 2]);
+          }
+        }
+      if (!whole && s.first && head == 0) {
+        // how many workers the tile's pieces are on: those that start at or before
+        // its last unit's first
+        const long long last =
+            s.head * __ldcg(p.c.ws_head) + __ldcg(p.c.ws_prefix + s.tile) +
+            (long long)(p.c.tile_cost + chunk_runs(s.t.kb, s.t.ke, kVecKeys) - 1) * s.t.cost;
+        int n = 0;
+#pragma unroll 1
+        for (int c = worker; c < p.c.grid; c += 32) {
+          const unsigned in = __ballot_sync(
+              kFull, c + lane < p.c.grid && __ldcg(p.c.ws_first + c + lane) <= last);
+          n += __popc(in);
+          if (in != kFull) break;
+        }
+        if (lane == 0) p.todo[worker] = make_int4(s.t.q0, s.t.n_tok, s.head, n);
+      }
+    }
+    return true;
+  }
+};
+
+template <typename T, int NT>
+constexpr int ctas_per_sm() {
+  return sizeof(T) == 2 && NT == 1 ? 2 : 1;
+}
+
+template <typename T, int D, int NT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
+    kv4_vec_kernel(const __grid_constant__ Kv4VecParams p) {
+  using R = Ring<D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + (blockDim.x >> 5) * R::kWarp + warp * kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  griddep_wait();  // the tile list, and whatever was written before it
+  griddep_launch();
+  const int worker = blockIdx.x * p.workers_per_cta + warp / p.heads_per_worker;
+  if (worker >= p.c.grid) return;
+  Worker<T, D, NT, CAP, BIAS> w(p);
+  w.lane = lane;
+  w.g = lane >> 2;
+  w.t = lane & 3;
+  w.ring = base + warp * R::kWarp;
+  w.bars = bars;
+  w.head = warp % p.heads_per_worker;
+  if (w.head == 0 && lane == 0) p.todo[worker] = make_int4(0, 0, 0, 0);
+  if (!w.run(worker)) {
+    if (lane == 0) atomicOr(p.c.status, (uint32_t)NSV_DEV_TIMEOUT);
+    // every copy issued lands before the CTA can end
+    for (uint32_t i = w.used; i < w.issued; ++i)
+      (void)warp_wait(bars + 8 * (i % kStages), (i / kStages) & 1);
+  }
+}
+
+// Joins the pieces of the tile that worker blockIdx.x starts and does not end, for
+// KV head blockIdx.y of its group: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+// Four warps take a query vector each, a lane D / 32 columns.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4VecParams p) {
+  constexpr int kVecs = 8 * NT;
+  griddep_wait();
+  griddep_launch();
+  const int worker = blockIdx.x, head = blockIdx.y;
+  const int4 todo = __ldcg(p.todo + worker);
+  if (todo.w == 0) return;
+  const int lane = threadIdx.x & 31;
+  const int sub = todo.z % p.subs;
+  const int kv_head = (todo.z / p.subs) * p.heads_per_worker + head;
+  const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
+  const float v_unit = p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f;
+  for (int v = threadIdx.x >> 5; v < todo.y * per; v += 4) {
+    float M = -INFINITY, L = 0.f, a[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) a[k] = 0.f;
+    constexpr int kAhead = 8;
+#pragma unroll 1
+    for (int b = 0; b < todo.w; b += kAhead) {
+      float2 ml[kAhead];
+      float x[kAhead][D / 32];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = min(b + i, todo.w - 1);
+        const size_t at =
+            ((size_t)(2 * (worker + j) + (j == 0 ? 1 : 0)) * p.heads_per_worker + head) * kVecs + v;
+        ml[i] = __ldcg(p.ml + at);
+        const float* src = p.acc + at * D + lane * (D / 32);
+        if constexpr (D == 128) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+          x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+          x[i][0] = f.x, x[i][1] = f.y;
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
+      if (top == -INFINITY) continue;
+      const float keep = ex2_approx(M - top);
+      M = top;
+      L *= keep;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) a[k] *= keep;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (b + i >= todo.w || ml[i].x == -INFINITY) continue;
+        const float w = ex2_approx(ml[i].x - M);
+        L = fmaf(w, ml[i].y, L);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) a[k] = fmaf(w, x[i][k], a[k]);
+      }
+    }
+    const float inv = L > 0.f ? v_unit / L : 0.f;
+    const int tok = v / per;
+    T* out = static_cast<T*>(p.c.out) +
+             (((size_t)todo.x + tok) * p.c.heads + kv_head * p.c.group + sub * kVecs + (v - tok * per)) * D +
+             lane * (D / 32);
+#pragma unroll
+    for (int k = 0; k < D / 32; k += 2) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float2*>(out + k) = make_float2(a[k] * inv, a[k + 1] * inv);
+      else
+        *reinterpret_cast<uint32_t*>(out + k) = pack_bf16(a[k] * inv, a[k + 1] * inv);
+    }
+  }
+}
+
+cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int D>
+constexpr int smem_bytes(int warps) {
+  return warps * (int)(Ring<D>::kWarp + kStages * 8);
+}
+
+template <typename T, int D, int NT, bool CAP, bool BIAS>
+cudaError_t launch_one(const Kv4VecParams& p, cudaStream_t stream) {
+  const int warps = p.workers_per_cta * p.heads_per_worker;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg =
+      config(dim3((unsigned)((p.c.grid + p.workers_per_cta - 1) / p.workers_per_cta)), warps * 32,
+             smem_bytes<D>(warps), stream, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_vec_kernel<T, D, NT, CAP, BIAS>, p);
+  if (e != cudaSuccess) return e;
+  cfg = config(dim3((unsigned)p.c.grid, (unsigned)p.heads_per_worker), 128, 0, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T, D, NT>, p);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_nt(const Kv4VecParams& p, cudaStream_t stream) {
+  const bool cap = p.c.cap > 0.f, bias = p.c.slopes != nullptr;
+  return cap ? (bias ? launch_one<T, D, NT, true, true>(p, stream)
+                     : launch_one<T, D, NT, true, false>(p, stream))
+             : (bias ? launch_one<T, D, NT, false, true>(p, stream)
+                     : launch_one<T, D, NT, false, false>(p, stream));
+}
+
+template <typename T, int D, int NT>
+cudaError_t set_attrs() {
+  const int bytes = smem_bytes<D>(kWarps);
+  cudaError_t e = cudaFuncSetAttribute(kv4_vec_kernel<T, D, NT, false, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv4_vec_kernel<T, D, NT, false, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv4_vec_kernel<T, D, NT, true, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv4_vec_kernel<T, D, NT, true, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
+}
+
+}  // namespace
+
+int kv4_vec_warps(int, int) { return kWarps; }
+int kv4_vec_ctas_per_sm(int dtype, int col_tiles) {
+  return dtype == NSV_BF16 && col_tiles == 1 ? 2 : 1;
+}
+
+cudaError_t prepare_kv4_vec() {
+  cudaError_t e = set_attrs<float, 64, 1>();
+  if (e == cudaSuccess) e = set_attrs<float, 128, 1>();
+  if (e == cudaSuccess) e = set_attrs<__nv_bfloat16, 64, 1>();
+  if (e == cudaSuccess) e = set_attrs<__nv_bfloat16, 128, 1>();
+  if (e == cudaSuccess) e = set_attrs<__nv_bfloat16, 64, 2>();
+  if (e == cudaSuccess) e = set_attrs<__nv_bfloat16, 128, 2>();
+  return e;
+}
+
+cudaError_t launch_kv4_vec(const Kv4VecParams& p, int dtype, int head_dim, int col_tiles,
+                           cudaStream_t stream) {
+  using B = __nv_bfloat16;
+  if (dtype == NSV_F32)
+    return head_dim == 64 ? launch_nt<float, 64, 1>(p, stream) : launch_nt<float, 128, 1>(p, stream);
+  if (col_tiles == 1)
+    return head_dim == 64 ? launch_nt<B, 64, 1>(p, stream) : launch_nt<B, 128, 1>(p, stream);
+  return head_dim == 64 ? launch_nt<B, 64, 2>(p, stream) : launch_nt<B, 128, 2>(p, stream);
+}
+
+}  // namespace nsv

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "chunk.cuh"
+#include "kv4.cuh"
 #include "nsv_common.cuh"
 
 namespace nsv {
@@ -103,7 +104,8 @@ int device_state(DeviceState** out) {
     if (cudaGetSymbolAddress(reinterpret_cast<void**>(&d.walked), g_walked) != cudaSuccess)
       return cuda_fail();
     if (prepare_decode_kernels() != cudaSuccess) return cuda_fail();
-    if (prepare_chunk_bf16() != cudaSuccess || prepare_chunk_f32() != cudaSuccess)
+    if (prepare_chunk_bf16() != cudaSuccess || prepare_chunk_f32() != cudaSuccess ||
+        prepare_kv4_vec() != cudaSuccess)
       return cuda_fail();
     if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return cuda_fail();

@@ -4,6 +4,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "kv4.cuh"
 #include "pages.cuh"
 
 namespace nsv {
@@ -15,8 +16,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // The parameters that follow from the shape and the device.
 int page_params(const nsv_shape* s, PageParams* p) {
-  const int64_t vecs =
-      (int64_t)s->num_kv_heads * kBlock * s->head_dim * (s->dtype == NSV_F32 ? 4 : 2) / 16;
+  const int64_t bytes = s->dtype == NSV_KV4 ? kv4_tile_bytes(s->head_dim)
+                                            : kBlock * s->head_dim * (s->dtype == NSV_F32 ? 4 : 2);
+  const int64_t vecs = s->num_kv_heads * bytes / 16;
   if (vecs > kMaxBlockVecs) return NSV_ERR_SHAPE;
   DeviceInfo d;
   const int rc = device_info(&d);
@@ -41,6 +43,14 @@ struct Args {
   int code() const { return null ? NSV_ERR_NULLPTR : misaligned ? NSV_ERR_ALIGN : NSV_OK; }
 };
 
+// The checks of nsv_shape, of which a 4-bit pool's type alone differs.
+int check_page_shape(const nsv_shape* s) {
+  if (!s || s->dtype != NSV_KV4) return check_shape(s);
+  nsv_shape t = *s;
+  t.dtype = NSV_BF16;
+  return check_shape(&t);
+}
+
 int check_ws(const nsv_shape* s, void* ws, size_t bytes) {
   return ws && aligned(ws, 256) && bytes >= page_ws_bytes(s->rows, s->num_blocks)
              ? NSV_OK
@@ -56,7 +66,7 @@ extern "C" {
 
 NSV_API int nsv_pages_workspace(const nsv_shape* shape, int64_t* bytes) {
   if (!bytes) return NSV_ERR_NULLPTR;
-  const int rc = check_shape(shape);
+  const int rc = check_page_shape(shape);
   if (rc) return rc;
   *bytes = (int64_t)page_ws_bytes(shape->rows, shape->num_blocks);
   return NSV_OK;
@@ -64,7 +74,7 @@ NSV_API int nsv_pages_workspace(const nsv_shape* shape, int64_t* bytes) {
 
 NSV_API int nsv_blocks_copy(const nsv_shape* shape, int32_t count, const int32_t* src,
                             const int32_t* dst, void* k_pool, void* v_pool, cudaStream_t stream) {
-  int rc = check_shape(shape);
+  int rc = check_page_shape(shape);
   if (rc) return rc;
   if (count < 0) return NSV_ERR_SHAPE;
   if (count == 0) return NSV_OK;
@@ -86,7 +96,7 @@ NSV_API int nsv_rows_fork(const nsv_shape* shape, int32_t count, const int32_t* 
                           const int32_t* children, int32_t* block_tables, int32_t* context_lens,
                           int32_t* block_refs, void* k_pool, void* v_pool, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream) {
-  int rc = check_shape(shape);
+  int rc = check_page_shape(shape);
   if (rc) return rc;
   if (count < 0 || count > shape->rows) return NSV_ERR_SHAPE;
   if (count == 0) return NSV_OK;
@@ -114,7 +124,7 @@ NSV_API int nsv_rows_extend(const nsv_shape* shape, int64_t tokens, const int32_
                             int32_t* block_tables, int32_t* context_lens, int32_t* block_refs,
                             int64_t* write_slots, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream) {
-  int rc = check_shape(shape);
+  int rc = check_page_shape(shape);
   if (rc) return rc;
   if (tokens < 0 || tokens >= (int64_t(1) << 30)) return NSV_ERR_SHAPE;
   if (shape->rows == 0 || tokens == 0) return NSV_OK;
@@ -139,7 +149,7 @@ NSV_API int nsv_rows_extend(const nsv_shape* shape, int64_t tokens, const int32_
 NSV_API int nsv_rows_free(const nsv_shape* shape, int32_t count, const int32_t* rows_list,
                           int32_t* block_tables, int32_t* context_lens, int32_t* block_refs,
                           cudaStream_t stream) {
-  int rc = check_shape(shape);
+  int rc = check_page_shape(shape);
   if (rc) return rc;
   if (count < 0) return NSV_ERR_SHAPE;
   if (shape->rows == 0 || count == 0) return NSV_OK;
@@ -161,7 +171,7 @@ NSV_API int nsv_blocks_compact(const nsv_shape* shape, int32_t* block_tables,
                                const int32_t* context_lens, int32_t* block_refs, void* k_pool,
                                void* v_pool, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream) {
-  int rc = check_shape(shape);
+  int rc = check_page_shape(shape);
   if (rc) return rc;
   Args a;
   a.need(block_refs, 4), a.need(k_pool, 16), a.need(v_pool, 16);

@@ -21,6 +21,19 @@ The chunk attention (paged_chunk, chunk_step) takes ragged batches instead:
                   chunk_starts[r + 1] - 1
   slopes          [num_heads] float32; see_begin, see_end [tokens] int32
 
+The rotating appends (rope_write; kv4_write into 4-bit pools) take
+
+  q, q_out        [tokens, num_heads, head_dim]; k_new, v_new [tokens,
+                  num_kv_heads, head_dim]; q, k_new and v_new may be slices of
+                  one projection's output (heads and dimensions contiguous)
+  positions       [tokens] int32; rotary [positions, rotary_dim] float32: the
+                  cosines of rotary_dim / 2 angles, then their sines
+
+4-bit pools (kv4_write, kv4_read, kv4_chunk, and the page operators):
+
+  k_pool, v_pool  [num_blocks + 1, num_kv_heads, 9 * head_dim] uint8
+  k_scales, v_scales  [num_kv_heads] float32, or None
+
 The page operators (blocks_copy, rows_fork, rows_extend, rows_free,
 blocks_compact) keep block_refs [num_blocks] int32, the references to each
 block (0: free), with the tables and lengths, and change them in place.
@@ -44,11 +57,11 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 ABI_VERSION = 102  # the layout of Shape and Plan below
-F32, BF16 = 0, 1
+F32, BF16, KV4 = 0, 1, 4
 (CONSUMER_AUTO, CONSUMER_CUDA, CONSUMER_TENSOR, CONSUMER_TENSOR_VECTOR_ROWS,
  CONSUMER_TENSOR_TMEM) = 0, 1, 2, 3, 4
 DEV_BAD_CTX, DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT = 1, 2, 4, 8
-DEV_BAD_CHUNK, DEV_BAD_ROW, DEV_NO_BLOCKS = 16, 32, 64
+DEV_BAD_CHUNK, DEV_BAD_ROW, DEV_NO_BLOCKS, DEV_BAD_POS = 16, 32, 64, 128
 ERRORS = {0: "NSV_OK", -1: "NSV_ERR_NULLPTR", -2: "NSV_ERR_DTYPE", -3: "NSV_ERR_SHAPE",
           -4: "NSV_ERR_ALIGN", -5: "NSV_ERR_RANGE", -6: "NSV_ERR_CAPTURE", -7: "NSV_ERR_CUDA",
           -8: "NSV_ERR_WORKSPACE", -10: "NSV_ERR_UNSUPPORTED"}
@@ -77,6 +90,12 @@ class Plan(ctypes.Structure):
 class Scores(ctypes.Structure):
     _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("see_begin", ctypes.c_void_p), ("see_end", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("num_positions", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _vp, _i32, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -118,6 +137,20 @@ _lib.nsv_paged_chunk.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _v
 _lib.nsv_chunk_step.restype = _i32
 _lib.nsv_chunk_step.argtypes = [_SP, ctypes.POINTER(Scores), _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp, _vp, _f, _vp, _vp, _sz, _vp]
+_RP = ctypes.POINTER(Rope)
+_lib.nsv_rope_write.restype = _i32
+_lib.nsv_rope_write.argtypes = [_SP, _RP, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
+                                _vp]
+_lib.nsv_kv4_write.restype = _i32
+_lib.nsv_kv4_write.argtypes = [_SP, _RP, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                               _vp, _vp, _vp]
+_lib.nsv_kv4_read.restype = _i32
+_lib.nsv_kv4_read.argtypes = [_SP, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.nsv_kv4_workspace.restype = _i32
+_lib.nsv_kv4_workspace.argtypes = [_SP, _i64, _i32, ctypes.POINTER(_i64)]
+_lib.nsv_kv4_chunk.restype = _i32
+_lib.nsv_kv4_chunk.argtypes = [_SP, ctypes.POINTER(Scores), _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _f, _vp, _vp, _sz, _vp]
 _lib.nsv_pages_workspace.restype = _i32
 _lib.nsv_pages_workspace.argtypes = [_SP, ctypes.POINTER(_i64)]
 _i32c = ctypes.c_int32
@@ -405,6 +438,17 @@ def _chunk_sizes(device, rows, heads, kv_heads, head_dim, max_blocks, num_blocks
     return ctypes.byref(shape), chunk_workspace_bytes(shape, tokens)
 
 
+def _scores_arg(softcap, slopes, see_begin, see_end, heads, tokens, dev):
+    """The nsv_scores of a call, None where it changes nothing."""
+    import torch
+    if not softcap and slopes is None and see_begin is None and see_end is None:
+        return None
+    return ctypes.byref(Scores(float(softcap),
+                               _arg(slopes, "slopes", torch.float32, (heads,), dev),
+                               _arg(see_begin, "see_begin", torch.int32, (tokens,), dev),
+                               _arg(see_end, "see_end", torch.int32, (tokens,), dev)))
+
+
 def _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out, softcap, slopes,
                 see_begin, see_end):
     import torch
@@ -422,12 +466,7 @@ def _chunk_args(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, out
             _arg(context_lens, "context_lens", i32, (R,), dev))
     out_ptr = _arg(out, "out", dt, qs, dev)
     shape, need = _chunk_sizes(dev, R, H, Hkv, D, MB, NB1 - 1, _dtype_code(k_pool), B, T)
-    scores = None
-    if softcap or slopes is not None or see_begin is not None or see_end is not None:
-        scores = ctypes.byref(Scores(float(softcap),
-                                     _arg(slopes, "slopes", torch.float32, (H,), dev),
-                                     _arg(see_begin, "see_begin", i32, (T,), dev),
-                                     _arg(see_end, "see_end", i32, (T,), dev)))
+    scores = _scores_arg(softcap, slopes, see_begin, see_end, H, T, dev)
     return shape, scores, T, ptrs, out_ptr, need, dev
 
 
@@ -461,6 +500,176 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
     return out
 
 
+def _heads_arg(t, what, dtype, heads, head_dim, tokens, dev):
+    """The pointer and token stride of [tokens, heads, head_dim], whose tokens may
+    lie apart (as in a slice of a projection's output)."""
+    if t.dtype != dtype or t.shape != (tokens, heads, head_dim):
+        raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, [tokens, heads, head_dim],
+                                                          t.dtype, list(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not on the current CUDA device %d" % (what, t.device, dev))
+    token, head, dim = t.stride()
+    if dim != 1 or (heads > 1 and head != head_dim):
+        raise ValueError("%s must have contiguous heads and dimensions" % what)
+    if tokens > 1 and token < heads * head_dim:
+        raise ValueError("the tokens of %s overlap" % what)
+    return t.data_ptr(), token if tokens > 1 else 0
+
+
+def kv4_pool(num_blocks, kv_heads, head_dim, device="cuda"):
+    """An empty 4-bit pool of `num_blocks` blocks and the sink."""
+    import torch
+    return torch.zeros((num_blocks + 1, kv_heads, 9 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _kv4_sizes(k_pool):
+    """Blocks, KV heads and head_dim of a 4-bit pool."""
+    import torch
+    if k_pool.dtype != torch.uint8 or k_pool.dim() != 3 or k_pool.shape[2] % 9:
+        raise ValueError("a 4-bit pool must be uint8 [blocks + 1, kv_heads, 9 * head_dim], got %s %s"
+                         % (k_pool.dtype, list(k_pool.shape)))
+    return k_pool.shape[0] - 1, k_pool.shape[1], k_pool.shape[2] // 9
+
+
+@functools.lru_cache(maxsize=4096)
+def _append_shape(heads, kv_heads, head_dim, num_blocks, dtype, block_size):
+    """A reference to the nsv_shape of these sizes (what an append does not use is 1)."""
+    return ctypes.byref(make_shape(1, heads, kv_heads, head_dim, 1, num_blocks, dtype, block_size))
+
+
+def _append_args(q, k_new, v_new, positions, rotary, write_slots, kv_heads, head_dim, q_out,
+                 interleaved, dev):
+    """What both rotating appends pass: the new tensors' pointers and strides, and
+    the nsv_rope (None without a rotation)."""
+    import torch
+    T, dt = write_slots.numel(), k_new.dtype
+    heads = kv_heads
+    q_args = (None, 0)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, head_dim]")
+        heads = q.shape[1]
+        q_args = _heads_arg(q, "q", dt, heads, head_dim, T, dev)
+    out = _arg(q_out, "q_out", dt, (T, heads, head_dim), dev)
+    k, ks = _heads_arg(k_new, "k_new", dt, kv_heads, head_dim, T, dev)
+    v, vs = _heads_arg(v_new, "v_new", dt, kv_heads, head_dim, T, dev)
+    slots = _arg(write_slots, "write_slots", torch.int64, (T,), dev)
+    rope = None
+    if rotary is not None or positions is not None:
+        if rotary is None or positions is None or rotary.dim() != 2:
+            raise ValueError("a rotation takes positions and a table [positions, rotary_dim]")
+        rope = ctypes.byref(Rope(_arg(rotary, "rotary", torch.float32, rotary.shape, dev),
+                                 _arg(positions, "positions", torch.int32, (T,), dev),
+                                 rotary.shape[0], rotary.shape[1], 1 if interleaved else 0))
+    return rope, heads, T, (T, q_args[0], k, v, q_args[1], ks, vs, slots), out
+
+
+def rope_write(q, k_new, v_new, positions, rotary, write_slots, k_pool, v_pool, q_out=None,
+               interleaved=False, stream=None):
+    """Rotate the queries into q_out and the keys on their way into the pools, and
+    append the values (nsv_rope_write in nsv.h).  q and q_out may be None."""
+    import torch
+    dev = torch.cuda.current_device()
+    if k_pool.dim() != 4 or k_new.dtype != k_pool.dtype:
+        raise ValueError("the pools must be [blocks + 1, kv_heads, 16, head_dim] of k_new's type")
+    pools = _pool_args(k_pool, v_pool, None, dev)
+    NB1, Hkv, B, D = k_pool.shape
+    rope, heads, _, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
+                                             q_out, interleaved, dev)
+    shape = _append_shape(heads, Hkv, D, NB1 - 1, _dtype_code(k_pool), B)
+    _check(_lib.nsv_rope_write(shape, rope, *args, *pools, out, _raw_stream(stream, dev)),
+           "nsv_rope_write")
+    return q_out
+
+
+def kv4_write(k_new, v_new, write_slots, k_pool, v_pool, k_scales=None, v_scales=None, q=None,
+              positions=None, rotary=None, q_out=None, interleaved=False, stream=None):
+    """Append keys and values to 4-bit pools (nsv_kv4_write in nsv.h); with positions
+    and a table the keys, and q into q_out, are rotated on the way."""
+    import torch
+    dev, f32, u8 = torch.cuda.current_device(), torch.float32, torch.uint8
+    blocks, Hkv, D = _kv4_sizes(k_pool)
+    rope, heads, _, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
+                                             q_out, interleaved, dev)
+    shape = _append_shape(heads, Hkv, D, blocks, _dtype_code(k_new), 16)
+    _check(_lib.nsv_kv4_write(shape, rope, _arg(k_scales, "k_scales", f32, (Hkv,), dev),
+                              _arg(v_scales, "v_scales", f32, (Hkv,), dev), *args,
+                              _arg(k_pool, "k_pool", u8, k_pool.shape, dev),
+                              _arg(v_pool, "v_pool", u8, k_pool.shape, dev), out,
+                              _raw_stream(stream, dev)), "nsv_kv4_write")
+    return q_out
+
+
+def kv4_read(slots, k_pool, v_pool, k, v, k_scales=None, v_scales=None, stream=None):
+    """Values of slots of 4-bit pools into k and v [slots, kv_heads, head_dim]."""
+    import torch
+    dev, f32, u8 = torch.cuda.current_device(), torch.float32, torch.uint8
+    blocks, Hkv, D = _kv4_sizes(k_pool)
+    T = slots.numel()
+    shape = _append_shape(Hkv, Hkv, D, blocks, _dtype_code(k), 16)
+    _check(_lib.nsv_kv4_read(shape, _arg(k_scales, "k_scales", f32, (Hkv,), dev),
+                             _arg(v_scales, "v_scales", f32, (Hkv,), dev), T,
+                             _arg(slots, "slots", torch.int64, (T,), dev),
+                             _arg(k_pool, "k_pool", u8, k_pool.shape, dev),
+                             _arg(v_pool, "v_pool", u8, k_pool.shape, dev),
+                             _arg(k, "k", k.dtype, (T, Hkv, D), dev),
+                             _arg(v, "v", k.dtype, (T, Hkv, D), dev), _raw_stream(stream, dev)),
+           "nsv_kv4_read")
+    return k, v
+
+
+def kv4_workspace_bytes(shape, tokens, num_sms=0):
+    """Workspace bytes of kv4_chunk for up to `tokens` tokens."""
+    n = _i64(0)
+    _check(_lib.nsv_kv4_workspace(ctypes.byref(shape), int(tokens), int(num_sms), ctypes.byref(n)),
+           "nsv_kv4_workspace")
+    return n.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_chunk_sizes(device, rows, heads, kv_heads, head_dim, max_blocks, num_blocks, dtype,
+                     query_len, tokens):
+    """A reference to the nsv_shape of these sizes, and its workspace bytes."""
+    shape = make_shape(rows, heads, kv_heads, head_dim, max_blocks, num_blocks, dtype,
+                       query_len=query_len)
+    return ctypes.byref(shape), kv4_workspace_bytes(shape, tokens)
+
+
+def kv4_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, scale, out,
+              k_scales=None, v_scales=None, softcap=0.0, slopes=None, see_begin=None, see_end=None,
+              max_new=0, workspace=None, stream=None):
+    """paged_chunk over 4-bit pools (nsv_kv4_chunk in nsv.h).  max_new: the most new
+    tokens that any row brings, or 0 where the caller does not know it (1 in a decode
+    step, which is fastest when it says so); more than that is flagged.  workspace:
+    kv4_workspace_bytes() of uint8, or None to allocate it."""
+    import torch
+    dev, f32, i32, u8 = torch.cuda.current_device(), torch.float32, torch.int32, torch.uint8
+    blocks, Hkv, D = _kv4_sizes(k_pool)
+    qs, bs = q.shape, block_tables.shape
+    if len(qs) != 3 or len(bs) != 2:
+        raise ValueError("q must be [tokens, heads, head_dim] and block_tables [rows, max_blocks]")
+    T, H, D2 = qs
+    if D2 != D:
+        raise ValueError("q head_dim %d != pool head_dim %d" % (D2, D))
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    # (beyond what query_len holds the call does not depend on it)
+    if H % Hkv or max_new * (H // Hkv) > 64:
+        max_new = 0
+    shape, need = _kv4_chunk_sizes(dev, bs[0], H, Hkv, D, bs[1], blocks, _dtype_code(q), max_new, T)
+    args = (shape, _scores_arg(softcap, slopes, see_begin, see_end, H, T, dev),
+            _arg(k_scales, "k_scales", f32, (Hkv,), dev),
+            _arg(v_scales, "v_scales", f32, (Hkv,), dev), T, _arg(q, "q", q.dtype, qs, dev),
+            _arg(k_pool, "k_pool", u8, k_pool.shape, dev),
+            _arg(v_pool, "v_pool", u8, k_pool.shape, dev),
+            _arg(block_tables, "block_tables", i32, bs, dev),
+            _arg(chunk_starts, "chunk_starts", i32, (bs[0] + 1,), dev),
+            _arg(context_lens, "context_lens", i32, bs[:1], dev), float(scale),
+            _arg(out, "out", q.dtype, qs, dev))
+    _call("nsv_kv4_chunk", args, need, workspace, stream, dev)
+    return out
+
+
 def pages_workspace_bytes(rows, num_blocks):
     """Workspace bytes of rows_fork, rows_extend and blocks_compact."""
     n = _i64(0)
@@ -478,8 +687,11 @@ def _page_sizes(rows, max_blocks, num_blocks, kv_heads, head_dim, dtype, block_s
 
 
 def _pool_args(k_pool, v_pool, num_blocks, dev):
+    import torch
     ks, dt = k_pool.shape, k_pool.dtype
-    if len(ks) != 4:
+    if dt == torch.uint8:
+        _kv4_sizes(k_pool)
+    elif len(ks) != 4:
         raise ValueError("the pools must be [blocks + 1, kv_heads, 16, head_dim]")
     if num_blocks is not None and ks[0] != num_blocks + 1:
         raise ValueError("the pools have %d blocks and the sink, block_refs %d"
@@ -498,6 +710,10 @@ def _cache_args(block_tables, context_lens, block_refs, dev):
 
 
 def _pool_sizes(rows, max_blocks, k_pool):
+    import torch
+    if k_pool.dtype == torch.uint8:
+        blocks, Hkv, D = _kv4_sizes(k_pool)
+        return _page_sizes(rows, max_blocks, blocks, Hkv, D, KV4, 16)
     NB1, Hkv, B, D = k_pool.shape
     return _page_sizes(rows, max_blocks, NB1 - 1, Hkv, D, _dtype_code(k_pool), B)
 
