@@ -105,6 +105,11 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
 }
 
 struct ChunkParams {
+  // a 4-bit cache (kv4.cuh): its pools, and the fp32 scales of its KV heads or null
+  const uint8_t* k4;
+  const uint8_t* v4;
+  const float* k_units;
+  const float* v_units;
   // bf16 only; tmap_q: boxes of 128, 64 and 32 MMA rows
   CUtensorMap tmap_q[3], tmap_k, tmap_v;
   const void* q;
@@ -141,9 +146,17 @@ struct ChunkParams {
   float cap;        // 0: scores are not capped
 };
 
+// A tensor map of the query tokens for boxes of `rows` MMA rows (chunk_api.cu).
+bool chunk_encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows,
+                    const void* q, CUtensorMap* map);
+
 // Launchers.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+// The tile lists of two kernels that share a batch, in one launch.
+cudaError_t launch_chunk_plans(const ChunkParams& a, const ChunkParams& b, cudaStream_t stream);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream);
+// The same over a 4-bit cache (k4, v4).
+cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t prepare_chunk_bf16();
 cudaError_t prepare_chunk_f32();

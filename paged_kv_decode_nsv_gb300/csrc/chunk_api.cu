@@ -47,11 +47,13 @@ bool encode_pool(const DeviceInfo& d, const nsv_shape* s, const void* pool, CUte
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // The query tokens as [head_dim][heads][tokens]; one box is 64 dims of the
 // query heads of one KV head for as many tokens as fit `rows` MMA rows (no map
 // where not even one does).
-bool encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows, const void* q,
-              CUtensorMap* map) {
+bool chunk_encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows,
+                    const void* q, CUtensorMap* map) {
   const int box_tokens = rows / (s->num_heads / s->num_kv_heads);
   if (box_tokens == 0) return true;
   const cuuint64_t D = (cuuint64_t)s->head_dim, H = (cuuint64_t)s->num_heads;
@@ -65,6 +67,8 @@ bool encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // All checks, then (with `append`) the append's launch, the plan's and the
 // attention's.
@@ -134,9 +138,9 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.whole_runs = kChunkWholeRuns;
   p.ws_first = reinterpret_cast<long long*>(p.ws_cta + p.grid);
   if (s->dtype == NSV_BF16 &&
-      (!encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||
-       !encode_q(d, s, tokens, kChunkHalfRows / 2, q, &p.tmap_q[1]) ||
-       !encode_q(d, s, tokens, kChunkHalfRows / 4, q, &p.tmap_q[2]) ||
+      (!chunk_encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||
+       !chunk_encode_q(d, s, tokens, kChunkHalfRows / 2, q, &p.tmap_q[1]) ||
+       !chunk_encode_q(d, s, tokens, kChunkHalfRows / 4, q, &p.tmap_q[2]) ||
        !encode_pool(d, s, k_pool, &p.tmap_k) || !encode_pool(d, s, v_pool, &p.tmap_v)))
     return cuda_fail();
   if (append && launch_kv_write(*append, stream) != cudaSuccess) return cuda_fail();

@@ -49,6 +49,7 @@
 // 5.
 
 #include "chunk.cuh"
+#include "kv4.cuh"
 
 namespace nsv {
 namespace {
@@ -56,7 +57,9 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-constexpr int kThreads = (kSoftWarps + 3) * 32;
+constexpr int kWidenWarps = 4;
+template <bool KV4>
+constexpr int kThreads = (kSoftWarps + 3 + (KV4 ? kWidenWarps : 0)) * 32;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr int kMetaRing = 16;
@@ -131,7 +134,7 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 }
 
 // ------------------------------------------------------------------ producer
-template <int D>
+template <int D, bool KV4>
 __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
                                         volatile int* s_meta, const volatile uint32_t* s_done,
                                         ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
@@ -167,6 +170,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
                       B.qfull());
     }
     ++nseg;
+    if (KV4) continue;  // keys and values have warps of their own
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
     auto block_id = [&](int j) -> int {  // lane's block of run j, -1 past the tile's keys
       const int b = (s.t.kb + j * kChunkKeys) / kBlock + lane;
@@ -196,6 +200,118 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
                       0, 0, coord, B.full(slot));
         ++i;
       }
+      ++run;
+    }
+  }
+  return true;
+}
+
+// --------------------------------------------------------------------- widening
+// A 4-bit cache's keys and values, by four warps: each takes 32 tokens of a run, 8 at a
+// time, a lane a quarter of one of them.  The numbers times their scales (exact in
+// bf16) go where the bulk copies of a bf16 cache would have put them, in the same
+// swizzle; 8 lanes write the same 16 bytes of 8 tokens, which lie in different banks.
+// Loads of the next run's keys (values) are in flight while this run's values (the next
+// keys) are widened.  Tokens that are not there become zeros.
+template <int D>
+__device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, unsigned char* smem,
+                                      volatile int* s_meta, ChunkWalk wk, int ww, int lane) {
+  using L = Smem<D>;
+  constexpr int kTile = kv4_tile_bytes(D), kWords = D / 32;  // words of a lane's quarter
+  const int row = lane & 7, part = lane >> 3;
+  uint32_t i = 0, run = 0;
+  struct Raw {
+    uint32_t w[4][kWords], s[4];
+  };
+  ChunkSegment s;
+#pragma unroll 1
+  while (wk.next<kChunkKeys>(p, s)) {
+    const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
+    auto block_id = [&](int j) -> int {  // lane's block of run j, -1 past the tile's keys
+      const int b = (s.t.kb + j * kChunkKeys) / kBlock + lane;
+      return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
+    };
+    // a lane's quarters of this warp's tokens of run j
+    auto load = [&](const uint8_t* pool, int ids, int j, Raw& r) {
+      const int left = s.t.ctx - s.t.kb - j * kChunkKeys - 32 * ww;  // tokens that are there
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int id = __shfl_sync(kFull, ids, 2 * ww + (q >> 1));
+        r.s[q] = 0;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) r.w[q][k] = 0;
+        if (id >= 0 && 8 * q + row < left) {
+          const int off = 8 * (q & 1) + row;
+          const uint8_t* t = pool + ((size_t)id * p.kv_heads + s.head) * kTile;
+          if constexpr (D == 128) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(t + off * 64 + part * 16));
+            r.w[q][0] = x.x, r.w[q][1] = x.y, r.w[q][2] = x.z, r.w[q][3] = x.w;
+            r.s[q] = __ldg(reinterpret_cast<const uint16_t*>(t + 8 * D + off * 8 + part * 2));
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(t + off * 32 + part * 8));
+            r.w[q][0] = x.x, r.w[q][1] = x.y;
+            r.s[q] = __ldg(t + 8 * D + off * 4 + part);
+          }
+        }
+      }
+    };
+    auto store = [&](const Raw& r) {
+      const uint32_t slot = i % L::kStages, ph = (i / L::kStages) & 1;
+      if (!warp_wait(B.empty(slot), ph ^ 1)) return false;
+      unsigned char* stage = smem + slot * L::kStage + row * 128;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        unsigned char* group = stage + (4 * ww + q) * (D / 64) * 1024;
+        const uint32_t sc = e4m3x2_to_half(r.s[q]);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          const uint32_t s2 = __byte_perm(sc, 0, k >= 2 ? 0x3232 : 0x1010);
+          uint32_t h[4];
+          e2m1x8_to_half(r.w[q][k], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[e] = hmul2(h[e], s2);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+            h[e] = pack_bf16(f.x, f.y);
+          }
+          const int chunk = part * kWords + k;  // 8 dimensions
+          *reinterpret_cast<uint4*>(group + (chunk >> 3) * 1024 + (((chunk & 7) ^ row) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.full(slot));
+      ++i;
+      return true;
+    };
+    // the ids of a run's blocks, -1 for those that are not there
+    auto check = [&](int ids, int j) {
+      const bool wanted = lane < kChunkKeys / kBlock &&
+                          (long long)s.t.kb + j * kChunkKeys + lane * kBlock < s.t.ke;
+      const bool ok = wanted && ids >= 0 && ids < p.pool_blocks;
+      if (wanted && !ok && ww == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+      return ok ? ids : -1;
+    };
+    Raw k, v;
+    int ids = check(block_id(s.j0), s.j0);
+    load(p.k4, ids, s.j0, k);
+    load(p.v4, ids, s.j0, v);
+    int next = s.j0 + 1 < s.j1 ? block_id(s.j0 + 1) : -1;
+#pragma unroll 1
+    for (int j = s.j0; j < s.j1; ++j) {
+      const unsigned mask = __ballot_sync(kFull, ids >= 0);
+      // (the meta ring has room for more runs than the stages hold)
+      if (ww == 0 && lane == 0) s_meta[run % kMetaRing] = (int)mask;
+      if (!store(k)) return false;
+      const bool more = j + 1 < s.j1;
+      if (more) {
+        ids = check(next, j + 1);
+        next = j + 2 < s.j1 ? block_id(j + 2) : -1;
+        load(p.k4, ids, j + 1, k);
+      }
+      if (!store(v)) return false;
+      if (more) load(p.v4, ids, j + 1, v);
       ++run;
     }
   }
@@ -341,12 +457,12 @@ struct RowState {
 // 16 warps each at its own place, did not fit the instruction cache, and warps
 // waited for instructions more than for anything else.
 template <int D, bool CAP, bool BIAS>
-__device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint32_t t_s,
+__device__ __forceinline__ bool fold_run(const ChunkParams& p, float k_unit, RowState& f, uint32_t t_s,
                                          uint32_t t_o, int t0, int col0, int NC, int hf, int copy,
                                          int mask, bool past, int bar, volatile PairWords* w,
                                          volatile float2* s_ml, uint32_t turn, int lane) {
   constexpr int kW = 16;
-  float mul = p.qscale;
+  float mul = p.qscale * k_unit;
   // positions that the row does not see; nothing to mask in most runs
   const int lo = f.see.x - t0 - col0, hi = f.see.y - t0 - col0;
   const int bm = mask >> (col0 / kBlock);
@@ -371,7 +487,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint
     // scale, cap, bias and mask, and put the result back
     const float d0 = (float)(f.pos - t0 - col0);
     const float cap_out = p.cap * 1.4426950408889634f;
-    const float cap_z = CAP ? p.scale / p.cap : 0.f, cap_in = cap_z * 2.8853900817779268f;
+    const float cap_z = CAP ? p.scale * k_unit / p.cap : 0.f, cap_in = cap_z * 2.8853900817779268f;
 #pragma unroll 1
     for (int c = 0; c < NC; c += kW) {
       float s[kW];
@@ -482,7 +598,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, RowState& f, uint
   return true;
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool KV4>
 __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
                                        unsigned char* smem, const volatile int* s_meta,
                                        int4* s_todo, uint32_t* s_done,
@@ -540,6 +656,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     f.l = 0.f;
     const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
+    const float k_unit = KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f;
     // the states' exchange is free: every warp has read the previous tile's
     if (nseg && !warp_wait(B.mlfree(), (nseg - 1) & 1)) return kTimedOut;
 #pragma unroll 1
@@ -552,7 +669,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
       // Values of positions that hold nothing (past the context, or in a
       // block that was not loaded) become zeros: their probability is 0, but
       // 0 * NaN is not.
-      if (mask != 0xff || s.t.ctx - t0 < kChunkKeys) {
+      if (!KV4 && (mask != 0xff || s.t.ctx - t0 < kChunkKeys)) {
         const uint32_t i = 2 * run + 1, slot = i % L::kStages;
         if (!warp_wait(B.full(slot), (i / L::kStages) & 1)) return kTimedOut;
         if (!((mask >> (r >> 4)) & 1) || r >= s.t.ctx - t0) {
@@ -564,7 +681,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
         fence_proxy_async_smem();
       }
       if (any_valid) {
-        const bool ok = fold_run<D, CAP, BIAS>(p, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
+        const bool ok = fold_run<D, CAP, BIAS>(p, k_unit, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
                                                copy, mask, past, bar, words,
                                                s_ml + x * kChunkHalfRows + r, turn, lane);
         if (!ok) return kPartnerFailed;
@@ -615,7 +732,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(B.mlfree());  // read: the next tile's states may go there
-    const float inv = whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f;
+    const float v_unit = KV4 && p.v_units ? __ldg(p.v_units + s.head) : 1.f;
+    const float inv = (whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f) * v_unit;
     w0 *= inv;
     w1 *= inv;
     // where the tile's rows go: row `off` of this KV head's
@@ -723,8 +841,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
   return kDone;
 }
 
-template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
+template <int D, bool CAP, bool BIAS, bool KV4>
+__global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
     const __grid_constant__ ChunkParams p) {
   using L = Smem<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -738,7 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   uint32_t* s_done = reinterpret_cast<uint32_t*>(smem + L::kOffDone);
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 2 * L::kStages + 2; ++i) mbar_init(smem0 + L::kOffBars + 8 * i, 1);
+      for (int i = 0; i < 2 * L::kStages + 2; ++i)
+        mbar_init(smem0 + L::kOffBars + 8 * i, KV4 && i < L::kStages ? kWidenWarps : 1);
       mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
@@ -777,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
     volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
-    const int end = softmax<D, CAP, BIAS>(p, B, smem, s_meta, s_todo, s_done, words, wk, warp,
+    const int end = softmax<D, CAP, BIAS, KV4>(p, B, smem, s_meta, s_todo, s_done, words, wk, warp,
                                           lane);
     // Every warp but one whose partner failed meets its partner once more: so a
     // partner that still works learns of a timeout at its next meeting, and none
@@ -790,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
     ok = end == kDone;
   } else if (warp == kSoftWarps) {
     uint32_t i = 0, nq = 0;
-    ok = produce<D>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
+    ok = produce<D, KV4>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
     // every copy issued lands before the CTA can end, even after a timeout
     for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
@@ -803,6 +922,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
       (void)mbar_wait(B.drained(), 0);
     }
     __syncwarp();
+  } else if (KV4 && warp >= kSoftWarps + 3) {
+    ok = widen<D>(p, B, smem, s_meta, wk, warp - kSoftWarps - 3, lane);
   } else {
     ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
   }
@@ -813,11 +934,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_bf16_kernel(
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool KV4>
 cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<KV4>);
   cfg.dynamicSmemBytes = Smem<D>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -825,22 +946,27 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_bf16_kernel<D, CAP, BIAS>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_bf16_kernel<D, CAP, BIAS, KV4>, p);
 }
 
-template <int D>
+template <int D, bool KV4>
 cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
   const bool cap = p.cap > 0.f, bias = p.slopes != nullptr;
-  return cap ? (bias ? launch_one<D, true, true>(p, stream)
-                     : launch_one<D, true, false>(p, stream))
-             : (bias ? launch_one<D, false, true>(p, stream)
-                     : launch_one<D, false, false>(p, stream));
+  return cap ? (bias ? launch_one<D, true, true, KV4>(p, stream)
+                     : launch_one<D, true, false, KV4>(p, stream))
+             : (bias ? launch_one<D, false, true, KV4>(p, stream)
+                     : launch_one<D, false, false, KV4>(p, stream));
 }
 
 template <int D, bool CAP, bool BIAS>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  const cudaError_t e =
+      cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS, false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  return e != cudaSuccess
+             ? e
+             : cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS, true>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
 }
 
 template <int D>
@@ -860,7 +986,11 @@ cudaError_t prepare_chunk_bf16() {
 }
 
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, stream) : launch_dim<128>(p, stream);
+  return head_dim == 64 ? launch_dim<64, false>(p, stream) : launch_dim<128, false>(p, stream);
+}
+
+cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64, true>(p, stream) : launch_dim<128, true>(p, stream);
 }
 
 }  // namespace nsv

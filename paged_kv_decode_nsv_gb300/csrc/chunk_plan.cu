@@ -64,14 +64,12 @@ __device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool 
   return c;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+__device__ __forceinline__ void plan(const ChunkParams& p) {
   __shared__ int s_first[kMaxRows + 1];  // tiles before each row
   __shared__ long long s_prefix[kPlanThreads];
   __shared__ long long s_warp[32];
   // a tile's key range, before its prefix takes its place
   int2* s_keys = reinterpret_cast<int2*>(s_prefix);
-  sm::griddep_wait();  // lengths and bounds may be the previous kernel's
-  sm::griddep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tt = p.tile_tokens;
 
@@ -218,7 +216,34 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   }
 }
 
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+  sm::griddep_wait();  // lengths and bounds may be the previous kernel's
+  sm::griddep_launch();
+  plan(p);
+}
+
+// One CTA for each list.
+__global__ void __launch_bounds__(kPlanThreads)
+    chunk_plans_kernel(const __grid_constant__ ChunkParams a, const __grid_constant__ ChunkParams b) {
+  sm::griddep_wait();
+  sm::griddep_launch();
+  plan(blockIdx.x ? b : a);
+}
+
 }  // namespace
+
+cudaError_t launch_chunk_plans(const ChunkParams& a, const ChunkParams& b, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_plans_kernel, a, b);
+}
 
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
   // (programmatic: its launch overlaps the previous kernel's end, and it waits for

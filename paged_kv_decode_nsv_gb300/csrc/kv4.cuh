@@ -70,6 +70,7 @@ struct Kv4VecParams {
 
 // Query vectors of a tile of the vector form: 8 a column tile of the MMA.
 constexpr int kVecKeys = 32;  // positions of one unit: two blocks
+constexpr int kVecMostVectors = 32;  // query vectors of a row and KV head, bf16
 constexpr int kVecTileCost = 1;   // of a tile, in units
 constexpr int kVecWholeRuns = 8;  // as kChunkWholeRuns
 

@@ -129,7 +129,7 @@ int col_tiles_for(const nsv_shape* s, int64_t tokens) {
   if (s->dtype == NSV_F32) return 1;
   const int64_t group = s->num_heads / s->num_kv_heads;
   const int64_t new_tokens =
-      s->query_len > 0 ? s->query_len : tokens <= s->rows ? 1 : kVecKeys;
+      s->query_len > 0 ? s->query_len : tokens <= s->rows ? 1 : kVecMostVectors;
   return group * new_tokens <= 8 ? 1 : 2;
 }
 
@@ -155,7 +155,19 @@ VecWs vec_ws(const nsv_shape* s, const VecForm& f, int64_t tokens) {
   return W;
 }
 
-// A larger batch's workspace serves a smaller one, whichever form that takes.
+// Most new tokens of a row that the vector form takes; rows that bring more go to the
+// form for many rows (chunk_bf16.cu), of which fp32 has none.
+int vec_tokens(const nsv_shape* s) {
+  return s->dtype == NSV_F32 ? 0x7fffffff : kVecMostVectors / (s->num_heads / s->num_kv_heads);
+}
+
+ChunkWs tile_ws(const nsv_shape* s, int64_t tokens, int num_sms) {
+  return make_chunk_ws(s->rows, tokens, s->num_kv_heads, s->num_heads / s->num_kv_heads,
+                       s->head_dim, s->dtype, num_sms);
+}
+
+// The vector form's workspace, then the other form's.  A larger batch's serves a smaller
+// one, whichever form that takes.
 uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
   nsv_shape any = *s;
   any.query_len = 0;
@@ -166,7 +178,101 @@ uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
     most = std::max({most, vec_ws(&any, vec_form(&any, ct, num_sms), tokens).total,
                      vec_ws(&one, vec_form(&one, ct, num_sms), tokens).total});
   }
-  return most;
+  if (s->dtype == NSV_F32) return most;
+  return (most + 255) / 256 * 256 + tile_ws(s, tokens, num_sms).total;
+}
+
+// What both forms' plans and kernels share of a call.
+struct Call {
+  const nsv_shape* s;
+  const nsv_scores* sc;
+  DeviceInfo d;
+  int64_t tokens;
+  const void* q;
+  const int32_t* block_tables;
+  const int32_t* chunk_starts;
+  const int32_t* context_lens;
+  float scale;
+  void* out;
+};
+
+void common_params(const Call& a, ChunkParams* c) {
+  const nsv_shape* s = a.s;
+  c->q = a.q;
+  c->block_tables = a.block_tables;
+  c->chunk_starts = a.chunk_starts;
+  c->context_lens = a.context_lens;
+  c->slopes = a.sc ? a.sc->slopes : nullptr;
+  c->see_begin = a.sc ? a.sc->see_begin : nullptr;
+  c->see_end = a.sc ? a.sc->see_end : nullptr;
+  c->out = a.out;
+  c->status = a.d.status;
+  c->pool_blocks = s->num_blocks + 1;
+  c->tokens = a.tokens;
+  c->rows = s->rows;
+  c->heads = s->num_heads;
+  c->group = s->num_heads / s->num_kv_heads;
+  c->max_blocks = s->max_blocks;
+  c->qscale = a.scale * 1.4426950408889634f;  // the kernels use exp2
+  c->scale = a.scale;
+  c->cap = a.sc ? a.sc->softcap : 0.f;
+}
+
+void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4VecParams* p) {
+  const nsv_shape* s = a.s;
+  ChunkParams& c = p->c;
+  common_params(a, &c);
+  c.ws_head = reinterpret_cast<long long*>(b);
+  c.ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
+  c.ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
+  c.ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
+  c.ws_first = reinterpret_cast<long long*>(c.ws_cta + f.workers);
+  c.ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
+  c.kv_heads = s->num_kv_heads / f.heads_per_worker * f.subs;
+  c.max_tiles = W.max_tiles;
+  c.tile_tokens = f.tile_tokens;
+  c.keys = kVecKeys;
+  c.grid = f.workers;
+  c.n_min = 0;
+  c.n_max = vec_tokens(s);
+  c.whole_runs = kVecWholeRuns;
+  c.tile_cost = kVecTileCost;
+  c.pair_units = c.half_units = 1;
+  p->todo = reinterpret_cast<int4*>(b + W.off_todo);
+  p->ml = reinterpret_cast<float2*>(b + W.off_ml);
+  p->acc = reinterpret_cast<float*>(b + W.off_acc);
+  p->kv_heads = s->num_kv_heads;
+  p->heads_per_worker = f.heads_per_worker;
+  p->workers_per_cta = f.workers_per_cta;
+  p->subs = f.subs;
+}
+
+bool tile_params(const Call& a, const ChunkWs& W, char* b, ChunkParams* c) {
+  const nsv_shape* s = a.s;
+  common_params(a, c);
+  c->ws_head = reinterpret_cast<long long*>(b);
+  c->ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
+  c->ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
+  c->ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
+  c->ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
+  c->ws_ml = reinterpret_cast<float2*>(b + W.off_ml);
+  c->ws_acc = reinterpret_cast<float*>(b + W.off_acc);
+  c->kv_heads = s->num_kv_heads;
+  c->max_tiles = W.max_tiles;
+  c->tile_rows = W.tile_rows;
+  c->tile_tokens = chunk_tile_tokens(s->dtype, c->group);
+  c->keys = kChunkKeys;
+  c->grid = a.d.num_sms;  // one CTA per SM: it takes all the tensor memory
+  c->n_min = vec_tokens(s) + 1;
+  c->n_max = 0x7fffffff;
+  c->whole_runs = kChunkWholeRuns;
+  c->tile_cost = kChunkTileCost;
+  c->pair_units = kChunkPairUnits;
+  c->half_units = kChunkHalfUnits;
+  c->ws_first = reinterpret_cast<long long*>(c->ws_cta + c->grid);
+  return chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows, a.q, &c->tmap_q[0]) &&
+         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 2, a.q, &c->tmap_q[1]) &&
+         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 4, a.q, &c->tmap_q[2]);
 }
 
 }  // namespace
@@ -268,64 +374,45 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
     return NSV_ERR_RANGE;
   DeviceInfo d;
   if ((rc = device_info(&d)) != NSV_OK) return rc;
-  if (!ws || ws_bytes < chunk4_ws_bytes(s, tokens, d.num_sms) || !aligned(ws, 256))
-    return NSV_ERR_WORKSPACE;
+  const uint64_t ws_need = chunk4_ws_bytes(s, tokens, d.num_sms);
+  if (!ws || ws_bytes < ws_need || !aligned(ws, 256)) return NSV_ERR_WORKSPACE;
+  const Call call{s, sc, d, tokens, q, block_tables, chunk_starts, context_lens, scale, out};
   const VecForm f = vec_form(s, col_tiles_for(s, tokens), d.num_sms);
   const VecWs W = vec_ws(s, f, tokens);
-  char* b = static_cast<char*>(ws);
   Kv4VecParams p;
   memset(&p, 0, sizeof p);
-  ChunkParams& c = p.c;
-  c.q = q;
-  c.block_tables = block_tables;
-  c.chunk_starts = chunk_starts;
-  c.context_lens = context_lens;
-  c.slopes = sc ? sc->slopes : nullptr;
-  c.see_begin = sc ? sc->see_begin : nullptr;
-  c.see_end = sc ? sc->see_end : nullptr;
-  c.out = out;
-  c.ws_head = reinterpret_cast<long long*>(b);
-  c.ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
-  c.ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
-  c.ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
-  c.ws_first = reinterpret_cast<long long*>(c.ws_cta + f.workers);
-  c.ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
-  c.status = d.status;
-  c.pool_blocks = s->num_blocks + 1;
-  c.tokens = tokens;
-  c.rows = s->rows;
-  c.heads = s->num_heads;
-  c.kv_heads = s->num_kv_heads / f.heads_per_worker * f.subs;
-  c.group = s->num_heads / s->num_kv_heads;
-  c.max_blocks = s->max_blocks;
-  c.max_tiles = W.max_tiles;
-  c.tile_tokens = f.tile_tokens;
-  c.keys = kVecKeys;
-  c.grid = f.workers;
-  c.n_min = 0;
-  c.n_max = s->query_len > 0 ? s->query_len : 0x7fffffff;
-  c.flag_above = s->query_len > 0;
-  c.whole_runs = kVecWholeRuns;
-  c.tile_cost = kVecTileCost;
-  c.pair_units = c.half_units = 1;
-  c.qscale = scale * 1.4426950408889634f;  // the kernels use exp2
-  c.scale = scale;
-  c.cap = sc ? sc->softcap : 0.f;
+  vec_params(call, f, W, static_cast<char*>(ws), &p);
   p.k_pool = static_cast<const uint8_t*>(k_pool);
   p.v_pool = static_cast<const uint8_t*>(v_pool);
   p.k_scales = k_scales;
   p.v_scales = v_scales;
-  p.todo = reinterpret_cast<int4*>(b + W.off_todo);
-  p.ml = reinterpret_cast<float2*>(b + W.off_ml);
-  p.acc = reinterpret_cast<float*>(b + W.off_acc);
-  p.kv_heads = s->num_kv_heads;
-  p.heads_per_worker = f.heads_per_worker;
-  p.workers_per_cta = f.workers_per_cta;
-  p.subs = f.subs;
-  if (launch_chunk_plan(c, stream) != cudaSuccess) return cuda_fail();
-  return launch_kv4_vec(p, s->dtype, s->head_dim, f.col_tiles, stream) == cudaSuccess
-             ? NSV_OK
-             : cuda_fail();
+  // Which forms rows of this call can take: both, unless the caller or the number of
+  // tokens rules one out.
+  const int64_t most = s->query_len > 0 ? s->query_len : tokens;
+  const bool vec = vec_tokens(s) > 0, tiles = std::min(most, tokens) > vec_tokens(s);
+  ChunkParams c;
+  memset(&c, 0, sizeof c);
+  if (tiles) {
+    const ChunkWs T = tile_ws(s, tokens, d.num_sms);
+    if (!tile_params(call, T, static_cast<char*>(ws) + ws_need - T.total, &c)) return cuda_fail();
+    c.k4 = p.k_pool;
+    c.v4 = p.v_pool;
+    c.k_units = k_scales;
+    c.v_units = v_scales;
+  }
+  // a row of more tokens than the caller named is read as having none
+  if (s->query_len > 0) {
+    ChunkParams& last = tiles ? c : p.c;
+    last.n_max = s->query_len;
+    last.flag_above = true;
+  }
+  cudaError_t e = !vec     ? launch_chunk_plan(c, stream)
+                  : !tiles ? launch_chunk_plan(p.c, stream)
+                           : launch_chunk_plans(p.c, c, stream);
+  if (e == cudaSuccess && tiles) e = launch_chunk_kv4(c, s->head_dim, stream);
+  if (e == cudaSuccess && vec)
+    e = launch_kv4_vec(p, s->dtype, s->head_dim, f.col_tiles, stream);
+  return e == cudaSuccess ? NSV_OK : cuda_fail();
 }
 
 }  // extern "C"
