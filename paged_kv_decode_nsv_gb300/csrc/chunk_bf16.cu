@@ -57,15 +57,23 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-constexpr int kWidenWarps = 4;
+// Over a 4-bit cache: warps 16-23 widen, 24 issues, 25 publishes, 26 and 27 fill the last
+// warpgroup up.  72 registers a thread at launch, dealt out anew (a multiple of 8 each;
+// 16 x 80 + 8 x 64 + 4 x 56 = 28 x 72).
+constexpr int kWidenWarps = 8;
+constexpr int kRegsSoft = 80, kRegsWiden = 64, kRegsRest = 56;
 template <bool KV4>
-constexpr int kThreads = (kSoftWarps + 3 + (KV4 ? kWidenWarps : 0)) * 32;
+constexpr int kThreads = (KV4 ? kSoftWarps + kWidenWarps + 4 : kSoftWarps + 3) * 32;
+template <bool KV4>
+constexpr int kMmaWarp = KV4 ? kSoftWarps + kWidenWarps : kSoftWarps + 1;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr int kMetaRing = 16;
 // The running maximum is raised only when a run exceeds it by more than this
 // (log2 units): probabilities stay <= 2^8, and most runs skip the rescale.
 constexpr float kSlack = 8.f;
+// fp16 ones are held times 2^7 (at most 2^15), so that small ones keep their digits.
+constexpr float kUpHalf = 7.f;
 
 template <int D>
 struct Smem {
@@ -88,7 +96,9 @@ struct Smem {
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
   static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address, then kOffDone
   static constexpr uint32_t kOffDone = kOffWord + 4;        // softmax warps done, over all tiles
-  static constexpr uint32_t kTotal = kOffWord + 16;
+  // A 4-bit cache: what brings scores to their size, float [4][8], a segment in turn.
+  static constexpr uint32_t kOffUp = kOffWord + 16;
+  static constexpr uint32_t kTotal = kOffUp + 128;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
@@ -134,7 +144,7 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 }
 
 // ------------------------------------------------------------------ producer
-template <int D, bool KV4>
+template <int D>
 __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
                                         volatile int* s_meta, const volatile uint32_t* s_done,
                                         ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
@@ -170,7 +180,6 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
                       B.qfull());
     }
     ++nseg;
-    if (KV4) continue;  // keys and values have warps of their own
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
     auto block_id = [&](int j) -> int {  // lane's block of run j, -1 past the tile's keys
       const int b = (s.t.kb + j * kChunkKeys) / kBlock + lane;
@@ -207,21 +216,102 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
 }
 
 // --------------------------------------------------------------------- widening
-// A 4-bit cache's keys and values, by four warps: each takes 32 tokens of a run, 8 at a
-// time, a lane a quarter of one of them.  The numbers times their scales (exact in
-// bf16) go where the bulk copies of a bf16 cache would have put them, in the same
-// swizzle; 8 lanes write the same 16 bytes of 8 tokens, which lie in different banks.
-// Loads of the next run's keys (values) are in flight while this run's values (the next
-// keys) are widened.  Tokens that are not there become zeros.
+// Over a 4-bit cache operands are fp16: its numbers times their scales are exact, and a
+// pair of them takes 11 instructions a word of 8 (bf16, which has no conversion from
+// e2m1, 23).  Eight warps fill the stages, and the query rows.
+//
+// Query rows: 32 rows (a softmax warp's) are scaled by one power of two, so that the
+// largest element lies in [2^14, 2^15): exact but for elements below 2^-28 of it, off by
+// 2^-40 of it at most.  Two passes, of which the first runs before the rows are free.
+template <int D>
+__device__ __forceinline__ bool widen_queries(const ChunkParams& p, const Bars<D>& B,
+                                              unsigned char* smem, const volatile uint32_t* s_done,
+                                              const ChunkSegment& s, uint32_t nseg,
+                                              uint32_t& shared, int ww, int lane) {
+  using L = Smem<D>;
+  constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows a load
+  const int copies = copies_of(p, s);
+  const int chunk = lane % kChunks, x = ww >> 2;
+  const int copy_rows = copies > 1 ? kChunkHalfRows / copies : kChunkHalfRows;
+  const bool used = copies == 0 || x == 0;
+  const int tok0 = x * (p.tile_tokens / 2);
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+  auto row_of = [&](int i) { return 32 * (ww & 3) + kRows * i + lane / kChunks; };
+  auto load = [&](int i) {
+    const int rc = row_of(i) & (copy_rows - 1);
+    const int ti = (int)((unsigned)rc / (unsigned)p.group), g = rc - ti * p.group;
+    const int tok = tok0 + ti;
+    if (!used || (ti + 1) * p.group > copy_rows || tok >= s.t.n_tok) return make_uint4(0, 0, 0, 0);
+    return __ldg(reinterpret_cast<const uint4*>(
+        q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D + chunk * 8));
+  };
+  constexpr int kBatch = 4;
+  uint32_t top = 0;  // of the elements' magnitudes, as bf16
+#pragma unroll 1
+  for (int i = 0; i < kChunks; i += kBatch) {
+    uint4 r[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) r[k] = load(i + k);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+    }
+  }
+  top = __reduce_max_sync(kFull, top);
+  const int e = min(126, 14 + 127 - (int)(top >> 23));
+  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+  if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
+  // (as in produce)
+  if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
+  if (copies == 0) shared = 0;
+  if (copies > 1) shared = nseg + 1;
+  if (used) {
+    if (lane == 0)
+      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + ww] =
+          __uint_as_float((uint32_t)(127 - e) << 23);
+    unsigned char* half = smem + L::kOffQ + x * L::kHalf + (chunk >> 3) * (kChunkHalfRows * 128);
+#pragma unroll 1
+    for (int i = 0; i < kChunks; i += kBatch) {
+      uint4 r[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r[k] = load(i + k);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+        for (int e2 = 0; e2 < 4; ++e2)
+          w[e2] = pack_half(__uint_as_float(w[e2] << 16) * mul,
+                            __uint_as_float(w[e2] & 0xffff0000u) * mul);
+        const int row = row_of(i + k);
+        *reinterpret_cast<uint4*>(half + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(B.qfull());
+  return true;
+}
+
+// Keys and values: a warp takes one block of a run, 8 tokens at a time, a lane a quarter
+// of one of them.  They go where the bulk copies of a bf16 cache would have put them, in
+// the same swizzle; 8 lanes write the same 16 bytes of 8 tokens, which lie in different
+// banks.  Loads of the next run's keys (values) are in flight while this run's values
+// (the next keys) are widened.  Tokens that are not there become zeros.
 template <int D>
 __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, unsigned char* smem,
-                                      volatile int* s_meta, ChunkWalk wk, int ww, int lane) {
+                                      volatile int* s_meta, const volatile uint32_t* s_done,
+                                      ChunkWalk wk, int ww, int lane) {
   using L = Smem<D>;
   constexpr int kTile = kv4_tile_bytes(D), kWords = D / 32;  // words of a lane's quarter
   const int row = lane & 7, part = lane >> 3;
-  uint32_t i = 0, run = 0;
+  uint32_t i = 0, run = 0, nseg = 0, shared = 0;
   struct Raw {
-    uint32_t w[4][kWords], s[4];
+    uint32_t w[2][kWords], s[2];
   };
   ChunkSegment s;
 #pragma unroll 1
@@ -231,18 +321,26 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
       const int b = (s.t.kb + j * kChunkKeys) / kBlock + lane;
       return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
     };
+    // the ids of a run's blocks, -1 for those that are not there
+    auto check = [&](int ids, int j) {
+      const bool wanted = lane < kChunkKeys / kBlock &&
+                          (long long)s.t.kb + j * kChunkKeys + lane * kBlock < s.t.ke;
+      const bool ok = wanted && ids >= 0 && ids < p.pool_blocks;
+      if (wanted && !ok && ww == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+      return ok ? ids : -1;
+    };
     // a lane's quarters of this warp's tokens of run j
     auto load = [&](const uint8_t* pool, int ids, int j, Raw& r) {
-      const int left = s.t.ctx - s.t.kb - j * kChunkKeys - 32 * ww;  // tokens that are there
+      const int left = s.t.ctx - s.t.kb - j * kChunkKeys - kBlock * ww;  // tokens that are there
+      const int id = __shfl_sync(kFull, ids, ww);
+      const uint8_t* t = pool + ((size_t)(unsigned)id * p.kv_heads + s.head) * kTile;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int id = __shfl_sync(kFull, ids, 2 * ww + (q >> 1));
+      for (int q = 0; q < 2; ++q) {
         r.s[q] = 0;
 #pragma unroll
         for (int k = 0; k < kWords; ++k) r.w[q][k] = 0;
-        if (id >= 0 && 8 * q + row < left) {
-          const int off = 8 * (q & 1) + row;
-          const uint8_t* t = pool + ((size_t)id * p.kv_heads + s.head) * kTile;
+        const int off = 8 * q + row;
+        if (id >= 0 && off < left) {
           if constexpr (D == 128) {
             const uint4 x = __ldg(reinterpret_cast<const uint4*>(t + off * 64 + part * 16));
             r.w[q][0] = x.x, r.w[q][1] = x.y, r.w[q][2] = x.z, r.w[q][3] = x.w;
@@ -258,10 +356,9 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
     auto store = [&](const Raw& r) {
       const uint32_t slot = i % L::kStages, ph = (i / L::kStages) & 1;
       if (!warp_wait(B.empty(slot), ph ^ 1)) return false;
-      unsigned char* stage = smem + slot * L::kStage + row * 128;
+      unsigned char* stage = smem + slot * L::kStage + 2 * ww * (D / 64) * 1024 + row * 128;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        unsigned char* group = stage + (4 * ww + q) * (D / 64) * 1024;
+      for (int q = 0; q < 2; ++q) {
         const uint32_t sc = e4m3x2_to_half(r.s[q]);
 #pragma unroll
         for (int k = 0; k < kWords; ++k) {
@@ -269,14 +366,10 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
           uint32_t h[4];
           e2m1x8_to_half(r.w[q][k], h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[e] = hmul2(h[e], s2);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
-            h[e] = pack_bf16(f.x, f.y);
-          }
+          for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], s2);
           const int chunk = part * kWords + k;  // 8 dimensions
-          *reinterpret_cast<uint4*>(group + (chunk >> 3) * 1024 + (((chunk & 7) ^ row) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(stage + (q * (D / 64) + (chunk >> 3)) * 1024 +
+                                    (((chunk & 7) ^ row) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
       fence_proxy_async_smem();
@@ -285,19 +378,13 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
       ++i;
       return true;
     };
-    // the ids of a run's blocks, -1 for those that are not there
-    auto check = [&](int ids, int j) {
-      const bool wanted = lane < kChunkKeys / kBlock &&
-                          (long long)s.t.kb + j * kChunkKeys + lane * kBlock < s.t.ke;
-      const bool ok = wanted && ids >= 0 && ids < p.pool_blocks;
-      if (wanted && !ok && ww == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-      return ok ? ids : -1;
-    };
     Raw k, v;
     int ids = check(block_id(s.j0), s.j0);
     load(p.k4, ids, s.j0, k);
     load(p.v4, ids, s.j0, v);
     int next = s.j0 + 1 < s.j1 ? block_id(s.j0 + 1) : -1;
+    if (!widen_queries<D>(p, B, smem, s_done, s, nseg, shared, ww, lane)) return false;
+    ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
       const unsigned mask = __ballot_sync(kFull, ids >= 0);
@@ -327,15 +414,16 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
 // stage are compile-time constants.  One thread, elected, runs all of this: the
 // votes that keep a whole warp together made a turn 1740 cycles long where its
 // MMAs take 1000.
-template <int D>
+template <int D, bool KV4>
 __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
                                           ChunkWalk wk) {
   using L = Smem<D>;
   // K and V stages: tokens in groups of 8, a group's 64-dim halves one
   // 1024-byte swizzle atom after the other
   constexpr uint32_t kGroup = (D / 64) * 1024u;
-  constexpr uint32_t idesc_s = umma_idesc_bf16(kChunkHalfRows, kChunkKeys, false);
-  constexpr uint32_t idesc_o = umma_idesc_bf16(kChunkHalfRows, D, true);
+  constexpr uint32_t kTypes = KV4 ? kIdescHalf : 0;
+  constexpr uint32_t idesc_s = umma_idesc_bf16(kChunkHalfRows, kChunkKeys, false) ^ kTypes;
+  constexpr uint32_t idesc_o = umma_idesc_bf16(kChunkHalfRows, D, true) ^ kTypes;
   const uint64_t dq = umma_desc128(smem0 + L::kOffQ, 16, 1024);
   const uint64_t dk = umma_desc128(smem0, 16, kGroup);
   const uint64_t dv = umma_desc128(smem0, 1024, kGroup);
@@ -456,13 +544,13 @@ struct RowState {
 // one with the row in registers: unrolled over 64 columns the loop's code, run by
 // 16 warps each at its own place, did not fit the instruction cache, and warps
 // waited for instructions more than for anything else.
-template <int D, bool CAP, bool BIAS>
-__device__ __forceinline__ bool fold_run(const ChunkParams& p, float k_unit, RowState& f, uint32_t t_s,
+template <int D, bool CAP, bool BIAS, bool KV4>
+__device__ __forceinline__ bool fold_run(const ChunkParams& p, float unit, RowState& f, uint32_t t_s,
                                          uint32_t t_o, int t0, int col0, int NC, int hf, int copy,
                                          int mask, bool past, int bar, volatile PairWords* w,
                                          volatile float2* s_ml, uint32_t turn, int lane) {
   constexpr int kW = 16;
-  float mul = p.qscale * k_unit;
+  float mul = p.qscale * unit;
   // positions that the row does not see; nothing to mask in most runs
   const int lo = f.see.x - t0 - col0, hi = f.see.y - t0 - col0;
   const int bm = mask >> (col0 / kBlock);
@@ -487,7 +575,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float k_unit, Row
     // scale, cap, bias and mask, and put the result back
     const float d0 = (float)(f.pos - t0 - col0);
     const float cap_out = p.cap * 1.4426950408889634f;
-    const float cap_z = CAP ? p.scale * k_unit / p.cap : 0.f, cap_in = cap_z * 2.8853900817779268f;
+    const float cap_z = CAP ? p.scale * unit / p.cap : 0.f, cap_in = cap_z * 2.8853900817779268f;
 #pragma unroll 1
     for (int c = 0; c < NC; c += kW) {
       float s[kW];
@@ -566,7 +654,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float k_unit, Row
       }
     }
   }
-  const float neg = f.m == -INFINITY ? 0.f : -f.m;
+  const float neg = f.m == -INFINITY ? 0.f : (KV4 ? kUpHalf : 0.f) - f.m;
   float l0 = 0.f, l1 = 0.f;
 #pragma unroll 1
   for (int c = 0; c < NC; c += kW) {
@@ -580,7 +668,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float k_unit, Row
       a = ex2_approx(a);
       b = ex2_approx(b);
       add2(l0, l1, a, b);
-      s[k / 2] = __uint_as_float(pack_bf16(a, b));
+      s[k / 2] = __uint_as_float(KV4 ? pack_half(a, b) : pack_bf16(a, b));
     }
     tmem_st8(t_s + col0 + c, s);
   }
@@ -615,6 +703,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
   const uint32_t t_o = lane_base + kColO;
   const int half_tok = p.tile_tokens / 2;
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
+  const volatile float* s_up = reinterpret_cast<const volatile float*>(smem + L::kOffUp);
   float* s_x = reinterpret_cast<float*>(smem + L::kOffX + (x * 2 + hf) * L::kQuarterX);
   uint32_t nscore = 0, nseg = 0, njoin = 0, nmeet = 0, run0 = 0, turn = 0;
   // the four warps with this stream and half meet
@@ -666,6 +755,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
       if (!warp_wait(B.scores(x), nscore++ & 1)) return kTimedOut;
       tc_fence_after();
       const int mask = s_meta[run % kMetaRing];
+      const float unit =
+          KV4 ? k_unit * s_up[(nseg & 3) * 8 + (pair ? x * 4 : 0) + (warp & 3)] : 1.f;
       // Values of positions that hold nothing (past the context, or in a
       // block that was not loaded) become zeros: their probability is 0, but
       // 0 * NaN is not.
@@ -681,7 +772,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
         fence_proxy_async_smem();
       }
       if (any_valid) {
-        const bool ok = fold_run<D, CAP, BIAS>(p, k_unit, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
+        const bool ok = fold_run<D, CAP, BIAS, KV4>(p, unit, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
                                                copy, mask, past, bar, words,
                                                s_ml + x * kChunkHalfRows + r, turn, lane);
         if (!ok) return kPartnerFailed;
@@ -857,7 +948,8 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < 2 * L::kStages + 2; ++i)
-        mbar_init(smem0 + L::kOffBars + 8 * i, KV4 && i < L::kStages ? kWidenWarps : 1);
+        mbar_init(smem0 + L::kOffBars + 8 * i,
+                  KV4 && (i < L::kStages || i == 2 * L::kStages) ? kWidenWarps : 1);
       mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
@@ -895,6 +987,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
   if (odd) {
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
+    if (KV4) reg_inc<kRegsSoft>();
     volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
     const int end = softmax<D, CAP, BIAS, KV4>(p, B, smem, s_meta, s_todo, s_done, words, wk, warp,
                                           lane);
@@ -907,25 +1000,29 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       (void)pair_sync(1 + (warp >> 3) * 4 + (warp & 3), words);
     }
     ok = end == kDone;
-  } else if (warp == kSoftWarps) {
+  } else if (KV4 && warp < kSoftWarps + kWidenWarps) {
+    reg_dec<kRegsWiden>();
+    ok = widen<D>(p, B, smem, s_meta, s_done, wk, warp - kSoftWarps, lane);
+  } else if (!KV4 && warp == kSoftWarps) {
     uint32_t i = 0, nq = 0;
-    ok = produce<D, KV4>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
+    ok = produce<D>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
     // every copy issued lands before the CTA can end, even after a timeout
     for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
       (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
     if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
-  } else if (warp == kSoftWarps + 1) {
-    if (elect_one()) {
-      ok = issue_mma<D>(p, B, smem0, wk);
-      if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
-      umma_commit(B.drained(), true);  // arrives once every MMA issued is done
-      (void)mbar_wait(B.drained(), 0);
-    }
-    __syncwarp();
-  } else if (KV4 && warp >= kSoftWarps + 3) {
-    ok = widen<D>(p, B, smem, s_meta, wk, warp - kSoftWarps - 3, lane);
   } else {
-    ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
+    if (KV4) reg_dec<kRegsRest>();
+    if (warp == kMmaWarp<KV4>) {
+      if (elect_one()) {
+        ok = issue_mma<D, KV4>(p, B, smem0, wk);
+        if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
+        umma_commit(B.drained(), true);  // arrives once every MMA issued is done
+        (void)mbar_wait(B.drained(), 0);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp<KV4> + 1) {
+      ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
+    }
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
   tc_fence_before();

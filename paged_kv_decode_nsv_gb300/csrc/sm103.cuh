@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -135,6 +136,8 @@ __device__ __forceinline__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// What differs in it where A and B are fp16.
+constexpr uint32_t kIdescHalf = (1u << 7) | (1u << 10);
 // The same of a kind::tf32 MMA: tf32 A and B (of each 32-bit element the upper 19
 // bits), both K-major.
 __device__ __forceinline__ constexpr uint32_t umma_idesc_tf32(int m, int n) {
@@ -298,6 +301,11 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
