@@ -57,11 +57,15 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-// Over a 4-bit cache: warps 16-23 widen, 24 issues, 25 publishes, 26 and 27 fill the last
-// warpgroup up.  72 registers a thread at launch, dealt out anew (a multiple of 8 each;
-// 16 x 80 + 8 x 64 + 4 x 56 = 28 x 72).
-constexpr int kWidenWarps = 8;
-constexpr int kRegsSoft = 80, kRegsWiden = 64, kRegsRest = 56;
+// Over a 4-bit cache: warps 16-19 widen, 20 issues, 21 publishes, 22 fetches tiles, 23 fills
+// the last warpgroup up.  80 registers a thread at launch, dealt out anew (a multiple of 8 each;
+// 16 x 88 + 4 x 64 + 4 x 64 = 24 x 80).
+constexpr int kWidenWarps = 4;
+// Tiles as they are in the pool wait in a ring of half runs (a run's keys or values).
+constexpr int kTileRing = 3;
+template <int D>
+constexpr uint32_t kHalfRun = kChunkKeys / kBlock * kv4_tile_bytes(D);
+constexpr int kRegsSoft = 88, kRegsWiden = 64, kRegsRest = 64;
 template <bool KV4>
 constexpr int kThreads = (KV4 ? kSoftWarps + kWidenWarps + 4 : kSoftWarps + 3) * 32;
 template <bool KV4>
@@ -75,10 +79,13 @@ constexpr float kSlack = 8.f;
 // fp16 ones are held times 2^7 (at most 2^15), so that small ones keep their digits.
 constexpr float kUpHalf = 7.f;
 
-template <int D>
+// Over a 4-bit cache there is one stage less, which makes room for the tiles as they are
+// in the pool (five: 970 us for 2048 tokens over 32768, with loads to registers in place
+// of that room; four: 942).
+template <int D, bool KV4>
 struct Smem {
   static constexpr uint32_t kStage = kChunkKeys * D * 2;  // K or V of one run
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStages = (KV4 ? 4 : 5) * (128 / D);
   static constexpr uint32_t kHalf = kChunkHalfRows * D * 2;  // query rows of one half
   static constexpr uint32_t kOffQ = kStages * kStage;
   // Exchange of the copies' outputs, [2 streams][2 halves][128 rows][16 columns]
@@ -98,14 +105,16 @@ struct Smem {
   static constexpr uint32_t kOffDone = kOffWord + 4;        // softmax warps done, over all tiles
   // A 4-bit cache: what brings scores to their size, float [4][8], a segment in turn.
   static constexpr uint32_t kOffUp = kOffWord + 16;
-  static constexpr uint32_t kTotal = kOffUp + 128;
+  static constexpr uint32_t kOffTiles = (kOffUp + 128 + 127) / 128 * 128;
+  static constexpr uint32_t kOffTileBars = kOffTiles + kTileRing * kHalfRun<D>;  // full, free
+  static constexpr uint32_t kTotal = KV4 ? kOffTileBars + 2 * kTileRing * 8 : kOffWord + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
-template <int D>
+template <int D, bool KV4>
 struct Bars {
   uint32_t b;
-  static constexpr int S = Smem<D>::kStages;
+  static constexpr int S = Smem<D, KV4>::kStages;
   __device__ uint32_t full(uint32_t i) const { return b + 8 * i; }
   __device__ uint32_t empty(uint32_t i) const { return b + 8 * (S + i); }
   __device__ uint32_t qfull() const { return b + 8 * (2 * S); }
@@ -145,10 +154,10 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 
 // ------------------------------------------------------------------ producer
 template <int D>
-__device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
+__device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, false>& B, uint32_t smem0,
                                         volatile int* s_meta, const volatile uint32_t* s_done,
                                         ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
-  using L = Smem<D>;
+  using L = Smem<D, false>;
   constexpr uint32_t kBlockBytes = kBlock * D * 2;
   const int half_tok = p.tile_tokens / 2;
   uint32_t run = 0;
@@ -218,66 +227,70 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D>& B, 
 // --------------------------------------------------------------------- widening
 // Over a 4-bit cache operands are fp16: its numbers times their scales are exact, and a
 // pair of them takes 11 instructions a word of 8 (bf16, which has no conversion from
-// e2m1, 23).  Eight warps fill the stages, and the query rows.
+// e2m1, 23).  Four warps fill the stages, and the query rows.
 //
 // Query rows: 32 rows (a softmax warp's) are scaled by one power of two, so that the
 // largest element lies in [2^14, 2^15): exact but for elements below 2^-28 of it, off by
 // 2^-40 of it at most.  Two passes, of which the first runs before the rows are free.
 template <int D>
-__device__ __forceinline__ bool widen_queries(const ChunkParams& p, const Bars<D>& B,
+__device__ __forceinline__ bool widen_queries(const ChunkParams& p, const Bars<D, true>& B,
                                               unsigned char* smem, const volatile uint32_t* s_done,
                                               const ChunkSegment& s, uint32_t nseg,
                                               uint32_t& shared, int ww, int lane) {
-  using L = Smem<D>;
+  using L = Smem<D, true>;
   constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows a load
   const int copies = copies_of(p, s);
-  const int chunk = lane % kChunks, x = ww >> 2;
+  const int chunk = lane % kChunks, halves = copies == 0 ? 2 : 1;
   const int copy_rows = copies > 1 ? kChunkHalfRows / copies : kChunkHalfRows;
-  const bool used = copies == 0 || x == 0;
-  const int tok0 = x * (p.tile_tokens / 2);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-  auto row_of = [&](int i) { return 32 * (ww & 3) + kRows * i + lane / kChunks; };
-  auto load = [&](int i) {
+  auto row_of = [&](int i) { return 32 * ww + kRows * i + lane / kChunks; };
+  auto load = [&](int x, int i) {
     const int rc = row_of(i) & (copy_rows - 1);
     const int ti = (int)((unsigned)rc / (unsigned)p.group), g = rc - ti * p.group;
-    const int tok = tok0 + ti;
-    if (!used || (ti + 1) * p.group > copy_rows || tok >= s.t.n_tok) return make_uint4(0, 0, 0, 0);
+    const int tok = x * (p.tile_tokens / 2) + ti;
+    if ((ti + 1) * p.group > copy_rows || tok >= s.t.n_tok) return make_uint4(0, 0, 0, 0);
     return __ldg(reinterpret_cast<const uint4*>(
         q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D + chunk * 8));
   };
   constexpr int kBatch = 4;
-  uint32_t top = 0;  // of the elements' magnitudes, as bf16
+  int exps[2] = {0, 0};  // of the powers of two
 #pragma unroll 1
-  for (int i = 0; i < kChunks; i += kBatch) {
-    uint4 r[kBatch];
+  for (int x = 0; x < halves; ++x) {
+    uint32_t top = 0;  // of the elements' magnitudes, as fp32
+#pragma unroll 1
+    for (int i = 0; i < kChunks; i += kBatch) {
+      uint4 r[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) r[k] = load(i + k);
+      for (int k = 0; k < kBatch; ++k) r[k] = load(x, i + k);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+      for (int k = 0; k < kBatch; ++k) {
+        const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+        for (int e = 0; e < 4; ++e)
+          top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+      }
     }
+    const int e = min(126, 14 + 127 - (int)(__reduce_max_sync(kFull, top) >> 23));
+    if (x) exps[1] = e; else exps[0] = e;
   }
-  top = __reduce_max_sync(kFull, top);
-  const int e = min(126, 14 + 127 - (int)(top >> 23));
-  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
   if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
   // (as in produce)
   if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
   if (copies == 0) shared = 0;
   if (copies > 1) shared = nseg + 1;
-  if (used) {
+#pragma unroll 1
+  for (int x = 0; x < halves; ++x) {
+    const int e = x ? exps[1] : exps[0];
+    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
     if (lane == 0)
-      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + ww] =
+      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + 4 * x + ww] =
           __uint_as_float((uint32_t)(127 - e) << 23);
     unsigned char* half = smem + L::kOffQ + x * L::kHalf + (chunk >> 3) * (kChunkHalfRows * 128);
 #pragma unroll 1
     for (int i = 0; i < kChunks; i += kBatch) {
       uint4 r[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) r[k] = load(i + k);
+      for (int k = 0; k < kBatch; ++k) r[k] = load(x, i + k);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
@@ -297,22 +310,15 @@ __device__ __forceinline__ bool widen_queries(const ChunkParams& p, const Bars<D
   return true;
 }
 
-// Keys and values: a warp takes one block of a run, 8 tokens at a time, a lane a quarter
-// of one of them.  They go where the bulk copies of a bf16 cache would have put them, in
-// the same swizzle; 8 lanes write the same 16 bytes of 8 tokens, which lie in different
-// banks.  Loads of the next run's keys (values) are in flight while this run's values
-// (the next keys) are widened.  Tokens that are not there become zeros.
+// The tiles of a run's keys, then of its values, by one warp into a ring of half runs: a
+// lane copies a block.
 template <int D>
-__device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, unsigned char* smem,
-                                      volatile int* s_meta, const volatile uint32_t* s_done,
-                                      ChunkWalk wk, int ww, int lane) {
-  using L = Smem<D>;
-  constexpr int kTile = kv4_tile_bytes(D), kWords = D / 32;  // words of a lane's quarter
-  const int row = lane & 7, part = lane >> 3;
-  uint32_t i = 0, run = 0, nseg = 0, shared = 0;
-  struct Raw {
-    uint32_t w[2][kWords], s[2];
-  };
+__device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, uint32_t smem0,
+                                            volatile int* s_meta, ChunkWalk wk, int lane,
+                                            uint32_t& issued) {
+  using L = Smem<D, true>;
+  constexpr uint32_t kTile = kv4_tile_bytes(D);
+  uint32_t run = 0, in = 0, parity = 1;
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
@@ -321,85 +327,113 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
       const int b = (s.t.kb + j * kChunkKeys) / kBlock + lane;
       return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
     };
-    // the ids of a run's blocks, -1 for those that are not there
-    auto check = [&](int ids, int j) {
+    int id = block_id(s.j0);
+#pragma unroll 1
+    for (int j = s.j0; j < s.j1; ++j) {
       const bool wanted = lane < kChunkKeys / kBlock &&
                           (long long)s.t.kb + j * kChunkKeys + lane * kBlock < s.t.ke;
-      const bool ok = wanted && ids >= 0 && ids < p.pool_blocks;
-      if (wanted && !ok && ww == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-      return ok ? ids : -1;
-    };
-    // a lane's quarters of this warp's tokens of run j
-    auto load = [&](const uint8_t* pool, int ids, int j, Raw& r) {
-      const int left = s.t.ctx - s.t.kb - j * kChunkKeys - kBlock * ww;  // tokens that are there
-      const int id = __shfl_sync(kFull, ids, ww);
-      const uint8_t* t = pool + ((size_t)(unsigned)id * p.kv_heads + s.head) * kTile;
+      const bool ok = wanted && id >= 0 && id < p.pool_blocks;
+      if (wanted && !ok) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+      const unsigned mask = __ballot_sync(kFull, ok);
+      const size_t at = ((size_t)(unsigned)id * p.kv_heads + s.head) * kTile;
+      id = j + 1 < s.j1 ? block_id(j + 1) : -1;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        r.s[q] = 0;
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) r.w[q][k] = 0;
-        const int off = 8 * q + row;
-        if (id >= 0 && off < left) {
-          if constexpr (D == 128) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(t + off * 64 + part * 16));
-            r.w[q][0] = x.x, r.w[q][1] = x.y, r.w[q][2] = x.z, r.w[q][3] = x.w;
-            r.s[q] = __ldg(reinterpret_cast<const uint16_t*>(t + 8 * D + off * 8 + part * 2));
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(t + off * 32 + part * 8));
-            r.w[q][0] = x.x, r.w[q][1] = x.y;
-            r.s[q] = __ldg(t + 8 * D + off * 4 + part);
-          }
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!warp_wait(smem0 + L::kOffTileBars + 8 * (kTileRing + in), parity)) return false;
+        const uint32_t full = smem0 + L::kOffTileBars + 8 * in;
+        if (lane == 0) {
+          // (the meta ring has room for more runs than the rings and stages hold)
+          if (kv == 0) s_meta[run % kMetaRing] = (int)mask;
+          mbar_arrive_tx(full, __popc(mask) * kTile);
         }
+        __syncwarp();
+        if (ok)
+          bulk_load(smem0 + L::kOffTiles + in * kHalfRun<D> + lane * kTile,
+                    (kv ? p.v4 : p.k4) + at, kTile, full);
+        ++issued;
+        if (++in == kTileRing) in = 0, parity ^= 1;
       }
-    };
-    auto store = [&](const Raw& r) {
-      const uint32_t slot = i % L::kStages, ph = (i / L::kStages) & 1;
-      if (!warp_wait(B.empty(slot), ph ^ 1)) return false;
-      unsigned char* stage = smem + slot * L::kStage + 2 * ww * (D / 64) * 1024 + row * 128;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint32_t sc = e4m3x2_to_half(r.s[q]);
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-          const uint32_t s2 = __byte_perm(sc, 0, k >= 2 ? 0x3232 : 0x1010);
-          uint32_t h[4];
-          e2m1x8_to_half(r.w[q][k], h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], s2);
-          const int chunk = part * kWords + k;  // 8 dimensions
-          *reinterpret_cast<uint4*>(stage + (q * (D / 64) + (chunk >> 3)) * 1024 +
-                                    (((chunk & 7) ^ row) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(B.full(slot));
-      ++i;
-      return true;
-    };
-    Raw k, v;
-    int ids = check(block_id(s.j0), s.j0);
-    load(p.k4, ids, s.j0, k);
-    load(p.v4, ids, s.j0, v);
-    int next = s.j0 + 1 < s.j1 ? block_id(s.j0 + 1) : -1;
+      ++run;
+    }
+  }
+  return true;
+}
+
+// Keys and values: a warp takes two blocks of a half run, 8 tokens at a time, a lane a
+// quarter of one of them.  They go where the bulk copies of a bf16 cache would have put
+// them, in the same swizzle; at head_dim 128 a token's upper two quarters are taken in
+// another order, so that the 8 lanes that write together do so to different banks.  Tokens
+// that are not there become zeros.
+template <int D>
+__device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>& B,
+                                      unsigned char* smem, const volatile int* s_meta,
+                                      const volatile uint32_t* s_done, ChunkWalk wk, int ww,
+                                      int lane) {
+  using L = Smem<D, true>;
+  constexpr uint32_t kTile = kv4_tile_bytes(D);
+  constexpr int kWords = D / 32;                         // words of a lane's quarter
+  constexpr int kEights = kChunkKeys / 8 / kWidenWarps;  // of tokens a half run
+  const int row = lane >> 2, part = lane & 3;
+  const uint32_t smem0 = smem_u32(smem);
+  uint32_t i = 0, run = 0, nseg = 0, shared = 0;
+  uint32_t out = 0, parity = 0;  // the ring slot to read, and its turn
+  ChunkSegment s;
+#pragma unroll 1
+  while (wk.next<kChunkKeys>(p, s)) {
     if (!widen_queries<D>(p, B, smem, s_done, s, nseg, shared, ww, lane)) return false;
     ++nseg;
 #pragma unroll 1
-    for (int j = s.j0; j < s.j1; ++j) {
-      const unsigned mask = __ballot_sync(kFull, ids >= 0);
-      // (the meta ring has room for more runs than the stages hold)
-      if (ww == 0 && lane == 0) s_meta[run % kMetaRing] = (int)mask;
-      if (!store(k)) return false;
-      const bool more = j + 1 < s.j1;
-      if (more) {
-        ids = check(next, j + 1);
-        next = j + 2 < s.j1 ? block_id(j + 2) : -1;
-        load(p.k4, ids, j + 1, k);
+    for (int h = 2 * s.j0; h < 2 * s.j1; ++h, ++i) {
+      const uint32_t full = smem0 + L::kOffTileBars + 8 * out;
+      const uint32_t slot = i % L::kStages, ph = (i / L::kStages) & 1;
+      const bool here = mbar_wait(full, parity) && mbar_wait(B.empty(slot), ph ^ 1);
+      if (!__all_sync(kFull, here)) return false;
+      const int mask = s_meta[run % kMetaRing] >> (kEights / 2 * ww);
+      // tokens that are there, of this warp's
+      const int left = s.t.ctx - s.t.kb - (h >> 1) * kChunkKeys - 8 * kEights * ww;
+      unsigned char* stage = smem + slot * L::kStage + kEights * ww * (D / 64) * 1024 + row * 128;
+      const unsigned char* tiles = smem + L::kOffTiles + out * kHalfRun<D> + kEights / 2 * ww * kTile;
+      uint32_t w[kEights][kWords], sc[kEights];
+#pragma unroll
+      for (int q = 0; q < kEights; ++q) {
+        const unsigned char* t = tiles + (q >> 1) * kTile;
+        const int off = 8 * (q & 1) + row;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(t + off * 64 + part * 16);
+          w[q][0] = x.x, w[q][1] = x.y, w[q][2] = x.z, w[q][3] = x.w;
+          sc[q] = *reinterpret_cast<const uint16_t*>(t + 8 * D + off * 8 + part * 2);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(t + off * 32 + part * 8);
+          w[q][0] = x.x, w[q][1] = x.y;
+          sc[q] = t[8 * D + off * 4 + part];
+        }
       }
-      if (!store(v)) return false;
-      if (more) load(p.v4, ids, j + 1, v);
-      ++run;
+#pragma unroll
+      for (int q = 0; q < kEights; ++q) {
+        if (8 * q + row >= left || !((mask >> (q >> 1)) & 1)) sc[q] = 0;
+        const uint32_t e = e4m3x2_to_half(sc[q]);
+        const bool swap = D == 128 && (part & 2);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          const uint32_t x = swap ? w[q][k ^ 2 % kWords] : w[q][k];
+          const uint32_t s2 = __byte_perm(e, 0, (k >= 2) != swap ? 0x3232 : 0x1010);
+          uint32_t g[4];
+          e2m1x8_to_half(x, g);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) g[n] = hmul2(g[n], s2);
+          const int chunk = part * kWords + (swap ? k ^ 2 : k);  // 8 dimensions
+          *reinterpret_cast<uint4*>(stage + (q * (D / 64) + (chunk >> 3)) * 1024 +
+                                    (((chunk & 7) ^ row) << 4)) = make_uint4(g[0], g[1], g[2], g[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();  // all lanes have read the tiles too
+      if (lane == 0) {
+        mbar_arrive(B.full(slot));
+        mbar_arrive(full + 8 * kTileRing);
+      }
+      if (++out == kTileRing) out = 0, parity ^= 1;
+      run += h & 1;
     }
   }
   return true;
@@ -415,9 +449,9 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D>& B, un
 // votes that keep a whole warp together made a turn 1740 cycles long where its
 // MMAs take 1000.
 template <int D, bool KV4>
-__device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D>& B, uint32_t smem0,
+__device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars<D, KV4>& B, uint32_t smem0,
                                           ChunkWalk wk) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   // K and V stages: tokens in groups of 8, a group's 64-dim halves one
   // 1024-byte swizzle atom after the other
   constexpr uint32_t kGroup = (D / 64) * 1024u;
@@ -687,12 +721,12 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float unit, RowSt
 }
 
 template <int D, bool CAP, bool BIAS, bool KV4>
-__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
+__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>& B,
                                        unsigned char* smem, const volatile int* s_meta,
                                        int4* s_todo, uint32_t* s_done,
                                        volatile PairWords* words, ChunkWalk wk, int warp,
                                        int lane) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   using T = __nv_bfloat16;
   const int x = warp >> 3;                     // stream
   const int hf = (warp >> 2) & 1;              // which of the pair: its half of the columns
@@ -935,11 +969,11 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D>& B,
 template <int D, bool CAP, bool BIAS, bool KV4>
 __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
     const __grid_constant__ ChunkParams p) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t smem0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Bars<D> B{smem0 + L::kOffBars};
+  const Bars<D, KV4> B{smem0 + L::kOffBars};
   volatile int* s_meta = reinterpret_cast<volatile int*>(smem + L::kOffMeta);
   volatile PairWords* s_pairs = reinterpret_cast<volatile PairWords*>(smem + L::kOffPairs);
   volatile uint32_t* s_word = reinterpret_cast<volatile uint32_t*>(smem + L::kOffWord);
@@ -950,6 +984,8 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       for (int i = 0; i < 2 * L::kStages + 2; ++i)
         mbar_init(smem0 + L::kOffBars + 8 * i,
                   KV4 && (i < L::kStages || i == 2 * L::kStages) ? kWidenWarps : 1);
+      for (int i = 0; KV4 && i < 2 * kTileRing; ++i)
+        mbar_init(smem0 + L::kOffTileBars + 8 * i, i < kTileRing ? 1 : kWidenWarps);
       mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
@@ -1001,15 +1037,19 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
     }
     ok = end == kDone;
   } else if (KV4 && warp < kSoftWarps + kWidenWarps) {
-    reg_dec<kRegsWiden>();
-    ok = widen<D>(p, B, smem, s_meta, s_done, wk, warp - kSoftWarps, lane);
+    if constexpr (KV4) {
+      reg_dec<kRegsWiden>();
+      ok = widen<D>(p, B, smem, s_meta, s_done, wk, warp - kSoftWarps, lane);
+    }
   } else if (!KV4 && warp == kSoftWarps) {
-    uint32_t i = 0, nq = 0;
-    ok = produce<D>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
-    // every copy issued lands before the CTA can end, even after a timeout
-    for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
-      (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
-    if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
+    if constexpr (!KV4) {
+      uint32_t i = 0, nq = 0;
+      ok = produce<D>(p, B, smem0, s_meta, s_done, wk, lane, i, nq);
+      // every copy issued lands before the CTA can end, even after a timeout
+      for (uint32_t k = i > (uint32_t)L::kStages ? i - L::kStages : 0; k < i; ++k)
+        (void)mbar_wait(B.full(k % L::kStages), (k / L::kStages) & 1);
+      if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
+    }
   } else {
     if (KV4) reg_dec<kRegsRest>();
     if (warp == kMmaWarp<KV4>) {
@@ -1022,6 +1062,14 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       __syncwarp();
     } else if (warp == kMmaWarp<KV4> + 1) {
       ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
+    } else if (warp == kMmaWarp<KV4> + 2) {
+      if constexpr (KV4) {
+        uint32_t issued = 0;
+        ok = fetch_tiles<D>(p, smem0, s_meta, wk, lane, issued);
+        // every copy issued lands before the CTA can end, even after a timeout
+        for (uint32_t k = issued > kTileRing ? issued - kTileRing : 0; k < issued; ++k)
+          (void)mbar_wait(smem0 + L::kOffTileBars + 8 * (k % kTileRing), (k / kTileRing) & 1);
+      }
     }
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
@@ -1036,7 +1084,7 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreads<KV4>);
-  cfg.dynamicSmemBytes = Smem<D>::kTotal;
+  cfg.dynamicSmemBytes = Smem<D, KV4>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1059,11 +1107,11 @@ template <int D, bool CAP, bool BIAS>
 cudaError_t set_attr() {
   const cudaError_t e =
       cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS, false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, false>::kTotal);
   return e != cudaSuccess
              ? e
              : cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, true>::kTotal);
 }
 
 template <int D>
