@@ -51,6 +51,9 @@ using namespace sm;
 constexpr int kWarps = 8;     // of a CTA, at most
 constexpr int kStages = 3;    // of a warp's ring
 constexpr float kLog2e = 1.4426950408889634f;
+// The running maximum of a vector that has seen nothing: below all scores, but finite, so
+// that its difference to a score has no special cases.
+constexpr float kLeast = -3e38f;
 
 template <typename T>
 struct Round;
@@ -116,21 +119,16 @@ __device__ __forceinline__ uint32_t both(uint32_t h, bool upper) {
   return __byte_perm(h, 0, upper ? 0x3232 : 0x1010);
 }
 
-// A share's walk, its next units and where their tiles are: the cursor that copies
-// run ahead with.
-struct Feed {
-  ChunkWalk wk;
-  ChunkSegment s;
-  const int32_t* table;
-  int j, ids, ids_from;  // next unit; lane's block id of the 32 blocks from ids_from on
-  bool more;
-  __device__ __forceinline__ void open(const Kv4VecParams& p) {
-    more = wk.next<kVecKeys>(p.c, s);
-    if (!more) return;
-    j = s.j0;
-    table = p.c.block_tables + (size_t)s.t.row * p.c.max_blocks;
-    ids_from = -0x40000000;
-  }
+// A warp's segments between the copies, which run ahead, and the work on them: a ring in
+// shared memory, because their registers are worth more elsewhere.  A segment has at least
+// one unit and copies are kStages units ahead at most, so that no more than kStages + 1
+// are open.
+constexpr int kSegments = 4;
+static_assert(kSegments > kStages, "segments that are open at a time");
+struct Segment {
+  int q0, n_tok, pos0, ctx;
+  int kb, j0, j1, head;
+  int tile, whole, first, valid;  // valid: 0 behind the share's last
 };
 
 template <typename T, int D, int NT, bool CAP, bool BIAS>
@@ -143,42 +141,68 @@ struct Worker {
   const Kv4VecParams& p;
   int lane, g, t;       // g: MMA row or column, t: its pair
   uint32_t ring, bars;  // shared-memory addresses
+  Segment* segments;
   int head;             // within a group of heads
-  uint32_t issued, used;
-  uint32_t valid;       // two bits a stage: blocks that hold something
-  Feed feed;
+  // The copies' side: the walk, what its segment has left, and the ring's next stage.
+  ChunkWalk wk;
+  const int32_t* table;
+  const uint8_t* pool;  // lanes 0 and 1: keys, 2 and 3: values; of the segment's KV head
+  int block, block_end, units;  // next block, one past the last that any vector sees
+  int ids, ids_from;    // the lane's block id of the 32 from ids_from on
+  uint32_t fill, opened;
+  uint32_t at, parity;  // the stage that is next to be worked on, and its turn
+  uint32_t missing;     // two bits a stage: blocks that are not there though they should be
 
   __device__ __forceinline__ Worker(const Kv4VecParams& p_) : p(p_) {}
 
+  // The next segment of the share.
+  __device__ __forceinline__ void open() {
+    ChunkSegment s;
+    const bool more = wk.next<kVecKeys>(p.c, s);
+    Segment* e = segments + opened % kSegments;
+    ++opened;
+    units = 0;
+    if (lane == 0) {
+      e->valid = more;
+      if (more) {
+        e->q0 = s.t.q0, e->n_tok = s.t.n_tok, e->pos0 = s.t.pos0, e->ctx = s.t.ctx;
+        e->kb = s.t.kb, e->j0 = s.j0, e->j1 = s.j1, e->head = s.head;
+        e->tile = s.tile, e->whole = s.first && s.last, e->first = s.first;
+      }
+    }
+    if (!more) return;
+    units = s.j1 - s.j0;
+    block = s.t.kb / kBlock + 2 * s.j0;
+    block_end = (int)((unsigned)(s.t.ke + kBlock - 1) / kBlock);
+    table = p.c.block_tables + (size_t)s.t.row * p.c.max_blocks;
+    pool = (lane < 2 ? p.k_pool : p.v_pool) +
+           (size_t)((s.head / p.subs) * p.heads_per_worker + head) * R::kTile;
+    ids_from = block - 32;
+  }
+
   // Copies of the next unit into the ring, if there is one.
   __device__ __forceinline__ void issue() {
-    if (!feed.more) return;
-    const ChunkSegment& s = feed.s;
-    const int b0 = s.t.kb / kBlock + 2 * feed.j;
-    if (b0 - feed.ids_from >= 32) {
-      const int b = b0 + lane;
-      feed.ids = (long long)b * kBlock < s.t.ke ? __ldg(feed.table + b) : -1;
-      feed.ids_from = b0;
+    if (units == 0) return;
+    if (block - ids_from >= 32) {
+      ids = block + lane < block_end ? __ldg(table + block + lane) : -1;
+      ids_from = block;
     }
-    const int which = lane & 1;
-    const int b = b0 + which;
-    const int id = __shfl_sync(kFull, feed.ids, b - feed.ids_from);
-    const bool wanted = (long long)b * kBlock < s.t.ke;
-    const bool ok = wanted && id >= 0 && id < p.c.pool_blocks;
-    if (wanted && !ok && lane < 2) atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-    const uint32_t mask = __ballot_sync(kFull, ok) & 3u;
-    const uint32_t slot = issued % kStages, bar = bars + 8 * slot;
+    const int b = block + (lane & 1);
+    const int id = __shfl_sync(kFull, ids, b - ids_from);
+    const bool ok = b < block_end && id >= 0 && id < p.c.pool_blocks;
+    const uint32_t mask = __ballot_sync(kFull, ok) & 3u, bar = bars + 8 * fill;
     if (lane == 0) mbar_arrive_tx(bar, __popc(mask) * 2 * R::kTile);
     __syncwarp();
-    if (lane < 4 && ok) {
-      const int kv_head = (s.head / p.subs) * p.heads_per_worker + head;
-      const uint8_t* pool = lane < 2 ? p.k_pool : p.v_pool;
-      bulk_load(ring + slot * R::kStage + lane * R::kTile,
-                pool + ((size_t)id * p.kv_heads + kv_head) * R::kTile, R::kTile, bar);
+    if (lane < 4 && ok)
+      bulk_load(ring + fill * R::kStage + lane * R::kTile,
+                pool + (size_t)(unsigned)id * ((unsigned)p.kv_heads * R::kTile), R::kTile, bar);
+    if (mask != 3u) {  // past the last block, or a bad one
+      if (b < block_end && !ok && lane < 2) atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+      missing |= (mask ^ 3u) << (2 * fill);
     }
-    valid = (valid & ~(3u << (2 * slot))) | (mask << (2 * slot));
-    ++issued;
-    if (++feed.j == s.j1) feed.open(p);
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    block += 2;
+    if (--units == 0) open();
   }
 
   // Scores of a block: c[nt], rows are tokens, columns query vectors.
@@ -227,59 +251,68 @@ struct Worker {
     }
   }
 
-  // o += V^T P of two blocks: rows are dimensions (lane g holds D / 8 that lie
-  // together), columns query vectors; dead: a bit for each of a lane's tokens (four a
-  // block) that holds nothing.
+  // A block's values as operands: rows are dimensions (lane g holds D / 8 that lie
+  // together), k indices tokens.  x[i][h]: a byte holds one dimension of two tokens, the k
+  // pair of an operand (h: even dimensions of the first and odd ones of the first, then of
+  // the second pair of tokens); e: the pairs' scales.  dead: a bit for each of a lane's four
+  // tokens that holds nothing.
+  static constexpr int kWords = D / 64;  // words of a lane's dimensions of one token
+  __device__ __forceinline__ void load_values(uint32_t tile, uint32_t dead,
+                                              uint32_t (&x)[kWords][4], uint32_t (&e2)[2]) const {
+    const uint32_t sc = tile + kv4_number_bytes(D);
+    uint32_t w[4][kWords], e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = ((2 * t + (j & 1)) ^ (t & 1)) + (j & 2) * 4;
+      if constexpr (D == 128) {
+        const uint2 v = lds64(tile + tok * 64 + g * 8);
+        w[j][0] = v.x, w[j][1] = v.y;
+        e[j] = lds8(sc + tok * 8 + g);
+      } else {
+        w[j][0] = lds32(tile + tok * 32 + g * 4);
+        e[j] = lds8(sc + tok * 4 + g / 2);
+      }
+    }
+    if (dead) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((dead >> j) & 1) e[j] = 0;
+    }
+    e2[0] = e4m3x2_to_half(e[0] | (e[1] << 8));
+    e2[1] = e4m3x2_to_half(e[2] | (e[3] << 8));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a = w[2 * h][i], c = w[2 * h + 1][i];
+        x[i][2 * h] = (a & 0x0f0f0f0fu) | ((c << 4) & 0xf0f0f0f0u);
+        x[i][2 * h + 1] = ((a >> 4) & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u);
+      }
+  }
+  static __device__ __forceinline__ void widen_values(const uint32_t (&x)[4],
+                                                      const uint32_t (&e2)[2],
+                                                      uint32_t (&a)[4][4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      e2m1x8_to_half(x[h], a[h]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[h][k] = hmul2(a[h][k], e2[h / 2]);
+    }
+  }
+
+  // o += V^T P of two blocks, columns are query vectors; dead: four bits a block.
   __device__ __forceinline__ void values(uint32_t tile,
                                          const uint32_t (&pb)[2][kParts][NT][2], uint32_t dead,
                                          float (&o)[kSteps][NT][4]) const {
-    constexpr int kWords = D / 64;  // words of a lane's dimensions of one token
-    uint32_t x[2][kWords][4], s[2][2];
+    if constexpr (kParts == 1) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint32_t base = tile + b * R::kTile, sc = base + kv4_number_bytes(D);
-      uint32_t w[4][kWords], e[4];
+      for (int b = 0; b < 2; ++b) {
+        uint32_t x[kWords][4], e2[2];
+        load_values(tile + b * R::kTile, dead >> (4 * b), x, e2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tok = ((2 * t + (j & 1)) ^ (t & 1)) + (j & 2) * 4;
-        if constexpr (D == 128) {
-          const uint2 v = lds64(base + tok * 64 + g * 8);
-          w[j][0] = v.x, w[j][1] = v.y;
-          e[j] = lds8(sc + tok * 8 + g);
-        } else {
-          w[j][0] = lds32(base + tok * 32 + g * 4);
-          e[j] = lds8(sc + tok * 4 + g / 2);
-        }
-      }
-      if (dead) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if ((dead >> (4 * b + j)) & 1) e[j] = 0;
-      }
-      s[b][0] = e4m3x2_to_half(e[0] | (e[1] << 8));
-      s[b][1] = e4m3x2_to_half(e[2] | (e[3] << 8));
-      // a byte of x: one dimension of two tokens, the k pair of an MMA operand
-#pragma unroll
-      for (int i = 0; i < kWords; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = w[2 * h][i], c = w[2 * h + 1][i];
-          x[b][i][2 * h] = (a & 0x0f0f0f0fu) | ((c << 4) & 0xf0f0f0f0u);      // even dimensions
-          x[b][i][2 * h + 1] = ((a >> 4) & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u);  // odd ones
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      if constexpr (kParts == 1) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int i = 0; i < kWords; ++i) {
           uint32_t a[4][4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            e2m1x8_to_half(x[b][i][h], a[h]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[h][k] = hmul2(a[h][k], s[b][h / 2]);
-          }
+          widen_values(x[i], e2, a);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -287,9 +320,16 @@ struct Worker {
               mma(o[4 * i + k][nt], a[0][k], a[1][k], a[2][k], a[3][k], pb[b][0][nt][0],
                   pb[b][0][nt][1]);
         }
-      } else {
-        // The tensor core's accumulator drops what it does not hold, always towards
-        // zero: each unit's sum starts at zero and is added up rounded.
+      }
+    } else {
+      // The tensor core's accumulator drops what it does not hold, always towards zero:
+      // each unit's sum starts at zero and is added up rounded.
+      uint32_t x[2][kWords][4], e2[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        load_values(tile + b * R::kTile, dead >> (4 * b), x[b], e2[b]);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
         float sum[4][NT][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -300,12 +340,7 @@ struct Worker {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t a[4][4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            e2m1x8_to_half(x[b][i][h], a[h]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[h][k] = hmul2(a[h][k], s[b][h / 2]);
-          }
+          widen_values(x[b][i], e2[b], a);
 #pragma unroll
           for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
@@ -327,28 +362,32 @@ struct Worker {
 
   // The whole share; false when a wait gave up.
   __device__ __forceinline__ bool run(int worker) {
-    feed.wk.init(p.c, worker);
-    ChunkWalk wk = feed.wk;
-    feed.open(p);
-    issued = used = valid = 0;
+    wk.init(p.c, worker);
+    opened = fill = missing = at = parity = 0;
+    open();
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue();
 
-    ChunkSegment s;
 #pragma unroll 1
-    while (wk.next<kVecKeys>(p.c, s)) {
-      const int sub = s.head % p.subs;
-      const int kv_head = (s.head / p.subs) * p.heads_per_worker + head;
+    for (uint32_t taken = 0;; ++taken) {
+      __syncwarp();
+      const volatile Segment* s = segments + taken % kSegments;
+      if (!s->valid) return true;
+      const int sub = s->head % p.subs;
+      const int kv_head = (s->head / p.subs) * p.heads_per_worker + head;
       const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
-      const int vecs = s.t.n_tok * per;
+      const int vecs = s->n_tok * per;
       const int h0 = kv_head * p.c.group + sub * kVecs;  // first query head
       auto row_of = [&](int v) {  // of query vector v, in q and out
         const int tok = v / per;
-        return ((size_t)s.t.q0 + tok) * p.c.heads + h0 + (v - tok * per);
+        return ((size_t)s->q0 + tok) * p.c.heads + h0 + (v - tok * per);
       };
-      // the query vectors as operands, and what brings their scores to log2 units
+      // the query vectors as operands, and what brings their scores to log2 units (the
+      // scale's sign goes with the vectors)
       uint32_t q[kParts][NT][kSteps][2];
-      float up[NT];  // lane's vector g of each column tile
+      float mul[NT][2];
+      const float k_unit =
+          fabsf(CAP ? p.c.scale : p.c.qscale) * (p.k_scales ? __ldg(p.k_scales + kv_head) : 1.f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int v = 8 * nt + g;
@@ -383,11 +422,11 @@ struct Worker {
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
         // top * 2^e in [2^14, 2^15), as far as 2^e is in range
         const int e = min(126, 14 + 127 - (int)(__float_as_uint(top) >> 23));
-        const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-        up[nt] = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), p.c.scale);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int i = 0; i < D / 4; i += 2) {
-          const float a = x[i] * mul, b = x[i + 1] * mul;
+          const float a = x[i] * up, b = x[i + 1] * up;
           const uint32_t h = pack_half(a, b);
           q[0][nt][i / 4][(i / 2) & 1] = h;
           if constexpr (kParts == 2) {
@@ -395,34 +434,38 @@ struct Worker {
             q[kParts - 1][nt][i / 4][(i / 2) & 1] = pack_half(a - f.x, b - f.y);
           }
         }
+        // (never 0: what is not seen, -inf, has to stay that)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          mul[nt][c] =
+              fmaxf(k_unit * __shfl_sync(kFull, down, 4 * (2 * t + c)), 1.17549435e-38f);
       }
-      // of the two columns of each column tile that this lane's scores are in
-      const float k_unit = p.k_scales ? __ldg(p.k_scales + kv_head) : 1.f;
-      float mul[NT][2], slope[NT][2], m[NT][2], l[NT][2], comp[NT][2];
-      int lo[NT][2], hi[NT][2], pos[NT][2];
-      int lo_all = 0, hi_all = 0x7fffffff;
+      // of the two columns of each column tile that this lane's scores are in: token,
+      // position, what it sees
+      auto token_of = [&](int nt, int c) { return (8 * nt + 2 * t + c) / per; };
+      auto sees = [&](int nt, int c) {
+        const int tok = token_of(nt, c);
+        return 8 * nt + 2 * t + c < vecs
+                   ? chunk_sees(p.c, (long long)s->q0 + tok, s->pos0 + tok, s->ctx)
+                   : make_int2(0, 0x7fffffff);
+      };
+      float m[NT][2], l[NT][2], comp[NT][2], slope[NT][2];
+      int pos[NT][2];
+      int lo_all = 0, hi_all = 0x7fffffff;  // positions that all vectors see
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int v = 8 * nt + 2 * t + c;
-          const float u = __shfl_sync(kFull, up[nt], 4 * (2 * t + c));
-          mul[nt][c] = (CAP ? p.c.scale : p.c.qscale) * k_unit * u;
-          slope[nt][c] = 0.f;
-          m[nt][c] = -INFINITY;
+          m[nt][c] = kLeast;
           l[nt][c] = comp[nt][c] = 0.f;
-          const int tok = v / per;
-          pos[nt][c] = s.t.pos0 + tok;
-          lo[nt][c] = 0;
-          hi[nt][c] = 0x7fffffff;
-          if (v < vecs) {
-            const int2 see = chunk_sees(p.c, (long long)s.t.q0 + tok, pos[nt][c], s.t.ctx);
-            lo[nt][c] = see.x;
-            hi[nt][c] = see.y;
-            if (BIAS) slope[nt][c] = __ldg(p.c.slopes + h0 + (v - tok * per)) * kLog2e;
+          if constexpr (BIAS) {
+            const int v = 8 * nt + 2 * t + c, tok = token_of(nt, c);
+            pos[nt][c] = s->pos0 + tok;
+            slope[nt][c] = v < vecs ? __ldg(p.c.slopes + h0 + (v - tok * per)) * kLog2e : 0.f;
           }
-          lo_all = max(lo_all, lo[nt][c]);
-          hi_all = min(hi_all, hi[nt][c]);
+          const int2 see = sees(nt, c);
+          lo_all = max(lo_all, see.x);
+          hi_all = min(hi_all, see.y);
         }
       lo_all = __reduce_max_sync(kFull, lo_all);
       hi_all = __reduce_min_sync(kFull, hi_all);
@@ -434,54 +477,59 @@ struct Worker {
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
 
+      int t0 = s->kb + s->j0 * kVecKeys;
 #pragma unroll 1
-      for (int j = s.j0; j < s.j1; ++j) {
+      for (int n = s->j1 - s->j0; n > 0; --n, t0 += kVecKeys) {
         issue();  // into the stage that the unit before last was in
-        const uint32_t slot = used % kStages;
-        if (!warp_wait(bars + 8 * slot, (used / kStages) & 1)) return false;
-        const uint32_t stage = ring + slot * R::kStage;
-        const int t0 = s.t.kb + j * kVecKeys;
-        const uint32_t have = (valid >> (2 * slot)) & 3u;
+        if (!warp_wait(bars + 8 * at, parity)) return false;
+        const uint32_t stage = ring + at * R::kStage;
         float x[2][NT][4];
 #pragma unroll
         for (int b = 0; b < 2; ++b) scores(stage + b * R::kTile, q, x[b]);
-        const bool dense = have == 3u && t0 >= lo_all && hi_all - t0 >= kVecKeys;
         const int row = g ^ ((g >> 1) & 1);  // this lane's first token within a block
-        uint32_t dead = 0;
-        // to log2 units; what is not seen to -inf
+        if constexpr (CAP || BIAS) {         // to log2 units
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = i & 1;
-              float y = x[b][nt][i] * mul[nt][c];
-              if (CAP) y = p.c.cap * kLog2e * tanhf(y / p.c.cap);
-              if (BIAS) {
-                const int rel = b * kBlock + row + (i & 2) * 4;
-                y -= slope[nt][c] * fabsf((float)(pos[nt][c] - t0 - rel));
-              }
-              x[b][nt][i] = y;
-            }
-        if (!dense) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int c = i & 1;
-                const int rel = b * kBlock + row + (i & 2) * 4;
-                if (!((have >> b) & 1) || rel < lo[nt][c] - t0 || rel >= hi[nt][c] - t0)
-                  x[b][nt][i] = -INFINITY;
+                float y = x[b][nt][i] * mul[nt][c];
+                if (CAP) y = p.c.cap * kLog2e * tanhf(y / p.c.cap);
+                if (BIAS) {
+                  const int rel = b * kBlock + row + (i & 2) * 4;
+                  y -= slope[nt][c] * fabsf((float)(pos[nt][c] - t0 - rel));
+                }
+                x[b][nt][i] = y;
               }
+        }
+        uint32_t dead = 0;
+        if (missing || t0 < lo_all || hi_all - t0 < kVecKeys) {  // what is not seen
+          const uint32_t gone = (missing >> (2 * at)) & 3u;
+          missing &= ~(3u << (2 * at));
+          const int ctx = s->ctx;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int2 see = sees(nt, c);
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int rel = b * kBlock + row + 8 * h;
+                  if (((gone >> b) & 1) || rel < see.x - t0 || rel >= see.y - t0)
+                    x[b][nt][2 * h + c] = -INFINITY;
+                }
+            }
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int rel = b * kBlock + ((2 * t + (k & 1)) ^ (t & 1)) + (k & 2) * 4;
-              if (!((have >> b) & 1) || rel >= s.t.ctx - t0) dead |= 1u << (4 * b + k);
+              if (((gone >> b) & 1) || rel >= ctx - t0) dead |= 1u << (4 * b + k);
             }
-          }
         }
         // the running maxima
         float mx[NT][2];
@@ -490,7 +538,9 @@ struct Worker {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            mx[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+            mx[nt][c] =
+                fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+            if (!CAP && !BIAS) mx[nt][c] *= mul[nt][c];
             raise |= mx[nt][c] > m[nt][c] + Round<T>::kSlack;
           }
         if (__any_sync(kFull, raise)) {
@@ -501,9 +551,9 @@ struct Worker {
               float y = mx[nt][c];
 #pragma unroll
               for (int d = 4; d < 32; d *= 2) y = fmaxf(y, __shfl_xor_sync(kFull, y, d));
-              const bool up_here = y > m[nt][c];
-              const float alpha = up_here ? ex2_approx(m[nt][c] - y) : 1.f;
-              if (up_here) m[nt][c] = y;
+              y = fmaxf(y, m[nt][c]);
+              const float alpha = ex2_approx(m[nt][c] - y);
+              m[nt][c] = y;
               l[nt][c] *= alpha;
               comp[nt][c] *= alpha;
 #pragma unroll
@@ -519,13 +569,14 @@ struct Worker {
         for (int nt = 0; nt < NT; ++nt) {
           float neg[2], sum[2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            neg[c] = m[nt][c] == -INFINITY ? 0.f : Round<T>::kUp - m[nt][c];
+          for (int c = 0; c < 2; ++c) neg[c] = Round<T>::kUp - m[nt][c];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             float w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ex2_approx(x[b][nt][i] + neg[i & 1]);
+            for (int i = 0; i < 4; ++i)
+              w[i] = ex2_approx(CAP || BIAS ? x[b][nt][i] + neg[i & 1]
+                                            : fmaf(x[b][nt][i], mul[nt][i & 1], neg[i & 1]));
 #pragma unroll
             for (int c = 0; c < 2; ++c) sum[c] = b ? sum[c] + (w[c] + w[c + 2]) : w[c] + w[c + 2];
 #pragma unroll
@@ -539,24 +590,29 @@ struct Worker {
               }
             }
           }
-          // (compensated: nearly equal weights round the same way each time)
+          // (fp32's is compensated: nearly equal weights round the same way each time)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float y = sum[c] - comp[nt][c];
-            const float z = l[nt][c] + y;
-            comp[nt][c] = (z - l[nt][c]) - y;
-            l[nt][c] = z;
+            if constexpr (kParts == 1) {
+              l[nt][c] += sum[c];
+            } else {
+              const float y = sum[c] - comp[nt][c];
+              const float z = l[nt][c] + y;
+              comp[nt][c] = (z - l[nt][c]) - y;
+              l[nt][c] = z;
+            }
           }
         }
         values(stage + 2 * R::kTile, pb, dead, o);
-        ++used;
+        at = at + 1 == kStages ? 0 : at + 1;
+        if (at == 0) parity ^= 1;
         __syncwarp();  // all lanes have read the stage
       }
 
       // The sums over the lanes that share a column; then the result or the piece.
-      const bool whole = s.first && s.last;
+      const bool whole = s->whole;
       const float v_unit = p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f;
-      const int slot = 2 * worker + (s.first ? 1 : 0);
+      const int slot = 2 * worker + (s->first ? 1 : 0);
       const size_t state = ((size_t)slot * p.heads_per_worker + head) * kVecs;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -594,12 +650,11 @@ struct Worker {
                   o[i][nt][c], o[i][nt][c + 2], o[i + 1][nt][c], o[i + 1][nt][c + 2]);
           }
         }
-      if (!whole && s.first && head == 0) {
+      if (!whole && s->first && head == 0) {
         // how many workers the tile's pieces are on: those that start at or before
         // its last unit's first
-        const long long last =
-            s.head * __ldcg(p.c.ws_head) + __ldcg(p.c.ws_prefix + s.tile) +
-            (long long)(p.c.tile_cost + chunk_runs(s.t.kb, s.t.ke, kVecKeys) - 1) * s.t.cost;
+        const long long last = s->head * __ldcg(p.c.ws_head) +
+                               __ldcg(p.c.ws_prefix + s->tile + 1) - 1;
         int n = 0;
 #pragma unroll 1
         for (int c = worker; c < p.c.grid; c += 32) {
@@ -608,10 +663,9 @@ struct Worker {
           n += __popc(in);
           if (in != kFull) break;
         }
-        if (lane == 0) p.todo[worker] = make_int4(s.t.q0, s.t.n_tok, s.head, n);
+        if (lane == 0) p.todo[worker] = make_int4(s->q0, s->n_tok, s->head, n);
       }
     }
-    return true;
   }
 };
 
@@ -625,11 +679,13 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
     kv4_vec_kernel(const __grid_constant__ Kv4VecParams p) {
   using R = Ring<D>;
   extern __shared__ __align__(128) unsigned char smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const uint32_t base = smem_u32(smem);
-  const uint32_t bars = base + (blockDim.x >> 5) * R::kWarp + warp * kStages * 8;
+  const uint32_t segments = warps * R::kWarp, bars = segments + warps * kSegments * sizeof(Segment);
+  Worker<T, D, NT, CAP, BIAS> w(p);
+  w.bars = base + bars + warp * kStages * 8;
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(w.bars + 8 * i, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -637,19 +693,21 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   griddep_launch();
   const int worker = blockIdx.x * p.workers_per_cta + warp / p.heads_per_worker;
   if (worker >= p.c.grid) return;
-  Worker<T, D, NT, CAP, BIAS> w(p);
   w.lane = lane;
   w.g = lane >> 2;
   w.t = lane & 3;
   w.ring = base + warp * R::kWarp;
-  w.bars = bars;
+  w.segments = reinterpret_cast<Segment*>(smem + segments) + warp * kSegments;
   w.head = warp % p.heads_per_worker;
   if (w.head == 0 && lane == 0) p.todo[worker] = make_int4(0, 0, 0, 0);
   if (!w.run(worker)) {
     if (lane == 0) atomicOr(p.c.status, (uint32_t)NSV_DEV_TIMEOUT);
     // every copy issued lands before the CTA can end
-    for (uint32_t i = w.used; i < w.issued; ++i)
-      (void)warp_wait(bars + 8 * (i % kStages), (i / kStages) & 1);
+    do {
+      (void)warp_wait(w.bars + 8 * w.at, w.parity);
+      w.at = w.at + 1 == kStages ? 0 : w.at + 1;
+      if (w.at == 0) w.parity ^= 1;
+    } while (w.at != w.fill);
   }
 }
 
@@ -670,7 +728,7 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ 
   const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
   const float v_unit = p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f;
   for (int v = threadIdx.x >> 5; v < todo.y * per; v += 4) {
-    float M = -INFINITY, L = 0.f, a[D / 32];
+    float M = kLeast, L = 0.f, a[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) a[k] = 0.f;
     constexpr int kAhead = 8;
@@ -696,7 +754,6 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ 
       float top = M;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
-      if (top == -INFINITY) continue;
       const float keep = ex2_approx(M - top);
       M = top;
       L *= keep;
@@ -704,7 +761,7 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ 
       for (int k = 0; k < D / 32; ++k) a[k] *= keep;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (b + i >= todo.w || ml[i].x == -INFINITY) continue;
+        if (b + i >= todo.w) continue;
         const float w = ex2_approx(ml[i].x - M);
         L = fmaf(w, ml[i].y, L);
 #pragma unroll
@@ -742,7 +799,7 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 
 template <int D>
 constexpr int smem_bytes(int warps) {
-  return warps * (int)(Ring<D>::kWarp + kStages * 8);
+  return warps * (int)(Ring<D>::kWarp + kSegments * sizeof(Segment) + kStages * 8);
 }
 
 template <typename T, int D, int NT, bool CAP, bool BIAS>
