@@ -553,9 +553,10 @@ typedef struct nsv_rope {
  *   write_slots   [tokens] int64, rules as in nsv_kv_write (a padded token names the
  *                 sink slot)
  *
- * Results are rounded once to the element type.  Uses num_heads (at most 2^20),
- * num_kv_heads, head_dim, block_size, num_blocks and dtype of the shape (the rest must
- * be valid).  0 <= tokens < 2^30.  Asynchronous, without workspace; may be captured.
+ * Results are rounded once to the element type.  Uses num_heads, num_kv_heads, head_dim,
+ * block_size, num_blocks and dtype of the shape (the rest must be valid).  0 <= tokens <
+ * 2^30, tokens * (num_heads + 2 num_kv_heads) < 2^34.  Asynchronous, without workspace; may
+ * be captured.
  */
 NSV_API int nsv_rope_write(const nsv_shape *shape, const nsv_rope *rope, int64_t tokens,
                            const void *q, const void *k_new, const void *v_new,
@@ -573,7 +574,7 @@ NSV_API int nsv_rope_write(const nsv_shape *shape, const nsv_rope *rope, int64_t
  * s = e4m3(max |y| / 6) and the numbers e2m1(y / s), zeros where s is 0; keys are
  * taken from the fp32 rotation.  Quotients are rounded to fp32, conversions to nearest
  * even, saturating (|y| beyond 2688 becomes that).  x must be finite, and k_scales and
- * v_scales positive and finite: choose them so that y lies around 1, because a scale
+ * v_scales within 2^-60 .. 2^60: choose them so that y lies around 1, because a scale
  * below 2^-6 has fewer digits and one below 2^-10 is 0.
  *
  * shape.dtype is the type of q, k_new, v_new and q_out.  rope NULL: nothing is rotated,

@@ -72,8 +72,9 @@ int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, cons
       !stride_of(s, k_stride, s->num_kv_heads, &p->k_stride) ||
       !stride_of(s, v_stride, s->num_kv_heads, &p->v_stride))
     return NSV_ERR_SHAPE;
-  // a token's units and their products stay within 32 bits
-  if (s->num_heads > (1 << 20)) return NSV_ERR_SHAPE;
+  // (a warp for a part of a token's heads; a grid holds 2^31 - 1 CTAs of eight)
+  if (tokens * ((int64_t)s->num_heads + 2 * (int64_t)s->num_kv_heads) >= (int64_t(1) << 34))
+    return NSV_ERR_SHAPE;
   DeviceInfo d;
   if ((rc = device_info(&d)) != NSV_OK) return rc;
   p->q = q;

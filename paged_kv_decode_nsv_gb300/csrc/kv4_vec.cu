@@ -77,34 +77,14 @@ struct Ring {
   static constexpr uint32_t kWarp = kStages * kStage;
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
+// Shared memory by its 32-bit address, as ordinary loads (which barriers order).
+template <typename V>
+__device__ __forceinline__ V lds(uint32_t a) {
+  return *static_cast<const V*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -112,7 +92,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t both(uint32_t h, bool upper) {
@@ -213,19 +193,19 @@ struct Worker {
     uint32_t w[2][D / 32];  // a lane's numbers of its two tokens
     uint32_t s[2][D / 64];  // their scales, doubled
     if constexpr (D == 128) {
-      const uint4 a = lds128(tile + r0 * 64 + t * 16), b = lds128(tile + r1 * 64 + t * 16);
+      const uint4 a = lds<uint4>(tile + r0 * 64 + t * 16), b = lds<uint4>(tile + r1 * 64 + t * 16);
       w[0][0] = a.x, w[0][1] = a.y, w[0][2] = a.z, w[0][3] = a.w;
       w[1][0] = b.x, w[1][1] = b.y, w[1][2] = b.z, w[1][3] = b.w;
-      const uint32_t e = e4m3x2_to_half(lds16(sc + r0 * 8 + 2 * t));
-      const uint32_t f = e4m3x2_to_half(lds16(sc + r1 * 8 + 2 * t));
+      const uint32_t e = e4m3x2_to_half(lds<uint16_t>(sc + r0 * 8 + 2 * t));
+      const uint32_t f = e4m3x2_to_half(lds<uint16_t>(sc + r1 * 8 + 2 * t));
       s[0][0] = both(e, false), s[0][1] = both(e, true);
       s[1][0] = both(f, false), s[1][1] = both(f, true);
     } else {
-      const uint2 a = lds64(tile + r0 * 32 + t * 8), b = lds64(tile + r1 * 32 + t * 8);
+      const uint2 a = lds<uint2>(tile + r0 * 32 + t * 8), b = lds<uint2>(tile + r1 * 32 + t * 8);
       w[0][0] = a.x, w[0][1] = a.y;
       w[1][0] = b.x, w[1][1] = b.y;
-      s[0][0] = both(e4m3x2_to_half(lds8(sc + r0 * 4 + t)), false);
-      s[1][0] = both(e4m3x2_to_half(lds8(sc + r1 * 4 + t)), false);
+      s[0][0] = both(e4m3x2_to_half(lds<uint8_t>(sc + r0 * 4 + t)), false);
+      s[1][0] = both(e4m3x2_to_half(lds<uint8_t>(sc + r1 * 4 + t)), false);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -265,12 +245,12 @@ struct Worker {
     for (int j = 0; j < 4; ++j) {
       const int tok = ((2 * t + (j & 1)) ^ (t & 1)) + (j & 2) * 4;
       if constexpr (D == 128) {
-        const uint2 v = lds64(tile + tok * 64 + g * 8);
+        const uint2 v = lds<uint2>(tile + tok * 64 + g * 8);
         w[j][0] = v.x, w[j][1] = v.y;
-        e[j] = lds8(sc + tok * 8 + g);
+        e[j] = lds<uint8_t>(sc + tok * 8 + g);
       } else {
-        w[j][0] = lds32(tile + tok * 32 + g * 4);
-        e[j] = lds8(sc + tok * 4 + g / 2);
+        w[j][0] = lds<uint32_t>(tile + tok * 32 + g * 4);
+        e[j] = lds<uint8_t>(sc + tok * 4 + g / 2);
       }
     }
     if (dead) {

@@ -24,8 +24,8 @@
 namespace nsv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHeadsPerThread = 4;
+constexpr int kThreads = 128;
+constexpr int kPasses = 2;  // heads of a lane whose loads go out together
 
 // 16 bytes of elements as fp32, and back.
 template <typename T>
@@ -75,246 +75,252 @@ __device__ __forceinline__ void load_f32(const float* p, float* x) {
   }
 }
 
-// What a thread that moves one pair of 16-byte vectors of a head does to it: which
-// vectors they are, and its cosines and sines.  Halves: vectors i and i + R/2 of
-// the rotated dimensions; interleaved and unrotated ones: 2i and 2i + 1.
+// 8 elements of a head: what a lane holds of one.
 template <typename T>
-struct Pair {
-  static constexpr int N = Vec<T>::N;
-  int v0, v1;
-  bool turn;
-  float c[N], s[N];
-  __device__ __forceinline__ void init(const RopeParams& p, int item, const float* row) {
-    const int half = p.rotary_dim / (2 * N);  // vectors of half the rotated dimensions
-    turn = item < half;
-    v0 = 2 * item, v1 = 2 * item + 1;
-    if (turn) {
-      if (!p.interleaved) v0 = item, v1 = item + half;
-      load_f32<N>(row + item * N, c);
-      load_f32<N>(row + p.rotary_dim / 2 + item * N, s);
-    }
+struct Eight {
+  static constexpr int N = 8 / Vec<T>::N;
+  uint4 r[N];
+  __device__ __forceinline__ void load(const T* x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const uint4*>(x)[i];
   }
-  __device__ __forceinline__ void apply(const RopeParams& p, uint4& r0, uint4& r1) const {
-    if (!turn) return;
-    float x[N], y[N];
-    Vec<T>::unpack(r0, x);
-    Vec<T>::unpack(r1, y);
-    if (p.interleaved) {
+  __device__ __forceinline__ void store(T* x) const {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float a = x[i], b = x[i + 1], d = y[i], e = y[i + 1];
-        x[i] = turn_a(a, b, c[i / 2], s[i / 2]);
-        x[i + 1] = turn_b(a, b, c[i / 2], s[i / 2]);
-        y[i] = turn_a(d, e, c[N / 2 + i / 2], s[N / 2 + i / 2]);
-        y[i + 1] = turn_b(d, e, c[N / 2 + i / 2], s[N / 2 + i / 2]);
-      }
-    } else {
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(x)[i] = r[i];
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float a = x[i], b = y[i];
-        x[i] = turn_a(a, b, c[i], s[i]);
-        y[i] = turn_b(a, b, c[i], s[i]);
-      }
-    }
-    r0 = Vec<T>::pack(x);
-    r1 = Vec<T>::pack(y);
+    for (int i = 0; i < N; ++i) r[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* y) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) Vec<T>::unpack(r[i], y + i * Vec<T>::N);
+  }
+  __device__ __forceinline__ void set(const float* y) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = Vec<T>::pack(y + i * Vec<T>::N);
   }
 };
 
-// The row of the table for a token: null without rotation; *ok false (and flagged
-// by `flag`) for a position that has none.
-__device__ __forceinline__ const float* table_row(const RopeParams& p, long long token, bool flag,
-                                                  bool* ok) {
-  *ok = true;
-  if (!p.positions) return nullptr;
-  const int pos = __ldg(p.positions + token);
-  if (pos < 0 || pos >= p.num_positions) {
-    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_POS);
-    *ok = false;
-    return nullptr;
+// What a lane holds of a head: dimensions 8 u .. and 8 v .., and what the rotation does to
+// them.  kPairs: halves, v is u's partner.  kOwn: interleaved or not rotated, u and v lie
+// together.  kApart: halves of which a scale's 16 dimensions do not lie in one; u and v lie
+// together, and their partners are loaded besides.
+enum : int { kPairs, kOwn, kApart };
+template <typename T>
+struct Turn {
+  int u, v, mode;
+  bool turn;
+  float c[8], s[8];
+  // The lane's place: `l` counts the head's lanes, of 16 dimensions each.
+  __device__ __forceinline__ void place(const RopeParams& p, int l, bool four) {
+    const int half = p.rotary_dim / 16;
+    mode = p.interleaved || l >= half ? kOwn : kPairs;
+    turn = p.positions && l < half;
+    u = 2 * l, v = 2 * l + 1;
+    if (four && !p.interleaved && (half & 1)) {
+      mode = kApart;
+      turn = p.positions != nullptr;
+    } else if (mode == kPairs) {
+      u = l, v = l + half;
+    }
   }
-  return p.rotary + (size_t)pos * p.rotary_dim;
-}
-
-// A token's write slot; -1 (and flagged) outside the pool.
-__device__ __forceinline__ long long slot_of(const RopeParams& p, long long token, bool flag) {
-  const long long slot = __ldg(p.write_slots + token);
-  if (slot >= 0 && slot < p.pool_slots) return slot;
-  if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_SLOT);
-  return -1;
-}
-
-// Query heads h0 .. of one token: a thread takes one pair of vectors of up to
-// four heads, whose loads go out together and share the cosines and sines.
-template <typename T, int D>
-__device__ __forceinline__ void turn_queries(const RopeParams& p, long long token, int h0,
-                                             int item, const float* row) {
-  constexpr int NV = D / Vec<T>::N;  // vectors of a head
-  Pair<T> t;
-  t.init(p, item, row);
-  const uint4* in =
-      reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + token * p.q_stride);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out)) + (size_t)token * p.heads * NV;
-  uint4 r[kHeadsPerThread][2];
-#pragma unroll
-  for (int j = 0; j < kHeadsPerThread; ++j)
-    if (h0 + j < p.heads) {
-      r[j][0] = in[(h0 + j) * NV + t.v0];
-      r[j][1] = in[(h0 + j) * NV + t.v1];
+  __device__ __forceinline__ void init(const RopeParams& p, const float* row) {
+    if (!turn || mode == kApart) return;
+    if (mode == kPairs) {
+      load_f32<8>(row + 8 * u, c);
+      load_f32<8>(row + p.rotary_dim / 2 + 8 * u, s);
+    } else {  // interleaved: pairs 4 u ..
+      load_f32<8>(row + 4 * u, c);
+      load_f32<8>(row + p.rotary_dim / 2 + 4 * u, s);
     }
+  }
+  // x: the head.
+  __device__ __forceinline__ void apply(const RopeParams& p, const T* x, const float* row,
+                                        float* a, float* b) const {
+    if (!turn) return;
+    if (mode == kPairs) {
 #pragma unroll
-  for (int j = 0; j < kHeadsPerThread; ++j)
-    if (h0 + j < p.heads) {
-      t.apply(p, r[j][0], r[j][1]);
-      out[(h0 + j) * NV + t.v0] = r[j][0];
-      out[(h0 + j) * NV + t.v1] = r[j][1];
+      for (int i = 0; i < 8; ++i) {
+        const float e = a[i], f = b[i];
+        a[i] = turn_a(e, f, c[i], s[i]);
+        b[i] = turn_b(e, f, c[i], s[i]);
+      }
+    } else if (mode == kOwn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float* y = i < 4 ? a + 2 * i : b + 2 * (i - 4);
+        const float e = y[0], f = y[1];
+        y[0] = turn_a(e, f, c[i], s[i]);
+        y[1] = turn_b(e, f, c[i], s[i]);
+      }
+    } else {
+      apart(p, x, row, 8 * u, a);
+      apart(p, x, row, 8 * v, b);
     }
+  }
+  static __device__ __forceinline__ void apart(const RopeParams& p, const T* x, const float* row,
+                                               int d, float* y) {
+    if (d >= p.rotary_dim) return;
+    const int half = p.rotary_dim / 2;
+    const bool upper = d >= half;
+    const int e = upper ? d - half : d;
+    float c8[8], s8[8], z[8];
+    load_f32<8>(row + e, c8);
+    load_f32<8>(row + half + e, s8);
+    Eight<T> o;
+    o.load(x + (upper ? e : d + half));
+    o.get(z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = upper ? turn_b(z[i], y[i], c8[i], s8[i]) : turn_a(y[i], z[i], c8[i], s8[i]);
+  }
+};
+
+// The quotient x / d rounded to nearest, from r = 1 / d rounded to nearest: the residual of
+// the first product is exact, and the correction by it rounds as the quotient does
+// (P. Markstein, Computation of elementary functions on the IBM RISC System/6000, 1990).
+// Where the residual underflows (|x| below 2^-101, d within 2^-60 .. 2^60) the quotient may
+// be off, but so far below the smallest number that it is stored as 0 either way.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float y = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-y, d, x), r, y);
 }
 
-// Units of a token: (four query heads, pair) and (KV head, pair), in this order.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p, int per_cta) {
+// 8 dimensions as numbers of scale s, whose reciprocal is r.
+__device__ __forceinline__ uint32_t numbers8(const float* y, float s, float r) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    w |= to_e2m1x2(quotient(y[i], s, r), quotient(y[i + 1], s, r)) << (4 * i);
+  return s == 0.f ? 0u : w;
+}
+
+// A unit is up to kPasses passes over one token's query heads, keys or values, by a warp: a
+// lane holds 16 dimensions of a head in each, all loads go out together, and the token's
+// cosines and sines serve them all.  The position's row of the table is the only load that
+// has to wait for another.  Times of 8192 tokens appended, and 16381 into 4 bits (with
+// their values read back, 17 us): 8 dimensions a lane, partners by shuffles 44 and 105 us;
+// a thread with four whole heads' pairs, 111 to 147 registers, 43 and 127.
+template <typename T, int D, bool FOUR>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5)
+    append_kernel(const RopeParams p, int q_units, int kv_units) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int NV = D / Vec<T>::N, kItems = NV / 2;
-  const int q_units = (p.q ? (p.heads + kHeadsPerThread - 1) / kHeadsPerThread : 0) * kItems;
-  const int units = q_units + p.kv_heads * kItems;
-  const long long first = (long long)blockIdx.x * per_cta;
-#pragma unroll 1
-  for (int u = threadIdx.x; u < per_cta * units; u += kThreads) {
-    const int ti = u / units, w = u - ti * units;
-    const long long token = first + ti;
-    if (token >= p.tokens) break;
-    bool ok;
-    const float* row = table_row(p, token, w == 0, &ok);
-    if (!ok) continue;
-    const int item = w % kItems;
-    if (w < q_units) {
-      turn_queries<T, D>(p, token, w / kItems * kHeadsPerThread, item, row);
-      continue;
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes of a head; heads of a pass
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
+  const int units = q_units + 2 * kv_units;
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const long long token = unit >> 32 ? unit / units : (uint32_t)unit / (uint32_t)units;
+  if (token >= p.tokens) return;
+  int n = (int)(unit - token * units);
+  const bool query = n < q_units, value = n >= q_units + kv_units;
+  n -= query ? 0 : value ? q_units + kv_units : q_units;
+  const int heads = query ? p.heads : p.kv_heads;
+  const T* src = query   ? static_cast<const T*>(p.q) + token * p.q_stride
+                 : value ? static_cast<const T*>(p.v) + token * p.v_stride
+                         : static_cast<const T*>(p.k) + token * p.k_stride;
+  const int h0 = n * kPasses * kHeads + lane / kLanes;
+  const int pos = p.positions ? __ldg(p.positions + token) : 0;
+  const long long slot = query ? 0 : __ldg(p.write_slots + token);
+  Turn<T> t;
+  t.place(p, l, FOUR && !query);
+  Eight<T> x[kPasses][2];
+#pragma unroll
+  for (int j = 0; j < kPasses; ++j) {
+    const int h = h0 + j * kHeads;
+    if (h < heads) {
+      x[j][0].load(src + (size_t)h * D + 8 * t.u);
+      x[j][1].load(src + (size_t)h * D + 8 * t.v);
+    } else {
+      x[j][0].clear();
+      x[j][1].clear();
     }
-    const int g = (w - q_units) / kItems;
-    const long long slot = slot_of(p, token, w == q_units);
-    if (slot < 0) continue;
-    Pair<T> t;
-    t.init(p, item, row);
-    const uint4* k =
-        reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + token * p.k_stride) + g * NV;
-    const uint4* v =
-        reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + token * p.v_stride) + g * NV;
-    uint4 k0 = k[t.v0], k1 = k[t.v1];
-    const uint4 v0 = v[t.v0], v1 = v[t.v1];
-    const size_t dst =
-        ((size_t)(slot / kBlock * p.kv_heads + g) * kBlock + slot % kBlock) * NV;
-    t.apply(p, k0, k1);
-    static_cast<uint4*>(p.k_pool)[dst + t.v0] = k0;
-    static_cast<uint4*>(p.k_pool)[dst + t.v1] = k1;
-    static_cast<uint4*>(p.v_pool)[dst + t.v0] = v0;
-    static_cast<uint4*>(p.v_pool)[dst + t.v1] = v1;
   }
-}
-
-// Elements d .. d + 7 of one head of one token, fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* x, int d, float* y) {
-#pragma unroll
-  for (int i = 0; i < 8; i += Vec<T>::N)
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(x + d + i), y + i);
-}
-
-// The same rotated.  (A half of the rotated dimensions is a whole number of eights.)
-template <typename T>
-__device__ __forceinline__ void load8_turned(const RopeParams& p, const T* x, int d,
-                                             const float* row, float* y) {
-  load8(x, d, y);
-  if (!row || d >= p.rotary_dim) return;
-  const int half = p.rotary_dim / 2;
-  if (p.interleaved) {
-    float c[4], s[4];
-    load_f32<4>(row + d / 2, c);
-    load_f32<4>(row + half + d / 2, s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1];
-      y[2 * i] = turn_a(a, b, c[i], s[i]);
-      y[2 * i + 1] = turn_b(a, b, c[i], s[i]);
+  // (flagged by the token's first keys' unit)
+  const bool flag = lane == 0 && n == 0 && !query && !value;
+  const float* row = nullptr;
+  if (p.positions) {
+    if (pos < 0 || pos >= p.num_positions) {
+      if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_POS);
+      return;
     }
+    row = p.rotary + (size_t)pos * p.rotary_dim;
+  }
+  if (slot < 0 || slot >= p.pool_slots) {
+    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_SLOT);
     return;
   }
-  float c[8], s[8], z[8];
-  const bool upper = d >= half;
-  const int e = upper ? d - half : d;
-  load_f32<8>(row + e, c);
-  load_f32<8>(row + half + e, s);
-  load8(x, upper ? e : d + half, z);  // the other of each pair
+  t.turn = t.turn && !value;
+  t.init(p, row);
+  const long long block = slot / kBlock;
+  const int off = (int)(slot % kBlock);
+  const float* units_of = value ? p.v_scales : p.k_scales;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    y[i] = upper ? turn_b(z[i], y[i], c[i], s[i]) : turn_a(y[i], z[i], c[i], s[i]);
-}
-
-// 16 dimensions of a token and KV head to their numbers and scale.
-__device__ __forceinline__ void store16(float* y, const float* head_scale, uint8_t* tile, int off,
-                                        int group, int head_dim) {
-  if (head_scale) {
-    const float h = __ldg(head_scale);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], h);
-  }
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
-  const uint32_t code = to_e4m3(__fdiv_rn(top, 6.f));
-  const __half2 wide = __half2(__half2_raw{(unsigned short)(e4m3x2_to_half(code) & 0xffffu), 0});
-  const float s = __low2float(wide);
-  uint32_t w[2] = {0u, 0u};
-  if (s > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 2)
-      w[i / 8] |= to_e2m1x2(__fdiv_rn(y[i], s), __fdiv_rn(y[i + 1], s)) << (4 * (i % 8));
-  }
-  *reinterpret_cast<uint2*>(tile + off * (head_dim / 2) + group * 8) = make_uint2(w[0], w[1]);
-  tile[kv4_number_bytes(head_dim) + off * (head_dim / 16) + group] = (uint8_t)code;
-}
-
-// Units of a token: (four query heads, pair), then (keys or values, KV head, 16
-// dimensions).
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const RopeParams p, int per_cta) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kItems = D / Vec<T>::N / 2, kGroups = D / 16;
-  const int q_units = (p.q ? (p.heads + kHeadsPerThread - 1) / kHeadsPerThread : 0) * kItems;
-  const int units = q_units + 2 * p.kv_heads * kGroups;
-  const long long first = (long long)blockIdx.x * per_cta;
-#pragma unroll 1
-  for (int u = threadIdx.x; u < per_cta * units; u += kThreads) {
-    const int ti = u / units, w = u - ti * units;
-    const long long token = first + ti;
-    if (token >= p.tokens) break;
-    bool ok;
-    const float* row = table_row(p, token, w == 0, &ok);
-    if (!ok) continue;
-    if (w < q_units) {
-      turn_queries<T, D>(p, token, w / kItems * kHeadsPerThread, w % kItems, row);
+  for (int j = 0; j < kPasses; ++j) {
+    const int h = h0 + j * kHeads;
+    if (!FOUR || query) {
+      if (h >= heads) continue;
+      if (t.turn) {
+        float a[8], b[8];
+        x[j][0].get(a);
+        x[j][1].get(b);
+        t.apply(p, src + (size_t)h * D, row, a, b);
+        x[j][0].set(a);
+        x[j][1].set(b);
+      }
+      T* out = query ? static_cast<T*>(p.q_out) + ((size_t)token * p.heads + h) * D
+                     : static_cast<T*>(value ? p.v_pool : p.k_pool) +
+                           ((size_t)(block * p.kv_heads + h) * kBlock + off) * D;
+      x[j][0].store(out + 8 * t.u);
+      x[j][1].store(out + 8 * t.v);
       continue;
     }
-    int g = (w - q_units) / kGroups;
-    const int group = (w - q_units) % kGroups;
-    const long long slot = slot_of(p, token, w == q_units);
-    if (slot < 0) continue;
-    const bool value = g >= p.kv_heads;
-    if (value) g -= p.kv_heads;
-    const T* x = (value ? static_cast<const T*>(p.v) + token * p.v_stride
-                        : static_cast<const T*>(p.k) + token * p.k_stride) + g * D;
-    float y[16];
-    load8_turned(p, x, group * 16, value ? nullptr : row, y);
-    load8_turned(p, x, group * 16 + 8, value ? nullptr : row, y + 8);
-    const float* scales = value ? p.v_scales : p.k_scales;
+    const bool real = h < heads;
+    float a[8], b[8];
+    x[j][0].get(a);
+    x[j][1].get(b);
+    if (real) t.apply(p, src + (size_t)h * D, row, a, b);
+    if (units_of) {
+      const float d = real ? __ldg(units_of + h) : 1.f, r = __frcp_rn(d);
+      const float most = 4096.f * d;  // beyond 2688 all quotients end the same
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = quotient(fminf(fmaxf(a[i], -most), most), d, r);
+        b[i] = quotient(fminf(fmaxf(b[i], -most), most), d, r);
+      }
+    }
+    float top_a = 0.f, top_b = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      top_a = fmaxf(top_a, fabsf(a[i]));
+      top_b = fmaxf(top_b, fabsf(b[i]));
+    }
+    // a scale's 16 dimensions: the lane's own, or 8 of its neighbour's
+    const float next_a = __shfl_xor_sync(sm::kFull, top_a, 1);
+    const float next_b = __shfl_xor_sync(sm::kFull, top_b, 1);
+    const bool pairs = t.mode == kPairs;
+    top_a = fmaxf(top_a, pairs ? next_a : top_b);
+    top_b = pairs ? fmaxf(top_b, next_b) : top_a;
+    const uint32_t code_a = to_e4m3(quotient(top_a, 6.f, 1.f / 6.f));
+    const uint32_t code_b = to_e4m3(quotient(top_b, 6.f, 1.f / 6.f));
+    const uint32_t wide = e4m3x2_to_half(code_a | (code_b << 8));
+    const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&wide));
+    const uint32_t wa = numbers8(a, s.x, __frcp_rn(s.x)), wb = numbers8(b, s.y, __frcp_rn(s.y));
+    if (!real) continue;
     uint8_t* tile = static_cast<uint8_t*>(value ? p.v_pool : p.k_pool) +
-                    (size_t)(slot / kBlock * p.kv_heads + g) * kv4_tile_bytes(D);
-    store16(y, scales ? scales + g : nullptr, tile, (int)(slot % kBlock), group, D);
+                    (size_t)(block * p.kv_heads + h) * kv4_tile_bytes(D);
+    uint32_t* num = reinterpret_cast<uint32_t*>(tile + off * (D / 2));
+    uint8_t* sc = tile + kv4_number_bytes(D) + off * (D / 16);
+    num[t.u] = wa;
+    num[t.v] = wb;
+    if (!(t.u & 1)) sc[t.u >> 1] = (uint8_t)code_a;
+    if (pairs && !(t.v & 1)) sc[t.v >> 1] = (uint8_t)code_b;
   }
 }
 
-// A thread widens 8 dimensions of a slot's key and value.
+// A thread widens 8 dimensions of the keys and values of kReads slots, whose loads go out
+// together.
+constexpr int kReads = 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4ReadParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -322,57 +328,71 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4ReadParams 
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int item = (int)(i % kItems);
   const long long th = i / kItems;
-  const long long token = th / p.kv_heads;
-  const int g = (int)(th - token * p.kv_heads);
-  if (token >= p.tokens) return;
-  const long long slot = __ldg(p.slots + token);
-  if (slot < 0 || slot >= p.pool_slots) {
-    if (item == 0 && g == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_SLOT);
-    return;
-  }
-  const size_t tile = (size_t)(slot / kBlock * p.kv_heads + g) * kv4_tile_bytes(D);
-  const int off = (int)(slot % kBlock);
-  const size_t at = tile + off * (D / 2) + item * 4;
-  const size_t sc = tile + kv4_number_bytes(D) + off * (D / 16) + item / 2;
-  const uint32_t num[2] = {__ldg(reinterpret_cast<const uint32_t*>(p.k_pool + at)),
-                           __ldg(reinterpret_cast<const uint32_t*>(p.v_pool + at))};
-  const uint32_t sb[2] = {__ldg(p.k_pool + sc), __ldg(p.v_pool + sc)};
+  const long long t0 = th / p.kv_heads;  // the thread's tokens are `step` apart
+  const int g = (int)(th - t0 * p.kv_heads);
+  const long long step = (p.tokens + kReads - 1) / kReads;
+  if (t0 >= step) return;
+  long long slot[kReads];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    uint32_t h[4];
-    e2m1x8_to_half(num[kv], h);
-    const uint32_t sh = e4m3x2_to_half(sb[kv]);
-    const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-    const float* scales = kv ? p.v_scales : p.k_scales;
-    const float unit = scales ? __ldg(scales + g) : 1.f;
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-      x[2 * j] = __fmul_rn(__fmul_rn(f.x, s), unit);
-      x[2 * j + 1] = __fmul_rn(__fmul_rn(f.y, s), unit);
+  for (int k = 0; k < kReads; ++k) {
+    const long long t = t0 + k * step;
+    slot[k] = t < p.tokens ? __ldg(p.slots + t) : -1;
+    if (slot[k] < 0 || slot[k] >= p.pool_slots) {
+      if (t < p.tokens && item == 0 && g == 0) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_SLOT);
+      slot[k] = -1;
     }
-    T* out = static_cast<T*>(kv ? p.v_out : p.k_out) + (size_t)th * D + item * 8;
+  }
+  uint32_t num[kReads][2], sb[kReads][2];
 #pragma unroll
-    for (int j = 0; j < 8; j += Vec<T>::N)
-      *reinterpret_cast<uint4*>(out + j) = Vec<T>::pack(x + j);
+  for (int k = 0; k < kReads; ++k) {
+    if (slot[k] < 0) continue;
+    const size_t tile = (size_t)(slot[k] / kBlock * p.kv_heads + g) * kv4_tile_bytes(D);
+    const int off = (int)(slot[k] % kBlock);
+    const size_t at = tile + off * (D / 2) + item * 4;
+    const size_t sc = tile + kv4_number_bytes(D) + off * (D / 16) + item / 2;
+    num[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k_pool + at));
+    num[k][1] = __ldg(reinterpret_cast<const uint32_t*>(p.v_pool + at));
+    sb[k][0] = __ldg(p.k_pool + sc);
+    sb[k][1] = __ldg(p.v_pool + sc);
+  }
+  const float unit[2] = {p.k_scales ? __ldg(p.k_scales + g) : 1.f,
+                         p.v_scales ? __ldg(p.v_scales + g) : 1.f};
+#pragma unroll
+  for (int k = 0; k < kReads; ++k) {
+    if (slot[k] < 0) continue;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t h[4];
+      e2m1x8_to_half(num[k][kv], h);
+      const uint32_t sh = e4m3x2_to_half(sb[k][kv]);
+      const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        x[2 * j] = __fmul_rn(__fmul_rn(f.x, s), unit[kv]);
+        x[2 * j + 1] = __fmul_rn(__fmul_rn(f.y, s), unit[kv]);
+      }
+      T* out = static_cast<T*>(kv ? p.v_out : p.k_out) +
+               ((size_t)(t0 + k * step) * p.kv_heads + g) * D + item * 8;
+#pragma unroll
+      for (int j = 0; j < 8; j += Vec<T>::N)
+        *reinterpret_cast<uint4*>(out + j) = Vec<T>::pack(x + j);
+    }
   }
 }
 
-// Tokens one CTA takes, so that its threads have a unit each.
-int tokens_per_cta(int units) { return units >= kThreads ? 1 : kThreads / units; }
-
 template <typename T, int D>
 cudaError_t launch_append(const RopeParams& p, bool four, cudaStream_t stream) {
-  const int items = D / Vec<T>::N / 2;
-  const int q_units = (p.q ? (p.heads + kHeadsPerThread - 1) / kHeadsPerThread : 0) * items;
-  const int units = q_units + p.kv_heads * (four ? 2 * (D / 16) : items);
-  const int per_cta = tokens_per_cta(units);
-  const unsigned grid = (unsigned)((p.tokens + per_cta - 1) / per_cta);
+  const int heads = kPasses * 512 / D;  // of a unit
+  const int q_units = p.q ? (p.heads + heads - 1) / heads : 0;
+  const int kv_units = (p.kv_heads + heads - 1) / heads;
+  const long long units = p.tokens * (q_units + 2 * kv_units);
+  const unsigned grid = (unsigned)((units * 32 + kThreads - 1) / kThreads);
   if (four)
-    kv4_write_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, per_cta);
+    append_kernel<T, D, true><<<grid, kThreads, 0, stream>>>(p, q_units, kv_units);
   else
-    rope_write_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, per_cta);
+    append_kernel<T, D, false><<<grid, kThreads, 0, stream>>>(p, q_units, kv_units);
   return cudaGetLastError();
 }
 
@@ -387,7 +407,7 @@ cudaError_t launch_any(const RopeParams& p, int dtype, int head_dim, bool four,
 
 template <typename T, int D>
 cudaError_t launch_read(const Kv4ReadParams& p, cudaStream_t stream) {
-  const long long n = p.tokens * p.kv_heads * (D / 8);
+  const long long n = (p.tokens + kReads - 1) / kReads * p.kv_heads * (D / 8);
   kv4_read_kernel<T, D><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -93,10 +93,10 @@ def test_sizes(nsv, kw, tokens, code):
     assert e.value.code == code
 
 
-def test_append_of_more_heads_than_units_are_counted_for(nsv):
-    s = _shape(nsv, num_heads=(1 << 20) + 2, num_kv_heads=(1 << 20) + 2)
+def test_append_of_more_heads_than_a_grid_holds(nsv):
+    s = _shape(nsv, num_heads=1 << 20, num_kv_heads=1 << 20)
     for four in (False, True):
-        assert _append(nsv, s, four) == -3
+        assert _append(nsv, s, four, tokens=(1 << 14) // 3 + 1) == -3
 
 
 def test_scales_are_aligned(nsv):
