@@ -267,6 +267,29 @@ __device__ __forceinline__ int2 chunk_sees(const ChunkParams& p, long long g, in
   return make_int2(b, max(e, 0));
 }
 
+// A row's new tokens and context length; none and 0 where they are bad.
+struct RowChunk {
+  int start, n, ctx;
+};
+
+__device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool flag) {
+  const int a = __ldg(p.chunk_starts + r), b = __ldg(p.chunk_starts + r + 1);
+  RowChunk c{a, b - a, __ldg(p.context_lens + r)};
+  if (a < 0 || b < a || b > p.tokens) {
+    c.n = 0;
+    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+  }
+  if (c.n < p.n_min || c.n > p.n_max) {
+    if (flag && p.flag_above && c.n > p.n_max) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+    c.n = 0;
+  }
+  if (c.ctx < 0 || (long long)c.ctx > (long long)p.max_blocks * kBlock) {
+    c.ctx = 0;
+    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CTX);
+  }
+  return c;
+}
+
 // Workspace slot of a cut tile's piece on CTA c: a CTA cuts at most the tile
 // that its range starts inside of (slot 0) and the one it starts but does not
 // finish (slot 1).

@@ -42,28 +42,6 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
   return v;
 }
 
-struct RowChunk {
-  int start, n, ctx;
-};
-
-__device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool flag) {
-  const int a = __ldg(p.chunk_starts + r), b = __ldg(p.chunk_starts + r + 1);
-  RowChunk c{a, b - a, __ldg(p.context_lens + r)};
-  if (a < 0 || b < a || b > p.tokens) {
-    c.n = 0;
-    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
-  }
-  if (c.n < p.n_min || c.n > p.n_max) {
-    if (flag && p.flag_above && c.n > p.n_max) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
-    c.n = 0;
-  }
-  if (c.ctx < 0 || (long long)c.ctx > (long long)p.max_blocks * kBlock) {
-    c.ctx = 0;
-    if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CTX);
-  }
-  return c;
-}
-
 __device__ __forceinline__ void plan(const ChunkParams& p) {
   __shared__ int s_first[kMaxRows + 1];  // tiles before each row
   __shared__ long long s_prefix[kPlanThreads];

@@ -64,6 +64,9 @@ struct Kv4VecParams {
   int4* todo;     // [workers] what each has to merge: {first query token, tokens, group, pieces}
   float2* ml;     // [workers][2][heads_per_worker][vectors]
   float* acc;     // [workers][2][heads_per_worker][vectors][head_dim]
+  // Where it is not 0 there is no list: every CTA works its shares out itself, a row
+  // having at most this many tiles.
+  int row_tiles;
   int kv_heads, heads_per_worker, workers_per_cta;
   int subs;       // parts that a KV head's query heads are taken in
 };
@@ -72,6 +75,9 @@ struct Kv4VecParams {
 constexpr int kVecKeys = 32;  // positions of one unit: two blocks
 constexpr int kVecMostVectors = 32;  // query vectors of a row and KV head, bf16
 constexpr int kVecTileCost = 1;   // of a tile, in units
+constexpr int kVecLeastUnits = 2; // of a share, where CTAs work them out themselves
+// The most tiles (rows times row_tiles) that they do it for: eight a thread.
+constexpr int kVecOwnTiles = 2048;
 constexpr int kVecWholeRuns = 8;  // as kChunkWholeRuns
 
 cudaError_t launch_rope_write(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);

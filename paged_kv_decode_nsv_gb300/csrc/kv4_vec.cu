@@ -108,8 +108,84 @@ static_assert(kSegments > kStages, "segments that are open at a time");
 struct Segment {
   int q0, n_tok, pos0, ctx;
   int kb, j0, j1, head;
-  int tile, whole, first, valid;  // valid: 0 behind the share's last
+  int whole, first, valid;  // valid: 0 behind the share's last
+  long long last;           // the tile's last unit, of all tiles' and groups'
 };
+
+constexpr uint32_t kSegmentBytes = kSegments * sizeof(Segment) + 32;  // and a Worker::Own
+
+// A tile as a CTA works it out that has no list: number `tile` of rows times row_tiles.
+struct OwnTile {
+  int row, q0, n_tok, pos0, kb, ke, ctx, units;  // units 0: there is none
+};
+__device__ __forceinline__ OwnTile own_tile(const Kv4VecParams& p, int tile, bool flag) {
+  OwnTile o;
+  o.row = p.row_tiles == 1 ? tile : tile / p.row_tiles;
+  const int i = tile - o.row * p.row_tiles, tok0 = i * p.c.tile_tokens;
+  const RowChunk c = row_chunk(p.c, o.row, flag && i == 0);
+  o.units = 0;
+  if (tok0 >= c.n) return o;
+  o.q0 = c.start + tok0;
+  o.n_tok = min(p.c.tile_tokens, c.n - tok0);
+  o.pos0 = c.ctx - c.n + tok0;
+  o.ctx = c.ctx;
+  o.kb = 0;
+  o.ke = max(0, min(o.pos0 + o.n_tok, c.ctx));
+  if (p.c.see_begin || p.c.see_end) {
+    int kb = 0x7fffffff;
+    o.ke = 0;
+    for (int t = 0; t < o.n_tok; ++t) {
+      const int2 v = chunk_sees(p.c, (long long)o.q0 + t, o.pos0 + t, c.ctx);
+      if (v.x < v.y) {
+        kb = min(kb, v.x);
+        o.ke = max(o.ke, v.y);
+      }
+    }
+    o.kb = kb < o.ke ? kb / kBlock * kBlock : 0;
+  }
+  o.units = p.c.tile_cost + chunk_runs(o.kb, o.ke, kVecKeys);
+  return o;
+}
+
+// The units of a CTA's threads' tiles, before each thread's; all of one group of heads.
+struct OwnPlan {
+  long long units, shares;  // of one group of heads; workers that have any
+  long long before[kWarps * 32 + 1];
+  long long warp_sum[kWarps];
+};
+// All threads of the CTA together.
+__device__ __forceinline__ void own_plan(const Kv4VecParams& p, OwnPlan* o) {
+  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  const int tiles = p.c.rows * p.row_tiles;
+  const int each = (tiles + blockDim.x - 1) / blockDim.x;
+  long long mine = 0;
+  for (int i = tid * each; i < min((tid + 1) * each, tiles); ++i)
+    mine += own_tile(p, i, blockIdx.x == 0).units;
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long x = __shfl_up_sync(kFull, upto, d);
+    if (lane >= d) upto += x;
+  }
+  if (lane == 31) o->warp_sum[tid >> 5] = upto;
+  __syncthreads();
+  long long base = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < tid >> 5) base += o->warp_sum[w];
+    total += o->warp_sum[w];
+  }
+  o->before[tid] = base + upto - mine;
+  if (tid == 0) {
+    // (a share is counted in 32 bits)
+    if (total > 0x7fffffffll / p.c.kv_heads * p.c.grid) {
+      if (blockIdx.x == 0) atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+      total = 0;
+    }
+    o->units = total;
+    o->shares = max(1ll, min(total * p.c.kv_heads / kVecLeastUnits, (long long)p.c.grid));
+  }
+  __syncthreads();
+}
 
 template <typename T, int D, int NT, bool CAP, bool BIAS>
 struct Worker {
@@ -125,6 +201,10 @@ struct Worker {
   int head;             // within a group of heads
   // The copies' side: the walk, what its segment has left, and the ring's next stage.
   ChunkWalk wk;
+  struct Own {
+    long long unit, all, shares;  // without a list: the next unit; of how many; workers
+  };
+  volatile Own* own;
   const int32_t* table;
   const uint8_t* pool;  // lanes 0 and 1: keys, 2 and 3: values; of the segment's KV head
   int block, block_end, units;  // next block, one past the last that any vector sees
@@ -135,10 +215,81 @@ struct Worker {
 
   __device__ __forceinline__ Worker(const Kv4VecParams& p_) : p(p_) {}
 
+  // Where the share of worker `w` starts, without a list.
+  __device__ __forceinline__ void start(const OwnPlan* o, int w) {
+    const long long U = o->units * p.c.kv_heads, n = o->shares;
+    wk.left = wk.head = wk.tile = wk.skip = 0;
+    wk.ntiles = p.c.rows * p.row_tiles;
+    const long long first = w < n ? w * U / n : U;
+    if (lane == 0) {
+      own->unit = first;
+      own->all = U;
+      own->shares = n;
+    }
+    __syncwarp();
+    if (first >= U) return;
+    wk.left = (int)((w + 1) * U / n - first);
+    wk.head = (int)(first / o->units);
+    const long long rem = first - wk.head * o->units;
+    int lo = 0, hi = blockDim.x;  // the last thread whose first unit is at most rem
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (o->before[mid] <= rem) lo = mid; else hi = mid;
+    }
+    // of its tiles (at most 8) the one that holds rem
+    const int each = (wk.ntiles + blockDim.x - 1) / blockDim.x, i = lo * each + lane;
+    const long long mine = lane < each && i < wk.ntiles ? own_tile(p, i, false).units : 0;
+    long long upto = o->before[lo] + mine;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) {
+      const long long x = __shfl_up_sync(kFull, upto - o->before[lo], d);
+      if (lane >= d) upto += x;
+    }
+    const int at = __ffs(__ballot_sync(kFull, rem < upto)) - 1;
+    wk.tile = lo * each + at;
+    wk.skip = (int)(rem - __shfl_sync(kFull, upto - mine, at));
+  }
+  // The next segment without a list.
+  __device__ __forceinline__ bool own_next(ChunkSegment& s, long long& last) {
+    __syncwarp();
+    long long unit = own->unit;
+    bool more = false;
+    while (!more && wk.left > 0) {
+      const OwnTile t = own_tile(p, wk.tile, false);
+      const int of_tile = t.units - wk.skip, take = min(wk.left, of_tile);
+      s.j0 = max(0, wk.skip - p.c.tile_cost);
+      s.j1 = max(0, wk.skip + take - p.c.tile_cost);
+      s.first = s.j0 == 0;
+      s.last = take == of_tile;
+      s.head = wk.head;
+      last = unit + of_tile - 1;
+      wk.left -= take;
+      unit += take;
+      wk.skip = 0;
+      if (take == of_tile && ++wk.tile == wk.ntiles) {
+        wk.tile = 0;
+        ++wk.head;
+      }
+      more = s.j0 != s.j1;  // (else none of the tile, or not a run of it)
+      s.t.row = t.row, s.t.q0 = t.q0, s.t.n_tok = t.n_tok, s.t.pos0 = t.pos0;
+      s.t.kb = t.kb, s.t.ke = t.ke, s.t.ctx = t.ctx;
+    }
+    __syncwarp();
+    if (lane == 0) own->unit = unit;
+    return more;
+  }
+
   // The next segment of the share.
   __device__ __forceinline__ void open() {
     ChunkSegment s;
-    const bool more = wk.next<kVecKeys>(p.c, s);
+    long long last = 0;
+    bool more;
+    if (p.row_tiles) {
+      more = own_next(s, last);
+    } else {
+      more = wk.next<kVecKeys>(p.c, s);
+      if (more) last = s.head * __ldcg(p.c.ws_head) + __ldcg(p.c.ws_prefix + s.tile + 1) - 1;
+    }
     Segment* e = segments + opened % kSegments;
     ++opened;
     units = 0;
@@ -147,7 +298,7 @@ struct Worker {
       if (more) {
         e->q0 = s.t.q0, e->n_tok = s.t.n_tok, e->pos0 = s.t.pos0, e->ctx = s.t.ctx;
         e->kb = s.t.kb, e->j0 = s.j0, e->j1 = s.j1, e->head = s.head;
-        e->tile = s.tile, e->whole = s.first && s.last, e->first = s.first;
+        e->whole = s.first && s.last, e->first = s.first, e->last = last;
       }
     }
     if (!more) return;
@@ -342,7 +493,7 @@ struct Worker {
 
   // The whole share; false when a wait gave up.
   __device__ __forceinline__ bool run(int worker) {
-    wk.init(p.c, worker);
+    if (!p.row_tiles) wk.init(p.c, worker);
     opened = fill = missing = at = parity = 0;
     open();
 #pragma unroll 1
@@ -633,11 +784,11 @@ struct Worker {
       if (!whole && s->first && head == 0) {
         // how many workers the tile's pieces are on: those that start at or before
         // its last unit's first
-        const long long last = s->head * __ldcg(p.c.ws_head) +
-                               __ldcg(p.c.ws_prefix + s->tile + 1) - 1;
+        const long long last = s->last;
         int n = 0;
+        if (p.row_tiles) n = (int)(((last + 1) * own->shares - 1) / own->all) - worker + 1;
 #pragma unroll 1
-        for (int c = worker; c < p.c.grid; c += 32) {
+        for (int c = worker; !p.row_tiles && c < p.c.grid; c += 32) {
           const unsigned in = __ballot_sync(
               kFull, c + lane < p.c.grid && __ldcg(p.c.ws_first + c + lane) <= last);
           n += __popc(in);
@@ -661,8 +812,9 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const uint32_t base = smem_u32(smem);
-  const uint32_t segments = warps * R::kWarp, bars = segments + warps * kSegments * sizeof(Segment);
-  Worker<T, D, NT, CAP, BIAS> w(p);
+  using W = Worker<T, D, NT, CAP, BIAS>;
+  const uint32_t segments = warps * R::kWarp, bars = segments + warps * kSegmentBytes;
+  W w(p);
   w.bars = base + bars + warp * kStages * 8;
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(w.bars + 8 * i, 1);
@@ -672,13 +824,22 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   griddep_wait();  // the tile list, and whatever was written before it
   griddep_launch();
   const int worker = blockIdx.x * p.workers_per_cta + warp / p.heads_per_worker;
-  if (worker >= p.c.grid) return;
   w.lane = lane;
   w.g = lane >> 2;
   w.t = lane & 3;
   w.ring = base + warp * R::kWarp;
-  w.segments = reinterpret_cast<Segment*>(smem + segments) + warp * kSegments;
+  w.segments = reinterpret_cast<Segment*>(smem + segments + warp * kSegmentBytes);
+  w.own = reinterpret_cast<volatile typename W::Own*>(w.segments + kSegments);
   w.head = warp % p.heads_per_worker;
+  if (p.row_tiles) {
+    OwnPlan* o = reinterpret_cast<OwnPlan*>(smem);  // where the ring will be
+    static_assert(sizeof(OwnPlan) <= R::kWarp, "the ring of one warp");
+    own_plan(p, o);
+    w.start(o, worker);
+    __syncthreads();  // (what was written there came by ordinary stores)
+    fence_proxy_async_smem();
+  }
+  if (worker >= p.c.grid) return;
   if (w.head == 0 && lane == 0) p.todo[worker] = make_int4(0, 0, 0, 0);
   if (!w.run(worker)) {
     if (lane == 0) atomicOr(p.c.status, (uint32_t)NSV_DEV_TIMEOUT);
@@ -691,38 +852,66 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   }
 }
 
-// Joins the pieces of the tile that worker blockIdx.x starts and does not end, for
-// KV head blockIdx.y of its group: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
-// Four warps take a query vector each, a lane D / 32 columns.
+// Joins the pieces of the tile that worker blockIdx.x starts and does not end, for KV head
+// blockIdx.y of its group: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.  A warp
+// takes one query vector, a lane D / 32 of its columns; where there are many pieces 2, 4 or
+// 8 warps share them.  (Few CTAs of 16 warps, one for each worker: 5 to 10 us slower.)
+constexpr int kMergeWarps = 8;
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4VecParams p) {
-  constexpr int kVecs = 8 * NT;
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    kv4_merge_kernel(const __grid_constant__ Kv4VecParams p) {
+  constexpr int kVecs = 8 * NT, kCols = D / 32, kAhead = D == 128 ? 4 : 8;
+  __shared__ float s_state[kMergeWarps][D + 2];
   griddep_wait();
   griddep_launch();
   const int worker = blockIdx.x, head = blockIdx.y;
   const int4 todo = __ldcg(p.todo + worker);
   if (todo.w == 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = todo.z % p.subs;
-  const int kv_head = (todo.z / p.subs) * p.heads_per_worker + head;
   const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
-  const float v_unit = p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f;
-  for (int v = threadIdx.x >> 5; v < todo.y * per; v += 4) {
-    float M = kLeast, L = 0.f, a[D / 32];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) a[k] = 0.f;
-    constexpr int kAhead = 8;
+  const int vecs = todo.y * per;
+  int parts = 1;
+  while (parts < kMergeWarps && parts * kAhead < todo.w) parts *= 2;
+  const int part = warp % parts;
+  const int b0 = (int)((long long)todo.w * part / parts);
+  const int b1 = (int)((long long)todo.w * (part + 1) / parts);
 #pragma unroll 1
-    for (int b = 0; b < todo.w; b += kAhead) {
-      float2 ml[kAhead];
-      float x[kAhead][D / 32];
+  for (int v0 = 0; v0 < vecs; v0 += kMergeWarps / parts) {
+    const int item = v0 + warp / parts, v = min(item, vecs - 1);
+    float M = kLeast, L = 0.f, a[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) a[k] = 0.f;
+    // takes states `ml` and `x` of n pieces in
+    auto take = [&](const float2* ml, float (*x)[kCols], int n) {
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
+      const float keep = ex2_approx(M - top);
+      M = top;
+      L *= keep;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) a[k] *= keep;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int j = min(b + i, todo.w - 1);
+        if (i >= n) continue;
+        const float w = ex2_approx(ml[i].x - M);
+        L = fmaf(w, ml[i].y, L);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) a[k] = fmaf(w, x[i][k], a[k]);
+      }
+    };
+#pragma unroll 1
+    for (int b = b0; b < b1 && item < vecs; b += kAhead) {
+      float2 ml[kAhead];
+      float x[kAhead][kCols];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = min(b + i, b1 - 1);
         const size_t at =
             ((size_t)(2 * (worker + j) + (j == 0 ? 1 : 0)) * p.heads_per_worker + head) * kVecs + v;
         ml[i] = __ldcg(p.ml + at);
-        const float* src = p.acc + at * D + lane * (D / 32);
+        const float* src = p.acc + at * D + lane * kCols;
         if constexpr (D == 128) {
           const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
           x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
@@ -731,30 +920,43 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ 
           x[i][0] = f.x, x[i][1] = f.y;
         }
       }
-      float top = M;
+      take(ml, x, b1 - b);
+    }
+    if (parts > 1) {  // the first of the warps that share joins their states, in order
+      __syncthreads();
+      float* st = s_state[warp];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
-      const float keep = ex2_approx(M - top);
-      M = top;
-      L *= keep;
+      for (int k = 0; k < kCols; ++k) st[lane * kCols + k] = a[k];
+      if (lane == 0) st[D] = M, st[D + 1] = L;
+      __syncthreads();
+      if (part == 0) {
+        M = kLeast, L = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) a[k] *= keep;
+        for (int k = 0; k < kCols; ++k) a[k] = 0.f;
+#pragma unroll 1
+        for (int b = 0; b < parts; b += kAhead) {
+          float2 ml[kAhead];
+          float x[kAhead][kCols];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (b + i >= todo.w) continue;
-        const float w = ex2_approx(ml[i].x - M);
-        L = fmaf(w, ml[i].y, L);
+          for (int i = 0; i < kAhead; ++i) {
+            const float* o = s_state[warp + min(b + i, parts - 1)];
+            ml[i] = make_float2(o[D], o[D + 1]);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) a[k] = fmaf(w, x[i][k], a[k]);
+            for (int k = 0; k < kCols; ++k) x[i][k] = o[lane * kCols + k];
+          }
+          take(ml, x, parts - b);
+        }
       }
     }
-    const float inv = L > 0.f ? v_unit / L : 0.f;
+    if (part != 0 || item >= vecs) continue;
+    const int kv_head = (todo.z / p.subs) * p.heads_per_worker + head;
+    const float inv = L > 0.f ? (p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f) / L : 0.f;
     const int tok = v / per;
     T* out = static_cast<T*>(p.c.out) +
-             (((size_t)todo.x + tok) * p.c.heads + kv_head * p.c.group + sub * kVecs + (v - tok * per)) * D +
-             lane * (D / 32);
+             (((size_t)todo.x + tok) * p.c.heads + kv_head * p.c.group + sub * kVecs +
+              (v - tok * per)) * D + lane * kCols;
 #pragma unroll
-    for (int k = 0; k < D / 32; k += 2) {
+    for (int k = 0; k < kCols; k += 2) {
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float2*>(out + k) = make_float2(a[k] * inv, a[k + 1] * inv);
       else
@@ -779,7 +981,7 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 
 template <int D>
 constexpr int smem_bytes(int warps) {
-  return warps * (int)(Ring<D>::kWarp + kSegments * sizeof(Segment) + kStages * 8);
+  return warps * (int)(Ring<D>::kWarp + kSegmentBytes + kStages * 8);
 }
 
 template <typename T, int D, int NT, bool CAP, bool BIAS>
@@ -791,7 +993,8 @@ cudaError_t launch_one(const Kv4VecParams& p, cudaStream_t stream) {
              smem_bytes<D>(warps), stream, &attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_vec_kernel<T, D, NT, CAP, BIAS>, p);
   if (e != cudaSuccess) return e;
-  cfg = config(dim3((unsigned)p.c.grid, (unsigned)p.heads_per_worker), 128, 0, stream, &attr);
+  cfg = config(dim3((unsigned)p.c.grid, (unsigned)p.heads_per_worker), kMergeWarps * 32, 0,
+               stream, &attr);
   return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T, D, NT>, p);
 }
 
