@@ -8,8 +8,10 @@
 // unrounded weights).
 //
 // A warp works alone: it takes its own share of the units (chunk.cuh; 32 positions,
-// two blocks), copies their tiles into its own ring in shared memory by bulk copies,
-// and needs no other warp until the end.  heads_per_worker warps, one per KV head,
+// two blocks), copies their tiles into its own ring in shared memory by 16-byte
+// asynchronous copies, and needs no other warp until the end.  (Four bulk copies a unit
+// instead: 165 us against 160 for 256 single tokens: a warp stands still for longer to issue
+// them than for nine copies a lane.)  heads_per_worker warps, one per KV head,
 // share the same rows and positions, so that the tiles of a block, which lie one
 // after the other, are read at about the same time.
 //
@@ -32,8 +34,7 @@
 // sum of two fp16 numbers (2^-23).
 //
 // A tile cut between workers leaves partial states; kv4_merge_kernel joins them in the
-// order of their positions.  Waits are bounded; one that gives up sets
-// NSV_DEV_TIMEOUT and its warp ends once its own copies have landed.
+// order of their positions.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -76,6 +77,17 @@ struct Ring {
   static constexpr uint32_t kStage = 4 * kTile;  // keys of two blocks, values of two blocks
   static constexpr uint32_t kWarp = kStages * kStage;
 };
+
+// An asynchronous copy of 16 bytes; the thread's copies so far become a group; a wait for
+// all of the thread's groups but the last N.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Shared memory by its 32-bit address, as ordinary loads (which barriers order).
 template <typename V>
@@ -196,7 +208,7 @@ struct Worker {
 
   const Kv4VecParams& p;
   int lane, g, t;       // g: MMA row or column, t: its pair
-  uint32_t ring, bars;  // shared-memory addresses
+  uint32_t ring;        // its shared-memory address
   Segment* segments;
   int head;             // within a group of heads
   // The copies' side: the walk, what its segment has left, and the ring's next stage.
@@ -206,11 +218,11 @@ struct Worker {
   };
   volatile Own* own;
   const int32_t* table;
-  const uint8_t* pool;  // lanes 0 and 1: keys, 2 and 3: values; of the segment's KV head
+  const uint8_t* pool;  // this lane's part of the segment's KV head's tiles
   int block, block_end, units;  // next block, one past the last that any vector sees
   int ids, ids_from;    // the lane's block id of the 32 from ids_from on
   uint32_t fill, opened;
-  uint32_t at, parity;  // the stage that is next to be worked on, and its turn
+  uint32_t at;          // the stage that is next to be worked on
   uint32_t missing;     // two bits a stage: blocks that are not there though they should be
 
   __device__ __forceinline__ Worker(const Kv4VecParams& p_) : p(p_) {}
@@ -306,34 +318,41 @@ struct Worker {
     block = s.t.kb / kBlock + 2 * s.j0;
     block_end = (int)((unsigned)(s.t.ke + kBlock - 1) / kBlock);
     table = p.c.block_tables + (size_t)s.t.row * p.c.max_blocks;
-    pool = (lane < 2 ? p.k_pool : p.v_pool) +
+    pool = (lane < 16 ? p.k_pool : p.v_pool) + (lane & 7) * 16 +
            (size_t)((s.head / p.subs) * p.heads_per_worker + head) * R::kTile;
     ids_from = block - 32;
   }
 
-  // Copies of the next unit into the ring, if there is one.
+  // Copies of the next unit into the ring, if there is one, as a group of their own: eight
+  // lanes a tile (the first block's keys, the second's, their values), whole lines.
   __device__ __forceinline__ void issue() {
-    if (units == 0) return;
-    if (block - ids_from >= 32) {
-      ids = block + lane < block_end ? __ldg(table + block + lane) : -1;
-      ids_from = block;
+    if (units != 0) {
+      if (block - ids_from >= 32) {
+        ids = block + lane < block_end ? __ldg(table + block + lane) : -1;
+        ids_from = block;
+      }
+      const int b = block + ((lane >> 3) & 1);
+      const int id = __shfl_sync(kFull, ids, b - ids_from);
+      const bool ok = b < block_end && id >= 0 && id < p.c.pool_blocks;
+      if (ok) {
+        const uint8_t* src = pool + (size_t)(unsigned)id * ((unsigned)p.kv_heads * R::kTile);
+        const uint32_t dst = ring + fill * R::kStage + (lane >> 3) * R::kTile + (lane & 7) * 16;
+#pragma unroll
+        for (uint32_t i = 0; i < R::kTile / 128; ++i) copy16(dst + i * 128, src + i * 128);
+        if (R::kTile % 128 && (lane & 7) * 16 < R::kTile % 128)
+          copy16(dst + R::kTile / 128 * 128, src + R::kTile / 128 * 128);
+      }
+      if (!__all_sync(kFull, ok)) {  // past the last block, or a bad one
+        const uint32_t there = __ballot_sync(kFull, ok);
+        missing |= (((there & 1u) | ((there >> 7) & 2u)) ^ 3u) << (2 * fill);
+        if (b < block_end && !ok && (lane == 0 || lane == 8))
+          atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_BLOCK);
+      }
+      fill = fill + 1 == kStages ? 0 : fill + 1;
+      block += 2;
+      if (--units == 0) open();
     }
-    const int b = block + (lane & 1);
-    const int id = __shfl_sync(kFull, ids, b - ids_from);
-    const bool ok = b < block_end && id >= 0 && id < p.c.pool_blocks;
-    const uint32_t mask = __ballot_sync(kFull, ok) & 3u, bar = bars + 8 * fill;
-    if (lane == 0) mbar_arrive_tx(bar, __popc(mask) * 2 * R::kTile);
-    __syncwarp();
-    if (lane < 4 && ok)
-      bulk_load(ring + fill * R::kStage + lane * R::kTile,
-                pool + (size_t)(unsigned)id * ((unsigned)p.kv_heads * R::kTile), R::kTile, bar);
-    if (mask != 3u) {  // past the last block, or a bad one
-      if (b < block_end && !ok && lane < 2) atomicOr(p.c.status, (uint32_t)NSV_DEV_BAD_BLOCK);
-      missing |= (mask ^ 3u) << (2 * fill);
-    }
-    fill = fill + 1 == kStages ? 0 : fill + 1;
-    block += 2;
-    if (--units == 0) open();
+    copy_group();
   }
 
   // Scores of a block: c[nt], rows are tokens, columns query vectors.
@@ -491,10 +510,10 @@ struct Worker {
     }
   }
 
-  // The whole share; false when a wait gave up.
-  __device__ __forceinline__ bool run(int worker) {
+  // The whole share.
+  __device__ __forceinline__ void run(int worker) {
     if (!p.row_tiles) wk.init(p.c, worker);
-    opened = fill = missing = at = parity = 0;
+    opened = fill = missing = at = 0;
     open();
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue();
@@ -503,7 +522,7 @@ struct Worker {
     for (uint32_t taken = 0;; ++taken) {
       __syncwarp();
       const volatile Segment* s = segments + taken % kSegments;
-      if (!s->valid) return true;
+      if (!s->valid) return;
       const int sub = s->head % p.subs;
       const int kv_head = (s->head / p.subs) * p.heads_per_worker + head;
       const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
@@ -611,8 +630,9 @@ struct Worker {
       int t0 = s->kb + s->j0 * kVecKeys;
 #pragma unroll 1
       for (int n = s->j1 - s->j0; n > 0; --n, t0 += kVecKeys) {
-        issue();  // into the stage that the unit before last was in
-        if (!warp_wait(bars + 8 * at, parity)) return false;
+        issue();  // into the stage that the unit before was in
+        copy_wait<kStages - 1>();
+        __syncwarp();  // every lane's copies of this unit are there
         const uint32_t stage = ring + at * R::kStage;
         float x[2][NT][4];
 #pragma unroll
@@ -736,7 +756,6 @@ struct Worker {
         }
         values(stage + 2 * R::kTile, pb, dead, o);
         at = at + 1 == kStages ? 0 : at + 1;
-        if (at == 0) parity ^= 1;
         __syncwarp();  // all lanes have read the stage
       }
 
@@ -813,14 +832,8 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const uint32_t base = smem_u32(smem);
   using W = Worker<T, D, NT, CAP, BIAS>;
-  const uint32_t segments = warps * R::kWarp, bars = segments + warps * kSegmentBytes;
+  const uint32_t segments = warps * R::kWarp;
   W w(p);
-  w.bars = base + bars + warp * kStages * 8;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(w.bars + 8 * i, 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
   griddep_wait();  // the tile list, and whatever was written before it
   griddep_launch();
   const int worker = blockIdx.x * p.workers_per_cta + warp / p.heads_per_worker;
@@ -836,20 +849,12 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
     static_assert(sizeof(OwnPlan) <= R::kWarp, "the ring of one warp");
     own_plan(p, o);
     w.start(o, worker);
-    __syncthreads();  // (what was written there came by ordinary stores)
-    fence_proxy_async_smem();
+    __syncthreads();
   }
   if (worker >= p.c.grid) return;
   if (w.head == 0 && lane == 0) p.todo[worker] = make_int4(0, 0, 0, 0);
-  if (!w.run(worker)) {
-    if (lane == 0) atomicOr(p.c.status, (uint32_t)NSV_DEV_TIMEOUT);
-    // every copy issued lands before the CTA can end
-    do {
-      (void)warp_wait(w.bars + 8 * w.at, w.parity);
-      w.at = w.at + 1 == kStages ? 0 : w.at + 1;
-      if (w.at == 0) w.parity ^= 1;
-    } while (w.at != w.fill);
-  }
+  w.run(worker);
+  copy_wait<0>();
 }
 
 // Joins the pieces of the tile that worker blockIdx.x starts and does not end, for KV head
@@ -981,7 +986,7 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 
 template <int D>
 constexpr int smem_bytes(int warps) {
-  return warps * (int)(Ring<D>::kWarp + kSegmentBytes + kStages * 8);
+  return warps * (int)(Ring<D>::kWarp + kSegmentBytes);
 }
 
 template <typename T, int D, int NT, bool CAP, bool BIAS>

@@ -500,20 +500,23 @@ def chunk_step(q, k_new, v_new, write_slots, k_pool, v_pool, block_tables, chunk
     return out
 
 
-def _heads_arg(t, what, dtype, heads, head_dim, tokens, dev):
+def _heads_arg(t, what, dtype, shape, dev):
     """The pointer and token stride of [tokens, heads, head_dim], whose tokens may
     lie apart (as in a slice of a projection's output)."""
-    if t.dtype != dtype or t.shape != (tokens, heads, head_dim):
-        raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, [tokens, heads, head_dim],
-                                                          t.dtype, list(t.shape)))
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s must be %s %s, got %s %s" % (what, dtype, list(shape), t.dtype,
+                                                          list(t.shape)))
     if t.get_device() != dev:
         raise ValueError("%s is on %s, not on the current CUDA device %d" % (what, t.device, dev))
     token, head, dim = t.stride()
-    if dim != 1 or (heads > 1 and head != head_dim):
+    tokens, heads, head_dim = shape
+    if dim != 1 or (head != head_dim and heads > 1):
         raise ValueError("%s must have contiguous heads and dimensions" % what)
-    if tokens > 1 and token < heads * head_dim:
+    if tokens <= 1:
+        return t.data_ptr(), 0
+    if token < heads * head_dim:
         raise ValueError("the tokens of %s overlap" % what)
-    return t.data_ptr(), token if tokens > 1 else 0
+    return t.data_ptr(), token
 
 
 def kv4_pool(num_blocks, kv_heads, head_dim, device="cuda"):
@@ -539,29 +542,35 @@ def _append_shape(heads, kv_heads, head_dim, num_blocks, dtype, block_size):
 
 def _append_args(q, k_new, v_new, positions, rotary, write_slots, kv_heads, head_dim, q_out,
                  interleaved, dev):
-    """What both rotating appends pass: the new tensors' pointers and strides, and
-    the nsv_rope (None without a rotation)."""
+    """What both rotating appends pass: the query heads, the nsv_rope (None without a
+    rotation), and tokens, tensors, strides and slots; q_out's pointer."""
     import torch
     T, dt = write_slots.numel(), k_new.dtype
-    heads = kv_heads
-    q_args = (None, 0)
+    one = (T,)
+    heads, q_ptr, q_stride, out = kv_heads, None, 0, None
     if q is not None:
-        if q.dim() != 3:
+        shape = q.shape
+        if len(shape) != 3:
             raise ValueError("q must be [tokens, heads, head_dim]")
-        heads = q.shape[1]
-        q_args = _heads_arg(q, "q", dt, heads, head_dim, T, dev)
-    out = _arg(q_out, "q_out", dt, (T, heads, head_dim), dev)
-    k, ks = _heads_arg(k_new, "k_new", dt, kv_heads, head_dim, T, dev)
-    v, vs = _heads_arg(v_new, "v_new", dt, kv_heads, head_dim, T, dev)
-    slots = _arg(write_slots, "write_slots", torch.int64, (T,), dev)
+        heads = shape[1]
+        want = (T, heads, head_dim)
+        q_ptr, q_stride = _heads_arg(q, "q", dt, want, dev)
+        out = _arg(q_out, "q_out", dt, want, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    want = (T, kv_heads, head_dim)
+    k, ks = _heads_arg(k_new, "k_new", dt, want, dev)
+    v, vs = _heads_arg(v_new, "v_new", dt, want, dev)
+    slots = _arg(write_slots, "write_slots", torch.int64, one, dev)
     rope = None
     if rotary is not None or positions is not None:
         if rotary is None or positions is None or rotary.dim() != 2:
             raise ValueError("a rotation takes positions and a table [positions, rotary_dim]")
-        rope = ctypes.byref(Rope(_arg(rotary, "rotary", torch.float32, rotary.shape, dev),
-                                 _arg(positions, "positions", torch.int32, (T,), dev),
-                                 rotary.shape[0], rotary.shape[1], 1 if interleaved else 0))
-    return rope, heads, T, (T, q_args[0], k, v, q_args[1], ks, vs, slots), out
+        n, dims = rotary.shape
+        rope = ctypes.byref(Rope(_arg(rotary, "rotary", torch.float32, (n, dims), dev),
+                                 _arg(positions, "positions", torch.int32, one, dev), n, dims,
+                                 1 if interleaved else 0))
+    return rope, heads, (T, q_ptr, k, v, q_stride, ks, vs, slots), out
 
 
 def rope_write(q, k_new, v_new, positions, rotary, write_slots, k_pool, v_pool, q_out=None,
@@ -570,12 +579,13 @@ def rope_write(q, k_new, v_new, positions, rotary, write_slots, k_pool, v_pool, 
     append the values (nsv_rope_write in nsv.h).  q and q_out may be None."""
     import torch
     dev = torch.cuda.current_device()
-    if k_pool.dim() != 4 or k_new.dtype != k_pool.dtype:
+    ks, dt = k_pool.shape, k_pool.dtype
+    if len(ks) != 4 or k_new.dtype != dt:
         raise ValueError("the pools must be [blocks + 1, kv_heads, 16, head_dim] of k_new's type")
-    pools = _pool_args(k_pool, v_pool, None, dev)
-    NB1, Hkv, B, D = k_pool.shape
-    rope, heads, _, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
-                                             q_out, interleaved, dev)
+    pools = _arg(k_pool, "k_pool", dt, ks, dev), _arg(v_pool, "v_pool", dt, ks, dev)
+    NB1, Hkv, B, D = ks
+    rope, heads, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
+                                          q_out, interleaved, dev)
     shape = _append_shape(heads, Hkv, D, NB1 - 1, _dtype_code(k_pool), B)
     _check(_lib.nsv_rope_write(shape, rope, *args, *pools, out, _raw_stream(stream, dev)),
            "nsv_rope_write")
@@ -589,8 +599,8 @@ def kv4_write(k_new, v_new, write_slots, k_pool, v_pool, k_scales=None, v_scales
     import torch
     dev, f32, u8 = torch.cuda.current_device(), torch.float32, torch.uint8
     blocks, Hkv, D = _kv4_sizes(k_pool)
-    rope, heads, _, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
-                                             q_out, interleaved, dev)
+    rope, heads, args, out = _append_args(q, k_new, v_new, positions, rotary, write_slots, Hkv, D,
+                                          q_out, interleaved, dev)
     shape = _append_shape(heads, Hkv, D, blocks, _dtype_code(k_new), 16)
     _check(_lib.nsv_kv4_write(shape, rope, _arg(k_scales, "k_scales", f32, (Hkv,), dev),
                               _arg(v_scales, "v_scales", f32, (Hkv,), dev), *args,

@@ -175,14 +175,14 @@ def test_binding_checks_layouts(nsv):
     cpu = torch.zeros(1).get_device()       # what a CPU tensor answers: no CUDA device's number
     fused = torch.zeros(5, 12, 64)
     q = fused[:, 4:8]
-    assert nsv._heads_arg(q, "q", torch.float32, 4, 64, 5, cpu) == (q.data_ptr(), 12 * 64)
-    assert nsv._heads_arg(q[:1], "q", torch.float32, 4, 64, 1, cpu)[1] == 0
+    assert nsv._heads_arg(q, "q", torch.float32, (5, 4, 64), cpu) == (q.data_ptr(), 12 * 64)
+    assert nsv._heads_arg(q[:1], "q", torch.float32, (1, 4, 64), cpu)[1] == 0
     for bad in (q.transpose(0, 1), fused[:, ::2][:, :4], fused.expand(5, 12, 64)[:, :4, ::1].double(),
                 torch.zeros(1, 4, 64).expand(5, 4, 64), torch.zeros(5, 4, 128)[..., ::2]):
         with pytest.raises(ValueError):
-            nsv._heads_arg(bad, "q", torch.float32, 4, 64, 5, cpu)
+            nsv._heads_arg(bad, "q", torch.float32, (5, 4, 64), cpu)
     with pytest.raises(ValueError):
-        nsv._heads_arg(q, "q", torch.float32, 4, 64, 5, 0)
+        nsv._heads_arg(q, "q", torch.float32, (5, 4, 64), 0)
     assert nsv._kv4_sizes(torch.zeros((4, 2, 9 * 64), dtype=torch.uint8)) == (3, 2, 64)
     for bad in (torch.zeros((4, 2, 9 * 64)), torch.zeros((4, 2, 100), dtype=torch.uint8),
                 torch.zeros((4, 2, 16, 72), dtype=torch.uint8)):
