@@ -59,13 +59,13 @@ using namespace sm;
 constexpr int kSoftWarps = 16;
 // Over a 4-bit cache: warps 16-19 widen, 20 issues, 21 publishes, 22 fetches tiles, 23 fills
 // the last warpgroup up.  80 registers a thread at launch, dealt out anew (a multiple of 8 each;
-// 16 x 88 + 4 x 64 + 4 x 64 = 24 x 80).
+// 16 x 88 + 4 x 72 + 4 x 56 = 24 x 80).
 constexpr int kWidenWarps = 4;
 // Tiles as they are in the pool wait in a ring of half runs (a run's keys or values).
 constexpr int kTileRing = 3;
 template <int D>
 constexpr uint32_t kHalfRun = kChunkKeys / kBlock * kv4_tile_bytes(D);
-constexpr int kRegsSoft = 88, kRegsWiden = 64, kRegsRest = 64;
+constexpr int kRegsSoft = 88, kRegsWiden = 72, kRegsRest = 56;
 template <bool KV4>
 constexpr int kThreads = (KV4 ? kSoftWarps + kWidenWarps + 4 : kSoftWarps + 3) * 32;
 template <bool KV4>
@@ -107,7 +107,8 @@ struct Smem {
   static constexpr uint32_t kOffUp = kOffWord + 16;
   static constexpr uint32_t kOffTiles = (kOffUp + 128 + 127) / 128 * 128;
   static constexpr uint32_t kOffTileBars = kOffTiles + kTileRing * kHalfRun<D>;  // full, free
-  static constexpr uint32_t kTotal = KV4 ? kOffTileBars + 2 * kTileRing * 8 : kOffWord + 16;
+  static constexpr uint32_t kOffRows = kOffTileBars + 2 * kTileRing * 8;  // query rows are there
+  static constexpr uint32_t kTotal = KV4 ? kOffRows + 8 : kOffWord + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
@@ -153,41 +154,54 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 }
 
 // ------------------------------------------------------------------ producer
+// A segment's query rows, onto the barrier `full`.
+template <int D, bool KV4>
+__device__ __forceinline__ bool load_queries(const ChunkParams& p, const Bars<D, KV4>& B,
+                                             uint32_t full, uint32_t smem0,
+                                             const volatile uint32_t* s_done,
+                                             const ChunkSegment& s, int lane, uint32_t nseg,
+                                             uint32_t& shared) {
+  using L = Smem<D, KV4>;
+  const int half_tok = p.tile_tokens / 2;
+  // the query rows: one box of (tokens, group heads, 64 dims) per half or
+  // copy and 64-dim slice; tokens past the tensor are filled with zeros
+  if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
+  const int copies = copies_of(p, s);
+  // The second half may still serve an earlier tile's copies.  (A count, not a
+  // barrier's parity: their epilogue can be two tiles behind.)
+  if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
+  if (copies == 0) shared = 0;
+  if (copies > 1) shared = nseg + 1;
+  if (lane == 0) {
+    const int boxes = copies == 0 ? 2 : copies;
+    const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
+    const int box_tok = box_rows / p.group;
+    const CUtensorMap* map = &p.tmap_q[copies == 4 ? 2 : copies == 2 ? 1 : 0];
+    mbar_arrive_tx(full, (uint32_t)(boxes * box_tok * p.group * D * 2));
+#pragma unroll 1
+    for (int x = 0; x < boxes; ++x)
+      for (int d = 0; d < D / 64; ++d)
+        tma_load_3d(smem0 + L::kOffQ + (copies == 0 ? x * L::kHalf : x * box_rows * 128) +
+                        d * (kChunkHalfRows * 128),
+                    map, d * 64, s.head * p.group, s.t.q0 + (copies == 0 ? x * half_tok : 0),
+                    full);
+  }
+  return true;
+}
+
 template <int D>
 __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, false>& B, uint32_t smem0,
                                         volatile int* s_meta, const volatile uint32_t* s_done,
                                         ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
   using L = Smem<D, false>;
   constexpr uint32_t kBlockBytes = kBlock * D * 2;
-  const int half_tok = p.tile_tokens / 2;
   uint32_t run = 0;
   uint32_t shared = 0;  // segments up to and with the last one whose copies were exchanged
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
-    // the query rows: one box of (tokens, group heads, 64 dims) per half or
-    // copy and 64-dim slice; tokens past the tensor are filled with zeros
-    if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
-    const int copies = copies_of(p, s);
-    // The second half may still serve an earlier tile's copies.  (A count, not a
-    // barrier's parity: their epilogue can be two tiles behind.)
-    if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
-    if (copies == 0) shared = 0;
-    if (copies > 1) shared = nseg + 1;
-    if (lane == 0) {
-      const int boxes = copies == 0 ? 2 : copies;
-      const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
-      const int box_tok = box_rows / p.group;
-      const CUtensorMap* map = &p.tmap_q[copies == 4 ? 2 : copies == 2 ? 1 : 0];
-      mbar_arrive_tx(B.qfull(), (uint32_t)(boxes * box_tok * p.group * D * 2));
-#pragma unroll 1
-      for (int x = 0; x < boxes; ++x)
-        for (int d = 0; d < D / 64; ++d)
-          tma_load_3d(smem0 + L::kOffQ + (copies == 0 ? x * L::kHalf : x * box_rows * 128) +
-                          d * (kChunkHalfRows * 128),
-                      map, d * 64, s.head * p.group, s.t.q0 + (copies == 0 ? x * half_tok : 0),
-                      B.qfull());
-    }
+    if (!load_queries<D, false>(p, B, B.qfull(), smem0, s_done, s, lane, nseg, shared))
+      return false;
     ++nseg;
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
     auto block_id = [&](int j) -> int {  // lane's block of run j, -1 past the tile's keys
@@ -231,94 +245,67 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, fals
 //
 // Query rows: 32 rows (a softmax warp's) are scaled by one power of two, so that the
 // largest element lies in [2^14, 2^15): exact but for elements below 2^-28 of it, off by
-// 2^-40 of it at most.  Two passes, of which the first runs before the rows are free.
+// 2^-40 of it at most.  They arrive as bulk copies bring them and are converted in place, by
+// a warp for the 32 rows of its number in each half.  (Loaded from global memory instead,
+// the two passes made a tile's start several us longer.)
 template <int D>
-__device__ __forceinline__ bool widen_queries(const ChunkParams& p, const Bars<D, true>& B,
-                                              unsigned char* smem, const volatile uint32_t* s_done,
-                                              const ChunkSegment& s, uint32_t nseg,
-                                              uint32_t& shared, int ww, int lane) {
+__device__ __forceinline__ void widen_queries(const ChunkParams& p, const Bars<D, true>& B,
+                                              unsigned char* smem, const ChunkSegment& s,
+                                              uint32_t nseg, int ww, int lane) {
   using L = Smem<D, true>;
-  constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows a load
-  const int copies = copies_of(p, s);
-  const int chunk = lane % kChunks, halves = copies == 0 ? 2 : 1;
+  const int copies = copies_of(p, s), halves = copies == 0 ? 2 : 1;
   const int copy_rows = copies > 1 ? kChunkHalfRows / copies : kChunkHalfRows;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-  auto row_of = [&](int i) { return 32 * ww + kRows * i + lane / kChunks; };
-  auto load = [&](int x, int i) {
-    const int rc = row_of(i) & (copy_rows - 1);
-    const int ti = (int)((unsigned)rc / (unsigned)p.group), g = rc - ti * p.group;
-    const int tok = x * (p.tile_tokens / 2) + ti;
-    if ((ti + 1) * p.group > copy_rows || tok >= s.t.n_tok) return make_uint4(0, 0, 0, 0);
-    return __ldg(reinterpret_cast<const uint4*>(
-        q + (((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g) * D + chunk * 8));
-  };
-  constexpr int kBatch = 4;
-  int exps[2] = {0, 0};  // of the powers of two
 #pragma unroll 1
   for (int x = 0; x < halves; ++x) {
+    // rows that are there, of those of a copy or half
+    const int there =
+        min(s.t.n_tok - x * (p.tile_tokens / 2), copy_rows / p.group) * p.group;
+    unsigned char* rows = smem + L::kOffQ + x * L::kHalf + ww * 32 * 128 + lane * 16;
+    auto at = [&](int i) {  // four rows' 64 dimensions
+      return reinterpret_cast<uint4*>(rows + (i >> 3) * (kChunkHalfRows * 128) + (i & 7) * 512);
+    };
     uint32_t top = 0;  // of the elements' magnitudes, as fp32
-#pragma unroll 1
-    for (int i = 0; i < kChunks; i += kBatch) {
-      uint4 r[kBatch];
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 r = *at(i);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      const int row = ww * 32 + 4 * (i & 7) + (lane >> 3);
+      if ((row & (copy_rows - 1)) >= there) continue;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) r[k] = load(x, i + k);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
-      }
+      for (int e = 0; e < 4; ++e)
+        top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
     }
     const int e = min(126, 14 + 127 - (int)(__reduce_max_sync(kFull, top) >> 23));
-    if (x) exps[1] = e; else exps[0] = e;
-  }
-  if (nseg && !warp_wait(B.qfree(), (nseg - 1) & 1)) return false;
-  // (as in produce)
-  if (copies == 0 && shared && !count_wait(s_done, shared * kSoftWarps)) return false;
-  if (copies == 0) shared = 0;
-  if (copies > 1) shared = nseg + 1;
-#pragma unroll 1
-  for (int x = 0; x < halves; ++x) {
-    const int e = x ? exps[1] : exps[0];
     const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
     if (lane == 0)
       reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + 4 * x + ww] =
           __uint_as_float((uint32_t)(127 - e) << 23);
-    unsigned char* half = smem + L::kOffQ + x * L::kHalf + (chunk >> 3) * (kChunkHalfRows * 128);
-#pragma unroll 1
-    for (int i = 0; i < kChunks; i += kBatch) {
-      uint4 r[kBatch];
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 r = *at(i);
+      uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) r[k] = load(x, i + k);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
-#pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2)
-          w[e2] = pack_half(__uint_as_float(w[e2] << 16) * mul,
-                            __uint_as_float(w[e2] & 0xffff0000u) * mul);
-        const int row = row_of(i + k);
-        *reinterpret_cast<uint4*>(half + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int k = 0; k < 4; ++k)
+        w[k] = pack_half(__uint_as_float(w[k] << 16) * mul,
+                         __uint_as_float(w[k] & 0xffff0000u) * mul);
+      *at(i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(B.qfull());
-  return true;
 }
 
-// The tiles of a run's keys, then of its values, by one warp into a ring of half runs: a
-// lane copies a block.
+// The query rows, and the tiles of a run's keys, then of its values, by one warp: tiles into
+// a ring of half runs, a lane copies a block.
 template <int D>
-__device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, uint32_t smem0,
-                                            volatile int* s_meta, ChunkWalk wk, int lane,
-                                            uint32_t& issued) {
+__device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, const Bars<D, true>& B,
+                                            uint32_t smem0, volatile int* s_meta,
+                                            const volatile uint32_t* s_done, ChunkWalk wk,
+                                            int lane, uint32_t& issued, uint32_t& nseg) {
   using L = Smem<D, true>;
   constexpr uint32_t kTile = kv4_tile_bytes(D);
-  uint32_t run = 0, in = 0, parity = 1;
+  uint32_t run = 0, in = 0, parity = 1, shared = 0;
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
@@ -328,6 +315,9 @@ __device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, uint32_t smem0
       return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
     };
     int id = block_id(s.j0);
+    if (!load_queries<D, true>(p, B, smem0 + L::kOffRows, smem0, s_done, s, lane, nseg, shared))
+      return false;
+    ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
       const bool wanted = lane < kChunkKeys / kBlock &&
@@ -367,20 +357,20 @@ __device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, uint32_t smem0
 template <int D>
 __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>& B,
                                       unsigned char* smem, const volatile int* s_meta,
-                                      const volatile uint32_t* s_done, ChunkWalk wk, int ww,
-                                      int lane) {
+                                      ChunkWalk wk, int ww, int lane) {
   using L = Smem<D, true>;
   constexpr uint32_t kTile = kv4_tile_bytes(D);
   constexpr int kWords = D / 32;                         // words of a lane's quarter
   constexpr int kEights = kChunkKeys / 8 / kWidenWarps;  // of tokens a half run
   const int row = lane >> 2, part = lane & 3;
   const uint32_t smem0 = smem_u32(smem);
-  uint32_t i = 0, run = 0, nseg = 0, shared = 0;
+  uint32_t i = 0, run = 0, nseg = 0;
   uint32_t out = 0, parity = 0;  // the ring slot to read, and its turn
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
-    if (!widen_queries<D>(p, B, smem, s_done, s, nseg, shared, ww, lane)) return false;
+    if (!warp_wait(smem0 + L::kOffRows, nseg & 1)) return false;
+    widen_queries<D>(p, B, smem, s, nseg, ww, lane);
     ++nseg;
 #pragma unroll 1
     for (int h = 2 * s.j0; h < 2 * s.j1; ++h, ++i) {
@@ -986,6 +976,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
                   KV4 && (i < L::kStages || i == 2 * L::kStages) ? kWidenWarps : 1);
       for (int i = 0; KV4 && i < 2 * kTileRing; ++i)
         mbar_init(smem0 + L::kOffTileBars + 8 * i, i < kTileRing ? 1 : kWidenWarps);
+      if (KV4) mbar_init(smem0 + L::kOffRows, 1);
       mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
@@ -1039,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
   } else if (KV4 && warp < kSoftWarps + kWidenWarps) {
     if constexpr (KV4) {
       reg_dec<kRegsWiden>();
-      ok = widen<D>(p, B, smem, s_meta, s_done, wk, warp - kSoftWarps, lane);
+      ok = widen<D>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
     }
   } else if (!KV4 && warp == kSoftWarps) {
     if constexpr (!KV4) {
@@ -1064,8 +1055,9 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
     } else if (warp == kMmaWarp<KV4> + 2) {
       if constexpr (KV4) {
-        uint32_t issued = 0;
-        ok = fetch_tiles<D>(p, smem0, s_meta, wk, lane, issued);
+        uint32_t issued = 0, nq = 0;
+        ok = fetch_tiles<D>(p, B, smem0, s_meta, s_done, wk, lane, issued, nq);
+        if (nq) (void)mbar_wait(smem0 + L::kOffRows, (nq - 1) & 1);
         // every copy issued lands before the CTA can end, even after a timeout
         for (uint32_t k = issued > kTileRing ? issued - kTileRing : 0; k < issued; ++k)
           (void)mbar_wait(smem0 + L::kOffTileBars + 8 * (k % kTileRing), (k / kTileRing) & 1);
