@@ -248,12 +248,16 @@ def test_unseen_keys_may_be_anything(dtype, new):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_bad_lengths_starts_blocks_and_counts(dtype):
+@pytest.mark.parametrize("most", [0, 1])     # with a list of tiles, and without
+def test_bad_lengths_starts_blocks_and_counts(dtype, most):
+    import functools
+
     import torch
     from paged_kv_decode_nsv_gb300 import nsv
+    call = functools.partial(globals()["call"], max_new=most)
     ctx, new = [300, 90, 33, 64], [1, 1, 1, 1]
     b = batch(ctx, new, 8, 2, 128, dtype)
-    good = check(b, dtype)
+    good = check(b, dtype, max_new=most)
     b["ctx"][1] = -3
     out = call(b, torch.full_like(b["q"], 7.5))
     assert nsv.device_status()[0] == nsv.DEV_BAD_CTX
@@ -274,7 +278,7 @@ def test_bad_lengths_starts_blocks_and_counts(dtype):
     # more new tokens than the caller said
     b = batch(ctx, [1, 3, 1, 1], 8, 2, 128, dtype)
     full = check(b, dtype)
-    out = call(b, torch.full_like(b["q"], 7.5), max_new=1)
+    out = globals()["call"](b, torch.full_like(b["q"], 7.5), max_new=1)
     assert nsv.device_status()[0] == nsv.DEV_BAD_CHUNK
     assert (out[1:4] == 7.5).all()
     assert torch.allclose(out[[0, 4, 5]].float(), full[[0, 4, 5]].float(), atol=0.03)
@@ -319,12 +323,60 @@ def test_queries_of_any_size(dtype, size):
     check(b, dtype, max_new=1, tol=(F32_TOL if dtype == "f32" else BF16_TOL) + scores * 128 ** 0.5 * 2.0 ** -22)
 
 
-def test_many_rows():
-    rng = np.random.default_rng(3)
-    ctx = rng.integers(0, 60, 8192).tolist()
-    b = batch(ctx, [1 if c else 0 for c in ctx], 4, 1, 64, "bf16")
-    check(b, "bf16", max_new=1)
+@pytest.mark.parametrize("rows,most", [(8192, 1), (2048, 1), (600, 3), (257, 8)])
+def test_many_rows(rows, most):
+    """Around the number of tiles up to which no list is planned, and the largest."""
+    rng = np.random.default_rng(rows)
+    ctx = rng.integers(0, 60, rows).tolist()
+    new = [min(c, int(rng.integers(0, most + 1))) for c in ctx]
+    b = batch(ctx, new, 4, 1, 64, "bf16")
+    check(b, "bf16", max_new=most)
     check(b, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30])
+def test_scales_of_either_sign_and_none(dtype, scale):
+    for ctx, new, most in (([300, 33, 5], [1, 1, 1], 1), ([300, 33, 150], [90, 1, 20], 0)):
+        b = batch(ctx, new, 8, 2, 128, dtype)
+        b["scale"] = scale
+        check(b, dtype, max_new=most)
+
+
+@pytest.mark.parametrize("new,most", [([1, 1, 1], 1), ([60, 40, 33], 0), ([20, 9, 70], 0)])
+def test_neighbours_do_not_matter(new, most):
+    """Query rows of other rows and of no row, whatever they hold, change no bit: query
+    vectors are scaled together with those they share a tile with."""
+    import torch
+    b = batch([400, 300, 70], new, 8, 2, 128, "bf16", pad=5)
+    want = check(b, "bf16", max_new=most)
+    for garbage in (float("nan"), float("inf"), 1e38):
+        for r in range(3):
+            at = int(sum(new[:r]))
+            q = b["q"].clone()
+            b["q"].fill_(garbage)
+            b["q"][at:at + new[r]] = q[at:at + new[r]]
+            out = call(b, torch.full_like(b["q"], 7.5), max_new=most)
+            b["q"].copy_(q)
+            assert torch.equal(out[at:at + new[r]], want[at:at + new[r]])
+
+
+def test_a_pool_past_four_gigabytes():
+    """The same bits from blocks whose bytes lie past 2^32 as from low ones."""
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    heads, kv_heads, dim = 32, 8, 128
+    b = batch([900, 333, 40], [1, 1, 1], heads, kv_heads, dim, "bf16", scaled=True)
+    c = batch([900, 333], [200, 40], heads, kv_heads, dim, "bf16", scaled=True)
+    blocks = (1 << 32) // (kv_heads * 9 * dim) + 500
+    pools = [torch.zeros((blocks + 1, kv_heads, 9 * dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for x, most in ((b, 1), (c, 0)):
+        want = check(x, "bf16", max_new=most)
+        n = x["k"].shape[0]
+        for p, name in zip(pools, ("k", "v")):
+            p[blocks - n:blocks] = x[name]
+        moved = {**x, "k": pools[0], "v": pools[1], "bt": x["bt"] + (blocks - n)}
+        assert torch.equal(call(moved, torch.empty_like(x["q"]), max_new=most), want)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

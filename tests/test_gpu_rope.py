@@ -115,6 +115,25 @@ def test_rope_write_in_place_and_without_queries(dtype):
     assert all(torch.equal(x, y) for x, y in zip(alone, b["pools"]))
 
 
+def test_layouts_that_would_overlap_or_misalign_are_refused():
+    import torch
+    from paged_kv_decode_nsv_gb300 import nsv
+    b = inputs(6, 8, 2, 128, "bf16", 128, False)
+    args = lambda **kw: [kw.get(n, b[n]) for n in ("q", "k", "v", "positions", "table", "slots")]  # noqa: E731
+    out = torch.empty_like(b["q"])
+    one = b["k"][:1].expand(6, 2, 128)
+    wide = torch.zeros((6, 2 * 128 + 4), dtype=torch.bfloat16, device="cuda")
+    for bad, error in ((dict(k=one), ValueError), (dict(v=wide[:, 4:].unflatten(1, (2, 128))), nsv.NsvError),
+                       (dict(v=wide[:, :256].unflatten(1, (2, 128))), nsv.NsvError),
+                       (dict(positions=b["positions"].long()), ValueError),
+                       (dict(table=b["table"][:, :24].contiguous()), nsv.NsvError),
+                       (dict(q=b["q"].float()), ValueError)):
+        with pytest.raises(error):
+            nsv.rope_write(*args(**bad), *b["pools"], out)
+    with pytest.raises(nsv.NsvError):
+        nsv.rope_write(*args(), *b["pools"], None)
+
+
 def test_rope_write_of_no_tokens():
     from paged_kv_decode_nsv_gb300 import nsv
     b = inputs(0, 8, 2, 128, "bf16", 128, False)
@@ -228,6 +247,25 @@ def test_kv4_write_at_every_edge_of_the_format():
     b = inputs(len(rows), 1, 1, 64, "f32", 64, True)
     b["k"], b["v"] = x.contiguous(), x.flip(0).contiguous()
     write4_and_check(b, "f32", rotate=False)
+    # head scales at both ends of their range, and ones that have no short reciprocal
+    for units in ((2.0 ** -60, 2.0 ** 60), (3.0, 1.0 / 3.0), (1.1e-5, 9.7e4), (0.7, 7.0)):
+        write4_and_check(b, "f32", rotate=False,
+                         scales=[torch.tensor([u], dtype=torch.float32).cuda() for u in units])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_kv4_write_of_many_random_values(dtype):
+    """Every rounding of two million values, of sizes over eight powers of two, is the
+    definition's, quotients next to a border among them."""
+    import torch
+    b = inputs(4096, 4, 2, 128, dtype, 128, True)
+    g = torch.Generator().manual_seed(9)
+    for name in ("k", "v"):
+        size = torch.exp2(torch.rand((4096, 2, 8), generator=g) * 8 - 6).repeat_interleave(16, -1)
+        b[name] = (b[name].float().cpu() * size).to(b[name].dtype).cuda()
+    units = [torch.tensor(u, dtype=torch.float32).cuda() for u in ((0.731, 1.0), (3.3, 0.0517))]
+    write4_and_check(b, dtype, scales=units)
+    write4_and_check(b, dtype, rotate=False)
 
 
 def test_kv4_read_leaves_bad_slots_and_takes_repeated_ones():
