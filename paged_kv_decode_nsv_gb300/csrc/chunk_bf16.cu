@@ -57,17 +57,15 @@ namespace {
 using namespace sm;
 
 constexpr int kSoftWarps = 16;
-// Over a 4-bit cache: warps 16-19 widen, 20 issues, 21 publishes, 22 fetches tiles, 23 fills
-// the last warpgroup up.  80 registers a thread at launch, dealt out anew (a multiple of 8 each;
-// 16 x 88 + 4 x 72 + 4 x 56 = 24 x 80).
-constexpr int kWidenWarps = 4;
+// Over a 4-bit cache: warps 16 and 17 widen, 18 issues, 19 fetches and then publishes.  (At
+// most 20 warps, five on a sub-partition, have 96 registers each.)
+constexpr int kWidenWarps = 2;
 // Tiles as they are in the pool wait in a ring of half runs (a run's keys or values).
 constexpr int kTileRing = 3;
 template <int D>
 constexpr uint32_t kHalfRun = kChunkKeys / kBlock * kv4_tile_bytes(D);
-constexpr int kRegsSoft = 88, kRegsWiden = 72, kRegsRest = 56;
 template <bool KV4>
-constexpr int kThreads = (KV4 ? kSoftWarps + kWidenWarps + 4 : kSoftWarps + 3) * 32;
+constexpr int kThreads = (KV4 ? kSoftWarps + kWidenWarps + 2 : kSoftWarps + 3) * 32;
 template <bool KV4>
 constexpr int kMmaWarp = KV4 ? kSoftWarps + kWidenWarps : kSoftWarps + 1;
 constexpr int kTmemCols = 512;
@@ -249,9 +247,9 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, fals
 // a warp for the 32 rows of its number in each half.  (Loaded from global memory instead,
 // the two passes made a tile's start several us longer.)
 template <int D>
-__device__ __forceinline__ void widen_queries(const ChunkParams& p, const Bars<D, true>& B,
-                                              unsigned char* smem, const ChunkSegment& s,
-                                              uint32_t nseg, int ww, int lane) {
+__device__ __forceinline__ void widen_queries(const ChunkParams& p, unsigned char* smem,
+                                              const ChunkSegment& s,
+                                              uint32_t nseg, int quad, int lane) {
   using L = Smem<D, true>;
   const int copies = copies_of(p, s), halves = copies == 0 ? 2 : 1;
   const int copy_rows = copies > 1 ? kChunkHalfRows / copies : kChunkHalfRows;
@@ -260,25 +258,27 @@ __device__ __forceinline__ void widen_queries(const ChunkParams& p, const Bars<D
     // rows that are there, of those of a copy or half
     const int there =
         min(s.t.n_tok - x * (p.tile_tokens / 2), copy_rows / p.group) * p.group;
-    unsigned char* rows = smem + L::kOffQ + x * L::kHalf + ww * 32 * 128 + lane * 16;
+    unsigned char* rows = smem + L::kOffQ + x * L::kHalf + quad * 32 * 128 + lane * 16;
     auto at = [&](int i) {  // four rows' 64 dimensions
       return reinterpret_cast<uint4*>(rows + (i >> 3) * (kChunkHalfRows * 128) + (i & 7) * 512);
     };
-    uint32_t top = 0;  // of the elements' magnitudes, as fp32
+    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);  // the largest magnitudes
 #pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
       const uint4 r = *at(i);
+      const int row = quad * 32 + 4 * (i & 7) + (lane >> 3);
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-      const int row = ww * 32 + 4 * (i & 7) + (lane >> 3);
-      if ((row & (copy_rows - 1)) >= there) continue;
+      if ((row & (copy_rows - 1)) < there) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+        for (int e = 0; e < 4; ++e)
+          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+      }
     }
-    const int e = min(126, 14 + 127 - (int)(__reduce_max_sync(kFull, top) >> 23));
+    const uint32_t most = __float_as_uint(fmaxf(__low2float(top), __high2float(top)));
+    const int e = min(126, 14 + 127 - (int)(__reduce_max_sync(kFull, most) >> 23));
     const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
     if (lane == 0)
-      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + 4 * x + ww] =
+      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + 4 * x + quad] =
           __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
@@ -291,9 +291,6 @@ __device__ __forceinline__ void widen_queries(const ChunkParams& p, const Bars<D
       *at(i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(B.qfull());
 }
 
 // The query rows, and the tiles of a run's keys, then of its values, by one warp: tiles into
@@ -349,8 +346,8 @@ __device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, const Bars<D, 
   return true;
 }
 
-// Keys and values: a warp takes two blocks of a half run, 8 tokens at a time, a lane a
-// quarter of one of them.  They go where the bulk copies of a bf16 cache would have put
+// Keys and values: a warp takes half of the blocks of a half run, 8 tokens at a time, a lane
+// a quarter of one of them.  They go where the bulk copies of a bf16 cache would have put
 // them, in the same swizzle; at head_dim 128 a token's upper two quarters are taken in
 // another order, so that the 8 lanes that write together do so to different banks.  Tokens
 // that are not there become zeros.
@@ -370,7 +367,12 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
     if (!warp_wait(smem0 + L::kOffRows, nseg & 1)) return false;
-    widen_queries<D>(p, B, smem, s, nseg, ww, lane);
+#pragma unroll 1
+    for (int quad = ww; quad < 4; quad += kWidenWarps)
+      widen_queries<D>(p, smem, s, nseg, quad, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.qfull());
     ++nseg;
 #pragma unroll 1
     for (int h = 2 * s.j0; h < 2 * s.j1; ++h, ++i) {
@@ -1014,7 +1016,6 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
   if (odd) {
     // nothing runs; the end below flags it
   } else if (warp < kSoftWarps) {
-    if (KV4) reg_inc<kRegsSoft>();
     volatile PairWords* words = s_pairs + (warp >> 3) * 4 + (warp & 3);
     const int end = softmax<D, CAP, BIAS, KV4>(p, B, smem, s_meta, s_todo, s_done, words, wk, warp,
                                           lane);
@@ -1029,7 +1030,6 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
     ok = end == kDone;
   } else if (KV4 && warp < kSoftWarps + kWidenWarps) {
     if constexpr (KV4) {
-      reg_dec<kRegsWiden>();
       ok = widen<D>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
     }
   } else if (!KV4 && warp == kSoftWarps) {
@@ -1042,7 +1042,6 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
     }
   } else {
-    if (KV4) reg_dec<kRegsRest>();
     if (warp == kMmaWarp<KV4>) {
       if (elect_one()) {
         ok = issue_mma<D, KV4>(p, B, smem0, wk);
@@ -1051,9 +1050,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
         (void)mbar_wait(B.drained(), 0);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp<KV4> + 1) {
-      ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
-    } else if (warp == kMmaWarp<KV4> + 2) {
+    } else {
       if constexpr (KV4) {
         uint32_t issued = 0, nq = 0;
         ok = fetch_tiles<D>(p, B, smem0, s_meta, s_done, wk, lane, issued, nq);
@@ -1062,6 +1059,8 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
         for (uint32_t k = issued > kTileRing ? issued - kTileRing : 0; k < issued; ++k)
           (void)mbar_wait(smem0 + L::kOffTileBars + 8 * (k % kTileRing), (k / kTileRing) & 1);
       }
+      if (ok)
+        ok = chunk_publish<kChunkKeys>(p, B.piece(0), B.piece(1), B.published(), s_todo, wk, lane);
     }
   }
   if (!ok && lane == 0) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
