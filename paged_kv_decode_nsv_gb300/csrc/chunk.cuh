@@ -110,6 +110,7 @@ struct ChunkParams {
   const uint8_t* v4;
   const float* k_units;
   const float* v_units;
+  const float* q_up;  // [tokens][heads]: what the converted query vectors are scaled down by
   // bf16 only; tmap_q: boxes of 128, 64 and 32 MMA rows
   CUtensorMap tmap_q[3], tmap_k, tmap_v;
   const void* q;
@@ -152,8 +153,17 @@ bool chunk_encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int
 
 // Launchers.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
-// The tile lists of two kernels that share a batch, in one launch.
-cudaError_t launch_chunk_plans(const ChunkParams& a, const ChunkParams& b, cudaStream_t stream);
+// The tile lists of two kernels that share a batch (a: null for one alone), and b's query
+// vectors converted to fp16 on the way, in one launch.
+struct ChunkQueries {
+  const void* q;  // bf16 [vectors][head_dim]
+  void* half;     // the same, each scaled by a power of two so that its largest element
+                  // lies in [2^14, 2^15)
+  float* up;      // [vectors] the inverse powers
+  long long vectors;
+};
+cudaError_t launch_chunk_plans(const ChunkParams* a, const ChunkParams& b, const ChunkQueries& q,
+                               int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream);
 // The same over a 4-bit cache (k4, v4).
 cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream);

@@ -101,12 +101,9 @@ struct Smem {
   static constexpr uint32_t kOffPairs = kOffMeta + kMetaRing * 4;  // PairWords [8]
   static constexpr uint32_t kOffWord = kOffPairs + 8 * 20;  // the TMEM address, then kOffDone
   static constexpr uint32_t kOffDone = kOffWord + 4;        // softmax warps done, over all tiles
-  // A 4-bit cache: what brings scores to their size, float [4][8], a segment in turn.
-  static constexpr uint32_t kOffUp = kOffWord + 16;
-  static constexpr uint32_t kOffTiles = (kOffUp + 128 + 127) / 128 * 128;
+  static constexpr uint32_t kOffTiles = (kOffWord + 16 + 127) / 128 * 128;
   static constexpr uint32_t kOffTileBars = kOffTiles + kTileRing * kHalfRun<D>;  // full, free
-  static constexpr uint32_t kOffRows = kOffTileBars + 2 * kTileRing * 8;  // query rows are there
-  static constexpr uint32_t kTotal = KV4 ? kOffRows + 8 : kOffWord + 16;
+  static constexpr uint32_t kTotal = KV4 ? kOffTileBars + 2 * kTileRing * 8 : kOffWord + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
@@ -152,10 +149,10 @@ __device__ __forceinline__ int copies_of(const ChunkParams& p, const ChunkSegmen
 }
 
 // ------------------------------------------------------------------ producer
-// A segment's query rows, onto the barrier `full`.
+// A segment's query rows.
 template <int D, bool KV4>
 __device__ __forceinline__ bool load_queries(const ChunkParams& p, const Bars<D, KV4>& B,
-                                             uint32_t full, uint32_t smem0,
+                                             uint32_t smem0,
                                              const volatile uint32_t* s_done,
                                              const ChunkSegment& s, int lane, uint32_t nseg,
                                              uint32_t& shared) {
@@ -175,14 +172,14 @@ __device__ __forceinline__ bool load_queries(const ChunkParams& p, const Bars<D,
     const int box_rows = copies == 0 ? kChunkHalfRows : kChunkHalfRows / copies;
     const int box_tok = box_rows / p.group;
     const CUtensorMap* map = &p.tmap_q[copies == 4 ? 2 : copies == 2 ? 1 : 0];
-    mbar_arrive_tx(full, (uint32_t)(boxes * box_tok * p.group * D * 2));
+    mbar_arrive_tx(B.qfull(), (uint32_t)(boxes * box_tok * p.group * D * 2));
 #pragma unroll 1
     for (int x = 0; x < boxes; ++x)
       for (int d = 0; d < D / 64; ++d)
         tma_load_3d(smem0 + L::kOffQ + (copies == 0 ? x * L::kHalf : x * box_rows * 128) +
                         d * (kChunkHalfRows * 128),
                     map, d * 64, s.head * p.group, s.t.q0 + (copies == 0 ? x * half_tok : 0),
-                    full);
+                    B.qfull());
   }
   return true;
 }
@@ -198,8 +195,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, fals
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
-    if (!load_queries<D, false>(p, B, B.qfull(), smem0, s_done, s, lane, nseg, shared))
-      return false;
+    if (!load_queries<D, false>(p, B, smem0, s_done, s, lane, nseg, shared)) return false;
     ++nseg;
     const int32_t* table = p.block_tables + (size_t)s.t.row * p.max_blocks;
     auto block_id = [&](int j) -> int {  // lane's block of run j, -1 past the tile's keys
@@ -239,59 +235,8 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, fals
 // --------------------------------------------------------------------- widening
 // Over a 4-bit cache operands are fp16: its numbers times their scales are exact, and a
 // pair of them takes 11 instructions a word of 8 (bf16, which has no conversion from
-// e2m1, 23).  Four warps fill the stages, and the query rows.
-//
-// Query rows: 32 rows (a softmax warp's) are scaled by one power of two, so that the
-// largest element lies in [2^14, 2^15): exact but for elements below 2^-28 of it, off by
-// 2^-40 of it at most.  They arrive as bulk copies bring them and are converted in place, by
-// a warp for the 32 rows of its number in each half.  (Loaded from global memory instead,
-// the two passes made a tile's start several us longer.)
-template <int D>
-__device__ __forceinline__ void widen_queries(const ChunkParams& p, unsigned char* smem,
-                                              const ChunkSegment& s,
-                                              uint32_t nseg, int quad, int lane) {
-  using L = Smem<D, true>;
-  const int copies = copies_of(p, s), halves = copies == 0 ? 2 : 1;
-  const int copy_rows = copies > 1 ? kChunkHalfRows / copies : kChunkHalfRows;
-#pragma unroll 1
-  for (int x = 0; x < halves; ++x) {
-    // rows that are there, of those of a copy or half
-    const int there =
-        min(s.t.n_tok - x * (p.tile_tokens / 2), copy_rows / p.group) * p.group;
-    unsigned char* rows = smem + L::kOffQ + x * L::kHalf + quad * 32 * 128 + lane * 16;
-    auto at = [&](int i) {  // four rows' 64 dimensions
-      return reinterpret_cast<uint4*>(rows + (i >> 3) * (kChunkHalfRows * 128) + (i & 7) * 512);
-    };
-    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);  // the largest magnitudes
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 r = *at(i);
-      const int row = quad * 32 + 4 * (i & 7) + (lane >> 3);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-      if ((row & (copy_rows - 1)) < there) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
-      }
-    }
-    const uint32_t most = __float_as_uint(fmaxf(__low2float(top), __high2float(top)));
-    const int e = min(126, 14 + 127 - (int)(__reduce_max_sync(kFull, most) >> 23));
-    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-    if (lane == 0)
-      reinterpret_cast<volatile float*>(smem + L::kOffUp)[(nseg & 3) * 8 + 4 * x + quad] =
-          __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 r = *at(i);
-      uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = pack_half(__uint_as_float(w[k] << 16) * mul,
-                         __uint_as_float(w[k] & 0xffff0000u) * mul);
-      *at(i) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-}
+// e2m1, 23).  The query rows have been scaled and converted when the tiles were listed
+// (chunk_plan.cu; two of this kernel's warps took 7 us a tile for it).
 
 // The query rows, and the tiles of a run's keys, then of its values, by one warp: tiles into
 // a ring of half runs, a lane copies a block.
@@ -312,8 +257,7 @@ __device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, const Bars<D, 
       return lane < kChunkKeys / kBlock && (long long)b * kBlock < s.t.ke ? __ldg(table + b) : -1;
     };
     int id = block_id(s.j0);
-    if (!load_queries<D, true>(p, B, smem0 + L::kOffRows, smem0, s_done, s, lane, nseg, shared))
-      return false;
+    if (!load_queries<D, true>(p, B, smem0, s_done, s, lane, nseg, shared)) return false;
     ++nseg;
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
@@ -361,19 +305,11 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
   constexpr int kEights = kChunkKeys / 8 / kWidenWarps;  // of tokens a half run
   const int row = lane >> 2, part = lane & 3;
   const uint32_t smem0 = smem_u32(smem);
-  uint32_t i = 0, run = 0, nseg = 0;
+  uint32_t i = 0, run = 0;
   uint32_t out = 0, parity = 0;  // the ring slot to read, and its turn
   ChunkSegment s;
 #pragma unroll 1
   while (wk.next<kChunkKeys>(p, s)) {
-    if (!warp_wait(smem0 + L::kOffRows, nseg & 1)) return false;
-#pragma unroll 1
-    for (int quad = ww; quad < 4; quad += kWidenWarps)
-      widen_queries<D>(p, smem, s, nseg, quad, lane);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(B.qfull());
-    ++nseg;
 #pragma unroll 1
     for (int h = 2 * s.j0; h < 2 * s.j1; ++h, ++i) {
       const uint32_t full = smem0 + L::kOffTileBars + 8 * out;
@@ -729,7 +665,6 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
   const uint32_t t_o = lane_base + kColO;
   const int half_tok = p.tile_tokens / 2;
   float2* s_ml = reinterpret_cast<float2*>(smem + L::kOffMl);
-  const volatile float* s_up = reinterpret_cast<const volatile float*>(smem + L::kOffUp);
   float* s_x = reinterpret_cast<float*>(smem + L::kOffX + (x * 2 + hf) * L::kQuarterX);
   uint32_t nscore = 0, nseg = 0, njoin = 0, nmeet = 0, run0 = 0, turn = 0;
   // the four warps with this stream and half meet
@@ -771,7 +706,10 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
     f.l = 0.f;
     const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
-    const float k_unit = KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f;
+    // what brings a 4-bit cache's scores to their size
+    float unit = KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f;
+    if (KV4 && valid)
+      unit *= __ldg(p.q_up + ((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g);
     // the states' exchange is free: every warp has read the previous tile's
     if (nseg && !warp_wait(B.mlfree(), (nseg - 1) & 1)) return kTimedOut;
 #pragma unroll 1
@@ -781,8 +719,6 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
       if (!warp_wait(B.scores(x), nscore++ & 1)) return kTimedOut;
       tc_fence_after();
       const int mask = s_meta[run % kMetaRing];
-      const float unit =
-          KV4 ? k_unit * s_up[(nseg & 3) * 8 + (pair ? x * 4 : 0) + (warp & 3)] : 1.f;
       // Values of positions that hold nothing (past the context, or in a
       // block that was not loaded) become zeros: their probability is 0, but
       // 0 * NaN is not.
@@ -975,10 +911,9 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
     if (lane == 0) {
       for (int i = 0; i < 2 * L::kStages + 2; ++i)
         mbar_init(smem0 + L::kOffBars + 8 * i,
-                  KV4 && (i < L::kStages || i == 2 * L::kStages) ? kWidenWarps : 1);
+                  KV4 && i < L::kStages ? kWidenWarps : 1);
       for (int i = 0; KV4 && i < 2 * kTileRing; ++i)
         mbar_init(smem0 + L::kOffTileBars + 8 * i, i < kTileRing ? 1 : kWidenWarps);
-      if (KV4) mbar_init(smem0 + L::kOffRows, 1);
       mbar_init(B.drained(), 1);
       for (int x = 0; x < 2; ++x) {
         mbar_init(B.scores(x), 1);
@@ -1054,7 +989,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
       if constexpr (KV4) {
         uint32_t issued = 0, nq = 0;
         ok = fetch_tiles<D>(p, B, smem0, s_meta, s_done, wk, lane, issued, nq);
-        if (nq) (void)mbar_wait(smem0 + L::kOffRows, (nq - 1) & 1);
+        if (nq) (void)mbar_wait(B.qfull(), (nq - 1) & 1);
         // every copy issued lands before the CTA can end, even after a timeout
         for (uint32_t k = issued > kTileRing ? issued - kTileRing : 0; k < issued; ++k)
           (void)mbar_wait(smem0 + L::kOffTileBars + 8 * (k % kTileRing), (k / kTileRing) & 1);

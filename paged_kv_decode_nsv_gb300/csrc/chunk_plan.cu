@@ -200,19 +200,58 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   plan(p);
 }
 
-// One CTA for each list.
+// Query vectors to fp16, scaled by a power of two each: exact but for elements below 2^-28
+// of a vector's largest, which are off by 2^-40 of it at most.  A lane holds 8 dimensions.
+template <int D>
+__device__ __forceinline__ void convert_queries(const ChunkQueries& c, int cta, int ctas) {
+  constexpr int kLanes = D / 8, kVecs = 32 / kLanes;  // lanes of a vector; vectors of a warp
+  const int lane = threadIdx.x & 31;
+  const long long step = (long long)ctas * (kPlanThreads / 32) * kVecs;
+  const long long first = ((long long)cta * (kPlanThreads / 32) + (threadIdx.x >> 5)) * kVecs;
+  for (long long v0 = first; v0 < c.vectors; v0 += step) {
+    const long long v = v0 + lane / kLanes;
+    const size_t at = (size_t)min(v, c.vectors - 1) * kLanes + lane % kLanes;
+    const uint4 r = __ldg(static_cast<const uint4*>(c.q) + at);
+    uint32_t w[4] = {r.x, r.y, r.z, r.w}, top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(sm::kFull, top, o));
+    const int e = min(126, 14 + 127 - (int)(top >> 23));
+    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = sm::pack_half(__uint_as_float(w[i] << 16) * mul,
+                           __uint_as_float(w[i] & 0xffff0000u) * mul);
+    if (v >= c.vectors) continue;
+    static_cast<uint4*>(c.half)[at] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane % kLanes == 0) c.up[v] = __uint_as_float((uint32_t)(127 - e) << 23);
+  }
+}
+
+// A CTA for each list (`both`: or for the second alone), the others for the query vectors.
+template <int D>
 __global__ void __launch_bounds__(kPlanThreads)
-    chunk_plans_kernel(const __grid_constant__ ChunkParams a, const __grid_constant__ ChunkParams b) {
+    chunk_plans_kernel(const __grid_constant__ ChunkParams a, const __grid_constant__ ChunkParams b,
+                       const __grid_constant__ ChunkQueries q, bool both) {
   sm::griddep_wait();
   sm::griddep_launch();
-  plan(blockIdx.x ? b : a);
+  if (blockIdx.x > 1) {
+    convert_queries<D>(q, blockIdx.x - 2, gridDim.x - 2);
+  } else if (blockIdx.x == 1 || both) {
+    plan(blockIdx.x ? b : a);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_plans(const ChunkParams& a, const ChunkParams& b, cudaStream_t stream) {
+cudaError_t launch_chunk_plans(const ChunkParams* a, const ChunkParams& b, const ChunkQueries& q,
+                               int head_dim, int num_sms, cudaStream_t stream) {
+  // (a CTA takes 64 vectors a turn at head_dim 128)
+  const long long ctas = (q.vectors + 63) / 64;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
+  cfg.gridDim = dim3((unsigned)(2 + (ctas < num_sms ? ctas : num_sms)));
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -220,7 +259,10 @@ cudaError_t launch_chunk_plans(const ChunkParams& a, const ChunkParams& b, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_plans_kernel, a, b);
+  const ChunkParams& first = a ? *a : b;
+  return head_dim == 64
+             ? cudaLaunchKernelEx(&cfg, chunk_plans_kernel<64>, first, b, q, a != nullptr)
+             : cudaLaunchKernelEx(&cfg, chunk_plans_kernel<128>, first, b, q, a != nullptr);
 }
 
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {

@@ -167,8 +167,13 @@ ChunkWs tile_ws(const nsv_shape* s, int64_t tokens, int num_sms) {
                        s->head_dim, s->dtype, num_sms);
 }
 
-// The vector form's workspace, then the other form's.  A larger batch's serves a smaller
-// one, whichever form that takes.
+// The converted query vectors and their powers of two.
+uint64_t queries_bytes(const nsv_shape* s, int64_t tokens) {
+  return ((uint64_t)tokens * s->num_heads * (s->head_dim * 2 + 4) + 255) / 256 * 256;
+}
+
+// The vector form's workspace, then the other form's, then the query vectors it converts.
+// A larger batch's serves a smaller one, whichever form that takes.
 uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
   nsv_shape any = *s;
   any.query_len = 0;
@@ -180,7 +185,8 @@ uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
                      vec_ws(&one, vec_form(&one, ct, num_sms), tokens).total});
   }
   if (s->dtype == NSV_F32) return most;
-  return (most + 255) / 256 * 256 + tile_ws(s, tokens, num_sms).total;
+  return (most + 255) / 256 * 256 + (tile_ws(s, tokens, num_sms).total + 255) / 256 * 256 +
+         queries_bytes(s, tokens);
 }
 
 // What both forms' plans and kernels share of a call.
@@ -248,7 +254,8 @@ void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4Vec
   p->subs = f.subs;
 }
 
-bool tile_params(const Call& a, const ChunkWs& W, char* b, ChunkParams* c) {
+bool tile_params(const Call& a, const ChunkWs& W, char* b, const ChunkQueries& q,
+                 ChunkParams* c) {
   const nsv_shape* s = a.s;
   common_params(a, c);
   c->ws_head = reinterpret_cast<long long*>(b);
@@ -271,9 +278,10 @@ bool tile_params(const Call& a, const ChunkWs& W, char* b, ChunkParams* c) {
   c->pair_units = kChunkPairUnits;
   c->half_units = kChunkHalfUnits;
   c->ws_first = reinterpret_cast<long long*>(c->ws_cta + c->grid);
-  return chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows, a.q, &c->tmap_q[0]) &&
-         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 2, a.q, &c->tmap_q[1]) &&
-         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 4, a.q, &c->tmap_q[2]);
+  c->q_up = q.up;
+  return chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows, q.half, &c->tmap_q[0]) &&
+         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 2, q.half, &c->tmap_q[1]) &&
+         chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 4, q.half, &c->tmap_q[2]);
 }
 
 }  // namespace
@@ -393,9 +401,15 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
   const bool vec = vec_tokens(s) > 0, tiles = std::min(most, tokens) > vec_tokens(s);
   ChunkParams c;
   memset(&c, 0, sizeof c);
+  ChunkQueries conv{};
   if (tiles) {
     const ChunkWs T = tile_ws(s, tokens, d.num_sms);
-    if (!tile_params(call, T, static_cast<char*>(ws) + ws_need - T.total, &c)) return cuda_fail();
+    char* end = static_cast<char*>(ws) + ws_need - queries_bytes(s, tokens);
+    conv.q = q;
+    conv.half = end;
+    conv.vectors = tokens * s->num_heads;
+    conv.up = reinterpret_cast<float*>(end + conv.vectors * s->head_dim * 2);
+    if (!tile_params(call, T, end - (T.total + 255) / 256 * 256, conv, &c)) return cuda_fail();
     c.k4 = p.k_pool;
     c.v4 = p.v_pool;
     c.k_units = k_scales;
@@ -413,9 +427,9 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
     if ((int64_t)s->rows * n <= kVecOwnTiles) p.row_tiles = n;
   }
   cudaError_t e = p.row_tiles ? cudaSuccess
-                  : !vec      ? launch_chunk_plan(c, stream)
                   : !tiles    ? launch_chunk_plan(p.c, stream)
-                              : launch_chunk_plans(p.c, c, stream);
+                              : launch_chunk_plans(vec ? &p.c : nullptr, c, conv, s->head_dim,
+                                                   d.num_sms, stream);
   if (e == cudaSuccess && tiles) e = launch_chunk_kv4(c, s->head_dim, stream);
   if (e == cudaSuccess && vec)
     e = launch_kv4_vec(p, s->dtype, s->head_dim, f.col_tiles, stream);
