@@ -292,9 +292,10 @@ __device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, const Bars<D, 
 
 // Keys and values: a warp takes half of the blocks of a half run, 8 tokens at a time, a lane
 // a quarter of one of them.  They go where the bulk copies of a bf16 cache would have put
-// them, in the same swizzle; at head_dim 128 a token's upper two quarters are taken in
-// another order, so that the 8 lanes that write together do so to different banks.  Tokens
-// that are not there become zeros.
+// them, in the same swizzle.  (At head_dim 128 two of the 8 lanes that write together meet in
+// each bank; words taken in another order, which avoids that, cost more than the meeting:
+// what these warps issue, the softmax beside them waits for.)  Tokens that are not there
+// become zeros.
 template <int D>
 __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>& B,
                                       unsigned char* smem, const volatile int* s_meta,
@@ -303,6 +304,7 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
   constexpr uint32_t kTile = kv4_tile_bytes(D);
   constexpr int kWords = D / 32;                         // words of a lane's quarter
   constexpr int kEights = kChunkKeys / 8 / kWidenWarps;  // of tokens a half run
+  constexpr int kThere = (1 << (kEights / 2)) - 1;       // all of the warp's blocks
   const int row = lane >> 2, part = lane & 3;
   const uint32_t smem0 = smem_u32(smem);
   uint32_t i = 0, run = 0;
@@ -336,20 +338,22 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
           sc[q] = t[8 * D + off * 4 + part];
         }
       }
+      if (left < 8 * kEights || (mask & kThere) != kThere) {
+#pragma unroll
+        for (int q = 0; q < kEights; ++q)
+          if (8 * q + row >= left || !((mask >> (q >> 1)) & 1)) sc[q] = 0;
+      }
 #pragma unroll
       for (int q = 0; q < kEights; ++q) {
-        if (8 * q + row >= left || !((mask >> (q >> 1)) & 1)) sc[q] = 0;
         const uint32_t e = e4m3x2_to_half(sc[q]);
-        const bool swap = D == 128 && (part & 2);
 #pragma unroll
         for (int k = 0; k < kWords; ++k) {
-          const uint32_t x = swap ? w[q][k ^ 2 % kWords] : w[q][k];
-          const uint32_t s2 = __byte_perm(e, 0, (k >= 2) != swap ? 0x3232 : 0x1010);
+          const uint32_t s2 = __byte_perm(e, 0, k >= 2 ? 0x3232 : 0x1010);
           uint32_t g[4];
-          e2m1x8_to_half(x, g);
+          e2m1x8_to_half(w[q][k], g);
 #pragma unroll
           for (int n = 0; n < 4; ++n) g[n] = hmul2(g[n], s2);
-          const int chunk = part * kWords + (swap ? k ^ 2 : k);  // 8 dimensions
+          const int chunk = part * kWords + k;  // 8 dimensions
           *reinterpret_cast<uint4*>(stage + (q * (D / 64) + (chunk >> 3)) * 1024 +
                                     (((chunk & 7) ^ row) << 4)) = make_uint4(g[0], g[1], g[2], g[3]);
         }

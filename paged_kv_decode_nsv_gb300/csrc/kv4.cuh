@@ -107,17 +107,20 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half(uint32_t x) {
       : "r"(x));
   return h;
 }
-// To nearest even, saturating: e4m3 of one value; e2m1 of two, the first in the low half.
+// To nearest even, saturating: e4m3 of one value; e2m1 of eight, the first lowest.
 __device__ __forceinline__ uint32_t to_e4m3(float x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
   return r & 0xffu;
 }
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

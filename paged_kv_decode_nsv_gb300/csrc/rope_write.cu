@@ -24,7 +24,7 @@
 namespace nsv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 constexpr int kPasses = 2;  // heads of a lane whose loads go out together
 
 // 16 bytes of elements as fp32, and back.
@@ -189,10 +189,10 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
 
 // 8 dimensions as numbers of scale s, whose reciprocal is r.
 __device__ __forceinline__ uint32_t numbers8(const float* y, float s, float r) {
-  uint32_t w = 0;
+  float z[8];
 #pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    w |= to_e2m1x2(quotient(y[i], s, r), quotient(y[i + 1], s, r)) << (4 * i);
+  for (int i = 0; i < 8; ++i) z[i] = quotient(y[i], s, r);
+  const uint32_t w = to_e2m1x8(z);
   return s == 0.f ? 0u : w;
 }
 
@@ -203,7 +203,7 @@ __device__ __forceinline__ uint32_t numbers8(const float* y, float s, float r) {
 // their values read back, 17 us): 8 dimensions a lane, partners by shuffles 44 and 105 us;
 // a thread with four whole heads' pairs, 111 to 147 registers, 43 and 127.
 template <typename T, int D, bool FOUR>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 16 : 10)
     append_kernel(const RopeParams p, int q_units, int kv_units) {
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes of a head; heads of a pass
@@ -280,20 +280,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5)
     x[j][0].get(a);
     x[j][1].get(b);
     if (real) t.apply(p, src + (size_t)h * D, row, a, b);
-    if (units_of) {
-      const float d = real ? __ldg(units_of + h) : 1.f, r = __frcp_rn(d);
-      const float most = 4096.f * d;  // beyond 2688 all quotients end the same
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = quotient(fminf(fmaxf(a[i], -most), most), d, r);
-        b[i] = quotient(fminf(fmaxf(b[i], -most), most), d, r);
-      }
-    }
     float top_a = 0.f, top_b = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       top_a = fmaxf(top_a, fabsf(a[i]));
       top_b = fmaxf(top_b, fabsf(b[i]));
+    }
+    if (units_of) {
+      const float d = real ? __ldg(units_of + h) : 1.f, r = __frcp_rn(d);
+      const float most = 4096.f * d;  // beyond 2688 all quotients end the same
+      if (__any_sync(sm::kFull, fmaxf(top_a, top_b) > most)) {
+        top_a = fminf(top_a, most);
+        top_b = fminf(top_b, most);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = fminf(fmaxf(a[i], -most), most);
+          b[i] = fminf(fmaxf(b[i], -most), most);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = quotient(a[i], d, r);
+        b[i] = quotient(b[i], d, r);
+      }
+      // (rounding keeps the order: the largest quotient is the largest's)
+      top_a = quotient(top_a, d, r);
+      top_b = quotient(top_b, d, r);
     }
     // a scale's 16 dimensions: the lane's own, or 8 of its neighbour's
     const float next_a = __shfl_xor_sync(sm::kFull, top_a, 1);
