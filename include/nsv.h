@@ -555,7 +555,7 @@ typedef struct nsv_rope {
  *
  * Results are rounded once to the element type.  Uses num_heads, num_kv_heads, head_dim,
  * block_size, num_blocks and dtype of the shape (the rest must be valid).  0 <= tokens <
- * 2^30, tokens * (num_heads + 2 num_kv_heads) < 2^34.  Asynchronous, without workspace; may
+ * 2^30, tokens * (num_heads + 2 num_kv_heads) < 2^33.  Asynchronous, without workspace; may
  * be captured.
  */
 NSV_API int nsv_rope_write(const nsv_shape *shape, const nsv_rope *rope, int64_t tokens,
@@ -604,10 +604,11 @@ NSV_API int nsv_kv4_read(const nsv_shape *shape, const float *k_scales, const fl
  * than query_len (1 for a decode step), and the call takes the form that suits it; a
  * row that brings more sets NSV_DEV_BAD_CHUNK and is read as having none.
  *
- * The pools' numbers times their scales are multiplied exactly.  bf16: weights are
- * rounded to fp16 or bf16 for the product with the values, their sum is not: up to 2^-8
- * of sum p |v| besides the output's own rounding.  fp32: queries and weights are off by
- * 2^-22 of themselves, products are added in fp32.
+ * The pools' numbers times their scales are multiplied exactly, sums are fp32.  bf16:
+ * elements of a query vector below 2^-28 of its largest may be dropped, and weights are
+ * rounded to fp16 for the product with the values, while their sum is not: up to 2^-11 of
+ * sum p |v| besides the output's own rounding (2^-8).  fp32: queries and weights are
+ * off by 2^-22 of themselves.
  *
  * workspace: as in nsv_paged_chunk, of the bytes that nsv_kv4_workspace gives (for any
  * query_len).

@@ -167,6 +167,7 @@ cudaError_t launch_chunk_plans(const ChunkParams* a, const ChunkParams& b, const
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream);
 // The same over a 4-bit cache (k4, v4).
 cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_kv4_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t prepare_chunk_bf16();
 cudaError_t prepare_chunk_f32();

@@ -46,8 +46,14 @@
 // when the accumulator kept the sums).  The same split on mma.sync (64 rows, two CTAs per
 // SM), where every warp splits the keys and values again, took 162, and multiply-adds on
 // the CUDA cores 207.
+//
+// Over a 4-bit cache (KV4): a loader's registers hold four numbers and their scale, whose
+// products are exact in tf32, so that keys and values have no lower parts: two products
+// instead of three, and buffers of two runs.  The heads' scales go to the scores' scale and
+// to the outputs' last factor.
 
 #include "chunk.cuh"
+#include "kv4.cuh"
 
 namespace nsv {
 namespace {
@@ -75,18 +81,20 @@ constexpr int kMetaRing = 8;
 // units): probabilities stay <= 2^8, and most runs skip the rescale.
 constexpr float kSlack = 8.f;
 
-template <int D>
+// (What a 4-bit cache holds is exact in tf32 and has no lower parts.)
+template <int D, bool KV4>
 struct Smem {
   static constexpr uint32_t kQ = kR * D * 4;  // upper parts of the query rows
   static constexpr uint32_t kKV = kC * D * 4;  // upper or lower parts of a run's keys or values
+  static constexpr uint32_t kRun = (KV4 ? 1 : 2) * kKV;
   // runs that the keys' and the values' buffers hold
-  static constexpr uint32_t kStages = D == 64 ? 2 : 1;
+  static constexpr uint32_t kStages = D == 64 || KV4 ? 2 : 1;
   static constexpr uint32_t kOffK = kQ;
-  static constexpr uint32_t kOffV = kOffK + kStages * 2 * kKV;
+  static constexpr uint32_t kOffV = kOffK + kStages * kRun;
   // Of a loader's 16 or 8 chunks of a run, on their way those it has no registers for
   // wait here: [loaders][chunks][128 threads] of 16 bytes.
-  static constexpr int kHeld = D == 64 ? 0 : 8;
-  static constexpr uint32_t kOffHeld = kOffV + kStages * 2 * kKV;
+  static constexpr int kHeld = D == 64 || KV4 ? 0 : 8;
+  static constexpr uint32_t kOffHeld = kOffV + kStages * kRun;
   static constexpr uint32_t kOffMax = kOffHeld + kHeld * kLoadWarps * 32 * 16;  // float2 [128]
   static constexpr uint32_t kOffSum = kOffMax + kR * 8;   // float [2][128]
   static constexpr uint32_t kOffTodo = kOffSum + kR * 8;  // int4 [2][2]: tiles to merge
@@ -153,10 +161,10 @@ __device__ __forceinline__ uint32_t operand_at(int rows, int r, int v) {
 // Four warps load the keys (KEYS) and four the values, each for itself, so that the
 // keys of a run are stored during products and its values during scores.  (Eight warps
 // for both in turn: 5.7 us a run instead of 3.7.)
-template <int D, bool KEYS>
+template <int D, bool KEYS, bool KV4>
 __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsigned char* smem,
                                      volatile int* s_meta, ChunkWalk wk, int warp, int lane) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   constexpr int kV = D / 4;                   // 16-byte chunks of a key
   constexpr int kT = kLoadWarps * 32 / 2;     // threads that share a run
   constexpr int kN = kC * kV / kT;            // a thread's chunks of a run: 16 or 8
@@ -165,6 +173,8 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
   constexpr int kHeld = L::kHeld;
   const int tid = (warp & 3) * 32 + lane;
   const int v = tid & (kV - 1), t1 = tid / kV;  // its chunk, and its first key or quad
+  constexpr int kQueries = 8;                 // chunks of a query row at a time
+  static_assert(KV4 || kN - kHeld == kQueries, "the registers of a run's chunks");
   const float* pool = static_cast<const float*>(KEYS ? p.k_pool : p.v_pool);
   uint32_t run = 0, nseg = 0;
   ChunkSegment s;
@@ -180,7 +190,8 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     auto block_ids = [&](int j) {
       return wanted(j) ? __ldg(table + (s.t.kb + j * kC) / kBlock + lane) : -1;
     };
-    float4 x[kN - kHeld];  // chunks kHeld and on
+    float4 x[kQueries];       // of a query row; of a run, chunks kHeld and on
+    uint32_t raw[KV4 ? kN : 1];  // a 4-bit cache: four numbers, and their scale above them
     unsigned char* held = smem + L::kOffHeld + ((KEYS ? 0 : kHeld) * kT + tid) * 16;
     // This thread's chunks i .. i + kSame - 1 of run j, on their way.  (One group of
     // copies for each part that is held, whether it has any or not.)
@@ -189,6 +200,19 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       const int t = KEYS ? t1 + i * kStep : 4 * (t1 + (i >> 2) * kStep);
       const int id = __shfl_sync(kFull, ids, t / kBlock);
       const bool ok = id >= 0 && id < p.pool_blocks;
+      if constexpr (KV4) {
+        const uint8_t* tile = (KEYS ? p.k4 : p.v4) +
+                              ((size_t)(ok ? id : 0) * p.kv_heads + s.head) * kv4_tile_bytes(D);
+#pragma unroll
+        for (int u = 0; u < kSame; ++u) {
+          const int dt = KEYS ? u * kStep : u, off = t % kBlock + dt;
+          raw[i + u] = 0;
+          if (ok && t + dt < left)
+            raw[i + u] = __ldg(reinterpret_cast<const uint16_t*>(tile + off * (D / 2)) + v) |
+                         (uint32_t)__ldg(tile + 8 * D + off * (D / 16) + v / 4) << 16;
+        }
+        return;
+      }
       const float4* at = reinterpret_cast<const float4*>(
           pool + (((size_t)(ok ? id : 0) * p.kv_heads + s.head) * kBlock + t % kBlock) * D) + v;
 #pragma unroll
@@ -204,6 +228,16 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       }
     };
     auto chunk = [&](int i) {
+      if constexpr (KV4) {
+        uint32_t h[4];
+        e2m1x8_to_half(raw[i], h);  // (of which two are numbers)
+        const uint32_t e = __byte_perm(e4m3x2_to_half(raw[i] >> 16), 0, 0x1010);
+        h[0] = hmul2(h[0], e);
+        h[1] = hmul2(h[1], e);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+        return make_float4(a.x, a.y, b.x, b.y);
+      } else
       return i < kHeld ? *reinterpret_cast<const float4*>(held + i * kT * 16) : x[i - kHeld];
     };
     int ids = block_ids(s.j0), ids_next = block_ids(s.j0 + 1);
@@ -225,9 +259,9 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     static_assert(kN == kV / 2, "a thread's part of a query row");
     const uint32_t t_q = ((uint32_t)((warp & 3) * 32) << 16) + kColQ + half * (D / 2);
 #pragma unroll
-    for (int b = 0; b < kN; b += kN - kHeld) {
+    for (int b = 0; b < kN; b += kQueries) {
 #pragma unroll
-      for (int i = 0; i < kN - kHeld; ++i) {
+      for (int i = 0; i < kQueries; ++i) {
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (valid) x[i] = __ldg(q + b + i);
       }
@@ -237,7 +271,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kN - kHeld; i += 2) {
+      for (int i = 0; i < kQueries; i += 2) {
         float lo[8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -260,7 +294,7 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
     for (int j = s.j0; j < s.j1; ++j, ++run) {
       const int ids_after = block_ids(j + 2);
       const uint32_t st = run % L::kStages;
-      unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV) + st * 2 * L::kKV;
+      unsigned char* dst = smem + (KEYS ? L::kOffK : L::kOffV) + st * L::kRun;
       const uint32_t empty = KEYS ? B.kempty(st) : B.vempty(st);
       if (!warp_wait(empty, ((run / L::kStages) & 1) ^ 1)) return false;
       if (KEYS && warp == 0) {
@@ -278,9 +312,9 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 #pragma unroll
           for (int u = 0; u < kSame; ++u) {
             unsigned char* at = dst + operand_at(kC, t1 + (i + u) * kStep, v);
-            const float4 y = chunk(i + u), h = hi4(y);
+            const float4 y = chunk(i + u), h = KV4 ? y : hi4(y);
             *reinterpret_cast<float4*>(at) = h;
-            *reinterpret_cast<float4*>(at + L::kKV) = lo4(y, h);
+            if (!KV4) *reinterpret_cast<float4*>(at + L::kKV) = lo4(y, h);
           }
         } else {
           // 4 keys of dims 4 v .. 4 v + 3, rows v, v + D/4, ... of the operand
@@ -290,9 +324,9 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             unsigned char* at = dst + operand_at(D, e * kV + v, t1 + (i >> 2) * kStep);
-            const float4 h = hi4(y[e]);
+            const float4 h = KV4 ? y[e] : hi4(y[e]);
             *reinterpret_cast<float4*>(at) = h;
-            *reinterpret_cast<float4*>(at + L::kKV) = lo4(y[e], h);
+            if (!KV4) *reinterpret_cast<float4*>(at + L::kKV) = lo4(y[e], h);
           }
         }
         if (more) fetch(i, ids_next, j + 1);
@@ -309,10 +343,10 @@ __device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsign
 }
 
 // ------------------------------------------------------------------------ MMA
-template <int D>
+template <int D, bool KV4>
 __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, uint32_t smem0,
                                           ChunkWalk wk) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   constexpr uint32_t idesc_s = umma_idesc_tf32(kR, kC), idesc_o = umma_idesc_tf32(kR, D);
   // (descriptors are linear in the start address: lower parts follow the upper ones)
   const uint64_t dq = umma_desc128(smem0, 16, 1024);
@@ -329,12 +363,12 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
     if (!mbar_wait(B.kfull(st), (i / L::kStages) & 1)) return false;
     tc_fence_after();
     const uint32_t d = (i & 1) * 128;
-    const uint64_t dk = dk0 + st * 2 * kLow;
+    const uint64_t dk = dk0 + st * (L::kRun >> 4);
 #pragma unroll
     for (int ks = 0; ks < D / 8; ++ks)
       umma_ts_tf32(d, kColQ + ks * 8, dk + step(kC, ks), idesc_s, ks > 0);
 #pragma unroll
-    for (int ks = 0; ks < D / 8; ++ks)
+    for (int ks = 0; !KV4 && ks < D / 8; ++ks)
       umma_ss_tf32(d, dq + step(kR, ks), dk + kLow + step(kC, ks), idesc_s, true);
 #pragma unroll
     for (int ks = 0; ks < D / 8; ++ks)
@@ -345,7 +379,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
   };
   auto values = [&](uint32_t i) {
     const uint32_t st = i % L::kStages;
-    const uint64_t dv = dv0 + st * 2 * kLow;
+    const uint64_t dv = dv0 + st * (L::kRun >> 4);
     if (!mbar_wait(B.vfull(st), (i / L::kStages) & 1)) return false;
     if (!mbar_wait(B.probs(i & 1), (i >> 1) & 1)) return false;
     if (i && !mbar_wait(B.oread(), (i - 1) & 1)) return false;
@@ -355,7 +389,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
     for (int ks = 0; ks < kC / 8; ++ks)
       umma_ts_tf32(kColO, a + kC + ks * 8, dv + step(D, ks), idesc_o, ks > 0);
 #pragma unroll
-    for (int ks = 0; ks < kC / 8; ++ks)
+    for (int ks = 0; !KV4 && ks < kC / 8; ++ks)
       umma_ts_tf32(kColO, a + ks * 8, dv + kLow + step(D, ks), idesc_o, true);
 #pragma unroll
     for (int ks = 0; ks < kC / 8; ++ks)
@@ -384,12 +418,12 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
 }
 
 // -------------------------------------------------------------------- softmax
-template <int D, bool CAP>
+template <int D, bool CAP, bool KV4>
 __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsigned char* smem,
                                        const volatile int* s_meta, int4* s_todo,
                                        volatile PairWords* words, ChunkWalk wk, int warp,
                                        int lane) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   constexpr int kH = kC / 2;  // this thread's scores of a run
   constexpr float kLog2e = 1.4426950408889634f;
   const int hf = warp >> 2;                  // which of the pair
@@ -437,6 +471,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       if (lane == 0) mbar_arrive(B.oread());
       return true;
     };
+    const float scale = p.scale * (KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f);
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
       const uint32_t t_s = t_lane + (run & 1) * 128 + hf * kH;
@@ -445,7 +480,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       tc_fence_after();
       float alpha = 1.f;
       if (any_valid) {
-        float mul = p.scale;
+        float mul = scale;
         if (CAP) {
 #pragma unroll 1
           for (int c = 0; c < kH; c += 8) {
@@ -453,7 +488,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
             tmem_ld8(t_s + c, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = p.cap * tanhf(x[k] * p.scale / p.cap);
+            for (int k = 0; k < 8; ++k) x[k] = p.cap * tanhf(x[k] * scale / p.cap);
             tmem_st8(t_s + c, x);
           }
           tmem_wait_st();
@@ -546,7 +581,8 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       l += s_sum[(hf ^ 1) * kR];
       const int slot = chunk_slot(blockIdx.x, s.first);
       const int row = tok * p.group + g;  // within the tile
-      const float w = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const float w = (whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f) *
+                      (KV4 && p.v_units ? __ldg(p.v_units + s.head) : 1.f);
       float* out = chunk_out<float>(p, s.t.q0, s.head, row, D);
       if (valid) {
 #pragma unroll
@@ -565,10 +601,10 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
   return warp_wait(B.published(), 0) ? kDone : kTimedOut;
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool KV4>
 __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
     const __grid_constant__ ChunkParams p) {
-  using L = Smem<D>;
+  using L = Smem<D, KV4>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t smem0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -618,7 +654,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   } else if (warp < kSoftWarps) {
     reg_inc<Regs<D>::kSoft>();
     volatile PairWords* words = s_pairs + (warp & 3);
-    const int end = softmax<D, CAP>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
+    const int end = softmax<D, CAP, KV4>(p, B, smem, s_meta, s_todo, words, wk, warp, lane);
     // Every warp but one whose partner failed meets its partner once more: so a
     // partner that still works learns of a timeout at its next meeting, and none
     // is left waiting.
@@ -631,13 +667,13 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   } else if (warp < kSoftWarps + kLoadWarps) {
     reg_dec<Regs<D>::kLoad>();
     ok = warp < kSoftWarps + kLoadWarps / 2
-             ? load<D, true>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane)
-             : load<D, false>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
+             ? load<D, true, KV4>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane)
+             : load<D, false, KV4>(p, B, smem, s_meta, wk, warp - kSoftWarps, lane);
   } else {
     reg_dec<kOtherRegs>();
     if (warp == kSoftWarps + kLoadWarps) {
       if (elect_one()) {
-        ok = issue_mma<D>(p, B, smem0, wk);
+        ok = issue_mma<D, KV4>(p, B, smem0, wk);
         if (!ok) atomicOr(p.status, (uint32_t)NSV_DEV_TIMEOUT);
         umma_commit(B.drained(), true);  // arrives once every MMA issued is done
         (void)mbar_wait(B.drained(), 0);
@@ -656,30 +692,42 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool KV4>
 cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreadsF32);
-  cfg.dynamicSmemBytes = Smem<D>::kTotal;
+  cfg.dynamicSmemBytes = Smem<D, KV4>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_f32_kernel<D, CAP>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_f32_kernel<D, CAP, KV4>, p);
+}
+
+template <bool KV4>
+cudaError_t launch_dim(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+  const bool cap = p.cap > 0.f;
+  if (head_dim == 64)
+    return cap ? launch_one<64, true, KV4>(p, stream) : launch_one<64, false, KV4>(p, stream);
+  return cap ? launch_one<128, true, KV4>(p, stream) : launch_one<128, false, KV4>(p, stream);
+}
+
+template <int D, bool CAP, bool KV4>
+cudaError_t set_attr() {
+  return cudaFuncSetAttribute(chunk_f32_kernel<D, CAP, KV4>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, KV4>::kTotal);
 }
 
 template <int D>
 cudaError_t set_attrs() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(chunk_f32_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Smem<D>::kTotal);
-  return e != cudaSuccess
-             ? e
-             : cudaFuncSetAttribute(chunk_f32_kernel<D, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  cudaError_t e;
+  if ((e = set_attr<D, false, false>()) != cudaSuccess) return e;
+  if ((e = set_attr<D, true, false>()) != cudaSuccess) return e;
+  if ((e = set_attr<D, false, true>()) != cudaSuccess) return e;
+  return set_attr<D, true, true>();
 }
 
 }  // namespace
@@ -690,10 +738,11 @@ cudaError_t prepare_chunk_f32() {
 }
 
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-  const bool cap = p.cap > 0.f;
-  if (head_dim == 64)
-    return cap ? launch_one<64, true>(p, stream) : launch_one<64, false>(p, stream);
-  return cap ? launch_one<128, true>(p, stream) : launch_one<128, false>(p, stream);
+  return launch_dim<false>(p, head_dim, stream);
+}
+
+cudaError_t launch_chunk_kv4_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+  return launch_dim<true>(p, head_dim, stream);
 }
 
 }  // namespace nsv

@@ -72,8 +72,8 @@ int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, cons
       !stride_of(s, k_stride, s->num_kv_heads, &p->k_stride) ||
       !stride_of(s, v_stride, s->num_kv_heads, &p->v_stride))
     return NSV_ERR_SHAPE;
-  // (a warp for a part of a token's heads; a grid holds 2^31 - 1 CTAs of eight)
-  if (tokens * ((int64_t)s->num_heads + 2 * (int64_t)s->num_kv_heads) >= (int64_t(1) << 34))
+  // (a warp for 8 or 16 of a token's heads, two in a CTA; a grid holds 2^31 - 1 CTAs)
+  if (tokens * ((int64_t)s->num_heads + 2 * (int64_t)s->num_kv_heads) >= (int64_t(1) << 33))
     return NSV_ERR_SHAPE;
   DeviceInfo d;
   if ((rc = device_info(&d)) != NSV_OK) return rc;
@@ -157,9 +157,10 @@ VecWs vec_ws(const nsv_shape* s, const VecForm& f, int64_t tokens) {
 }
 
 // Most new tokens of a row that the vector form takes; rows that bring more go to the
-// form for many rows (chunk_bf16.cu), of which fp32 has none.
+// forms for many rows (chunk_bf16.cu, chunk_f32.cu).
 int vec_tokens(const nsv_shape* s) {
-  return s->dtype == NSV_F32 ? 0x7fffffff : kVecMostVectors / (s->num_heads / s->num_kv_heads);
+  return (s->dtype == NSV_F32 ? kVecMostVectorsF32 : kVecMostVectors) /
+         (s->num_heads / s->num_kv_heads);
 }
 
 ChunkWs tile_ws(const nsv_shape* s, int64_t tokens, int num_sms) {
@@ -167,8 +168,9 @@ ChunkWs tile_ws(const nsv_shape* s, int64_t tokens, int num_sms) {
                        s->head_dim, s->dtype, num_sms);
 }
 
-// The converted query vectors and their powers of two.
+// The converted query vectors and their powers of two (bf16).
 uint64_t queries_bytes(const nsv_shape* s, int64_t tokens) {
+  if (s->dtype == NSV_F32) return 0;
   return ((uint64_t)tokens * s->num_heads * (s->head_dim * 2 + 4) + 255) / 256 * 256;
 }
 
@@ -184,7 +186,6 @@ uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
     most = std::max({most, vec_ws(&any, vec_form(&any, ct, num_sms), tokens).total,
                      vec_ws(&one, vec_form(&one, ct, num_sms), tokens).total});
   }
-  if (s->dtype == NSV_F32) return most;
   return (most + 255) / 256 * 256 + (tile_ws(s, tokens, num_sms).total + 255) / 256 * 256 +
          queries_bytes(s, tokens);
 }
@@ -269,15 +270,17 @@ bool tile_params(const Call& a, const ChunkWs& W, char* b, const ChunkQueries& q
   c->max_tiles = W.max_tiles;
   c->tile_rows = W.tile_rows;
   c->tile_tokens = chunk_tile_tokens(s->dtype, c->group);
-  c->keys = kChunkKeys;
+  const bool f32 = s->dtype == NSV_F32;
+  c->keys = f32 ? kChunkKeysF32 : kChunkKeys;
   c->grid = a.d.num_sms;  // one CTA per SM: it takes all the tensor memory
   c->n_min = vec_tokens(s) + 1;
   c->n_max = 0x7fffffff;
   c->whole_runs = kChunkWholeRuns;
-  c->tile_cost = kChunkTileCost;
-  c->pair_units = kChunkPairUnits;
-  c->half_units = kChunkHalfUnits;
+  c->tile_cost = f32 ? kChunkTileCostF32 : kChunkTileCost;
+  c->pair_units = f32 ? 1 : kChunkPairUnits;
+  c->half_units = f32 ? 1 : kChunkHalfUnits;
   c->ws_first = reinterpret_cast<long long*>(c->ws_cta + c->grid);
+  if (f32) return true;
   c->q_up = q.up;
   return chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows, q.half, &c->tmap_q[0]) &&
          chunk_encode_q(a.d, s, a.tokens, kChunkHalfRows / 2, q.half, &c->tmap_q[1]) &&
@@ -405,10 +408,12 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
   if (tiles) {
     const ChunkWs T = tile_ws(s, tokens, d.num_sms);
     char* end = static_cast<char*>(ws) + ws_need - queries_bytes(s, tokens);
-    conv.q = q;
-    conv.half = end;
-    conv.vectors = tokens * s->num_heads;
-    conv.up = reinterpret_cast<float*>(end + conv.vectors * s->head_dim * 2);
+    if (s->dtype == NSV_BF16) {
+      conv.q = q;
+      conv.half = end;
+      conv.vectors = tokens * s->num_heads;
+      conv.up = reinterpret_cast<float*>(end + conv.vectors * s->head_dim * 2);
+    }
     if (!tile_params(call, T, end - (T.total + 255) / 256 * 256, conv, &c)) return cuda_fail();
     c.k4 = p.k_pool;
     c.v4 = p.v_pool;
@@ -430,7 +435,9 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
                   : !tiles    ? launch_chunk_plan(p.c, stream)
                               : launch_chunk_plans(vec ? &p.c : nullptr, c, conv, s->head_dim,
                                                    d.num_sms, stream);
-  if (e == cudaSuccess && tiles) e = launch_chunk_kv4(c, s->head_dim, stream);
+  if (e == cudaSuccess && tiles)
+    e = s->dtype == NSV_F32 ? launch_chunk_kv4_f32(c, s->head_dim, stream)
+                            : launch_chunk_kv4(c, s->head_dim, stream);
   if (e == cudaSuccess && vec)
     e = launch_kv4_vec(p, s->dtype, s->head_dim, f.col_tiles, stream);
   return e == cudaSuccess ? NSV_OK : cuda_fail();
