@@ -1,5 +1,6 @@
 """GB300-native batched paged-attention reads and KV append: the decode read, the
-attention of ragged chunks of new tokens, and the page operators of their cache.
+attention of ragged chunks of new tokens, appends that rotate on the way, a cache held
+in 4 bits, and the page operators of their caches.
 
 The compute path is the C-ABI library ``libnsv.so`` (hand-written CUDA for
 sm_103a, sources in ``csrc/``, declarations in ``include/nsv.h``).  The thin
