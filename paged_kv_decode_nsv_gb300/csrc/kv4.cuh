@@ -73,8 +73,8 @@ struct Kv4VecParams {
 
 // Query vectors of a tile of the vector form: 8 a column tile of the MMA.
 constexpr int kVecKeys = 32;  // positions of one unit: two blocks
-constexpr int kVecMostVectors = 32, kVecMostVectorsF32 = 64;  // of a row and KV head
-constexpr int kVecTileCost = 1;   // of a tile, in units
+constexpr int kVecMostVectors = 24, kVecMostVectorsF32 = 64;  // of a row and KV head
+constexpr int kVecTileCost = 3;   // of a tile, in units
 constexpr int kVecLeastUnits = 2; // of a share, where CTAs work them out themselves
 // The most tiles (rows times row_tiles) that they do it for: eight a thread.
 constexpr int kVecOwnTiles = 2048;

@@ -857,10 +857,11 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
   copy_wait<0>();
 }
 
-// Joins the pieces of the tile that worker blockIdx.x starts and does not end, for KV head
-// blockIdx.y of its group: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.  A warp
-// takes one query vector, a lane D / 32 of its columns; where there are many pieces 2, 4 or
-// 8 warps share them.  (Few CTAs of 16 warps, one for each worker: 5 to 10 us slower.)
+// Joins the pieces of cut tiles, for KV head blockIdx.y of their groups:
+// out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.  A warp takes one query vector, a
+// lane D / 32 of its columns; where there are many pieces 2, 4 or 8 warps share them.  CTA
+// blockIdx.x stands for a worker: those whose workers have the first pieces of a tile share its
+// vectors.  (Few CTAs of 16 warps, one for each worker: 5 to 10 us slower.)
 constexpr int kMergeWarps = 8;
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -869,103 +870,113 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ float s_state[kMergeWarps][D + 2];
   griddep_wait();
   griddep_launch();
-  const int worker = blockIdx.x, head = blockIdx.y;
-  const int4 todo = __ldcg(p.todo + worker);
-  if (todo.w == 0) return;
+  const int head = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = todo.z % p.subs;
-  const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
-  const int vecs = todo.y * per;
-  int parts = 1;
-  while (parts < kMergeWarps && parts * kAhead < todo.w) parts *= 2;
-  const int part = warp % parts;
-  const int b0 = (int)((long long)todo.w * part / parts);
-  const int b1 = (int)((long long)todo.w * (part + 1) / parts);
+  // the tile that this worker starts, and the one of which it has a later piece
+  int4 near = make_int4(0, 0, 0, 0);
+  if ((int)blockIdx.x >= lane) near = __ldcg(p.todo + blockIdx.x - lane);
+  const int before = __ffs(__ballot_sync(kFull, near.w != 0 && lane > 0)) - 1;
 #pragma unroll 1
-  for (int v0 = 0; v0 < vecs; v0 += kMergeWarps / parts) {
-    const int item = v0 + warp / parts, v = min(item, vecs - 1);
-    float M = kLeast, L = 0.f, a[kCols];
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) a[k] = 0.f;
-    // takes states `ml` and `x` of n pieces in
-    auto take = [&](const float2* ml, float (*x)[kCols], int n) {
-      float top = M;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
-      const float keep = ex2_approx(M - top);
-      M = top;
-      L *= keep;
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) a[k] *= keep;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (i >= n) continue;
-        const float w = ex2_approx(ml[i].x - M);
-        L = fmaf(w, ml[i].y, L);
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) a[k] = fmaf(w, x[i][k], a[k]);
-      }
-    };
+  for (int back = max(0, before); back >= 0; back = back > 0 ? 0 : -1) {
+    const int4 todo = make_int4(__shfl_sync(kFull, near.x, back), __shfl_sync(kFull, near.y, back),
+                                __shfl_sync(kFull, near.z, back), __shfl_sync(kFull, near.w, back));
+    if (todo.w <= back) continue;
+    const int worker = blockIdx.x - back;
+    const int sub = todo.z % p.subs;
+    const int per = p.subs > 1 ? min(kVecs, p.c.group - sub * kVecs) : p.c.group;
+    const int vecs = todo.y * per;
+    int parts = 1;
+    while (parts < kMergeWarps && parts * kAhead < todo.w) parts *= 2;
+    const int part = warp % parts;
+    const int b0 = (int)((long long)todo.w * part / parts);
+    const int b1 = (int)((long long)todo.w * (part + 1) / parts);
 #pragma unroll 1
-    for (int b = b0; b < b1 && item < vecs; b += kAhead) {
-      float2 ml[kAhead];
-      float x[kAhead][kCols];
+    for (int v0 = back * (kMergeWarps / parts); v0 < vecs;
+         v0 += min(todo.w, 32) * (kMergeWarps / parts)) {
+      const int item = v0 + warp / parts, v = min(item, vecs - 1);
+      float M = kLeast, L = 0.f, a[kCols];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = min(b + i, b1 - 1);
-        const size_t at =
-            ((size_t)(2 * (worker + j) + (j == 0 ? 1 : 0)) * p.heads_per_worker + head) * kVecs + v;
-        ml[i] = __ldcg(p.ml + at);
-        const float* src = p.acc + at * D + lane * kCols;
-        if constexpr (D == 128) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-          x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-          x[i][0] = f.x, x[i][1] = f.y;
+      for (int k = 0; k < kCols; ++k) a[k] = 0.f;
+      // takes states `ml` and `x` of n pieces in
+      auto take = [&](const float2* ml, float (*x)[kCols], int n) {
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
+        const float keep = ex2_approx(M - top);
+        M = top;
+        L *= keep;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) a[k] *= keep;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (i >= n) continue;
+          const float w = ex2_approx(ml[i].x - M);
+          L = fmaf(w, ml[i].y, L);
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) a[k] = fmaf(w, x[i][k], a[k]);
         }
-      }
-      take(ml, x, b1 - b);
-    }
-    if (parts > 1) {  // the first of the warps that share joins their states, in order
-      __syncthreads();
-      float* st = s_state[warp];
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) st[lane * kCols + k] = a[k];
-      if (lane == 0) st[D] = M, st[D + 1] = L;
-      __syncthreads();
-      if (part == 0) {
-        M = kLeast, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) a[k] = 0.f;
+      };
 #pragma unroll 1
-        for (int b = 0; b < parts; b += kAhead) {
-          float2 ml[kAhead];
-          float x[kAhead][kCols];
+      for (int b = b0; b < b1 && item < vecs; b += kAhead) {
+        float2 ml[kAhead];
+        float x[kAhead][kCols];
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const float* o = s_state[warp + min(b + i, parts - 1)];
-            ml[i] = make_float2(o[D], o[D + 1]);
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) x[i][k] = o[lane * kCols + k];
+        for (int i = 0; i < kAhead; ++i) {
+          const int j = min(b + i, b1 - 1);
+          const size_t slot = 2 * (size_t)(worker + j) + (j == 0 ? 1 : 0);
+          const size_t at = (slot * p.heads_per_worker + head) * kVecs + v;
+          ml[i] = __ldcg(p.ml + at);
+          const float* src = p.acc + at * D + lane * kCols;
+          if constexpr (D == 128) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+            x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+            x[i][0] = f.x, x[i][1] = f.y;
           }
-          take(ml, x, parts - b);
+        }
+        take(ml, x, b1 - b);
+      }
+      if (parts > 1) {  // the first of the warps that share joins their states, in order
+        __syncthreads();
+        float* st = s_state[warp];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) st[lane * kCols + k] = a[k];
+        if (lane == 0) st[D] = M, st[D + 1] = L;
+        __syncthreads();
+        if (part == 0) {
+          M = kLeast, L = 0.f;
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) a[k] = 0.f;
+#pragma unroll 1
+          for (int b = 0; b < parts; b += kAhead) {
+            float2 ml[kAhead];
+            float x[kAhead][kCols];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              const float* o = s_state[warp + min(b + i, parts - 1)];
+              ml[i] = make_float2(o[D], o[D + 1]);
+#pragma unroll
+              for (int k = 0; k < kCols; ++k) x[i][k] = o[lane * kCols + k];
+            }
+            take(ml, x, parts - b);
+          }
         }
       }
-    }
-    if (part != 0 || item >= vecs) continue;
-    const int kv_head = (todo.z / p.subs) * p.heads_per_worker + head;
-    const float inv = L > 0.f ? (p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f) / L : 0.f;
-    const int tok = v / per;
-    T* out = static_cast<T*>(p.c.out) +
-             (((size_t)todo.x + tok) * p.c.heads + kv_head * p.c.group + sub * kVecs +
-              (v - tok * per)) * D + lane * kCols;
+      if (part != 0 || item >= vecs) continue;
+      const int kv_head = (todo.z / p.subs) * p.heads_per_worker + head;
+      const float inv = L > 0.f ? (p.v_scales ? __ldg(p.v_scales + kv_head) : 1.f) / L : 0.f;
+      const int tok = v / per;
+      T* out = static_cast<T*>(p.c.out) +
+               (((size_t)todo.x + tok) * p.c.heads + kv_head * p.c.group + sub * kVecs +
+                (v - tok * per)) * D + lane * kCols;
 #pragma unroll
-    for (int k = 0; k < kCols; k += 2) {
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float2*>(out + k) = make_float2(a[k] * inv, a[k + 1] * inv);
-      else
-        *reinterpret_cast<uint32_t*>(out + k) = pack_bf16(a[k] * inv, a[k + 1] * inv);
+      for (int k = 0; k < kCols; k += 2) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float2*>(out + k) = make_float2(a[k] * inv, a[k + 1] * inv);
+        else
+          *reinterpret_cast<uint32_t*>(out + k) = pack_bf16(a[k] * inv, a[k + 1] * inv);
+      }
     }
   }
 }

@@ -4,16 +4,16 @@ by row, and the serving loop around it.
 Tolerances, per (token, head), against `big`, the largest over the dims of
 |out| + sum p |v| (p: the softmax's weights):
 
-  fp32  Queries and weights are the sum of two fp16 numbers, off by at most 2^-22 of
-        themselves; products of 128 terms, the exponential, the running rescales
+  fp32  Queries and weights are the sum of two fp16 or tf32 numbers, off by at most 2^-21
+        of themselves; products of 128 terms, the exponential, the running rescales
         and the sum each cost a few 2^-24 relative to the scores' size.  Scores here
         are below 16 in log2 units, so a weight is off by at most about
         16 * 128 * 2^-24 = 1.2e-4 in the worst case and by sqrt(128) in place of
         128, 1.1e-5, as the terms' signs fall: 4e-5 of sum p |v|.
-  bf16  The weights are rounded by half a step of bf16 at most, 2^-8 of each, and
-        their sum is taken before: together at most 2^-8 sum p |v|.  So is the
-        output, at most 2^-8 of itself.  2^-12 is left for the scores' fp32
-        arithmetic, the exponential unit and the products of these errors.
+  bf16  The weights are rounded by half a step of fp16 at most, 2^-11 of each (those
+        below 2^-29 of the largest by 2^-40 of it), and their sum is taken before.  The
+        output is rounded by at most 2^-8 of itself.  What is left of 2^-8 + 2^-12
+        of |out| + sum p |v| is for the scores' fp32 arithmetic and the exponential unit.
 """
 
 import numpy as np
@@ -293,17 +293,18 @@ def test_rows_cut_into_many_pieces(dtype, heads, kv_heads, rows, ctx, new):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_long_sums_of_equal_weights(dtype):
+@pytest.mark.parametrize("new", [1, 40])
+def test_long_sums_of_equal_weights(dtype, new):
     """Equal scores over 65536 positions: the mean of the values.  Weights of 2^k add up
     exactly, so that fp32 is off by the sums' rounding alone: within 2^-19."""
     import torch
     n = 65536
-    b = batch([n], [1], 4, 2, 128, dtype)
+    b = batch([n], [new], 4, 2, 128, dtype)
     b["q"].zero_()
-    check(b, dtype, max_new=1, tol=2.0 ** -19 if dtype == "f32" else None)
+    check(b, dtype, max_new=1 if new == 1 else 0, tol=2.0 ** -19 if dtype == "f32" else None)
     b["v"][..., :8 * 128] = 0x55            # 3
     b["v"][..., 8 * 128:] = 0x38            # 1
-    out = call(b, torch.empty_like(b["q"]), max_new=1)
+    out = call(b, torch.empty_like(b["q"]), max_new=1 if new == 1 else 0)
     assert (out.double() - 3.0).abs().max() <= (3 * 2.0 ** -19 if dtype == "f32" else 3 * 2.0 ** -8)
 
 
@@ -343,13 +344,25 @@ def test_scales_of_either_sign_and_none(dtype, scale):
         check(b, dtype, max_new=most)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (20, 4), (40, 1)])
+def test_either_side_of_the_forms(dtype, heads, kv_heads):
+    """Rows of the most query vectors that the form for few takes, and of one token more."""
+    at = (64 if dtype == "f32" else 24) // (heads // kv_heads)
+    new = [at, at + 1, 1, 2 * at + 1, 0, max(1, at - 1)]
+    check(batch([300, 77, 129, 200, 0, 50], new, heads, kv_heads, 128, dtype, pad=2), dtype)
+    for most in (at, at + 1):
+        check(batch([300, 77, 129], [most, 1, 0], heads, kv_heads, 64, dtype), dtype, max_new=most)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("new,most", [([1, 1, 1], 1), ([60, 40, 33], 0), ([20, 9, 70], 0)])
-def test_neighbours_do_not_matter(new, most):
+def test_neighbours_do_not_matter(dtype, new, most):
     """Query rows of other rows and of no row, whatever they hold, change no bit: query
     vectors are scaled together with those they share a tile with."""
     import torch
-    b = batch([400, 300, 70], new, 8, 2, 128, "bf16", pad=5)
-    want = check(b, "bf16", max_new=most)
+    b = batch([400, 300, 70], new, 8, 2, 128, dtype, pad=5)
+    want = check(b, dtype, max_new=most)
     for garbage in (float("nan"), float("inf"), 1e38):
         for r in range(3):
             at = int(sum(new[:r]))
@@ -361,17 +374,18 @@ def test_neighbours_do_not_matter(new, most):
             assert torch.equal(out[at:at + new[r]], want[at:at + new[r]])
 
 
-def test_a_pool_past_four_gigabytes():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_pool_past_four_gigabytes(dtype):
     """The same bits from blocks whose bytes lie past 2^32 as from low ones."""
     import torch
     from paged_kv_decode_nsv_gb300 import nsv
     heads, kv_heads, dim = 32, 8, 128
-    b = batch([900, 333, 40], [1, 1, 1], heads, kv_heads, dim, "bf16", scaled=True)
-    c = batch([900, 333], [200, 40], heads, kv_heads, dim, "bf16", scaled=True)
+    b = batch([900, 333, 40], [1, 1, 1], heads, kv_heads, dim, dtype, scaled=True)
+    c = batch([900, 333], [200, 40], heads, kv_heads, dim, dtype, scaled=True)
     blocks = (1 << 32) // (kv_heads * 9 * dim) + 500
     pools = [torch.zeros((blocks + 1, kv_heads, 9 * dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
     for x, most in ((b, 1), (c, 0)):
-        want = check(x, "bf16", max_new=most)
+        want = check(x, dtype, max_new=most)
         n = x["k"].shape[0]
         for p, name in zip(pools, ("k", "v")):
             p[blocks - n:blocks] = x[name]
