@@ -71,14 +71,26 @@ struct Kv4VecParams {
   int subs;       // parts that a KV head's query heads are taken in
 };
 
-// Query vectors of a tile of the vector form: 8 a column tile of the MMA.
-constexpr int kVecKeys = 32;  // positions of one unit: two blocks
-constexpr int kVecMostVectors = 24, kVecMostVectorsF32 = 64;  // of a row and KV head
-constexpr int kVecTileCost = 3;   // of a tile, in units
-constexpr int kVecLeastUnits = 2; // of a share, where CTAs work them out themselves
-// The most tiles (rows times row_tiles) that they do it for: eight a thread.
+constexpr int kVecKeys = 32;  // positions of one unit of the vector form: two blocks
+// Most query vectors of a row and KV head that it takes; rows that bring more go to the
+// tcgen05 forms.  29 rows over 4000 positions, 32 heads, 8 KV heads: bf16, 24 vectors 103 us
+// here and 112 there, 32 vectors 130 and 113; fp32, 64 vectors 283 and 326, 128 534 and 336.
+// (One row over 30000 alone: 12 vectors 67 and 44.)
+constexpr int kVecMostVectors = 24, kVecMostVectorsF32 = 64;
+// Cost of a tile, in units.  256 single tokens: 160 us at 1, 158.6 at 3; a few short rows do
+// not care up to 3 (18.9 us; 19.5 at 5).
+constexpr int kVecTileCost = 3;
+// Least units of a share, where CTAs work them out themselves (a few short rows: 26 us at 1,
+// 19.7 to 22 at 2, 20.5 at 4).
+constexpr int kVecLeastUnits = 2;
+// Most pieces of a tile, counting all shares as one tile's where there are few tiles.  One token
+// over 131072 positions, 8 heads of 1 KV head: 128 pieces 56 us, 256 42, 384 40, 2432 75; two
+// over 32768, head_dim 64: 23, 21, 25.
+constexpr int kVecMostPieces = 256;
+// The most tiles (rows times row_tiles) that CTAs work their shares out of themselves: eight
+// a thread.  With a list instead, 256 single tokens take 165 us in place of 160, four 23.6 in
+// place of 18.9.
 constexpr int kVecOwnTiles = 2048;
-constexpr int kVecWholeRuns = 8;  // as kChunkWholeRuns
 
 cudaError_t launch_rope_write(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_kv4_write(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);

@@ -107,7 +107,7 @@ struct VecForm {
   int col_tiles, tile_tokens, subs, heads_per_worker, workers_per_cta, workers;
 };
 
-VecForm vec_form(const nsv_shape* s, int col_tiles, int num_sms) {
+VecForm vec_form(const nsv_shape* s, int col_tiles, int64_t tokens, int num_sms) {
   VecForm f;
   const int group = s->num_heads / s->num_kv_heads;
   f.col_tiles = col_tiles;
@@ -121,14 +121,17 @@ VecForm vec_form(const nsv_shape* s, int col_tiles, int num_sms) {
     if (s->num_kv_heads % h == 0) f.heads_per_worker = h;
   f.workers_per_cta = warps / f.heads_per_worker;
   f.workers = num_sms * kv4_vec_ctas_per_sm(s->dtype, col_tiles) * f.workers_per_cta;
+  // (few tiles: pieces that are too many take longer to join than they save)
+  const int64_t tiles = std::min(tokens, s->rows + tokens / f.tile_tokens);
+  const int64_t most = tiles * (s->num_kv_heads / f.heads_per_worker) * f.subs * kVecMostPieces;
+  f.workers = (int)std::max<int64_t>(1, std::min<int64_t>(f.workers, most));
   return f;
 }
 
 // fp32 takes one column tile (its operands are two parts each).  bf16 takes two where a
 // KV head has more than 8 query heads or the caller says that rows bring more than 8 query
-// vectors; where it does not say, most rows bring one token, and those that bring many
-// go to the other form (a 509-token chunk among 32 single tokens, 4 vectors each: 134 us
-// with two column tiles, 122 with one).
+// vectors; where it does not say, most rows bring one token (a 509-token chunk among 32
+// single tokens, 4 vectors each: 134 us with two column tiles, 131 with one).
 int col_tiles_for(const nsv_shape* s) {
   if (s->dtype == NSV_F32) return 1;
   return s->num_heads / s->num_kv_heads * std::max(1, s->query_len) <= 8 ? 1 : 2;
@@ -183,8 +186,8 @@ uint64_t chunk4_ws_bytes(const nsv_shape* s, int64_t tokens, int num_sms) {
   for (int ct = 1; ct <= (s->dtype == NSV_F32 ? 1 : 2); ++ct) {
     nsv_shape one = any;
     one.query_len = 1;  // tiles of a single token: the longest list
-    most = std::max({most, vec_ws(&any, vec_form(&any, ct, num_sms), tokens).total,
-                     vec_ws(&one, vec_form(&one, ct, num_sms), tokens).total});
+    most = std::max({most, vec_ws(&any, vec_form(&any, ct, tokens, num_sms), tokens).total,
+                     vec_ws(&one, vec_form(&one, ct, tokens, num_sms), tokens).total});
   }
   return (most + 255) / 256 * 256 + (tile_ws(s, tokens, num_sms).total + 255) / 256 * 256 +
          queries_bytes(s, tokens);
@@ -243,7 +246,7 @@ void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4Vec
   c.grid = f.workers;
   c.n_min = 0;
   c.n_max = vec_tokens(s);
-  c.whole_runs = kVecWholeRuns;
+  c.whole_runs = kChunkWholeRuns;  // (1 and 32: no difference)
   c.tile_cost = kVecTileCost;
   c.pair_units = c.half_units = 1;
   p->todo = reinterpret_cast<int4*>(b + W.off_todo);
@@ -389,7 +392,7 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
   const uint64_t ws_need = chunk4_ws_bytes(s, tokens, d.num_sms);
   if (!ws || ws_bytes < ws_need || !aligned(ws, 256)) return NSV_ERR_WORKSPACE;
   const Call call{s, sc, d, tokens, q, block_tables, chunk_starts, context_lens, scale, out};
-  const VecForm f = vec_form(s, col_tiles_for(s), d.num_sms);
+  const VecForm f = vec_form(s, col_tiles_for(s), tokens, d.num_sms);
   const VecWs W = vec_ws(s, f, tokens);
   Kv4VecParams p;
   memset(&p, 0, sizeof p);
