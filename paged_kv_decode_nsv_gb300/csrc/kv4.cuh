@@ -71,6 +71,7 @@ struct Kv4VecParams {
   int subs;       // parts that a KV head's query heads are taken in
 };
 
+constexpr int kVecWarps = 8;  // of a CTA of the vector form, at most
 constexpr int kVecKeys = 32;  // positions of one unit of the vector form: two blocks
 // Most query vectors of a row and KV head that it takes; rows that bring more go to the
 // tcgen05 forms.  29 rows over 4000 positions, 32 heads, 8 KV heads: bf16, 24 vectors 103 us
@@ -98,8 +99,7 @@ cudaError_t launch_kv4_read(const Kv4ReadParams& p, int dtype, int head_dim, cud
 cudaError_t launch_kv4_vec(const Kv4VecParams& p, int dtype, int head_dim, int col_tiles,
                            cudaStream_t stream);
 cudaError_t prepare_kv4_vec();
-// Warps of one CTA of the vector form, and its CTAs per SM.
-int kv4_vec_warps(int dtype, int col_tiles);
+// CTAs per SM of the vector form.
 int kv4_vec_ctas_per_sm(int dtype, int col_tiles);
 
 #ifdef __CUDACC__

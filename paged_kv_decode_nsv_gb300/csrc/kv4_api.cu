@@ -115,7 +115,7 @@ VecForm vec_form(const nsv_shape* s, int col_tiles, int64_t tokens, int num_sms)
   f.subs = (group + vecs - 1) / vecs;
   f.tile_tokens = std::max(1, vecs / group);
   if (s->query_len > 0) f.tile_tokens = std::min(f.tile_tokens, (int)s->query_len);
-  const int warps = kv4_vec_warps(s->dtype, col_tiles);
+  const int warps = kVecWarps;
   f.heads_per_worker = 1;
   for (int h = 2; h <= warps; ++h)
     if (s->num_kv_heads % h == 0) f.heads_per_worker = h;
