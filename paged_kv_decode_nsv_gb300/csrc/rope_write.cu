@@ -323,15 +323,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 16 : 10)
     const uint32_t wide = e4m3x2_to_half(code_a | (code_b << 8));
     const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&wide));
     const uint32_t wa = numbers8(a, s.x, __frcp_rn(s.x)), wb = numbers8(b, s.y, __frcp_rn(s.y));
+    const uint32_t other = __shfl_xor_sync(sm::kFull, lane & 1 ? wa : wb, 1);
     if (!real) continue;
     uint8_t* tile = static_cast<uint8_t*>(value ? p.v_pool : p.k_pool) +
                     (size_t)(block * p.kv_heads + h) * kv4_tile_bytes(D);
-    uint32_t* num = reinterpret_cast<uint32_t*>(tile + off * (D / 2));
-    uint8_t* sc = tile + kv4_number_bytes(D) + off * (D / 16);
-    num[t.u] = wa;
-    num[t.v] = wb;
-    if (!(t.u & 1)) sc[t.u >> 1] = (uint8_t)code_a;
-    if (pairs && !(t.v & 1)) sc[t.v >> 1] = (uint8_t)code_b;
+    // 16 dimensions that lie together: of partners, the even lane stores a's and the odd one b's
+    const bool upper = pairs && (lane & 1);
+    const int first = upper ? t.v - 1 : t.u;
+    const uint2 num = make_uint2(upper ? other : wa, pairs && !upper ? other : wb);
+    *reinterpret_cast<uint2*>(tile + off * (D / 2) + first * 4) = num;
+    tile[kv4_number_bytes(D) + off * (D / 16) + first / 2] = (uint8_t)(upper ? code_b : code_a);
   }
 }
 
