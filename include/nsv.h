@@ -636,7 +636,8 @@ NSV_API int nsv_kv4_chunk(const nsv_shape *shape, const nsv_scores *scores,
  *
  * They use shape.rows, max_blocks, num_blocks, block_size, and, where blocks
  * are copied, num_kv_heads (a block of one pool is at most 256 MiB), head_dim and
- * dtype, NSV_KV4 for 4-bit pools (the rest must be valid).  Without rows or items a call does nothing.
+ * dtype, NSV_KV4 for 4-bit pools (the rest must be valid).  Without rows or items a
+ * call does nothing.
  * Data pointers must be 16-byte aligned, index arrays to their element.
  * workspace: at least the bytes nsv_pages_workspace gives, 256-byte aligned,
  * owned by the caller, uninitialised; operators that overlap on the GPU need

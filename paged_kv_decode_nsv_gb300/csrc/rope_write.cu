@@ -16,7 +16,8 @@
 // All three kernels move each byte once, and HBM or the launch bounds them: 8192 tokens of
 // 32 query and 8 KV heads, head_dim 128, bf16, rotated 35 us (88 % of the copy bandwidth);
 // 65536 tokens of 8 KV heads read back 64 us (81 %, mostly writes).  Quantising 16381 tokens
-// takes 83 us where its bytes take 51: divisions and conversions fill the issue slots.
+// takes 76 us where its bytes take 51 (72 registers a thread; 64, which spill, 78, and 80, with
+// fewer warps, 81).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,6 +80,9 @@ __device__ __forceinline__ void load_f32(const float* p, float* x) {
     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
   }
 }
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // 8 elements of a head: what a lane holds of one.
 template <typename T>
@@ -170,15 +174,14 @@ struct Turn {
     const int half = p.rotary_dim / 2;
     const bool upper = d >= half;
     const int e = upper ? d - half : d;
-    float c8[8], s8[8], z[8];
-    load_f32<8>(row + e, c8);
-    load_f32<8>(row + half + e, s8);
-    Eight<T> o;
-    o.load(x + (upper ? e : d + half));
-    o.get(z);
+    const float *c = row + e, *sn = row + half + e;
+    const T* o = x + (upper ? e : d + half);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = upper ? turn_b(z[i], y[i], c8[i], s8[i]) : turn_a(y[i], z[i], c8[i], s8[i]);
+    for (int i = 0; i < 8; ++i) {
+      const float z = to_float(o[i]);
+      const float ci = __ldg(c + i), si = __ldg(sn + i);
+      y[i] = upper ? turn_b(z, y[i], ci, si) : turn_a(y[i], z, ci, si);
+    }
   }
 };
 
@@ -205,10 +208,10 @@ __device__ __forceinline__ uint32_t numbers8(const float* y, float s, float r) {
 // lane holds 16 dimensions of a head in each, all loads go out together, and the token's
 // cosines and sines serve them all.  The position's row of the table is the only load that
 // has to wait for another.  Times of 8192 tokens appended, and 16381 into 4 bits (with
-// their values read back, 17 us): 8 dimensions a lane, partners by shuffles 44 and 105 us;
+// their values read back, 16 us), before later steps: 8 dimensions a lane, partners by shuffles 44 and 105 us;
 // a thread with four whole heads' pairs, 111 to 147 registers, 43 and 127.
 template <typename T, int D, bool FOUR>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 16 : 10)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 10 : FOUR ? 14 : 16)
     append_kernel(const RopeParams p, int q_units, int kv_units) {
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes of a head; heads of a pass

@@ -650,7 +650,8 @@ def kv4_chunk(q, k_pool, v_pool, block_tables, chunk_starts, context_lens, scale
               max_new=0, workspace=None, stream=None):
     """paged_chunk over 4-bit pools (nsv_kv4_chunk in nsv.h).  max_new: the most new
     tokens that any row brings, or 0 where the caller does not know it (1 in a decode
-    step, which is fastest when it says so); more than that is flagged.  workspace:
+    step, which is fastest when it says so); a row of more is flagged.  Numbers that
+    make more than 64 query vectors of a KV head count as 0.  workspace:
     kv4_workspace_bytes() of uint8, or None to allocate it."""
     import torch
     dev, f32, i32, u8 = torch.cuda.current_device(), torch.float32, torch.int32, torch.uint8
