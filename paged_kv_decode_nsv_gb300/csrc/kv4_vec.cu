@@ -255,12 +255,12 @@ struct Worker {
       const int mid = (lo + hi) >> 1;
       if (o->before[mid] <= rem) lo = mid; else hi = mid;
     }
-    // of its tiles (at most 8) the one that holds rem
+    // of its tiles (at most 13: a CTA has 5 warps or more) the one that holds rem
     const int each = (wk.ntiles + blockDim.x - 1) / blockDim.x, i = lo * each + lane;
     const long long mine = lane < each && i < wk.ntiles ? own_tile(p, i, false).units : 0;
     long long upto = o->before[lo] + mine;
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2) {
+    for (int d = 1; d < 16; d *= 2) {
       const long long x = __shfl_up_sync(kFull, upto - o->before[lo], d);
       if (lane >= d) upto += x;
     }

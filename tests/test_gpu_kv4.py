@@ -324,13 +324,16 @@ def test_queries_of_any_size(dtype, size):
     check(b, dtype, max_new=1, tol=(F32_TOL if dtype == "f32" else BF16_TOL) + scores * 128 ** 0.5 * 2.0 ** -22)
 
 
-@pytest.mark.parametrize("rows,most", [(8192, 1), (2048, 1), (600, 3), (257, 8)])
-def test_many_rows(rows, most):
-    """Around the number of tiles up to which no list is planned, and the largest."""
+@pytest.mark.parametrize("rows,most,heads,kv_heads", [
+    (8192, 1, 4, 1), (2048, 1, 4, 1), (600, 3, 4, 1), (257, 8, 4, 1),
+    (2048, 1, 5, 5), (2048, 1, 6, 3), (1024, 2, 7, 7), (2047, 1, 12, 6), (2049, 1, 5, 5)])
+def test_many_rows(rows, most, heads, kv_heads):
+    """Around the number of tiles up to which no list is planned, with CTAs of 8 warps and
+    of fewer, and the largest."""
     rng = np.random.default_rng(rows)
     ctx = rng.integers(0, 60, rows).tolist()
     new = [min(c, int(rng.integers(0, most + 1))) for c in ctx]
-    b = batch(ctx, new, 4, 1, 64, "bf16")
+    b = batch(ctx, new, heads, kv_heads, 64, "bf16")
     check(b, "bf16", max_new=most)
     check(b, "bf16")
 
