@@ -201,3 +201,19 @@ def test_page_operators_take_four_bit_pools_and_attention_does_not(nsv):
     with pytest.raises(nsv.NsvError) as e:
         nsv.chunk_workspace_bytes(_shape(nsv, dtype=nsv.KV4), 10, num_sms=152)
     assert e.value.code == -2
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kv_heads,group,head_dim", [
+    (1, 1, 64), (8, 4, 128), (5, 3, 64), (7, 1, 128), (1, 64, 128), (12, 5, 64), (3, 17, 128)])
+def test_a_larger_batch_has_no_smaller_workspace(nsv, dtype, kv_heads, group, head_dim):
+    """A workspace made for the largest batch serves all others."""
+    def size(rows, tokens):
+        shape = nsv.make_shape(rows, kv_heads * group, kv_heads, head_dim, 10, 100, dtype)
+        return nsv.kv4_workspace_bytes(shape, tokens, 152)
+
+    rows = [1, 2, 3, 31, 257, 3000]
+    tokens = [0, 1, 2, 7, 8, 9, 33, 256, 300, 2049, 70000]
+    for i, r in enumerate(rows):
+        for j, t in enumerate(tokens):
+            assert size(r, t) >= max(size(r, tokens[max(0, j - 1)]), size(rows[max(0, i - 1)], t))
