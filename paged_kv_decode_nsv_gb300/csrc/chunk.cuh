@@ -105,13 +105,8 @@ inline ChunkWs make_chunk_ws(int rows, long long tokens, int kv_heads, int group
 }
 
 struct ChunkParams {
-  // a 4-bit cache (kv4.cuh): its pools, and the fp32 scales of its KV heads or null
-  const uint8_t* k4;
-  const uint8_t* v4;
-  const float* k_units;
-  const float* v_units;
-  const float* q_up;  // [tokens][heads]: what the converted query vectors are scaled down by
-  // bf16 only; tmap_q: boxes of 128, 64 and 32 MMA rows
+  // bf16 only; tmap_q: boxes of 128, 64 and 32 MMA rows.  (First: behind other fields they
+  // cross 128-byte lines, which costs a call half a microsecond.)
   CUtensorMap tmap_q[3], tmap_k, tmap_v;
   const void* q;
   const void* k_pool;
@@ -145,6 +140,12 @@ struct ChunkParams {
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
+  // a 4-bit cache (kv4.cuh): its pools, and the fp32 scales of its KV heads or null
+  const uint8_t* k4;
+  const uint8_t* v4;
+  const float* k_units;
+  const float* v_units;
+  const float* q_up;  // [tokens][heads]: what the converted query vectors are scaled down by
 };
 
 // A tensor map of the query tokens for boxes of `rows` MMA rows (chunk_api.cu).

@@ -197,9 +197,10 @@ __device__ __forceinline__ bool load_queries(const ChunkParams& p, const Bars<D,
 }
 
 template <int D>
-__device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, false>& B, uint32_t smem0,
-                                        volatile int* s_meta, const volatile uint32_t* s_done,
-                                        ChunkWalk wk, int lane, uint32_t& i, uint32_t& nseg) {
+__device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, false>& B,
+                                        uint32_t smem0, volatile int* s_meta,
+                                        const volatile uint32_t* s_done, ChunkWalk wk, int lane,
+                                        uint32_t& i, uint32_t& nseg) {
   using L = Smem<D, false>;
   constexpr uint32_t kBlockBytes = kBlock * D * 2;
   uint32_t run = 0;
@@ -334,7 +335,8 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
       // tokens that are there, of this warp's
       const int left = s.t.ctx - s.t.kb - (h >> 1) * kChunkKeys - 8 * kEights * ww;
       unsigned char* stage = smem + slot * L::kStage + kEights * ww * (D / 64) * 1024 + row * 128;
-      const unsigned char* tiles = smem + L::kOffTiles + out * kHalfRun<D> + kEights / 2 * ww * kTile;
+      const unsigned char* tiles =
+          smem + L::kOffTiles + out * kHalfRun<D> + kEights / 2 * ww * kTile;
       uint32_t w[kEights][kWords], sc[kEights];
 #pragma unroll
       for (int q = 0; q < kEights; ++q) {
@@ -367,7 +369,8 @@ __device__ __forceinline__ bool widen(const ChunkParams& p, const Bars<D, true>&
           for (int n = 0; n < 4; ++n) g[n] = hmul2(g[n], s2);
           const int chunk = part * kWords + k;  // 8 dimensions
           *reinterpret_cast<uint4*>(stage + (q * (D / 64) + (chunk >> 3)) * 1024 +
-                                    (((chunk & 7) ^ row) << 4)) = make_uint4(g[0], g[1], g[2], g[3]);
+                                    (((chunk & 7) ^ row) << 4)) =
+              make_uint4(g[0], g[1], g[2], g[3]);
         }
       }
       fence_proxy_async_smem();
@@ -632,7 +635,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float unit, RowSt
       }
     }
   }
-  const float neg = f.m == -INFINITY ? 0.f : (KV4 ? kUpHalf : 0.f) - f.m;
+  const float neg = f.m == -INFINITY ? 0.f : KV4 ? kUpHalf - f.m : -f.m;
   float l0 = 0.f, l1 = 0.f;
 #pragma unroll 1
   for (int c = 0; c < NC; c += kW) {
@@ -750,9 +753,9 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
         fence_proxy_async_smem();
       }
       if (any_valid) {
-        const bool ok = fold_run<D, CAP, BIAS, KV4>(p, unit, f, t_s, t_o + x * D, t0, col0, 64 >> shift, hf,
-                                               copy, mask, past, bar, words,
-                                               s_ml + x * kChunkHalfRows + r, turn, lane);
+        const bool ok = fold_run<D, CAP, BIAS, KV4>(p, unit, f, t_s, t_o + x * D, t0, col0,
+                                                    64 >> shift, hf, copy, mask, past, bar, words,
+                                                    s_ml + x * kChunkHalfRows + r, turn, lane);
         if (!ok) return kPartnerFailed;
         ++turn;
       }
@@ -1053,7 +1056,8 @@ cudaError_t set_attr() {
   return e != cudaSuccess
              ? e
              : cudaFuncSetAttribute(chunk_bf16_kernel<D, CAP, BIAS, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, true>::kTotal);
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Smem<D, true>::kTotal);
 }
 
 template <int D>

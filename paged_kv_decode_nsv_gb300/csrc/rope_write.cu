@@ -208,8 +208,9 @@ __device__ __forceinline__ uint32_t numbers8(const float* y, float s, float r) {
 // lane holds 16 dimensions of a head in each, all loads go out together, and the token's
 // cosines and sines serve them all.  The position's row of the table is the only load that
 // has to wait for another.  Times of 8192 tokens appended, and 16381 into 4 bits (with
-// their values read back, 16 us), before later steps: 8 dimensions a lane, partners by shuffles 44 and 105 us;
-// a thread with four whole heads' pairs, 111 to 147 registers, 43 and 127.
+// their values read back, 16 us), before later steps: 8 dimensions a lane, partners by
+// shuffles 44 and 105 us; a thread with four whole heads' pairs, 111 to 147 registers, 43
+// and 127.
 template <typename T, int D, bool FOUR>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 10 : FOUR ? 14 : 16)
     append_kernel(const RopeParams p, int q_units, int kv_units) {
