@@ -45,7 +45,7 @@
 // element nearly 2^15, and probabilities are rounded to fp16 (2^-11).  Twenty warps: 16 and 17
 // widen tiles, which wait as they are in the pool in a ring of half runs, into the stages; 18
 // issues; 19 fetches tiles by bulk copies and publishes at the end.  2048 tokens over 32768
-// positions, 32 heads, 8 KV heads: 875 us, 1.22 PFLOP/s; 751 with the widening left out, which is
+// positions, 32 heads, 8 KV heads: 875 to 884 us, 1.2 PFLOP/s; 751 with the widening left out, which is
 // what the bf16 cache takes.  The widening warps' instructions take the softmax warps' issue
 // slots.  (bf16 operands, four widening warps: 1351, e2m1 converts only to fp16; eight widening
 // warps 1076, four and a fetching warp 926; query rows by the bulk copies 909; two widening

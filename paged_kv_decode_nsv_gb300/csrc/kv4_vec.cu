@@ -870,6 +870,10 @@ __global__ void __launch_bounds__(kWarps * 32, (ctas_per_sm<T, NT>()))
 // blockIdx.x stands for a worker: those whose workers have the first pieces of a tile share its
 // vectors.  (Few CTAs of 16 warps, one for each worker: 5 to 10 us slower.)
 constexpr int kMergeWarps = 8;
+// Most CTAs that share a tile: one for each vector that 8 warps take at a time.  (Of 32, whose
+// tiles' list each CTA has to read, the call after a chunk of 2048 tokens starts later: 900 us
+// a call in place of 880; 4: one long row of 16 vectors 74 us in place of 60.)
+constexpr int kMergeShared = 16;
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     kv4_merge_kernel(const __grid_constant__ Kv4VecParams p) {
@@ -881,7 +885,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the tile that this worker starts, and the one of which it has a later piece
   int4 near = make_int4(0, 0, 0, 0);
-  if ((int)blockIdx.x >= lane) near = __ldcg(p.todo + blockIdx.x - lane);
+  if (lane < kMergeShared && (int)blockIdx.x >= lane)
+    near = __ldcg(p.todo + blockIdx.x - lane);
+  if (__ballot_sync(kFull, near.w > lane) == 0) return;
   const int before = __ffs(__ballot_sync(kFull, near.w != 0 && lane > 0)) - 1;
 #pragma unroll 1
   for (int back = max(0, before); back >= 0; back = back > 0 ? 0 : -1) {
@@ -899,7 +905,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int b1 = (int)((long long)todo.w * (part + 1) / parts);
 #pragma unroll 1
     for (int v0 = back * (kMergeWarps / parts); v0 < vecs;
-         v0 += min(todo.w, 32) * (kMergeWarps / parts)) {
+         v0 += min(todo.w, kMergeShared) * (kMergeWarps / parts)) {
       const int item = v0 + warp / parts, v = min(item, vecs - 1);
       float M = kLeast, L = 0.f, a[kCols];
 #pragma unroll
