@@ -605,10 +605,11 @@ NSV_API int nsv_kv4_read(const nsv_shape *shape, const float *k_scales, const fl
  * row that brings more sets NSV_DEV_BAD_CHUNK and is read as having none.
  *
  * The pools' numbers times their scales are multiplied exactly, sums are fp32.  bf16:
- * elements of a query vector below 2^-28 of its largest may be dropped, and weights are
- * rounded to fp16 for the product with the values, while their sum is not: up to 2^-11 of
- * sum p |v| besides the output's own rounding (2^-8).  fp32: queries and weights are
- * off by 2^-22 of themselves.
+ * elements of a query vector below 2^-28 of its largest are off by up to 2^-39 of that, and
+ * weights are rounded to fp16 for the product with the values, while their sum is not: each is
+ * off by up to 2^-11 of itself, or 2^-32 of the vector's largest where that is more, besides
+ * the output's own rounding (2^-8).  fp32: queries and weights are off by up to 2^-22 of
+ * themselves, or 2^-51 of their vector's largest where that is more.
  *
  * workspace: as in nsv_paged_chunk, of the bytes that nsv_kv4_workspace gives (for any
  * query_len).

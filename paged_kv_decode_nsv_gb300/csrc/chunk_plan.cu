@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 }
 
 // Query vectors to fp16, scaled by a power of two each: exact but for elements below 2^-28
-// of a vector's largest, which are off by 2^-40 of it at most.  A lane holds 8 dimensions.
+// of a vector's largest, which are off by 2^-39 of it at most.  A lane holds 8 dimensions.
 template <int D>
 __device__ __forceinline__ void convert_queries(const ChunkQueries& c, int cta, int ctas) {
   constexpr int kLanes = D / 8, kVecs = 32 / kLanes;  // lanes of a vector; vectors of a warp

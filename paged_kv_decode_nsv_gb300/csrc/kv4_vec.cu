@@ -27,11 +27,16 @@
 // MMA row r of the scores and k index r of the output stand for token
 // r ^ ((r >> 1) & 1) of a block, which halves the bank conflicts of the values' loads.
 //
-// Rounding: query vectors are scaled by a power of two to [2^14, 2^15) and are exact in
-// fp16 but for elements below 2^-28 of their vector's largest; fp32 ones are the sum of
-// two fp16 numbers (2^-23).  Weights are scaled by 2^kUp to at most 2^15, then
-// rounded to fp16 (2^-11, where the output's rounding to bf16 is 2^-8), for fp32 to the
-// sum of two fp16 numbers (2^-23).
+// Rounding: query vectors are scaled by a power of two, so that their largest element lies in
+// [2^14, 2^15).  bf16 ones are then exact in fp16 but for elements below 2^-28 of their
+// vector's largest, which are off by 2^-39 of it at most.  Weights are held times 2^kUp, at
+// most 2^15, and rounded to fp16: 2^-11 of themselves (the output's rounding to bf16 is 2^-8),
+// or 2^-32 of the largest where that is more.
+// fp32's queries and weights are the sum of two fp16 numbers, hi + 2^-12 lo, and the products
+// with the lower parts are summed apart and scaled down: off by 2^-23 of themselves, below
+// 2^-28 of the largest by up to 2^-51 of it.  (Without a power of two of their own the lower
+// parts end at 2^-39 of the largest, and what lies below 2^-17 of it loses digits; 256 single
+// tokens over 4096 positions take 303 us so, and 312 with it.)
 //
 // A tile cut between workers leaves partial states; kv4_merge_kernel joins them in the
 // order of their positions.
@@ -77,6 +82,14 @@ struct Round<float> {
   static constexpr int kParts = 2;
   static constexpr float kSlack = 1.f, kUp = 14.f;
 };
+// The lower parts' own power of two: half a step of the largest upper part, 2^3, times it is
+// still in fp16's range.
+constexpr float kLowUp = 4096.f, kLowDown = 1.f / 4096.f;
+// x - hi, the upper parts' rest, as lower parts.
+__device__ __forceinline__ uint32_t lower_parts(float x, float y, uint32_t hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_half((x - f.x) * kLowUp, (y - f.y) * kLowUp);
+}
 
 template <int D>
 struct Ring {
@@ -384,10 +397,11 @@ struct Worker {
       s[0][0] = both(e4m3x2_to_half(lds<uint8_t>(sc + r0 * 4 + t)), false);
       s[1][0] = both(e4m3x2_to_half(lds<uint8_t>(sc + r1 * 4 + t)), false);
     }
+    float low[NT][4];  // of the lower parts
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+      for (int i = 0; i < 4; ++i) c[nt][i] = low[nt][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {  // 8 dimensions of a lane: two k steps
       uint32_t a[2][4];
@@ -403,8 +417,14 @@ struct Worker {
         for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma(c[nt], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
-                q[part][nt][2 * i + j][0], q[part][nt][2 * i + j][1]);
+            mma(part ? low[nt] : c[nt], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1],
+                a[1][2 * j + 1], q[part][nt][2 * i + j][0], q[part][nt][2 * i + j][1]);
+    }
+    if constexpr (kParts == 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[nt][i] = fmaf(low[nt][i], kLowDown, c[nt][i]);
     }
   }
 
@@ -487,13 +507,13 @@ struct Worker {
         load_values(tile + b * R::kTile, dead >> (4 * b), x[b], e2[b]);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        float sum[4][NT][4];
+        float sum[4][NT][4], low[4][NT][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[k][nt][j] = 0.f;
+            for (int j = 0; j < 4; ++j) sum[k][nt][j] = low[k][nt][j] = 0.f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t a[4][4];
@@ -504,15 +524,16 @@ struct Worker {
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma(sum[k][nt], a[0][k], a[1][k], a[2][k], a[3][k], pb[b][part][nt][0],
-                    pb[b][part][nt][1]);
+                mma(part ? low[k][nt] : sum[k][nt], a[0][k], a[1][k], a[2][k], a[3][k],
+                    pb[b][part][nt][0], pb[b][part][nt][1]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[4 * i + k][nt][j] += sum[k][nt][j];
+            for (int j = 0; j < 4; ++j)
+              o[4 * i + k][nt][j] += fmaf(low[k][nt][j], kLowDown, sum[k][nt][j]);
       }
     }
   }
@@ -586,10 +607,8 @@ struct Worker {
           const float a = x[i] * up, b = x[i + 1] * up;
           const uint32_t h = pack_half(a, b);
           q[0][nt][i / 4][(i / 2) & 1] = h;
-          if constexpr (kParts == 2) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            q[kParts - 1][nt][i / 4][(i / 2) & 1] = pack_half(a - f.x, b - f.y);
-          }
+          if constexpr (kParts == 2)
+            q[kParts - 1][nt][i / 4][(i / 2) & 1] = lower_parts(a, b, h);
         }
         // (never 0: what is not seen, -inf, has to stay that)
 #pragma unroll
@@ -741,11 +760,9 @@ struct Worker {
             for (int h = 0; h < 2; ++h) {
               const uint32_t up2 = pack_half(w[2 * h], w[2 * h + 1]);
               pb[b][0][nt][h] = transpose8x8(up2);
-              if constexpr (kParts == 2) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&up2));
+              if constexpr (kParts == 2)
                 pb[b][kParts - 1][nt][h] =
-                    transpose8x8(pack_half(w[2 * h] - f.x, w[2 * h + 1] - f.y));
-              }
+                    transpose8x8(lower_parts(w[2 * h], w[2 * h + 1], up2));
             }
           }
           // (fp32's is compensated: nearly equal weights round the same way each time)
