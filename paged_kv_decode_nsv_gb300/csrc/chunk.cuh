@@ -34,6 +34,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "nsv_common.cuh"
 #include "sm103.cuh"
 
@@ -132,21 +134,28 @@ struct ChunkParams {
   int rows, heads, kv_heads, group, max_blocks;
   int max_tiles, tile_rows, tile_tokens, keys;  // keys: positions of one unit
   int grid;         // CTAs of the attention kernel
-  int n_min, n_max; // rows that bring fewer or more tokens have no tiles
-  bool flag_above;  // more than n_max is an error (NSV_DEV_BAD_CHUNK)
-  int whole_runs;   // where there is a CTA for each tile, the most runs of a whole one
   int tile_cost;    // a tile's own cost, in runs
   int pair_units, half_units;  // units of a run of a tile that fills both halves, or one
   float qscale;     // scale * log2(e)
   float scale;
   float cap;        // 0: scores are not capped
-  // a 4-bit cache (kv4.cuh): its pools, and the fp32 scales of its KV heads or null
+};
+
+// Over a 4-bit cache (kv4.cuh).  (Not among the parameters above, which every call over a
+// bf16 or fp32 cache passes: there they cost a 2048-token prompt over a bf16 cache 56.0 us in
+// place of 55.5 on one GPU, and nothing on another.)
+struct Chunk4Params : ChunkParams {
+  int n_min, n_max; // rows that bring fewer or more tokens have no tiles
+  bool flag_above;  // more than n_max is an error (NSV_DEV_BAD_CHUNK)
+  // its pools, and the fp32 scales of its KV heads or null
   const uint8_t* k4;
   const uint8_t* v4;
   const float* k_units;
   const float* v_units;
   const float* q_up;  // [tokens][heads]: what the converted query vectors are scaled down by
 };
+template <bool KV4>
+using ChunkArgs = std::conditional_t<KV4, Chunk4Params, ChunkParams>;
 
 // A tensor map of the query tokens for boxes of `rows` MMA rows (chunk_api.cu).
 bool chunk_encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int rows,
@@ -154,6 +163,7 @@ bool chunk_encode_q(const DeviceInfo& d, const nsv_shape* s, int64_t tokens, int
 
 // Launchers.
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_plan(const Chunk4Params& p, cudaStream_t stream);
 // The tile lists of two kernels that share a batch (a: null for one alone), and b's query
 // vectors converted to fp16 on the way, in one launch.
 struct ChunkQueries {
@@ -163,12 +173,13 @@ struct ChunkQueries {
   float* up;      // [vectors] the inverse powers
   long long vectors;
 };
-cudaError_t launch_chunk_plans(const ChunkParams* a, const ChunkParams& b, const ChunkQueries& q,
-                               int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_chunk_plans(const Chunk4Params* a, const Chunk4Params& b,
+                               const ChunkQueries& q, int head_dim, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t stream);
 // The same over a 4-bit cache (k4, v4).
-cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream);
-cudaError_t launch_chunk_kv4_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_kv4(const Chunk4Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_kv4_f32(const Chunk4Params& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t stream);
 cudaError_t prepare_chunk_bf16();
 cudaError_t prepare_chunk_f32();
@@ -284,22 +295,35 @@ struct RowChunk {
   int start, n, ctx;
 };
 
-__device__ __forceinline__ RowChunk row_chunk(const ChunkParams& p, int r, bool flag) {
+template <typename P>
+__device__ __forceinline__ RowChunk row_chunk(const P& p, int r, bool flag) {
   const int a = __ldg(p.chunk_starts + r), b = __ldg(p.chunk_starts + r + 1);
   RowChunk c{a, b - a, __ldg(p.context_lens + r)};
   if (a < 0 || b < a || b > p.tokens) {
     c.n = 0;
     if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
   }
-  if (c.n < p.n_min || c.n > p.n_max) {
-    if (flag && p.flag_above && c.n > p.n_max) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
-    c.n = 0;
+  if constexpr (std::is_same_v<P, Chunk4Params>) {
+    if (c.n < p.n_min || c.n > p.n_max) {
+      if (flag && p.flag_above && c.n > p.n_max) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CHUNK);
+      c.n = 0;
+    }
   }
   if (c.ctx < 0 || (long long)c.ctx > (long long)p.max_blocks * kBlock) {
     c.ctx = 0;
     if (flag) atomicOr(p.status, (uint32_t)NSV_DEV_BAD_CTX);
   }
   return c;
+}
+
+// The scales of a KV head's keys and values.
+__device__ __forceinline__ float k_unit(const ChunkParams&, int) { return 1.f; }
+__device__ __forceinline__ float v_unit(const ChunkParams&, int) { return 1.f; }
+__device__ __forceinline__ float k_unit(const Chunk4Params& p, int head) {
+  return p.k_units ? __ldg(p.k_units + head) : 1.f;
+}
+__device__ __forceinline__ float v_unit(const Chunk4Params& p, int head) {
+  return p.v_units ? __ldg(p.v_units + head) : 1.f;
 }
 
 // Workspace slot of a cut tile's piece on CTA c: a CTA cuts at most the tile

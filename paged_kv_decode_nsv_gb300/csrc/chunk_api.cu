@@ -133,9 +133,6 @@ int chunk_impl(const nsv_shape* s, const nsv_scores* sc, int64_t tokens, const v
   p.tile_cost = s->dtype == NSV_F32 ? kChunkTileCostF32 : kChunkTileCost;
   p.pair_units = s->dtype == NSV_F32 ? 1 : kChunkPairUnits;
   p.half_units = s->dtype == NSV_F32 ? 1 : kChunkHalfUnits;
-  p.n_min = 0;
-  p.n_max = 0x7fffffff;
-  p.whole_runs = kChunkWholeRuns;
   p.ws_first = reinterpret_cast<long long*>(p.ws_cta + p.grid);
   if (s->dtype == NSV_BF16 &&
       (!chunk_encode_q(d, s, tokens, kChunkHalfRows, q, &p.tmap_q[0]) ||

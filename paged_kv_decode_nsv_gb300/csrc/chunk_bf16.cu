@@ -254,7 +254,7 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const Bars<D, fals
 // The query rows, and the tiles of a run's keys, then of its values, by one warp: tiles into
 // a ring of half runs, a lane copies a block.
 template <int D>
-__device__ __forceinline__ bool fetch_tiles(const ChunkParams& p, const Bars<D, true>& B,
+__device__ __forceinline__ bool fetch_tiles(const Chunk4Params& p, const Bars<D, true>& B,
                                             uint32_t smem0, volatile int* s_meta,
                                             const volatile uint32_t* s_done, ChunkWalk wk,
                                             int lane, uint32_t& issued, uint32_t& nseg) {
@@ -668,7 +668,7 @@ __device__ __forceinline__ bool fold_run(const ChunkParams& p, float unit, RowSt
 }
 
 template <int D, bool CAP, bool BIAS, bool KV4>
-__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>& B,
+__device__ __forceinline__ int softmax(const ChunkArgs<KV4>& p, const Bars<D, KV4>& B,
                                        unsigned char* smem, const volatile int* s_meta,
                                        int4* s_todo, uint32_t* s_done,
                                        volatile PairWords* words, ChunkWalk wk, int warp,
@@ -726,9 +726,11 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
     const bool past = !BIAS || __all_sync(kFull, !valid || f.see.y <= f.pos + 1);
     const int step = pair ? 1 : 2;
     // what brings a 4-bit cache's scores to their size
-    float unit = KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f;
-    if (KV4 && valid)
-      unit *= __ldg(p.q_up + ((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g);
+    float unit = k_unit(p, s.head);
+    if constexpr (KV4) {
+      if (valid)
+        unit *= __ldg(p.q_up + ((size_t)s.t.q0 + tok) * p.heads + s.head * p.group + g);
+    }
     // the states' exchange is free: every warp has read the previous tile's
     if (nseg && !warp_wait(B.mlfree(), (nseg - 1) & 1)) return kTimedOut;
 #pragma unroll 1
@@ -804,8 +806,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(B.mlfree());  // read: the next tile's states may go there
-    const float v_unit = KV4 && p.v_units ? __ldg(p.v_units + s.head) : 1.f;
-    const float inv = (whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f) * v_unit;
+    const float inv = (whole ? (Lsum > 0.f ? 1.f / Lsum : 0.f) : 1.f) * v_unit(p, s.head);
     w0 *= inv;
     w1 *= inv;
     // where the tile's rows go: row `off` of this KV head's
@@ -915,7 +916,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars<D, KV4>&
 
 template <int D, bool CAP, bool BIAS, bool KV4>
 __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
-    const __grid_constant__ ChunkParams p) {
+    const __grid_constant__ ChunkArgs<KV4> p) {
   using L = Smem<D, KV4>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t smem0 = smem_u32(smem);
@@ -1025,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads<KV4>, 1) chunk_bf16_kernel(
 }
 
 template <int D, bool CAP, bool BIAS, bool KV4>
-cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
+cudaError_t launch_one(const ChunkArgs<KV4>& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreads<KV4>);
@@ -1040,7 +1041,7 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
 }
 
 template <int D, bool KV4>
-cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
+cudaError_t launch_dim(const ChunkArgs<KV4>& p, cudaStream_t stream) {
   const bool cap = p.cap > 0.f, bias = p.slopes != nullptr;
   return cap ? (bias ? launch_one<D, true, true, KV4>(p, stream)
                      : launch_one<D, true, false, KV4>(p, stream))
@@ -1080,7 +1081,7 @@ cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t s
   return head_dim == 64 ? launch_dim<64, false>(p, stream) : launch_dim<128, false>(p, stream);
 }
 
-cudaError_t launch_chunk_kv4(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_chunk_kv4(const Chunk4Params& p, int head_dim, cudaStream_t stream) {
   return head_dim == 64 ? launch_dim<64, true>(p, stream) : launch_dim<128, true>(p, stream);
 }
 

@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t operand_at(int rows, int r, int v) {
 // keys of a run are stored during products and its values during scores.  (Eight warps
 // for both in turn: 5.7 us a run instead of 3.7.)
 template <int D, bool KEYS, bool KV4>
-__device__ __forceinline__ bool load(const ChunkParams& p, const Bars& B, unsigned char* smem,
+__device__ __forceinline__ bool load(const ChunkArgs<KV4>& p, const Bars& B, unsigned char* smem,
                                      volatile int* s_meta, ChunkWalk wk, int warp, int lane) {
   using L = Smem<D, KV4>;
   constexpr int kV = D / 4;                   // 16-byte chunks of a key
@@ -419,7 +419,7 @@ __device__ __forceinline__ bool issue_mma(const ChunkParams& p, const Bars& B, u
 
 // -------------------------------------------------------------------- softmax
 template <int D, bool CAP, bool KV4>
-__device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsigned char* smem,
+__device__ __forceinline__ int softmax(const ChunkArgs<KV4>& p, const Bars& B, unsigned char* smem,
                                        const volatile int* s_meta, int4* s_todo,
                                        volatile PairWords* words, ChunkWalk wk, int warp,
                                        int lane) {
@@ -471,7 +471,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       if (lane == 0) mbar_arrive(B.oread());
       return true;
     };
-    const float scale = p.scale * (KV4 && p.k_units ? __ldg(p.k_units + s.head) : 1.f);
+    const float scale = p.scale * k_unit(p, s.head);
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++run) {
       const uint32_t t_s = t_lane + (run & 1) * 128 + hf * kH;
@@ -582,7 +582,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
       const int slot = chunk_slot(blockIdx.x, s.first);
       const int row = tok * p.group + g;  // within the tile
       const float w = (whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f) *
-                      (KV4 && p.v_units ? __ldg(p.v_units + s.head) : 1.f);
+                      v_unit(p, s.head);
       float* out = chunk_out<float>(p, s.t.q0, s.head, row, D);
       if (valid) {
 #pragma unroll
@@ -603,7 +603,7 @@ __device__ __forceinline__ int softmax(const ChunkParams& p, const Bars& B, unsi
 
 template <int D, bool CAP, bool KV4>
 __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
-    const __grid_constant__ ChunkParams p) {
+    const __grid_constant__ ChunkArgs<KV4> p) {
   using L = Smem<D, KV4>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t smem0 = smem_u32(smem);
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreadsF32, 1) chunk_f32_kernel(
 }
 
 template <int D, bool CAP, bool KV4>
-cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
+cudaError_t launch_one(const ChunkArgs<KV4>& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreadsF32);
@@ -708,7 +708,7 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t stream) {
 }
 
 template <bool KV4>
-cudaError_t launch_dim(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_dim(const ChunkArgs<KV4>& p, int head_dim, cudaStream_t stream) {
   const bool cap = p.cap > 0.f;
   if (head_dim == 64)
     return cap ? launch_one<64, true, KV4>(p, stream) : launch_one<64, false, KV4>(p, stream);
@@ -741,7 +741,7 @@ cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t st
   return launch_dim<false>(p, head_dim, stream);
 }
 
-cudaError_t launch_chunk_kv4_f32(const ChunkParams& p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_chunk_kv4_f32(const Chunk4Params& p, int head_dim, cudaStream_t stream) {
   return launch_dim<true>(p, head_dim, stream);
 }
 

@@ -42,7 +42,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_warp,
   return v;
 }
 
-__device__ __forceinline__ void plan(const ChunkParams& p) {
+template <typename P>
+__device__ __forceinline__ void plan(const P& p) {
   __shared__ int s_first[kMaxRows + 1];  // tiles before each row
   __shared__ long long s_prefix[kPlanThreads];
   __shared__ long long s_warp[32];
@@ -156,7 +157,7 @@ __device__ __forceinline__ void plan(const ChunkParams& p) {
   // on one side of a tile to the tile's edge saved pieces to merge, but the uneven
   // shares cost more: a 2048-token prompt 58 us instead of 56.)
   __syncthreads();
-  const bool whole = !__syncthreads_or(longest > p.whole_runs) &&
+  const bool whole = !__syncthreads_or(longest > kChunkWholeRuns) &&
                      (long long)ntiles * p.kv_heads <= p.grid;
   const long long U = units * p.kv_heads;
   const int run = p.pair_units;
@@ -194,7 +195,8 @@ __device__ __forceinline__ void plan(const ChunkParams& p) {
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+template <typename P>
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const P p) {
   sm::griddep_wait();  // lengths and bounds may be the previous kernel's
   sm::griddep_launch();
   plan(p);
@@ -233,7 +235,8 @@ __device__ __forceinline__ void convert_queries(const ChunkQueries& c, int cta, 
 // A CTA for each list (`both`: or for the second alone), the others for the query vectors.
 template <int D>
 __global__ void __launch_bounds__(kPlanThreads)
-    chunk_plans_kernel(const __grid_constant__ ChunkParams a, const __grid_constant__ ChunkParams b,
+    chunk_plans_kernel(const __grid_constant__ Chunk4Params a,
+                       const __grid_constant__ Chunk4Params b,
                        const __grid_constant__ ChunkQueries q, bool both) {
   sm::griddep_wait();
   sm::griddep_launch();
@@ -244,28 +247,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_chunk_plans(const ChunkParams* a, const ChunkParams& b, const ChunkQueries& q,
-                               int head_dim, int num_sms, cudaStream_t stream) {
-  // (a CTA takes 64 vectors a turn at head_dim 128)
-  const long long ctas = (q.vectors + 63) / 64;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 + (ctas < num_sms ? ctas : num_sms)));
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const ChunkParams& first = a ? *a : b;
-  return head_dim == 64
-             ? cudaLaunchKernelEx(&cfg, chunk_plans_kernel<64>, first, b, q, a != nullptr)
-             : cudaLaunchKernelEx(&cfg, chunk_plans_kernel<128>, first, b, q, a != nullptr);
-}
-
-cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
+template <typename P>
+cudaError_t launch_plan(const P& p, cudaStream_t stream) {
   // (programmatic: its launch overlaps the previous kernel's end, and it waits for
   // that kernel before it reads anything)
   cudaLaunchConfig_t cfg = {};
@@ -277,7 +260,36 @@ cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p);
+  return cudaLaunchKernelEx(&cfg, chunk_plan_kernel<P>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_plans(const Chunk4Params* a, const Chunk4Params& b,
+                               const ChunkQueries& q, int head_dim, int num_sms,
+                               cudaStream_t stream) {
+  // (a CTA takes 64 vectors a turn at head_dim 128)
+  const long long ctas = (q.vectors + 63) / 64;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 + (ctas < num_sms ? ctas : num_sms)));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const Chunk4Params& first = a ? *a : b;
+  return head_dim == 64
+             ? cudaLaunchKernelEx(&cfg, chunk_plans_kernel<64>, first, b, q, a != nullptr)
+             : cudaLaunchKernelEx(&cfg, chunk_plans_kernel<128>, first, b, q, a != nullptr);
+}
+
+cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
+  return launch_plan(p, stream);
+}
+cudaError_t launch_chunk_plan(const Chunk4Params& p, cudaStream_t stream) {
+  return launch_plan(p, stream);
 }
 
 }  // namespace nsv

@@ -56,7 +56,7 @@ struct Kv4ReadParams {
 
 // The vector form of the attention: few query vectors per tile, on mma.sync.
 struct Kv4VecParams {
-  ChunkParams c;  // its plan: kv_heads counts the groups of heads that workers take
+  Chunk4Params c;  // its plan: kv_heads counts the groups of heads that workers take
   const uint8_t* k_pool;
   const uint8_t* v_pool;
   const float* k_scales;

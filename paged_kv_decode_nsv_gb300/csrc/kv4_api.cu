@@ -231,7 +231,7 @@ void common_params(const Call& a, ChunkParams* c) {
 
 void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4VecParams* p) {
   const nsv_shape* s = a.s;
-  ChunkParams& c = p->c;
+  Chunk4Params& c = p->c;
   common_params(a, &c);
   c.ws_head = reinterpret_cast<long long*>(b);
   c.ws_prefix = reinterpret_cast<long long*>(b + W.off_prefix);
@@ -246,7 +246,6 @@ void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4Vec
   c.grid = f.workers;
   c.n_min = 0;
   c.n_max = vec_tokens(s);
-  c.whole_runs = kChunkWholeRuns;  // (1 and 32: no difference)
   c.tile_cost = kVecTileCost;
   c.pair_units = c.half_units = 1;
   p->todo = reinterpret_cast<int4*>(b + W.off_todo);
@@ -259,7 +258,7 @@ void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4Vec
 }
 
 bool tile_params(const Call& a, const ChunkWs& W, char* b, const ChunkQueries& q,
-                 ChunkParams* c) {
+                 Chunk4Params* c) {
   const nsv_shape* s = a.s;
   common_params(a, c);
   c->ws_head = reinterpret_cast<long long*>(b);
@@ -278,7 +277,6 @@ bool tile_params(const Call& a, const ChunkWs& W, char* b, const ChunkQueries& q
   c->grid = a.d.num_sms;  // one CTA per SM: it takes all the tensor memory
   c->n_min = vec_tokens(s) + 1;
   c->n_max = 0x7fffffff;
-  c->whole_runs = kChunkWholeRuns;
   c->tile_cost = f32 ? kChunkTileCostF32 : kChunkTileCost;
   c->pair_units = f32 ? 1 : kChunkPairUnits;
   c->half_units = f32 ? 1 : kChunkHalfUnits;
@@ -405,7 +403,7 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
   // tokens rules one out.
   const int64_t most = s->query_len > 0 ? s->query_len : tokens;
   const bool vec = vec_tokens(s) > 0, tiles = std::min(most, tokens) > vec_tokens(s);
-  ChunkParams c;
+  Chunk4Params c;
   memset(&c, 0, sizeof c);
   ChunkQueries conv{};
   if (tiles) {
@@ -425,7 +423,7 @@ NSV_API int nsv_kv4_chunk(const nsv_shape* s, const nsv_scores* sc, const float*
   }
   // a row of more tokens than the caller named is read as having none
   if (s->query_len > 0) {
-    ChunkParams& last = tiles ? c : p.c;
+    Chunk4Params& last = tiles ? c : p.c;
     last.n_max = s->query_len;
     last.flag_above = true;
   }
