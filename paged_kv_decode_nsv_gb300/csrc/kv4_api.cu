@@ -46,8 +46,9 @@ bool stride_of(const nsv_shape* s, int64_t given, int heads, long long* stride) 
 // there is nothing to do.
 int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, const void* q,
                   const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
-                  int64_t v_stride, const int64_t* write_slots, void* k_pool, void* v_pool,
-                  void* q_out, bool rope_needed, RopeParams* p, bool* nothing) {
+                  int64_t v_stride, const int64_t* write_slots, const float* k_scales,
+                  const float* v_scales, void* k_pool, void* v_pool, void* q_out,
+                  bool rope_needed, RopeParams* p, bool* nothing) {
   int rc = check_tokens(s, tokens);
   if (rc) return rc;
   memset(p, 0, sizeof *p);
@@ -56,6 +57,7 @@ int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, cons
   Args a;
   a.need(k_new, 16), a.need(v_new, 16), a.need(write_slots, 8);
   a.need(k_pool, 16), a.need(v_pool, 16);
+  a.may(k_scales, 4), a.may(v_scales, 4);
   if (rope) {
     a.need(rope->positions, 4), a.need(rope->table, 16);
   } else if (rope_needed) {
@@ -88,6 +90,8 @@ int append_params(const nsv_shape* s, const nsv_rope* rope, int64_t tokens, cons
     p->interleaved = rope->interleaved;
   }
   p->write_slots = write_slots;
+  p->k_scales = k_scales;
+  p->v_scales = v_scales;
   p->q_out = q_out;
   p->k_pool = k_pool;
   p->v_pool = v_pool;
@@ -302,7 +306,8 @@ NSV_API int nsv_rope_write(const nsv_shape* shape, const nsv_rope* rope, int64_t
   RopeParams p;
   bool nothing;
   const int rc = append_params(shape, rope, tokens, q, k_new, v_new, q_stride, k_stride, v_stride,
-                               write_slots, k_pool, v_pool, q_out, true, &p, &nothing);
+                               write_slots, nullptr, nullptr, k_pool, v_pool, q_out, true, &p,
+                               &nothing);
   if (rc || nothing) return rc;
   return launch_rope_write(p, shape->dtype, shape->head_dim, stream) == cudaSuccess ? NSV_OK
                                                                                      : cuda_fail();
@@ -316,11 +321,9 @@ NSV_API int nsv_kv4_write(const nsv_shape* shape, const nsv_rope* rope, const fl
   RopeParams p;
   bool nothing;
   const int rc = append_params(shape, rope, tokens, q, k_new, v_new, q_stride, k_stride, v_stride,
-                               write_slots, k_pool, v_pool, q_out, false, &p, &nothing);
+                               write_slots, k_scales, v_scales, k_pool, v_pool, q_out, false, &p,
+                               &nothing);
   if (rc || nothing) return rc;
-  if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return NSV_ERR_ALIGN;
-  p.k_scales = k_scales;
-  p.v_scales = v_scales;
   return launch_kv4_write(p, shape->dtype, shape->head_dim, stream) == cudaSuccess ? NSV_OK
                                                                                     : cuda_fail();
 }
