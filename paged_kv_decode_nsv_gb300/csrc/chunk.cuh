@@ -125,7 +125,7 @@ struct ChunkParams {
   int4* ws_tiles;
   int4* ws_cta;
   long long* ws_first;
-  int32_t* ws_cnt;
+  int32_t* ws_cnt;  // null where a kernel of its own merges (kv4_vec.cu)
   float2* ws_ml;
   float* ws_acc;
   uint32_t* status;

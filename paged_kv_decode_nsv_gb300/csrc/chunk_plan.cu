@@ -150,7 +150,8 @@ __device__ __forceinline__ void plan(const P& p) {
     p.ws_head[0] = units;
     p.ws_head[1] = ntiles;
   }
-  for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
+  if (!std::is_same_v<P, Chunk4Params> || p.ws_cnt)
+    for (long long i = tid; i < (long long)ntiles * p.kv_heads; i += kPlanThreads) p.ws_cnt[i] = 0;
   // Where each CTA's share of the units starts: c * U / n for the first n CTAs, of
   // at least a run's units each, so that a run starts in every share that lies
   // within a tile; the others get none.  (Moving a boundary that leaves a run or less

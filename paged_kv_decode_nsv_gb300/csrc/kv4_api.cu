@@ -142,7 +142,7 @@ int col_tiles_for(const nsv_shape* s) {
 }
 
 struct VecWs {
-  uint64_t off_prefix, off_tiles, off_cta, off_cnt, off_todo, off_ml, off_acc, total;
+  uint64_t off_prefix, off_tiles, off_cta, off_todo, off_ml, off_acc, total;
   int max_tiles;
 };
 
@@ -150,13 +150,11 @@ VecWs vec_ws(const nsv_shape* s, const VecForm& f, int64_t tokens) {
   auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
   VecWs W;
   W.max_tiles = (int)(s->rows + tokens / f.tile_tokens);
-  const uint64_t groups = (uint64_t)s->num_kv_heads / f.heads_per_worker * f.subs;
   const uint64_t states = (uint64_t)f.workers * 2 * f.heads_per_worker * 8 * f.col_tiles;
   W.off_prefix = 256;
   W.off_tiles = W.off_prefix + up((uint64_t)(W.max_tiles + 1) * 8);
   W.off_cta = W.off_tiles + up((uint64_t)W.max_tiles * 32);
-  W.off_cnt = W.off_cta + up((uint64_t)f.workers * 24);
-  W.off_todo = W.off_cnt + up((uint64_t)W.max_tiles * groups * 4);
+  W.off_todo = W.off_cta + up((uint64_t)f.workers * 24);
   W.off_ml = W.off_todo + up((uint64_t)f.workers * 16);
   W.off_acc = W.off_ml + up(states * 8);
   W.total = W.off_acc + states * s->head_dim * 4;
@@ -242,7 +240,6 @@ void vec_params(const Call& a, const VecForm& f, const VecWs& W, char* b, Kv4Vec
   c.ws_tiles = reinterpret_cast<int4*>(b + W.off_tiles);
   c.ws_cta = reinterpret_cast<int4*>(b + W.off_cta);
   c.ws_first = reinterpret_cast<long long*>(c.ws_cta + f.workers);
-  c.ws_cnt = reinterpret_cast<int32_t*>(b + W.off_cnt);
   c.kv_heads = s->num_kv_heads / f.heads_per_worker * f.subs;
   c.max_tiles = W.max_tiles;
   c.tile_tokens = f.tile_tokens;
