@@ -573,9 +573,10 @@ NSV_API int nsv_rope_write(const nsv_shape *shape, const nsv_rope *rope, int64_t
  * A token's 16 dimensions x, as y = x / k_scales[kv_head], get the scale
  * s = e4m3(max |y| / 6) and the numbers e2m1(y / s), zeros where s is 0; keys are
  * taken from the fp32 rotation.  Quotients are rounded to fp32, conversions to nearest
- * even, saturating (|y| beyond 2688 becomes that).  x must be finite, and k_scales and
- * v_scales within 2^-60 .. 2^60: choose them so that y lies around 1, because a scale
- * below 2^-6 has fewer digits and one below 2^-10 is 0.
+ * even, saturating (|y| beyond 2688 becomes that).  x must be finite: the 16 dimensions
+ * of any other, and those that it is rotated into, hold unspecified numbers, NaN among
+ * them.  k_scales and v_scales lie within 2^-60 .. 2^60: choose them so that y lies around
+ * 1, because a scale below 2^-6 has fewer digits and one below 2^-10 is 0.
  *
  * shape.dtype is the type of q, k_new, v_new and q_out.  rope NULL: nothing is rotated,
  * and q and q_out must be NULL.  Everything else as in nsv_rope_write.

@@ -74,9 +74,16 @@ struct Kv4VecParams {
 constexpr int kVecWarps = 8;  // of a CTA of the vector form, at most
 constexpr int kVecKeys = 32;  // positions of one unit of the vector form: two blocks
 // Most query vectors of a row and KV head that it takes; rows that bring more go to the
-// tcgen05 forms.  29 rows over 4000 positions, 32 heads, 8 KV heads: bf16, 24 vectors 103 us
-// here and 112 there, 32 vectors 130 and 113; fp32, 64 vectors 283 and 326, 128 534 and 336.
-// (One row over 30000 alone: 12 vectors 67 and 44.)
+// tcgen05 forms.  The rule looks at a row's vectors alone, not at the call's rows or contexts,
+// nor at whether the caller names the most tokens of a row, which saves the planning launch
+// and, in bf16, takes two column tiles.  In us here, named and not, and there, replayed from a
+// graph, 32 heads, 8 KV heads, head_dim 128 (of a row; "-": not taken):
+//                                 12 vectors       24              32              64
+//   bf16  29 rows over 4000     50   72   97   82   96  100   83  117  101  150  209  102
+//         1 row over 30000      26   33   37   33   39   41    -    -    -   49   67   44
+//   fp32  29 rows over 4000      -    -    -    -    -    -  148  155  309  277  286  311
+//         1 row over 30000      32   34   72    -    -    -    -    -    -   81   84   78
+// (Named, 32 vectors of bf16 would gain as much as 24 do.)
 constexpr int kVecMostVectors = 24, kVecMostVectorsF32 = 64;
 // Cost of a tile, in units.  256 single tokens: 160 us at 1, 158.6 at 3; a few short rows do
 // not care up to 3 (18.9 us; 19.5 at 5).
@@ -84,9 +91,12 @@ constexpr int kVecTileCost = 3;
 // Least units of a share, where CTAs work them out themselves (a few short rows: 26 us at 1,
 // 19.7 to 22 at 2, 20.5 at 4).
 constexpr int kVecLeastUnits = 2;
-// Most pieces of a tile, counting all shares as one tile's where there are few tiles.  One token
-// over 131072 positions, 8 heads of 1 KV head: 128 pieces 56 us, 256 42, 384 40, 2432 75; two
-// over 32768, head_dim 64: 23, 21, 25.
+// Workers for each tile and group of heads, at most: so the most pieces of a tile where all
+// are alike.  It binds only where a call has few tiles; beside others a long tile is cut into
+// what its share of the units gives.  One token over 131072 positions, 8 heads of 1 KV head: 128
+// pieces 56 us, 256 42, 384 40, 2432 75; two over 32768, head_dim 64: 23, 21, 25.  (Replayed
+// from a graph 35 us alone, and beside 1, 3, 10 and 30 rows of 200 to 600 positions 37, 41, 63
+// and 64; with 32 heads over 8 51 to 54 in all of these.)
 constexpr int kVecMostPieces = 256;
 // The most tiles (rows times row_tiles) that CTAs work their shares out of themselves: eight
 // a thread.  With a list instead, 256 single tokens take 165 us in place of 160, four 23.6 in

@@ -42,11 +42,11 @@
 // order of their positions.
 //
 // What bounds it: the latency of a warp's unit, widening and MMAs together, at 16 warps on an
-// SM (registers).  256 single tokens over 512 to 8192 positions, 32 heads, 8 KV heads, head_dim
+// SM (128 registers a thread, of which 40 to 84 bytes are spilled at head_dim 128).  256 single tokens over 512 to 8192 positions, 32 heads, 8 KV heads, head_dim
 // 128: 159 us, 5.0 TB/s of the cache's bytes.  The copies alone take 131, the work without them
 // 144, each with the 12 us of the launches' start and the merge; a sub-partition issues 0.57
 // instructions a cycle, the ALU pipe is 52 % busy and the tensor pipe 21 %.  Scores a unit
-// ahead of the values: 173 instead of 167; 20 warps of 96 registers: 196 (spills).
+// ahead of the values: 173 instead of 167; 20 warps of 96 registers, which spill more: 196.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

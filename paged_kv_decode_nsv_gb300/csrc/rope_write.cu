@@ -13,11 +13,14 @@
 // keys are quantised from the unrounded rotation.  Quotients are rounded to fp32 and
 // conversions to nearest even.
 //
-// All three kernels move each byte once, and HBM or the launch bounds them: 8192 tokens of
-// 32 query and 8 KV heads, head_dim 128, bf16, rotated 35 us (88 % of the copy bandwidth);
-// 65536 tokens of 8 KV heads read back 64 us (81 %, mostly writes).  Quantising 16381 tokens
-// takes 76 us where its bytes take 51 (72 registers a thread; 64, which spill, 78, and 80, with
-// fewer warps, 81).
+// All three kernels move each byte once.  The launch bounds small calls of each, and HBM
+// large ones of the append that keeps the type and of the read: 8192 tokens of 32 query and 8
+// KV heads, head_dim 128, rotated 35 us in bf16 (88 % of the copy bandwidth) and 62 in fp32
+// (98 %); 65536 tokens of 8 KV heads read back 64 us (81 %, mostly writes) and 126 (73 %).
+// Quantising is bound by its chain of loads, divisions and conversions: 16381 tokens take 76
+// us in bf16 where their bytes take 51, 8192 in fp32 58 where theirs take 52.  (72 registers a
+// thread in bf16, of which 20 bytes are spilled; 64, which spill more, 78, and 80, with fewer
+// warps, 81.  fp32 has 96 and spills 4 bytes.)
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
