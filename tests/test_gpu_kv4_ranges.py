@@ -1,7 +1,6 @@
 """The attention over a 4-bit cache at the ends of what its arguments may be (GPU): head scales
 from 2^-60 to 2^60, for keys or values alone too, and queries of thousands."""
 
-import numpy as np
 import pytest
 
 import test_gpu_kv4 as T
